@@ -10,6 +10,7 @@ Names follow the C ABI: ``nvfp4_quantize``, ``nvfp4_rht_quantize``,
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -18,7 +19,10 @@ import torch
 __all__ = ["NVFP4Tensor", "NVFP4Error", "nvfp4_quantize", "nvfp4_rht_quantize", "nvfp4_quantize_dual", "nvfp4_amax",
            "nvfp4_quantize_amax", "MXFP4Tensor", "mxfp4_quantize", "mxfp4_gemm", "MXFP8Tensor", "mxfp8_quantize",
            "mxfp8_gemm",
-           "nvfp4_dequantize", "nvfp4_gemm", "nvfp4_gemm_ws", "nvfp4_gemm_noalloc", "gemm_workspace", "lib", "LIB_PATH", "F32", "BF16", "RNE", "SR"]
+           "nvfp4_dequantize", "nvfp4_gemm", "nvfp4_gemm_ws", "nvfp4_gemm_noalloc", "gemm_workspace",
+           "nvfp4_layer_norm", "nvfp4_layer_norm_backward", "nvfp4_matvec", "mxfp4_matvec", "nvfp4_distill_topk",
+           "nvfp4_distill_topk_backward", "nvfp4_distill_topk_step",
+           "lib", "LIB_PATH", "F32", "BF16", "RNE", "SR"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libnvfp4.so")
@@ -46,8 +50,10 @@ _lib = None
 # every symbol the header declares
 EXPORTS = ("nvfp4_quantize", "nvfp4_rht_quantize", "nvfp4_amax", "nvfp4_quantize_amax", "nvfp4_quantize_dual",
            "mxfp4_quantize", "mxfp4_gemm", "nvfp4_dequantize", "nvfp4_gemm", "nvfp4_gemm_ws",
-           "nvfp4_gemm_workspace_bytes", "nvfp4_gemm_noalloc", "mxfp8_quantize", "mxfp8_gemm", "nvfp4_probe_mfma",
-           "nvfp4_probe_philox", "nvfp4_status_string")
+           "nvfp4_gemm_workspace_bytes", "nvfp4_gemm_noalloc", "mxfp8_quantize", "mxfp8_gemm", "nvfp4_layer_norm",
+           "nvfp4_layer_norm_backward", "nvfp4_layer_norm_backward_workspace_bytes", "nvfp4_matvec", "mxfp4_matvec",
+           "nvfp4_distill_topk", "nvfp4_distill_topk_backward", "nvfp4_distill_topk_step",
+           "nvfp4_distill_topk_workspace_bytes", "nvfp4_probe_mfma", "nvfp4_probe_philox", "nvfp4_status_string")
 
 
 def lib() -> ctypes.CDLL:
@@ -90,6 +96,27 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_gemm_noalloc.argtypes = [pt, pt, vp, ci, i64, vp]
         L.nvfp4_gemm_noalloc.restype = ci
         L.nvfp4_gemm_workspace_bytes.restype = i64
+        cf = ctypes.c_float
+        L.nvfp4_layer_norm.argtypes = [vp, ci, i64, i64, i64, vp, vp, ci, cf, vp, ci, i64, vp, vp, vp, vp]
+        L.nvfp4_layer_norm.restype = ci
+        L.nvfp4_layer_norm_backward.argtypes = [vp, ci, i64, vp, ci, i64, i64, i64, vp, vp, vp, ci, vp, i64, vp, vp,
+                                                ci, vp, i64, vp]
+        L.nvfp4_layer_norm_backward.restype = ci
+        L.nvfp4_layer_norm_backward_workspace_bytes.argtypes = [i64, i64]
+        L.nvfp4_layer_norm_backward_workspace_bytes.restype = i64
+        L.nvfp4_matvec.argtypes = [pt, vp, ci, i64, i64, vp, ci, i64, vp]
+        L.nvfp4_matvec.restype = ci
+        L.mxfp4_matvec.argtypes = [mt, vp, ci, i64, i64, vp, ci, i64, vp]
+        L.mxfp4_matvec.restype = ci
+        rows = [vp, ci, i64, i64, i64, vp, ci, vp, ci, i64, cf]       # logits, indices, teacher, temperature
+        L.nvfp4_distill_topk.argtypes = rows + [vp, vp, vp, i64, vp]
+        L.nvfp4_distill_topk.restype = ci
+        L.nvfp4_distill_topk_backward.argtypes = rows + [vp, vp, vp, i64, vp]
+        L.nvfp4_distill_topk_backward.restype = ci
+        L.nvfp4_distill_topk_step.argtypes = rows + [vp, vp, vp, vp, i64, vp, i64, vp]
+        L.nvfp4_distill_topk_step.restype = ci
+        L.nvfp4_distill_topk_workspace_bytes.argtypes = [i64, i64]
+        L.nvfp4_distill_topk_workspace_bytes.restype = i64
         L.nvfp4_probe_mfma.argtypes = [i64, vp, vp]
         L.nvfp4_probe_mfma.restype = ci
         L.nvfp4_probe_philox.argtypes = [i64, vp, vp]
@@ -546,3 +573,235 @@ def mxfp8_gemm(a: MXFP8Tensor, b: MXFP8Tensor, out_dtype=torch.float32, out: tor
         _check(lib().mxfp8_gemm(ctypes.byref(ca), ctypes.byref(cb), out.data_ptr(), code, ldc,
                                 _stream_handle(stream, dev)), "mxfp8_gemm")
     return out
+
+
+# ----------------------------------------------------------------------------
+# The operators around the 4-bit linear layer.  Their inputs are matrices with
+# unit column stride and any row stride of at least their width.  Outputs and
+# scratch are allocated for the stream the call runs on, so memory freed by
+# another stream's unfinished work is not reused.
+# ----------------------------------------------------------------------------
+
+def _on(device: torch.device, stream):
+    """The context that makes `device` and `stream` current; nothing to do
+    (and nothing to pay) where they are already."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _require_matrix(t: torch.Tensor, name: str, device: torch.device | None = None, shape=None) -> int:
+    """A [rows, cols] GPU matrix with unit column stride and rows that do not
+    overlap; returns its leading dimension."""
+    if not isinstance(t, torch.Tensor):
+        raise NVFP4Error(f"{name} must be a tensor")
+    _require_device(t, name)
+    if device is not None and t.device != device:
+        raise NVFP4Error(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 2:
+        raise NVFP4Error(f"{name} must be a 2-D tensor, got shape {tuple(t.shape)}")
+    rows, cols = t.shape
+    if shape is not None and (rows, cols) != shape:
+        raise NVFP4Error(f"{name} must have shape {shape}, got {(rows, cols)}")
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1:
+        raise NVFP4Error(f"{name} must be row-major (unit column stride)")
+    if rows <= 1:
+        return max(cols, 1)
+    if s0 < cols:
+        raise NVFP4Error(f"{name}: rows overlap (row stride < columns)")
+    return s0
+
+
+def _param(t, name: str, cols: int, device: torch.device):
+    """A parameter vector or None: (pointer, dtype code)."""
+    if t is None:
+        return None, F32
+    if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.shape[0] != cols:
+        raise NVFP4Error(f"{name} must be a vector of {cols} elements")
+    code = _dtype_code(t)
+    _require_buffer(t, name, t.dtype, cols, device)
+    return t.data_ptr(), code
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def nvfp4_layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                     eps: float = 1e-5, out_dtype=None, amax: bool = False, out: torch.Tensor | None = None,
+                     stream=None):
+    """Layer norm of the rows of x [rows, cols] (f32/bf16): (y, mean, rstd),
+    y in `out_dtype` (x's by default), mean and rstd f32 [rows].  With amax,
+    (y, mean, rstd, amax): the f32 [1] maximum of |y| that
+    nvfp4_quantize_amax takes on axis 1 (see include/nvfp4.h)."""
+    ldx = _require_matrix(x, "x")
+    dev = x.device
+    rows, cols = x.shape
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    ycode = _out_code(out_dtype)
+    wp, wcode = _param(weight, "weight", cols, dev)
+    bp, bcode = _param(bias, "bias", cols, dev)
+    if wp is None:
+        wcode = bcode
+    elif bp is not None and bcode != wcode:
+        raise NVFP4Error("weight and bias must have the same dtype")
+    with _on(dev, stream):
+        y = torch.empty((rows, cols), dtype=out_dtype, device=dev) if out is None else out
+        ldy = _require_matrix_out(y, rows, cols, out_dtype, dev) if out is not None else max(cols, 1)
+        stats = torch.empty((2, rows), dtype=torch.float32, device=dev)
+        top = torch.empty(1, dtype=torch.float32, device=dev) if amax else None
+        p = stats.data_ptr()
+        _check(lib().nvfp4_layer_norm(x.data_ptr(), _dtype_code(x), rows, cols, ldx, wp, bp, wcode, float(eps),
+                                      y.data_ptr(), ycode, ldy, p, p + 4 * rows, _ptr(top),
+                                      _stream_handle(stream, dev)), "nvfp4_layer_norm")
+    mean, rstd = stats.unbind(0)
+    return (y, mean, rstd, top) if amax else (y, mean, rstd)
+
+
+def nvfp4_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                              weight: torch.Tensor | None = None, grad_dtype=torch.float32, stream=None):
+    """The gradients of nvfp4_layer_norm: (dx in x's dtype, dweight, dbias),
+    the latter [cols] in `grad_dtype`."""
+    ldx = _require_matrix(x, "x")
+    dev = x.device
+    rows, cols = x.shape
+    lddy = _require_matrix(dy, "dy", dev, (rows, cols))
+    _require_buffer(mean, "mean", torch.float32, rows, dev)
+    _require_buffer(rstd, "rstd", torch.float32, rows, dev)
+    wp, wcode = _param(weight, "weight", cols, dev)
+    gcode = _out_code(grad_dtype)
+    need = int(lib().nvfp4_layer_norm_backward_workspace_bytes(rows, cols))
+    if need < 0:
+        _check(need, "nvfp4_layer_norm_backward")
+    with _on(dev, stream):
+        dx = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+        dwb = torch.empty((2, cols), dtype=grad_dtype, device=dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        p = dwb.data_ptr()
+        _check(lib().nvfp4_layer_norm_backward(dy.data_ptr(), _dtype_code(dy), lddy, x.data_ptr(), _dtype_code(x),
+                                               rows, cols, ldx, mean.data_ptr(), rstd.data_ptr(), wp, wcode,
+                                               dx.data_ptr(), cols, p, p + cols * dwb.element_size(), gcode,
+                                               ws.data_ptr(), need, _stream_handle(stream, dev)),
+               "nvfp4_layer_norm_backward")
+    dweight, dbias = dwb.unbind(0)
+    return dx, dweight, dbias
+
+
+def _matvec(fn, what, w, x, out_dtype, out, stream):
+    ldx = _require_matrix(x, "x")
+    dev = x.device
+    if w.device != dev:
+        raise NVFP4Error(f"weights on {w.device}, x on {dev}")
+    tokens, k = x.shape
+    if k != w.k:
+        raise NVFP4Error(f"x must have {w.k} columns, got {k}")
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    code = _out_code(out_dtype)
+    cw = w._c()
+    with _on(dev, stream):
+        y = torch.empty((tokens, w.outer), dtype=out_dtype, device=dev) if out is None else out
+        ldy = _require_matrix_out(y, tokens, w.outer, out_dtype, dev) if out is not None else max(w.outer, 1)
+        _check(fn(ctypes.byref(cw), x.data_ptr(), _dtype_code(x), tokens, ldx, y.data_ptr(), code, ldy,
+                  _stream_handle(stream, dev)), what)
+    return y
+
+
+def nvfp4_matvec(w: NVFP4Tensor, x: torch.Tensor, out_dtype=None, out: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """y [tokens, N] = x . W^T for unquantized x [tokens, K] (f32/bf16, made
+    for 1 to 16 tokens) and NVFP4 weights W [N, K]; y in `out_dtype` (x's by
+    default)."""
+    return _matvec(lib().nvfp4_matvec, "nvfp4_matvec", w, x, out_dtype, out, stream)
+
+
+def mxfp4_matvec(w: MXFP4Tensor, x: torch.Tensor, out_dtype=None, out: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """nvfp4_matvec with MXFP4 weights."""
+    return _matvec(lib().mxfp4_matvec, "mxfp4_matvec", w, x, out_dtype, out, stream)
+
+
+def _distill_args(logits, indices, teacher, temperature):
+    """Checks the inputs that the distillation calls share; returns their
+    leading C arguments."""
+    ldz = _require_matrix(logits, "logits")
+    dev = logits.device
+    tokens, vocab = logits.shape
+    if not isinstance(indices, torch.Tensor) or indices.dtype not in (torch.int32, torch.int64):
+        raise NVFP4Error("indices must be an int32 or int64 tensor")
+    if indices.dim() != 2 or indices.shape[0] != tokens:
+        raise NVFP4Error(f"indices must have shape ({tokens}, top), got {tuple(indices.shape)}")
+    if not isinstance(teacher, torch.Tensor) or teacher.shape != indices.shape:
+        raise NVFP4Error("teacher must be a tensor of indices' shape")
+    top = indices.shape[1]
+    _require_buffer(indices, "indices", indices.dtype, tokens * top, dev)
+    _require_buffer(teacher, "teacher", teacher.dtype, tokens * top, dev)
+    return (logits.data_ptr(), _dtype_code(logits), tokens, vocab, ldz, indices.data_ptr(),
+            32 if indices.dtype == torch.int32 else 64, teacher.data_ptr(), _dtype_code(teacher), top,
+            float(temperature))
+
+
+def _distill_workspace(tokens: int, vocab: int, device):
+    need = int(lib().nvfp4_distill_topk_workspace_bytes(tokens, vocab))
+    if need < 0:
+        _check(need, "nvfp4_distill_topk")
+    return torch.empty(need, dtype=torch.uint8, device=device), need
+
+
+def nvfp4_distill_topk(logits: torch.Tensor, indices: torch.Tensor, teacher: torch.Tensor,
+                       temperature: float = 1.0, stream=None):
+    """The distillation loss of logits [tokens, vocab] (f32/bf16) against a
+    teacher's best logits [tokens, top] at `indices` (-1 = no entry):
+    (loss, lse), f32 [tokens] (see include/nvfp4.h)."""
+    args = _distill_args(logits, indices, teacher, temperature)
+    dev = logits.device
+    tokens, vocab = logits.shape
+    with _on(dev, stream):
+        res = torch.empty((2, tokens), dtype=torch.float32, device=dev)
+        ws, need = _distill_workspace(tokens, vocab, dev)
+        p = res.data_ptr()
+        _check(lib().nvfp4_distill_topk(*args, p, p + 4 * tokens, ws.data_ptr(), need, _stream_handle(stream, dev)),
+               "nvfp4_distill_topk")
+    return res.unbind(0)
+
+
+def nvfp4_distill_topk_backward(logits: torch.Tensor, indices: torch.Tensor, teacher: torch.Tensor,
+                                lse: torch.Tensor, dloss: torch.Tensor, temperature: float = 1.0,
+                                out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient of sum_t dloss_t loss_t with respect to the logits, in
+    their dtype, from the forward call's lse."""
+    args = _distill_args(logits, indices, teacher, temperature)
+    dev = logits.device
+    tokens, vocab = logits.shape
+    _require_buffer(lse, "lse", torch.float32, tokens, dev)
+    _require_buffer(dloss, "dloss", torch.float32, tokens, dev)
+    with _on(dev, stream):
+        dz = torch.empty((tokens, vocab), dtype=logits.dtype, device=dev) if out is None else out
+        ldd = _require_matrix_out(dz, tokens, vocab, logits.dtype, dev) if out is not None else max(vocab, 1)
+        _check(lib().nvfp4_distill_topk_backward(*args, lse.data_ptr(), dloss.data_ptr(), dz.data_ptr(), ldd,
+                                                 _stream_handle(stream, dev)), "nvfp4_distill_topk_backward")
+    return dz
+
+
+def nvfp4_distill_topk_step(logits: torch.Tensor, indices: torch.Tensor, teacher: torch.Tensor,
+                            weight: torch.Tensor, temperature: float = 1.0, out: torch.Tensor | None = None,
+                            stream=None):
+    """Loss and gradient in one call: (loss, lse, dlogits), dlogits being the
+    gradient of sum_t weight_t loss_t (weight f32 [tokens])."""
+    args = _distill_args(logits, indices, teacher, temperature)
+    dev = logits.device
+    tokens, vocab = logits.shape
+    _require_buffer(weight, "weight", torch.float32, tokens, dev)
+    with _on(dev, stream):
+        dz = torch.empty((tokens, vocab), dtype=logits.dtype, device=dev) if out is None else out
+        ldd = _require_matrix_out(dz, tokens, vocab, logits.dtype, dev) if out is not None else max(vocab, 1)
+        res = torch.empty((2, tokens), dtype=torch.float32, device=dev)
+        ws, need = _distill_workspace(tokens, vocab, dev)
+        p = res.data_ptr()
+        _check(lib().nvfp4_distill_topk_step(*args, weight.data_ptr(), p, p + 4 * tokens, dz.data_ptr(), ldd,
+                                             ws.data_ptr(), need, _stream_handle(stream, dev)),
+               "nvfp4_distill_topk_step")
+    loss, lse = res.unbind(0)
+    return loss, lse, dz

@@ -86,6 +86,58 @@ int quantize_common(const void *x, int x_dtype, int64_t rows, int64_t cols, int 
   return hip_status(e);
 }
 
+inline bool dtype_ok(int d) { return d == NVFP4_F32 || d == NVFP4_BF16; }
+inline uintptr_t dtype_size(int d) { return d == NVFP4_F32 ? 4 : 2; }
+
+// A row-major [rows][ld] matrix of `cols` used columns: size and leading
+// dimension.
+inline bool matrix_ok(int64_t rows, int64_t cols, int64_t ld) {
+  return rows >= 0 && cols >= 0 && ld >= cols && count_ok(rows, ld);
+}
+
+// Do the used bytes of two matrices of the same shape and type meet?
+inline bool overlap(const void *a, int64_t lda, const void *b, int64_t ldb, int64_t rows, int64_t cols, int64_t size) {
+  if (rows <= 0 || cols <= 0) return false;
+  const uintptr_t a0 = (uintptr_t)a, a1 = a0 + (uintptr_t)(((rows - 1) * lda + cols) * size);
+  const uintptr_t b0 = (uintptr_t)b, b1 = b0 + (uintptr_t)(((rows - 1) * ldb + cols) * size);
+  return a0 < b1 && b0 < a1;
+}
+
+// The widest row layer norm takes (its column grids stay far inside 2^31).
+constexpr int64_t kMaxNormCols = 1LL << 31;
+// The matvec puts 16 weight rows on the grid's x dimension and 16 tokens on
+// its y dimension.
+constexpr int64_t kMaxMatvecRows = (int64_t)INT32_MAX * 16;
+constexpr int64_t kMaxMatvecTokens = 65535LL * 16;
+// The distillation kernels keep vocabulary indices in 32 bits.
+constexpr int64_t kMaxVocab = INT32_MAX;
+
+int matvec_common(bool mx, const uint8_t *codes, const uint8_t *scales, const float *meta, int64_t N, int64_t K,
+                  const void *x, int x_dtype, int64_t tokens, int64_t ldx, void *y, int y_dtype, int64_t ldy,
+                  void *hip_stream) {
+  if (!dtype_ok(x_dtype) || !dtype_ok(y_dtype)) return NVFP4_ERR_ENUM;
+  if (!matrix_ok(tokens, K, ldx) || !matrix_ok(tokens, N, ldy)) return NVFP4_ERR_SHAPE;
+  if (N > kMaxMatvecRows || tokens > kMaxMatvecTokens) return NVFP4_ERR_SHAPE;
+  if (tokens > 0 && N > 0 && (!y || (K > 0 && !x))) return NVFP4_ERR_NULL;
+  if (!aligned(x, dtype_size(x_dtype)) || !aligned(y, dtype_size(y_dtype))) return NVFP4_ERR_ALIGN;
+  return hip_status(nvfp4::launch_matvec(mx, codes, scales, meta, N, K, x, x_dtype, tokens, ldx, y, y_dtype, ldy,
+                                         (hipStream_t)hip_stream));
+}
+
+// The arguments that the three distillation calls share.
+int check_distill(const void *z, int z_dtype, int64_t tokens, int64_t vocab, int64_t ldz, const void *indices,
+                  int index_bits, const void *teacher, int t_dtype, int64_t top, float tau, const float *lse) {
+  if (!dtype_ok(z_dtype) || !dtype_ok(t_dtype) || (index_bits != 32 && index_bits != 64)) return NVFP4_ERR_ENUM;
+  if (vocab < 1 || vocab > kMaxVocab || !matrix_ok(tokens, vocab, ldz)) return NVFP4_ERR_SHAPE;
+  if (top < 0 || top > nvfp4::distill_max_top() || !count_ok(tokens, top)) return NVFP4_ERR_SHAPE;
+  if (!(tau > 0.0f) || tau > 3.0e38f) return NVFP4_ERR_VALUE;
+  if (tokens > 0 && (!z || !lse || (top > 0 && (!indices || !teacher)))) return NVFP4_ERR_NULL;
+  if (!aligned(z, dtype_size(z_dtype)) || !aligned(teacher, dtype_size(t_dtype)) || !aligned(lse, 4) ||
+      !aligned(indices, index_bits / 8))
+    return NVFP4_ERR_ALIGN;
+  return NVFP4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -272,6 +324,121 @@ int nvfp4_gemm_noalloc(const nvfp4_tensor *a, const nvfp4_tensor *b, void *c, in
                                              b->outer, a->k, c, c_dtype, ldc, ws, (hipStream_t)hip_stream));
 }
 
+int nvfp4_layer_norm(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void *weight,
+                     const void *bias, int w_dtype, float eps, void *y, int y_dtype, int64_t ldy, float *mean,
+                     float *rstd, float *amax, void *hip_stream) {
+  if (!dtype_ok(x_dtype) || !dtype_ok(w_dtype) || !dtype_ok(y_dtype)) return NVFP4_ERR_ENUM;
+  if (cols < 1 || cols > kMaxNormCols || !matrix_ok(rows, cols, ldx) || !matrix_ok(rows, cols, ldy))
+    return NVFP4_ERR_SHAPE;
+  if (!(eps >= 0.0f) || eps > 3.0e38f) return NVFP4_ERR_VALUE;
+  if (rows > 0 && (!x || !y || !mean || !rstd)) return NVFP4_ERR_NULL;
+  if (!aligned(x, dtype_size(x_dtype)) || !aligned(y, dtype_size(y_dtype)) || !aligned(weight, dtype_size(w_dtype)) ||
+      !aligned(bias, dtype_size(w_dtype)) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(amax, 4))
+    return NVFP4_ERR_ALIGN;
+  return hip_status(nvfp4::launch_layer_norm(x, x_dtype, rows, cols, ldx, weight, bias, w_dtype, eps, y, y_dtype, ldy,
+                                             mean, rstd, amax, (hipStream_t)hip_stream));
+}
+
+int64_t nvfp4_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  if (cols < 1 || cols > kMaxNormCols || !matrix_ok(rows, cols, cols)) return NVFP4_ERR_SHAPE;
+  return nvfp4::layer_norm_backward_workspace_bytes(rows, cols);
+}
+
+int nvfp4_layer_norm_backward(const void *dy, int dy_dtype, int64_t lddy, const void *x, int x_dtype, int64_t rows,
+                              int64_t cols, int64_t ldx, const float *mean, const float *rstd, const void *weight,
+                              int w_dtype, void *dx, int64_t lddx, void *dweight, void *dbias, int g_dtype,
+                              void *workspace, int64_t workspace_bytes, void *hip_stream) {
+  if (!dtype_ok(dy_dtype) || !dtype_ok(x_dtype) || !dtype_ok(w_dtype) || !dtype_ok(g_dtype)) return NVFP4_ERR_ENUM;
+  if (cols < 1 || cols > kMaxNormCols || !matrix_ok(rows, cols, ldx) || !matrix_ok(rows, cols, lddy) ||
+      !matrix_ok(rows, cols, lddx))
+    return NVFP4_ERR_SHAPE;
+  const int64_t need = nvfp4::layer_norm_backward_workspace_bytes(rows, cols);
+  if (workspace_bytes < need) return NVFP4_ERR_SHAPE;
+  if (rows > 0 && (!dy || !x || !mean || !rstd || !dx)) return NVFP4_ERR_NULL;
+  if (need > 0 && !workspace) return NVFP4_ERR_NULL;
+  if (!aligned(dy, dtype_size(dy_dtype)) || !aligned(x, dtype_size(x_dtype)) || !aligned(dx, dtype_size(x_dtype)) ||
+      !aligned(weight, dtype_size(w_dtype)) || !aligned(dweight, dtype_size(g_dtype)) ||
+      !aligned(dbias, dtype_size(g_dtype)) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(workspace, 16))
+    return NVFP4_ERR_ALIGN;
+  return hip_status(nvfp4::launch_layer_norm_backward(dy, dy_dtype, lddy, x, x_dtype, ldx, mean, rstd, weight, w_dtype,
+                                                      dx, lddx, dweight, dbias, g_dtype, workspace, rows, cols,
+                                                      (hipStream_t)hip_stream));
+}
+
+int nvfp4_matvec(const nvfp4_tensor *w, const void *x, int x_dtype, int64_t tokens, int64_t ldx, void *y, int y_dtype,
+                 int64_t ldy, void *hip_stream) {
+  const int st = check_tensor(w);
+  if (st != NVFP4_OK) return st;
+  return matvec_common(false, w->codes, w->scales, w->meta, w->outer, w->k, x, x_dtype, tokens, ldx, y, y_dtype, ldy,
+                       hip_stream);
+}
+
+int mxfp4_matvec(const mxfp4_tensor *w, const void *x, int x_dtype, int64_t tokens, int64_t ldx, void *y, int y_dtype,
+                 int64_t ldy, void *hip_stream) {
+  if (!w) return NVFP4_ERR_NULL;
+  if (w->outer < 0 || w->k < 0 || w->k % 32 != 0 || !count_ok(w->outer, w->k)) return NVFP4_ERR_SHAPE;
+  if (w->outer > 0 && w->k > 0 && (!w->codes || !w->scales)) return NVFP4_ERR_NULL;
+  if (!aligned(w->codes, 16)) return NVFP4_ERR_ALIGN;
+  return matvec_common(true, w->codes, w->scales, nullptr, w->outer, w->k, x, x_dtype, tokens, ldx, y, y_dtype, ldy,
+                       hip_stream);
+}
+
+int64_t nvfp4_distill_topk_workspace_bytes(int64_t tokens, int64_t vocab) {
+  if (vocab < 1 || vocab > kMaxVocab || !matrix_ok(tokens, vocab, vocab)) return NVFP4_ERR_SHAPE;
+  return nvfp4::distill_workspace_bytes(tokens, vocab);
+}
+
+int nvfp4_distill_topk(const void *logits, int z_dtype, int64_t tokens, int64_t vocab, int64_t ldz,
+                       const void *indices, int index_bits, const void *teacher, int t_dtype, int64_t top,
+                       float temperature, float *loss, float *lse, void *workspace, int64_t workspace_bytes,
+                       void *hip_stream) {
+  const int st = check_distill(logits, z_dtype, tokens, vocab, ldz, indices, index_bits, teacher, t_dtype, top,
+                               temperature, lse);
+  if (st != NVFP4_OK) return st;
+  const int64_t need = nvfp4::distill_workspace_bytes(tokens, vocab);
+  if (workspace_bytes < need) return NVFP4_ERR_SHAPE;
+  if ((tokens > 0 && !loss) || (need > 0 && !workspace)) return NVFP4_ERR_NULL;
+  if (!aligned(loss, 4) || !aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
+  return hip_status(nvfp4::launch_distill(logits, z_dtype, tokens, vocab, ldz, indices, index_bits == 64, teacher,
+                                          t_dtype, (int)top, temperature, nullptr, loss, lse, nullptr, 0, workspace,
+                                          true, (hipStream_t)hip_stream));
+}
+
+int nvfp4_distill_topk_backward(const void *logits, int z_dtype, int64_t tokens, int64_t vocab, int64_t ldz,
+                                const void *indices, int index_bits, const void *teacher, int t_dtype, int64_t top,
+                                float temperature, const float *lse, const float *dloss, void *dlogits, int64_t lddz,
+                                void *hip_stream) {
+  const int st = check_distill(logits, z_dtype, tokens, vocab, ldz, indices, index_bits, teacher, t_dtype, top,
+                               temperature, lse);
+  if (st != NVFP4_OK) return st;
+  if (!matrix_ok(tokens, vocab, lddz)) return NVFP4_ERR_SHAPE;
+  if (tokens > 0 && (!dloss || !dlogits)) return NVFP4_ERR_NULL;
+  if (!aligned(dloss, 4) || !aligned(dlogits, dtype_size(z_dtype))) return NVFP4_ERR_ALIGN;
+  if (overlap(logits, ldz, dlogits, lddz, tokens, vocab, dtype_size(z_dtype))) return NVFP4_ERR_SHAPE;
+  return hip_status(nvfp4::launch_distill(logits, z_dtype, tokens, vocab, ldz, indices, index_bits == 64, teacher,
+                                          t_dtype, (int)top, temperature, dloss, nullptr, const_cast<float *>(lse),
+                                          dlogits, lddz, nullptr, false, (hipStream_t)hip_stream));
+}
+
+int nvfp4_distill_topk_step(const void *logits, int z_dtype, int64_t tokens, int64_t vocab, int64_t ldz,
+                            const void *indices, int index_bits, const void *teacher, int t_dtype, int64_t top,
+                            float temperature, const float *weight, float *loss, float *lse, void *dlogits,
+                            int64_t lddz, void *workspace, int64_t workspace_bytes, void *hip_stream) {
+  const int st = check_distill(logits, z_dtype, tokens, vocab, ldz, indices, index_bits, teacher, t_dtype, top,
+                               temperature, lse);
+  if (st != NVFP4_OK) return st;
+  if (!matrix_ok(tokens, vocab, lddz)) return NVFP4_ERR_SHAPE;
+  const int64_t need = nvfp4::distill_workspace_bytes(tokens, vocab);
+  if (workspace_bytes < need) return NVFP4_ERR_SHAPE;
+  if ((tokens > 0 && (!weight || !loss || !dlogits)) || (need > 0 && !workspace)) return NVFP4_ERR_NULL;
+  if (!aligned(weight, 4) || !aligned(loss, 4) || !aligned(dlogits, dtype_size(z_dtype)) || !aligned(workspace, 16))
+    return NVFP4_ERR_ALIGN;
+  if (overlap(logits, ldz, dlogits, lddz, tokens, vocab, dtype_size(z_dtype))) return NVFP4_ERR_SHAPE;
+  return hip_status(nvfp4::launch_distill(logits, z_dtype, tokens, vocab, ldz, indices, index_bits == 64, teacher,
+                                          t_dtype, (int)top, temperature, weight, loss, lse, dlogits, lddz, workspace,
+                                          true, (hipStream_t)hip_stream));
+}
+
 const char *nvfp4_status_string(int status) {
   switch (status) {
     case NVFP4_OK: return "ok";
@@ -280,6 +447,7 @@ const char *nvfp4_status_string(int status) {
     case NVFP4_ERR_ENUM: return "invalid enum value";
     case NVFP4_ERR_HIP: return "HIP launch failed";
     case NVFP4_ERR_ALIGN: return "misaligned pointer";
+    case NVFP4_ERR_VALUE: return "scalar argument out of range";
     default: return "unknown status";
   }
 }

@@ -51,6 +51,32 @@ hipError_t launch_mx8_gemm(const uint8_t *a_codes, const uint8_t *a_scales, cons
                            const uint8_t *b_scales, int64_t M, int64_t N, int64_t K, void *c, int c_dtype, int64_t ldc,
                            hipStream_t stream);
 
+// Layer norm over rows (stats in mean/rstd; amax, w, b, dw, db may be null;
+// dtypes 0 = f32, 1 = bf16; leading dimensions in elements).  The backward's
+// workspace: layer_norm_backward_workspace_bytes, 16-byte aligned.
+hipError_t launch_layer_norm(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void *w,
+                             const void *b, int w_dtype, float eps, void *y, int y_dtype, int64_t ldy, float *mean,
+                             float *rstd, float *amax, hipStream_t stream);
+int64_t layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+hipError_t launch_layer_norm_backward(const void *dy, int dy_dtype, int64_t lddy, const void *x, int x_dtype,
+                                      int64_t ldx, const float *mean, const float *rstd, const void *w, int w_dtype,
+                                      void *dx, int64_t lddx, void *dw, void *db, int g_dtype, void *workspace,
+                                      int64_t rows, int64_t cols, hipStream_t stream);
+
+// y[t][n] = sum_k x[t][k] w[n][k] with NVFP4 (mx = false) or MXFP4 weights.
+hipError_t launch_matvec(bool mx, const uint8_t *codes, const uint8_t *scales, const float *meta, int64_t N, int64_t K,
+                         const void *x, int x_dtype, int64_t tokens, int64_t ldx, void *y, int y_dtype, int64_t ldy,
+                         hipStream_t stream);
+
+// Distillation from a teacher's top logits: with stats, loss and lse are
+// formed from z; without, lse is read.  dz (with weight) may be null when
+// stats is set.  workspace: distill_workspace_bytes, 8-byte aligned.
+int distill_max_top();
+int64_t distill_workspace_bytes(int64_t rows, int64_t V);
+hipError_t launch_distill(const void *z, int z_dtype, int64_t rows, int64_t V, int64_t ldz, const void *idx, int idx64,
+                          const void *t, int t_dtype, int top, float tau, const float *weight, float *loss, float *lse,
+                          void *dz, int64_t lddz, void *workspace, bool stats, hipStream_t stream);
+
 hipError_t launch_dequantize(const uint8_t *codes, const uint8_t *scales, const float *meta, int64_t outer,
                              int64_t k, void *y, int y_dtype, hipStream_t stream);
 

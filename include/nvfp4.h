@@ -54,7 +54,8 @@ typedef enum {
                               size beyond a documented limit                */
     NVFP4_ERR_ENUM = -3,   /* unknown dtype / rounding / axis value           */
     NVFP4_ERR_HIP = -4,    /* a HIP launch failed                             */
-    NVFP4_ERR_ALIGN = -5   /* a pointer or leading dimension is misaligned    */
+    NVFP4_ERR_ALIGN = -5,  /* a pointer or leading dimension is misaligned    */
+    NVFP4_ERR_VALUE = -6   /* a scalar (eps, temperature) is out of range     */
 } nvfp4_status;
 
 typedef enum { NVFP4_F32 = 0, NVFP4_BF16 = 1 } nvfp4_dtype;
@@ -368,6 +369,119 @@ int mxfp8_quantize(const void *x, int x_dtype, int64_t rows, int64_t cols, int a
  */
 int mxfp8_gemm(const mxfp8_tensor *a, const mxfp8_tensor *b, void *c, int c_dtype,
                int64_t ldc, void *hip_stream);
+
+/*
+ * nvfp4_layer_norm -- layer norm of every row of x, the norm in front of a
+ * 4-bit linear layer:
+ *   m = sum x / cols,  v = sum (x - m)^2 / cols,  r = 1 / sqrt(v + eps)
+ *   y = (x - m) r weight + bias
+ *  x         : device, row-major [rows][ldx], x_dtype, ldx >= cols >= 1 (at
+ *              most 2^31 columns), aligned to its element only.
+ *  weight,
+ *  bias      : device, w_dtype [cols]; NULL = 1 and 0.
+ *  eps       : >= 0 and finite (NVFP4_ERR_VALUE otherwise).
+ *  y         : device, row-major [rows][ldy], y_dtype (bf16 = nearest even of
+ *              the binary32 value, rounded once).
+ *  mean,rstd : device, f32 [rows], m and r for the backward pass.
+ *  amax      : device, f32 [1], or NULL.  The maximum |y| as stored (on IEEE
+ *              bit patterns: NaN > Inf > finite; 0 when rows == 0), so that
+ *              nvfp4_quantize_amax of y on axis 1 with it equals
+ *              nvfp4_quantize bit for bit without the first read of y.
+ * All sums are binary32, the variance a sum of squared differences from the
+ * mean.  A row's non-finite values reach that row only.  Outputs must not
+ * overlap inputs.  Deterministic.  Enqueues one kernel, two with amax.
+ */
+int nvfp4_layer_norm(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void *weight,
+                     const void *bias, int w_dtype, float eps, void *y, int y_dtype, int64_t ldy, float *mean,
+                     float *rstd, float *amax, void *hip_stream);
+
+/*
+ * nvfp4_layer_norm_backward -- the gradients of nvfp4_layer_norm: with
+ * a = dy weight and h = (x - mean) rstd,
+ *   dx = rstd (a - sum(a) / cols - h sum(a h) / cols)     (x_dtype, [rows][lddx])
+ *   dweight = sum over rows of dy h,  dbias = sum over rows of dy   (g_dtype, [cols])
+ *  dweight,
+ *  dbias     : either may be NULL; zeros when rows == 0.
+ *  workspace : device, at least nvfp4_layer_norm_backward_workspace_bytes
+ *              (rows, cols) bytes, 16-byte aligned, contents ignored and
+ *              overwritten; calls that share one must not overlap in time.
+ * The sums over rows are binary32 partial sums of fixed sets of rows, added
+ * in a fixed order: deterministic on one device.  The workspace size is
+ * NVFP4_ERR_SHAPE for sizes that the call itself refuses.
+ */
+int nvfp4_layer_norm_backward(const void *dy, int dy_dtype, int64_t lddy, const void *x, int x_dtype, int64_t rows,
+                              int64_t cols, int64_t ldx, const float *mean, const float *rstd, const void *weight,
+                              int w_dtype, void *dx, int64_t lddx, void *dweight, void *dbias, int g_dtype,
+                              void *workspace, int64_t workspace_bytes, void *hip_stream);
+int64_t nvfp4_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * nvfp4_matvec, mxfp4_matvec -- a few rows of unquantized activations times
+ * a 4-bit weight matrix, the single-token form of the linear layer:
+ *   y[t][n] = g sum_k x[t][k] e2m1(code[n][k]) e4m3(scale[n][k/16])       (NVFP4)
+ *   y[t][n] =   sum_k x[t][k] e2m1(code[n][k]) 2^(scale[n][k/32] - 127)   (MXFP4)
+ *  w      : the weights [outer = N][k], quantized on axis 1 (W [out, in]).
+ *  x      : device, row-major [tokens][ldx], x_dtype, ldx >= k, aligned to
+ *           its element only.
+ *  y      : device, row-major [tokens][ldy], y_dtype, ldy >= N.
+ *  tokens : made for 1 to 16 (the weights are read once for every 16);
+ *           at most 1 048 560.  N <= 16 * INT32_MAX.
+ * Weights and bf16 x enter the product exactly; a float32 x to within
+ * 2^-133 of its value.  Sums are binary32.  k == 0 gives zeros.
+ * Deterministic.  Enqueues one kernel.
+ */
+int nvfp4_matvec(const nvfp4_tensor *w, const void *x, int x_dtype, int64_t tokens, int64_t ldx, void *y, int y_dtype,
+                 int64_t ldy, void *hip_stream);
+int mxfp4_matvec(const mxfp4_tensor *w, const void *x, int x_dtype, int64_t tokens, int64_t ldx, void *y, int y_dtype,
+                 int64_t ldy, void *hip_stream);
+
+/*
+ * nvfp4_distill_topk -- the distillation loss of a student's logits against
+ * a teacher's best logits, by which a model brought to 4 bits is trained:
+ *   p    = softmax(teacher / temperature) over the row's valid entries
+ *   lse  = log sum_v exp(logits_v / temperature)
+ *   loss = temperature^2 sum_k p_k (log p_k - (logits_{i_k} / temperature - lse))
+ *  logits  : device, row-major [tokens][ldz], z_dtype, ldz >= vocab,
+ *            1 <= vocab <= INT32_MAX, aligned to its element only.
+ *  indices : device, [tokens][top] of int32 or int64 (index_bits 32 or 64):
+ *            vocabulary indices i_k.  An entry is valid when its index lies
+ *            in [0, vocab) and its teacher logit is above -infinity; shorter
+ *            lists are filled up with -1.  0 <= top <= 1024.
+ *  teacher : device, t_dtype [tokens][top].
+ *  temperature : > 0 and finite (NVFP4_ERR_VALUE otherwise).
+ *  loss, lse   : device, f32 [tokens].
+ *  workspace   : device, nvfp4_distill_topk_workspace_bytes(tokens, vocab)
+ *                bytes, 16-byte aligned, contents ignored and overwritten;
+ *                calls that share one must not overlap in time.
+ * A row without a valid entry has loss 0 and gradient 0 whatever its logits.
+ * An index listed twice counts twice.  Logits of -infinity or of the type's
+ * lowest value are ordinary (a vocabulary mask).
+ *
+ * nvfp4_distill_topk_backward -- the gradient of sum_t dloss_t loss_t, from
+ * the lse of the forward call:
+ *   dlogits_v = dloss temperature (exp(logits_v / temperature - lse) - sum_{k: i_k = v} p_k)
+ *  dlogits : device, z_dtype, row-major [tokens][lddz]; must not overlap
+ *            logits (NVFP4_ERR_SHAPE).
+ *  Rows with dloss == 0 get zeros.
+ *
+ * nvfp4_distill_topk_step -- both in one call, for a program that knows its
+ * rows' weights beforehand: loss and lse as above and dlogits with
+ * dloss = weight.
+ * Deterministic.  Sums are binary32.
+ */
+int nvfp4_distill_topk(const void *logits, int z_dtype, int64_t tokens, int64_t vocab, int64_t ldz,
+                       const void *indices, int index_bits, const void *teacher, int t_dtype, int64_t top,
+                       float temperature, float *loss, float *lse, void *workspace, int64_t workspace_bytes,
+                       void *hip_stream);
+int nvfp4_distill_topk_backward(const void *logits, int z_dtype, int64_t tokens, int64_t vocab, int64_t ldz,
+                                const void *indices, int index_bits, const void *teacher, int t_dtype, int64_t top,
+                                float temperature, const float *lse, const float *dloss, void *dlogits, int64_t lddz,
+                                void *hip_stream);
+int nvfp4_distill_topk_step(const void *logits, int z_dtype, int64_t tokens, int64_t vocab, int64_t ldz,
+                            const void *indices, int index_bits, const void *teacher, int t_dtype, int64_t top,
+                            float temperature, const float *weight, float *loss, float *lse, void *dlogits,
+                            int64_t lddz, void *workspace, int64_t workspace_bytes, void *hip_stream);
+int64_t nvfp4_distill_topk_workspace_bytes(int64_t tokens, int64_t vocab);
 
 /*
  * nvfp4_probe_mfma -- measurement helper, not part of the method: launches
