@@ -105,8 +105,9 @@ inline bool overlap(const void *a, int64_t lda, const void *b, int64_t ldb, int6
 
 // The widest row layer norm takes (its column grids stay far inside 2^31).
 constexpr int64_t kMaxNormCols = 1LL << 31;
-// The matvec puts 16 weight rows on the grid's x dimension and 16 tokens on
-// its y dimension.
+// The matvec puts at least 16 weight rows on the grid's x dimension and 16
+// tokens on its y dimension; its offsets inside 64 weight rows are 32-bit,
+// as in the GEMMs (kMaxGemmK).
 constexpr int64_t kMaxMatvecRows = (int64_t)INT32_MAX * 16;
 constexpr int64_t kMaxMatvecTokens = 65535LL * 16;
 // The distillation kernels keep vocabulary indices in 32 bits.
@@ -114,14 +115,18 @@ constexpr int64_t kMaxVocab = INT32_MAX;
 
 int matvec_common(bool mx, const uint8_t *codes, const uint8_t *scales, const float *meta, int64_t N, int64_t K,
                   const void *x, int x_dtype, int64_t tokens, int64_t ldx, void *y, int y_dtype, int64_t ldy,
-                  void *hip_stream) {
+                  void *workspace, int64_t workspace_bytes, void *hip_stream) {
   if (!dtype_ok(x_dtype) || !dtype_ok(y_dtype)) return NVFP4_ERR_ENUM;
   if (!matrix_ok(tokens, K, ldx) || !matrix_ok(tokens, N, ldy)) return NVFP4_ERR_SHAPE;
-  if (N > kMaxMatvecRows || tokens > kMaxMatvecTokens) return NVFP4_ERR_SHAPE;
+  if (N > kMaxMatvecRows || tokens > kMaxMatvecTokens || K > kMaxGemmK) return NVFP4_ERR_SHAPE;
   if (tokens > 0 && N > 0 && (!y || (K > 0 && !x))) return NVFP4_ERR_NULL;
-  if (!aligned(x, dtype_size(x_dtype)) || !aligned(y, dtype_size(y_dtype))) return NVFP4_ERR_ALIGN;
+  const int64_t need = nvfp4::matvec_workspace_bytes(N, K, tokens, x_dtype == NVFP4_F32);
+  if (workspace_bytes < need) return NVFP4_ERR_SHAPE;
+  if (need > 0 && !workspace) return NVFP4_ERR_NULL;
+  if (!aligned(x, dtype_size(x_dtype)) || !aligned(y, dtype_size(y_dtype)) || !aligned(workspace, 16))
+    return NVFP4_ERR_ALIGN;
   return hip_status(nvfp4::launch_matvec(mx, codes, scales, meta, N, K, x, x_dtype, tokens, ldx, y, y_dtype, ldy,
-                                         (hipStream_t)hip_stream));
+                                         workspace, (hipStream_t)hip_stream));
 }
 
 // The arguments that the three distillation calls share.
@@ -365,22 +370,30 @@ int nvfp4_layer_norm_backward(const void *dy, int dy_dtype, int64_t lddy, const 
                                                       (hipStream_t)hip_stream));
 }
 
+int64_t nvfp4_matvec_workspace_bytes(int64_t n, int64_t k, int64_t tokens, int x_dtype) {
+  if (!dtype_ok(x_dtype)) return NVFP4_ERR_ENUM;
+  if (n < 0 || k < 0 || k % 16 != 0 || !matrix_ok(tokens, k, k) || !matrix_ok(tokens, n, n) || !count_ok(n, k) ||
+      n > kMaxMatvecRows || tokens > kMaxMatvecTokens || k > kMaxGemmK)
+    return NVFP4_ERR_SHAPE;
+  return nvfp4::matvec_workspace_bytes(n, k, tokens, x_dtype == NVFP4_F32);
+}
+
 int nvfp4_matvec(const nvfp4_tensor *w, const void *x, int x_dtype, int64_t tokens, int64_t ldx, void *y, int y_dtype,
-                 int64_t ldy, void *hip_stream) {
+                 int64_t ldy, void *workspace, int64_t workspace_bytes, void *hip_stream) {
   const int st = check_tensor(w);
   if (st != NVFP4_OK) return st;
   return matvec_common(false, w->codes, w->scales, w->meta, w->outer, w->k, x, x_dtype, tokens, ldx, y, y_dtype, ldy,
-                       hip_stream);
+                       workspace, workspace_bytes, hip_stream);
 }
 
 int mxfp4_matvec(const mxfp4_tensor *w, const void *x, int x_dtype, int64_t tokens, int64_t ldx, void *y, int y_dtype,
-                 int64_t ldy, void *hip_stream) {
+                 int64_t ldy, void *workspace, int64_t workspace_bytes, void *hip_stream) {
   if (!w) return NVFP4_ERR_NULL;
   if (w->outer < 0 || w->k < 0 || w->k % 32 != 0 || !count_ok(w->outer, w->k)) return NVFP4_ERR_SHAPE;
   if (w->outer > 0 && w->k > 0 && (!w->codes || !w->scales)) return NVFP4_ERR_NULL;
   if (!aligned(w->codes, 16)) return NVFP4_ERR_ALIGN;
   return matvec_common(true, w->codes, w->scales, nullptr, w->outer, w->k, x, x_dtype, tokens, ldx, y, y_dtype, ldy,
-                       hip_stream);
+                       workspace, workspace_bytes, hip_stream);
 }
 
 int64_t nvfp4_distill_topk_workspace_bytes(int64_t tokens, int64_t vocab) {

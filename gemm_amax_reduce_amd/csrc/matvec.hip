@@ -4,14 +4,21 @@
 //   NVFP4   y[t][n] = g * sum_k x[t][k] * e2m1(code[n][k]) * e4m3(scale[n][k/16])
 //   MXFP4   y[t][n] =     sum_k x[t][k] * e2m1(code[n][k]) * 2^(scale[n][k/32] - 127)
 //
-// The weights are read once and everything else is small, so the kernel is
-// bound by the N * K / 2 bytes of codes and the scales beside them.  A tile
-// is 16 weight rows; its waves split K in steps of 128 and multiply on the
-// 16x16x32 bf16 MFMA with the weights as the A operand and up to 16 tokens
-// as the B operand, so 1 to 16 tokens cost the same instructions.  A lane
-// holds 32 consecutive k of one weight row -- one 16-byte load of codes, and
-// whole scale groups -- and takes them in four MFMAs; the k order of an MFMA
-// is free as long as both operands agree on it.
+// The weights are read once and everything else is small, so the kernels are
+// bound by the N * K / 2 bytes of codes and the scales beside them.  Two
+// forms, both with 32 consecutive k of one weight row per lane and load (16
+// bytes of codes, whole scale groups):
+//
+//  * k_matvec_row, one token: a wave walks whole weight rows (contiguous
+//    runs of 1 KB per load), its share of x stays in registers, and a pair
+//    of products is one v_dot2_f32_bf16 on decoded codes; the block scale is
+//    applied to a block's sum.  About one instruction per weight.
+//  * k_matvec_tile, more tokens: tiles of 16 weight rows on the 16x16x32
+//    bf16 MFMA with the weights as the A operand and up to 16 tokens as the
+//    B operand, so 2 to 16 tokens cost the same.  A lane's 32 k enter four
+//    MFMAs; the k order of an MFMA is free as long as both operands agree.
+//    The block scale has to be multiplied into every weight here, about two
+//    instructions per NVFP4 weight.
 //
 // A decoded weight q * S has at most 6 significant bits (2 of E2M1, 4 of
 // E4M3) and an exponent in bf16's range, so it is exact in bf16, and so is
@@ -23,6 +30,8 @@
 #include "nvfp4_kernels.h"
 #include "row_common.h"
 
+#include <algorithm>
+
 namespace nvfp4 {
 
 namespace {
@@ -31,159 +40,542 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-typedef u32x4_t u32x4_a8 __attribute__((aligned(8)));
+typedef uint32_t u32x4_a8 __attribute__((ext_vector_type(4), aligned(8)));
+typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint16_t u16_a1 __attribute__((aligned(1)));
+typedef uint32_t u32_a1 __attribute__((aligned(1)));
+typedef uint32_t u32x2_a1 __attribute__((ext_vector_type(2), aligned(1)));
 
-constexpr int kTileRows = 16;    // weight rows of a tile
-constexpr int kTokens = 16;      // tokens of a tile
-constexpr int kStepK = 128;      // k of one wave step: 4 lanes a row, 32 each
-constexpr int kMvWaves = 8;
+// ------------------------------------------------------------- operands --
 
-// 8 codes (one word) times the group's scale as 8 bf16.
-template <bool MX> struct Decode;
-template <> struct Decode<false> {
-  __device__ __forceinline__ static u32x4_t run(uint32_t w, float s) {
+// The scales of a lane's 32 k, as loaded and as two factors (k 0-15, 16-31).
+template <bool MX> struct Scale;
+template <> struct Scale<false> {
+  static constexpr int kPerByte = 16;
+  uint32_t raw;
+  __device__ __forceinline__ void load(const uint8_t *p) { raw = *reinterpret_cast<const u16_a1 *>(p); }
+  __device__ __forceinline__ float lo() const { return __builtin_amdgcn_cvt_f32_fp8((int)raw, 0); }
+  __device__ __forceinline__ float hi() const { return __builtin_amdgcn_cvt_f32_fp8((int)raw, 1); }
+};
+template <> struct Scale<true> {
+  static constexpr int kPerByte = 32;
+  uint32_t raw;
+  __device__ __forceinline__ void load(const uint8_t *p) { raw = *p; }
+  // 2^(e - 127); e = 0 is the denormal 2^-127
+  __device__ __forceinline__ float lo() const { return __uint_as_float(raw ? raw << 23 : 0x00400000u); }
+  __device__ __forceinline__ float hi() const { return lo(); }
+};
+
+// 8 codes (one word) as 8 bf16: NVFP4 codes times the block scale s (exact
+// in f32 and in bf16), MXFP4 by the conversion's own power-of-two scale.
+template <bool MX> __device__ __forceinline__ bf16x8_t decode8(uint32_t w, float s) {
+  u32x4_t v;
+  if (MX) {
+    v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
+    v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
+    v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
+    v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
+  } else {
     const float2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
     const float2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
     const float2_t c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
     const float2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-    return (u32x4_t){pack_bf16(a.x * s, a.y * s), pack_bf16(b.x * s, b.y * s), pack_bf16(c.x * s, c.y * s),
-                     pack_bf16(d.x * s, d.y * s)};
+    v[0] = pack_bf16(a.x * s, a.y * s);
+    v[1] = pack_bf16(b.x * s, b.y * s);
+    v[2] = pack_bf16(c.x * s, c.y * s);
+    v[3] = pack_bf16(d.x * s, d.y * s);
   }
-};
-template <> struct Decode<true> {
-  __device__ __forceinline__ static u32x4_t run(uint32_t w, float s) {
-    const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
-    const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
-    const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
-    const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
-    return (u32x4_t){__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
-                     __builtin_bit_cast(uint32_t, d)};
+  return __builtin_bit_cast(bf16x8_t, v);
+}
+
+// 32 consecutive x of one token as loaded: 16-byte pieces at any alignment.
+template <typename X> struct Act {
+  static constexpr int kPieces = 32 * sizeof(X) / 16;
+  u32x4_t v[kPieces];
+  __device__ __forceinline__ void load(const X *p) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) v[i] = *reinterpret_cast<const u32x4_a2 *>((const char *)p + 16 * i);
+  }
+  // zero the first n of the 32
+  __device__ __forceinline__ void drop(int n) {
+    constexpr int kPerWord = 4 / sizeof(X);
+#pragma unroll
+    for (int i = 0; i < 4 * kPieces; ++i)
+      if (i * kPerWord < n) v[i >> 2][i & 3] = 0;      // n is a multiple of 16
   }
 };
 
-// 8 consecutive x as NP bf16 operands whose sum is x.
-template <typename X> struct Parts;
-template <> struct Parts<uint16_t> {
-  static constexpr int kCount = 1;
-  __device__ __forceinline__ static void load(u32x4_t *p, const uint16_t *x) {
-    p[0] = *reinterpret_cast<const u32x4_a2 *>(x);
-  }
-};
-template <> struct Parts<float> {
-  static constexpr int kCount = 3;
-  __device__ __forceinline__ static void load(u32x4_t *p, const float *x) {
-    const f32x4_a4 a = *reinterpret_cast<const f32x4_a4 *>(x), b = *reinterpret_cast<const f32x4_a4 *>(x + 4);
-    const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t hi[2], mid[2], lo[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float f = v[2 * i + j];
-        hi[j] = __float_as_uint(f);
-        // an Inf or NaN goes whole into the first part (its top bits with
-        // the quiet bit set for a NaN), the others are 0 then
-        const bool finite = (hi[j] & 0x7F800000u) != 0x7F800000u;
-        if (f != f) hi[j] |= 0x00400000u;
-        hi[j] &= 0xFFFF0000u;
-        const float r = finite ? f - __uint_as_float(hi[j]) : 0.0f;
-        mid[j] = __float_as_uint(r) & 0xFFFF0000u;
-        lo[j] = __float_as_uint(r - __uint_as_float(mid[j])) & 0xFFFF0000u;
-      }
-      p[0][i] = (hi[0] >> 16) | hi[1];
-      p[1][i] = (mid[0] >> 16) | mid[1];
-      p[2][i] = (lo[0] >> 16) | lo[1];
-    }
-  }
-};
+// The last load of a row may reach past its end: it is moved back to the
+// row's last 32 k, and the x of those already taken are zeroed.  Returns the
+// k to load from and how many of the 32 to drop (32 past the end).
+__device__ __forceinline__ int last_window(int64_t &k, int64_t K) {
+  const int64_t at = min(k, K - 32);
+  const int drop = (int)min(k - at, (int64_t)32);
+  k = at;
+  return drop;
+}
 
-template <bool MX, typename X>
-__global__ __launch_bounds__(64 * kMvWaves) void k_matvec(const uint8_t *codes, const uint8_t *scales,
-                                                          const float *meta, int64_t N, int64_t K, const X *x,
-                                                          int64_t tokens, int64_t ldx, void *y, int y_bf16,
-                                                          int64_t ldy) {
-  constexpr int kGroup = MX ? 32 : 16;
-  __shared__ f32x4_t part[kMvWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r = lane & 15, quarter = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * kTileRows, t0 = (int64_t)blockIdx.y * kTokens;
-  const int64_t n = min(n0 + r, N - 1);              // rows past the end repeat the last one and are not stored
-  const uint8_t *crow = codes + n * (K / 2);
-  const uint8_t *srow = scales + n * (K / kGroup);
-  const bool token = t0 + r < tokens;
-  const X *xrow = x + (token ? t0 + r : 0) * ldx;
-  f32x4_t acc = {0, 0, 0, 0};
-  for (int64_t k = (int64_t)wave * kStepK + quarter * 32; k - quarter * 32 < K; k += kMvWaves * kStepK) {
-    u32x4_t c = {0, 0, 0, 0};
-    float s0 = 0.0f, s1 = 0.0f;
-    int words = 0;                                    // groups of 8 k that lie inside the row
-    if (k + 32 <= K) {
-      c = *reinterpret_cast<const u32x4_a8 *>(crow + k / 2);
-      words = 4;
-    } else if (!MX && k + 16 <= K) {
-      const u32x2_t h = *reinterpret_cast<const u32x2_t *>(crow + k / 2);
-      c = (u32x4_t){h[0], h[1], 0, 0};
-      words = 2;
+__device__ __forceinline__ void store_y(void *y, int y_bf16, int64_t at, float v) {
+  if (y_bf16) ((uint16_t *)y)[at] = (uint16_t)pack_bf16(v, 0.0f);
+  else ((float *)y)[at] = v;
+}
+
+// ------------------------------------------------------ 2 to 16 tokens --
+
+constexpr int kStepK = 128;      // k of one MFMA step: 4 lanes a row, 32 each
+constexpr int kTokens = 16;      // tokens of a launch's y index
+constexpr int kTileWaves = 12;   // waves of a workgroup, at most
+constexpr int kTurnBytes = 4096; // 16 columns x 128 k of bf16
+
+// The B operand's columns.  bf16: one column a token.  float32: three
+// columns a token, the parts hi, mid and lo, so that one MFMA serves five
+// tokens and the parts are added at the end.
+template <typename X> constexpr int columns() { return sizeof(X) == 2 ? 1 : 3; }
+
+// 8 consecutive x as the column's bf16 values, zero from `left` on (left a
+// multiple of 16, so all or none).
+__device__ __forceinline__ u32x4_t column8(const uint16_t *x, int64_t left, int) {
+  if (left <= 0) return (u32x4_t){0, 0, 0, 0};
+  return *reinterpret_cast<const u32x4_a2 *>(x);
+}
+__device__ __forceinline__ u32x4_t column8(const float *x, int64_t left, int part) {
+  u32x4_t out = {0, 0, 0, 0};
+  if (left <= 0) return out;
+  const f32x4_a4 a = *reinterpret_cast<const f32x4_a4 *>(x), b = *reinterpret_cast<const f32x4_a4 *>(x + 4);
+  const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float f = v[2 * i + h];
+      // an Inf or NaN goes whole into the first part (with the quiet bit
+      // set for a NaN, whose payload may lie below), the others are 0 then
+      const bool finite = (__float_as_uint(f) & 0x7F800000u) != 0x7F800000u;
+      const uint32_t hi = (__float_as_uint(f) | (f != f ? 0x00400000u : 0u)) & 0xFFFF0000u;
+      const float r = finite ? f - __uint_as_float(hi) : 0.0f;
+      const float mid = __uint_as_float(__float_as_uint(r) & 0xFFFF0000u);
+      w[h] = part == 0 ? hi : __float_as_uint(part == 1 ? r : r - mid);
     }
-    if (MX) {
-      // 2^(e - 127) as a float; e = 0 is the denormal 2^-127
-      if (words) {
-        const uint32_t e = srow[k / 32];
-        s0 = s1 = __uint_as_float(e ? e << 23 : 0x00400000u);
+    out[i] = __builtin_amdgcn_perm(w[1], w[0], 0x07060302u);
+  }
+  return out;
+}
+
+// The codes and scales of one tile of 16 weight rows, SW steps, as loaded.
+// The scales of a whole slice come as one run of SB bytes a row (4 lanes a
+// row) and reach the lanes that use them through LDS; where the slice passes
+// the row's end every lane loads its own.
+template <bool MX, int SW> struct Tile {
+  static constexpr int kG = Scale<MX>::kPerByte;
+  static constexpr int kSB = SW * kStepK / kG;
+  u32x4_t c[SW];
+  u32x4_t s;
+  __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales, int64_t tile, int64_t N, int64_t K,
+                                       const uint32_t *k, bool whole, uint32_t k0, int lane) {
+    const int64_t n0 = tile * 16;
+    const uint32_t last = (uint32_t)min(N - 1 - n0, (int64_t)15);     // rows past the end repeat the last one
+    const uint8_t *cb = codes + n0 * (K / 2), *sb = scales + n0 * (K / kG);
+    const uint32_t row = min((uint32_t)lane & 15u, last);
+#pragma unroll
+    for (int i = 0; i < SW; ++i) c[i] = *reinterpret_cast<const u32x4_a8 *>(cb + (row * (uint32_t)(K / 2) + k[i] / 2));
+    if (whole) {
+      const uint8_t *p = sb + (min((uint32_t)lane >> 2, last) * (uint32_t)(K / kG) + k0 / kG + (lane & 3) * (kSB / 4));
+      if (kSB == 32) {
+        const u32x2_a1 v = *reinterpret_cast<const u32x2_a1 *>(p);
+        s = (u32x4_t){v[0], v[1], 0, 0};
+      } else if (kSB == 16) {
+        s = (u32x4_t){*reinterpret_cast<const u32_a1 *>(p), 0, 0, 0};
+      } else {
+        s = (u32x4_t){*reinterpret_cast<const u16_a1 *>(p), 0, 0, 0};
       }
     } else {
-      if (words) s0 = e4m3_to_f32(srow[k / 16]);
-      if (words == 4) s1 = e4m3_to_f32(srow[k / 16 + 1]);
-    }
+      s = (u32x4_t){0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      u32x4_t b[Parts<X>::kCount];
-#pragma unroll
-      for (int p = 0; p < Parts<X>::kCount; ++p) b[p] = (u32x4_t){0, 0, 0, 0};
-      if (token && j < words) Parts<X>::load(b, xrow + k + 8 * j);
-      const bf16x8_t a = __builtin_bit_cast(bf16x8_t, Decode<MX>::run(c[j], j < 2 ? s0 : s1));
-#pragma unroll
-      for (int p = 0; p < Parts<X>::kCount; ++p)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, b[p]), acc, 0, 0, 0);
+      for (int i = 0; i < SW; ++i) {
+        Scale<MX> t;
+        t.load(sb + (row * (uint32_t)(K / kG) + k[i] / kG));
+        s[i] = t.raw;
+      }
     }
   }
-  // lane: token t0 + (lane & 15), weight rows n0 + 4 * (lane >> 4) + i
-  part[wave][lane] = acc;
-  __syncthreads();
-  if (wave == 0 && token) {
-    for (int w = 1; w < kMvWaves; ++w) acc += part[w][lane];
-    const float g = MX ? 1.0f : meta[1];
-    const int64_t nn = n0 + 4 * quarter;
+  // the lane's scales of every step
+  __device__ __forceinline__ void spread(Scale<MX> *out, char *lds, bool whole, int lane) const {
+    if (!whole) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (nn + i >= N) break;
-      const float v = acc[i] * g;
-      const int64_t at = (t0 + r) * ldy + nn + i;
-      if (y_bf16) ((uint16_t *)y)[at] = (uint16_t)pack_bf16(v, 0.0f);
-      else ((float *)y)[at] = v;
+      for (int i = 0; i < SW; ++i) out[i].raw = s[i];
+      return;
     }
+    // (byte copies: what is stored as words is read as bytes and pairs)
+    __builtin_memcpy(lds + lane * (kSB / 4), &s, kSB / 4);
+    const char *at = lds + (lane & 15) * kSB + (lane >> 4) * (32 / kG);
+#pragma unroll
+    for (int i = 0; i < SW; ++i) {
+      out[i].raw = 0;
+      __builtin_memcpy(&out[i].raw, at + i * (kStepK / kG), 32 / kG);
+    }
+  }
+};
+
+// A workgroup holds the columns of all its tokens over its range of K in
+// registers -- each wave a slice of SW steps -- and walks tiles of 16 weight
+// rows, blockIdx.x, blockIdx.x + gridDim.x, ...: only codes and scales move
+// in the loop.  The waves' sums of a tile meet in LDS and one wave, another
+// one each time, adds and stores them.  With more than one range of K
+// (gridDim.z) the sums go to `partial` [z][token][n] instead.
+// SL: 16-column slabs; grid: (tile walkers, tokens / 16, ranges of K).
+template <bool MX, typename X, int SL, int SW>
+__global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *codes, const uint8_t *scales,
+                                                                 const float *meta, int64_t N, int64_t K, const X *x,
+                                                                 int64_t tokens, int64_t ldx, void *y, int y_bf16,
+                                                                 int64_t ldy, float *partial) {
+  constexpr int kC = columns<X>();
+  extern __shared__ __align__(16) char lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  const int row = lane & 15, quarter = lane >> 4;
+  const int64_t t0 = (int64_t)blockIdx.y * kTokens;
+  const int live = (int)min(tokens - t0, (int64_t)kTokens);
+  const int64_t k0 = ((int64_t)blockIdx.z * waves + wave) * (SW * kStepK);
+  const bool whole = k0 + SW * kStepK <= K;
+
+  // x into registers, by way of LDS: an MFMA's lane wants 8 k of its own
+  // column, which as a load would touch 64 places; so 64-byte runs of k are
+  // loaded, 4 lanes a column, and turned in a region of the wave's own.
+  // Piece (column, p) of run i lies at slot 4 column + (p ^ (column / 4)):
+  // stores and reads then fall on all banks.
+  bf16x8_t b[SW][4][SL];
+  uint32_t k[SW];
+  {
+    char *const turn = lds + wave * kTurnBytes;
+    const int col = lane >> 2, piece = lane & 3;
+    const int write = 16 * (4 * col + (piece ^ (col >> 2)));
+#pragma unroll
+    for (int s = 0; s < SW; ++s) {
+      const int64_t ks = k0 + s * kStepK;
+      int64_t at = ks + quarter * 32;
+      const int drop = last_window(at, K);
+      k[s] = (uint32_t)at;
+#pragma unroll
+      for (int l = 0; l < SL; ++l) {
+        const int v = min(16 * l + col, live * kC - 1);     // columns past the last repeat it: they are independent
+        const X *xr = x + (t0 + v / kC) * ldx;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t kk = ks + 32 * i + 8 * piece;
+          *reinterpret_cast<u32x4_t *>(turn + i * 1024 + write) = column8(xr + kk, K - kk, v % kC);
+        }
+        // a lane moved back by 16 finds its x in the other half
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int p = drop == 16 ? j ^ 2 : j;
+          b[s][j][l] = *reinterpret_cast<const bf16x8_t *>(turn + quarter * 1024 + 16 * (4 * row + (p ^ (row >> 2))));
+        }
+      }
+    }
+  }
+  __syncthreads();
+
+  char *const scale_lds = lds + wave * 512;
+  f32x4_t *const part = reinterpret_cast<f32x4_t *>(lds + waves * 512);       // [2][waves][SL][64]
+  const float g = MX ? 1.0f : meta[1];
+  const int64_t tiles = (N + 15) / 16;
+  const auto work = [&](const Tile<MX, SW> &t, int64_t tile, int turn) {
+    constexpr int kA = SL == 1 ? 2 : 1;       // one slab: two accumulators, so that MFMAs do not wait for each other
+    f32x4_t acc[kA][SL];
+#pragma unroll
+    for (int l = 0; l < SL; ++l) acc[0][l] = acc[kA - 1][l] = (f32x4_t){0, 0, 0, 0};
+    Scale<MX> sc[SW];
+    t.spread(sc, scale_lds, whole, lane);
+#pragma unroll
+    for (int s = 0; s < SW; ++s)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bf16x8_t a = decode8<MX>(t.c[s][j], j < 2 ? sc[s].lo() : sc[s].hi());
+#pragma unroll
+        for (int l = 0; l < SL; ++l)
+          acc[j % kA][l] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[s][j][l], acc[j % kA][l], 0, 0, 0);
+      }
+    f32x4_t *const mine = part + (turn & 1) * waves * SL * 64;
+#pragma unroll
+    for (int l = 0; l < SL; ++l) mine[(wave * SL + l) * 64 + lane] = kA == 2 ? acc[0][l] + acc[kA - 1][l] : acc[0][l];
+    __syncthreads();
+    if (wave != turn % waves || row >= live) return;
+    // lane: token t0 + row, weight rows 16 tile + 4 quarter + i
+    f32x4_t sum = {0, 0, 0, 0};
+    for (int w = 0; w < waves; ++w)
+#pragma unroll
+      for (int p = 0; p < kC; ++p) {
+        const int v = row * kC + p;
+        sum += mine[(w * SL + v / 16) * 64 + quarter * 16 + v % 16];
+      }
+    const int64_t n = 16 * tile + 4 * quarter;
+    if (n >= N) return;
+    if (partial) {
+      float *o = partial + ((int64_t)blockIdx.z * tokens + t0 + row) * N + n;
+      if (n + 4 <= N) *reinterpret_cast<f32x4_a4 *>(o) = sum;
+      else
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (n + i < N) o[i] = sum[i];
+      return;
+    }
+    const int64_t at = (t0 + row) * ldy + n;
+    if (n + 4 <= N && y_bf16) {
+      *reinterpret_cast<u32x2_a2 *>((uint16_t *)y + at) =
+          (u32x2_t){pack_bf16(sum[0] * g, sum[1] * g), pack_bf16(sum[2] * g, sum[3] * g)};
+    } else if (n + 4 <= N) {
+      *reinterpret_cast<f32x4_a4 *>((float *)y + at) = sum * g;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (n + i < N) store_y(y, y_bf16, at + i, sum[i] * g);
+    }
+  };
+
+  const uint32_t ku = (uint32_t)k0;
+  const int64_t step = gridDim.x;
+  Tile<MX, SW> a, c;
+  int64_t t = blockIdx.x;
+  a.load(codes, scales, t, N, K, k, whole, ku, lane);
+  // two tiles in flight; the last loads repeat a tile of the walk
+  for (int turn = 0;; turn += 2) {
+    const int64_t t1 = t + step, t2 = t1 + step;
+    c.load(codes, scales, t1 < tiles ? t1 : t, N, K, k, whole, ku, lane);
+    work(a, t, turn);
+    if (t1 >= tiles) break;
+    a.load(codes, scales, t2 < tiles ? t2 : t1, N, K, k, whole, ku, lane);
+    work(c, t1, turn + 1);
+    if (t2 >= tiles) break;
+    t = t2;
   }
 }
 
+// y = g times the sum of the ranges' partial sums, in their order.
+__global__ __launch_bounds__(256) void k_matvec_join(const float *partial, int ranges, const float *meta, int64_t N,
+                                                     int64_t tokens, void *y, int y_bf16, int64_t ldy) {
+  const float g = meta ? meta[1] : 1.0f;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < N * tokens; i += (int64_t)gridDim.x * 256) {
+    float sum = 0.0f;
+    for (int z = 0; z < ranges; ++z) sum += partial[z * tokens * N + i];
+    store_y(y, y_bf16, i / N * ldy + i % N, sum * g);
+  }
+}
+
+// K = 16, less than a lane's load (or 0): one thread an output.
+template <typename X>
+__global__ __launch_bounds__(256) void k_matvec_short(const uint8_t *codes, const uint8_t *scales, const float *meta,
+                                                      int64_t N, int64_t K, const X *x, int64_t tokens, int64_t ldx,
+                                                      void *y, int y_bf16, int64_t ldy) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < N * tokens; i += (int64_t)gridDim.x * 256) {
+    const int64_t n = i % N, t = i / N;
+    float sum = 0.0f;
+    if (K) {
+      const u32x2_t c = *reinterpret_cast<const u32x2_t *>(codes + n * 8);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float2_t q = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4((c[k >> 3] >> (4 * (k & 7))) & 15u, 1.0f, 0);
+        sum = __builtin_fmaf(to_float(x[t * ldx + k]), q.x, sum);
+      }
+      sum *= e4m3_to_f32(scales[n]) * meta[1];
+    }
+    store_y(y, y_bf16, t * ldy + n, sum);
+  }
+}
+constexpr int64_t kFlatGrid = 1 << 16;
+
+// ------------------------------------------------------------ one token --
+
+// A lane's products with 32 weights of one row: sum x q s.
+template <bool MX> __device__ __forceinline__ float dot32(const u32x4_t &c, const Scale<MX> &s, const Act<uint16_t> &x) {
+  float p[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bf16x8_t q = decode8<true>(c[j], 1.0f);
+    const u32x4_t qw = __builtin_bit_cast(u32x4_t, q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[j >> 1] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, (uint32_t)qw[i]),
+                                                  __builtin_bit_cast(bf16x2_t, (uint32_t)x.v[j][i]), p[j >> 1], false);
+  }
+  return MX ? (p[0] + p[1]) * s.lo() : __builtin_fmaf(p[0], s.lo(), p[1] * s.hi());
+}
+template <bool MX> __device__ __forceinline__ float dot32(const u32x4_t &c, const Scale<MX> &s, const Act<float> &x) {
+  float p[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2_t q[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[j], 1.0f, 0),
+                           __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[j], 1.0f, 1),
+                           __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[j], 1.0f, 2),
+                           __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[j], 1.0f, 3)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u32x4_t &v = x.v[2 * j + (i >> 1)];
+      p[j >> 1] = __builtin_fmaf(q[i].x, __uint_as_float(v[2 * (i & 1)]), p[j >> 1]);
+      p[j >> 1] = __builtin_fmaf(q[i].y, __uint_as_float(v[2 * (i & 1) + 1]), p[j >> 1]);
+    }
+  }
+  return MX ? (p[0] + p[1]) * s.lo() : __builtin_fmaf(p[0], s.lo(), p[1] * s.hi());
+}
+
+constexpr int kRowWaves = 4;
+constexpr int kWaveK = 64 * 32;         // k of one wave load
+
+// One weight row's share of a wave: J loads.
+template <bool MX, int J> struct RowPart {
+  u32x4_t c[J];
+  Scale<MX> s[J];
+  __device__ __forceinline__ void load(const uint8_t *cr, const uint8_t *sr, const uint32_t *k) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      c[j] = *reinterpret_cast<const u32x4_a8 *>(cr + k[j] / 2);
+      s[j].load(sr + k[j] / Scale<MX>::kPerByte);
+    }
+  }
+};
+
+// The workgroup's four waves hold J loads of x each: WK waves share a row
+// (K <= WK * J * 2048), 4 / WK rows are worked on at a time.
+template <bool MX, typename X, int J, int WK>
+__global__ __launch_bounds__(64 * kRowWaves) void k_matvec_row(const uint8_t *codes, const uint8_t *scales,
+                                                               const float *meta, int64_t N, int64_t K, const X *x,
+                                                               void *y, int y_bf16) {
+  constexpr int kRows = kRowWaves / WK;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kw = wave % WK;
+  uint32_t k[J];
+  Act<X> xv[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    int64_t at = (int64_t)((kw * J + j) * 64 + lane) * 32;
+    const int drop = last_window(at, K);
+    k[j] = (uint32_t)at;
+    xv[j].load(x + at);
+    xv[j].drop(drop);
+  }
+  const float g = MX ? 1.0f : meta[1];
+  const int64_t stride = (int64_t)gridDim.x * kRows;
+  const int64_t first = (int64_t)blockIdx.x * kRows + wave / WK;
+  __shared__ float share[2][kRowWaves];
+  RowPart<MX, J> a, b;
+  const auto load = [&](RowPart<MX, J> &p, int64_t n) {
+    n = min(n, N - 1);
+    p.load(codes + n * (K / 2), scales + n * (K / Scale<MX>::kPerByte), k);
+  };
+  const auto finish = [&](const RowPart<MX, J> &p, int64_t n, int turn) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) sum += dot32<MX>(p.c[j], p.s[j], xv[j]);
+    sum = wave_sum(sum);
+    if (WK > 1) {
+      if (lane == 0) share[turn][wave] = sum;
+      __syncthreads();
+      sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WK; ++w) sum += share[turn][wave - kw + w];
+    }
+    if (lane == 0 && kw == 0 && n < N) store_y(y, y_bf16, n, sum * g);
+  };
+  // the workgroup's waves make the same number of turns (barriers)
+  load(a, first);
+  for (int64_t n = first; n - wave / WK < N; n += 2 * stride) {
+    load(b, n + stride);
+    finish(a, n, 0);
+    load(a, n + 2 * stride);
+    finish(b, n + stride, 1);
+  }
+}
+
+// ------------------------------------------------------------- launches --
+
+// How a product of more than one token is cut: SL slabs of 16 columns, SW
+// steps a wave (16 SL SW registers of x), `waves` of them a workgroup,
+// `ranges` of K, and the workgroups that walk the tiles of one range.
+struct Cut {
+  int sl, sw, waves, ranges, walkers;
+};
+Cut cut_for(int64_t N, int64_t K, int64_t tokens, bool f32) {
+  Cut c;
+  const int cols = (int)std::min<int64_t>(tokens, kTokens) * (f32 ? 3 : 1);
+  c.sl = (cols + 15) / 16;
+  c.sw = c.sl == 1 ? 4 : 2;
+  const int64_t slices = (K + c.sw * kStepK - 1) / (c.sw * kStepK);
+  const int most = c.sl == 3 ? 9 : kTileWaves;          // (9 waves' sums of three slabs fill 64 KB of LDS)
+  c.ranges = (int)((slices + most - 1) / most);
+  c.waves = (int)((slices + c.ranges - 1) / c.ranges);
+  // one round of workgroups: as many as fit the CUs' waves, the tiles dealt evenly
+  const int64_t tiles = (N + 15) / 16, blocks = (tokens + kTokens - 1) / kTokens;
+  const int64_t room = (int64_t)device_cus() * (kTileWaves / c.waves);
+  const int64_t want = std::min(tiles, std::max<int64_t>(1, room / (c.ranges * blocks)));
+  const int64_t per = (tiles + want - 1) / want;
+  c.walkers = (int)((tiles + per - 1) / per);
+  return c;
+}
+
+template <bool MX, typename X, int SL, int SW>
+void tile(const Cut &c, const uint8_t *codes, const uint8_t *scales, const float *meta, int64_t N, int64_t K, const X *x,
+          int64_t tokens, int64_t ldx, void *y, int y_bf16, int64_t ldy, void *workspace, hipStream_t stream) {
+  const dim3 grid((unsigned)c.walkers, (unsigned)((tokens + kTokens - 1) / kTokens), (unsigned)c.ranges);
+  const size_t lds = c.waves * std::max<size_t>(kTurnBytes, 512 + 2 * SL * 64 * sizeof(f32x4_t));
+  float *partial = c.ranges > 1 ? (float *)workspace : nullptr;
+  k_matvec_tile<MX, X, SL, SW><<<grid, 64 * c.waves, lds, stream>>>(codes, scales, meta, N, K, x, tokens, ldx, y,
+                                                                    y_bf16, ldy, partial);
+  if (partial)
+    k_matvec_join<<<(unsigned)std::min(kFlatGrid, (N * tokens + 255) / 256), 256, 0, stream>>>(
+        partial, c.ranges, MX ? nullptr : meta, N, tokens, y, y_bf16, ldy);
+}
+
+template <bool MX, typename X, int J, int WK>
+void rows(const uint8_t *codes, const uint8_t *scales, const float *meta, int64_t N, int64_t K, const X *x, void *y,
+          int y_bf16, hipStream_t stream) {
+  const int64_t per = kRowWaves / WK;
+  const unsigned grid = (unsigned)std::min<int64_t>((N + per - 1) / per, (int64_t)device_cus() * 4);
+  k_matvec_row<MX, X, J, WK><<<grid, 64 * kRowWaves, 0, stream>>>(codes, scales, meta, N, K, x, y, y_bf16);
+}
+
+// One token whose x fits the registers of a workgroup.
+bool one_token(int64_t tokens, int64_t K) { return tokens == 1 && K >= 32 && K <= 4 * 3 * kWaveK; }
+
 template <bool MX, typename X>
-void matvec(const uint8_t *codes, const uint8_t *scales, const float *meta, int64_t N, int64_t K, const void *x,
-            int64_t tokens, int64_t ldx, void *y, int y_bf16, int64_t ldy, hipStream_t stream) {
-  const dim3 grid((unsigned)((N + kTileRows - 1) / kTileRows), (unsigned)((tokens + kTokens - 1) / kTokens));
-  k_matvec<MX, X><<<grid, 64 * kMvWaves, 0, stream>>>(codes, scales, meta, N, K, (const X *)x, tokens, ldx, y, y_bf16,
-                                                      ldy);
+void matvec(const uint8_t *codes, const uint8_t *scales, const float *meta, int64_t N, int64_t K, const void *xv,
+            int64_t tokens, int64_t ldx, void *y, int yb, int64_t ldy, void *ws, hipStream_t st) {
+  const X *x = (const X *)xv;
+  if (one_token(tokens, K)) {
+    if (K <= kWaveK) rows<MX, X, 1, 1>(codes, scales, meta, N, K, x, y, yb, st);
+    else if (K <= 2 * kWaveK) rows<MX, X, 2, 1>(codes, scales, meta, N, K, x, y, yb, st);
+    else if (K <= 3 * kWaveK) rows<MX, X, 3, 1>(codes, scales, meta, N, K, x, y, yb, st);
+    else if (K <= 8 * kWaveK) rows<MX, X, 2, 4>(codes, scales, meta, N, K, x, y, yb, st);
+    else rows<MX, X, 3, 4>(codes, scales, meta, N, K, x, y, yb, st);
+    return;
+  }
+  if (K < 32) {
+    const unsigned grid = (unsigned)std::min(kFlatGrid, (N * tokens + 255) / 256);
+    k_matvec_short<X><<<grid, 256, 0, st>>>(codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy);
+    return;
+  }
+  const Cut c = cut_for(N, K, tokens, sizeof(X) == 4);
+  if (c.sl == 1) tile<MX, X, 1, 4>(c, codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy, ws, st);
+  else if (sizeof(X) == 4 && c.sl == 2) tile<MX, float, 2, 2>(c, codes, scales, meta, N, K, (const float *)xv, tokens, ldx, y, yb, ldy, ws, st);
+  else if (sizeof(X) == 4) tile<MX, float, 3, 2>(c, codes, scales, meta, N, K, (const float *)xv, tokens, ldx, y, yb, ldy, ws, st);
 }
 
 }  // namespace
 
+int64_t matvec_workspace_bytes(int64_t N, int64_t K, int64_t tokens, bool f32) {
+  if (N <= 0 || tokens <= 0 || K < 32 || one_token(tokens, K)) return 0;
+  const Cut c = cut_for(N, K, tokens, f32);
+  return c.ranges > 1 ? 4 * c.ranges * tokens * N : 0;
+}
+
 hipError_t launch_matvec(bool mx, const uint8_t *codes, const uint8_t *scales, const float *meta, int64_t N, int64_t K,
                          const void *x, int x_dtype, int64_t tokens, int64_t ldx, void *y, int y_dtype, int64_t ldy,
-                         hipStream_t stream) {
+                         void *ws, hipStream_t stream) {
   if (N > 0 && tokens > 0) {
     const int yb = y_dtype == 1;
-    if (mx && x_dtype == 1) matvec<true, uint16_t>(codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy, stream);
-    else if (mx) matvec<true, float>(codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy, stream);
-    else if (x_dtype == 1) matvec<false, uint16_t>(codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy, stream);
-    else matvec<false, float>(codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy, stream);
+    if (mx && x_dtype == 1) matvec<true, uint16_t>(codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy, ws, stream);
+    else if (mx) matvec<true, float>(codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy, ws, stream);
+    else if (x_dtype == 1) matvec<false, uint16_t>(codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy, ws, stream);
+    else matvec<false, float>(codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy, ws, stream);
   }
   return hipGetLastError();
 }

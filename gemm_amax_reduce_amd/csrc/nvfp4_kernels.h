@@ -64,9 +64,11 @@ hipError_t launch_layer_norm_backward(const void *dy, int dy_dtype, int64_t lddy
                                       int64_t rows, int64_t cols, hipStream_t stream);
 
 // y[t][n] = sum_k x[t][k] w[n][k] with NVFP4 (mx = false) or MXFP4 weights.
+// ws: matvec_workspace_bytes, 16-byte aligned (none where that is 0).
+int64_t matvec_workspace_bytes(int64_t N, int64_t K, int64_t tokens, bool f32);
 hipError_t launch_matvec(bool mx, const uint8_t *codes, const uint8_t *scales, const float *meta, int64_t N, int64_t K,
                          const void *x, int x_dtype, int64_t tokens, int64_t ldx, void *y, int y_dtype, int64_t ldy,
-                         hipStream_t stream);
+                         void *ws, hipStream_t stream);
 
 // Distillation from a teacher's top logits: with stats, loss and lse are
 // formed from z; without, lse is read.  dz (with weight) may be null when

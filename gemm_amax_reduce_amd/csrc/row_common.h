@@ -135,15 +135,29 @@ __device__ __forceinline__ void load_param8(float *v, const void *p, int is_bf16
   }
 }
 
+// Reductions over the wave, the result in every lane: four exchanges inside a
+// row of 16 lanes ride on the operation (DPP: pairs, quads, mirrored halves,
+// mirrored rows), then the rows and the halves are swapped.  Both operands
+// of a commutative operation only change places between lanes, so every
+// lane has the same bits.
+template <int CTRL> __device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+template <typename Op> __device__ __forceinline__ float wave_reduce(float v, Op op) {
+  v = op(v, dpp<0xB1>(v));      // quad_perm 1,0,3,2
+  v = op(v, dpp<0x4E>(v));      // quad_perm 2,3,0,1
+  v = op(v, dpp<0x141>(v));     // row_half_mirror
+  v = op(v, dpp<0x140>(v));     // row_mirror
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_int(v), __float_as_int(v), false, false);
+  v = op(__int_as_float(p[0]), __int_as_float(p[1]));
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_int(v), __float_as_int(v), false, false);
+  return op(__int_as_float(q[0]), __int_as_float(q[1]));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+  return wave_reduce(v, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ float wave_fmax(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
-  return v;
+  return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // The sum over the workgroup, in every thread; the order of additions is

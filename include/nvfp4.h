@@ -425,15 +425,22 @@ int64_t nvfp4_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
  *           its element only.
  *  y      : device, row-major [tokens][ldy], y_dtype, ldy >= N.
  *  tokens : made for 1 to 16 (the weights are read once for every 16);
- *           at most 1 048 560.  N <= 16 * INT32_MAX.
+ *           at most 1 048 560.  N <= 16 * INT32_MAX, k <= 2^25 - 16.
+ *  workspace : device, at least nvfp4_matvec_workspace_bytes(N, k, tokens,
+ *           x_dtype) bytes (for both formats), 16-byte aligned, contents
+ *           ignored and overwritten; often 0, and NULL will do then.  Calls
+ *           that share one must not overlap in time.
  * Weights and bf16 x enter the product exactly; a float32 x to within
  * 2^-133 of its value.  Sums are binary32.  k == 0 gives zeros.
- * Deterministic.  Enqueues one kernel.
+ * Deterministic on one device.  Enqueues one kernel, or two where there is a
+ * workspace.  The workspace size is NVFP4_ERR_SHAPE / NVFP4_ERR_ENUM for
+ * arguments that the calls refuse.
  */
 int nvfp4_matvec(const nvfp4_tensor *w, const void *x, int x_dtype, int64_t tokens, int64_t ldx, void *y, int y_dtype,
-                 int64_t ldy, void *hip_stream);
+                 int64_t ldy, void *workspace, int64_t workspace_bytes, void *hip_stream);
 int mxfp4_matvec(const mxfp4_tensor *w, const void *x, int x_dtype, int64_t tokens, int64_t ldx, void *y, int y_dtype,
-                 int64_t ldy, void *hip_stream);
+                 int64_t ldy, void *workspace, int64_t workspace_bytes, void *hip_stream);
+int64_t nvfp4_matvec_workspace_bytes(int64_t n, int64_t k, int64_t tokens, int x_dtype);
 
 /*
  * nvfp4_distill_topk -- the distillation loss of a student's logits against

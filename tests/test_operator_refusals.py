@@ -70,7 +70,7 @@ def test_workspace_sizes(L):
     assert L.nvfp4_distill_topk_workspace_bytes(0, 64) == 0
 
 
-MV = dict(x=FAKE, xd=1, tokens=2, ldx=64, y=FAKE, yd=0, ldy=8, stream=None)
+MV = dict(x=FAKE, xd=1, tokens=2, ldx=64, y=FAKE, yd=0, ldy=8, ws=None, bytes=0, stream=None)
 
 
 @_no_gpu
@@ -78,7 +78,7 @@ MV = dict(x=FAKE, xd=1, tokens=2, ldx=64, y=FAKE, yd=0, ldy=8, stream=None)
 @pytest.mark.parametrize("bad,status", [
     (dict(xd=4), ENUM), (dict(yd=4), ENUM), (dict(tokens=-1), SHAPE), (dict(tokens=1048561), SHAPE),
     (dict(ldx=63), SHAPE), (dict(ldy=7), SHAPE), (dict(x=None), NULL), (dict(y=None), NULL), (dict(x=FAKE + 1), ALIGN),
-    (dict(y=FAKE + 2), ALIGN)])
+    (dict(y=FAKE + 2), ALIGN), (dict(ws=FAKE + 8), ALIGN)])
 def test_matvec(L, mx, bad, status):
     w = nv._MXTensor(FAKE, FAKE, 8, 64) if mx else nv._CTensor(FAKE, FAKE, FAKE, 8, 64)
     fn = L.mxfp4_matvec if mx else L.nvfp4_matvec
@@ -195,3 +195,27 @@ def test_binding_refuses_bad_tensors():
         with pytest.raises(nv.NVFP4Error, match=match):
             call()
             pytest.fail(f"case {i} was not refused")
+
+
+@_no_gpu
+def test_matvec_size_limits(L):
+    k = 1 << 25
+    args = list({**MV, "ldx": k}.values())
+    assert L.nvfp4_matvec(ctypes.byref(nv._CTensor(FAKE, FAKE, FAKE, 8, k)), *args) == SHAPE
+    assert L.mxfp4_matvec(ctypes.byref(nv._MXTensor(FAKE, FAKE, 8, k)), *args) == SHAPE
+
+
+@_no_gpu
+def test_matvec_workspace(L):
+    size = L.nvfp4_matvec_workspace_bytes
+    assert size(8, 64, 2, 7) == ENUM
+    for bad in ((-1, 64, 2), (8, 40, 2), (8, -16, 2), (8, 64, -1), (8, 64, 1048561), (8, 1 << 25, 2)):
+        assert size(*bad, 1) == SHAPE
+    assert size(8, 64, 1, 1) == 0 and size(0, 64, 2, 1) == 0 and size(8, 64, 0, 0) == 0 and size(8, 16, 2, 0) == 0
+    k = 1 << 20
+    need = size(8, k, 2, 1)
+    assert need > 0 and need % 4 == 0
+    w = nv._CTensor(FAKE, FAKE, FAKE, 8, k)
+    args = {**MV, "ldx": k}
+    assert L.nvfp4_matvec(ctypes.byref(w), *{**args, "ws": FAKE, "bytes": need - 1}.values()) == SHAPE
+    assert L.nvfp4_matvec(ctypes.byref(w), *{**args, "bytes": need}.values()) == NULL
