@@ -26,6 +26,7 @@
 // each of 8 bits: exact for every value whose low part does not fall below
 // the bf16 range.  Products are exact in binary32 and added there; the
 // tensor scale g is applied once to the sum.
+#include "gemm_common.h"
 #include "nvfp4_device.h"
 #include "nvfp4_kernels.h"
 #include "row_common.h"
@@ -88,6 +89,17 @@ template <bool MX> __device__ __forceinline__ bf16x8_t decode8(uint32_t w, float
   return __builtin_bit_cast(bf16x8_t, v);
 }
 
+// The same as 8 f16, where every q * S is exact, too: one conversion and one
+// packed product for two weights, half of what the bf16 form takes.
+__device__ __forceinline__ half8_t decode8_f16(uint32_t w, half2_t s) {
+  half2_t v[4];
+  v[0] = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0)) * s;
+  v[1] = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1)) * s;
+  v[2] = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2)) * s;
+  v[3] = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3)) * s;
+  return (half8_t){v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]};
+}
+
 // 32 consecutive x of one token as loaded: 16-byte pieces at any alignment.
 template <typename X> struct Act {
   static constexpr int kPieces = 32 * sizeof(X) / 16;
@@ -124,7 +136,9 @@ __device__ __forceinline__ void store_y(void *y, int y_bf16, int64_t at, float v
 
 constexpr int kStepK = 128;      // k of one MFMA step: 4 lanes a row, 32 each
 constexpr int kTokens = 16;      // tokens of a launch's y index
-constexpr int kTileWaves = 12;   // waves of a workgroup, at most
+// waves of a workgroup, at most (three slabs: their sums take 6 KB of LDS a wave)
+constexpr int kTileWaves = 12;
+constexpr int max_waves(int slabs) { return slabs == 3 ? 8 : kTileWaves; }
 constexpr int kTurnBytes = 4096; // 16 columns x 128 k of bf16
 
 // The B operand's columns.  bf16: one column a token.  float32: three
@@ -162,82 +176,70 @@ __device__ __forceinline__ u32x4_t column8(const float *x, int64_t left, int par
   return out;
 }
 
-// The codes and scales of one tile of 16 weight rows, SW steps, as loaded.
-// The scales of a whole slice come as one run of SB bytes a row (4 lanes a
-// row) and reach the lanes that use them through LDS; where the slice passes
-// the row's end every lane loads its own.
-template <bool MX, int SW> struct Tile {
-  static constexpr int kG = Scale<MX>::kPerByte;
-  static constexpr int kSB = SW * kStepK / kG;
-  u32x4_t c[SW];
-  u32x4_t s;
-  __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales, int64_t tile, int64_t N, int64_t K,
-                                       const uint32_t *k, bool whole, uint32_t k0, int lane) {
-    const int64_t n0 = tile * 16;
-    const uint32_t last = (uint32_t)min(N - 1 - n0, (int64_t)15);     // rows past the end repeat the last one
-    const uint8_t *cb = codes + n0 * (K / 2), *sb = scales + n0 * (K / kG);
-    const uint32_t row = min((uint32_t)lane & 15u, last);
-#pragma unroll
-    for (int i = 0; i < SW; ++i) c[i] = *reinterpret_cast<const u32x4_a8 *>(cb + (row * (uint32_t)(K / 2) + k[i] / 2));
-    if (whole) {
-      const uint8_t *p = sb + (min((uint32_t)lane >> 2, last) * (uint32_t)(K / kG) + k0 / kG + (lane & 3) * (kSB / 4));
-      if (kSB == 32) {
-        const u32x2_a1 v = *reinterpret_cast<const u32x2_a1 *>(p);
-        s = (u32x4_t){v[0], v[1], 0, 0};
-      } else if (kSB == 16) {
-        s = (u32x4_t){*reinterpret_cast<const u32_a1 *>(p), 0, 0, 0};
-      } else {
-        s = (u32x4_t){*reinterpret_cast<const u16_a1 *>(p), 0, 0, 0};
-      }
-    } else {
-      s = (u32x4_t){0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < SW; ++i) {
-        Scale<MX> t;
-        t.load(sb + (row * (uint32_t)(K / kG) + k[i] / kG));
-        s[i] = t.raw;
-      }
-    }
-  }
-  // the lane's scales of every step
-  __device__ __forceinline__ void spread(Scale<MX> *out, char *lds, bool whole, int lane) const {
-    if (!whole) {
-#pragma unroll
-      for (int i = 0; i < SW; ++i) out[i].raw = s[i];
-      return;
-    }
-    // (byte copies: what is stored as words is read as bytes and pairs)
-    __builtin_memcpy(lds + lane * (kSB / 4), &s, kSB / 4);
-    const char *at = lds + (lane & 15) * kSB + (lane >> 4) * (32 / kG);
-#pragma unroll
-    for (int i = 0; i < SW; ++i) {
-      out[i].raw = 0;
-      __builtin_memcpy(&out[i].raw, at + i * (kStepK / kG), 32 / kG);
-    }
-  }
-};
-
 // A workgroup holds the columns of all its tokens over its range of K in
 // registers -- each wave a slice of SW steps -- and walks tiles of 16 weight
 // rows, blockIdx.x, blockIdx.x + gridDim.x, ...: only codes and scales move
-// in the loop.  The waves' sums of a tile meet in LDS and one wave, another
-// one each time, adds and stores them.  With more than one range of K
-// (gridDim.z) the sums go to `partial` [z][token][n] instead.
+// in the loop, codes straight to the lanes that multiply them, a tile ahead.  A tile's scales are fetched by the whole workgroup in rows' runs
+// (a lane's own would be 2 bytes out of every line) and pass through LDS.
+// The waves' sums of a tile meet in LDS, too, behind the tile's one barrier,
+// and four waves, other ones each time, add and store them.  With more than
+// one range of K (gridDim.z) the sums go to `partial` [z][token][n] instead.
 // SL: 16-column slabs; grid: (tile walkers, tokens / 16, ranges of K).
 template <bool MX, typename X, int SL, int SW>
 __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *codes, const uint8_t *scales,
                                                                  const float *meta, int64_t N, int64_t K, const X *x,
                                                                  int64_t tokens, int64_t ldx, void *y, int y_bf16,
-                                                                 int64_t ldy, float *partial) {
+                                                                 int64_t ldy, float *partial, int long_walk) {
   constexpr int kC = columns<X>();
+  constexpr int kG = Scale<MX>::kPerByte;
+  constexpr int kSB = SW * kStepK / kG;              // scale bytes of a slice's row
+  constexpr int kPiece = kSB / 4;                    // of which a thread fetches a quarter
   extern __shared__ __align__(16) char lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int waves = blockDim.x >> 6;
+  const int threads = __builtin_amdgcn_readfirstlane(blockDim.x), waves = threads >> 6;
   const int row = lane & 15, quarter = lane >> 4;
   const int64_t t0 = (int64_t)blockIdx.y * kTokens;
   const int live = (int)min(tokens - t0, (int64_t)kTokens);
-  const int64_t k0 = ((int64_t)blockIdx.z * waves + wave) * (SW * kStepK);
-  const bool whole = k0 + SW * kStepK <= K;
+  const int64_t kz = (int64_t)blockIdx.z * waves * (SW * kStepK);
+  const int64_t k0 = kz + wave * (SW * kStepK);
+  const int64_t tiles = (N + 15) / 16, step = gridDim.x;
+
+  // codes of one tile
+  uint32_t k[SW];
+  int half = 0;                                      // steps (as bits) in which the lane was moved back by 16
+#pragma unroll
+  for (int s = 0; s < SW; ++s) {
+    int64_t at = k0 + s * kStepK + quarter * 32;
+    half |= (last_window(at, K) == 16) << s;
+    k[s] = (uint32_t)at;
+  }
+  // through a view of the tile's rows, which is empty past the last tile:
+  // what lies outside reads as 0 and moves nothing
+  const auto load_codes = [&](u32x4_t *c, int64_t tile) {
+    const int64_t n0 = min(tile, tiles - 1) * 16;
+    const uint32_t rows = tile < tiles ? (uint32_t)min(N - n0, (int64_t)16) : 0u;
+    const __amdgpu_buffer_rsrc_t view = make_rsrc(codes + n0 * (K / 2), rows * (uint32_t)(K / 2));
+#pragma unroll
+    for (int s = 0; s < SW; ++s)
+      c[s] = __builtin_amdgcn_raw_buffer_load_b128(view, (uint32_t)row * (uint32_t)(K / 2) + k[s] / 2, 0, 0);
+  };
+  // scales: piece `sp` of row `sr` of the tile's runs of waves * kSB bytes;
+  // a piece that passes the row's end is fetched from before it and shifted
+  const int pieces = waves * 4, sr = threadIdx.x / pieces, sp = threadIdx.x % pieces;
+  const int64_t row_bytes = K / kG, want = kz / kG + sp * kPiece;
+  const int over = (int)min(max(want + kPiece - row_bytes, (int64_t)0), (int64_t)kPiece);
+  const uint32_t sfrom = (uint32_t)min(want, row_bytes - kPiece);
+  const int shift = 8 * min(over, kPiece - 1);
+  const uint64_t keep = over == kPiece ? 0 : ~(uint64_t)0;
+  const int stride = waves * kSB + 4;                // + 4: the 16 rows' reads fall on different banks
+  const auto load_scales = [&](int64_t tile) {
+    const int64_t n0 = tile * 16;
+    const uint32_t r = min((uint32_t)sr, (uint32_t)min(N - 1 - n0, (int64_t)15));
+    uint64_t v = 0;
+    const uint8_t *p = scales + n0 * row_bytes + (r * (uint32_t)row_bytes + sfrom);
+    __builtin_memcpy(&v, p, kPiece);
+    return v;
+  };
 
   // x into registers, by way of LDS: an MFMA's lane wants 8 k of its own
   // column, which as a load would touch 64 places; so 64-byte runs of k are
@@ -245,109 +247,209 @@ __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *
   // Piece (column, p) of run i lies at slot 4 column + (p ^ (column / 4)):
   // stores and reads then fall on all banks.
   bf16x8_t b[SW][4][SL];
-  uint32_t k[SW];
+  u32x4_t c0[SW], c1[SW];
+  const int64_t first = blockIdx.x;
+  const auto clamp = [&](int64_t t) { return t < tiles ? t : first; };
+  load_codes(c0, first);
+  const uint64_t sc_first = load_scales(first);
+  uint64_t sc_next = load_scales(clamp(first + step));
   {
     char *const turn = lds + wave * kTurnBytes;
     const int col = lane >> 2, piece = lane & 3;
     const int write = 16 * (4 * col + (piece ^ (col >> 2)));
+    u32x4_t raw[SW][SL][4];
 #pragma unroll
-    for (int s = 0; s < SW; ++s) {
-      const int64_t ks = k0 + s * kStepK;
-      int64_t at = ks + quarter * 32;
-      const int drop = last_window(at, K);
-      k[s] = (uint32_t)at;
+    for (int s = 0; s < SW; ++s)
 #pragma unroll
       for (int l = 0; l < SL; ++l) {
         const int v = min(16 * l + col, live * kC - 1);     // columns past the last repeat it: they are independent
         const X *xr = x + (t0 + v / kC) * ldx;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int64_t kk = ks + 32 * i + 8 * piece;
-          *reinterpret_cast<u32x4_t *>(turn + i * 1024 + write) = column8(xr + kk, K - kk, v % kC);
+          const int64_t kk = k0 + s * kStepK + 32 * i + 8 * piece;
+          raw[s][l][i] = column8(xr + kk, K - kk, v % kC);
         }
+      }
+#pragma unroll
+    for (int s = 0; s < SW; ++s)
+#pragma unroll
+      for (int l = 0; l < SL; ++l) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4_t *>(turn + i * 1024 + write) = raw[s][l][i];
         // a lane moved back by 16 finds its x in the other half
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int p = drop == 16 ? j ^ 2 : j;
+          const int p = j ^ (((half >> s) & 1) << 1);
           b[s][j][l] = *reinterpret_cast<const bf16x8_t *>(turn + quarter * 1024 + 16 * (4 * row + (p ^ (row >> 2))));
         }
       }
+  }
+  // NVFP4: where a column's values span at most 29 binades they are as exact
+  // in f16, moved by a power of two so that the largest lies in [2^14, 2^15)
+  // and the smallest at 2^-14 or above (8 bits of f16's 11, no subnormals);
+  // the weights decode in half the instructions there.  A wave whose columns do not all allow it
+  // (or hold an Inf or NaN) stays with bf16.
+  bool f16 = false;
+  int move[SL];
+#pragma unroll
+  for (int l = 0; l < SL; ++l) move[l] = 0;
+  if (!MX && long_walk) {
+    bool fits = true;
+#pragma unroll
+    for (int l = 0; l < SL; ++l) {
+      ushort2_t hi = {0, 0}, lo = {0xFFFF, 0xFFFF};       // of the magnitudes, and of those less 1 (0 becomes the largest)
+#pragma unroll
+      for (int s = 0; s < SW; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const u32x4_t w = __builtin_bit_cast(u32x4_t, b[s][j][l]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const ushort2_t m = __builtin_bit_cast(ushort2_t, (uint32_t)w[i] & 0x7FFF7FFFu);
+            hi = __builtin_elementwise_max(hi, m);
+            lo = __builtin_elementwise_min(lo, m - (ushort2_t){1, 1});
+          }
+        }
+      int top = max((int)hi[0], (int)hi[1]), low = min((int)lo[0], (int)lo[1]);
+      top = max(top, __shfl_xor(top, 16, 64));            // the column's other three lanes
+      low = min(low, __shfl_xor(low, 16, 64));
+      top = max(top, __shfl_xor(top, 32, 64));
+      low = min(low, __shfl_xor(low, 32, 64));
+      const int top_e = top >> 7, low_e = max((low + 1) >> 7, 1);
+      fits &= top_e < 255 && (top == 0 || low_e >= top_e - 28);
+      move[l] = top == 0 ? 0 : top_e - 127 - 14;
+    }
+    f16 = __all(fits);
+    if (f16) {
+#pragma unroll
+      for (int l = 0; l < SL; ++l)
+#pragma unroll
+        for (int s = 0; s < SW; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const u32x4_t w = __builtin_bit_cast(u32x4_t, b[s][j][l]);
+            half8_t h;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              h[2 * i] = (_Float16)__builtin_amdgcn_ldexpf(bf16_lo(w[i]), -move[l]);
+              h[2 * i + 1] = (_Float16)__builtin_amdgcn_ldexpf(bf16_hi(w[i]), -move[l]);
+            }
+            b[s][j][l] = __builtin_bit_cast(bf16x8_t, h);
+          }
+    } else {
+#pragma unroll
+      for (int l = 0; l < SL; ++l) move[l] = 0;
     }
   }
   __syncthreads();
 
-  char *const scale_lds = lds + wave * 512;
-  f32x4_t *const part = reinterpret_cast<f32x4_t *>(lds + waves * 512);       // [2][waves][SL][64]
+  constexpr int kSums = max_waves(SL) * SL * 64;                   // sums of one tile, waves that do not exist counted
+  f32x4_t *const part = reinterpret_cast<f32x4_t *>(lds);          // [2][waves][SL][64]
+  char *const scale_lds = lds + 2 * kSums * sizeof(f32x4_t);       // [2][16][stride]
+  const auto put_scales = [&](uint64_t v, int turn) {
+    v = (v >> shift) & keep;
+    __builtin_memcpy(scale_lds + (turn & 1) * 16 * stride + sr * stride + sp * kPiece, &v, kPiece);
+  };
+  put_scales(sc_first, 0);
+  __syncthreads();
+
   const float g = MX ? 1.0f : meta[1];
-  const int64_t tiles = (N + 15) / 16;
-  const auto work = [&](const Tile<MX, SW> &t, int64_t tile, int turn) {
+  int from = 0;
+  const auto work = [&](const u32x4_t *c, int64_t tile, int turn) {
     constexpr int kA = SL == 1 ? 2 : 1;       // one slab: two accumulators, so that MFMAs do not wait for each other
     f32x4_t acc[kA][SL];
 #pragma unroll
     for (int l = 0; l < SL; ++l) acc[0][l] = acc[kA - 1][l] = (f32x4_t){0, 0, 0, 0};
     Scale<MX> sc[SW];
-    t.spread(sc, scale_lds, whole, lane);
+    const char *at = scale_lds + (turn & 1) * 16 * stride + row * stride;
 #pragma unroll
-    for (int s = 0; s < SW; ++s)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bf16x8_t a = decode8<MX>(t.c[s][j], j < 2 ? sc[s].lo() : sc[s].hi());
-#pragma unroll
-        for (int l = 0; l < SL; ++l)
-          acc[j % kA][l] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[s][j][l], acc[j % kA][l], 0, 0, 0);
-      }
-    f32x4_t *const mine = part + (turn & 1) * waves * SL * 64;
-#pragma unroll
-    for (int l = 0; l < SL; ++l) mine[(wave * SL + l) * 64 + lane] = kA == 2 ? acc[0][l] + acc[kA - 1][l] : acc[0][l];
-    __syncthreads();
-    if (wave != turn % waves || row >= live) return;
-    // lane: token t0 + row, weight rows 16 tile + 4 quarter + i
-    f32x4_t sum = {0, 0, 0, 0};
-    for (int w = 0; w < waves; ++w)
-#pragma unroll
-      for (int p = 0; p < kC; ++p) {
-        const int v = row * kC + p;
-        sum += mine[(w * SL + v / 16) * 64 + quarter * 16 + v % 16];
-      }
-    const int64_t n = 16 * tile + 4 * quarter;
-    if (n >= N) return;
-    if (partial) {
-      float *o = partial + ((int64_t)blockIdx.z * tokens + t0 + row) * N + n;
-      if (n + 4 <= N) *reinterpret_cast<f32x4_a4 *>(o) = sum;
-      else
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-          if (n + i < N) o[i] = sum[i];
-      return;
+    for (int s = 0; s < SW; ++s) {
+      const uint32_t o = (k[s] - (uint32_t)kz) / kG;
+      // NVFP4: the pair of a lane moved back starts at an odd byte; its
+      // first scale meets only zeros, so the second's pair will do
+      if (MX) sc[s].raw = *reinterpret_cast<const uint8_t *>(at + o);
+      else sc[s].raw = (uint32_t)*reinterpret_cast<const uint16_t *>(at + ((o + 1) & ~1u)) << (((half >> s) & 1) * 8);
     }
-    const int64_t at = (t0 + row) * ldy + n;
-    if (n + 4 <= N && y_bf16) {
-      *reinterpret_cast<u32x2_a2 *>((uint16_t *)y + at) =
-          (u32x2_t){pack_bf16(sum[0] * g, sum[1] * g), pack_bf16(sum[2] * g, sum[3] * g)};
-    } else if (n + 4 <= N) {
-      *reinterpret_cast<f32x4_a4 *>((float *)y + at) = sum * g;
+    if (!MX && f16) {
+#pragma unroll
+      for (int s = 0; s < SW; ++s) {
+        const _Float16 lo = (_Float16)sc[s].lo(), hi = (_Float16)sc[s].hi();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const half8_t a = decode8_f16(c[s][j], j < 2 ? (half2_t){lo, lo} : (half2_t){hi, hi});
+#pragma unroll
+          for (int l = 0; l < SL; ++l)
+            acc[j % kA][l] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, __builtin_bit_cast(half8_t, b[s][j][l]),
+                                                                    acc[j % kA][l], 0, 0, 0);
+        }
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < 3; ++i)
-        if (n + i < N) store_y(y, y_bf16, at + i, sum[i] * g);
+      for (int s = 0; s < SW; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bf16x8_t a = decode8<MX>(c[s][j], j < 2 ? sc[s].lo() : sc[s].hi());
+#pragma unroll
+          for (int l = 0; l < SL; ++l)
+            acc[j % kA][l] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[s][j][l], acc[j % kA][l], 0, 0, 0);
+        }
     }
+    f32x4_t *const mine = part + (turn & 1) * kSums;
+#pragma unroll
+    for (int l = 0; l < SL; ++l) {
+      f32x4_t v = kA == 2 ? acc[0][l] + acc[kA - 1][l] : acc[0][l];
+      if (!MX)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_ldexpf(v[i], move[l]);
+      mine[(wave * SL + l) * 64 + lane] = v;
+    }
+    put_scales(sc_next, turn + 1);
+    __syncthreads();
+    // 256 outputs, 16 consecutive rows of a token together, dealt to four
+    // waves, other ones each time; the sums are read four waves' at a time
+    constexpr int kBatch = 4;
+    int o = (int)threadIdx.x - from;
+    if (o < 0) o += threads;
+    for (; o < 256; o += threads) {
+      const int i = o & 15, token = o >> 4;
+      const int64_t n = 16 * tile + i;
+      if (token >= live || n >= N) continue;
+      const float *f = reinterpret_cast<const float *>(mine) + (i >> 2) * 64 + (i & 3);
+      float sum = 0.0f;
+      for (int w0 = 0; w0 < waves; w0 += kBatch) {
+        float v[kBatch][kC];
+#pragma unroll
+        for (int p = 0; p < kC; ++p) {
+          const int col = token * kC + p;
+          const float *fc = f + w0 * SL * 256 + (col >> 4) * 256 + (col & 15) * 4;
+#pragma unroll
+          for (int w = 0; w < kBatch; ++w) v[w][p] = fc[w * SL * 256];
+        }
+#pragma unroll
+        for (int w = 0; w < kBatch; ++w)
+#pragma unroll
+          for (int p = 0; p < kC; ++p) sum += w0 + w < waves ? v[w][p] : 0.0f;
+      }
+      if (partial) partial[((int64_t)blockIdx.z * tokens + t0 + token) * N + n] = sum;
+      else store_y(y, y_bf16, (t0 + token) * ldy + n, sum * g);
+    }
+    from += 256;
+    while (from >= threads) from -= threads;
   };
 
-  const uint32_t ku = (uint32_t)k0;
-  const int64_t step = gridDim.x;
-  Tile<MX, SW> a, c;
-  int64_t t = blockIdx.x;
-  a.load(codes, scales, t, N, K, k, whole, ku, lane);
-  // two tiles in flight; the last loads repeat a tile of the walk
-  for (int turn = 0;; turn += 2) {
-    const int64_t t1 = t + step, t2 = t1 + step;
-    c.load(codes, scales, t1 < tiles ? t1 : t, N, K, k, whole, ku, lane);
-    work(a, t, turn);
-    if (t1 >= tiles) break;
-    a.load(codes, scales, t2 < tiles ? t2 : t1, N, K, k, whole, ku, lane);
-    work(c, t1, turn + 1);
-    if (t2 >= tiles) break;
-    t = t2;
+  // one turn: the loads of a later tile, then this tile
+  int turn = 0;
+  const auto round = [&](const u32x4_t *now, u32x4_t *next, int64_t t) {
+    load_codes(next, t + step);
+    const uint64_t sc_later = load_scales(clamp(t + 2 * step));
+    __builtin_amdgcn_sched_barrier(0);       // the loads go out before this tile's work, not after it
+    work(now, t, turn++);
+    sc_next = sc_later;
+    return t + step < tiles;
+  };
+  for (int64_t t = first;; t += 2 * step) {
+    if (!round(c0, c1, t)) break;
+    if (!round(c1, c0, t + step)) break;
   }
 }
 
@@ -362,24 +464,30 @@ __global__ __launch_bounds__(256) void k_matvec_join(const float *partial, int r
   }
 }
 
-// K = 16, less than a lane's load (or 0): one thread an output.
-template <typename X>
+// K below 128, where a row has less than a step's codes: one thread an output.
+constexpr int64_t kShortK = 128;
+template <bool MX, typename X>
 __global__ __launch_bounds__(256) void k_matvec_short(const uint8_t *codes, const uint8_t *scales, const float *meta,
                                                       int64_t N, int64_t K, const X *x, int64_t tokens, int64_t ldx,
                                                       void *y, int y_bf16, int64_t ldy) {
+  constexpr int kG = Scale<MX>::kPerByte;
+  const float g = MX ? 1.0f : meta[1];
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < N * tokens; i += (int64_t)gridDim.x * 256) {
     const int64_t n = i % N, t = i / N;
     float sum = 0.0f;
-    if (K) {
-      const u32x2_t c = *reinterpret_cast<const u32x2_t *>(codes + n * 8);
+    for (int k0 = 0; k0 < K; k0 += 16) {
+      const u32x2_t c = *reinterpret_cast<const u32x2_t *>(codes + n * (K / 2) + k0 / 2);
+      Scale<MX> sc;
+      sc.raw = scales[n * (K / kG) + k0 / kG];
+      float p = 0.0f;
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
         const float2_t q = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4((c[k >> 3] >> (4 * (k & 7))) & 15u, 1.0f, 0);
-        sum = __builtin_fmaf(to_float(x[t * ldx + k]), q.x, sum);
+        p = __builtin_fmaf(to_float(x[t * ldx + k0 + k]), q.x, p);
       }
-      sum *= e4m3_to_f32(scales[n]) * meta[1];
+      sum = __builtin_fmaf(p, sc.lo(), sum);
     }
-    store_y(y, y_bf16, t * ldy + n, sum);
+    store_y(y, y_bf16, t * ldy + n, sum * g);
   }
 }
 constexpr int64_t kFlatGrid = 1 << 16;
@@ -492,7 +600,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void k_matvec_row(const uint8_t *co
 // steps a wave (16 SL SW registers of x), `waves` of them a workgroup,
 // `ranges` of K, and the workgroups that walk the tiles of one range.
 struct Cut {
-  int sl, sw, waves, ranges, walkers;
+  int sl, sw, waves, ranges, walkers, long_walk;
 };
 Cut cut_for(int64_t N, int64_t K, int64_t tokens, bool f32) {
   Cut c;
@@ -500,15 +608,21 @@ Cut cut_for(int64_t N, int64_t K, int64_t tokens, bool f32) {
   c.sl = (cols + 15) / 16;
   c.sw = c.sl == 1 ? 4 : 2;
   const int64_t slices = (K + c.sw * kStepK - 1) / (c.sw * kStepK);
-  const int most = c.sl == 3 ? 9 : kTileWaves;          // (9 waves' sums of three slabs fill 64 KB of LDS)
-  c.ranges = (int)((slices + most - 1) / most);
-  c.waves = (int)((slices + c.ranges - 1) / c.ranges);
+  const int most = max_waves(c.sl);
+  for (c.ranges = (int)((slices + most - 1) / most);; ++c.ranges) {
+    c.waves = (int)((slices + c.ranges - 1) / c.ranges);
+    // the last range needs a lane's 32 k of its own
+    if (K - (int64_t)(c.ranges - 1) * c.waves * c.sw * kStepK >= 32) break;
+  }
   // one round of workgroups: as many as fit the CUs' waves, the tiles dealt evenly
   const int64_t tiles = (N + 15) / 16, blocks = (tokens + kTokens - 1) / kTokens;
   const int64_t room = (int64_t)device_cus() * (kTileWaves / c.waves);
   const int64_t want = std::min(tiles, std::max<int64_t>(1, room / (c.ranges * blocks)));
   const int64_t per = (tiles + want - 1) / want;
   c.walkers = (int)((tiles + per - 1) / per);
+  // bringing x to f16 pays from about 8 tiles on (1.3 us more at the start, a
+  // fifth less a tile: 131075 x 5120 90 -> 77 us, 20480 x 5120 18.4 -> 19.7)
+  c.long_walk = per >= 8;
   return c;
 }
 
@@ -516,10 +630,12 @@ template <bool MX, typename X, int SL, int SW>
 void tile(const Cut &c, const uint8_t *codes, const uint8_t *scales, const float *meta, int64_t N, int64_t K, const X *x,
           int64_t tokens, int64_t ldx, void *y, int y_bf16, int64_t ldy, void *workspace, hipStream_t stream) {
   const dim3 grid((unsigned)c.walkers, (unsigned)((tokens + kTokens - 1) / kTokens), (unsigned)c.ranges);
-  const size_t lds = c.waves * std::max<size_t>(kTurnBytes, 512 + 2 * SL * 64 * sizeof(f32x4_t));
+  const size_t run = c.waves * SW * kStepK / Scale<MX>::kPerByte;       // scale bytes of a row
+  const size_t lds =
+      std::max<size_t>(c.waves * kTurnBytes, 2 * max_waves(SL) * SL * 64 * sizeof(f32x4_t) + 32 * (run + 4));
   float *partial = c.ranges > 1 ? (float *)workspace : nullptr;
   k_matvec_tile<MX, X, SL, SW><<<grid, 64 * c.waves, lds, stream>>>(codes, scales, meta, N, K, x, tokens, ldx, y,
-                                                                    y_bf16, ldy, partial);
+                                                                    y_bf16, ldy, partial, c.long_walk);
   if (partial)
     k_matvec_join<<<(unsigned)std::min(kFlatGrid, (N * tokens + 255) / 256), 256, 0, stream>>>(
         partial, c.ranges, MX ? nullptr : meta, N, tokens, y, y_bf16, ldy);
@@ -534,7 +650,7 @@ void rows(const uint8_t *codes, const uint8_t *scales, const float *meta, int64_
 }
 
 // One token whose x fits the registers of a workgroup.
-bool one_token(int64_t tokens, int64_t K) { return tokens == 1 && K >= 32 && K <= 4 * 3 * kWaveK; }
+bool one_token(int64_t tokens, int64_t K) { return tokens == 1 && K >= kShortK && K <= 4 * 3 * kWaveK; }
 
 template <bool MX, typename X>
 void matvec(const uint8_t *codes, const uint8_t *scales, const float *meta, int64_t N, int64_t K, const void *xv,
@@ -548,9 +664,9 @@ void matvec(const uint8_t *codes, const uint8_t *scales, const float *meta, int6
     else rows<MX, X, 3, 4>(codes, scales, meta, N, K, x, y, yb, st);
     return;
   }
-  if (K < 32) {
+  if (K < kShortK) {
     const unsigned grid = (unsigned)std::min(kFlatGrid, (N * tokens + 255) / 256);
-    k_matvec_short<X><<<grid, 256, 0, st>>>(codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy);
+    k_matvec_short<MX, X><<<grid, 256, 0, st>>>(codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy);
     return;
   }
   const Cut c = cut_for(N, K, tokens, sizeof(X) == 4);
@@ -562,7 +678,7 @@ void matvec(const uint8_t *codes, const uint8_t *scales, const float *meta, int6
 }  // namespace
 
 int64_t matvec_workspace_bytes(int64_t N, int64_t K, int64_t tokens, bool f32) {
-  if (N <= 0 || tokens <= 0 || K < 32 || one_token(tokens, K)) return 0;
+  if (N <= 0 || tokens <= 0 || K < kShortK || one_token(tokens, K)) return 0;
   const Cut c = cut_for(N, K, tokens, f32);
   return c.ranges > 1 ? 4 * c.ranges * tokens * N : 0;
 }

@@ -241,3 +241,39 @@ def test_offsets_past_32_bits():
         q[:, 0::2], q[:, 1::2] = GRID[c & 15], GRID[c >> 4]
         s = scales[r:r + 40].cpu().view(torch.float8_e4m3fn).double().numpy()
         _check(y[:, r:r + 40], x, q * np.repeat(s, 16, 1) * meta[1].double().item(), f"rows from {r}")
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 7, 16])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [512, 1504])
+def test_wide_range_within_a_token(dt, tokens, k):
+    """Activations from 2^-60 to 2^60 side by side, the large ones under zero
+    weights in half the rows: those rows' sums are of the small ones, which
+    therefore have to keep all their bits."""
+    n = 40
+    w, wd = _weights("nvfp4", n, k, 97)
+    x = _x(tokens, k, torch.float32, 101)
+    for t in range(tokens):
+        x[t, t % 16] = 2.0 ** 60
+        x[t, 300 + t] = 0.0
+        x[t, 20 + t] *= 2.0 ** -60
+    if tokens > 2:
+        x[1] = x[1].clamp(-1, 1) * 2.0 ** -40 + 0.0     # one token of ordinary spread between them
+        x[2] = 0.0
+    x = x.to(DT[dt])
+    w.codes[: n // 2, :8] = 0
+    wd[: n // 2, :16] = 0.0
+    _check(_run("nvfp4", w, x, out_dtype=torch.float32), x, wd, f"{dt} {tokens} K={k}")
+
+
+@pytest.mark.parametrize("tokens", [2, 16])
+def test_ranges_of_k_join(tokens):
+    """Long reductions are cut among workgroups and joined: K whole and not in
+    the pieces that a cut has, an odd N, an output view."""
+    for k in (6144, 7200, 20480 + 16, 24576):
+        w, wd = _weights("nvfp4", 35, k, k)
+        for dt in ("bf16", "f32"):
+            x = _x(tokens, k, DT[dt], 103, pad=1)
+            base = torch.full((tokens, 40), 9.0, dtype=torch.bfloat16, device="cuda")
+            _check(_run("nvfp4", w, x, out_dtype=torch.bfloat16, out=base[:, :35]), x, wd, f"K={k} {dt}")
+            assert torch.all(base[:, 35:] == 9.0)
