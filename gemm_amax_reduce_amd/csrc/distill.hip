@@ -114,7 +114,7 @@ __device__ __forceinline__ bool load_teacher(Teacher &te, const void *idx, int i
     te.lp[k] = d;
     s += te.at[k] >= 0 ? __builtin_amdgcn_exp2f(d) : 0.0f;
   }
-  const float l = __builtin_amdgcn_logf(block_sum(s, te.share[1]));
+  const float l = __builtin_amdgcn_logf(block_sum(s, te.share[1], kDT / 64));
   for (int k = threadIdx.x; k < top; k += kDT) te.lp[k] -= l;
   __syncthreads();
   return some;
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(kDT) void k_distill_finish(const T *z, int64_t ldz,
           const float q = (to_float(zr[te.at[k]]) - top_z) * scale - l2;    // log2 of the student's share
           a = __builtin_fmaf(p, te.lp[k] - q, a);
         }
-      a = block_sum(a, sums);
+      a = block_sum(a, sums, kDT / 64);
       if (threadIdx.x == 0) {
         loss[row] = some ? tau * tau * kLn2 * a : 0.0f;
         lse[row] = top_z / tau + l2 * kLn2;

@@ -40,46 +40,56 @@ template <typename T> __device__ __forceinline__ uint32_t absmax8(const Row8<T> 
 }
 
 // One workgroup per row, rows blockIdx.x, blockIdx.x + gridDim.x, ...; the
-// threads keep their columns' weights and biases over all of them.
+// threads keep their columns' weights and biases over all of them, and a row
+// is fetched while the one before it is worked on.
 template <typename X, typename Y, int VPT>
-__global__ __launch_bounds__(kMaxThreads) void k_ln_forward(const X *x, int64_t ldx, const void *w, const void *b, int w_bf16, Y *y,
-                                       int64_t ldy, float *mean, float *rstd, uint32_t *amax, int64_t rows,
-                                       int64_t cols, float eps) {
+__global__ __launch_bounds__(kMaxThreads) void k_ln_forward(const X *x, int64_t ldx, const void *w, const void *b,
+                                                            int w_bf16, Y *y, int64_t ldy, float *mean, float *rstd,
+                                                            uint32_t *amax, int64_t rows, int64_t cols, float eps,
+                                                            int threads) {
   __shared__ float part[2][2][kMaxWaves];
   __shared__ uint32_t umax[kMaxWaves];
-  const int64_t step = (int64_t)blockDim.x * 8;
-  const int64_t c0 = (int64_t)threadIdx.x * 8;
+  const int waves = threads >> 6;
+  const float inv = 1.0f / (float)cols;
+  Span sp[VPT];
   float wv[VPT][8], bv[VPT][8];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    load_param8(wv[j], w, w_bf16, c0 + j * step, cols, 1.0f);
-    load_param8(bv[j], b, w_bf16, c0 + j * step, cols, 0.0f);
+    sp[j] = Span((int64_t)(threadIdx.x + j * threads) * 8, cols);
+    load_param8(wv[j], w, w_bf16, sp[j].at, cols, 1.0f);
+    load_param8(bv[j], b, w_bf16, sp[j].at, cols, 0.0f);
   }
   uint32_t top = 0;
   int turn = 0;
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
+  Row8<X> next[VPT];
+  int64_t row = blockIdx.x;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) next[j].load(x + row * ldx + sp[j].at);
+  while (row < rows) {
     float v[VPT][8];
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      Row8<X> q;
-      load_row8(q, x + row * ldx, c0 + j * step, cols);
-      q.get(v[j]);
+      next[j].get(v[j]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += v[j][i];
+      for (int i = 0; i < 8; ++i) s += sp[j].mine(i) ? v[j][i] : 0.0f;
     }
-    const float m = block_sum(s, part[turn][0]) / (float)cols;
+    const int64_t later = row + gridDim.x, fetch = min(later, rows - 1);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) next[j].load(x + fetch * ldx + sp[j].at);
+    __builtin_amdgcn_sched_barrier(0);       // the loads go out before this row's work, not after it
+    const float m = block_sum(s, part[turn][0], waves) * inv;
     float s2 = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int64_t left = cols - (c0 + j * step);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[j][i] = i < left ? v[j][i] - m : 0.0f;
-        s2 = __builtin_fmaf(v[j][i], v[j][i], s2);
+        v[j][i] -= m;
+        const float d = sp[j].mine(i) ? v[j][i] : 0.0f;
+        s2 = __builtin_fmaf(d, d, s2);
       }
     }
-    const float var = block_sum(s2, part[turn][1]) / (float)cols;
+    const float var = block_sum(s2, part[turn][1], waves) * inv;
     const float r = 1.0f / __builtin_sqrtf(var + eps);
     if (threadIdx.x == 0) {
       mean[row] = m;
@@ -87,17 +97,15 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_forward(const X *x, int64_t 
     }
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int64_t at = c0 + j * step;
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] = __builtin_fmaf(v[j][i] * r, wv[j][i], bv[j][i]);
       Row8<Y> q;
       q.set(v[j]);
-      store_row8(q, y + row * ldy, at, cols);
-      if (amax && at < cols) {
-        // past the end v = fma(0, 1, 0) = 0 (or a NaN that the row holds anyway)
-        top = max(top, absmax8(q));
-      }
+      if (sp[j].dup < 8) q.store(y + row * ldy + sp[j].at);
+      if (amax) top = max(top, absmax8(q));
     }
+    row = later;
+    turn ^= 1;
   }
   if (amax) {
 #pragma unroll
@@ -105,21 +113,21 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_forward(const X *x, int64_t 
     if ((threadIdx.x & 63) == 0) umax[threadIdx.x >> 6] = top;
     __syncthreads();
     if (threadIdx.x == 0) {
-      for (int i = 1; i < (int)(blockDim.x >> 6); ++i) top = max(top, umax[i]);
+      for (int i = 1; i < waves; ++i) top = max(top, umax[i]);
       // the value only grows, so a workgroup that cannot raise it skips the atomic
       if (top > __hip_atomic_load(amax, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(amax, top);
     }
   }
 }
 
-// Rows wider than the registers of a workgroup hold: the row is read three
-// times (the second and third time from the caches).
+// Rows wider than the registers of a workgroup hold, or narrower than one
+// vector: the row is read three times (the second and third from the caches).
 template <typename X, typename Y>
 __global__ __launch_bounds__(kMaxThreads) void k_ln_forward_wide(const X *x, int64_t ldx, const void *w, const void *b, int w_bf16,
                                             Y *y, int64_t ldy, float *mean, float *rstd, uint32_t *amax,
                                             int64_t rows, int64_t cols, float eps) {
   __shared__ float part[2][2][kMaxWaves];
-  const int64_t step = (int64_t)blockDim.x * 8;
+  const int64_t step = (int64_t)kMaxThreads * 8;
   const int64_t c0 = (int64_t)threadIdx.x * 8;
   uint32_t top = 0;
   int turn = 0;
@@ -135,7 +143,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_forward_wide(const X *x, int
       for (int i = 0; i < 8; ++i) t += v[i];
       s += t;
     }
-    const float m = block_sum(s, part[turn][0]) / (float)cols;
+    const float m = block_sum(s, part[turn][0], kMaxWaves) / (float)cols;
     float s2 = 0.0f;
     for (int64_t at = c0; at < cols; at += step) {
       Row8<X> q;
@@ -149,7 +157,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_forward_wide(const X *x, int
       }
       s2 += t;
     }
-    const float var = block_sum(s2, part[turn][1]) / (float)cols;
+    const float var = block_sum(s2, part[turn][1], kMaxWaves) / (float)cols;
     const float r = 1.0f / __builtin_sqrtf(var + eps);
     if (threadIdx.x == 0) {
       mean[row] = m;
@@ -178,13 +186,155 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_forward_wide(const X *x, int
   }
 }
 
-// Backward, first kernel: the two row sums (mean of a, mean of a h).
+// Backward where a row fits the registers.  A workgroup has `groups` groups
+// of `tpr` threads, each of which walks rows of its own: x and dy of a row
+// are read once and stay in registers between the reduction of the two row
+// sums and dx, the next row's are fetched meanwhile, and every thread adds
+// up dw and db of its columns over all its rows.  At the end the groups'
+// sums meet in LDS, and the workgroup leaves one partial row of dw and one of
+// db.  partial: [gridDim.x][2][cols]; dynamic LDS: (groups - 1) * cols floats.
+template <typename X, typename D, int VPT, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_ln_backward(const D *dy, int64_t lddy, const X *x, int64_t ldx,
+                                                         const float *mean, const float *rstd, const void *w,
+                                                         int w_bf16, X *dx, int64_t lddx, float *partial, int64_t rows,
+                                                         int64_t cols, int tpr, int groups) {
+  __shared__ float2 part[2][kMaxWaves];
+  extern __shared__ float sums[];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wpr = tpr >> 6;
+  const int group = wave / wpr, t = threadIdx.x - group * tpr;
+  const int64_t stride = (int64_t)gridDim.x * groups;
+  const float inv = 1.0f / (float)cols;
+  Span sp[VPT];
+  float wv[VPT][8], dw[VPT][8], db[VPT][8];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    sp[j] = Span((int64_t)(t + j * tpr) * 8, cols);
+    load_param8(wv[j], w, w_bf16, sp[j].at, cols, 1.0f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[j][i] = db[j][i] = 0.0f;
+  }
+  Row8<X> xn[VPT];
+  Row8<D> dn[VPT];
+  float mn, rn;
+  const auto fetch = [&](int64_t r) {
+    r = min(r, rows - 1);              // (past the last row: fetched, not used)
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      xn[j].load(x + r * ldx + sp[j].at);
+      dn[j].load(dy + r * lddy + sp[j].at);
+    }
+    mn = mean[r];
+    rn = rstd[r];
+  };
+  int64_t row = (int64_t)blockIdx.x * groups + group;
+  fetch(row);
+  // the workgroup's groups make the same number of turns (barriers)
+  int turn = 0;
+  for (int64_t first = (int64_t)blockIdx.x * groups; first < rows; first += stride, row += stride, turn ^= 1) {
+    const float m = mn, r = rn;
+    float s1 = 0.0f, s2 = 0.0f;
+    Row8<X> xc[VPT];
+    Row8<D> dc[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      xc[j] = xn[j];
+      dc[j] = dn[j];
+    }
+    fetch(row + stride);
+    __builtin_amdgcn_sched_barrier(0);       // the loads go out before this row's work, not after it
+    if (row < rows) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        float xv[8], dv[8];
+        xc[j].get(xv);
+        dc[j].get(dv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float h = (xv[i] - m) * r, a = sp[j].mine(i) ? dv[i] * wv[j][i] : 0.0f;
+          dw[j][i] = __builtin_fmaf(dv[i], h, dw[j][i]);
+          db[j][i] += dv[i];
+          s1 += a;
+          // (a stays out of the sum as it is: 0 times an h that is not finite would enter it)
+          s2 = sp[j].mine(i) ? __builtin_fmaf(a, h, s2) : s2;
+        }
+      }
+    }
+    s1 = wave_sum(s1);
+    s2 = wave_sum(s2);
+    if (wpr > 1) {
+      if ((threadIdx.x & 63) == 0) part[turn][wave] = make_float2(s1, s2);
+      __syncthreads();
+      s1 = s2 = 0.0f;
+      for (int i = 0; i < wpr; ++i) {
+        const float2 p = part[turn][group * wpr + i];
+        s1 += p.x;
+        s2 += p.y;
+      }
+    }
+    s1 *= inv;
+    s2 *= inv;
+    if (row < rows) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        // h and a once more, from the row as it was read: to keep them over the
+        // reduction would take twice the registers for 16-bit types
+        float o[8], xv[8], dv[8];
+        xc[j].get(xv);
+        dc[j].get(dv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          o[i] = r * __builtin_fmaf(-(xv[i] - m) * r, s2, __builtin_fmaf(dv[i], wv[j][i], -s1));
+        Row8<X> q;
+        q.set(o);
+        if (sp[j].dup < 8) q.store(dx + row * lddx + sp[j].at);
+      }
+    }
+  }
+  // dw, then db
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (groups > 1) {
+      __syncthreads();
+      if (group > 0) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+          Row8<float> q;
+          q.set(k ? db[j] : dw[j]);
+          q.store(sums + (int64_t)(group - 1) * cols + sp[j].at);
+        }
+      }
+      __syncthreads();
+    }
+    if (group == 0) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = k ? db[j][i] : dw[j][i];
+        for (int g = 1; g < groups; ++g) {
+          Row8<float> q;
+          float u[8];
+          q.load(sums + (int64_t)(g - 1) * cols + sp[j].at);
+          q.get(u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += u[i];
+        }
+        Row8<float> q;
+        q.set(v);
+        if (sp[j].dup < 8) q.store(partial + ((int64_t)blockIdx.x * 2 + k) * cols + sp[j].at);
+      }
+    }
+  }
+}
+
+// Wider rows, first kernel: the two row sums (mean of a, mean of a h).
 template <typename X, typename D>
-__global__ __launch_bounds__(kMaxThreads) void k_ln_backward_rows(const D *dy, int64_t lddy, const X *x, int64_t ldx, const float *mean,
-                                             const float *rstd, const void *w, int w_bf16, float2 *sums,
-                                             int64_t rows, int64_t cols) {
+__global__ __launch_bounds__(kMaxThreads) void k_ln_backward_rows(const D *dy, int64_t lddy, const X *x, int64_t ldx,
+                                                                  const float *mean, const float *rstd, const void *w,
+                                                                  int w_bf16, float2 *sums, int64_t rows,
+                                                                  int64_t cols) {
   __shared__ float part[2][2][kMaxWaves];
-  const int64_t step = (int64_t)blockDim.x * 8;
+  const int64_t step = (int64_t)kMaxThreads * 8;
   int turn = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
     const float m = mean[row], r = rstd[row];
@@ -208,14 +358,14 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_backward_rows(const D *dy, i
       s1 += t1;
       s2 += t2;
     }
-    const float a1 = block_sum(s1, part[turn][0]) / (float)cols;
-    const float a2 = block_sum(s2, part[turn][1]) / (float)cols;
+    const float a1 = block_sum(s1, part[turn][0], kMaxWaves) / (float)cols;
+    const float a2 = block_sum(s2, part[turn][1], kMaxWaves) / (float)cols;
     if (threadIdx.x == 0) sums[row] = make_float2(a1, a2);
   }
 }
 
-// Backward, second kernel: dx, and this workgroup's rows' share of dw and db
-// for its 8 * blockDim.x columns.  partial: [gridDim.y][2][cols].
+// Wider rows, second kernel: dx, and this workgroup's rows' share of dw and
+// db for its 2048 columns.  partial: [gridDim.y][2][cols].
 template <typename X, typename D>
 __global__ __launch_bounds__(256) void k_ln_backward_cols(const D *dy, int64_t lddy, const X *x, int64_t ldx,
                                                           const float *mean, const float *rstd, const void *w,
@@ -254,21 +404,27 @@ __global__ __launch_bounds__(256) void k_ln_backward_cols(const D *dy, int64_t l
   store_row8(q, partial + ((int64_t)blockIdx.y * 2 + 1) * cols, at, cols);
 }
 
-// Backward, last kernel: dw and db from the partial sums, in a fixed order.
-// 64 columns per workgroup (of the 2 cols that dw and db make together), 4
-// interleaved shares of the partials added at the end.
-__global__ __launch_bounds__(256) void k_ln_backward_sum(const float *partial, int64_t parts, int64_t cols, void *dw,
-                                                         void *db, int g_bf16) {
-  __shared__ float share[4][64];
+// Backward, last kernel: dw and db from the partial rows, in a fixed order:
+// 64 columns per workgroup (of the 2 cols that dw and db make together), 16
+// interleaved shares of the rows, added at the end.
+constexpr int kShares = 16;
+__global__ __launch_bounds__(64 * kShares) void k_ln_backward_sum(const float *partial, int64_t parts, int64_t cols,
+                                                                  void *dw, void *db, int g_bf16) {
+  __shared__ float share[kShares][64];
   const int lane = threadIdx.x & 63, group = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
   float s = 0.0f;
-  if (c < 2 * cols)
-    for (int64_t p = group; p < parts; p += 4) s += partial[p * 2 * cols + c];
+  if (c < 2 * cols) {
+    const float *p = partial + c;
+#pragma unroll 8
+    for (int64_t k = group; k < parts; k += kShares) s += p[k * 2 * cols];
+  }
   share[group][lane] = s;
   __syncthreads();
   if (group == 0 && c < 2 * cols) {
-    s = (share[0][lane] + share[1][lane]) + (share[2][lane] + share[3][lane]);
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kShares; ++i) s += share[i][lane];
     void *out = c < cols ? dw : db;
     const int64_t k = c < cols ? c : c - cols;
     if (!out) return;
@@ -286,43 +442,87 @@ template <typename X, typename Y>
 void forward(const void *x, int64_t ldx, const void *w, const void *b, int w_bf16, void *y, int64_t ldy, float *mean,
              float *rstd, uint32_t *amax, int64_t rows, int64_t cols, float eps, hipStream_t stream) {
   const int64_t vectors = (cols + 7) / 8;
-  const unsigned grid = (unsigned)std::min<int64_t>(rows, (int64_t)device_cus() * 8);
   const X *xp = (const X *)x;
   Y *yp = (Y *)y;
-  if (vectors <= kMaxThreads)
-    k_ln_forward<X, Y, 1><<<grid, threads_for(vectors, 1), 0, stream>>>(xp, ldx, w, b, w_bf16, yp, ldy, mean, rstd,
-                                                                       amax, rows, cols, eps);
-  else if (vectors <= 2 * kMaxThreads)
-    k_ln_forward<X, Y, 2><<<grid, threads_for(vectors, 2), 0, stream>>>(xp, ldx, w, b, w_bf16, yp, ldy, mean, rstd,
-                                                                       amax, rows, cols, eps);
+  // one 8-element vector a thread where that makes a workgroup of up to 256
+  // threads, else two (fewer waves to wait for at a row's two reductions)
+  const int vpt = cols < 8 ? 0 : vectors <= 256 ? 1 : vectors <= 2 * kMaxThreads ? 2 : 0;
+  const int threads = vpt ? threads_for(vectors, vpt) : kMaxThreads;
+  // one round of workgroups: 20 waves a CU
+  const unsigned grid = (unsigned)std::min<int64_t>(rows, (int64_t)device_cus() * std::max(1, 20 * 64 / threads));
+  if (vpt == 1)
+    k_ln_forward<X, Y, 1><<<grid, threads, 0, stream>>>(xp, ldx, w, b, w_bf16, yp, ldy, mean, rstd, amax, rows, cols,
+                                                       eps, threads);
+  else if (vpt == 2)
+    k_ln_forward<X, Y, 2><<<grid, threads, 0, stream>>>(xp, ldx, w, b, w_bf16, yp, ldy, mean, rstd, amax, rows, cols,
+                                                       eps, threads);
   else
-    k_ln_forward_wide<X, Y><<<grid, kMaxThreads, 0, stream>>>(xp, ldx, w, b, w_bf16, yp, ldy, mean, rstd, amax, rows,
-                                                             cols, eps);
+    k_ln_forward_wide<X, Y><<<grid, threads, 0, stream>>>(xp, ldx, w, b, w_bf16, yp, ldy, mean, rstd, amax, rows, cols,
+                                                         eps);
 }
 
-// Rows' shares of the column sums: one per workgroup row of the grid.
-int64_t backward_parts(int64_t rows, int64_t cols) {
-  const int64_t col_groups = (cols + 2047) / 2048;
-  const int64_t want = std::max<int64_t>(1, (int64_t)device_cus() * 8 / col_groups);
-  return std::min<int64_t>(std::min<int64_t>((rows + 7) / 8, want), 2048);
+// How a backward pass is cut: vectors per thread (0 = the two kernels for
+// wider rows, which also take those of less than one vector), threads a row, rows a workgroup works on at a time, and the
+// partial rows of dw and db, one per workgroup (per workgroup row of the
+// grid for wider rows).
+struct BackCut {
+  int vpt, tpr, groups;
+  int64_t parts;
+};
+// Threads of a workgroup, by the registers that a thread takes (119 with two
+// bf16 vectors each of x and dy, 146 with f32, 206 with four bf16 vectors).
+constexpr int back_threads(int vpt, bool narrow) { return vpt == 4 ? 512 : narrow ? 1024 : 768; }
+BackCut back_cut(int64_t rows, int64_t cols, bool narrow) {      // narrow: x and dy are both bf16
+  const int64_t vectors = (cols + 7) / 8;
+  BackCut c;
+  // (four vectors of f32 do not fit the registers of 512 threads)
+  c.vpt = cols < 8 ? 0 : vectors <= 64 ? 1 : vectors <= 1024 ? 2 : vectors <= 2048 && narrow ? 4 : 0;
+  if (c.vpt) {
+    c.tpr = threads_for(vectors, c.vpt);
+    c.groups = std::max(1, back_threads(c.vpt, narrow) / c.tpr);
+    const int64_t rounds = (rows + c.groups - 1) / c.groups;
+    // one workgroup a CU, and two rounds for it at least: what the partial
+    // rows cost to write and add up stays below a pass over the data
+    c.parts = std::min((rounds + 1) / 2, (int64_t)device_cus());
+  } else {
+    c.tpr = c.groups = 0;
+    const int64_t col_groups = (cols + 2047) / 2048;
+    const int64_t want = std::max<int64_t>(1, (int64_t)device_cus() * 8 / col_groups);
+    c.parts = std::min<int64_t>((rows + 7) / 8, want);
+  }
+  return c;
 }
 
 template <typename X, typename D>
 void backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, const float *mean, const float *rstd,
               const void *w, int w_bf16, void *dx, int64_t lddx, void *dw, void *db, int g_bf16, void *workspace,
               int64_t rows, int64_t cols, hipStream_t stream) {
-  const int64_t parts = backward_parts(rows, cols);
-  float2 *sums = (float2 *)workspace;
-  float *partial = (float *)workspace + 2 * rows;
-  if (rows > 0) {
-    const unsigned grid = (unsigned)std::min<int64_t>(rows, (int64_t)device_cus() * 8);
-    k_ln_backward_rows<X, D><<<grid, threads_for((cols + 7) / 8, 1), 0, stream>>>(
-        (const D *)dy, lddy, (const X *)x, ldx, mean, rstd, w, w_bf16, sums, rows, cols);
-    k_ln_backward_cols<X, D><<<dim3((unsigned)((cols + 2047) / 2048), (unsigned)parts), 256, 0, stream>>>(
-        (const D *)dy, lddy, (const X *)x, ldx, mean, rstd, w, w_bf16, sums, (X *)dx, lddx, partial, rows, cols);
+  const BackCut c = back_cut(rows, cols, sizeof(X) + sizeof(D) == 4);
+  const D *dp = (const D *)dy;
+  const X *xp = (const X *)x;
+  X *op = (X *)dx;
+  float *partial = (float *)workspace + (c.vpt ? 0 : 2 * rows);
+  if (rows > 0 && c.vpt) {
+    const size_t lds = (size_t)(c.groups - 1) * cols * sizeof(float);
+    const auto launch = [&](auto kernel) {
+      kernel<<<(unsigned)c.parts, c.tpr * c.groups, lds, stream>>>(dp, lddy, xp, ldx, mean, rstd, w, w_bf16, op, lddx,
+                                                                  partial, rows, cols, c.tpr, c.groups);
+    };
+    constexpr bool narrow = sizeof(X) + sizeof(D) == 4;
+    if (c.vpt == 1) launch(k_ln_backward<X, D, 1, back_threads(1, narrow)>);
+    else if (c.vpt == 2) launch(k_ln_backward<X, D, 2, back_threads(2, narrow)>);
+    else if constexpr (narrow) launch(k_ln_backward<X, D, 4, back_threads(4, true)>);
+  } else if (rows > 0) {
+    float2 *sums = (float2 *)workspace;
+    const unsigned grid = (unsigned)std::min<int64_t>(rows, (int64_t)device_cus() * 2);
+    k_ln_backward_rows<X, D><<<grid, kMaxThreads, 0, stream>>>(dp, lddy, xp, ldx, mean, rstd, w, w_bf16, sums, rows,
+                                                              cols);
+    k_ln_backward_cols<X, D><<<dim3((unsigned)((cols + 2047) / 2048), (unsigned)c.parts), 256, 0, stream>>>(
+        dp, lddy, xp, ldx, mean, rstd, w, w_bf16, sums, op, lddx, partial, rows, cols);
   }
   if (dw || db)
-    k_ln_backward_sum<<<(unsigned)((2 * cols + 63) / 64), 256, 0, stream>>>(partial, parts, cols, dw, db, g_bf16);
+    k_ln_backward_sum<<<(unsigned)((2 * cols + 63) / 64), 64 * kShares, 0, stream>>>(partial, c.parts, cols, dw, db,
+                                                                                    g_bf16);
 }
 
 }  // namespace
@@ -347,7 +547,8 @@ hipError_t launch_layer_norm(const void *x, int x_dtype, int64_t rows, int64_t c
 }
 
 int64_t layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
-  return 8 * rows + 8 * cols * backward_parts(rows, cols);
+  const BackCut a = back_cut(rows, cols, false), b = back_cut(rows, cols, true);     // whatever the types
+  return std::max((a.vpt ? 0 : 8 * rows) + 8 * cols * a.parts, (b.vpt ? 0 : 8 * rows) + 8 * cols * b.parts);
 }
 
 hipError_t launch_layer_norm_backward(const void *dy, int dy_dtype, int64_t lddy, const void *x, int x_dtype,

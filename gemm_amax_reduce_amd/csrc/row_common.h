@@ -118,6 +118,22 @@ __device__ __forceinline__ void store_row8(const Row8<T> &r, T *row, int64_t at,
   else if (at < n) r.store_part(row + at, (int)(n - at));
 }
 
+// A thread's 8 columns of rows of n >= 8 elements, from position at on.  Where
+// they pass the row's end they are moved back onto its last 8, so that every
+// load and store is a whole one: the first `dup` of them then belong to other
+// threads as well, and only sums over the row have to leave them out (a
+// duplicate store writes the same value).  dup = 8: all of them.
+struct Span {
+  int64_t at;
+  int dup;
+  Span() = default;
+  __device__ __forceinline__ Span(int64_t from, int64_t n) {
+    at = min(from, n - 8);
+    dup = (int)min(from - at, (int64_t)8);
+  }
+  __device__ __forceinline__ bool mine(int i) const { return i >= dup; }
+};
+
 // A parameter vector (f32 or bf16 by a wave-uniform flag), 8 from position
 // at, `fill` past the end and where the vector is absent.
 __device__ __forceinline__ void load_param8(float *v, const void *p, int is_bf16, int64_t at, int64_t n, float fill) {
@@ -160,14 +176,15 @@ __device__ __forceinline__ float wave_fmax(float v) {
   return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// The sum over the workgroup, in every thread; the order of additions is
-// fixed.  part: LDS, one float per wave; the caller leaves a barrier between
-// two uses of the same array.
-__device__ __forceinline__ float block_sum(float v, float *part) {
-  const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+// The sum over the workgroup's `waves` waves, in every thread; the order of
+// additions is fixed.  part: LDS, one float per wave; the caller leaves a
+// barrier between two uses of the same array.  (The number of waves is an
+// argument: blockDim reads as a vector load with its own wait on this
+// target, and in a loop that would stall whatever is being fetched ahead.)
+__device__ __forceinline__ float block_sum(float v, float *part, int waves) {
   v = wave_sum(v);
   if (waves == 1) return v;
-  if ((threadIdx.x & 63) == 0) part[wave] = v;
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
   __syncthreads();
   float s = 0.0f;
   for (int i = 0; i < waves; ++i) s += part[i];
