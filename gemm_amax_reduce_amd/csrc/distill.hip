@@ -22,7 +22,9 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kDT = 256;             // threads of a workgroup
+constexpr int kDT = 256;             // threads of a segment's workgroup
+constexpr int kRowThreads = 1024;    // threads of a row's workgroup, at most
+constexpr int kMaxWaves = kRowThreads / 64;
 constexpr int kMaxTop = 1024;        // entries of a teacher's list
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -39,35 +41,252 @@ __device__ __forceinline__ float2 join(float2 a, float2 b, float scale) {
   return make_float2(m, sa + sb);
 }
 
-// Statistics of one segment of one row.
+// exp(z / tau - lse), with lse = top_z / tau + l2 ln 2
+__device__ __forceinline__ float share_of(float z, float top_z, float scale, float l2) {
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(z - top_z, scale, -l2));
+}
+
+// The sum of 2^((v - m) scale) over 8 values, the first `dup` left out.
+// All -inf (m = -inf) give 0, a NaN gives NaN.
+__device__ __forceinline__ float exp_sum8(const float *v, float m, float scale, int dup, bool ragged) {
+  float s = 0.0f;
+  if (!ragged) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += __builtin_amdgcn_exp2f((v[i] - m) * scale);
+    return dup ? 0.0f : s;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s += i >= dup ? __builtin_amdgcn_exp2f((v[i] - m) * scale) : 0.0f;
+  return s;
+}
+
+// A row's teacher list in LDS: the binary logarithm of p, and the index (-1
+// where invalid).  p itself is 2^lp where it is used: log p taken from p
+// would be -inf for the smallest shares.
+struct Teacher {
+  float lp[kMaxTop];
+  int32_t at[kMaxTop];
+  float share[2][kMaxWaves];
+};
+struct List {
+  const void *idx, *t;
+  int idx64, t_bf16, top;
+  __device__ __forceinline__ int64_t index(int64_t row, int k) const {
+    const int64_t e = row * top + k;
+    return idx64 ? ((const int64_t *)idx)[e] : (int64_t)((const int32_t *)idx)[e];
+  }
+  __device__ __forceinline__ float logit(int64_t row, int k) const {
+    const int64_t e = row * top + k;
+    return t_bf16 ? bf16_bits_f32(((const uint16_t *)t)[e]) : ((const float *)t)[e];
+  }
+};
+// The thread's first entry, fetched before anything else.
+struct Entry {
+  int64_t i = -1;
+  float v = 0.0f;
+  __device__ __forceinline__ Entry(const List &l, int64_t row) {
+    if ((int)threadIdx.x < l.top) {
+      i = l.index(row, threadIdx.x);
+      v = l.logit(row, threadIdx.x);
+    }
+  }
+};
+// Returns whether any entry is valid; all threads see the list then.
+__device__ __forceinline__ bool load_teacher(Teacher &te, const List &l, Entry e, int64_t row, int64_t V, float scale,
+                                             int threads) {
+  const int waves = threads >> 6;
+  float m = -INFINITY;
+  bool any = false;
+  for (int k = threadIdx.x; k < l.top; k += threads) {
+    if (k != (int)threadIdx.x) {
+      e.i = l.index(row, k);
+      e.v = l.logit(row, k);
+    }
+    const bool ok = e.i >= 0 && e.i < V && e.v != -INFINITY;
+    te.at[k] = ok ? (int32_t)e.i : -1;
+    te.lp[k] = e.v;
+    if (ok) m = fmaxf(m, e.v);
+    any |= ok;
+  }
+  m = wave_fmax(m);
+  if ((threadIdx.x & 63) == 0) te.share[0][threadIdx.x >> 6] = m;
+  const bool some = __syncthreads_or(any);
+  for (int w = 0; w < waves; ++w) m = fmaxf(m, te.share[0][w]);
+  float s = 0.0f;
+  for (int k = threadIdx.x; k < l.top; k += threads) {
+    const float d = (te.lp[k] - m) * scale;
+    te.lp[k] = d;
+    s += te.at[k] >= 0 ? __builtin_amdgcn_exp2f(d) : 0.0f;
+  }
+  const float n = __builtin_amdgcn_logf(block_sum(s, te.share[1], waves));
+  for (int k = threadIdx.x; k < l.top; k += threads) te.lp[k] -= n;
+  __syncthreads();
+  return some;
+}
+
+// The sum over the list of p (log2 p - log2 q); zr: the student's row.
+template <typename T>
+__device__ __forceinline__ float list_sum(const Teacher &te, const T *zr, int top, float top_z, float scale, float l2,
+                                          int threads) {
+  float a = 0.0f;
+  for (int k = threadIdx.x; k < top; k += threads) {
+    const float p = __builtin_amdgcn_exp2f(te.lp[k]);
+    if (te.at[k] < 0 || p == 0.0f) continue;      // 0 log 0 = 0
+    const float q = (to_float(zr[te.at[k]]) - top_z) * scale - l2;    // log2 of the student's share
+    a = __builtin_fmaf(p, te.lp[k] - q, a);
+  }
+  return a;
+}
+
+// The gradient at the listed entries of [begin, end), stored over what the
+// student's share alone gave.  An index that is listed twice takes the sum
+// of its shares, in list order, so its writers store the same value.
+template <typename T>
+__device__ __forceinline__ void list_gradient(const Teacher &te, const T *zr, T *dr, int top, int64_t begin, int64_t end,
+                                              float c, float top_z, float scale, float l2, int threads) {
+  __syncthreads();
+  for (int k = threadIdx.x; k < top; k += threads) {
+    const int32_t i = te.at[k];
+    if (i < begin || i >= end) continue;
+    float p = 0.0f;
+#pragma unroll 4
+    for (int j = 0; j < top; ++j) p += te.at[j] == i ? __builtin_amdgcn_exp2f(te.lp[j]) : 0.0f;
+    store_one(dr + i, c * (share_of(to_float(zr[i]), top_z, scale, l2) - p));
+  }
+}
+
+// The thread's j-th vector of a row of V >= 8 (at most 2^17) elements, as in
+// Span but in 32 bits.  `from` is made opaque before each use of all of them,
+// so that a use computes the positions anew instead of keeping VPT of them.
+struct Vectors {
+  uint32_t from, step, last;
+  __device__ __forceinline__ Vectors(int threads, int64_t V)
+      : from(threadIdx.x * 8), step(threads * 8), last((uint32_t)V - 8) {}
+  __device__ __forceinline__ void anew() { asm volatile("" : "+v"(from)); }
+  __device__ __forceinline__ uint32_t at(int j) const { return min(from + j * step, last); }
+  __device__ __forceinline__ int dup(int j) const { return (int)min(from + j * step - at(j), 8u); }
+};
+
+// A whole row in the registers of one workgroup: read once, written once.
+// Its vectors of 8 are dealt out VPT to a thread.  The list is fetched first
+// and worked on while the row arrives.
+template <typename T, int VPT>
+__global__ __launch_bounds__(kRowThreads) void k_distill_row(const T *z, int64_t ldz, int64_t V, List list, float tau,
+                                                             const float *weight, float *loss, float *lse, T *dz,
+                                                             int64_t lddz, int threads) {
+  __shared__ Teacher te;
+  __shared__ float part[3][kMaxWaves];
+  const int64_t row = blockIdx.x;
+  const int waves = threads >> 6;
+  const float scale = kLog2e / tau;
+  const bool ragged = V & 7;
+  const T *zr = z + row * ldz;
+  const Entry first(list, row);
+  Vectors vec(threads, V);
+  Row8<T> q[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) q[j].load(zr + vec.at(j));
+  __builtin_amdgcn_sched_barrier(0);
+  const bool some = load_teacher(te, list, first, row, V, scale, threads);
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    float v[8];
+    q[j].get(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, v[i]);
+  }
+  m = wave_fmax(m);
+  if ((threadIdx.x & 63) == 0) part[0][threadIdx.x >> 6] = m;
+  __syncthreads();
+  for (int w = 0; w < waves; ++w) m = fmaxf(m, part[0][w]);
+  float s = 0.0f;
+  vec.anew();
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) q[j].keep_packed();
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    float v[8];
+    q[j].get(v);
+    s += exp_sum8(v, m, scale, vec.dup(j), ragged);
+  }
+  s = block_sum(s, part[1], waves);
+  const float l2 = __builtin_amdgcn_logf(s);
+  float a = some ? list_sum(te, zr, list.top, m, scale, l2, threads) : 0.0f;
+  a = block_sum(a, part[2], waves);
+  if (threadIdx.x == 0) {
+    loss[row] = some ? tau * tau * kLn2 * a : 0.0f;
+    lse[row] = m / tau + l2 * kLn2;
+  }
+  const float c = some ? weight[row] * tau : 0.0f;
+  T *dr = dz + row * lddz;
+  vec.anew();
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) q[j].keep_packed();
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    float v[8];
+    q[j].get(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c * share_of(v[i], m, scale, l2);
+    if (c == 0.0f)                     // the same for the whole row: zeros even where a logit is NaN
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    q[j].set(v);
+    if (vec.dup(j) < 8) q[j].store(dr + vec.at(j));
+  }
+  if (c != 0.0f) list_gradient(te, zr, dr, list.top, 0, V, c, m, scale, l2, threads);
+}
+
+// Without a gradient, for few rows, or for rows that registers do not hold:
+// statistics of one segment of one row, kBatch vectors of a thread in flight
+// together.  A vector that passes the segment's end is moved back inside it.
+constexpr int kBatch = 4;
 template <typename T>
 __global__ __launch_bounds__(kDT) void k_distill_stats(const T *z, int64_t ldz, int64_t V, int64_t seg_len,
                                                        float scale, float2 *part) {
   __shared__ float2 share[kDT / 64];
   const int64_t row = blockIdx.y, seg = blockIdx.x;
-  const T *zr = z + row * ldz;
-  const int64_t end = min(V, (seg + 1) * seg_len);
+  const int64_t begin = seg * seg_len, n = min(V - begin, seg_len);
+  const T *zr = z + row * ldz + begin;
   float2 st = make_float2(-INFINITY, 0.0f);
-  for (int64_t at = seg * seg_len + threadIdx.x * 8; at < end; at += kDT * 8) {
-    Row8<T> q;
-    load_row8(q, zr, at, end);
-    float v[8];
-    q.get(v);
-    float m = st.x;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = at + i < end ? v[i] : -INFINITY;
-      m = fmaxf(m, v[i]);
+  if (n < 8) {                       // less than a vector: an element a thread
+    if ((int64_t)threadIdx.x < n) {
+      const float v = to_float(zr[threadIdx.x]);
+      st = v != v ? make_float2(-INFINITY, v) : make_float2(v, v > -INFINITY ? 1.0f : 0.0f);
     }
-    if (m > -INFINITY) {             // fmaxf passes a NaN by: it enters through the sum
-      float s = st.x == m ? st.y : st.y * __builtin_amdgcn_exp2f((st.x - m) * scale);
+  } else {
+    const bool ragged = n & 7;
+    for (int64_t at = threadIdx.x * 8; at < n; at += kBatch * kDT * 8) {
+      Row8<T> q[kBatch];
+      Span sp[kBatch];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += __builtin_amdgcn_exp2f((v[i] - m) * scale);
-      st = make_float2(m, s);
-    } else {
+      for (int j = 0; j < kBatch; ++j) {
+        sp[j] = Span(at + j * kDT * 8, n);
+        q[j].load(zr + sp[j].at);
+      }
+      float m = st.x;
+      float v[kBatch][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (v[i] != v[i]) st.y = v[i];
+      for (int j = 0; j < kBatch; ++j) {
+        q[j].get(v[j]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, v[j][i]);
+      }
+      // fmaxf passes a NaN by: it enters through the sum.  (m = -inf: all were
+      // masked so far, and -inf - -inf would be NaN.)
+      if (m > -INFINITY) {
+        float s = st.x == m ? st.y : st.y * __builtin_amdgcn_exp2f((st.x - m) * scale);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) s += exp_sum8(v[j], m, scale, sp[j].dup, ragged);
+        st = make_float2(m, s);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (v[j][i] != v[j][i]) st.y = v[j][i];
+      }
     }
   }
 #pragma unroll
@@ -81,56 +300,12 @@ __global__ __launch_bounds__(kDT) void k_distill_stats(const T *z, int64_t ldz, 
   }
 }
 
-// A row's teacher list in LDS: the binary logarithm of p, and the index (-1
-// where invalid); load_teacher returns whether any entry is valid.  p itself
-// is 2^lp where it is used: log p taken from p would be -inf for the
-// smallest shares.
-struct Teacher {
-  float lp[kMaxTop];
-  int32_t at[kMaxTop];
-  float share[2][kDT / 64];
-};
-__device__ __forceinline__ bool load_teacher(Teacher &te, const void *idx, int idx64, const void *t, int t_bf16,
-                                             int64_t row, int top, int64_t V, float scale) {
-  float m = -INFINITY;
-  bool any = false;
-  for (int k = threadIdx.x; k < top; k += kDT) {
-    const int64_t e = row * top + k;
-    const int64_t i = idx64 ? ((const int64_t *)idx)[e] : (int64_t)((const int32_t *)idx)[e];
-    const float v = t_bf16 ? bf16_bits_f32(((const uint16_t *)t)[e]) : ((const float *)t)[e];
-    const bool ok = i >= 0 && i < V && v != -INFINITY;
-    te.at[k] = ok ? (int32_t)i : -1;
-    te.lp[k] = v;
-    if (ok) m = fmaxf(m, v);
-    any |= ok;
-  }
-  m = wave_fmax(m);
-  if ((threadIdx.x & 63) == 0) te.share[0][threadIdx.x >> 6] = m;
-  const bool some = __syncthreads_or(any);
-  for (int w = 0; w < kDT / 64; ++w) m = fmaxf(m, te.share[0][w]);
-  float s = 0.0f;
-  for (int k = threadIdx.x; k < top; k += kDT) {
-    const float d = (te.lp[k] - m) * scale;
-    te.lp[k] = d;
-    s += te.at[k] >= 0 ? __builtin_amdgcn_exp2f(d) : 0.0f;
-  }
-  const float l = __builtin_amdgcn_logf(block_sum(s, te.share[1], kDT / 64));
-  for (int k = threadIdx.x; k < top; k += kDT) te.lp[k] -= l;
-  __syncthreads();
-  return some;
-}
-
-__device__ __forceinline__ float share_of(float z, float top_z, float scale, float l2) {
-  return __builtin_amdgcn_exp2f(__builtin_fmaf(z - top_z, scale, -l2));
-}
-
 // Loss and log-sum-exp of a row from its segments' statistics (part != null),
 // and, with GRAD, the gradient of one segment.  Without part the log-sum-exp
 // is read from lse and no loss is formed.  grid: (segments or 1, rows).
 template <typename T, bool GRAD>
 __global__ __launch_bounds__(kDT) void k_distill_finish(const T *z, int64_t ldz, int64_t V, int64_t seg_len,
-                                                        int segments, const float2 *part, const void *idx, int idx64,
-                                                        const void *t, int t_bf16, int top, float tau,
+                                                        int segments, const float2 *part, List list, float tau,
                                                         const float *weight, float *loss, float *lse, T *dz,
                                                         int64_t lddz) {
   __shared__ Teacher te;
@@ -138,8 +313,7 @@ __global__ __launch_bounds__(kDT) void k_distill_finish(const T *z, int64_t ldz,
   const int64_t row = blockIdx.y, seg = blockIdx.x;
   const float scale = kLog2e / tau;
   const T *zr = z + row * ldz;
-  const bool some = load_teacher(te, idx, idx64, t, t_bf16, row, top, V, scale);
-  // exp(z / tau - lse) = 2^((z - top) scale - l2)
+  const bool some = load_teacher(te, list, Entry(list, row), row, V, scale, kDT);
   float top_z, l2;
   if (part) {
     float2 st = part[row * segments];
@@ -147,14 +321,7 @@ __global__ __launch_bounds__(kDT) void k_distill_finish(const T *z, int64_t ldz,
     top_z = st.x;
     l2 = __builtin_amdgcn_logf(st.y);
     if (seg == 0) {
-      float a = 0.0f;
-      if (some)
-        for (int k = threadIdx.x; k < top; k += kDT) {
-          const float p = __builtin_amdgcn_exp2f(te.lp[k]);
-          if (te.at[k] < 0 || p == 0.0f) continue;      // 0 log 0 = 0
-          const float q = (to_float(zr[te.at[k]]) - top_z) * scale - l2;    // log2 of the student's share
-          a = __builtin_fmaf(p, te.lp[k] - q, a);
-        }
+      float a = some ? list_sum(te, zr, list.top, top_z, scale, l2, kDT) : 0.0f;
       a = block_sum(a, sums, kDT / 64);
       if (threadIdx.x == 0) {
         loss[row] = some ? tau * tau * kLn2 * a : 0.0f;
@@ -168,31 +335,38 @@ __global__ __launch_bounds__(kDT) void k_distill_finish(const T *z, int64_t ldz,
   if (!GRAD) return;
   const float c = some ? weight[row] * tau : 0.0f;
   T *dr = dz + row * lddz;
-  const int64_t begin = seg * seg_len, end = min(V, begin + seg_len);
-  for (int64_t at = begin + threadIdx.x * 8; at < end; at += kDT * 8) {
-    Row8<T> q;
-    load_row8(q, zr, at, end);
+  const int64_t begin = seg * seg_len, end = min(V, begin + seg_len), n = end - begin;
+  const auto gradient = [&](Row8<T> &q) {
     float v[8];
     q.get(v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c == 0.0f ? 0.0f : c * share_of(v[i], top_z, scale, l2);
+    for (int i = 0; i < 8; ++i) v[i] = c * share_of(v[i], top_z, scale, l2);
+    if (c == 0.0f)                     // the same for the whole row: zeros even where a logit is NaN
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
     q.set(v);
-    store_row8(q, dr, at, end);
+  };
+  if (n < 8) {
+    if (threadIdx.x == 0) {
+      Row8<T> q;
+      load_row8(q, zr + begin, 0, n);
+      gradient(q);
+      store_row8(q, dr + begin, 0, n);
+    }
+  } else {
+    for (int64_t at = threadIdx.x * 8; at < n; at += kBatch * kDT * 8) {
+      Row8<T> q[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) q[j].load(zr + begin + Span(at + j * kDT * 8, n).at);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const Span sp(at + j * kDT * 8, n);
+        gradient(q[j]);
+        if (sp.dup < 8) q[j].store(dr + begin + sp.at);
+      }
+    }
   }
-  if (c == 0.0f) return;
-  // the listed entries again, with the teacher's share; an index that is
-  // listed twice takes the sum of its shares, in list order, so its writers
-  // store the same value
-  __syncthreads();
-  for (int k = threadIdx.x; k < top; k += kDT) {
-    const int32_t i = te.at[k];
-    if (i < begin || i >= end) continue;
-    float p = 0.0f;
-    for (int j = 0; j < top; ++j)
-      if (te.at[j] == i) p += __builtin_amdgcn_exp2f(te.lp[j]);
-    const float g = c * (share_of(to_float(zr[i]), top_z, scale, l2) - p);
-    store_one(dr + i, g);
-  }
+  if (c != 0.0f) list_gradient(te, zr, dr, list.top, begin, end, c, top_z, scale, l2, kDT);
 }
 
 struct Split {
@@ -209,29 +383,54 @@ Split split_for(int64_t T, int64_t V) {
   return {len, (int)((V + len - 1) / len)};
 }
 
+// Vectors per thread of the one-workgroup-a-row form (loss and gradient in
+// one pass); 0 where the segments' form is taken: rows that 1024 threads do not hold in 64 registers each (or
+// shorter than a vector), or too few to give every CU one.
+int row_vectors(int64_t rows, int64_t V, bool f32) {
+  const int64_t vectors = (V + 7) / 8;
+  if (V < 8 || rows < device_cus() * 3 / 4) return 0;
+  if (vectors <= 4 * 256) return 4;
+  if (vectors <= 8 * kRowThreads) return 8;
+  return vectors <= 16 * kRowThreads && !f32 ? 16 : 0;
+}
+
+template <typename T, int VPT>
+void rows_of(const T *z, int64_t rows, int64_t V, int64_t ldz, const List &list, float tau, const float *weight,
+             float *loss, float *lse, T *dz, int64_t lddz, hipStream_t stream) {
+  const int threads = (int)(((V + 7) / 8 + VPT - 1) / VPT + 63) / 64 * 64;
+  k_distill_row<T, VPT><<<(unsigned)rows, threads, 0, stream>>>(z, ldz, V, list, tau, weight, loss, lse, dz, lddz,
+                                                               threads);
+}
+
 template <typename T>
-void run(const void *z, int64_t rows, int64_t V, int64_t ldz, const void *idx, int idx64, const void *t, int t_bf16,
-         int top, float tau, const float *weight, float *loss, float *lse, void *dz, int64_t lddz, void *workspace,
-         bool stats, hipStream_t stream) {
+void run(const void *zv, int64_t rows, int64_t V, int64_t ldz, List list, float tau, const float *weight, float *loss,
+         float *lse, void *dz, int64_t lddz, void *workspace, bool stats, hipStream_t stream) {
+  const T *z = (const T *)zv;
+  const int vpt = stats && dz ? row_vectors(rows, V, sizeof(T) == 4) : 0;
+  if (vpt == 4) rows_of<T, 4>(z, rows, V, ldz, list, tau, weight, loss, lse, (T *)dz, lddz, stream);
+  else if (vpt == 8) rows_of<T, 8>(z, rows, V, ldz, list, tau, weight, loss, lse, (T *)dz, lddz, stream);
+  else if (vpt == 16)
+    rows_of<uint16_t, 16>((const uint16_t *)zv, rows, V, ldz, list, tau, weight, loss, lse, (uint16_t *)dz, lddz, stream);
+  if (vpt) return;
   const Split sp = split_for(rows, V);
   float2 *part = stats ? (float2 *)workspace : nullptr;
   // rows on the grid's y dimension, 65535 at most per launch
   for (int64_t r = 0; r < rows; r += 65535) {
     const unsigned n = (unsigned)std::min<int64_t>(65535, rows - r);
-    const T *zr = (const T *)z + r * ldz;
-    const char *ir = (const char *)idx + r * top * (idx64 ? 8 : 4);
-    const char *tr = (const char *)t + r * top * (t_bf16 ? 2 : 4);
+    const T *zr = z + r * ldz;
+    List lr = list;
+    lr.idx = (const char *)list.idx + r * list.top * (list.idx64 ? 8 : 4);
+    lr.t = (const char *)list.t + r * list.top * (list.t_bf16 ? 2 : 4);
     float2 *pr = part ? part + r * sp.segments : nullptr;
     if (stats)
       k_distill_stats<T><<<dim3(sp.segments, n), kDT, 0, stream>>>(zr, ldz, V, sp.seg_len, kLog2e / tau, pr);
     if (dz)
-      k_distill_finish<T, true><<<dim3(sp.segments, n), kDT, 0, stream>>>(
-          zr, ldz, V, sp.seg_len, sp.segments, pr, ir, idx64, tr, t_bf16, top, tau, weight + r,
-          loss ? loss + r : nullptr, lse + r, (T *)dz + r * lddz, lddz);
+      k_distill_finish<T, true><<<dim3(sp.segments, n), kDT, 0, stream>>>(zr, ldz, V, sp.seg_len, sp.segments, pr, lr,
+                                                                         tau, weight + r, loss ? loss + r : nullptr,
+                                                                         lse + r, (T *)dz + r * lddz, lddz);
     else
-      k_distill_finish<T, false><<<dim3(1, n), kDT, 0, stream>>>(zr, ldz, V, sp.seg_len, sp.segments, pr, ir, idx64,
-                                                                 tr, t_bf16, top, tau, nullptr, loss + r, lse + r,
-                                                                 nullptr, 0);
+      k_distill_finish<T, false><<<dim3(1, n), kDT, 0, stream>>>(zr, ldz, V, sp.seg_len, sp.segments, pr, lr, tau,
+                                                                 nullptr, loss + r, lse + r, nullptr, 0);
   }
 }
 
@@ -245,12 +444,9 @@ hipError_t launch_distill(const void *z, int z_dtype, int64_t rows, int64_t V, i
                           const void *t, int t_dtype, int top, float tau, const float *weight, float *loss, float *lse,
                           void *dz, int64_t lddz, void *workspace, bool stats, hipStream_t stream) {
   if (rows > 0) {
-    if (z_dtype == 1)
-      run<uint16_t>(z, rows, V, ldz, idx, idx64, t, t_dtype == 1, top, tau, weight, loss, lse, dz, lddz, workspace,
-                    stats, stream);
-    else
-      run<float>(z, rows, V, ldz, idx, idx64, t, t_dtype == 1, top, tau, weight, loss, lse, dz, lddz, workspace, stats,
-                 stream);
+    const List list = {idx, t, idx64, t_dtype == 1, top};
+    if (z_dtype == 1) run<uint16_t>(z, rows, V, ldz, list, tau, weight, loss, lse, dz, lddz, workspace, stats, stream);
+    else run<float>(z, rows, V, ldz, list, tau, weight, loss, lse, dz, lddz, workspace, stats, stream);
   }
   return hipGetLastError();
 }

@@ -47,6 +47,9 @@ template <> struct Row8<uint16_t> {
     r = (u32x4_a4){w[0], w[1], w[2], w[3]};
   }
   __device__ __forceinline__ void zero() { r = (u32x4_a4){0, 0, 0, 0}; }
+  // Opaque to the compiler: what was computed from the raw bits before is
+  // computed anew after it, instead of being kept in twice the registers.
+  __device__ __forceinline__ void keep_packed() { asm volatile("" : "+v"(r)); }
   __device__ __forceinline__ void get(float *v) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -81,6 +84,7 @@ template <> struct Row8<float> {
     set(v);
   }
   __device__ __forceinline__ void zero() { a = b = (f32x4_a4){0, 0, 0, 0}; }
+  __device__ __forceinline__ void keep_packed() {}
   __device__ __forceinline__ void get(float *v) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
