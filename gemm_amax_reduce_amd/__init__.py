@@ -584,14 +584,16 @@ def mxfp8_gemm(a: MXFP8Tensor, b: MXFP8Tensor, out_dtype=torch.float32, out: tor
 # another stream's unfinished work is not reused.
 # ----------------------------------------------------------------------------
 
+_here = contextlib.nullcontext()
+_current_device = torch.cuda.current_device
+
+
 def _on(device: torch.device, stream):
     """The context that makes `device` and `stream` current; nothing to do
     (and nothing to pay) where they are already."""
     if stream is not None:
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    return _here if _current_device() == device.index else torch.cuda.device(device)
 
 
 def _require_matrix(t: torch.Tensor, name: str, device: torch.device | None = None, shape=None) -> int:

@@ -373,12 +373,14 @@ struct Split {
   int64_t seg_len;
   int segments;
 };
-// Segments of a row: enough workgroups to fill the GPU, none shorter than
-// four loads of every thread, their starts at whole 8-element vectors.
+// Segments of a row: enough workgroups to fill the GPU twice over (16 a CU;
+// 777 rows of 50021 f32: 1 segment 34 us, 2 32, 4 29, 8 28), none longer than
+// 32768 elements, none shorter than four loads of every thread, their starts
+// at whole 8-element vectors.
 Split split_for(int64_t T, int64_t V) {
   const int64_t vec = (int64_t)kDT * 8;
-  const int64_t want = std::max<int64_t>(1, (int64_t)device_cus() * 8 / std::max<int64_t>(1, T));
-  int64_t s = std::max<int64_t>(1, std::min<int64_t>(want, V / (4 * vec)));
+  const int64_t want = std::max<int64_t>(V / 32768, (int64_t)device_cus() * 16 / std::max<int64_t>(1, T));
+  const int64_t s = std::max<int64_t>(1, std::min<int64_t>(want, V / (4 * vec)));
   const int64_t len = ((V + s - 1) / s + vec - 1) / vec * vec;
   return {len, (int)((V + len - 1) / len)};
 }
