@@ -100,26 +100,16 @@ __device__ __forceinline__ half8_t decode8_f16(uint32_t w, half2_t s) {
   return (half8_t){v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]};
 }
 
-// 32 consecutive x of one token as loaded: 16-byte pieces at any alignment.
+// 32 consecutive x of one token, 16-byte pieces.
 template <typename X> struct Act {
   static constexpr int kPieces = 32 * sizeof(X) / 16;
   u32x4_t v[kPieces];
-  __device__ __forceinline__ void load(const X *p) {
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) v[i] = *reinterpret_cast<const u32x4_a2 *>((const char *)p + 16 * i);
-  }
-  // zero the first n of the 32
-  __device__ __forceinline__ void drop(int n) {
-    constexpr int kPerWord = 4 / sizeof(X);
-#pragma unroll
-    for (int i = 0; i < 4 * kPieces; ++i)
-      if (i * kPerWord < n) v[i >> 2][i & 3] = 0;      // n is a multiple of 16
-  }
 };
 
-// The last load of a row may reach past its end: it is moved back to the
-// row's last 32 k, and the x of those already taken are zeroed.  Returns the
-// k to load from and how many of the 32 to drop (32 past the end).
+// A lane's last load of a row may reach past the end: it is moved back to the
+// row's last 32 k, and meets zeros where it is not the row's own.  Makes k
+// where to load from; returns by how many it was moved, 32 if nothing of the
+// row is left.
 __device__ __forceinline__ int last_window(int64_t &k, int64_t K) {
   const int64_t at = min(k, K - 32);
   const int drop = (int)min(k - at, (int64_t)32);
@@ -549,22 +539,39 @@ __global__ __launch_bounds__(64 * kRowWaves) void k_matvec_row(const uint8_t *co
                                                                const float *meta, int64_t N, int64_t K, const X *x,
                                                                void *y, int y_bf16) {
   constexpr int kRows = kRowWaves / WK;
+  // x through LDS: a lane's 32 k would be a load of 64 lines of memory.  Each
+  // of J rounds takes the waves' j-th loads; unit u (16 bytes) lies at slot u
+  // with its lowest bits turned by the next ones, so that 16 lanes' reads of
+  // one piece each fall on all banks.
+  constexpr int kUnit = 16 / sizeof(X), kPieces = Act<X>::kPieces;
+  constexpr int kWaveUnits = kWaveK / kUnit, kLoads = WK * kWaveUnits / (64 * kRowWaves);
+  __shared__ u32x4_t turned[WK * kWaveUnits];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = wave % WK;
-  uint32_t k[J];
-  Act<X> xv[J];
+  const auto slot = [](uint32_t u) { return u ^ ((u >> 4) & (kPieces - 1)); };
+  u32x4_t raw[J][kLoads];
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    int64_t at = (int64_t)((kw * J + j) * 64 + lane) * 32;
-    const int drop = last_window(at, K);
-    k[j] = (uint32_t)at;
-    xv[j].load(x + at);
-    xv[j].drop(drop);
-  }
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int u = threadIdx.x + i * 64 * kRowWaves;
+      const int64_t at = (int64_t)(u / kWaveUnits * J + j) * kWaveK + u % kWaveUnits * kUnit;
+      raw[j][i] = (u32x4_t){0, 0, 0, 0};
+      if (at < K) raw[j][i] = *reinterpret_cast<const u32x4_a2 *>(x + at);
+    }
   const float g = MX ? 1.0f : meta[1];
   const int64_t stride = (int64_t)gridDim.x * kRows;
   const int64_t first = (int64_t)blockIdx.x * kRows + wave / WK;
   __shared__ float share[2][kRowWaves];
+  uint32_t k[J];
+  int half = 0;                                      // loads (as bits) that were moved back by 16
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    int64_t at = (int64_t)((kw * J + j) * 64 + lane) * 32;
+    half |= (last_window(at, K) == 16) << j;
+    k[j] = (uint32_t)at;
+  }
+  Act<X> xv[J];
   RowPart<MX, J> a, b;
   const auto load = [&](RowPart<MX, J> &p, int64_t n) {
     n = min(n, N - 1);
@@ -584,8 +591,19 @@ __global__ __launch_bounds__(64 * kRowWaves) void k_matvec_row(const uint8_t *co
     }
     if (lane == 0 && kw == 0 && n < N) store_y(y, y_bf16, n, sum * g);
   };
-  // the workgroup's waves make the same number of turns (barriers)
   load(a, first);
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    if (j) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) turned[slot(threadIdx.x + i * 64 * kRowWaves)] = raw[j][i];
+    __syncthreads();
+    // (moved back by 16: its x are the load's first half, zeros before them)
+    const int swap = ((half >> j) & 1) * (kPieces / 2);
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) xv[j].v[p] = turned[slot(kw * kWaveUnits + lane * kPieces + (p ^ swap))];
+  }
+  // the workgroup's waves make the same number of turns (barriers)
   for (int64_t n = first; n - wave / WK < N; n += 2 * stride) {
     load(b, n + stride);
     finish(a, n, 0);
@@ -644,8 +662,10 @@ void tile(const Cut &c, const uint8_t *codes, const uint8_t *scales, const float
 template <bool MX, typename X, int J, int WK>
 void rows(const uint8_t *codes, const uint8_t *scales, const float *meta, int64_t N, int64_t K, const X *x, void *y,
           int y_bf16, hipStream_t stream) {
-  const int64_t per = kRowWaves / WK;
-  const unsigned grid = (unsigned)std::min<int64_t>((N + per - 1) / per, (int64_t)device_cus() * 4);
+  // 12 waves a CU (20480 x 5120: 13.5 us, with 16 waves 14.7, 32 16.1), the rows dealt evenly
+  const int64_t per = kRowWaves / WK, turns = (N + per - 1) / per, slots = (int64_t)device_cus() * 3;
+  const int64_t each = (turns + slots - 1) / slots;
+  const unsigned grid = (unsigned)((turns + each - 1) / each);
   k_matvec_row<MX, X, J, WK><<<grid, 64 * kRowWaves, 0, stream>>>(codes, scales, meta, N, K, x, y, y_bf16);
 }
 
