@@ -625,9 +625,11 @@ def _param(t, name: str, cols: int, device: torch.device):
         return None, F32
     if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.shape[0] != cols:
         raise NVFP4Error(f"{name} must be a vector of {cols} elements")
-    code = _dtype_code(t)
-    _require_buffer(t, name, t.dtype, cols, device)
-    return t.data_ptr(), code
+    if t.device != device:
+        raise NVFP4Error(f"{name} must be a GPU tensor on {device}")
+    if not t.is_contiguous():
+        raise NVFP4Error(f"{name} must be contiguous")
+    return t.data_ptr(), _dtype_code(t)
 
 
 def _ptr(t):
@@ -665,15 +667,16 @@ def nvfp4_layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: 
     elif bp is not None and bcode != wcode:
         raise NVFP4Error("weight and bias must have the same dtype")
     with _on(dev, stream):
-        y = torch.empty((rows, cols), dtype=out_dtype, device=dev) if out is None else out
-        ldy = _require_matrix_out(y, rows, cols, out_dtype, dev) if out is not None else max(cols, 1)
-        stats = torch.empty((2, rows), dtype=torch.float32, device=dev)
+        if out is None:
+            y, ldy = torch.empty((rows, cols), dtype=out_dtype, device=dev), max(cols, 1)
+        else:
+            y, ldy = out, _require_matrix_out(out, rows, cols, out_dtype, dev)
+        mean = torch.empty(rows, dtype=torch.float32, device=dev)
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
         top = torch.empty(1, dtype=torch.float32, device=dev) if amax else None
-        p = stats.data_ptr()
-        _check(lib().nvfp4_layer_norm(x.data_ptr(), _dtype_code(x), rows, cols, ldx, wp, bp, wcode, float(eps),
-                                      y.data_ptr(), ycode, ldy, p, p + 4 * rows, _ptr(top),
-                                      _current_handle(dev)), "nvfp4_layer_norm")
-    mean, rstd = stats.unbind(0)
+        _check(lib().nvfp4_layer_norm(x.data_ptr(), _dtype_code(x), rows, cols, ldx, wp, bp, wcode, eps, y.data_ptr(),
+                                      ycode, ldy, mean.data_ptr(), rstd.data_ptr(), _ptr(top), _current_handle(dev)),
+               "nvfp4_layer_norm")
     return (y, mean, rstd, top) if amax else (y, mean, rstd)
 
 
@@ -694,15 +697,14 @@ def nvfp4_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Ten
         _check(need, "nvfp4_layer_norm_backward")
     with _on(dev, stream):
         dx = torch.empty((rows, cols), dtype=x.dtype, device=dev)
-        dwb = torch.empty((2, cols), dtype=grad_dtype, device=dev)
+        dweight = torch.empty(cols, dtype=grad_dtype, device=dev)
+        dbias = torch.empty(cols, dtype=grad_dtype, device=dev)
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        p = dwb.data_ptr()
         _check(lib().nvfp4_layer_norm_backward(dy.data_ptr(), _dtype_code(dy), lddy, x.data_ptr(), _dtype_code(x),
                                                rows, cols, ldx, mean.data_ptr(), rstd.data_ptr(), wp, wcode,
-                                               dx.data_ptr(), cols, p, p + cols * dwb.element_size(), gcode,
+                                               dx.data_ptr(), cols, dweight.data_ptr(), dbias.data_ptr(), gcode,
                                                ws.data_ptr(), need, _current_handle(dev)),
                "nvfp4_layer_norm_backward")
-    dweight, dbias = dwb.unbind(0)
     return dx, dweight, dbias
 
 
@@ -779,12 +781,12 @@ def nvfp4_distill_topk(logits: torch.Tensor, indices: torch.Tensor, teacher: tor
     dev = logits.device
     tokens, vocab = logits.shape
     with _on(dev, stream):
-        res = torch.empty((2, tokens), dtype=torch.float32, device=dev)
+        loss = torch.empty(tokens, dtype=torch.float32, device=dev)
+        lse = torch.empty(tokens, dtype=torch.float32, device=dev)
         ws, need = _distill_workspace(tokens, vocab, dev)
-        p = res.data_ptr()
-        _check(lib().nvfp4_distill_topk(*args, p, p + 4 * tokens, ws.data_ptr(), need, _current_handle(dev)),
-               "nvfp4_distill_topk")
-    return res.unbind(0)
+        _check(lib().nvfp4_distill_topk(*args, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), need,
+                                        _current_handle(dev)), "nvfp4_distill_topk")
+    return loss, lse
 
 
 def nvfp4_distill_topk_backward(logits: torch.Tensor, indices: torch.Tensor, teacher: torch.Tensor,
@@ -817,11 +819,10 @@ def nvfp4_distill_topk_step(logits: torch.Tensor, indices: torch.Tensor, teacher
     with _on(dev, stream):
         dz = torch.empty((tokens, vocab), dtype=logits.dtype, device=dev) if out is None else out
         ldd = _require_matrix_out(dz, tokens, vocab, logits.dtype, dev) if out is not None else max(vocab, 1)
-        res = torch.empty((2, tokens), dtype=torch.float32, device=dev)
+        loss = torch.empty(tokens, dtype=torch.float32, device=dev)
+        lse = torch.empty(tokens, dtype=torch.float32, device=dev)
         ws, need = _distill_workspace(tokens, vocab, dev)
-        p = res.data_ptr()
-        _check(lib().nvfp4_distill_topk_step(*args, weight.data_ptr(), p, p + 4 * tokens, dz.data_ptr(), ldd,
-                                             ws.data_ptr(), need, _current_handle(dev)),
+        _check(lib().nvfp4_distill_topk_step(*args, weight.data_ptr(), loss.data_ptr(), lse.data_ptr(), dz.data_ptr(),
+                                             ldd, ws.data_ptr(), need, _current_handle(dev)),
                "nvfp4_distill_topk_step")
-    loss, lse = res.unbind(0)
     return loss, lse, dz

@@ -63,9 +63,10 @@ __device__ __forceinline__ float exp_sum8(const float *v, float m, float scale, 
 // A row's teacher list in LDS: the binary logarithm of p, and the index (-1
 // where invalid).  p itself is 2^lp where it is used: log p taken from p
 // would be -inf for the smallest shares.
+// z: the student's logits at the list.
 struct Teacher {
-  float lp[kMaxTop];
-  int32_t at[kMaxTop];
+  alignas(16) int32_t at[kMaxTop];
+  float lp[kMaxTop], z[kMaxTop];
   float share[2][kMaxWaves];
 };
 struct List {
@@ -92,12 +93,17 @@ struct Entry {
   }
 };
 // Returns whether any entry is valid; all threads see the list then.
-__device__ __forceinline__ bool load_teacher(Teacher &te, const List &l, Entry e, int64_t row, int64_t V, float scale,
-                                             int threads) {
+template <typename T>
+__device__ __forceinline__ bool load_teacher(Teacher &te, const List &l, Entry e, const T *zr, int64_t row, int64_t V,
+                                             float scale, int threads) {
   const int waves = threads >> 6;
   float m = -INFINITY;
   bool any = false;
-  for (int k = threadIdx.x; k < l.top; k += threads) {
+  for (int k = threadIdx.x; k < (l.top + 3) / 4 * 4; k += threads) {
+    if (k >= l.top) {                  // filled up to whole vectors of four
+      te.at[k] = -1;
+      continue;
+    }
     if (k != (int)threadIdx.x) {
       e.i = l.index(row, k);
       e.v = l.logit(row, k);
@@ -105,6 +111,7 @@ __device__ __forceinline__ bool load_teacher(Teacher &te, const List &l, Entry e
     const bool ok = e.i >= 0 && e.i < V && e.v != -INFINITY;
     te.at[k] = ok ? (int32_t)e.i : -1;
     te.lp[k] = e.v;
+    te.z[k] = ok ? to_float(zr[e.i]) : 0.0f;
     if (ok) m = fmaxf(m, e.v);
     any |= ok;
   }
@@ -124,15 +131,13 @@ __device__ __forceinline__ bool load_teacher(Teacher &te, const List &l, Entry e
   return some;
 }
 
-// The sum over the list of p (log2 p - log2 q); zr: the student's row.
-template <typename T>
-__device__ __forceinline__ float list_sum(const Teacher &te, const T *zr, int top, float top_z, float scale, float l2,
-                                          int threads) {
+// The sum over the list of p (log2 p - log2 q).
+__device__ __forceinline__ float list_sum(const Teacher &te, int top, float top_z, float scale, float l2, int threads) {
   float a = 0.0f;
   for (int k = threadIdx.x; k < top; k += threads) {
     const float p = __builtin_amdgcn_exp2f(te.lp[k]);
     if (te.at[k] < 0 || p == 0.0f) continue;      // 0 log 0 = 0
-    const float q = (to_float(zr[te.at[k]]) - top_z) * scale - l2;    // log2 of the student's share
+    const float q = (te.z[k] - top_z) * scale - l2;    // log2 of the student's share
     a = __builtin_fmaf(p, te.lp[k] - q, a);
   }
   return a;
@@ -142,16 +147,25 @@ __device__ __forceinline__ float list_sum(const Teacher &te, const T *zr, int to
 // student's share alone gave.  An index that is listed twice takes the sum
 // of its shares, in list order, so its writers store the same value.
 template <typename T>
-__device__ __forceinline__ void list_gradient(const Teacher &te, const T *zr, T *dr, int top, int64_t begin, int64_t end,
-                                              float c, float top_z, float scale, float l2, int threads) {
+__device__ __forceinline__ void list_gradient(const Teacher &te, T *dr, int top, int64_t begin, int64_t end, float c,
+                                              float top_z, float scale, float l2, int threads) {
   __syncthreads();
   for (int k = threadIdx.x; k < top; k += threads) {
     const int32_t i = te.at[k];
     if (i < begin || i >= end) continue;
-    float p = 0.0f;
+    int same = 0;
 #pragma unroll 4
-    for (int j = 0; j < top; ++j) p += te.at[j] == i ? __builtin_amdgcn_exp2f(te.lp[j]) : 0.0f;
-    store_one(dr + i, c * (share_of(to_float(zr[i]), top_z, scale, l2) - p));
+    for (int j = 0; j < (top + 3) / 4; ++j) {
+      const int4 a = *reinterpret_cast<const int4 *>(te.at + 4 * j);
+      same += (a.x == i) + (a.y == i) + (a.z == i) + (a.w == i);
+    }
+    float p = 0.0f;
+    if (same == 1) {
+      p = __builtin_amdgcn_exp2f(te.lp[k]);
+    } else {
+      for (int j = 0; j < top; ++j) p += te.at[j] == i ? __builtin_amdgcn_exp2f(te.lp[j]) : 0.0f;
+    }
+    store_one(dr + i, c * (share_of(te.z[k], top_z, scale, l2) - p));
   }
 }
 
@@ -170,7 +184,7 @@ struct Vectors {
 // A whole row in the registers of one workgroup: read once, written once.
 // Its vectors of 8 are dealt out VPT to a thread.  The list is fetched first
 // and worked on while the row arrives.
-template <typename T, int VPT>
+template <typename T, int VPT, bool GRAD>
 __global__ __launch_bounds__(kRowThreads) void k_distill_row(const T *z, int64_t ldz, int64_t V, List list, float tau,
                                                              const float *weight, float *loss, float *lse, T *dz,
                                                              int64_t lddz, int threads) {
@@ -187,7 +201,7 @@ __global__ __launch_bounds__(kRowThreads) void k_distill_row(const T *z, int64_t
 #pragma unroll
   for (int j = 0; j < VPT; ++j) q[j].load(zr + vec.at(j));
   __builtin_amdgcn_sched_barrier(0);
-  const bool some = load_teacher(te, list, first, row, V, scale, threads);
+  const bool some = load_teacher(te, list, first, zr, row, V, scale, threads);
   float m = -INFINITY;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
@@ -212,12 +226,13 @@ __global__ __launch_bounds__(kRowThreads) void k_distill_row(const T *z, int64_t
   }
   s = block_sum(s, part[1], waves);
   const float l2 = __builtin_amdgcn_logf(s);
-  float a = some ? list_sum(te, zr, list.top, m, scale, l2, threads) : 0.0f;
+  float a = some ? list_sum(te, list.top, m, scale, l2, threads) : 0.0f;
   a = block_sum(a, part[2], waves);
   if (threadIdx.x == 0) {
     loss[row] = some ? tau * tau * kLn2 * a : 0.0f;
     lse[row] = m / tau + l2 * kLn2;
   }
+  if (!GRAD) return;
   const float c = some ? weight[row] * tau : 0.0f;
   T *dr = dz + row * lddz;
   vec.anew();
@@ -235,7 +250,7 @@ __global__ __launch_bounds__(kRowThreads) void k_distill_row(const T *z, int64_t
     q[j].set(v);
     if (vec.dup(j) < 8) q[j].store(dr + vec.at(j));
   }
-  if (c != 0.0f) list_gradient(te, zr, dr, list.top, 0, V, c, m, scale, l2, threads);
+  if (c != 0.0f) list_gradient(te, dr, list.top, 0, V, c, m, scale, l2, threads);
 }
 
 // Without a gradient, for few rows, or for rows that registers do not hold:
@@ -313,7 +328,7 @@ __global__ __launch_bounds__(kDT) void k_distill_finish(const T *z, int64_t ldz,
   const int64_t row = blockIdx.y, seg = blockIdx.x;
   const float scale = kLog2e / tau;
   const T *zr = z + row * ldz;
-  const bool some = load_teacher(te, list, Entry(list, row), row, V, scale, kDT);
+  const bool some = load_teacher(te, list, Entry(list, row), zr, row, V, scale, kDT);
   float top_z, l2;
   if (part) {
     float2 st = part[row * segments];
@@ -321,7 +336,7 @@ __global__ __launch_bounds__(kDT) void k_distill_finish(const T *z, int64_t ldz,
     top_z = st.x;
     l2 = __builtin_amdgcn_logf(st.y);
     if (seg == 0) {
-      float a = some ? list_sum(te, zr, list.top, top_z, scale, l2, kDT) : 0.0f;
+      float a = some ? list_sum(te, list.top, top_z, scale, l2, kDT) : 0.0f;
       a = block_sum(a, sums, kDT / 64);
       if (threadIdx.x == 0) {
         loss[row] = some ? tau * tau * kLn2 * a : 0.0f;
@@ -366,7 +381,7 @@ __global__ __launch_bounds__(kDT) void k_distill_finish(const T *z, int64_t ldz,
       }
     }
   }
-  if (c != 0.0f) list_gradient(te, zr, dr, list.top, begin, end, c, top_z, scale, l2, kDT);
+  if (c != 0.0f) list_gradient(te, dr, list.top, begin, end, c, top_z, scale, l2, kDT);
 }
 
 struct Split {
@@ -385,30 +400,37 @@ Split split_for(int64_t T, int64_t V) {
   return {len, (int)((V + len - 1) / len)};
 }
 
-// Vectors per thread of the one-workgroup-a-row form (loss and gradient in
-// one pass); 0 where the segments' form is taken: rows that 1024 threads do not hold in 64 registers each (or
-// shorter than a vector), or too few to give every CU one.
-int row_vectors(int64_t rows, int64_t V, bool f32) {
+// Vectors per thread of the one-workgroup-a-row form; 0 where the segments'
+// form is taken: rows that 1024 threads do not hold in 64 registers each, or
+// shorter than a vector; and, of rows above 128 KB, a loss alone (777 x 50021
+// f32: 37 us in segments, 62 in rows) or too few for the CUs (100 x 131072
+// bf16 with the gradient: 28 us and 31; 200 rows: 44 and 39).
+int row_vectors(int64_t rows, int64_t V, int size, bool gradient) {
   const int64_t vectors = (V + 7) / 8;
-  if (V < 8 || rows < device_cus() * 3 / 4) return 0;
+  if (V < 8) return 0;
+  if (V * size > (128 << 10) && (!gradient || rows < device_cus() / 2)) return 0;
   if (vectors <= 4 * 256) return 4;
   if (vectors <= 8 * kRowThreads) return 8;
-  return vectors <= 16 * kRowThreads && !f32 ? 16 : 0;
+  return vectors <= 16 * kRowThreads && size == 2 ? 16 : 0;
 }
 
 template <typename T, int VPT>
 void rows_of(const T *z, int64_t rows, int64_t V, int64_t ldz, const List &list, float tau, const float *weight,
              float *loss, float *lse, T *dz, int64_t lddz, hipStream_t stream) {
   const int threads = (int)(((V + 7) / 8 + VPT - 1) / VPT + 63) / 64 * 64;
-  k_distill_row<T, VPT><<<(unsigned)rows, threads, 0, stream>>>(z, ldz, V, list, tau, weight, loss, lse, dz, lddz,
-                                                               threads);
+  if (dz)
+    k_distill_row<T, VPT, true><<<(unsigned)rows, threads, 0, stream>>>(z, ldz, V, list, tau, weight, loss, lse, dz,
+                                                                       lddz, threads);
+  else
+    k_distill_row<T, VPT, false><<<(unsigned)rows, threads, 0, stream>>>(z, ldz, V, list, tau, nullptr, loss, lse,
+                                                                        nullptr, 0, threads);
 }
 
 template <typename T>
 void run(const void *zv, int64_t rows, int64_t V, int64_t ldz, List list, float tau, const float *weight, float *loss,
          float *lse, void *dz, int64_t lddz, void *workspace, bool stats, hipStream_t stream) {
   const T *z = (const T *)zv;
-  const int vpt = stats && dz ? row_vectors(rows, V, sizeof(T) == 4) : 0;
+  const int vpt = stats ? row_vectors(rows, V, sizeof(T), dz != nullptr) : 0;
   if (vpt == 4) rows_of<T, 4>(z, rows, V, ldz, list, tau, weight, loss, lse, (T *)dz, lddz, stream);
   else if (vpt == 8) rows_of<T, 8>(z, rows, V, ldz, list, tau, weight, loss, lse, (T *)dz, lddz, stream);
   else if (vpt == 16)
