@@ -122,13 +122,30 @@ __device__ __forceinline__ void store_y(void *y, int y_bf16, int64_t at, float v
   else ((float *)y)[at] = v;
 }
 
+// Up to 4 consecutive outputs, positions at .. at + 3, none from `end` on.
+__device__ __forceinline__ void store_rows(void *y, int y_bf16, int64_t at, int64_t end, const f32x4_t &v) {
+  if (at + 4 <= end && y_bf16) {
+    *reinterpret_cast<u32x2_a2 *>((uint16_t *)y + at) = (u32x2_t){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+  } else if (at + 4 <= end) {
+    *reinterpret_cast<f32x4_a4 *>((float *)y + at) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (at + i < end) store_y(y, y_bf16, at + i, v[i]);
+  }
+}
+
 // ------------------------------------------------------ 2 to 16 tokens --
 
 constexpr int kStepK = 128;      // k of one MFMA step: 4 lanes a row, 32 each
 constexpr int kTokens = 16;      // tokens of a launch's y index
-// waves of a workgroup, at most (three slabs: their sums take 6 KB of LDS a wave)
+// Waves of a workgroup, at most, and those of them that multiply (three
+// slabs: their sums take 6 KB of LDS a wave).  From three waves on (or with
+// several slabs), one more adds up what the others leave: the additions'
+// latency would else stand between one tile's barrier and the next.
 constexpr int kTileWaves = 12;
-constexpr int max_waves(int slabs) { return slabs == 3 ? 8 : kTileWaves; }
+constexpr int max_waves(int slabs) { return slabs == 3 ? 8 : kTileWaves - 1; }
+bool has_helper(int waves, int slabs) { return waves > 2 || slabs > 1; }
 constexpr int kTurnBytes = 4096; // 16 columns x 128 k of bf16
 
 // The B operand's columns.  bf16: one column a token.  float32: three
@@ -172,27 +189,63 @@ __device__ __forceinline__ u32x4_t column8(const float *x, int64_t left, int par
 // in the loop, codes straight to the lanes that multiply them, a tile ahead.  A tile's scales are fetched by the whole workgroup in rows' runs
 // (a lane's own would be 2 bytes out of every line) and pass through LDS.
 // The waves' sums of a tile meet in LDS, too, behind the tile's one barrier,
-// and four waves, other ones each time, add and store them.  With more than
+// and an extra wave adds and stores them meanwhile.  With more than
 // one range of K (gridDim.z) the sums go to `partial` [z][token][n] instead.
 // SL: 16-column slabs; grid: (tile walkers, tokens / 16, ranges of K).
-template <bool MX, typename X, int SL, int SW>
+template <bool MX, typename X, int SL, int SW, bool HELPER>
 __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *codes, const uint8_t *scales,
                                                                  const float *meta, int64_t N, int64_t K, const X *x,
                                                                  int64_t tokens, int64_t ldx, void *y, int y_bf16,
-                                                                 int64_t ldy, float *partial, int long_walk) {
+                                                                 int64_t ldy, float *partial, int waves, int long_walk) {
   constexpr int kC = columns<X>();
   constexpr int kG = Scale<MX>::kPerByte;
   constexpr int kSB = SW * kStepK / kG;              // scale bytes of a slice's row
   constexpr int kPiece = kSB / 4;                    // of which a thread fetches a quarter
   extern __shared__ __align__(16) char lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int threads = __builtin_amdgcn_readfirstlane(blockDim.x), waves = threads >> 6;
   const int row = lane & 15, quarter = lane >> 4;
   const int64_t t0 = (int64_t)blockIdx.y * kTokens;
   const int live = (int)min(tokens - t0, (int64_t)kTokens);
   const int64_t kz = (int64_t)blockIdx.z * waves * (SW * kStepK);
   const int64_t k0 = kz + wave * (SW * kStepK);
   const int64_t tiles = (N + 15) / 16, step = gridDim.x;
+
+  constexpr int kSums = max_waves(SL) * SL * 64;                   // sums of one tile, waves that do not exist counted
+  f32x4_t *const part = reinterpret_cast<f32x4_t *>(lds);          // [2][waves][SL][64]
+  const float g = MX ? 1.0f : meta[1];
+  // adds the waves' sums of a tile, a lane 4 weight rows of a token, and
+  // stores them; they are read four waves' at a time (those of waves that do
+  // not exist are left out)
+  const auto finish = [&](int64_t tile, int turn) {
+    if (row >= live) return;
+    f32x4_t sum = {0, 0, 0, 0};
+#pragma unroll
+    for (int p = 0; p < kC; ++p) {
+      const int col = row * kC + p;
+      const f32x4_t *f = part + (turn & 1) * kSums + (col >> 4) * 64 + quarter * 16 + (col & 15);
+      for (int w0 = 0; w0 < waves; w0 += 4) {
+        f32x4_t v[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) v[w] = f[(w0 + w) * SL * 64];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) sum += w0 + w < waves ? v[w] : (f32x4_t){0, 0, 0, 0};
+      }
+    }
+    const int64_t n = 16 * tile + 4 * quarter;
+    if (partial) store_rows(partial + ((int64_t)blockIdx.z * tokens + t0 + row) * N, 0, n, N, sum);
+    else store_rows(y, y_bf16, (t0 + row) * ldy + n, (t0 + row) * ldy + N, sum * g);
+  };
+  if (HELPER && wave == waves) {
+    // the extra wave only finishes tiles, while the others are at the next one
+    __syncthreads();
+    __syncthreads();
+    int turn = 0;
+    for (int64_t t = blockIdx.x; t < tiles; t += step, ++turn) {
+      __syncthreads();
+      finish(t, turn);
+    }
+    return;
+  }
 
   // codes of one tile
   uint32_t k[SW];
@@ -333,8 +386,6 @@ __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *
   }
   __syncthreads();
 
-  constexpr int kSums = max_waves(SL) * SL * 64;                   // sums of one tile, waves that do not exist counted
-  f32x4_t *const part = reinterpret_cast<f32x4_t *>(lds);          // [2][waves][SL][64]
   char *const scale_lds = lds + 2 * kSums * sizeof(f32x4_t);       // [2][16][stride]
   const auto put_scales = [&](uint64_t v, int turn) {
     v = (v >> shift) & keep;
@@ -343,8 +394,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *
   put_scales(sc_first, 0);
   __syncthreads();
 
-  const float g = MX ? 1.0f : meta[1];
-  int from = 0;
+  int adder = 0;
   const auto work = [&](const u32x4_t *c, int64_t tile, int turn) {
     constexpr int kA = SL == 1 ? 2 : 1;       // one slab: two accumulators, so that MFMAs do not wait for each other
     f32x4_t acc[kA][SL];
@@ -395,36 +445,10 @@ __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *
     }
     put_scales(sc_next, turn + 1);
     __syncthreads();
-    // 256 outputs, 16 consecutive rows of a token together, dealt to four
-    // waves, other ones each time; the sums are read four waves' at a time
-    constexpr int kBatch = 4;
-    int o = (int)threadIdx.x - from;
-    if (o < 0) o += threads;
-    for (; o < 256; o += threads) {
-      const int i = o & 15, token = o >> 4;
-      const int64_t n = 16 * tile + i;
-      if (token >= live || n >= N) continue;
-      const float *f = reinterpret_cast<const float *>(mine) + (i >> 2) * 64 + (i & 3);
-      float sum = 0.0f;
-      for (int w0 = 0; w0 < waves; w0 += kBatch) {
-        float v[kBatch][kC];
-#pragma unroll
-        for (int p = 0; p < kC; ++p) {
-          const int col = token * kC + p;
-          const float *fc = f + w0 * SL * 256 + (col >> 4) * 256 + (col & 15) * 4;
-#pragma unroll
-          for (int w = 0; w < kBatch; ++w) v[w][p] = fc[w * SL * 256];
-        }
-#pragma unroll
-        for (int w = 0; w < kBatch; ++w)
-#pragma unroll
-          for (int p = 0; p < kC; ++p) sum += w0 + w < waves ? v[w][p] : 0.0f;
-      }
-      if (partial) partial[((int64_t)blockIdx.z * tokens + t0 + token) * N + n] = sum;
-      else store_y(y, y_bf16, (t0 + token) * ldy + n, sum * g);
+    if (!HELPER) {
+      if (wave == adder) finish(tile, turn);
+      adder = adder + 1 < waves ? adder + 1 : 0;
     }
-    from += 256;
-    while (from >= threads) from -= threads;
   };
 
   // one turn: the loads of a later tile, then this tile
@@ -634,7 +658,7 @@ Cut cut_for(int64_t N, int64_t K, int64_t tokens, bool f32) {
   }
   // one round of workgroups: as many as fit the CUs' waves, the tiles dealt evenly
   const int64_t tiles = (N + 15) / 16, blocks = (tokens + kTokens - 1) / kTokens;
-  const int64_t room = (int64_t)device_cus() * (kTileWaves / c.waves);
+  const int64_t room = (int64_t)device_cus() * (kTileWaves / (c.waves + has_helper(c.waves, c.sl)));
   const int64_t want = std::min(tiles, std::max<int64_t>(1, room / (c.ranges * blocks)));
   const int64_t per = (tiles + want - 1) / want;
   c.walkers = (int)((tiles + per - 1) / per);
@@ -652,8 +676,12 @@ void tile(const Cut &c, const uint8_t *codes, const uint8_t *scales, const float
   const size_t lds =
       std::max<size_t>(c.waves * kTurnBytes, 2 * max_waves(SL) * SL * 64 * sizeof(f32x4_t) + 32 * (run + 4));
   float *partial = c.ranges > 1 ? (float *)workspace : nullptr;
-  k_matvec_tile<MX, X, SL, SW><<<grid, 64 * c.waves, lds, stream>>>(codes, scales, meta, N, K, x, tokens, ldx, y,
-                                                                    y_bf16, ldy, partial, c.long_walk);
+  const auto launch = [&](auto kernel, int waves) {
+    kernel<<<grid, 64 * waves, lds, stream>>>(codes, scales, meta, N, K, x, tokens, ldx, y, y_bf16, ldy, partial,
+                                              c.waves, c.long_walk);
+  };
+  if (has_helper(c.waves, SL)) launch(k_matvec_tile<MX, X, SL, SW, true>, c.waves + 1);
+  else if constexpr (SL == 1) launch(k_matvec_tile<MX, X, SL, SW, false>, c.waves);
   if (partial)
     k_matvec_join<<<(unsigned)std::min(kFlatGrid, (N * tokens + 255) / 256), 256, 0, stream>>>(
         partial, c.ranges, MX ? nullptr : meta, N, tokens, y, y_bf16, ldy);
