@@ -156,6 +156,15 @@ def _require_buffer(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int, 
         raise NVFP4Error(f"{name} must be contiguous with at least {numel} elements")
 
 
+def _vector(t, name: str, dtype: torch.dtype, numel: int, device: torch.device) -> int:
+    """The address of a device vector that the kernels read whole
+    (_require_buffer says what is wrong with one that they cannot)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.numel() >= numel
+            and t.device == device and t.is_contiguous()):
+        _require_buffer(t, name, dtype, numel, device)
+    return t.data_ptr()
+
+
 def _out_code(dtype) -> int:
     if dtype == torch.float32:
         return F32
@@ -205,10 +214,9 @@ class NVFP4Tensor:
         if self.outer < 0 or self.k < 0 or self.k % 16:
             raise NVFP4Error(f"invalid NVFP4 shape ({self.outer}, {self.k})")
         dev = self.codes.device
-        _require_buffer(self.codes, "codes", torch.uint8, self.outer * (self.k // 2), dev)
-        _require_buffer(self.scales, "scales", torch.uint8, self.outer * (self.k // 16), dev)
-        _require_buffer(self.meta, "meta", torch.float32, 2, dev)
-        return _CTensor(self.codes.data_ptr(), self.scales.data_ptr(), self.meta.data_ptr(), self.outer, self.k)
+        return _CTensor(_vector(self.codes, "codes", torch.uint8, self.outer * (self.k // 2), dev),
+                        _vector(self.scales, "scales", torch.uint8, self.outer * (self.k // 16), dev),
+                        _vector(self.meta, "meta", torch.float32, 2, dev), self.outer, self.k)
 
     @property
     def shape(self):
@@ -476,9 +484,9 @@ class MXFP4Tensor:
         if self.outer < 0 or self.k < 0 or self.k % 32:
             raise NVFP4Error(f"invalid MXFP4 shape ({self.outer}, {self.k})")
         dev = self.codes.device
-        _require_buffer(self.codes, "codes", torch.uint8, self.outer * (self.k // 2), dev)
-        _require_buffer(self.scales, "scales", torch.uint8, self.outer * (self.k // 32), dev)
-        return _MXTensor(self.codes.data_ptr(), self.scales.data_ptr(), self.outer, self.k)
+        return _MXTensor(_vector(self.codes, "codes", torch.uint8, self.outer * (self.k // 2), dev),
+                         _vector(self.scales, "scales", torch.uint8, self.outer * (self.k // 32), dev), self.outer,
+                         self.k)
 
 
 def mxfp4_quantize(x: torch.Tensor, axis: int = 1, out: MXFP4Tensor | None = None, stream=None) -> MXFP4Tensor:
@@ -625,11 +633,7 @@ def _param(t, name: str, cols: int, device: torch.device):
         return None, F32
     if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.shape[0] != cols:
         raise NVFP4Error(f"{name} must be a vector of {cols} elements")
-    if t.device != device:
-        raise NVFP4Error(f"{name} must be a GPU tensor on {device}")
-    if not t.is_contiguous():
-        raise NVFP4Error(f"{name} must be contiguous")
-    return t.data_ptr(), _dtype_code(t)
+    return _vector(t, name, t.dtype, cols, device), _dtype_code(t)
 
 
 def _ptr(t):
@@ -688,20 +692,20 @@ def nvfp4_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Ten
     dev = x.device
     rows, cols = x.shape
     lddy = _require_matrix(dy, "dy", dev, (rows, cols))
-    _require_buffer(mean, "mean", torch.float32, rows, dev)
-    _require_buffer(rstd, "rstd", torch.float32, rows, dev)
+    mp = _vector(mean, "mean", torch.float32, rows, dev)
+    rp = _vector(rstd, "rstd", torch.float32, rows, dev)
     wp, wcode = _param(weight, "weight", cols, dev)
     gcode = _out_code(grad_dtype)
-    need = int(lib().nvfp4_layer_norm_backward_workspace_bytes(rows, cols))
+    need = lib().nvfp4_layer_norm_backward_workspace_bytes(rows, cols)
     if need < 0:
         _check(need, "nvfp4_layer_norm_backward")
     with _on(dev, stream):
-        dx = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+        dx = x.new_empty((rows, cols))
         dweight = torch.empty(cols, dtype=grad_dtype, device=dev)
         dbias = torch.empty(cols, dtype=grad_dtype, device=dev)
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
         _check(lib().nvfp4_layer_norm_backward(dy.data_ptr(), _dtype_code(dy), lddy, x.data_ptr(), _dtype_code(x),
-                                               rows, cols, ldx, mean.data_ptr(), rstd.data_ptr(), wp, wcode,
+                                               rows, cols, ldx, mp, rp, wp, wcode,
                                                dx.data_ptr(), cols, dweight.data_ptr(), dbias.data_ptr(), gcode,
                                                ws.data_ptr(), need, _current_handle(dev)),
                "nvfp4_layer_norm_backward")
@@ -719,7 +723,7 @@ def _matvec(fn, what, w, x, out_dtype, out, stream):
     out_dtype = x.dtype if out_dtype is None else out_dtype
     code = _out_code(out_dtype)
     cw, xcode = w._c(), _dtype_code(x)
-    need = int(lib().nvfp4_matvec_workspace_bytes(w.outer, k, tokens, xcode))
+    need = lib().nvfp4_matvec_workspace_bytes(w.outer, k, tokens, xcode)
     if need < 0:
         _check(need, what)
     with _on(dev, stream):
@@ -758,18 +762,20 @@ def _distill_args(logits, indices, teacher, temperature):
     if not isinstance(teacher, torch.Tensor) or teacher.shape != indices.shape:
         raise NVFP4Error("teacher must be a tensor of indices' shape")
     top = indices.shape[1]
-    _require_buffer(indices, "indices", indices.dtype, tokens * top, dev)
-    _require_buffer(teacher, "teacher", teacher.dtype, tokens * top, dev)
-    return (logits.data_ptr(), _dtype_code(logits), tokens, vocab, ldz, indices.data_ptr(),
-            32 if indices.dtype == torch.int32 else 64, teacher.data_ptr(), _dtype_code(teacher), top,
-            float(temperature))
+    return (logits.data_ptr(), _dtype_code(logits), tokens, vocab, ldz,
+            _vector(indices, "indices", indices.dtype, tokens * top, dev), 32 if indices.dtype is torch.int32 else 64,
+            _vector(teacher, "teacher", teacher.dtype, tokens * top, dev), _dtype_code(teacher), top, temperature)
 
 
 def _distill_workspace(tokens: int, vocab: int, device):
-    need = int(lib().nvfp4_distill_topk_workspace_bytes(tokens, vocab))
+    """(tensor or None, address or None, size) of the scratch memory."""
+    need = lib().nvfp4_distill_topk_workspace_bytes(tokens, vocab)
     if need < 0:
         _check(need, "nvfp4_distill_topk")
-    return torch.empty(need, dtype=torch.uint8, device=device), need
+    if need == 0:
+        return None, None, 0
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), need
 
 
 def nvfp4_distill_topk(logits: torch.Tensor, indices: torch.Tensor, teacher: torch.Tensor,
@@ -783,8 +789,8 @@ def nvfp4_distill_topk(logits: torch.Tensor, indices: torch.Tensor, teacher: tor
     with _on(dev, stream):
         loss = torch.empty(tokens, dtype=torch.float32, device=dev)
         lse = torch.empty(tokens, dtype=torch.float32, device=dev)
-        ws, need = _distill_workspace(tokens, vocab, dev)
-        _check(lib().nvfp4_distill_topk(*args, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), need,
+        ws, wsp, need = _distill_workspace(tokens, vocab, dev)
+        _check(lib().nvfp4_distill_topk(*args, loss.data_ptr(), lse.data_ptr(), wsp, need,
                                         _current_handle(dev)), "nvfp4_distill_topk")
     return loss, lse
 
@@ -797,12 +803,12 @@ def nvfp4_distill_topk_backward(logits: torch.Tensor, indices: torch.Tensor, tea
     args = _distill_args(logits, indices, teacher, temperature)
     dev = logits.device
     tokens, vocab = logits.shape
-    _require_buffer(lse, "lse", torch.float32, tokens, dev)
-    _require_buffer(dloss, "dloss", torch.float32, tokens, dev)
+    lp = _vector(lse, "lse", torch.float32, tokens, dev)
+    gp = _vector(dloss, "dloss", torch.float32, tokens, dev)
     with _on(dev, stream):
-        dz = torch.empty((tokens, vocab), dtype=logits.dtype, device=dev) if out is None else out
+        dz = logits.new_empty((tokens, vocab)) if out is None else out
         ldd = _require_matrix_out(dz, tokens, vocab, logits.dtype, dev) if out is not None else max(vocab, 1)
-        _check(lib().nvfp4_distill_topk_backward(*args, lse.data_ptr(), dloss.data_ptr(), dz.data_ptr(), ldd,
+        _check(lib().nvfp4_distill_topk_backward(*args, lp, gp, dz.data_ptr(), ldd,
                                                  _current_handle(dev)), "nvfp4_distill_topk_backward")
     return dz
 
@@ -815,14 +821,14 @@ def nvfp4_distill_topk_step(logits: torch.Tensor, indices: torch.Tensor, teacher
     args = _distill_args(logits, indices, teacher, temperature)
     dev = logits.device
     tokens, vocab = logits.shape
-    _require_buffer(weight, "weight", torch.float32, tokens, dev)
+    gp = _vector(weight, "weight", torch.float32, tokens, dev)
     with _on(dev, stream):
-        dz = torch.empty((tokens, vocab), dtype=logits.dtype, device=dev) if out is None else out
+        dz = logits.new_empty((tokens, vocab)) if out is None else out
         ldd = _require_matrix_out(dz, tokens, vocab, logits.dtype, dev) if out is not None else max(vocab, 1)
         loss = torch.empty(tokens, dtype=torch.float32, device=dev)
         lse = torch.empty(tokens, dtype=torch.float32, device=dev)
-        ws, need = _distill_workspace(tokens, vocab, dev)
-        _check(lib().nvfp4_distill_topk_step(*args, weight.data_ptr(), loss.data_ptr(), lse.data_ptr(), dz.data_ptr(),
-                                             ldd, ws.data_ptr(), need, _current_handle(dev)),
+        ws, wsp, need = _distill_workspace(tokens, vocab, dev)
+        _check(lib().nvfp4_distill_topk_step(*args, gp, loss.data_ptr(), lse.data_ptr(), dz.data_ptr(),
+                                             ldd, wsp, need, _current_handle(dev)),
                "nvfp4_distill_topk_step")
     return loss, lse, dz

@@ -462,7 +462,10 @@ void run(const void *zv, int64_t rows, int64_t V, int64_t ldz, List list, float 
 
 int distill_max_top() { return kMaxTop; }
 
-int64_t distill_workspace_bytes(int64_t rows, int64_t V) { return 8 * rows * split_for(rows, V).segments; }
+int64_t distill_workspace_bytes(int64_t rows, int64_t V) {
+  // none where every type's rows go whole through one workgroup
+  return row_vectors(rows, V, 4, false) ? 0 : 8 * rows * split_for(rows, V).segments;
+}
 
 hipError_t launch_distill(const void *z, int z_dtype, int64_t rows, int64_t V, int64_t ldz, const void *idx, int idx64,
                           const void *t, int t_dtype, int top, float tau, const float *weight, float *loss, float *lse,

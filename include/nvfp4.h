@@ -459,7 +459,8 @@ int64_t nvfp4_matvec_workspace_bytes(int64_t n, int64_t k, int64_t tokens, int x
  *  loss, lse   : device, f32 [tokens].
  *  workspace   : device, nvfp4_distill_topk_workspace_bytes(tokens, vocab)
  *                bytes, 16-byte aligned, contents ignored and overwritten;
- *                calls that share one must not overlap in time.
+ *                0 for short rows, and NULL will do then.  Calls that share
+ *                one must not overlap in time.
  * A row without a valid entry has loss 0 and gradient 0 whatever its logits.
  * An index listed twice counts twice.  Logits of -infinity or of the type's
  * lowest value are ordinary (a vocabulary mask).

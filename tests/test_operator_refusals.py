@@ -123,8 +123,10 @@ def test_distill_shared(L, bad, status):
 @_no_gpu
 def test_distill_own_arguments(L):
     assert _call(L.nvfp4_distill_topk, FORWARD, loss=None) == NULL
-    assert _call(L.nvfp4_distill_topk, FORWARD, ws=None) == NULL
-    assert _call(L.nvfp4_distill_topk, FORWARD, bytes=0) == SHAPE
+    long = dict(vocab=1 << 20, ldz=1 << 20)            # rows that need a workspace
+    assert L.nvfp4_distill_topk_workspace_bytes(4, 100) == 0 < L.nvfp4_distill_topk_workspace_bytes(4, 1 << 20)
+    assert _call(L.nvfp4_distill_topk, FORWARD, **long, ws=None) == NULL
+    assert _call(L.nvfp4_distill_topk, FORWARD, **long, bytes=0) == SHAPE
     assert _call(L.nvfp4_distill_topk, FORWARD, ws=FAKE + 8) == ALIGN
     assert _call(L.nvfp4_distill_topk_backward, BACKWARD, dloss=None) == NULL
     assert _call(L.nvfp4_distill_topk_backward, BACKWARD, dz=None) == NULL
@@ -134,7 +136,7 @@ def test_distill_own_arguments(L):
     assert _call(L.nvfp4_distill_topk_step, STEP, weight=None) == NULL
     assert _call(L.nvfp4_distill_topk_step, STEP, loss=None) == NULL
     assert _call(L.nvfp4_distill_topk_step, STEP, dz=FAKE + 100) == SHAPE
-    assert _call(L.nvfp4_distill_topk_step, STEP, bytes=0) == SHAPE
+    assert _call(L.nvfp4_distill_topk_step, STEP, **{**long, "lddz": 1 << 20, "dz": 1 << 30}, bytes=0) == SHAPE
     assert _call(L.nvfp4_distill_topk_step, STEP, dz=2 * FAKE + 1) == ALIGN
 
 
