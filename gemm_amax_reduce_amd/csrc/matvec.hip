@@ -9,13 +9,14 @@
 // forms, both with 32 consecutive k of one weight row per lane and load (16
 // bytes of codes, whole scale groups):
 //
-//  * k_matvec_row, one token: a wave walks whole weight rows (contiguous
+//  * k_matvec_row, up to 4 tokens: a wave walks whole weight rows (contiguous
 //    runs of 1 KB per load), its share of x stays in registers, and a pair
 //    of products is one v_dot2_f32_bf16 on decoded codes; the block scale is
-//    applied to a block's sum.  About one instruction per weight.
+//    applied to a block's sum.  Half an instruction per weight and half a
+//    one per product.
 //  * k_matvec_tile, more tokens: tiles of 16 weight rows on the 16x16x32
 //    bf16 MFMA with the weights as the A operand and up to 16 tokens as the
-//    B operand, so 2 to 16 tokens cost the same.  A lane's 32 k enter four
+//    B operand, so 1 to 16 tokens cost the same.  A lane's 32 k enter four
 //    MFMAs; the k order of an MFMA is free as long as both operands agree.
 //    The block scale has to be multiplied into every weight here, about two
 //    instructions per NVFP4 weight.
@@ -32,6 +33,7 @@
 #include "row_common.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace nvfp4 {
 
@@ -135,7 +137,7 @@ __device__ __forceinline__ void store_rows(void *y, int y_bf16, int64_t at, int6
   }
 }
 
-// ------------------------------------------------------ 2 to 16 tokens --
+// ---------------------------------------------------- up to 16 tokens --
 
 constexpr int kStepK = 128;      // k of one MFMA step: 4 lanes a row, 32 each
 constexpr int kTokens = 16;      // tokens of a launch's y index
@@ -506,7 +508,7 @@ __global__ __launch_bounds__(256) void k_matvec_short(const uint8_t *codes, cons
 }
 constexpr int64_t kFlatGrid = 1 << 16;
 
-// ------------------------------------------------------------ one token --
+// ----------------------------------------------------- up to 4 tokens --
 
 // A lane's products with 32 weights of one row: sum x q s.
 template <bool MX> __device__ __forceinline__ float dot32(const u32x4_t &c, const Scale<MX> &s, const Act<uint16_t> &x) {
@@ -540,53 +542,93 @@ template <bool MX> __device__ __forceinline__ float dot32(const u32x4_t &c, cons
   return MX ? (p[0] + p[1]) * s.lo() : __builtin_fmaf(p[0], s.lo(), p[1] * s.hi());
 }
 
-constexpr int kRowWaves = 4;
 constexpr int kWaveK = 64 * 32;         // k of one wave load
 
-// One weight row's share of a wave: J loads.
-template <bool MX, int J> struct RowPart {
-  u32x4_t c[J];
-  Scale<MX> s[J];
-  __device__ __forceinline__ void load(const uint8_t *cr, const uint8_t *sr, const uint32_t *k) {
+// C sums over the wave at once.  A swap of halves (then of odd and even rows
+// of 16 lanes) between two values and one addition fold both of them into
+// one register, each in its own lanes; what is left takes four additions
+// with rotated lanes.  On return value i is v[i % slots] in the lanes of row
+// (of 16) i / slots, for C >= 4; for C = 2 in the rows 0-1 and 2-3, for C = 1
+// in all.
+template <int C> constexpr int sum_slots() { return C >= 4 ? C / 4 : 1; }
+template <int C> __device__ __forceinline__ int sum_row(int i) { return C >= 4 ? i / (C / 4) : 2 * i; }
+template <int C> __device__ __forceinline__ void wave_sums(float *v) {
+  static_assert(C == 1 || C == 2 || C % 4 == 0, "sums come in fours");
+  constexpr int kHalf = C > 1 ? C / 2 : 1, kSlots = sum_slots<C>();
+  // the pair of a register: another value, or itself where one is left
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      c[j] = *reinterpret_cast<const u32x4_a8 *>(cr + k[j] / 2);
-      s[j].load(sr + k[j] / Scale<MX>::kPerByte);
+  for (int i = 0; i < kHalf; ++i) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_int(v[i]), __float_as_int(v[C > 1 ? i + kHalf : i]),
+                                                    false, false);
+    v[i] = __int_as_float(p[0]) + __int_as_float(p[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_int(v[i]), __float_as_int(v[C >= 4 ? i + kSlots : i]),
+                                                    false, false);
+    v[i] = __int_as_float(p[0]) + __int_as_float(p[1]);
+    v[i] += dpp<0xB1>(v[i]);
+    v[i] += dpp<0x4E>(v[i]);
+    v[i] += dpp<0x141>(v[i]);
+    v[i] += dpp<0x140>(v[i]);
+  }
+}
+
+// R weight rows' share of a wave: J loads each.
+template <bool MX, int J, int R> struct RowPart {
+  u32x4_t c[R][J];
+  Scale<MX> s[R][J];
+  __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales, int64_t n, int64_t N, int64_t K,
+                                       const uint32_t *k) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = min(n + r, N - 1);          // past the end: the last one again, not stored
+      const uint8_t *cr = codes + row * (K / 2), *sr = scales + row * (K / Scale<MX>::kPerByte);
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        c[r][j] = *reinterpret_cast<const u32x4_a8 *>(cr + k[j] / 2);
+        s[r][j].load(sr + k[j] / Scale<MX>::kPerByte);
+      }
     }
   }
 };
 
-// The workgroup's four waves hold J loads of x each: WK waves share a row
-// (K <= WK * J * 2048), 4 / WK rows are worked on at a time.
-template <bool MX, typename X, int J, int WK>
-__global__ __launch_bounds__(64 * kRowWaves) void k_matvec_row(const uint8_t *codes, const uint8_t *scales,
-                                                               const float *meta, int64_t N, int64_t K, const X *x,
-                                                               void *y, int y_bf16) {
-  constexpr int kRows = kRowWaves / WK;
+// The workgroup's waves hold J loads of each token's x: WK waves share a row
+// (K <= WK * J * 2048), the others work on rows of their own, R at a time
+// (so that every wave has some 3 KB in flight, twice).
+constexpr int row_waves(int wk) { return wk == 3 ? 3 : 4; }
+template <bool MX, typename X, int J, int WK, int R, int T>
+__global__ __launch_bounds__(64 * row_waves(WK), T <= 2 ? 3 : 2) void k_matvec_row(const uint8_t *codes, const uint8_t *scales,
+                                                                   const float *meta, int64_t N, int64_t K,
+                                                                   const X *x, int64_t ldx, void *y, int y_bf16,
+                                                                   int64_t ldy) {
+  constexpr int kWaves = row_waves(WK), kThreads = 64 * kWaves, kRows = kWaves / WK * R, kC = R * T;
   // x through LDS: a lane's 32 k would be a load of 64 lines of memory.  Each
-  // of J rounds takes the waves' j-th loads; unit u (16 bytes) lies at slot u
-  // with its lowest bits turned by the next ones, so that 16 lanes' reads of
-  // one piece each fall on all banks.
+  // of J T rounds takes the waves' j-th loads of one token; unit u (16 bytes)
+  // lies at slot u with its lowest bits turned by the next ones, so that 16
+  // lanes' reads of one piece each fall on all banks.
   constexpr int kUnit = 16 / sizeof(X), kPieces = Act<X>::kPieces;
-  constexpr int kWaveUnits = kWaveK / kUnit, kLoads = WK * kWaveUnits / (64 * kRowWaves);
+  constexpr int kWaveUnits = kWaveK / kUnit, kLoads = WK * kWaveUnits / kThreads;
   __shared__ u32x4_t turned[WK * kWaveUnits];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = wave % WK;
   const auto slot = [](uint32_t u) { return u ^ ((u >> 4) & (kPieces - 1)); };
-  u32x4_t raw[J][kLoads];
+  u32x4_t raw[T][J][kLoads];
 #pragma unroll
-  for (int j = 0; j < J; ++j)
+  for (int t = 0; t < T; ++t)
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int u = threadIdx.x + i * 64 * kRowWaves;
-      const int64_t at = (int64_t)(u / kWaveUnits * J + j) * kWaveK + u % kWaveUnits * kUnit;
-      raw[j][i] = (u32x4_t){0, 0, 0, 0};
-      if (at < K) raw[j][i] = *reinterpret_cast<const u32x4_a2 *>(x + at);
-    }
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int u = threadIdx.x + i * kThreads;
+        const int64_t at = (int64_t)(u / kWaveUnits * J + j) * kWaveK + u % kWaveUnits * kUnit;
+        const u32x4_t v = *reinterpret_cast<const u32x4_a2 *>(x + t * ldx + (at < K ? at : 0));
+        raw[t][j][i] = at < K ? v : (u32x4_t){0, 0, 0, 0};
+      }
   const float g = MX ? 1.0f : meta[1];
   const int64_t stride = (int64_t)gridDim.x * kRows;
-  const int64_t first = (int64_t)blockIdx.x * kRows + wave / WK;
-  __shared__ float share[2][kRowWaves];
+  const int64_t mine = wave / WK * R, first = (int64_t)blockIdx.x * kRows + mine;
+  __shared__ float share[2][kWaves][kC];
   uint32_t k[J];
   int half = 0;                                      // loads (as bits) that were moved back by 16
 #pragma unroll
@@ -595,43 +637,60 @@ __global__ __launch_bounds__(64 * kRowWaves) void k_matvec_row(const uint8_t *co
     half |= (last_window(at, K) == 16) << j;
     k[j] = (uint32_t)at;
   }
-  Act<X> xv[J];
-  RowPart<MX, J> a, b;
-  const auto load = [&](RowPart<MX, J> &p, int64_t n) {
-    n = min(n, N - 1);
-    p.load(codes + n * (K / 2), scales + n * (K / Scale<MX>::kPerByte), k);
-  };
-  const auto finish = [&](const RowPart<MX, J> &p, int64_t n, int turn) {
-    float sum = 0.0f;
+  Act<X> xv[T][J];
+  RowPart<MX, J, R> a, b;
+  const auto finish = [&](const RowPart<MX, J, R> &p, int64_t n, int turn) {
+    // sum i = (row i / T of the R, token i % T)
+    float v[kC];
 #pragma unroll
-    for (int j = 0; j < J; ++j) sum += dot32<MX>(p.c[j], p.s[j], xv[j]);
-    sum = wave_sum(sum);
-    if (WK > 1) {
-      if (lane == 0) share[turn][wave] = sum;
-      __syncthreads();
-      sum = 0.0f;
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int w = 0; w < WK; ++w) sum += share[turn][wave - kw + w];
+      for (int t = 0; t < T; ++t) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) sum += dot32<MX>(p.c[r][j], p.s[r][j], xv[t][j]);
+        v[r * T + t] = sum;
+      }
+    wave_sums<kC>(v);
+    const auto store = [&](int i, float sum) {
+      if (n + i / T < N) store_y(y, y_bf16, i % T * ldy + n + i / T, sum * g);
+    };
+    if (WK == 1) {
+#pragma unroll
+      for (int i = 0; i < kC; ++i)
+        if (lane == 16 * sum_row<kC>(i)) store(i, v[i % sum_slots<kC>()]);
+      return;
     }
-    if (lane == 0 && kw == 0 && n < N) store_y(y, y_bf16, n, sum * g);
-  };
-  load(a, first);
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    if (j) __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) turned[slot(threadIdx.x + i * 64 * kRowWaves)] = raw[j][i];
+    for (int i = 0; i < kC; ++i)
+      if (lane == 16 * sum_row<kC>(i)) share[turn][wave][i] = v[i % sum_slots<kC>()];
     __syncthreads();
-    // (moved back by 16: its x are the load's first half, zeros before them)
-    const int swap = ((half >> j) & 1) * (kPieces / 2);
+    if (kw == 0 && lane < kC) {
+      float sum = 0.0f;
 #pragma unroll
-    for (int p = 0; p < kPieces; ++p) xv[j].v[p] = turned[slot(kw * kWaveUnits + lane * kPieces + (p ^ swap))];
-  }
+      for (int w = 0; w < WK; ++w) sum += share[turn][wave + w][lane];
+      store(lane, sum);
+    }
+  };
+  a.load(codes, scales, first, N, K, k);
+#pragma unroll
+  for (int t = 0; t < T; ++t)
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      if (t + j) __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) turned[slot(threadIdx.x + i * kThreads)] = raw[t][j][i];
+      __syncthreads();
+      // (moved back by 16: its x are the load's first half, zeros before them)
+      const int swap = ((half >> j) & 1) * (kPieces / 2);
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) xv[t][j].v[p] = turned[slot(kw * kWaveUnits + lane * kPieces + (p ^ swap))];
+    }
   // the workgroup's waves make the same number of turns (barriers)
-  for (int64_t n = first; n - wave / WK < N; n += 2 * stride) {
-    load(b, n + stride);
+  for (int64_t n = first; n - mine < N; n += 2 * stride) {
+    b.load(codes, scales, n + stride, N, K, k);
     finish(a, n, 0);
-    load(a, n + 2 * stride);
+    a.load(codes, scales, n + 2 * stride, N, K, k);
     finish(b, n + stride, 1);
   }
 }
@@ -668,65 +727,102 @@ Cut cut_for(int64_t N, int64_t K, int64_t tokens, bool f32) {
   return c;
 }
 
-template <bool MX, typename X, int SL, int SW>
-void tile(const Cut &c, const uint8_t *codes, const uint8_t *scales, const float *meta, int64_t N, int64_t K, const X *x,
-          int64_t tokens, int64_t ldx, void *y, int y_bf16, int64_t ldy, void *workspace, hipStream_t stream) {
-  const dim3 grid((unsigned)c.walkers, (unsigned)((tokens + kTokens - 1) / kTokens), (unsigned)c.ranges);
+// What every launch of a product passes on.
+template <typename X> struct Product {
+  const uint8_t *codes, *scales;
+  const float *meta;
+  int64_t N, K;
+  const X *x;
+  int64_t tokens, ldx;
+  void *y;
+  int y_bf16;
+  int64_t ldy;
+  void *ws;
+  hipStream_t stream;
+};
+
+template <bool MX, int SL, int SW, typename X> void tile(const Cut &c, const Product<X> &p) {
+  const dim3 grid((unsigned)c.walkers, (unsigned)((p.tokens + kTokens - 1) / kTokens), (unsigned)c.ranges);
   const size_t run = c.waves * SW * kStepK / Scale<MX>::kPerByte;       // scale bytes of a row
   const size_t lds =
       std::max<size_t>(c.waves * kTurnBytes, 2 * max_waves(SL) * SL * 64 * sizeof(f32x4_t) + 32 * (run + 4));
-  float *partial = c.ranges > 1 ? (float *)workspace : nullptr;
+  float *partial = c.ranges > 1 ? (float *)p.ws : nullptr;
   const auto launch = [&](auto kernel, int waves) {
-    kernel<<<grid, 64 * waves, lds, stream>>>(codes, scales, meta, N, K, x, tokens, ldx, y, y_bf16, ldy, partial,
-                                              c.waves, c.long_walk);
+    kernel<<<grid, 64 * waves, lds, p.stream>>>(p.codes, p.scales, p.meta, p.N, p.K, p.x, p.tokens, p.ldx, p.y, p.y_bf16,
+                                                p.ldy, partial, c.waves, c.long_walk);
   };
   if (has_helper(c.waves, SL)) launch(k_matvec_tile<MX, X, SL, SW, true>, c.waves + 1);
   else if constexpr (SL == 1) launch(k_matvec_tile<MX, X, SL, SW, false>, c.waves);
   if (partial)
-    k_matvec_join<<<(unsigned)std::min(kFlatGrid, (N * tokens + 255) / 256), 256, 0, stream>>>(
-        partial, c.ranges, MX ? nullptr : meta, N, tokens, y, y_bf16, ldy);
+    k_matvec_join<<<(unsigned)std::min(kFlatGrid, (p.N * p.tokens + 255) / 256), 256, 0, p.stream>>>(
+        partial, c.ranges, MX ? nullptr : p.meta, p.N, p.tokens, p.y, p.y_bf16, p.ldy);
 }
 
-template <bool MX, typename X, int J, int WK>
-void rows(const uint8_t *codes, const uint8_t *scales, const float *meta, int64_t N, int64_t K, const X *x, void *y,
-          int y_bf16, hipStream_t stream) {
-  // 12 waves a CU (20480 x 5120: 13.5 us, with 16 waves 14.7, 32 16.1), the rows dealt evenly
-  const int64_t per = kRowWaves / WK, turns = (N + per - 1) / per, slots = (int64_t)device_cus() * 3;
+template <bool MX, int J, int WK, int R, int T, typename X> void rows(const Product<X> &p) {
+  // 12 waves a CU (one token, 20480 x 5120: 13.5 us, with 16 waves 14.7, 32
+  // 16.1), the rows dealt evenly
+  constexpr int kWaves = row_waves(WK);
+  const int64_t per = kWaves / WK * R, turns = (p.N + per - 1) / per, slots = (int64_t)device_cus() * (12 / kWaves);
   const int64_t each = (turns + slots - 1) / slots;
   const unsigned grid = (unsigned)((turns + each - 1) / each);
-  k_matvec_row<MX, X, J, WK><<<grid, 64 * kRowWaves, 0, stream>>>(codes, scales, meta, N, K, x, y, y_bf16);
+  k_matvec_row<MX, X, J, WK, R, T><<<grid, 64 * kWaves, 0, p.stream>>>(p.codes, p.scales, p.meta, p.N, p.K, p.x, p.ldx,
+                                                                      p.y, p.y_bf16, p.ldy);
 }
 
-// One token whose x fits the registers of a workgroup.
-bool one_token(int64_t tokens, int64_t K) { return tokens == 1 && K >= kShortK && K <= 4 * 3 * kWaveK; }
+// Products for k_matvec_row: tokens whose x fits the registers of a workgroup
+// (one up to K = 24576, two in bf16 up to 16384, four up to 8192), of which
+// more than one only up to 2e8 products: each costs an instruction there,
+// while the tiles' cost does not grow with the tokens.  us, rows / tiles, for
+// 2, 3, 4 tokens in bf16: 5120 x 5120 8.1 9.1 10.5 / 10.3, 20480 x 2048 8.0
+// 9.5 11.1 / 12.8, 10000 x 8192 13.5 16.1 18.2 / 17.7, 20480 x 5120 18.8 22.5
+// 26.7 / 17.2; in f32 5120 x 5120 9.3 13.4 15.7 / 17.2, 20480 x 5120 23.3
+// 35.8 42.1 / 25.5.
+bool by_rows(int64_t N, int64_t K, int64_t tokens, bool f32) {
+  if (K < kShortK) return false;
+  if (tokens == 1) return K <= 12 * kWaveK;
+  if (tokens > 4 || K > (tokens == 2 && !f32 ? 8 : 4) * kWaveK) return false;
+  return N * K <= 200000000 / tokens;
+}
 
-template <bool MX, typename X>
-void matvec(const uint8_t *codes, const uint8_t *scales, const float *meta, int64_t N, int64_t K, const void *xv,
-            int64_t tokens, int64_t ldx, void *y, int yb, int64_t ldy, void *ws, hipStream_t st) {
-  const X *x = (const X *)xv;
-  if (one_token(tokens, K)) {
-    if (K <= kWaveK) rows<MX, X, 1, 1>(codes, scales, meta, N, K, x, y, yb, st);
-    else if (K <= 2 * kWaveK) rows<MX, X, 2, 1>(codes, scales, meta, N, K, x, y, yb, st);
-    else if (K <= 3 * kWaveK) rows<MX, X, 3, 1>(codes, scales, meta, N, K, x, y, yb, st);
-    else if (K <= 8 * kWaveK) rows<MX, X, 2, 4>(codes, scales, meta, N, K, x, y, yb, st);
-    else rows<MX, X, 3, 4>(codes, scales, meta, N, K, x, y, yb, st);
-    return;
+template <bool MX, int T, typename X> void rows_of(const Product<X> &p) {
+  const int64_t loads = (p.K + kWaveK - 1) / kWaveK;
+  if constexpr (T == 1) {
+    if (loads <= 1) rows<MX, 1, 1, 4, T>(p);
+    else if (loads <= 2) rows<MX, 2, 1, 2, T>(p);
+    else if (loads <= 3) rows<MX, 3, 1, 1, T>(p);
+    else if (loads <= 4) rows<MX, 1, 4, 4, T>(p);
+    else if (loads <= 8) rows<MX, 2, 4, 2, T>(p);
+    else rows<MX, 3, 4, 1, T>(p);
+  } else {
+    if (loads <= 1) rows<MX, 1, 1, 4, T>(p);
+    else if (loads <= 2) rows<MX, 1, 2, 4, T>(p);
+    else if (loads <= 3) rows<MX, 1, 3, 4, T>(p);
+    else if (loads <= 4) rows<MX, 1, 4, 4, T>(p);
+    else if constexpr (T == 2 && sizeof(X) == 2) rows<MX, 2, 4, 2, T>(p);
   }
-  if (K < kShortK) {
-    const unsigned grid = (unsigned)std::min(kFlatGrid, (N * tokens + 255) / 256);
-    k_matvec_short<MX, X><<<grid, 256, 0, st>>>(codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy);
-    return;
+}
+
+template <bool MX, typename X> void matvec(const Product<X> &p) {
+  if (by_rows(p.N, p.K, p.tokens, sizeof(X) == 4)) {
+    if (p.tokens == 1) rows_of<MX, 1>(p);
+    else if (p.tokens == 2) rows_of<MX, 2>(p);
+    else if (p.tokens == 3) rows_of<MX, 3>(p);
+    else rows_of<MX, 4>(p);
+  } else if (p.K < kShortK) {
+    const unsigned grid = (unsigned)std::min(kFlatGrid, (p.N * p.tokens + 255) / 256);
+    k_matvec_short<MX, X><<<grid, 256, 0, p.stream>>>(p.codes, p.scales, p.meta, p.N, p.K, p.x, p.tokens, p.ldx, p.y,
+                                                     p.y_bf16, p.ldy);
+  } else {
+    const Cut c = cut_for(p.N, p.K, p.tokens, sizeof(X) == 4);
+    if (c.sl == 1) tile<MX, 1, 4>(c, p);
+    else if constexpr (sizeof(X) == 4) c.sl == 2 ? tile<MX, 2, 2>(c, p) : tile<MX, 3, 2>(c, p);
   }
-  const Cut c = cut_for(N, K, tokens, sizeof(X) == 4);
-  if (c.sl == 1) tile<MX, X, 1, 4>(c, codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy, ws, st);
-  else if (sizeof(X) == 4 && c.sl == 2) tile<MX, float, 2, 2>(c, codes, scales, meta, N, K, (const float *)xv, tokens, ldx, y, yb, ldy, ws, st);
-  else if (sizeof(X) == 4) tile<MX, float, 3, 2>(c, codes, scales, meta, N, K, (const float *)xv, tokens, ldx, y, yb, ldy, ws, st);
 }
 
 }  // namespace
 
 int64_t matvec_workspace_bytes(int64_t N, int64_t K, int64_t tokens, bool f32) {
-  if (N <= 0 || tokens <= 0 || K < kShortK || one_token(tokens, K)) return 0;
+  if (N <= 0 || tokens <= 0 || K < kShortK || by_rows(N, K, tokens, f32)) return 0;
   const Cut c = cut_for(N, K, tokens, f32);
   return c.ranges > 1 ? 4 * c.ranges * tokens * N : 0;
 }
@@ -735,11 +831,14 @@ hipError_t launch_matvec(bool mx, const uint8_t *codes, const uint8_t *scales, c
                          const void *x, int x_dtype, int64_t tokens, int64_t ldx, void *y, int y_dtype, int64_t ldy,
                          void *ws, hipStream_t stream) {
   if (N > 0 && tokens > 0) {
-    const int yb = y_dtype == 1;
-    if (mx && x_dtype == 1) matvec<true, uint16_t>(codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy, ws, stream);
-    else if (mx) matvec<true, float>(codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy, ws, stream);
-    else if (x_dtype == 1) matvec<false, uint16_t>(codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy, ws, stream);
-    else matvec<false, float>(codes, scales, meta, N, K, x, tokens, ldx, y, yb, ldy, ws, stream);
+    const auto run = [&](auto *xt) {
+      using X = std::remove_const_t<std::remove_pointer_t<decltype(xt)>>;
+      const Product<X> p = {codes, scales, meta, N, K, xt, tokens, ldx, y, y_dtype == 1, ldy, ws, stream};
+      if (mx) matvec<true>(p);
+      else matvec<false>(p);
+    };
+    if (x_dtype == 1) run((const uint16_t *)x);
+    else run((const float *)x);
   }
   return hipGetLastError();
 }

@@ -277,3 +277,14 @@ def test_ranges_of_k_join(tokens):
             base = torch.full((tokens, 40), 9.0, dtype=torch.bfloat16, device="cuda")
             _check(_run("nvfp4", w, x, out_dtype=torch.bfloat16, out=base[:, :35]), x, wd, f"K={k} {dt}")
             assert torch.all(base[:, 35:] == 9.0)
+
+
+@pytest.mark.parametrize("k", [128, 2032, 2048, 2064, 4096, 4112, 6144, 6160, 8192, 8208, 16384, 16400, 24576, 24592])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_few_tokens_at_every_length(dt, k):
+    """One to five tokens where a row just fills, overfills or leaves part of
+    the loads of the waves that share it; an odd number of weight rows."""
+    w, wd = _weights("nvfp4", 11, k, k + 1)
+    for tokens in (1, 2, 3, 4, 5):
+        x = _x(tokens, k, DT[dt], 107 + tokens, pad=2, shift=1)
+        _check(_run("nvfp4", w, x, out_dtype=torch.float32), x, wd, f"{dt} {tokens} K={k}")
