@@ -155,32 +155,39 @@ constexpr int kTurnBytes = 4096; // 16 columns x 128 k of bf16
 // tokens and the parts are added at the end.
 template <typename X> constexpr int columns() { return sizeof(X) == 2 ? 1 : 3; }
 
-// 8 consecutive x as the column's bf16 values, zero from `left` on (left a
-// multiple of 16, so all or none).
-__device__ __forceinline__ u32x4_t column8(const uint16_t *x, int64_t left, int) {
-  if (left <= 0) return (u32x4_t){0, 0, 0, 0};
-  return *reinterpret_cast<const u32x4_a2 *>(x);
-}
-__device__ __forceinline__ u32x4_t column8(const float *x, int64_t left, int part) {
-  u32x4_t out = {0, 0, 0, 0};
-  if (left <= 0) return out;
-  const f32x4_a4 a = *reinterpret_cast<const f32x4_a4 *>(x), b = *reinterpret_cast<const f32x4_a4 *>(x + 4);
-  const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+// The three bf16 parts of 8 float32 values, a pair in each word.
+struct Parts {
+  u32x4_t v[3];
+};
+__device__ __forceinline__ Parts split8(const f32x4_t &a, const f32x4_t &b) {
+  constexpr uint32_t kHigh = 0xFFFF0000u;
+  const float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  uint32_t hi[8];
+  float r[8];
+  float odd = 0.0f;                                  // NaN if a remainder is, so where an x is Inf or NaN
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    hi[i] = __float_as_uint(f[i]) & kHigh;
+    r[i] = f[i] - __uint_as_float(hi[i]);
+    odd += r[i];
+  }
+  if (odd != odd) {
+    // an Inf or NaN goes whole into the first part (with the quiet bit set
+    // for a NaN, whose payload may lie below), the others are 0 then
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (f[i] != f[i]) hi[i] |= 0x00400000u;
+      if ((__float_as_uint(f[i]) & 0x7F800000u) == 0x7F800000u) r[i] = 0.0f;
+    }
+  }
+  Parts out;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t w[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float f = v[2 * i + h];
-      // an Inf or NaN goes whole into the first part (with the quiet bit
-      // set for a NaN, whose payload may lie below), the others are 0 then
-      const bool finite = (__float_as_uint(f) & 0x7F800000u) != 0x7F800000u;
-      const uint32_t hi = (__float_as_uint(f) | (f != f ? 0x00400000u : 0u)) & 0xFFFF0000u;
-      const float r = finite ? f - __uint_as_float(hi) : 0.0f;
-      const float mid = __uint_as_float(__float_as_uint(r) & 0xFFFF0000u);
-      w[h] = part == 0 ? hi : __float_as_uint(part == 1 ? r : r - mid);
-    }
-    out[i] = __builtin_amdgcn_perm(w[1], w[0], 0x07060302u);
+    const uint32_t r0 = __float_as_uint(r[2 * i]), r1 = __float_as_uint(r[2 * i + 1]);
+    const float lo0 = r[2 * i] - __uint_as_float(r0 & kHigh), lo1 = r[2 * i + 1] - __uint_as_float(r1 & kHigh);
+    out.v[0][i] = __builtin_amdgcn_perm(hi[2 * i + 1], hi[2 * i], 0x07060302u);
+    out.v[1][i] = __builtin_amdgcn_perm(r1, r0, 0x07060302u);
+    out.v[2][i] = __builtin_amdgcn_perm(__float_as_uint(lo1), __float_as_uint(lo0), 0x07060302u);
   }
   return out;
 }
@@ -188,8 +195,9 @@ __device__ __forceinline__ u32x4_t column8(const float *x, int64_t left, int par
 // A workgroup holds the columns of all its tokens over its range of K in
 // registers -- each wave a slice of SW steps -- and walks tiles of 16 weight
 // rows, blockIdx.x, blockIdx.x + gridDim.x, ...: only codes and scales move
-// in the loop, codes straight to the lanes that multiply them, a tile ahead.  A tile's scales are fetched by the whole workgroup in rows' runs
-// (a lane's own would be 2 bytes out of every line) and pass through LDS.
+// in the loop, codes straight to the lanes that multiply them, a tile ahead.
+// A tile's scales are fetched by the whole workgroup in rows' runs (a lane's
+// own would be 2 bytes out of every line) and pass through LDS.
 // The waves' sums of a tile meet in LDS, too, behind the tile's one barrier,
 // and an extra wave adds and stores them meanwhile.  With more than
 // one range of K (gridDim.z) the sums go to `partial` [z][token][n] instead.
@@ -287,10 +295,10 @@ __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *
   };
 
   // x into registers, by way of LDS: an MFMA's lane wants 8 k of its own
-  // column, which as a load would touch 64 places; so 64-byte runs of k are
-  // loaded, 4 lanes a column, and turned in a region of the wave's own.
-  // Piece (column, p) of run i lies at slot 4 column + (p ^ (column / 4)):
-  // stores and reads then fall on all banks.
+  // column, which as a load would touch 64 places; so runs of k are loaded
+  // and turned, a step at a time, in a region of the wave's own.  Piece p (8
+  // k) of run i (32 k) of a column lies so that stores (4 pieces of 4 columns
+  // or 4 runs) and reads (one piece of 16 columns) fall on all banks.
   bf16x8_t b[SW][4][SL];
   u32x4_t c0[SW], c1[SW];
   const int64_t first = blockIdx.x;
@@ -299,41 +307,84 @@ __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *
   const uint64_t sc_first = load_scales(first);
   uint64_t sc_next = load_scales(clamp(first + step));
   {
-    char *const turn = lds + wave * kTurnBytes;
-    const int col = lane >> 2, piece = lane & 3;
-    const int write = 16 * (4 * col + (piece ^ (col >> 2)));
-    u32x4_t raw[SW][SL][4];
+    char *const turn = lds + wave * (SL * kTurnBytes);
+    const auto slot = [&](int col, int i, int p) {
+      return turn + (col >> 4) * kTurnBytes + i * 1024 + 16 * (4 * ((col & 15) ^ i) + (p ^ ((col & 15) >> 2)));
+    };
+    // a step's columns from LDS (past the last it is repeated: columns are
+    // independent); a lane moved back by 16 finds its x in the other half
+    const auto take = [&](int s) {
 #pragma unroll
-    for (int s = 0; s < SW; ++s)
+      for (int l = 0; l < SL; ++l)
 #pragma unroll
-      for (int l = 0; l < SL; ++l) {
-        const int v = min(16 * l + col, live * kC - 1);     // columns past the last repeat it: they are independent
-        const X *xr = x + (t0 + v / kC) * ldx;
+        for (int j = 0; j < 4; ++j)
+          b[s][j][l] = *reinterpret_cast<const bf16x8_t *>(
+              slot(min(16 * l + row, live * kC - 1), quarter, j ^ (((half >> s) & 1) << 1)));
+    };
+    if constexpr (sizeof(X) == 2) {
+      // 64-byte runs, 4 lanes a token
+      const int col = lane >> 2, piece = lane & 3;
+      const X *xr = x + (t0 + min(col, live - 1)) * ldx;
+      u32x4_t raw[SW][4];
+#pragma unroll
+      for (int s = 0; s < SW; ++s)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int64_t kk = k0 + s * kStepK + 32 * i + 8 * piece;
-          raw[s][l][i] = column8(xr + kk, K - kk, v % kC);
+          const int64_t at = k0 + s * kStepK + 32 * i + 8 * piece;
+          const u32x4_t v = *reinterpret_cast<const u32x4_a2 *>(xr + (at < K ? at : 0));
+          raw[s][i] = at < K ? v : (u32x4_t){0, 0, 0, 0};
         }
+#pragma unroll
+      for (int s = 0; s < SW; ++s) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4_t *>(slot(col, i, piece)) = raw[s][i];
+        take(s);
+      }
+    } else {
+      // a step of a token is 16 lanes' pieces; four tokens a load, the last
+      // ones of all steps in one more
+      constexpr int kT = 16 * SL / 3, kFull = kT / 4, kLeft = kT % 4;
+      static_assert(kLeft == 0 || SW * kLeft == 4, "what is left of the steps fills one load");
+      f32x4_t raw[SW * kFull + 1][2];
+      const auto fetch = [&](f32x4_t *v, int token, int s) {
+        const int64_t at = k0 + s * kStepK + 8 * (lane & 15);
+        const X *from = x + (t0 + min(token, live - 1)) * ldx + (at < K ? at : 0);
+        const f32x4_t v0 = *reinterpret_cast<const f32x4_a4 *>(from);
+        const f32x4_t v1 = *reinterpret_cast<const f32x4_a4 *>(from + 4);
+        v[0] = at < K ? v0 : (f32x4_t){0, 0, 0, 0};
+        v[1] = at < K ? v1 : (f32x4_t){0, 0, 0, 0};
+      };
+      const auto put = [&](const Parts &q, int token) {
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+          if (token < live) *reinterpret_cast<u32x4_t *>(slot(3 * token + p, (lane & 15) >> 2, lane & 3)) = q.v[p];
+      };
+      const int left_token = 4 * kFull + (kLeft ? quarter % (kLeft ? kLeft : 1) : 0);
+      const int left_step = kLeft ? quarter / (kLeft ? kLeft : 1) : 0;
+#pragma unroll
+      for (int s = 0; s < SW; ++s)
+#pragma unroll
+        for (int i = 0; i < kFull; ++i) fetch(raw[s * kFull + i], 4 * i + quarter, s);
+      Parts left;
+      if (kLeft) {
+        fetch(raw[SW * kFull], left_token, left_step);
+        left = split8(raw[SW * kFull][0], raw[SW * kFull][1]);
       }
 #pragma unroll
-    for (int s = 0; s < SW; ++s)
+      for (int s = 0; s < SW; ++s) {
 #pragma unroll
-      for (int l = 0; l < SL; ++l) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4_t *>(turn + i * 1024 + write) = raw[s][l][i];
-        // a lane moved back by 16 finds its x in the other half
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int p = j ^ (((half >> s) & 1) << 1);
-          b[s][j][l] = *reinterpret_cast<const bf16x8_t *>(turn + quarter * 1024 + 16 * (4 * row + (p ^ (row >> 2))));
-        }
+        for (int i = 0; i < kFull; ++i)
+          put(split8(raw[s * kFull + i][0], raw[s * kFull + i][1]), 4 * i + quarter);
+        if (kLeft && left_step == s) put(left, left_token);
+        take(s);
       }
+    }
   }
   // NVFP4: where a column's values span at most 29 binades they are as exact
   // in f16, moved by a power of two so that the largest lies in [2^14, 2^15)
   // and the smallest at 2^-14 or above (8 bits of f16's 11, no subnormals);
-  // the weights decode in half the instructions there.  A wave whose columns do not all allow it
-  // (or hold an Inf or NaN) stays with bf16.
+  // the weights decode in half the instructions there.  A wave whose columns
+  // do not all allow it (or hold an Inf or NaN) stays with bf16.
   bool f16 = false;
   int move[SL];
 #pragma unroll
@@ -598,10 +649,9 @@ template <bool MX, int J, int R> struct RowPart {
 // (so that every wave has some 3 KB in flight, twice).
 constexpr int row_waves(int wk) { return wk == 3 ? 3 : 4; }
 template <bool MX, typename X, int J, int WK, int R, int T>
-__global__ __launch_bounds__(64 * row_waves(WK), T <= 2 ? 3 : 2) void k_matvec_row(const uint8_t *codes, const uint8_t *scales,
-                                                                   const float *meta, int64_t N, int64_t K,
-                                                                   const X *x, int64_t ldx, void *y, int y_bf16,
-                                                                   int64_t ldy) {
+__global__ __launch_bounds__(64 * row_waves(WK), T <= 2 ? 3 : 2) void
+k_matvec_row(const uint8_t *codes, const uint8_t *scales, const float *meta, int64_t N, int64_t K, const X *x, int64_t ldx,
+             void *y, int y_bf16, int64_t ldy) {
   constexpr int kWaves = row_waves(WK), kThreads = 64 * kWaves, kRows = kWaves / WK * R, kC = R * T;
   // x through LDS: a lane's 32 k would be a load of 64 lines of memory.  Each
   // of J T rounds takes the waves' j-th loads of one token; unit u (16 bytes)
@@ -745,7 +795,7 @@ template <bool MX, int SL, int SW, typename X> void tile(const Cut &c, const Pro
   const dim3 grid((unsigned)c.walkers, (unsigned)((p.tokens + kTokens - 1) / kTokens), (unsigned)c.ranges);
   const size_t run = c.waves * SW * kStepK / Scale<MX>::kPerByte;       // scale bytes of a row
   const size_t lds =
-      std::max<size_t>(c.waves * kTurnBytes, 2 * max_waves(SL) * SL * 64 * sizeof(f32x4_t) + 32 * (run + 4));
+      std::max<size_t>(c.waves * SL * kTurnBytes, 2 * max_waves(SL) * SL * 64 * sizeof(f32x4_t) + 32 * (run + 4));
   float *partial = c.ranges > 1 ? (float *)p.ws : nullptr;
   const auto launch = [&](auto kernel, int waves) {
     kernel<<<grid, 64 * waves, lds, p.stream>>>(p.codes, p.scales, p.meta, p.N, p.K, p.x, p.tokens, p.ldx, p.y, p.y_bf16,
@@ -771,17 +821,17 @@ template <bool MX, int J, int WK, int R, int T, typename X> void rows(const Prod
 
 // Products for k_matvec_row: tokens whose x fits the registers of a workgroup
 // (one up to K = 24576, two in bf16 up to 16384, four up to 8192), of which
-// more than one only up to 2e8 products: each costs an instruction there,
-// while the tiles' cost does not grow with the tokens.  us, rows / tiles, for
-// 2, 3, 4 tokens in bf16: 5120 x 5120 8.1 9.1 10.5 / 10.3, 20480 x 2048 8.0
-// 9.5 11.1 / 12.8, 10000 x 8192 13.5 16.1 18.2 / 17.7, 20480 x 5120 18.8 22.5
-// 26.7 / 17.2; in f32 5120 x 5120 9.3 13.4 15.7 / 17.2, 20480 x 5120 23.3
-// 35.8 42.1 / 25.5.
+// more than one only up to 2e8 products (four in f32 1e8): each costs an
+// instruction there, while the tiles' cost does not grow with the tokens.
+// us, rows / tiles, for 2, 3, 4 tokens of NVFP4 in bf16: 5120 x 5120 7.9 8.9
+// 10.3 / 10.3, 20480 x 2048 8.6 9.3 11.9 / 12.9, 10000 x 8192 13.9 16.0 18.4
+// / 17.8, 20480 x 5120 18.6 22.6 27.1 / 17.4; in f32 5120 x 2048 6.3 7.3 8.9
+// / 10.5, 5120 x 5120 9.3 11.2 15.3 / 12.5, 20480 x 5120 23.6 30.0 41.2 / 19.5.
 bool by_rows(int64_t N, int64_t K, int64_t tokens, bool f32) {
   if (K < kShortK) return false;
   if (tokens == 1) return K <= 12 * kWaveK;
   if (tokens > 4 || K > (tokens == 2 && !f32 ? 8 : 4) * kWaveK) return false;
-  return N * K <= 200000000 / tokens;
+  return N * K <= (f32 && tokens == 4 ? 100000000 : 200000000) / tokens;
 }
 
 template <bool MX, int T, typename X> void rows_of(const Product<X> &p) {
