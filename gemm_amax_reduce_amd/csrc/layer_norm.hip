@@ -42,7 +42,7 @@ template <typename T> __device__ __forceinline__ uint32_t absmax8(const Row8<T> 
 // One workgroup per row, rows blockIdx.x, blockIdx.x + gridDim.x, ...; the
 // threads keep their columns' weights and biases over all of them, and a row
 // is fetched while the one before it is worked on.
-template <typename X, typename Y, int VPT>
+template <typename X, typename Y, int VPT, bool ONCE>
 __global__ __launch_bounds__(kMaxThreads) void k_ln_forward(const X *x, int64_t ldx, const void *w, const void *b,
                                                             int w_bf16, Y *y, int64_t ldy, float *mean, float *rstd,
                                                             uint32_t *amax, int64_t rows, int64_t cols, float eps,
@@ -51,20 +51,21 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_forward(const X *x, int64_t 
   __shared__ uint32_t umax[kMaxWaves];
   const int waves = threads >> 6;
   const float inv = 1.0f / (float)cols;
-  Span sp[VPT];
+  constexpr bool kSplit = sizeof(X) + sizeof(Y) > 4;
+  Piece<kSplit> sp[VPT];
   float wv[VPT][8], bv[VPT][8];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    sp[j] = Span((int64_t)(threadIdx.x + j * threads) * 8, cols);
-    load_param8(wv[j], w, w_bf16, sp[j].at, cols, 1.0f);
-    load_param8(bv[j], b, w_bf16, sp[j].at, cols, 0.0f);
+    sp[j] = Piece<kSplit>(Piece<kSplit>::start(threadIdx.x + j * threads), (uint32_t)cols);
+    param_piece(wv[j], w, w_bf16, sp[j], 1.0f);
+    param_piece(bv[j], b, w_bf16, sp[j], 0.0f);
   }
   uint32_t top = 0;
   int turn = 0;
   Row8<X> next[VPT];
   int64_t row = blockIdx.x;
 #pragma unroll
-  for (int j = 0; j < VPT; ++j) next[j].load(x + row * ldx + sp[j].at);
+  for (int j = 0; j < VPT; ++j) load_piece<ONCE>(next[j], x + row * ldx, sp[j]);
   while (row < rows) {
     float v[VPT][8];
     float s = 0.0f;
@@ -76,7 +77,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_forward(const X *x, int64_t 
     }
     const int64_t later = row + gridDim.x, fetch = min(later, rows - 1);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) next[j].load(x + fetch * ldx + sp[j].at);
+    for (int j = 0; j < VPT; ++j) load_piece<ONCE>(next[j], x + fetch * ldx, sp[j]);
     __builtin_amdgcn_sched_barrier(0);       // the loads go out before this row's work, not after it
     const float m = block_sum(s, part[turn][0], waves) * inv;
     float s2 = 0.0f;
@@ -101,7 +102,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_forward(const X *x, int64_t 
       for (int i = 0; i < 8; ++i) v[j][i] = __builtin_fmaf(v[j][i] * r, wv[j][i], bv[j][i]);
       Row8<Y> q;
       q.set(v[j]);
-      if (sp[j].dup < 8) q.store(y + row * ldy + sp[j].at);
+      store_piece(q, y + row * ldy, sp[j]);
       if (amax) top = max(top, absmax8(q));
     }
     row = later;
@@ -193,7 +194,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_forward_wide(const X *x, int
 // up dw and db of its columns over all its rows.  At the end the groups'
 // sums meet in LDS, and the workgroup leaves one partial row of dw and one of
 // db.  partial: [gridDim.x][2][cols]; dynamic LDS: (groups - 1) * cols floats.
-template <typename X, typename D, int VPT, int THREADS>
+template <typename X, typename D, int VPT, int THREADS, bool ONCE>
 __global__ __launch_bounds__(THREADS) void k_ln_backward(const D *dy, int64_t lddy, const X *x, int64_t ldx,
                                                          const float *mean, const float *rstd, const void *w,
                                                          int w_bf16, X *dx, int64_t lddx, float *partial, int64_t rows,
@@ -204,12 +205,13 @@ __global__ __launch_bounds__(THREADS) void k_ln_backward(const D *dy, int64_t ld
   const int group = wave / wpr, t = threadIdx.x - group * tpr;
   const int64_t stride = (int64_t)gridDim.x * groups;
   const float inv = 1.0f / (float)cols;
-  Span sp[VPT];
+  constexpr bool kSplit = sizeof(X) + sizeof(D) > 4;
+  Piece<kSplit> sp[VPT];
   float wv[VPT][8], dw[VPT][8], db[VPT][8];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    sp[j] = Span((int64_t)(t + j * tpr) * 8, cols);
-    load_param8(wv[j], w, w_bf16, sp[j].at, cols, 1.0f);
+    sp[j] = Piece<kSplit>(Piece<kSplit>::start(t + j * tpr), (uint32_t)cols);
+    param_piece(wv[j], w, w_bf16, sp[j], 1.0f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = db[j][i] = 0.0f;
   }
@@ -220,8 +222,8 @@ __global__ __launch_bounds__(THREADS) void k_ln_backward(const D *dy, int64_t ld
     r = min(r, rows - 1);              // (past the last row: fetched, not used)
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      xn[j].load(x + r * ldx + sp[j].at);
-      dn[j].load(dy + r * lddy + sp[j].at);
+      load_piece<ONCE>(xn[j], x + r * ldx, sp[j]);
+      load_piece<ONCE>(dn[j], dy + r * lddy, sp[j]);
     }
     mn = mean[r];
     rn = rstd[r];
@@ -286,7 +288,7 @@ __global__ __launch_bounds__(THREADS) void k_ln_backward(const D *dy, int64_t ld
           o[i] = r * __builtin_fmaf(-(xv[i] - m) * r, s2, __builtin_fmaf(dv[i], wv[j][i], -s1));
         Row8<X> q;
         q.set(o);
-        if (sp[j].dup < 8) q.store(dx + row * lddx + sp[j].at);
+        store_piece(q, dx + row * lddx, sp[j]);
       }
     }
   }
@@ -300,7 +302,7 @@ __global__ __launch_bounds__(THREADS) void k_ln_backward(const D *dy, int64_t ld
         for (int j = 0; j < VPT; ++j) {
           Row8<float> q;
           q.set(k ? db[j] : dw[j]);
-          q.store(sums + (int64_t)(group - 1) * cols + sp[j].at);
+          store_piece(q, sums + (int64_t)(group - 1) * cols, sp[j]);
         }
       }
       __syncthreads();
@@ -314,14 +316,14 @@ __global__ __launch_bounds__(THREADS) void k_ln_backward(const D *dy, int64_t ld
         for (int g = 1; g < groups; ++g) {
           Row8<float> q;
           float u[8];
-          q.load(sums + (int64_t)(g - 1) * cols + sp[j].at);
+          load_piece(q, sums + (int64_t)(g - 1) * cols, sp[j]);
           q.get(u);
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] += u[i];
         }
         Row8<float> q;
         q.set(v);
-        if (sp[j].dup < 8) q.store(partial + ((int64_t)blockIdx.x * 2 + k) * cols + sp[j].at);
+        store_piece(q, partial + ((int64_t)blockIdx.x * 2 + k) * cols, sp[j]);
       }
     }
   }
@@ -451,12 +453,12 @@ void forward(const void *x, int64_t ldx, const void *w, const void *b, int w_bf1
   // one round of workgroups, 16 waves a CU (4096 x 5120: 18.7 us, with 20 waves
   // 21.7, one workgroup a row 22)
   const unsigned grid = (unsigned)std::min<int64_t>(rows, (int64_t)device_cus() * std::max(1, 16 * 64 / threads));
-  if (vpt == 1)
-    k_ln_forward<X, Y, 1><<<grid, threads, 0, stream>>>(xp, ldx, w, b, w_bf16, yp, ldy, mean, rstd, amax, rows, cols,
-                                                       eps, threads);
-  else if (vpt == 2)
-    k_ln_forward<X, Y, 2><<<grid, threads, 0, stream>>>(xp, ldx, w, b, w_bf16, yp, ldy, mean, rstd, amax, rows, cols,
-                                                       eps, threads);
+  const auto launch = [&](auto kernel) {
+    kernel<<<grid, threads, 0, stream>>>(xp, ldx, w, b, w_bf16, yp, ldy, mean, rstd, amax, rows, cols, eps, threads);
+  };
+  const bool once = reads_once(rows * cols * (int64_t)(sizeof(X) + sizeof(Y)));
+  if (vpt == 1) with_flag(once, [&](auto o) { launch(k_ln_forward<X, Y, 1, o.value>); });
+  else if (vpt == 2) with_flag(once, [&](auto o) { launch(k_ln_forward<X, Y, 2, o.value>); });
   else
     k_ln_forward_wide<X, Y><<<grid, threads, 0, stream>>>(xp, ldx, w, b, w_bf16, yp, ldy, mean, rstd, amax, rows, cols,
                                                          eps);
@@ -510,9 +512,11 @@ void backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, const fl
                                                                   partial, rows, cols, c.tpr, c.groups);
     };
     constexpr bool narrow = sizeof(X) + sizeof(D) == 4;
-    if (c.vpt == 1) launch(k_ln_backward<X, D, 1, back_threads(1, narrow)>);
-    else if (c.vpt == 2) launch(k_ln_backward<X, D, 2, back_threads(2, narrow)>);
-    else if constexpr (narrow) launch(k_ln_backward<X, D, 4, back_threads(4, true)>);
+    with_flag(reads_once(rows * cols * (int64_t)(2 * sizeof(X) + sizeof(D))), [&](auto o) {
+      if (c.vpt == 1) launch(k_ln_backward<X, D, 1, back_threads(1, narrow), o.value>);
+      else if (c.vpt == 2) launch(k_ln_backward<X, D, 2, back_threads(2, narrow), o.value>);
+      else if constexpr (narrow) launch(k_ln_backward<X, D, 4, back_threads(4, true), o.value>);
+    });
   } else if (rows > 0) {
     float2 *sums = (float2 *)workspace;
     const unsigned grid = (unsigned)std::min<int64_t>(rows, (int64_t)device_cus() * 2);

@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace nvfp4 {
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
@@ -15,6 +17,7 @@ typedef float f32x2_t __attribute__((ext_vector_type(2)));
 // 16-byte global accesses at any address, so one form serves every row and
 // the types only promise the element's own alignment.
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
@@ -122,21 +125,112 @@ __device__ __forceinline__ void store_row8(const Row8<T> &r, T *row, int64_t at,
   else if (at < n) r.store_part(row + at, (int)(n - at));
 }
 
-// A thread's 8 columns of rows of n >= 8 elements, from position at on.  Where
-// they pass the row's end they are moved back onto its last 8, so that every
-// load and store is a whole one: the first `dup` of them then belong to other
-// threads as well, and only sums over the row have to leave them out (a
-// duplicate store writes the same value).  dup = 8: all of them.
-struct Span {
-  int64_t at;
-  int dup;
-  Span() = default;
-  __device__ __forceinline__ Span(int64_t from, int64_t n) {
-    at = min(from, n - 8);
-    dup = (int)min(from - at, (int64_t)8);
+// Whether a call that moves that many bytes reads its matrices past the
+// caches' usual order (nontemporal): above the 256 MB that the last cache
+// holds, what is read only pushes out what was written, which whoever is next
+// reads.  Each followed by a pass over its result, us: layer norm backward of
+// 32768 x 8192 bf16 518 -> 489, distillation's gradient of 4096 x 50016 bf16
+// 340 -> 312, of 512 x 131072 f32 179 -> 154; 4096 x 5120 bf16, which fits,
+// would go from 58 to 64.
+inline bool reads_once(int64_t bytes) { return bytes > ((int64_t)256 << 20); }
+// f(std::true_type) or f(std::false_type)
+template <typename F> inline void with_flag(bool flag, F f) {
+  if (flag) f(std::true_type());
+  else f(std::false_type());
+}
+
+// A thread's 8 columns of rows of n >= 8 elements (n below 2^31), the q-th of
+// the row.  16-bit types take 8 in a row, one 16-byte load.  With SPLIT, for
+// kernels of which a matrix is f32, they are two times 4, and a wave's 512
+// lie in two blocks of 256, lane after lane: each load then covers whole
+// lines.  (32 bytes a lane in two loads leave every line to both of them: a
+// copy like that reaches 5.1 TB/s, lane after lane 5.9.)
+//
+// Where columns would pass the row's end they are moved back onto its last 4
+// or 8, so that every load and store is a whole one: the first of them then
+// belong to other threads as well, and only sums over the row have to leave
+// them out (a duplicate store writes the same value).
+template <bool SPLIT> struct Piece;
+template <> struct Piece<false> {
+  uint32_t a;
+  int dup;                       // how many of the 8 are others'
+  Piece() = default;
+  static __device__ __forceinline__ uint32_t start(uint32_t q) { return q * 8; }
+  __device__ __forceinline__ Piece(uint32_t from, uint32_t n) {
+    a = min(from, n - 8);
+    dup = (int)min(from - a, 8u);
   }
   __device__ __forceinline__ bool mine(int i) const { return i >= dup; }
+  // of two sums, over the first 4 and the last 4, where rows are whole pieces
+  __device__ __forceinline__ float sum_mine(float lo, float hi) const { return dup ? 0.0f : lo + hi; }
 };
+template <> struct Piece<true> {
+  uint32_t a, b;                 // positions of the first and the last 4
+  int da, db;                    // how many of each are others'
+  Piece() = default;
+  static __device__ __forceinline__ uint32_t start(uint32_t q) { return (q & ~63u) * 8 + (q & 63u) * 4; }
+  __device__ __forceinline__ Piece(uint32_t from, uint32_t n) {
+    a = min(from, n - 4);
+    b = min(from + 256, n - 4);
+    da = (int)min(from - a, 4u);
+    db = (int)min(from + 256 - b, 4u);
+  }
+  __device__ __forceinline__ bool mine(int i) const { return i < 4 ? i >= da : i - 4 >= db; }
+  __device__ __forceinline__ float sum_mine(float lo, float hi) const { return (da ? 0.0f : lo) + (db ? 0.0f : hi); }
+};
+// ONCE: past the caches' usual order.  (A template's choice: two branches of
+// one kernel are merged into the plain load.)
+template <typename V, bool ONCE, typename T> __device__ __forceinline__ V load_as(const T *p) {
+  const V *v = reinterpret_cast<const V *>(p);
+  return ONCE ? __builtin_nontemporal_load(v) : *v;
+}
+template <bool ONCE = false, typename T>
+__device__ __forceinline__ void load_piece(Row8<T> &r, const T *row, const Piece<false> &p) {
+  if constexpr (sizeof(T) == 2) {
+    r.r = load_as<u32x4_a2, ONCE>(row + p.a);
+  } else {
+    r.a = load_as<f32x4_a4, ONCE>(row + p.a);
+    r.b = load_as<f32x4_a4, ONCE>(row + p.a + 4);
+  }
+}
+template <bool ONCE = false, typename T>
+__device__ __forceinline__ void load_piece(Row8<T> &r, const T *row, const Piece<true> &p) {
+  if constexpr (sizeof(T) == 2) {
+    const u32x2_a2 x = load_as<u32x2_a2, ONCE>(row + p.a), y = load_as<u32x2_a2, ONCE>(row + p.b);
+    r.r = (u32x4_a4){x[0], x[1], y[0], y[1]};
+  } else {
+    r.a = load_as<f32x4_a4, ONCE>(row + p.a);
+    r.b = load_as<f32x4_a4, ONCE>(row + p.b);
+  }
+}
+template <typename T> __device__ __forceinline__ void store_piece(const Row8<T> &r, T *row, const Piece<false> &p) {
+  if (p.dup < 8) r.store(row + p.a);
+}
+__device__ __forceinline__ void store_piece(const Row8<uint16_t> &r, uint16_t *row, const Piece<true> &p) {
+  if (p.da < 4) *reinterpret_cast<u32x2_a2 *>(row + p.a) = (u32x2_a2){r.r[0], r.r[1]};
+  if (p.db < 4) *reinterpret_cast<u32x2_a2 *>(row + p.b) = (u32x2_a2){r.r[2], r.r[3]};
+}
+__device__ __forceinline__ void store_piece(const Row8<float> &r, float *row, const Piece<true> &p) {
+  if (p.da < 4) *reinterpret_cast<f32x4_a4 *>(row + p.a) = r.a;
+  if (p.db < 4) *reinterpret_cast<f32x4_a4 *>(row + p.b) = r.b;
+}
+// Of a parameter vector of n elements (f32 or bf16 by a wave-uniform flag),
+// `fill` where it is absent.
+template <bool SPLIT>
+__device__ __forceinline__ void param_piece(float *v, const void *p, int is_bf16, const Piece<SPLIT> &at, float fill) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = fill;
+  if (!p) return;
+  if (is_bf16) {
+    Row8<uint16_t> r;
+    load_piece(r, (const uint16_t *)p, at);
+    r.get(v);
+  } else {
+    Row8<float> r;
+    load_piece(r, (const float *)p, at);
+    r.get(v);
+  }
+}
 
 // A parameter vector (f32 or bf16 by a wave-uniform flag), 8 from position
 // at, `fill` past the end and where the vector is absent.
