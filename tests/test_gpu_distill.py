@@ -276,6 +276,22 @@ def test_rows_past_one_launch():
     assert torch.allclose(back, grad, rtol=0, atol=2 * 4 * U * 164)
 
 
+@pytest.mark.parametrize("dt,tokens,vocab", [("bf16", 8300, 8190), ("bf16", 2100, 32801), ("bf16", 1100, 65537),
+                                             ("bf16", 521, 131101), ("f32", 8300, 4099), ("f32", 1040, 33001),
+                                             ("f32", 500, 70003)])
+def test_large_calls(dt, tokens, vocab):
+    """More logits than the last cache holds; some of the rows are checked."""
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    z = (3 * torch.randn((tokens, vocab), generator=g, device="cuda")).to(DT[dt])
+    idx = torch.randint(-1, vocab, (tokens, 20), generator=g, device="cuda")
+    t = 2 * torch.randn((tokens, 20), generator=g, device="cuda")
+    weight = torch.rand(tokens, generator=g, device="cuda")
+    print(f"[distill] {tokens}x{vocab} {dt}", flush=True)
+    rows = torch.tensor([0, 1, tokens // 2, tokens - 2, tokens - 1], device="cuda")
+    for label, out in zip(("pair", "step"), _all(z, idx, t, 1.5, weight)):
+        _check(z[rows], idx[rows], t[rows], 1.5, weight[rows], [o[rows] for o in out], label)
+
+
 def test_other_stream_and_repeat():
     z, idx, t, weight = _inputs(9, 40000, 32, "bf16", 41)
     want = nv.nvfp4_distill_topk_step(z, idx, t, weight)

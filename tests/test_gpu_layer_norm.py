@@ -158,6 +158,33 @@ def test_many_rows():
         assert torch.equal(p, q)          # the sums' order is fixed
 
 
+@pytest.mark.parametrize("cols", [511, 2041, 4099, 12293])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_large_calls(dt, cols):
+    """More than the last cache holds: rows do not know of each other, so some
+    of them come out bit for bit as in a small call; the sums over all rows
+    are checked against float64."""
+    rows = 272_000_000 // (4 if dt == "bf16" else 8) // cols
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = (torch.randn((rows, cols), generator=g, device="cuda") * 2 + 0.5).to(DT[dt])
+    dy = torch.randn((rows, cols), generator=g, device="cuda").to(DT[dt])
+    w, b = torch.randn(cols, generator=g, device="cuda"), torch.randn(cols, generator=g, device="cuda")
+    print(f"[layer norm] {rows}x{cols} {dt}", flush=True)
+    y, mean, rstd = nv.nvfp4_layer_norm(x, w, b)
+    dx, dw, db = nv.nvfp4_layer_norm_backward(dy, x, mean, rstd, w, grad_dtype=torch.float32)
+    for at in (slice(0, 3), slice(rows // 2, rows // 2 + 5), slice(rows - 4, rows)):
+        ys, ms, rs = nv.nvfp4_layer_norm(x[at], w, b)
+        assert torch.equal(ys, y[at]) and torch.equal(ms, mean[at]) and torch.equal(rs, rstd[at])
+        assert torch.equal(nv.nvfp4_layer_norm_backward(dy[at], x[at], ms, rs, w)[0], dx[at])
+    sums = torch.zeros((4, cols), dtype=torch.float64, device="cuda")
+    for at in range(0, rows, 4096):
+        d = dy[at:at + 4096].double()
+        h = (x[at:at + 4096].double() - mean[at:at + 4096, None].double()) * rstd[at:at + 4096, None].double()
+        sums += torch.stack([(d * h).sum(0), (d * h).abs().sum(0), d.sum(0), d.abs().sum(0)])
+    assert torch.all((dw.double() - sums[0]).abs() <= (rows + 4) * U * sums[1])
+    assert torch.all((db.double() - sums[2]).abs() <= (rows + 2) * U * sums[3])
+
+
 def test_large_mean_keeps_the_variance():
     """x = 4096 + noise: the variance is taken about the mean, so its digits
     do not cancel (the bound grows only with the rounding of the mean)."""
