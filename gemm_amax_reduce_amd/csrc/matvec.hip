@@ -636,7 +636,10 @@ template <bool MX, int J, int R> struct RowPart {
       const uint8_t *cr = codes + row * (K / 2), *sr = scales + row * (K / Scale<MX>::kPerByte);
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        c[r][j] = *reinterpret_cast<const u32x4_a8 *>(cr + k[j] / 2);
+        // read once (one token, 131075 x 5120: 66.2 -> 58.8 us, 20480 x 5120
+        // 13.9 -> 13.3, the same where the weights stay in the last cache;
+        // the tiles' loads of half a line lose by it: 72 -> 85)
+        c[r][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a8 *>(cr + k[j] / 2));
         s[r][j].load(sr + k[j] / Scale<MX>::kPerByte);
       }
     }
