@@ -51,7 +51,7 @@ _lib = None
 EXPORTS = ("nvfp4_quantize", "nvfp4_rht_quantize", "nvfp4_amax", "nvfp4_quantize_amax", "nvfp4_quantize_dual",
            "mxfp4_quantize", "mxfp4_gemm", "nvfp4_dequantize", "nvfp4_gemm", "nvfp4_gemm_ws",
            "nvfp4_gemm_workspace_bytes", "nvfp4_gemm_noalloc", "mxfp8_quantize", "mxfp8_gemm", "nvfp4_layer_norm",
-           "nvfp4_layer_norm_backward", "nvfp4_layer_norm_backward_workspace_bytes", "nvfp4_matvec", "mxfp4_matvec",
+           "nvfp4_layer_norm_workspace_bytes", "nvfp4_layer_norm_backward", "nvfp4_layer_norm_backward_workspace_bytes", "nvfp4_matvec", "mxfp4_matvec",
            "nvfp4_matvec_workspace_bytes", "nvfp4_distill_topk", "nvfp4_distill_topk_backward",
            "nvfp4_distill_topk_step", "nvfp4_distill_topk_workspace_bytes", "nvfp4_probe_mfma", "nvfp4_probe_philox", "nvfp4_status_string")
 
@@ -97,7 +97,9 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_gemm_noalloc.restype = ci
         L.nvfp4_gemm_workspace_bytes.restype = i64
         cf = ctypes.c_float
-        L.nvfp4_layer_norm.argtypes = [vp, ci, i64, i64, i64, vp, vp, ci, cf, vp, ci, i64, vp, vp, vp, vp]
+        L.nvfp4_layer_norm.argtypes = [vp, ci, i64, i64, i64, vp, vp, ci, cf, vp, ci, i64, vp, vp, vp, vp, i64, vp]
+        L.nvfp4_layer_norm_workspace_bytes.argtypes = [i64, i64]
+        L.nvfp4_layer_norm_workspace_bytes.restype = i64
         L.nvfp4_layer_norm.restype = ci
         L.nvfp4_layer_norm_backward.argtypes = [vp, ci, i64, vp, ci, i64, i64, i64, vp, vp, vp, ci, vp, i64, vp, vp,
                                                 ci, vp, i64, vp]
@@ -677,10 +679,15 @@ def nvfp4_layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: 
             y, ldy = out, _require_matrix_out(out, rows, cols, out_dtype, dev)
         mean = torch.empty(rows, dtype=torch.float32, device=dev)
         rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-        top = torch.empty(1, dtype=torch.float32, device=dev) if amax else None
+        top, ws, need = None, None, 0
+        if amax:
+            top = torch.empty(1, dtype=torch.float32, device=dev)
+            need = lib().nvfp4_layer_norm_workspace_bytes(rows, cols)
+            if need > 0:
+                ws = torch.empty(need, dtype=torch.uint8, device=dev)
         _check(lib().nvfp4_layer_norm(x.data_ptr(), _dtype_code(x), rows, cols, ldx, wp, bp, wcode, eps, y.data_ptr(),
-                                      ycode, ldy, mean.data_ptr(), rstd.data_ptr(), _ptr(top), _current_handle(dev)),
-               "nvfp4_layer_norm")
+                                      ycode, ldy, mean.data_ptr(), rstd.data_ptr(), _ptr(top), _ptr(ws), need,
+                                      _current_handle(dev)), "nvfp4_layer_norm")
     return (y, mean, rstd, top) if amax else (y, mean, rstd)
 
 

@@ -329,19 +329,27 @@ int nvfp4_gemm_noalloc(const nvfp4_tensor *a, const nvfp4_tensor *b, void *c, in
                                              b->outer, a->k, c, c_dtype, ldc, ws, (hipStream_t)hip_stream));
 }
 
+int64_t nvfp4_layer_norm_workspace_bytes(int64_t rows, int64_t cols) {
+  if (cols < 1 || cols > kMaxNormCols || !matrix_ok(rows, cols, cols)) return NVFP4_ERR_SHAPE;
+  return nvfp4::layer_norm_workspace_bytes(rows, cols);
+}
+
 int nvfp4_layer_norm(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void *weight,
                      const void *bias, int w_dtype, float eps, void *y, int y_dtype, int64_t ldy, float *mean,
-                     float *rstd, float *amax, void *hip_stream) {
+                     float *rstd, float *amax, void *workspace, int64_t workspace_bytes, void *hip_stream) {
   if (!dtype_ok(x_dtype) || !dtype_ok(w_dtype) || !dtype_ok(y_dtype)) return NVFP4_ERR_ENUM;
   if (cols < 1 || cols > kMaxNormCols || !matrix_ok(rows, cols, ldx) || !matrix_ok(rows, cols, ldy))
     return NVFP4_ERR_SHAPE;
   if (!(eps >= 0.0f) || eps > 3.0e38f) return NVFP4_ERR_VALUE;
+  const int64_t need = amax ? nvfp4::layer_norm_workspace_bytes(rows, cols) : 0;
+  if (workspace_bytes < need) return NVFP4_ERR_SHAPE;
   if (rows > 0 && (!x || !y || !mean || !rstd)) return NVFP4_ERR_NULL;
+  if (need > 0 && !workspace) return NVFP4_ERR_NULL;
   if (!aligned(x, dtype_size(x_dtype)) || !aligned(y, dtype_size(y_dtype)) || !aligned(weight, dtype_size(w_dtype)) ||
-      !aligned(bias, dtype_size(w_dtype)) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(amax, 4))
+      !aligned(bias, dtype_size(w_dtype)) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(amax, 4) || !aligned(workspace, 4))
     return NVFP4_ERR_ALIGN;
   return hip_status(nvfp4::launch_layer_norm(x, x_dtype, rows, cols, ldx, weight, bias, w_dtype, eps, y, y_dtype, ldy,
-                                             mean, rstd, amax, (hipStream_t)hip_stream));
+                                             mean, rstd, amax, workspace, (hipStream_t)hip_stream));
 }
 
 int64_t nvfp4_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {

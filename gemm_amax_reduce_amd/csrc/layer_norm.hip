@@ -25,8 +25,28 @@ namespace {
 constexpr int kMaxThreads = 1024;
 constexpr int kMaxWaves = kMaxThreads / 64;
 
-__global__ void k_amax_init(uint32_t *amax) {
-  if (threadIdx.x == 0) *amax = 0;
+// top becomes the wave's maximum, left in the wave's place of `share` (LDS).
+__device__ __forceinline__ void wave_umax_to(uint32_t *share, uint32_t &top) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, 64));
+  if ((threadIdx.x & 63) == 0) share[threadIdx.x >> 6] = top;
+}
+
+// The tensor maximum from the workgroups' own.  (Atomics on one word take
+// some 10 ns each, and the workgroups come to their ends together: 4096 x 5120
+// 22.8 us with atomics, 8192 x 512 33.)
+constexpr int kJoinThreads = 1024;
+__global__ __launch_bounds__(kJoinThreads) void k_amax_join(const uint32_t *part, int n, uint32_t *amax) {
+  __shared__ uint32_t share[kJoinThreads / 64];
+  uint32_t top = 0;
+  for (int i = threadIdx.x; i < n; i += kJoinThreads) top = max(top, part[i]);
+  wave_umax_to(share, top);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 1; i < kJoinThreads / 64; ++i) top = max(top, share[i]);
+    *amax = top;
+  }
 }
 
 // |value as stored| as a bit pattern (NaN > Inf > finite).
@@ -109,14 +129,11 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_forward(const X *x, int64_t 
     turn ^= 1;
   }
   if (amax) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, 64));
-    if ((threadIdx.x & 63) == 0) umax[threadIdx.x >> 6] = top;
+    wave_umax_to(umax, top);
     __syncthreads();
     if (threadIdx.x == 0) {
       for (int i = 1; i < waves; ++i) top = max(top, umax[i]);
-      // the value only grows, so a workgroup that cannot raise it skips the atomic
-      if (top > __hip_atomic_load(amax, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(amax, top);
+      amax[blockIdx.x] = top;
     }
   }
 }
@@ -124,9 +141,10 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_forward(const X *x, int64_t 
 // Rows wider than the registers of a workgroup hold, or narrower than one
 // vector: the row is read three times (the second and third from the caches).
 template <typename X, typename Y>
-__global__ __launch_bounds__(kMaxThreads) void k_ln_forward_wide(const X *x, int64_t ldx, const void *w, const void *b, int w_bf16,
-                                            Y *y, int64_t ldy, float *mean, float *rstd, uint32_t *amax,
-                                            int64_t rows, int64_t cols, float eps) {
+__global__ __launch_bounds__(kMaxThreads) void k_ln_forward_wide(const X *x, int64_t ldx, const void *w, const void *b,
+                                                                 int w_bf16, Y *y, int64_t ldy, float *mean,
+                                                                 float *rstd, uint32_t *amax, int64_t rows,
+                                                                 int64_t cols, float eps) {
   __shared__ float part[2][2][kMaxWaves];
   const int64_t step = (int64_t)kMaxThreads * 8;
   const int64_t c0 = (int64_t)threadIdx.x * 8;
@@ -181,9 +199,13 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_forward_wide(const X *x, int
     }
   }
   if (amax) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, 64));
-    if ((threadIdx.x & 63) == 0) atomicMax(amax, top);
+    __shared__ uint32_t umax[kMaxWaves];
+    wave_umax_to(umax, top);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < kMaxWaves; ++i) top = max(top, umax[i]);
+      amax[blockIdx.x] = top;
+    }
   }
 }
 
@@ -440,28 +462,42 @@ int threads_for(int64_t vectors, int vpt) {
   return (int)std::min<int64_t>(kMaxThreads, (t + 63) / 64 * 64);
 }
 
-template <typename X, typename Y>
-void forward(const void *x, int64_t ldx, const void *w, const void *b, int w_bf16, void *y, int64_t ldy, float *mean,
-             float *rstd, uint32_t *amax, int64_t rows, int64_t cols, float eps, hipStream_t stream) {
+// How a forward pass is cut: vectors per thread (0 = the wide kernel),
+// threads and number of the workgroups.
+struct ForwardCut {
+  int vpt, threads;
+  unsigned grid;
+};
+ForwardCut forward_cut(int64_t rows, int64_t cols) {
   const int64_t vectors = (cols + 7) / 8;
-  const X *xp = (const X *)x;
-  Y *yp = (Y *)y;
+  ForwardCut c;
   // one 8-element vector a thread where that makes a workgroup of up to 256
   // threads, else two (fewer waves to wait for at a row's two reductions)
-  const int vpt = cols < 8 ? 0 : vectors <= 256 ? 1 : vectors <= 2 * kMaxThreads ? 2 : 0;
-  const int threads = vpt ? threads_for(vectors, vpt) : kMaxThreads;
+  c.vpt = cols < 8 ? 0 : vectors <= 256 ? 1 : vectors <= 2 * kMaxThreads ? 2 : 0;
+  c.threads = c.vpt ? threads_for(vectors, c.vpt) : kMaxThreads;
   // one round of workgroups, 16 waves a CU (4096 x 5120: 18.7 us, with 20 waves
   // 21.7, one workgroup a row 22)
-  const unsigned grid = (unsigned)std::min<int64_t>(rows, (int64_t)device_cus() * std::max(1, 16 * 64 / threads));
+  c.grid = (unsigned)std::min<int64_t>(rows, (int64_t)device_cus() * std::max(1, 16 * 64 / c.threads));
+  return c;
+}
+
+// amax: a place for each workgroup's maximum, or null
+template <typename X, typename Y>
+void forward(const ForwardCut &c, const void *x, int64_t ldx, const void *w, const void *b, int w_bf16, void *y,
+             int64_t ldy, float *mean, float *rstd, uint32_t *amax, int64_t rows, int64_t cols, float eps,
+             hipStream_t stream) {
+  const X *xp = (const X *)x;
+  Y *yp = (Y *)y;
   const auto launch = [&](auto kernel) {
-    kernel<<<grid, threads, 0, stream>>>(xp, ldx, w, b, w_bf16, yp, ldy, mean, rstd, amax, rows, cols, eps, threads);
+    kernel<<<c.grid, c.threads, 0, stream>>>(xp, ldx, w, b, w_bf16, yp, ldy, mean, rstd, amax, rows, cols, eps,
+                                             c.threads);
   };
   const bool once = reads_once(rows * cols * (int64_t)(sizeof(X) + sizeof(Y)));
-  if (vpt == 1) with_flag(once, [&](auto o) { launch(k_ln_forward<X, Y, 1, o.value>); });
-  else if (vpt == 2) with_flag(once, [&](auto o) { launch(k_ln_forward<X, Y, 2, o.value>); });
+  if (c.vpt == 1) with_flag(once, [&](auto o) { launch(k_ln_forward<X, Y, 1, o.value>); });
+  else if (c.vpt == 2) with_flag(once, [&](auto o) { launch(k_ln_forward<X, Y, 2, o.value>); });
   else
-    k_ln_forward_wide<X, Y><<<grid, threads, 0, stream>>>(xp, ldx, w, b, w_bf16, yp, ldy, mean, rstd, amax, rows, cols,
-                                                         eps);
+    k_ln_forward_wide<X, Y><<<c.grid, c.threads, 0, stream>>>(xp, ldx, w, b, w_bf16, yp, ldy, mean, rstd, amax, rows,
+                                                             cols, eps);
 }
 
 // How a backward pass is cut: vectors per thread (0 = the two kernels for
@@ -532,22 +568,29 @@ void backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, const fl
 
 }  // namespace
 
+int64_t layer_norm_workspace_bytes(int64_t rows, int64_t cols) {
+  const int64_t grid = forward_cut(rows, cols).grid;
+  return grid > 1 ? 4 * grid : 0;
+}
+
 hipError_t launch_layer_norm(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void *w,
                              const void *b, int w_dtype, float eps, void *y, int y_dtype, int64_t ldy, float *mean,
-                             float *rstd, float *amax, hipStream_t stream) {
-  if (amax) k_amax_init<<<1, 64, 0, stream>>>((uint32_t *)amax);
+                             float *rstd, float *amax, void *workspace, hipStream_t stream) {
+  const ForwardCut c = forward_cut(rows, cols);
+  // (a single workgroup's maximum is the tensor's)
+  uint32_t *part = (uint32_t *)(amax && c.grid > 1 ? workspace : amax);
   if (rows > 0) {
-    uint32_t *um = (uint32_t *)amax;
     const int wb = w_dtype == 1;
     if (x_dtype == 1 && y_dtype == 1)
-      forward<uint16_t, uint16_t>(x, ldx, w, b, wb, y, ldy, mean, rstd, um, rows, cols, eps, stream);
+      forward<uint16_t, uint16_t>(c, x, ldx, w, b, wb, y, ldy, mean, rstd, part, rows, cols, eps, stream);
     else if (x_dtype == 1)
-      forward<uint16_t, float>(x, ldx, w, b, wb, y, ldy, mean, rstd, um, rows, cols, eps, stream);
+      forward<uint16_t, float>(c, x, ldx, w, b, wb, y, ldy, mean, rstd, part, rows, cols, eps, stream);
     else if (y_dtype == 1)
-      forward<float, uint16_t>(x, ldx, w, b, wb, y, ldy, mean, rstd, um, rows, cols, eps, stream);
+      forward<float, uint16_t>(c, x, ldx, w, b, wb, y, ldy, mean, rstd, part, rows, cols, eps, stream);
     else
-      forward<float, float>(x, ldx, w, b, wb, y, ldy, mean, rstd, um, rows, cols, eps, stream);
+      forward<float, float>(c, x, ldx, w, b, wb, y, ldy, mean, rstd, part, rows, cols, eps, stream);
   }
+  if (amax && c.grid != 1) k_amax_join<<<1, kJoinThreads, 0, stream>>>(part, (int)c.grid, (uint32_t *)amax);
   return hipGetLastError();
 }
 

@@ -52,11 +52,13 @@ hipError_t launch_mx8_gemm(const uint8_t *a_codes, const uint8_t *a_scales, cons
                            hipStream_t stream);
 
 // Layer norm over rows (stats in mean/rstd; amax, w, b, dw, db may be null;
-// dtypes 0 = f32, 1 = bf16; leading dimensions in elements).  The backward's
-// workspace: layer_norm_backward_workspace_bytes, 16-byte aligned.
+// dtypes 0 = f32, 1 = bf16; leading dimensions in elements).  Workspaces:
+// layer_norm_workspace_bytes with amax, 4-byte aligned, and the backward's
+// layer_norm_backward_workspace_bytes, 16-byte aligned.
+int64_t layer_norm_workspace_bytes(int64_t rows, int64_t cols);
 hipError_t launch_layer_norm(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void *w,
                              const void *b, int w_dtype, float eps, void *y, int y_dtype, int64_t ldy, float *mean,
-                             float *rstd, float *amax, hipStream_t stream);
+                             float *rstd, float *amax, void *workspace, hipStream_t stream);
 int64_t layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
 hipError_t launch_layer_norm_backward(const void *dy, int dy_dtype, int64_t lddy, const void *x, int x_dtype,
                                       int64_t ldx, const float *mean, const float *rstd, const void *w, int w_dtype,

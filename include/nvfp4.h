@@ -387,13 +387,20 @@ int mxfp8_gemm(const mxfp8_tensor *a, const mxfp8_tensor *b, void *c, int c_dtyp
  *              bit patterns: NaN > Inf > finite; 0 when rows == 0), so that
  *              nvfp4_quantize_amax of y on axis 1 with it equals
  *              nvfp4_quantize bit for bit without the first read of y.
+ *  workspace : device, with amax at least nvfp4_layer_norm_workspace_bytes
+ *              (rows, cols) bytes (0 for a single row), 4-byte aligned,
+ *              contents ignored and overwritten; calls that share one must
+ *              not overlap in time.  Unused (may be NULL) without amax.
  * All sums are binary32, the variance a sum of squared differences from the
  * mean.  A row's non-finite values reach that row only.  Outputs must not
- * overlap inputs.  Deterministic.  Enqueues one kernel, two with amax.
+ * overlap inputs.  Deterministic.  Enqueues one kernel, two with amax (one for
+ * a single row).  The workspace size is NVFP4_ERR_SHAPE for sizes that the
+ * call itself refuses.
  */
 int nvfp4_layer_norm(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void *weight,
                      const void *bias, int w_dtype, float eps, void *y, int y_dtype, int64_t ldy, float *mean,
-                     float *rstd, float *amax, void *hip_stream);
+                     float *rstd, float *amax, void *workspace, int64_t workspace_bytes, void *hip_stream);
+int64_t nvfp4_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
 
 /*
  * nvfp4_layer_norm_backward -- the gradients of nvfp4_layer_norm: with

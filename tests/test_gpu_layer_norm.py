@@ -237,6 +237,19 @@ def test_maximum_feeds_the_quantizer():
         assert torch.equal(p.codes, q.codes) and torch.equal(p.scales, q.scales) and torch.equal(p.meta, q.meta)
 
 
+@pytest.mark.parametrize("rows,cols", [(9001, 24), (4100, 700), (700, 5003), (600, 16500)])
+def test_maximum_over_many_workgroups(rows, cols):
+    x, _, w, b = _inputs(rows, cols, torch.bfloat16, torch.float32, 41)
+    y, _, _, amax = nv.nvfp4_layer_norm(x, w, b, amax=True)
+    assert amax.item() == y.float().abs().max().item()
+    for value in (float("inf"), float("nan")):
+        x[rows - 1, cols - 1] = value            # the row's mean is not finite then
+        assert np.isnan(nv.nvfp4_layer_norm(x, w, b, amax=True)[3].item())
+        x[rows - 1, cols - 1] = 0.0
+    b[cols // 2] = float("-inf")                 # an infinite output, no NaN
+    assert nv.nvfp4_layer_norm(x, w, b, amax=True)[3].item() == float("inf")
+
+
 def test_gradient_against_differences():
     """The directional derivative of sum(dy * y) from central differences of
     the float64 formula; the kernel's share of the error is its bound, the

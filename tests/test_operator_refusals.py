@@ -26,7 +26,7 @@ def _call(fn, good, **bad):
 
 
 NORM = dict(x=FAKE, xd=1, rows=4, cols=64, ldx=64, w=FAKE, b=FAKE, wd=1, eps=1e-5, y=FAKE, yd=1, ldy=64, mean=FAKE,
-            rstd=FAKE, amax=FAKE, stream=None)
+            rstd=FAKE, amax=FAKE, ws=FAKE, bytes=1 << 20, stream=None)
 
 
 @_no_gpu
@@ -36,7 +36,8 @@ NORM = dict(x=FAKE, xd=1, rows=4, cols=64, ldx=64, w=FAKE, b=FAKE, wd=1, eps=1e-
     (dict(cols=(1 << 31) + 1, ldx=1 << 32, ldy=1 << 32), SHAPE), (dict(eps=-1e-9), VALUE), (dict(eps=math.nan), VALUE),
     (dict(eps=math.inf), VALUE), (dict(x=None), NULL), (dict(y=None), NULL), (dict(mean=None), NULL),
     (dict(rstd=None), NULL), (dict(x=FAKE + 1), ALIGN), (dict(xd=0, x=FAKE + 2), ALIGN), (dict(w=FAKE + 1), ALIGN),
-    (dict(amax=FAKE + 2), ALIGN), (dict(mean=FAKE + 2), ALIGN)])
+    (dict(amax=FAKE + 2), ALIGN), (dict(mean=FAKE + 2), ALIGN),
+    (dict(bytes=0), SHAPE), (dict(ws=None), NULL), (dict(ws=FAKE + 2), ALIGN)])
 def test_layer_norm(L, bad, status):
     assert _call(L.nvfp4_layer_norm, NORM, **bad) == status
 
@@ -64,6 +65,10 @@ def test_workspace_sizes(L):
     need = L.nvfp4_layer_norm_backward_workspace_bytes(1000, 64)
     assert need > 0
     assert _call(L.nvfp4_layer_norm_backward, BACK, rows=1000, bytes=need - 1) == SHAPE
+    assert L.nvfp4_layer_norm_workspace_bytes(-1, 64) == SHAPE
+    assert L.nvfp4_layer_norm_workspace_bytes(4, 0) == SHAPE
+    assert L.nvfp4_layer_norm_workspace_bytes(0, 64) == L.nvfp4_layer_norm_workspace_bytes(1, 64) == 0
+    assert L.nvfp4_layer_norm_workspace_bytes(4, 64) == 16
     assert L.nvfp4_distill_topk_workspace_bytes(-1, 64) == SHAPE
     assert L.nvfp4_distill_topk_workspace_bytes(4, 0) == SHAPE
     assert L.nvfp4_distill_topk_workspace_bytes(4, 1 << 31) == SHAPE
