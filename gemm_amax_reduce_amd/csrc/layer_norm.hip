@@ -144,9 +144,10 @@ template <typename X, typename Y>
 __global__ __launch_bounds__(kMaxThreads) void k_ln_forward_wide(const X *x, int64_t ldx, const void *w, const void *b,
                                                                  int w_bf16, Y *y, int64_t ldy, float *mean,
                                                                  float *rstd, uint32_t *amax, int64_t rows,
-                                                                 int64_t cols, float eps) {
+                                                                 int64_t cols, float eps, int threads) {
   __shared__ float part[2][2][kMaxWaves];
-  const int64_t step = (int64_t)kMaxThreads * 8;
+  const int waves = threads >> 6;
+  const int64_t step = (int64_t)threads * 8;
   const int64_t c0 = (int64_t)threadIdx.x * 8;
   uint32_t top = 0;
   int turn = 0;
@@ -162,7 +163,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_forward_wide(const X *x, int
       for (int i = 0; i < 8; ++i) t += v[i];
       s += t;
     }
-    const float m = block_sum(s, part[turn][0], kMaxWaves) / (float)cols;
+    const float m = block_sum(s, part[turn][0], waves) / (float)cols;
     float s2 = 0.0f;
     for (int64_t at = c0; at < cols; at += step) {
       Row8<X> q;
@@ -176,7 +177,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_forward_wide(const X *x, int
       }
       s2 += t;
     }
-    const float var = block_sum(s2, part[turn][1], kMaxWaves) / (float)cols;
+    const float var = block_sum(s2, part[turn][1], waves) / (float)cols;
     const float r = 1.0f / __builtin_sqrtf(var + eps);
     if (threadIdx.x == 0) {
       mean[row] = m;
@@ -203,7 +204,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_forward_wide(const X *x, int
     wave_umax_to(umax, top);
     __syncthreads();
     if (threadIdx.x == 0) {
-      for (int i = 1; i < kMaxWaves; ++i) top = max(top, umax[i]);
+      for (int i = 1; i < waves; ++i) top = max(top, umax[i]);
       amax[blockIdx.x] = top;
     }
   }
@@ -356,9 +357,10 @@ template <typename X, typename D>
 __global__ __launch_bounds__(kMaxThreads) void k_ln_backward_rows(const D *dy, int64_t lddy, const X *x, int64_t ldx,
                                                                   const float *mean, const float *rstd, const void *w,
                                                                   int w_bf16, float2 *sums, int64_t rows,
-                                                                  int64_t cols) {
+                                                                  int64_t cols, int threads) {
   __shared__ float part[2][2][kMaxWaves];
-  const int64_t step = (int64_t)kMaxThreads * 8;
+  const int waves = threads >> 6;
+  const int64_t step = (int64_t)threads * 8;
   int turn = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
     const float m = mean[row], r = rstd[row];
@@ -382,8 +384,8 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_backward_rows(const D *dy, i
       s1 += t1;
       s2 += t2;
     }
-    const float a1 = block_sum(s1, part[turn][0], kMaxWaves) / (float)cols;
-    const float a2 = block_sum(s2, part[turn][1], kMaxWaves) / (float)cols;
+    const float a1 = block_sum(s1, part[turn][0], waves) / (float)cols;
+    const float a2 = block_sum(s2, part[turn][1], waves) / (float)cols;
     if (threadIdx.x == 0) sums[row] = make_float2(a1, a2);
   }
 }
@@ -462,6 +464,14 @@ int threads_for(int64_t vectors, int vpt) {
   return (int)std::min<int64_t>(kMaxThreads, (t + 63) / 64 * 64);
 }
 
+// Threads of a row for the kernels that take any width, and how many such
+// workgroups: 32 waves a CU, one wave a row where that holds it (forward of
+// 65536 x 6: 60 us, in workgroups of 1024 threads 760).
+int any_width_threads(int64_t cols) { return cols < 8 ? 64 : kMaxThreads; }
+unsigned any_width_grid(int64_t rows, int64_t cols) {
+  return (unsigned)std::min<int64_t>(rows, (int64_t)device_cus() * (32 * 64 / any_width_threads(cols)));
+}
+
 // How a forward pass is cut: vectors per thread (0 = the wide kernel),
 // threads and number of the workgroups.
 struct ForwardCut {
@@ -474,7 +484,12 @@ ForwardCut forward_cut(int64_t rows, int64_t cols) {
   // one 8-element vector a thread where that makes a workgroup of up to 256
   // threads, else two (fewer waves to wait for at a row's two reductions)
   c.vpt = cols < 8 ? 0 : vectors <= 256 ? 1 : vectors <= 2 * kMaxThreads ? 2 : 0;
-  c.threads = c.vpt ? threads_for(vectors, c.vpt) : kMaxThreads;
+  if (!c.vpt) {
+    c.threads = any_width_threads(cols);
+    c.grid = any_width_grid(rows, cols);
+    return c;
+  }
+  c.threads = threads_for(vectors, c.vpt);
   // one round of workgroups, 16 waves a CU (4096 x 5120: 18.7 us, with 20 waves
   // 21.7, one workgroup a row 22)
   c.grid = (unsigned)std::min<int64_t>(rows, (int64_t)device_cus() * std::max(1, 16 * 64 / c.threads));
@@ -495,9 +510,7 @@ void forward(const ForwardCut &c, const void *x, int64_t ldx, const void *w, con
   const bool once = reads_once(rows * cols * (int64_t)(sizeof(X) + sizeof(Y)));
   if (c.vpt == 1) with_flag(once, [&](auto o) { launch(k_ln_forward<X, Y, 1, o.value>); });
   else if (c.vpt == 2) with_flag(once, [&](auto o) { launch(k_ln_forward<X, Y, 2, o.value>); });
-  else
-    k_ln_forward_wide<X, Y><<<c.grid, c.threads, 0, stream>>>(xp, ldx, w, b, w_bf16, yp, ldy, mean, rstd, amax, rows,
-                                                             cols, eps);
+  else launch(k_ln_forward_wide<X, Y>);
 }
 
 // How a backward pass is cut: vectors per thread (0 = the two kernels for
@@ -555,9 +568,9 @@ void backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, const fl
     });
   } else if (rows > 0) {
     float2 *sums = (float2 *)workspace;
-    const unsigned grid = (unsigned)std::min<int64_t>(rows, (int64_t)device_cus() * 2);
-    k_ln_backward_rows<X, D><<<grid, kMaxThreads, 0, stream>>>(dp, lddy, xp, ldx, mean, rstd, w, w_bf16, sums, rows,
-                                                              cols);
+    const int threads = any_width_threads(cols);
+    k_ln_backward_rows<X, D><<<any_width_grid(rows, cols), threads, 0, stream>>>(dp, lddy, xp, ldx, mean, rstd, w, w_bf16,
+                                                                                sums, rows, cols, threads);
     k_ln_backward_cols<X, D><<<dim3((unsigned)((cols + 2047) / 2048), (unsigned)c.parts), 256, 0, stream>>>(
         dp, lddy, xp, ldx, mean, rstd, w, w_bf16, sums, op, lddx, partial, rows, cols);
   }
