@@ -10,9 +10,16 @@
 // A row without a valid entry has loss 0 and gradient 0 whatever z holds.
 // Bound by HBM: the student's logits are read (and, for a gradient, written)
 // once or twice, an exponential and some ten operations each; the teacher's
-// lists are small.  Rows are cut into segments of the vocabulary, so that
-// few rows still fill the GPU; each segment leaves its running maximum and
-// sum, and the segments are joined in a fixed order.
+// lists are small.  A row that fits the registers of a workgroup is read once
+// for everything.  Longer rows, and few of them, are cut into segments of the
+// vocabulary, so that they fill the GPU; each segment leaves its running
+// maximum and sum, and the segments are joined in a fixed order.
+//
+// Measured on one MI355X, kernels alone: whole rows, loss 24 x 32768 bf16 6.1
+// us (1.6 MB: latency), 8192 x 32768 bf16 87 us (6.1 TB/s), loss and gradient
+// 4096 x 131072 bf16 451 us (4.8 TB/s), 2048 x 50016 f32 172 us (4.8 TB/s); in
+// segments, 777 x 50021 f32 statistics 26 us (5.9 TB/s), loss 4.3 to 4.9 us,
+// gradient 58 us (5.4 TB/s), 1024 x 131072 bf16 loss 50 us (5.4 TB/s).
 #include "nvfp4_kernels.h"
 #include "row_common.h"
 
@@ -395,9 +402,10 @@ struct Split {
   int segments;
 };
 // Segments of a row: enough workgroups to fill the GPU twice over (16 a CU;
-// 777 rows of 50021 f32: 1 segment 34 us, 2 32, 4 29, 8 28), none longer than
-// 32768 elements, none shorter than four loads of every thread, their starts
-// at whole 8-element vectors.
+// loss and gradient of 777 rows of 50021 f32: 1 segment 94 us, 2 85, 5 84, 10
+// 83.5), a longer vocabulary at least
+// one per 32768 elements, none shorter than four loads of every thread, their
+// starts at whole 8-element vectors.
 Split split_for(int64_t T, int64_t V) {
   const int64_t vec = (int64_t)kDT * 8;
   const int64_t want = std::max<int64_t>(V / 32768, (int64_t)device_cus() * 16 / std::max<int64_t>(1, T));
@@ -408,9 +416,10 @@ Split split_for(int64_t T, int64_t V) {
 
 // Vectors per thread of the one-workgroup-a-row form; 0 where the segments'
 // form is taken: rows that 1024 threads do not hold in 64 registers each, or
-// shorter than a vector; and, of rows above 128 KB, a loss alone (777 x 50021
-// f32: 37 us in segments, 62 in rows) or too few for the CUs (100 x 131072
-// bf16 with the gradient: 28 us and 31; 200 rows: 44 and 39).
+// shorter than a vector; and, of rows above 128 KB, a loss alone (2048 x 50016
+// f32: 75 us in segments, 89 in rows) or too few for the CUs (24 x 65536 bf16
+// with the gradient: 10.8 us in segments, 12.5 in rows; 128 rows 19.5 and
+// 19.3, 512 rows 46 and 31).
 int row_vectors(int64_t rows, int64_t V, int size, bool gradient) {
   const int64_t vectors = (V + 7) / 8;
   if (V < 8) return 0;

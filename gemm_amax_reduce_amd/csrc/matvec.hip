@@ -27,6 +27,13 @@
 // each of 8 bits: exact for every value whose low part does not fall below
 // the bf16 range.  Products are exact in binary32 and added there; the
 // tensor scale g is applied once to the sum.
+//
+// Measured on one MI355X, kernels alone, with weights that no cache holds:
+// rows, one bf16 token, NVFP4 5120 x 5120 5.4 us (2.7 TB/s: 2.3 us of reading
+// behind a start of 3), 20480 x 5120 12.5 us (4.7 TB/s), 131075 x 5120 61 us
+// (6.2 TB/s); tiles, 8 bf16 tokens, 20480 x 5120 18 us, 131075 x 5120 74.6 us
+// (5.1 TB/s), 5 f32 tokens of MXFP4 5120 x 20480 17.9 us and 4 us for joining
+// the ranges of K; 8 f32 tokens of 131075 x 5120, two slabs of columns, 139 us.
 #include "gemm_common.h"
 #include "nvfp4_device.h"
 #include "nvfp4_kernels.h"
