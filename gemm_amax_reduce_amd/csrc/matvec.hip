@@ -33,7 +33,7 @@
 // behind a start of 3), 20480 x 5120 12.5 us (4.7 TB/s), 131075 x 5120 61 us
 // (6.2 TB/s); tiles, 8 bf16 tokens, 20480 x 5120 18 us, 131075 x 5120 74.6 us
 // (5.1 TB/s), 5 f32 tokens of MXFP4 5120 x 20480 17.9 us and 4 us for joining
-// the ranges of K; 8 f32 tokens of 131075 x 5120, two slabs of columns, 139 us.
+// the ranges of K; 8 f32 tokens of NVFP4 131075 x 5120, in two slabs of columns, 114.
 #include "gemm_common.h"
 #include "nvfp4_device.h"
 #include "nvfp4_kernels.h"
