@@ -710,11 +710,11 @@ def nvfp4_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Ten
         dx = x.new_empty((rows, cols))
         dweight = torch.empty(cols, dtype=grad_dtype, device=dev)
         dbias = torch.empty(cols, dtype=grad_dtype, device=dev)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
         _check(lib().nvfp4_layer_norm_backward(dy.data_ptr(), _dtype_code(dy), lddy, x.data_ptr(), _dtype_code(x),
                                                rows, cols, ldx, mp, rp, wp, wcode,
                                                dx.data_ptr(), cols, dweight.data_ptr(), dbias.data_ptr(), gcode,
-                                               ws.data_ptr(), need, _current_handle(dev)),
+                                               _ptr(ws), need, _current_handle(dev)),
                "nvfp4_layer_norm_backward")
     return dx, dweight, dbias
 

@@ -223,12 +223,14 @@ __global__ __launch_bounds__(kMaxThreads) void k_ln_forward_wide(const X *x, int
 // sums and dx, the next row's are fetched meanwhile, and every thread adds
 // up dw and db of its columns over all its rows.  At the end the groups'
 // sums meet in LDS, and the workgroup leaves one partial row of dw and one of
-// db.  partial: [gridDim.x][2][cols]; dynamic LDS: (groups - 1) * cols floats.
+// db, or, if it is the only one, dw and db themselves (each may be null).
+// partial: [gridDim.x][2][cols]; dynamic LDS: (groups - 1) * cols floats.
 template <typename X, typename D, int VPT, int THREADS, bool ONCE>
 __global__ __launch_bounds__(THREADS) void k_ln_backward(const D *dy, int64_t lddy, const X *x, int64_t ldx,
                                                          const float *mean, const float *rstd, const void *w,
-                                                         int w_bf16, X *dx, int64_t lddx, float *partial, int64_t rows,
-                                                         int64_t cols, int tpr, int groups) {
+                                                         int w_bf16, X *dx, int64_t lddx, float *partial, void *dw_out,
+                                                         void *db_out, int g_bf16, int64_t rows, int64_t cols, int tpr,
+                                                         int groups) {
   __shared__ float2 part[2][kMaxWaves];
   extern __shared__ float sums[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wpr = tpr >> 6;
@@ -351,9 +353,17 @@ __global__ __launch_bounds__(THREADS) void k_ln_backward(const D *dy, int64_t ld
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] += u[i];
         }
-        Row8<float> q;
-        q.set(v);
-        store_piece(q, partial + ((int64_t)blockIdx.x * 2 + k) * cols, sp[j]);
+        void *const out = gridDim.x > 1 ? partial + ((int64_t)blockIdx.x * 2 + k) * cols : k ? db_out : dw_out;
+        if (!out) continue;
+        if (gridDim.x == 1 && g_bf16) {
+          Row8<uint16_t> q;
+          q.set(v);
+          store_piece(q, (uint16_t *)out, sp[j]);
+        } else {
+          Row8<float> q;
+          q.set(v);
+          store_piece(q, (float *)out, sp[j]);
+        }
       }
     }
   }
@@ -485,18 +495,23 @@ struct ForwardCut {
   int vpt, threads;
   unsigned grid;
 };
-ForwardCut forward_cut(int64_t rows, int64_t cols) {
+ForwardCut forward_cut(int64_t rows, int64_t cols, bool amax) {
   const int64_t vectors = (cols + 7) / 8;
   ForwardCut c;
   // one 8-element vector a thread where that makes a workgroup of up to 256
   // threads, else two (fewer waves to wait for at a row's two reductions)
   c.vpt = cols < 8 ? 0 : vectors <= 256 ? 1 : vectors <= 2 * kMaxThreads ? 2 : 0;
+  c.threads = c.vpt ? threads_for(vectors, c.vpt) : any_width_threads(cols);
+  // the maximum over a few rows: one workgroup, whose own it is (4 x 5120: 13.4
+  // us a call, with a second kernel 17.4)
+  if (amax && rows <= 4) {
+    c.grid = (unsigned)std::min<int64_t>(rows, 1);
+    return c;
+  }
   if (!c.vpt) {
-    c.threads = any_width_threads(cols);
     c.grid = any_width_grid(rows, cols);
     return c;
   }
-  c.threads = threads_for(vectors, c.vpt);
   // one round of workgroups, 16 waves a CU (4096 x 5120: 18.7 us, with 20 waves
   // 21.7, one workgroup a row 22)
   c.grid = (unsigned)std::min<int64_t>(rows, (int64_t)device_cus() * std::max(1, 16 * 64 / c.threads));
@@ -541,8 +556,10 @@ BackCut back_cut(int64_t rows, int64_t cols, bool narrow) {      // narrow: x an
     c.groups = std::max(1, back_threads(c.vpt, narrow) / c.tpr);
     const int64_t rounds = (rows + c.groups - 1) / c.groups;
     // one workgroup a CU, and two rounds for it at least: what the partial
-    // rows cost to write and add up stays below a pass over the data
-    c.parts = std::min((rounds + 1) / 2, (int64_t)device_cus());
+    // rows cost to write and add up stays below a pass over the data.  Up to
+    // four rounds one workgroup does without partial rows and the kernel that
+    // adds them (6 x 5120 bf16: 13.5 us a call, in two kernels 17.3).
+    c.parts = rounds <= 4 ? std::min<int64_t>(rounds, 1) : std::min((rounds + 1) / 2, (int64_t)device_cus());
   } else {
     c.tpr = c.groups = 0;
     const int64_t col_groups = (cols + 2047) / 2048;
@@ -565,7 +582,8 @@ void backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, const fl
     const size_t lds = (size_t)(c.groups - 1) * cols * sizeof(float);
     const auto launch = [&](auto kernel) {
       kernel<<<(unsigned)c.parts, c.tpr * c.groups, lds, stream>>>(dp, lddy, xp, ldx, mean, rstd, w, w_bf16, op, lddx,
-                                                                  partial, rows, cols, c.tpr, c.groups);
+                                                                  partial, dw, db, g_bf16, rows, cols, c.tpr,
+                                                                  c.groups);
     };
     constexpr bool narrow = sizeof(X) + sizeof(D) == 4;
     with_flag(reads_once(rows * cols * (int64_t)(2 * sizeof(X) + sizeof(D))), [&](auto o) {
@@ -581,7 +599,7 @@ void backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, const fl
     k_ln_backward_cols<X, D><<<dim3((unsigned)((cols + 2047) / 2048), (unsigned)c.parts), 256, 0, stream>>>(
         dp, lddy, xp, ldx, mean, rstd, w, w_bf16, sums, op, lddx, partial, rows, cols);
   }
-  if (dw || db)
+  if ((dw || db) && !(rows > 0 && c.vpt && c.parts == 1))
     k_ln_backward_sum<<<(unsigned)((2 * cols + 63) / 64), 64 * kShares, 0, stream>>>(partial, c.parts, cols, dw, db,
                                                                                     g_bf16);
 }
@@ -589,14 +607,14 @@ void backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, const fl
 }  // namespace
 
 int64_t layer_norm_workspace_bytes(int64_t rows, int64_t cols) {
-  const int64_t grid = forward_cut(rows, cols).grid;
+  const int64_t grid = forward_cut(rows, cols, true).grid;
   return grid > 1 ? 4 * grid : 0;
 }
 
 hipError_t launch_layer_norm(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void *w,
                              const void *b, int w_dtype, float eps, void *y, int y_dtype, int64_t ldy, float *mean,
                              float *rstd, float *amax, void *workspace, hipStream_t stream) {
-  const ForwardCut c = forward_cut(rows, cols);
+  const ForwardCut c = forward_cut(rows, cols, amax != nullptr);
   // (a single workgroup's maximum is the tensor's)
   uint32_t *part = (uint32_t *)(amax && c.grid > 1 ? workspace : amax);
   if (rows > 0) {
@@ -615,8 +633,10 @@ hipError_t launch_layer_norm(const void *x, int x_dtype, int64_t rows, int64_t c
 }
 
 int64_t layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
-  const BackCut a = back_cut(rows, cols, false), b = back_cut(rows, cols, true);     // whatever the types
-  return std::max((a.vpt ? 0 : 8 * rows) + 8 * cols * a.parts, (b.vpt ? 0 : 8 * rows) + 8 * cols * b.parts);
+  const auto need = [&](const BackCut &c) {
+    return c.vpt ? (c.parts > 1 ? 8 * cols * c.parts : 0) : 8 * rows + 8 * cols * c.parts;
+  };
+  return std::max(need(back_cut(rows, cols, false)), need(back_cut(rows, cols, true)));     // whatever the types
 }
 
 hipError_t launch_layer_norm_backward(const void *dy, int dy_dtype, int64_t lddy, const void *x, int x_dtype,

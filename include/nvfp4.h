@@ -388,13 +388,13 @@ int mxfp8_gemm(const mxfp8_tensor *a, const mxfp8_tensor *b, void *c, int c_dtyp
  *              nvfp4_quantize_amax of y on axis 1 with it equals
  *              nvfp4_quantize bit for bit without the first read of y.
  *  workspace : device, with amax at least nvfp4_layer_norm_workspace_bytes
- *              (rows, cols) bytes (0 for a single row), 4-byte aligned,
+ *              (rows, cols) bytes (0 for a few rows), 4-byte aligned,
  *              contents ignored and overwritten; calls that share one must
  *              not overlap in time.  Unused (may be NULL) without amax.
  * All sums are binary32, the variance a sum of squared differences from the
  * mean.  A row's non-finite values reach that row only.  Outputs must not
  * overlap inputs.  Deterministic.  Enqueues one kernel, two with amax (one for
- * a single row).  The workspace size is NVFP4_ERR_SHAPE for sizes that the
+ * a few rows).  The workspace size is NVFP4_ERR_SHAPE for sizes that the
  * call itself refuses.
  */
 int nvfp4_layer_norm(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void *weight,
@@ -410,8 +410,8 @@ int64_t nvfp4_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
  *  dweight,
  *  dbias     : either may be NULL; zeros when rows == 0.
  *  workspace : device, at least nvfp4_layer_norm_backward_workspace_bytes
- *              (rows, cols) bytes, 16-byte aligned, contents ignored and
- *              overwritten; calls that share one must not overlap in time.
+ *              (rows, cols) bytes (0 for a few rows, NULL then allowed),
+ *              16-byte aligned, contents ignored and overwritten; calls that share one must not overlap in time.
  * The sums over rows are binary32 partial sums of fixed sets of rows, added
  * in a fixed order: deterministic on one device.  The workspace size is
  * NVFP4_ERR_SHAPE for sizes that the call itself refuses.

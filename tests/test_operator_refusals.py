@@ -37,7 +37,7 @@ NORM = dict(x=FAKE, xd=1, rows=4, cols=64, ldx=64, w=FAKE, b=FAKE, wd=1, eps=1e-
     (dict(eps=math.inf), VALUE), (dict(x=None), NULL), (dict(y=None), NULL), (dict(mean=None), NULL),
     (dict(rstd=None), NULL), (dict(x=FAKE + 1), ALIGN), (dict(xd=0, x=FAKE + 2), ALIGN), (dict(w=FAKE + 1), ALIGN),
     (dict(amax=FAKE + 2), ALIGN), (dict(mean=FAKE + 2), ALIGN),
-    (dict(bytes=0), SHAPE), (dict(ws=None), NULL), (dict(ws=FAKE + 2), ALIGN)])
+    (dict(rows=9, bytes=0), SHAPE), (dict(rows=9, ws=None), NULL), (dict(ws=FAKE + 2), ALIGN)])
 def test_layer_norm(L, bad, status):
     assert _call(L.nvfp4_layer_norm, NORM, **bad) == status
 
@@ -49,9 +49,9 @@ BACK = dict(dy=FAKE, dyd=1, lddy=64, x=FAKE, xd=1, rows=4, cols=64, ldx=64, mean
 @_no_gpu
 @pytest.mark.parametrize("bad,status", [
     (dict(dyd=3), ENUM), (dict(xd=3), ENUM), (dict(wd=3), ENUM), (dict(gd=3), ENUM), (dict(cols=0), SHAPE),
-    (dict(rows=-1), SHAPE), (dict(lddy=1), SHAPE), (dict(ldx=1), SHAPE), (dict(lddx=1), SHAPE), (dict(bytes=0), SHAPE),
+    (dict(rows=-1), SHAPE), (dict(lddy=1), SHAPE), (dict(ldx=1), SHAPE), (dict(lddx=1), SHAPE), (dict(rows=1000, bytes=0), SHAPE),
     (dict(dy=None), NULL), (dict(x=None), NULL), (dict(mean=None), NULL), (dict(rstd=None), NULL),
-    (dict(dx=None), NULL), (dict(ws=None), NULL), (dict(ws=FAKE + 8), ALIGN), (dict(dw=FAKE + 2), ALIGN),
+    (dict(dx=None), NULL), (dict(rows=1000, ws=None), NULL), (dict(ws=FAKE + 8), ALIGN), (dict(dw=FAKE + 2), ALIGN),
     (dict(dx=FAKE + 1), ALIGN)])
 def test_layer_norm_backward(L, bad, status):
     assert _call(L.nvfp4_layer_norm_backward, BACK, **bad) == status
@@ -68,7 +68,7 @@ def test_workspace_sizes(L):
     assert L.nvfp4_layer_norm_workspace_bytes(-1, 64) == SHAPE
     assert L.nvfp4_layer_norm_workspace_bytes(4, 0) == SHAPE
     assert L.nvfp4_layer_norm_workspace_bytes(0, 64) == L.nvfp4_layer_norm_workspace_bytes(1, 64) == 0
-    assert L.nvfp4_layer_norm_workspace_bytes(4, 64) == 16
+    assert L.nvfp4_layer_norm_workspace_bytes(5, 64) == 20
     assert L.nvfp4_distill_topk_workspace_bytes(-1, 64) == SHAPE
     assert L.nvfp4_distill_topk_workspace_bytes(4, 0) == SHAPE
     assert L.nvfp4_distill_topk_workspace_bytes(4, 1 << 31) == SHAPE
