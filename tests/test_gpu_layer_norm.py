@@ -119,6 +119,20 @@ def test_mixed_types(xd, yd, wd, cols):
     _check_backward(x, dy, mean, rstd, w, grad_dtype=DT[wd])
 
 
+@pytest.mark.parametrize("xd,yd", [("bf16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("rows,cols", [(3, 8), (5, 9), (4, 77), (40, 515), (7, 2051), (9, 5003)])
+def test_mixed_types_odd_widths(xd, yd, rows, cols):
+    """Rows of both types that start and end anywhere."""
+    x, _, w, b = _inputs(rows, cols, DT[xd], DT[yd], rows + cols, pad=1, shift=1)
+    y, mean, rstd, amax = nv.nvfp4_layer_norm(x, w, b, out_dtype=DT[yd], amax=True)
+    want, _, _, bound = _ref_forward(x, w, b, 1e-5)
+    _check(y, want, bound, DT[yd], f"{xd} -> {yd} {rows}x{cols}")
+    assert amax.item() == y.float().abs().max().item()
+    dy = _matrix(torch.randn((rows, cols), generator=torch.Generator().manual_seed(8)), DT[yd], 3, 1)
+    _check_backward(x, dy, mean, rstd, w, grad_dtype=DT[xd])
+    _check_backward(x, dy, mean, rstd, None)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,cols,pad,shift", [(5, 40, 3, 1), (6, 1001, 5, 3), (3, 8191, 1, 0), (2, 17000, 7, 5)])
 def test_strides_and_alignment(dt, rows, cols, pad, shift):
