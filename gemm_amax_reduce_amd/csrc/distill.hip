@@ -442,7 +442,7 @@ void rows_of(const T *z, int64_t rows, int64_t V, int64_t ldz, const List &list,
       kernel<<<(unsigned)rows, threads, 0, stream>>>(z, ldz, V, list, tau, weight, loss, lse, dz, lddz, threads);
     };
     if (dz) launch(k_distill_row<T, VPT, true, o.value>);
-    else launch(k_distill_row<T, VPT, false, o.value>);
+    else if constexpr (VPT < 16) launch(k_distill_row<T, VPT, false, o.value>);      // (longer rows: see row_vectors)
   });
 }
 
