@@ -222,7 +222,9 @@ __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *
   const int row = lane & 15, quarter = lane >> 4;
   const int64_t t0 = (int64_t)blockIdx.y * kTokens;
   const int live = (int)min(tokens - t0, (int64_t)kTokens);
-  const int64_t kz = (int64_t)blockIdx.z * waves * (SW * kStepK);
+  // a range's own k begin at `own`; one that would have only 16 of them (half a
+  // lane's load, NVFP4) starts 16 before, and meets zeros there
+  const int64_t own = (int64_t)blockIdx.z * waves * (SW * kStepK), kz = MX ? own : min(own, K - 32);
   const int64_t k0 = kz + wave * (SW * kStepK);
   const int64_t tiles = (N + 15) / 16, step = gridDim.x;
 
@@ -314,6 +316,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *
   uint64_t sc_next = load_scales(clamp(first + step));
   {
     char *const turn = lds + wave * (SL * kTurnBytes);
+    const auto mine = [&](int64_t at) { return at < K && (MX || at >= own); };
     const auto slot = [&](int col, int i, int p) {
       return turn + (col >> 4) * kTurnBytes + i * 1024 + 16 * (4 * ((col & 15) ^ i) + (p ^ ((col & 15) >> 2)));
     };
@@ -337,8 +340,8 @@ __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int64_t at = k0 + s * kStepK + 32 * i + 8 * piece;
-          const u32x4_t v = *reinterpret_cast<const u32x4_a2 *>(xr + (at < K ? at : 0));
-          raw[s][i] = at < K ? v : (u32x4_t){0, 0, 0, 0};
+          const u32x4_t v = *reinterpret_cast<const u32x4_a2 *>(xr + (mine(at) ? at : 0));
+          raw[s][i] = mine(at) ? v : (u32x4_t){0, 0, 0, 0};
         }
 #pragma unroll
       for (int s = 0; s < SW; ++s) {
@@ -354,11 +357,11 @@ __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *
       f32x4_t raw[SW * kFull + 1][2];
       const auto fetch = [&](f32x4_t *v, int token, int s) {
         const int64_t at = k0 + s * kStepK + 8 * (lane & 15);
-        const X *from = x + (t0 + min(token, live - 1)) * ldx + (at < K ? at : 0);
+        const X *from = x + (t0 + min(token, live - 1)) * ldx + (mine(at) ? at : 0);
         const f32x4_t v0 = *reinterpret_cast<const f32x4_a4 *>(from);
         const f32x4_t v1 = *reinterpret_cast<const f32x4_a4 *>(from + 4);
-        v[0] = at < K ? v0 : (f32x4_t){0, 0, 0, 0};
-        v[1] = at < K ? v1 : (f32x4_t){0, 0, 0, 0};
+        v[0] = mine(at) ? v0 : (f32x4_t){0, 0, 0, 0};
+        v[1] = mine(at) ? v1 : (f32x4_t){0, 0, 0, 0};
       };
       const auto put = [&](const Parts &q, int token) {
 #pragma unroll
@@ -769,11 +772,8 @@ Cut cut_for(int64_t N, int64_t K, int64_t tokens, bool f32) {
   c.sw = c.sl == 1 ? 4 : 2;
   const int64_t slices = (K + c.sw * kStepK - 1) / (c.sw * kStepK);
   const int most = max_waves(c.sl);
-  for (c.ranges = (int)((slices + most - 1) / most);; ++c.ranges) {
-    c.waves = (int)((slices + c.ranges - 1) / c.ranges);
-    // the last range needs a lane's 32 k of its own
-    if (K - (int64_t)(c.ranges - 1) * c.waves * c.sw * kStepK >= 32) break;
-  }
+  c.ranges = (int)((slices + most - 1) / most);
+  c.waves = (int)((slices + c.ranges - 1) / c.ranges);       // (the last range has a slice at least: waves <= most)
   // one round of workgroups: as many as fit the CUs' waves, the tiles dealt evenly
   const int64_t tiles = (N + 15) / 16, blocks = (tokens + kTokens - 1) / kTokens;
   const int64_t room = (int64_t)device_cus() * (kTileWaves / (c.waves + has_helper(c.waves, c.sl)));
