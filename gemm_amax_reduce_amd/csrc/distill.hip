@@ -57,8 +57,9 @@ __device__ __forceinline__ float share_of(float z, float top_z, float scale, flo
 template <typename T> using Cols = Piece<sizeof(T) == 4>;
 template <typename T> __device__ __forceinline__ bool is_ragged(int64_t n) { return n & (sizeof(T) == 4 ? 3 : 7); }
 
-// The sum of 2^((v - m) scale) over 8 values, those of others left out.
-// All -inf (m = -inf) give 0, a NaN gives NaN.
+// The sum of 2^((v - m) scale) over 8 values, those of others left out; a NaN
+// gives NaN.  m is finite: with -inf, of values all masked, -inf - -inf would
+// be NaN.
 template <bool SPLIT>
 __device__ __forceinline__ float exp_sum8(const float *v, float m, float scale, const Piece<SPLIT> &p, bool ragged) {
   float e[8];
@@ -225,6 +226,7 @@ __global__ __launch_bounds__(kRowThreads) void k_distill_row(const T *z, int64_t
   __syncthreads();
   for (int w = 0; w < waves; ++w) m = fmaxf(m, part[0][w]);
   float s = 0.0f;
+  const float base = m > -INFINITY ? m : 0.0f;       // a row masked as a whole: its sum is 0
   vec.anew();
 #pragma unroll
   for (int j = 0; j < VPT; ++j) q[j].keep_packed();
@@ -232,7 +234,7 @@ __global__ __launch_bounds__(kRowThreads) void k_distill_row(const T *z, int64_t
   for (int j = 0; j < VPT; ++j) {
     float v[8];
     q[j].get(v);
-    s += exp_sum8(v, m, scale, vec[j], ragged);
+    s += exp_sum8(v, base, scale, vec[j], ragged);
   }
   s = block_sum(s, part[1], waves);
   const float l2 = __builtin_amdgcn_logf(s);

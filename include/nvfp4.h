@@ -470,7 +470,8 @@ int64_t nvfp4_matvec_workspace_bytes(int64_t n, int64_t k, int64_t tokens, int x
  *                one must not overlap in time.
  * A row without a valid entry has loss 0 and gradient 0 whatever its logits.
  * An index listed twice counts twice.  Logits of -infinity or of the type's
- * lowest value are ordinary (a vocabulary mask).
+ * lowest value are ordinary (a vocabulary mask); lse of a row of nothing but
+ * -infinity is -infinity.
  *
  * nvfp4_distill_topk_backward -- the gradient of sum_t dloss_t loss_t, from
  * the lse of the forward call:
