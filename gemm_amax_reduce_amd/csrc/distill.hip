@@ -265,17 +265,12 @@ __global__ __launch_bounds__(kRowThreads) void k_distill_row(const T *z, int64_t
   if (c != 0.0f) list_gradient(te, dr, list.top, 0, V, c, m, scale, l2, threads);
 }
 
-// Without a gradient, for few rows, or for rows that registers do not hold:
-// statistics of one segment of one row, kBatch vectors of a thread in flight
-// together.  A vector that passes the segment's end is moved back inside it.
+// Statistics of n logits by a workgroup of kDT threads, in every thread; kBatch
+// vectors of a thread in flight together.  A vector that passes the end is
+// moved back inside.  share: LDS.
 constexpr int kBatch = 4;
 template <typename T, bool ONCE>
-__global__ __launch_bounds__(kDT) void k_distill_stats(const T *z, int64_t ldz, int64_t V, int64_t seg_len,
-                                                       float scale, float2 *part) {
-  __shared__ float2 share[kDT / 64];
-  const int64_t row = blockIdx.y, seg = blockIdx.x;
-  const int64_t begin = seg * seg_len, n = min(V - begin, seg_len);
-  const T *zr = z + row * ldz + begin;
+__device__ __forceinline__ float2 span_stats(const T *zr, int64_t n, float scale, float2 *share) {
   float2 st = make_float2(-INFINITY, 0.0f);
   if (n < 8) {                       // less than a vector: an element a thread
     if ((int64_t)threadIdx.x < n) {
@@ -321,11 +316,28 @@ __global__ __launch_bounds__(kDT) void k_distill_stats(const T *z, int64_t ldz, 
     st = join(st, make_float2(__shfl_xor(st.x, off, 64), __shfl_xor(st.y, off, 64)), scale);
   if ((threadIdx.x & 63) == 0) share[threadIdx.x >> 6] = st;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kDT / 64; ++w) st = join(st, share[w], scale);
-    part[row * gridDim.x + seg] = st;
-  }
+  st = share[0];
+  for (int w = 1; w < kDT / 64; ++w) st = join(st, share[w], scale);
+  return st;
 }
+
+// Without a gradient, for few rows, or for rows that registers do not hold:
+// statistics of one segment of one row.
+template <typename T, bool ONCE>
+__global__ __launch_bounds__(kDT) void k_distill_stats(const T *z, int64_t ldz, int64_t V, int64_t seg_len,
+                                                       float scale, float2 *part) {
+  __shared__ float2 share[kDT / 64];
+  const int64_t row = blockIdx.y, seg = blockIdx.x;
+  const int64_t begin = seg * seg_len, n = min(V - begin, seg_len);
+  const float2 st = span_stats<T, ONCE>(z + row * ldz + begin, n, scale, share);
+  if (threadIdx.x == 0) part[row * gridDim.x + seg] = st;
+}
+
+// A saved log-sum-exp, rounded to binary32, leaves a share an error of
+// |lse| 2^-23 of itself: 2^-11 here.  From there on (a row that lies as a whole
+// at a mask's value, up to the type's lowest, whose lse may have overflowed)
+// the gradient's workgroups form the row's statistics anew.
+constexpr float kFarLse = 4096.0f;
 
 // Loss and log-sum-exp of a row from its segments' statistics (part != null),
 // and, with GRAD, the gradient of one segment.  Without part the log-sum-exp
@@ -361,6 +373,12 @@ __global__ __launch_bounds__(kDT) void k_distill_finish(const T *z, int64_t ldz,
   }
   if (!GRAD) return;
   const float c = some ? weight[row] * tau : 0.0f;
+  if (!part && c != 0.0f && fabsf(lse[row]) >= kFarLse) {
+    __shared__ float2 share[kDT / 64];
+    const float2 st = span_stats<T, false>(zr, V, scale, share);
+    top_z = st.x;
+    l2 = __builtin_amdgcn_logf(st.y);
+  }
   T *dr = dz + row * lddz;
   const int64_t begin = seg * seg_len, end = min(V, begin + seg_len), n = end - begin;
   const auto gradient = [&](Row8<T> &q) {

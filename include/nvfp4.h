@@ -478,7 +478,10 @@ int64_t nvfp4_matvec_workspace_bytes(int64_t n, int64_t k, int64_t tokens, int x
  *   dlogits_v = dloss temperature (exp(logits_v / temperature - lse) - sum_{k: i_k = v} p_k)
  *  dlogits : device, z_dtype, row-major [tokens][lddz]; must not overlap
  *            logits (NVFP4_ERR_SHAPE).
- *  Rows with dloss == 0 get zeros.
+ *  Rows with dloss == 0 get zeros.  lse in binary32 leaves the shares a
+ *  relative error of |lse| 2^-23; from |lse| = 4096 on (a row that lies as a
+ *  whole at a mask's value) the call reads such a row once more and forms its
+ *  log-sum-exp anew, also where lse has overflowed.
  *
  * nvfp4_distill_topk_step -- both in one call, for a program that knows its
  * rows' weights beforehand: loss and lse as above and dlogits with
