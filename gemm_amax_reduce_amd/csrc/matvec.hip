@@ -70,8 +70,10 @@ template <> struct Scale<true> {
   static constexpr int kPerByte = 32;
   uint32_t raw;
   __device__ __forceinline__ void load(const uint8_t *p) { raw = *p; }
-  // 2^(e - 127); e = 0 is the denormal 2^-127
-  __device__ __forceinline__ float lo() const { return __uint_as_float(raw ? raw << 23 : 0x00400000u); }
+  // 2^(e - 127); e = 0 is the denormal 2^-127 and e = 255 NaN (both by the next bit below the exponent's)
+  __device__ __forceinline__ float lo() const {
+    return __uint_as_float(raw << 23 | (raw - 1 < 254 ? 0u : 0x00400000u));
+  }
   __device__ __forceinline__ float hi() const { return lo(); }
 };
 

@@ -437,6 +437,7 @@ int64_t nvfp4_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
  *           x_dtype) bytes (for both formats), 16-byte aligned, contents
  *           ignored and overwritten; often 0, and NULL will do then.  Calls
  *           that share one must not overlap in time.
+ * An MXFP4 scale of 255 is E8M0's NaN and makes its row NaN.
  * Weights and bf16 x enter the product exactly; a float32 x to within
  * 2^-133 of its value.  Sums are binary32.  k == 0 gives zeros.
  * Deterministic on one device.  Enqueues one kernel, or two where there is a
