@@ -318,7 +318,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *
   uint64_t sc_next = load_scales(clamp(first + step));
   {
     char *const turn = lds + wave * (SL * kTurnBytes);
-    const auto mine = [&](int64_t at) { return at < K && (MX || at >= own); };
+    const auto mine = [&](int64_t at) { return (uint32_t)(at - own) < (uint32_t)(K - own); };
     const auto slot = [&](int col, int i, int p) {
       return turn + (col >> 4) * kTurnBytes + i * 1024 + 16 * (4 * ((col & 15) ^ i) + (p ^ ((col & 15) >> 2)));
     };
