@@ -22,8 +22,8 @@
 //    instructions per NVFP4 weight.
 //
 // A decoded weight q * S has at most 6 significant bits (2 of E2M1, 4 of
-// E4M3) and an exponent in bf16's range, so it is exact in bf16, and so is
-// bf16 x.  A float32 x is split into three bf16 parts, x = hi + mid + lo,
+// E4M3) and an exponent in bf16's range (MXFP4 at a quarter where its scales
+// are at their largest), so it is exact in bf16, and so is bf16 x.  A float32 x is split into three bf16 parts, x = hi + mid + lo,
 // each of 8 bits: exact for every value whose low part does not fall below
 // the bf16 range.  Products are exact in binary32 and added there; the
 // tensor scale g is applied once to the sum.
@@ -75,6 +75,13 @@ template <> struct Scale<true> {
     return __uint_as_float(raw << 23 | (raw - 1 < 254 ? 0u : 0x00400000u));
   }
   __device__ __forceinline__ float hi() const { return lo(); }
+  // From 253 on a weight, at most 6 times as large, may pass bf16's range.  A
+  // quarter of the scale, 2^-129 to 2^125, keeps all weights in it (the
+  // smallest as denormals, exact).
+  static constexpr uint32_t kFar = 253;
+  __device__ __forceinline__ float quarter() const {
+    return raw == 255 ? lo() : __builtin_amdgcn_ldexpf(1.0f, (int)raw - 129);
+  }
 };
 
 // 8 codes (one word) as 8 bf16: NVFP4 codes times the block scale s (exact
@@ -474,6 +481,15 @@ __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *
       if (MX) sc[s].raw = *reinterpret_cast<const uint8_t *>(at + o);
       else sc[s].raw = (uint32_t)*reinterpret_cast<const uint16_t *>(at + ((o + 1) & ~1u)) << (((half >> s) & 1) * 8);
     }
+    // MXFP4: weights of the scales from 2^126 on may pass bf16's range; where a
+    // wave holds one, its tile is decoded at a quarter
+    bool far = false;
+    if constexpr (MX) {
+      uint32_t top = sc[0].raw;
+#pragma unroll
+      for (int s = 1; s < SW; ++s) top = max(top, sc[s].raw);
+      far = __any(top >= Scale<MX>::kFar);
+    }
     if (!MX && f16) {
 #pragma unroll
       for (int s = 0; s < SW; ++s) {
@@ -486,6 +502,18 @@ __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *
             acc[j % kA][l] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, __builtin_bit_cast(half8_t, b[s][j][l]),
                                                                     acc[j % kA][l], 0, 0, 0);
         }
+      }
+    } else if (far) {
+      if constexpr (MX) {
+#pragma unroll
+        for (int s = 0; s < SW; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const bf16x8_t a = decode8<false>(c[s][j], sc[s].quarter());
+#pragma unroll
+            for (int l = 0; l < SL; ++l)
+              acc[j % kA][l] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[s][j][l], acc[j % kA][l], 0, 0, 0);
+          }
       }
     } else {
 #pragma unroll
@@ -502,9 +530,8 @@ __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *
 #pragma unroll
     for (int l = 0; l < SL; ++l) {
       f32x4_t v = kA == 2 ? acc[0][l] + acc[kA - 1][l] : acc[0][l];
-      if (!MX)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_ldexpf(v[i], move[l]);
+      for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_ldexpf(v[i], MX ? 2 * far : move[l]);
       mine[(wave * SL + l) * 64 + lane] = v;
     }
     put_scales(sc_next, turn + 1);

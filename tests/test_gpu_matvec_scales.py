@@ -1,6 +1,10 @@
-"""GPU checks of the MXFP4 matrix-vector products over E8M0's scale codes; 255
-is NaN.  Bounds as for any scales: products are exact in binary32 where they
-are normal numbers, the sum is within 1e-5 of the sum of magnitudes."""
+"""GPU checks of the MXFP4 matrix-vector products over every E8M0 scale code:
+0 (2^-127) to 254 (2^127), and 255, which is NaN.
+
+A weight is 2^(code - 127) times at most 6, so it may lie above bf16's and
+binary32's range; what counts is that its products with the activations do
+not.  Bounds as for any scales: products are exact in binary32 where they are
+normal numbers, the sum is within 1e-5 of the sum of magnitudes."""
 import numpy as np
 import pytest
 import torch
@@ -38,6 +42,30 @@ def _check(y, x, w, rows=slice(None)):
     want, mass = (xd @ w.T)[:, rows], (np.abs(xd) @ np.abs(w).T)[:, rows]
     assert mass.max() < 3e38, "the case itself overflows"
     assert np.all(np.abs(y.double().cpu().numpy()[:, rows] - want) <= 1e-5 * mass)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [32, 96, 128, 416, 1056, 6176])
+@pytest.mark.parametrize("lo,hi,scale", [(0, 3, 2.0 ** 60), (250, 254, 2.0 ** -40), (60, 254, 2.0 ** -40)])
+def test_whole_range_of_scales(lo, hi, scale, k, dt):
+    w, wd = _weights(k, lo, hi, k + lo)
+    for tokens in TOKENS:
+        print(f"[matvec] scales {lo}..{hi} {tokens}x{N}x{k} {dt}", flush=True)
+        x = _x(tokens, k, dt, scale)
+        _check(nv.mxfp4_matvec(w, x, out_dtype=torch.float32), x, wd)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [96, 1056])
+def test_smallest_beside_largest(k, dt):
+    """Rows of the smallest scales keep their digits beside a row of the
+    largest, whose own sums overflow here."""
+    w, wd = _weights(k, 0, 2, 5, [(9, b, 254) for b in range(k // 32)])
+    rows = [r for r in range(N) if r != 9]
+    wd[9] = 0.0
+    for tokens in TOKENS:
+        x = _x(tokens, k, dt, 2.0 ** 60)
+        _check(nv.mxfp4_matvec(w, x, out_dtype=torch.float32), x, wd, rows)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
