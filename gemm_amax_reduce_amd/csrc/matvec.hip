@@ -592,7 +592,7 @@ __global__ __launch_bounds__(256) void k_matvec_short(const uint8_t *codes, cons
       }
       sum = __builtin_fmaf(p, sc.lo(), sum);
     }
-    store_y(y, y_bf16, t * ldy + n, sum * g);
+    store_y(y, y_bf16, t * ldy + n, K > 0 ? sum * g : 0.0f);      // (g of no weights may be anything)
   }
 }
 constexpr int64_t kFlatGrid = 1 << 16;
