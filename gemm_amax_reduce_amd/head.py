@@ -25,13 +25,20 @@ from .linear import NVFP4Linear
 MATVEC_TOKENS = 16
 
 
+def _matrix(x: torch.Tensor) -> torch.Tensor:
+    """x, or a copy of it, as the kernels read a matrix: unit column stride,
+    rows that do not overlap (a transposed, expanded or windowed x is copied)."""
+    if x.dim() == 2 and (x.stride(1) != 1 or x.stride(0) < x.shape[1]):
+        return x.contiguous()
+    return x
+
+
 class LayerNormFunction(torch.autograd.Function):
     """y = layer norm of the rows of x [tokens, features], in x's dtype."""
 
     @staticmethod
     def forward(ctx, x, weight, bias, eps: float):
-        if x.dim() == 2 and x.stride(1) != 1:
-            x = x.contiguous()
+        x = _matrix(x)
         y, mean, rstd = nvfp4_layer_norm(x, weight, bias, eps=eps)
         ctx.save_for_backward(x, mean, rstd, weight)
         ctx.has_bias = bias is not None
@@ -53,8 +60,7 @@ class DistillTopKFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, logits, indices, teacher, temperature: float):
-        if logits.dim() == 2 and logits.stride(1) != 1:
-            logits = logits.contiguous()
+        logits = _matrix(logits)
         loss, lse = nvfp4_distill_topk(logits, indices, teacher, temperature=temperature)
         ctx.save_for_backward(logits, indices, teacher, lse)
         ctx.temperature = temperature
