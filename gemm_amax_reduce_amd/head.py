@@ -134,7 +134,7 @@ class NVFP4Head(torch.nn.Module):
         quantized with the maximum that the norm hands over and multiplied by
         the NVFP4 GEMM."""
         lead = x.shape[:-1]
-        rows = x.reshape(-1, x.shape[-1])
+        rows = _matrix(x.reshape(-1, x.shape[-1]))
         w, b, eps = self.norm.weight.detach(), self.norm.bias.detach(), self.norm.eps
         if rows.shape[0] <= MATVEC_TOKENS:
             h, _, _ = nvfp4_layer_norm(rows, w, b, eps=eps)

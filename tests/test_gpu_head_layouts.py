@@ -44,3 +44,13 @@ def test_loss(name):
     a, b = H.distill_topk_loss(got, idx, t), H.distill_topk_loss(want, idx, t)
     assert torch.equal(a, b)
     assert torch.equal(torch.autograd.grad(a, got)[0], torch.autograd.grad(b, want)[0])
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("rows", [1, 5, 16, 17, 48])
+def test_answer(rows, name):
+    torch.manual_seed(6)
+    head = H.NVFP4Head(64, 80, device="cuda", dtype=torch.float32)
+    packed = head.pack()
+    x = _layouts(rows, 64)[name]
+    assert torch.equal(head.answer(x, packed), head.answer(x.contiguous().clone(), packed))
