@@ -60,7 +60,7 @@ class DistillTopKFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, logits, indices, teacher, temperature: float):
-        logits = _matrix(logits)
+        logits, indices, teacher = _matrix(logits), indices.contiguous(), teacher.contiguous()
         loss, lse = nvfp4_distill_topk(logits, indices, teacher, temperature=temperature)
         ctx.save_for_backward(logits, indices, teacher, lse)
         ctx.temperature = temperature

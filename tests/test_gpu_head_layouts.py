@@ -54,3 +54,15 @@ def test_answer(rows, name):
     packed = head.pack()
     x = _layouts(rows, 64)[name]
     assert torch.equal(head.answer(x, packed), head.answer(x.contiguous().clone(), packed))
+
+
+def test_loss_of_shortened_lists():
+    """The best of longer lists, as slices of them, and lists by columns."""
+    z = torch.randn((6, 40), device="cuda", requires_grad=True)
+    best = torch.topk(torch.randn((6, 40), device="cuda"), 8, 1)
+    for idx, t in ((best.indices[:, :3], best.values[:, :3]),
+                   (best.indices.t().contiguous().t(), best.values.t().contiguous().t())):
+        a = H.distill_topk_loss(z, idx, t, temperature=2.0)
+        b = H.distill_topk_loss(z, idx.contiguous(), t.contiguous(), temperature=2.0)
+        assert torch.equal(a, b)
+        assert torch.equal(torch.autograd.grad(a, z)[0], torch.autograd.grad(b, z)[0])
