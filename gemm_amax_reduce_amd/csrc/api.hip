@@ -95,12 +95,19 @@ inline bool matrix_ok(int64_t rows, int64_t cols, int64_t ld) {
   return rows >= 0 && cols >= 0 && ld >= cols && count_ok(rows, ld);
 }
 
-// Do the used bytes of two matrices of the same shape and type meet?
-inline bool overlap(const void *a, int64_t lda, const void *b, int64_t ldb, int64_t rows, int64_t cols, int64_t size) {
-  if (rows <= 0 || cols <= 0) return false;
-  const uintptr_t a0 = (uintptr_t)a, a1 = a0 + (uintptr_t)(((rows - 1) * lda + cols) * size);
-  const uintptr_t b0 = (uintptr_t)b, b1 = b0 + (uintptr_t)(((rows - 1) * ldb + cols) * size);
-  return a0 < b1 && b0 < a1;
+// Do the used bytes of two matrices of `rows` rows meet?  pitch: bytes from
+// row to row, used: those of a row that are its own.  (Matrices of one pitch
+// may lie side by side, each in the other's gaps; of two pitches that meet
+// as a whole no two are told apart.)
+inline bool overlap(const void *a, int64_t pitch_a, int64_t used_a, const void *b, int64_t pitch_b, int64_t used_b,
+                    int64_t rows) {
+  if (rows <= 0 || used_a <= 0 || used_b <= 0) return false;
+  const uintptr_t a0 = (uintptr_t)a, a1 = a0 + (uintptr_t)((rows - 1) * pitch_a + used_a);
+  const uintptr_t b0 = (uintptr_t)b, b1 = b0 + (uintptr_t)((rows - 1) * pitch_b + used_b);
+  if (a0 >= b1 || b0 >= a1) return false;
+  if (rows == 1 || pitch_a != pitch_b) return true;
+  const int64_t d = ((int64_t)(b0 - a0) % pitch_a + pitch_a) % pitch_a;      // b's rows start there in a's
+  return d < used_a || d + used_b > pitch_a;
 }
 
 // The widest row layer norm takes (its column grids stay far inside 2^31).
@@ -435,7 +442,8 @@ int nvfp4_distill_topk_backward(const void *logits, int z_dtype, int64_t tokens,
   if (!matrix_ok(tokens, vocab, lddz)) return NVFP4_ERR_SHAPE;
   if (tokens > 0 && (!dloss || !dlogits)) return NVFP4_ERR_NULL;
   if (!aligned(dloss, 4) || !aligned(dlogits, dtype_size(z_dtype))) return NVFP4_ERR_ALIGN;
-  if (overlap(logits, ldz, dlogits, lddz, tokens, vocab, dtype_size(z_dtype))) return NVFP4_ERR_SHAPE;
+  const int64_t e = dtype_size(z_dtype);
+  if (overlap(logits, ldz * e, vocab * e, dlogits, lddz * e, vocab * e, tokens)) return NVFP4_ERR_SHAPE;
   return hip_status(nvfp4::launch_distill(logits, z_dtype, tokens, vocab, ldz, indices, index_bits == 64, teacher,
                                           t_dtype, (int)top, temperature, dloss, nullptr, const_cast<float *>(lse),
                                           dlogits, lddz, nullptr, false, (hipStream_t)hip_stream));
@@ -454,7 +462,8 @@ int nvfp4_distill_topk_step(const void *logits, int z_dtype, int64_t tokens, int
   if ((tokens > 0 && (!weight || !loss || !dlogits)) || (need > 0 && !workspace)) return NVFP4_ERR_NULL;
   if (!aligned(weight, 4) || !aligned(loss, 4) || !aligned(dlogits, dtype_size(z_dtype)) || !aligned(workspace, 16))
     return NVFP4_ERR_ALIGN;
-  if (overlap(logits, ldz, dlogits, lddz, tokens, vocab, dtype_size(z_dtype))) return NVFP4_ERR_SHAPE;
+  const int64_t e = dtype_size(z_dtype);
+  if (overlap(logits, ldz * e, vocab * e, dlogits, lddz * e, vocab * e, tokens)) return NVFP4_ERR_SHAPE;
   return hip_status(nvfp4::launch_distill(logits, z_dtype, tokens, vocab, ldz, indices, index_bits == 64, teacher,
                                           t_dtype, (int)top, temperature, weight, loss, lse, dlogits, lddz, workspace,
                                           true, (hipStream_t)hip_stream));

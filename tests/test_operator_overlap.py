@@ -1,0 +1,52 @@
+"""Outputs that meet inputs are refused; matrices that lie side by side in one
+buffer do not meet."""
+import ctypes
+
+import pytest
+import torch
+
+import gemm_amax_reduce_amd as nv
+
+_no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="fake-pointer argument tests run only without a GPU")
+SHAPE, HIP = -2, -4
+A = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def L():
+    return nv.lib()
+
+
+def _meets(a, lda, b, ldb, rows, cols):
+    """By the elements' addresses."""
+    at = lambda p, ld: {p + 2 * (r * ld + c) + i for r in range(rows) for c in range(cols) for i in (0, 1)}
+    return bool(at(a, lda) & at(b, ldb))
+
+
+@_no_gpu
+@pytest.mark.parametrize("rows", [1, 2, 3])
+def test_distillation(L, rows):
+    """Every shift of one matrix against another in the same rows; what does
+    not meet gets as far as the launch, which fails without a GPU."""
+    cols = 3
+    for ld in (3, 5, 6, 8):
+        for shift in range(-rows * ld - 2, rows * ld + 3):
+            b = A + 2 * shift
+            got = L.nvfp4_distill_topk_backward(A, 1, rows, cols, ld, None, 64, None, 1, 0, 1.0, 4 * A, 4 * A, b, ld,
+                                                None)
+            assert got == (SHAPE if _meets(A, ld, b, ld, rows, cols) else HIP), (ld, shift)
+
+
+@pytest.mark.gpu
+def test_distillation_beside_its_logits():
+    """Logits and gradient as the two halves of one buffer."""
+    buf = torch.full((6, 200), 7.0, device="cuda", dtype=torch.bfloat16)
+    buf[:, :90] = torch.randn((6, 90), device="cuda")
+    z, dz = buf[:, :90], buf[:, 100:190]
+    idx = torch.randint(0, 90, (6, 4), device="cuda")
+    t, weight = torch.randn((6, 4), device="cuda"), torch.rand(6, device="cuda")
+    want = nv.nvfp4_distill_topk_step(z.clone(), idx, t, weight)
+    got = nv.nvfp4_distill_topk_step(z, idx, t, weight, out=dz)
+    for p, q in zip(got, want):
+        assert torch.equal(p, q)
+    assert torch.all(buf[:, 90:100] == 7) and torch.all(buf[:, 190:] == 7)
