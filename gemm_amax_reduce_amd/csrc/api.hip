@@ -355,6 +355,8 @@ int nvfp4_layer_norm(const void *x, int x_dtype, int64_t rows, int64_t cols, int
   if (!aligned(x, dtype_size(x_dtype)) || !aligned(y, dtype_size(y_dtype)) || !aligned(weight, dtype_size(w_dtype)) ||
       !aligned(bias, dtype_size(w_dtype)) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(amax, 4) || !aligned(workspace, 4))
     return NVFP4_ERR_ALIGN;
+  const int64_t xs = dtype_size(x_dtype), ys = dtype_size(y_dtype);
+  if (overlap(x, ldx * xs, cols * xs, y, ldy * ys, cols * ys, rows)) return NVFP4_ERR_SHAPE;
   return hip_status(nvfp4::launch_layer_norm(x, x_dtype, rows, cols, ldx, weight, bias, w_dtype, eps, y, y_dtype, ldy,
                                              mean, rstd, amax, workspace, (hipStream_t)hip_stream));
 }
@@ -380,6 +382,10 @@ int nvfp4_layer_norm_backward(const void *dy, int dy_dtype, int64_t lddy, const 
       !aligned(weight, dtype_size(w_dtype)) || !aligned(dweight, dtype_size(g_dtype)) ||
       !aligned(dbias, dtype_size(g_dtype)) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(workspace, 16))
     return NVFP4_ERR_ALIGN;
+  const int64_t xs = dtype_size(x_dtype), ds = dtype_size(dy_dtype);
+  if (overlap(dy, lddy * ds, cols * ds, dx, lddx * xs, cols * xs, rows) ||
+      overlap(x, ldx * xs, cols * xs, dx, lddx * xs, cols * xs, rows))
+    return NVFP4_ERR_SHAPE;
   return hip_status(nvfp4::launch_layer_norm_backward(dy, dy_dtype, lddy, x, x_dtype, ldx, mean, rstd, weight, w_dtype,
                                                       dx, lddx, dweight, dbias, g_dtype, workspace, rows, cols,
                                                       (hipStream_t)hip_stream));

@@ -393,7 +393,8 @@ int mxfp8_gemm(const mxfp8_tensor *a, const mxfp8_tensor *b, void *c, int c_dtyp
  *              not overlap in time.  Unused (may be NULL) without amax.
  * All sums are binary32, the variance a sum of squared differences from the
  * mean.  A row's non-finite values reach that row only.  Outputs must not
- * overlap inputs.  Deterministic.  Enqueues one kernel, two with amax (one for
+ * overlap inputs (NVFP4_ERR_SHAPE for x and y; rows of both may lie side by
+ * side in one buffer).  Deterministic.  Enqueues one kernel, two with amax (one for
  * a few rows).  The workspace size is NVFP4_ERR_SHAPE for sizes that the
  * call itself refuses.
  */
@@ -407,6 +408,7 @@ int64_t nvfp4_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
  * a = dy weight and h = (x - mean) rstd,
  *   dx = rstd (a - sum(a) / cols - h sum(a h) / cols)     (x_dtype, [rows][lddx])
  *   dweight = sum over rows of dy h,  dbias = sum over rows of dy   (g_dtype, [cols])
+ *  dx        : must not overlap dy or x (NVFP4_ERR_SHAPE).
  *  dweight,
  *  dbias     : either may be NULL; zeros when rows == 0.
  *  workspace : device, at least nvfp4_layer_norm_backward_workspace_bytes

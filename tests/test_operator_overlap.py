@@ -50,3 +50,43 @@ def test_distillation_beside_its_logits():
     for p, q in zip(got, want):
         assert torch.equal(p, q)
     assert torch.all(buf[:, 90:100] == 7) and torch.all(buf[:, 190:] == 7)
+
+
+@_no_gpu
+@pytest.mark.parametrize("xd,yd", [(1, 1), (0, 1), (1, 0)])
+@pytest.mark.parametrize("rows", [1, 3])
+def test_layer_norm(L, rows, xd, yd):
+    """y against x, and the gradient dx (x's type) against dy (of type yd) and x."""
+    cols, size = 3, {0: 4, 1: 2}
+    far, ws = 4 * A, 8 * A
+    for ldx, ldy in ((3, 3), (8, 8), (8, 16), (16, 8)):
+        for shift in range(-4 * rows * 16, 4 * rows * 16 + 1, 4):
+            at = lambda p, ld, d: {p + size[d] * (r * ld + c) + i for r in range(rows) for c in range(cols)
+                                   for i in range(size[d])}
+            b = A + shift
+            fwd = L.nvfp4_layer_norm(A, xd, rows, cols, ldx, None, None, 0, 1e-5, b, yd, ldy, far, far, None, None, 0,
+                                     None)
+            # dx first against dy, then against x
+            back_dy = L.nvfp4_layer_norm_backward(b, yd, ldy, far, xd, rows, cols, cols, far, far, None, 0, A, ldx,
+                                                  None, None, 0, ws, 1 << 30, None)
+            back_x = L.nvfp4_layer_norm_backward(far, xd, cols, b, xd, rows, cols, ldy, far, far, None, 0, A, ldx, None,
+                                                 None, 0, ws, 1 << 30, None)
+            for got, d in ((fwd, yd), (back_dy, yd), (back_x, xd)):
+                meets = bool(at(A, ldx, xd) & at(b, ldy, d))
+                if meets or ldx * size[xd] == ldy * size[d]:
+                    assert got == (SHAPE if meets else HIP), (ldx, ldy, shift)
+                else:                            # of two pitches: refused where the whole ranges meet
+                    assert got in (SHAPE, HIP)
+
+
+@pytest.mark.gpu
+def test_layer_norm_refuses_its_input():
+    x = torch.randn((6, 64), device="cuda")
+    for out in (x, x.view(12, 32)[:6].view(3, 64)):
+        with pytest.raises(nv.NVFP4Error, match="shape"):
+            nv.nvfp4_layer_norm(x[:out.shape[0]], out=out)
+    buf = torch.full((6, 200), 7.0, device="cuda")
+    buf[:, :90] = torch.randn((6, 90), device="cuda")
+    want = nv.nvfp4_layer_norm(buf[:, :90].clone())[0]
+    assert torch.equal(nv.nvfp4_layer_norm(buf[:, :90], out=buf[:, 100:190])[0], want)
+    assert torch.all(buf[:, 90:100] == 7) and torch.all(buf[:, 190:] == 7)
