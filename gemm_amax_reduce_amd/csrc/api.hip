@@ -132,6 +132,8 @@ int matvec_common(bool mx, const uint8_t *codes, const uint8_t *scales, const fl
   if (need > 0 && !workspace) return NVFP4_ERR_NULL;
   if (!aligned(x, dtype_size(x_dtype)) || !aligned(y, dtype_size(y_dtype)) || !aligned(workspace, 16))
     return NVFP4_ERR_ALIGN;
+  const int64_t xs = dtype_size(x_dtype), ys = dtype_size(y_dtype);
+  if (overlap(x, ldx * xs, K * xs, y, ldy * ys, N * ys, tokens)) return NVFP4_ERR_SHAPE;
   return hip_status(nvfp4::launch_matvec(mx, codes, scales, meta, N, K, x, x_dtype, tokens, ldx, y, y_dtype, ldy,
                                          workspace, (hipStream_t)hip_stream));
 }

@@ -432,7 +432,8 @@ int64_t nvfp4_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
  *  w      : the weights [outer = N][k], quantized on axis 1 (W [out, in]).
  *  x      : device, row-major [tokens][ldx], x_dtype, ldx >= k, aligned to
  *           its element only.
- *  y      : device, row-major [tokens][ldy], y_dtype, ldy >= N.
+ *  y      : device, row-major [tokens][ldy], y_dtype, ldy >= N; must not
+ *           overlap x (NVFP4_ERR_SHAPE; their rows may lie side by side).
  *  tokens : made for 1 to 16 (the weights are read once for every 16);
  *           at most 1 048 560.  N <= 16 * INT32_MAX, k <= 2^25 - 16.
  *  workspace : device, at least nvfp4_matvec_workspace_bytes(N, k, tokens,

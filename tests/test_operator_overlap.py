@@ -90,3 +90,31 @@ def test_layer_norm_refuses_its_input():
     want = nv.nvfp4_layer_norm(buf[:, :90].clone())[0]
     assert torch.equal(nv.nvfp4_layer_norm(buf[:, :90], out=buf[:, 100:190])[0], want)
     assert torch.all(buf[:, 90:100] == 7) and torch.all(buf[:, 190:] == 7)
+
+
+@_no_gpu
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("tokens", [1, 3])
+def test_matvec(L, mx, tokens):
+    """y (f32, N = 5) against x (bf16, K = 32)."""
+    n, k, far = 5, 32, 4 * A
+    w = nv._MXTensor(far, far, n, k) if mx else nv._CTensor(far, far, far, n, k)
+    fn = L.mxfp4_matvec if mx else L.nvfp4_matvec
+    for ldx, ldy in ((32, 16), (48, 24), (64, 32)):
+        at = lambda p, ld, size, cols: {p + size * r * ld + i for r in range(tokens) for i in range(size * cols)}
+        for shift in range(-256, 257, 4):
+            y = A + shift
+            meets = bool(at(A, ldx, 2, k) & at(y, ldy, 4, n))
+            got = fn(ctypes.byref(w), A, 1, tokens, ldx, y, 0, ldy, None, 0, None)
+            assert got == (SHAPE if meets else HIP), (ldx, shift)
+
+
+@pytest.mark.gpu
+def test_matvec_refuses_its_input():
+    x = torch.randn((4, 64), device="cuda")
+    w = nv.nvfp4_quantize(torch.randn((64, 64), device="cuda"))
+    with pytest.raises(nv.NVFP4Error, match="shape"):
+        nv.nvfp4_matvec(w, x, out=x)
+    buf = torch.cat([x, torch.zeros_like(x)], 1)
+    want = nv.nvfp4_matvec(w, x)
+    assert torch.equal(nv.nvfp4_matvec(w, buf[:, :64], out=buf[:, 64:]), want) and torch.equal(buf[:, :64], x)
