@@ -602,6 +602,8 @@ def _on(device: torch.device, stream):
     """The context that makes `device` and `stream` current; nothing to do
     (and nothing to pay) where they are already."""
     if stream is not None:
+        if stream.device != device:
+            raise NVFP4Error(f"stream of {stream.device}, tensors on {device}")
         return torch.cuda.stream(stream)
     return _here if _current_device() == device.index else torch.cuda.device(device)
 
