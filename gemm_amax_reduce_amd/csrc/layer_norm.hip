@@ -448,14 +448,14 @@ __global__ __launch_bounds__(256) void k_ln_backward_cols(const D *dy, int64_t l
 }
 
 // Backward, last kernel: dw and db from the partial rows, in a fixed order:
-// 64 columns per workgroup (of the 2 cols that dw and db make together), 16
-// interleaved shares of the rows, added at the end.
+// 64 columns per workgroup (from `first` on, of the 2 cols that dw and db make
+// together), 16 interleaved shares of the rows, added at the end.
 constexpr int kShares = 16;
 __global__ __launch_bounds__(64 * kShares) void k_ln_backward_sum(const float *partial, int64_t parts, int64_t cols,
-                                                                  void *dw, void *db, int g_bf16) {
+                                                                  int64_t first, void *dw, void *db, int g_bf16) {
   __shared__ float share[kShares][64];
   const int lane = threadIdx.x & 63, group = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  const int64_t c = first + (int64_t)blockIdx.x * 64 + lane;
   float s = 0.0f;
   if (c < 2 * cols) {
     const float *p = partial + c;
@@ -599,9 +599,13 @@ void backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, const fl
     k_ln_backward_cols<X, D><<<dim3((unsigned)((cols + 2047) / 2048), (unsigned)c.parts), 256, 0, stream>>>(
         dp, lddy, xp, ldx, mean, rstd, w, w_bf16, sums, op, lddx, partial, rows, cols);
   }
-  if ((dw || db) && !(rows > 0 && c.vpt && c.parts == 1))
-    k_ln_backward_sum<<<(unsigned)((2 * cols + 63) / 64), 64 * kShares, 0, stream>>>(partial, c.parts, cols, dw, db,
-                                                                                    g_bf16);
+  if ((dw || db) && !(rows > 0 && c.vpt && c.parts == 1)) {
+    // a grid's threads are counted in 32 bits
+    constexpr int64_t kMost = (int64_t)64 << 21;
+    for (int64_t first = 0; first < 2 * cols; first += kMost)
+      k_ln_backward_sum<<<(unsigned)((std::min(2 * cols - first, kMost) + 63) / 64), 64 * kShares, 0, stream>>>(
+          partial, c.parts, cols, first, dw, db, g_bf16);
+  }
 }
 
 }  // namespace
