@@ -84,6 +84,11 @@ struct Teacher {
 struct List {
   const void *idx, *t;
   int idx64, t_bf16, top;
+  // the lists of the rows from `row` on
+  List from(int64_t row) const {
+    return {(const char *)idx + row * top * (idx64 ? 8 : 4), (const char *)t + row * top * (t_bf16 ? 2 : 4), idx64,
+            t_bf16, top};
+  }
   __device__ __forceinline__ int64_t index(int64_t row, int k) const {
     const int64_t e = row * top + k;
     return idx64 ? ((const int64_t *)idx)[e] : (int64_t)((const int32_t *)idx)[e];
@@ -459,7 +464,12 @@ void rows_of(const T *z, int64_t rows, int64_t V, int64_t ldz, const List &list,
   const bool once = reads_once(2 * rows * V * (int64_t)sizeof(T));
   with_flag(once, [&](auto o) {
     const auto launch = [&](auto kernel) {
-      kernel<<<(unsigned)rows, threads, 0, stream>>>(z, ldz, V, list, tau, weight, loss, lse, dz, lddz, threads);
+      // a grid's threads are counted in 32 bits
+      constexpr int64_t kMost = 1 << 21;
+      for (int64_t r = 0; r < rows; r += kMost)
+        kernel<<<(unsigned)std::min(rows - r, kMost), threads, 0, stream>>>(
+            z + r * ldz, ldz, V, list.from(r), tau, dz ? weight + r : nullptr, loss + r, lse + r,
+            dz ? dz + r * lddz : nullptr, lddz, threads);
     };
     if (dz) launch(k_distill_row<T, VPT, true, o.value>);
     else if constexpr (VPT < 16) launch(k_distill_row<T, VPT, false, o.value>);      // (longer rows: see row_vectors)
@@ -483,9 +493,7 @@ void run(const void *zv, int64_t rows, int64_t V, int64_t ldz, List list, float 
   for (int64_t r = 0; r < rows; r += 65535) {
     const unsigned n = (unsigned)std::min<int64_t>(65535, rows - r);
     const T *zr = z + r * ldz;
-    List lr = list;
-    lr.idx = (const char *)list.idx + r * list.top * (list.idx64 ? 8 : 4);
-    lr.t = (const char *)list.t + r * list.top * (list.t_bf16 ? 2 : 4);
+    const List lr = list.from(r);
     float2 *pr = part ? part + r * sp.segments : nullptr;
     with_flag(once, [&](auto o) {
       if (stats)

@@ -1,5 +1,5 @@
 """GPU checks of sizes whose launches pass 2^32 threads: long rows in the last
-kernel of the layer norm's backward pass."""
+kernel of the layer norm's backward pass, many short rows in distillation."""
 import pytest
 import torch
 
@@ -38,3 +38,23 @@ def test_layer_norm_backward_of_long_rows():
         want = r * (a - s1 - h * s2)
         bound = r * (off * (1 + h.abs()) + 8 * U * (a.abs() + s1.abs() + (h * s2).abs()))
         assert torch.all((dx[:, s].double() - want).abs() <= bound + 2.0 ** -8 * (want.abs() + bound))
+
+
+def test_distillation_of_many_short_rows():
+    """2^26 + 64 rows of 8 logits: every 64 rows are the same ones."""
+    block, tokens = 64, 2 ** 26 + 64
+    g = torch.Generator(device="cuda").manual_seed(2)
+    z = (3 * torch.randn((block, 8), device="cuda", generator=g)).to(torch.bfloat16)
+    idx = torch.randint(-1, 8, (block, 2), device="cuda", generator=g, dtype=torch.int32)
+    t = torch.randn((block, 2), device="cuda", generator=g).to(torch.bfloat16)
+    weight = torch.rand(block, device="cuda", generator=g)
+    want = nv.nvfp4_distill_topk_step(z, idx, t, weight)
+    times = tokens // block
+    z, idx, t, weight = z.repeat(times, 1), idx.repeat(times, 1), t.repeat(times, 1), weight.repeat(times)
+    print(f"[distill] {tokens}x8", flush=True)
+    step = nv.nvfp4_distill_topk_step(z, idx, t, weight)
+    loss, lse = nv.nvfp4_distill_topk(z, idx, t)
+    for got, one in ((step[0], want[0]), (step[1], want[1]), (loss, want[0]), (lse, want[1])):
+        assert torch.all(got.view(times, block) == one)
+    for part in step[2].view(times, block, 8).split(2 ** 16):
+        assert torch.all(part == want[2])
