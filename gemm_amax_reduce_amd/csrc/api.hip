@@ -4,6 +4,7 @@
 #include "nvfp4.h"
 #include "nvfp4_kernels.h"
 
+#include <float.h>
 #include <stdint.h>
 
 namespace {
@@ -144,7 +145,7 @@ int check_distill(const void *z, int z_dtype, int64_t tokens, int64_t vocab, int
   if (!dtype_ok(z_dtype) || !dtype_ok(t_dtype) || (index_bits != 32 && index_bits != 64)) return NVFP4_ERR_ENUM;
   if (vocab < 1 || vocab > kMaxVocab || !matrix_ok(tokens, vocab, ldz)) return NVFP4_ERR_SHAPE;
   if (top < 0 || top > nvfp4::distill_max_top() || !count_ok(tokens, top)) return NVFP4_ERR_SHAPE;
-  if (!(tau > 0.0f) || tau > 3.0e38f) return NVFP4_ERR_VALUE;
+  if (!(tau >= FLT_MIN) || tau > 3.0e38f) return NVFP4_ERR_VALUE;      // (log2(e) / tau stays finite)
   if (tokens > 0 && (!z || !lse || (top > 0 && (!indices || !teacher)))) return NVFP4_ERR_NULL;
   if (!aligned(z, dtype_size(z_dtype)) || !aligned(teacher, dtype_size(t_dtype)) || !aligned(lse, 4) ||
       !aligned(indices, index_bits / 8))

@@ -466,7 +466,7 @@ int64_t nvfp4_matvec_workspace_bytes(int64_t n, int64_t k, int64_t tokens, int x
  *            in [0, vocab) and its teacher logit is above -infinity; shorter
  *            lists are filled up with -1.  0 <= top <= 1024.
  *  teacher : device, t_dtype [tokens][top].
- *  temperature : > 0 and finite (NVFP4_ERR_VALUE otherwise).
+ *  temperature : at least 2^-126 and finite (NVFP4_ERR_VALUE otherwise).
  *  loss, lse   : device, f32 [tokens].
  *  workspace   : device, nvfp4_distill_topk_workspace_bytes(tokens, vocab)
  *                bytes, 16-byte aligned, contents ignored and overwritten;
