@@ -16,8 +16,10 @@
 //    one per product.
 //  * k_matvec_tile, more tokens: tiles of 16 weight rows on the 16x16x32
 //    bf16 MFMA with the weights as the A operand and up to 16 tokens as the
-//    B operand, so 1 to 16 tokens cost the same.  A lane's 32 k enter four
-//    MFMAs; the k order of an MFMA is free as long as both operands agree.
+//    B operand, so 1 to 16 bf16 tokens cost the same (f32 tokens take three
+//    columns each: one slab of 16 up to 5 of them, two up to 10, three up to
+//    16).  A lane's 32 k enter four MFMAs; the k order of an MFMA is free as
+//    long as both operands agree.
 //    The block scale has to be multiplied into every weight here, about two
 //    instructions per NVFP4 weight.
 //
@@ -32,8 +34,8 @@
 // rows, one bf16 token, NVFP4 5120 x 5120 5.4 us (2.7 TB/s: 2.3 us of reading
 // behind a start of 3), 20480 x 5120 12.5 us (4.7 TB/s), 131075 x 5120 61 us
 // (6.2 TB/s); tiles, 8 bf16 tokens, 20480 x 5120 18 us, 131075 x 5120 74.6 us
-// (5.1 TB/s), 5 f32 tokens of MXFP4 5120 x 20480 17.9 us and 4 us for joining
-// the ranges of K; 8 f32 tokens of NVFP4 131075 x 5120, in two slabs of columns, 114.
+// (5.1 TB/s), 5 f32 tokens of MXFP4 5120 x 20480 17.0 us and 3.9 us for joining
+// the ranges of K; 8 f32 tokens of NVFP4 131075 x 5120, in two slabs of columns, 111.
 #include "gemm_common.h"
 #include "nvfp4_device.h"
 #include "nvfp4_kernels.h"
@@ -865,6 +867,10 @@ template <bool MX, int J, int WK, int R, int T, typename X> void rows(const Prod
 // 10.3 / 10.3, 20480 x 2048 8.6 9.3 11.9 / 12.9, 10000 x 8192 13.9 16.0 18.4
 // / 17.8, 20480 x 5120 18.6 22.6 27.1 / 17.4; in f32 5120 x 2048 6.3 7.3 8.9
 // / 10.5, 5120 x 5120 9.3 11.2 15.3 / 12.5, 20480 x 5120 23.6 30.0 41.2 / 19.5.
+// The limits lie between these sizes, one for 2 and 3 tokens of both types, and
+// are not the break-evens themselves: 3 bf16 tokens of 10000 x 8192 go by tiles
+// (17.8 against 16.0), and 2 or 3 f32 tokens go by rows up to 1e8 and 6.7e7
+// weights where by the lines between the f32 figures tiles lead from some 6e7 and 3.5e7 on.
 bool by_rows(int64_t N, int64_t K, int64_t tokens, bool f32) {
   if (K < kShortK) return false;
   if (tokens == 1) return K <= 12 * kWaveK;
