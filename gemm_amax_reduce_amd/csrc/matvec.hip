@@ -25,17 +25,20 @@
 //
 // A decoded weight q * S has at most 6 significant bits (2 of E2M1, 4 of
 // E4M3) and an exponent in bf16's range (MXFP4 at a quarter where its scales
-// are at their largest), so it is exact in bf16, and so is bf16 x.  A float32 x is split into three bf16 parts, x = hi + mid + lo,
-// each of 8 bits: exact for every value whose low part does not fall below
-// the bf16 range.  Products are exact in binary32 and added there; the
-// tensor scale g is applied once to the sum.
+// are at their largest), so it is exact in bf16, and so is bf16 x.  A float32
+// x is split into three bf16 parts, x = hi + mid + lo, each of 8 bits: exact
+// for every value whose low part does not fall below the bf16 range.  Products
+// are exact in binary32 and added there; the tensor scale g is applied once to
+// the sum.
 //
-// Measured on one MI355X, kernels alone, with weights that no cache holds:
-// rows, one bf16 token, NVFP4 5120 x 5120 5.4 us (2.7 TB/s: 2.3 us of reading
-// behind a start of 3), 20480 x 5120 12.5 us (4.7 TB/s), 131075 x 5120 61 us
-// (6.2 TB/s); tiles, 8 bf16 tokens, 20480 x 5120 18 us, 131075 x 5120 74.6 us
-// (5.1 TB/s), 5 f32 tokens of MXFP4 5120 x 20480 17.0 us and 3.9 us for joining
-// the ranges of K; 8 f32 tokens of NVFP4 131075 x 5120, in two slabs of columns, 111.
+// Measured on one MI355X, kernels alone, two sets of weights in turn: rows, one
+// bf16 token, NVFP4 5120 x 5120 5.4 us (2.7 TB/s: 2.3 us of reading behind a
+// start of 3), 20480 x 5120 12.6 us (4.7 TB/s); tiles, 8 bf16 tokens, 131075 x
+// 5120 73.9 us (5.1 TB/s), 5 f32 tokens of MXFP4 5120 x 20480 17.0 us and 3.9
+// us for joining the ranges of K.  Whole calls with weights that no cache
+// holds: one bf16 token 20480 x 5120 12.8 us, MXFP4 13.4, 131075 x 5120 58.2
+// (6.5 TB/s) and 59.1; 8 bf16 tokens 20480 x 5120 17.3; f32, NVFP4, 16 tokens
+// 20480 x 5120 (three slabs) 29.6, 8 tokens 131075 x 5120 (two slabs) 111.
 #include "gemm_common.h"
 #include "nvfp4_device.h"
 #include "nvfp4_kernels.h"
