@@ -111,7 +111,8 @@ inline bool overlap(const void *a, int64_t pitch_a, int64_t used_a, const void *
   return d < used_a || d + used_b > pitch_a;
 }
 
-// The widest row layer norm takes (its column grids stay far inside 2^31).
+// The widest row layer norm takes (grids over its columns stay far inside 2^31
+// workgroups, and are launched in parts where their threads would pass 2^32).
 constexpr int64_t kMaxNormCols = 1LL << 31;
 // The matvec puts at least 16 weight rows on the grid's x dimension and 16
 // tokens on its y dimension; its offsets inside 64 weight rows are 32-bit,
