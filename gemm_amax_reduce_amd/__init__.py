@@ -20,7 +20,8 @@ __all__ = ["NVFP4Tensor", "NVFP4Error", "nvfp4_quantize", "nvfp4_rht_quantize", 
            "nvfp4_quantize_amax", "MXFP4Tensor", "mxfp4_quantize", "mxfp4_gemm", "MXFP8Tensor", "mxfp8_quantize",
            "mxfp8_gemm",
            "nvfp4_dequantize", "nvfp4_gemm", "nvfp4_gemm_ws", "nvfp4_gemm_noalloc", "gemm_workspace",
-           "nvfp4_layer_norm", "nvfp4_layer_norm_backward", "nvfp4_matvec", "mxfp4_matvec", "nvfp4_distill_topk",
+           "nvfp4_layer_norm", "nvfp4_layer_norm_backward", "nvfp4_rms_norm", "mxfp8_rms_norm",
+           "nvfp4_rms_norm_backward", "nvfp4_matvec", "mxfp4_matvec", "nvfp4_distill_topk",
            "nvfp4_distill_topk_backward", "nvfp4_distill_topk_step",
            "lib", "LIB_PATH", "F32", "BF16", "RNE", "SR"]
 
@@ -51,7 +52,9 @@ _lib = None
 EXPORTS = ("nvfp4_quantize", "nvfp4_rht_quantize", "nvfp4_amax", "nvfp4_quantize_amax", "nvfp4_quantize_dual",
            "mxfp4_quantize", "mxfp4_gemm", "nvfp4_dequantize", "nvfp4_gemm", "nvfp4_gemm_ws",
            "nvfp4_gemm_workspace_bytes", "nvfp4_gemm_noalloc", "mxfp8_quantize", "mxfp8_gemm", "nvfp4_layer_norm",
-           "nvfp4_layer_norm_workspace_bytes", "nvfp4_layer_norm_backward", "nvfp4_layer_norm_backward_workspace_bytes", "nvfp4_matvec", "mxfp4_matvec",
+           "nvfp4_layer_norm_workspace_bytes", "nvfp4_layer_norm_backward", "nvfp4_layer_norm_backward_workspace_bytes",
+           "nvfp4_rms_norm", "mxfp8_rms_norm", "nvfp4_rms_norm_backward", "nvfp4_rms_norm_backward_workspace_bytes",
+           "nvfp4_matvec", "mxfp4_matvec",
            "nvfp4_matvec_workspace_bytes", "nvfp4_distill_topk", "nvfp4_distill_topk_backward",
            "nvfp4_distill_topk_step", "nvfp4_distill_topk_workspace_bytes", "nvfp4_probe_mfma", "nvfp4_probe_philox", "nvfp4_status_string")
 
@@ -106,6 +109,16 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_layer_norm_backward.restype = ci
         L.nvfp4_layer_norm_backward_workspace_bytes.argtypes = [i64, i64]
         L.nvfp4_layer_norm_backward_workspace_bytes.restype = i64
+        rms = [vp, ci, i64, i64, i64, vp, ci, i64, vp, i64, vp, ci, cf]      # x, residual, h, weight, eps
+        L.nvfp4_rms_norm.argtypes = rms + [vp, ci, i64, vp, vp]
+        L.nvfp4_rms_norm.restype = ci
+        L.mxfp8_rms_norm.argtypes = rms + [mt, vp, vp]
+        L.mxfp8_rms_norm.restype = ci
+        L.nvfp4_rms_norm_backward.argtypes = [vp, ci, i64, vp, ci, i64, i64, i64, vp, vp, ci, vp, i64, vp, i64, vp, ci,
+                                              vp, i64, vp]
+        L.nvfp4_rms_norm_backward.restype = ci
+        L.nvfp4_rms_norm_backward_workspace_bytes.argtypes = [i64, i64]
+        L.nvfp4_rms_norm_backward_workspace_bytes.restype = i64
         L.nvfp4_matvec.argtypes = [pt, vp, ci, i64, i64, vp, ci, i64, vp, i64, vp]
         L.nvfp4_matvec.restype = ci
         L.mxfp4_matvec.argtypes = [mt, vp, ci, i64, i64, vp, ci, i64, vp, i64, vp]
@@ -719,6 +732,107 @@ def nvfp4_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Ten
                                                _ptr(ws), need, _current_handle(dev)),
                "nvfp4_layer_norm_backward")
     return dx, dweight, dbias
+
+
+def _rms_args(x, weight, residual, residual_out):
+    """Checks what the two RMS norm calls share; returns (x's device, h or
+    None, the leading C arguments up to the weight's dtype, h's place in
+    them).  h is made by the caller's stream where it is not given."""
+    ldx = _require_matrix(x, "x")
+    dev = x.device
+    rows, cols = x.shape
+    wp, wcode = _param(weight, "weight", cols, dev)
+    if residual is None:
+        if residual_out is not None:
+            raise NVFP4Error("residual_out needs a residual")
+        return dev, None, [x.data_ptr(), _dtype_code(x), rows, cols, ldx, None, F32, max(cols, 1), None, max(cols, 1),
+                           wp, wcode]
+    ldr = _require_matrix(residual, "residual", dev, (rows, cols))
+    rcode = _dtype_code(residual)
+    if residual_out is None:
+        h, ldh = residual.new_empty((rows, cols)), max(cols, 1)
+    else:
+        h, ldh = residual_out, _require_matrix_out(residual_out, rows, cols, residual.dtype, dev)
+    return dev, h, [x.data_ptr(), _dtype_code(x), rows, cols, ldx, residual.data_ptr(), rcode, ldr, h.data_ptr(), ldh,
+                    wp, wcode]
+
+
+def _stream_device(x, stream):
+    """_on for the device of an input that is yet to be checked."""
+    return _on(x.device, stream) if isinstance(x, torch.Tensor) and x.is_cuda else _here
+
+
+def nvfp4_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                   eps: float = 1e-6, out_dtype=None, out: torch.Tensor | None = None,
+                   residual_out: torch.Tensor | None = None, stream=None):
+    """RMS norm of the rows of x [rows, cols] (f32/bf16), or of the sum
+    h = x + residual: (y, rstd), with a residual (y, rstd, h).  y in
+    `out_dtype` (x's by default), rstd f32 [rows], h in the residual's dtype,
+    new or in `residual_out`, which may be the residual (see include/nvfp4.h)."""
+    with _stream_device(x, stream):
+        dev, h, args = _rms_args(x, weight, residual, residual_out)
+        rows, cols = x.shape
+        out_dtype = x.dtype if out_dtype is None else out_dtype
+        ycode = _out_code(out_dtype)
+        if out is None:
+            y, ldy = torch.empty((rows, cols), dtype=out_dtype, device=dev), max(cols, 1)
+        else:
+            y, ldy = out, _require_matrix_out(out, rows, cols, out_dtype, dev)
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        _check(lib().nvfp4_rms_norm(*args, eps, y.data_ptr(), ycode, ldy, rstd.data_ptr(), _current_handle(dev)),
+               "nvfp4_rms_norm")
+    return (y, rstd) if h is None else (y, rstd, h)
+
+
+def mxfp8_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                   eps: float = 1e-6, out: "MXFP8Tensor | None" = None, residual_out: torch.Tensor | None = None,
+                   stream=None):
+    """nvfp4_rms_norm with y in MXFP8 on axis 1 (cols a multiple of 32)."""
+    with _stream_device(x, stream):
+        dev, h, args = _rms_args(x, weight, residual, residual_out)
+        rows, cols = x.shape
+        if cols % 32:
+            raise NVFP4Error(f"MXFP8 needs a multiple of 32 columns, got {cols}")
+        if out is None:
+            out = MXFP8Tensor.empty(rows, cols, device=dev)
+        _same_device(out, x)
+        ct = out._c()
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        _check(lib().mxfp8_rms_norm(*args, eps, ctypes.byref(ct), rstd.data_ptr(), _current_handle(dev)),
+               "mxfp8_rms_norm")
+    return (out, rstd) if h is None else (out, rstd, h)
+
+
+def nvfp4_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor | None = None,
+                            dh: torch.Tensor | None = None, grad_dtype=torch.float32, stream=None):
+    """The gradients of nvfp4_rms_norm: (dx in h's dtype, dweight [cols] in
+    `grad_dtype`).  h is what was normed (x itself without a residual), dh the
+    gradient that reaches it from the residual stream; dx is the gradient of
+    x and of the residual alike."""
+    ldh = _require_matrix(h, "h")
+    dev = h.device
+    rows, cols = h.shape
+    lddy = _require_matrix(dy, "dy", dev, (rows, cols))
+    rp = _vector(rstd, "rstd", torch.float32, rows, dev)
+    wp, wcode = _param(weight, "weight", cols, dev)
+    lddh = max(cols, 1)
+    if dh is not None:
+        lddh = _require_matrix(dh, "dh", dev, (rows, cols))
+        if dh.dtype != h.dtype:
+            raise NVFP4Error(f"dh must have h's dtype {h.dtype}, got {dh.dtype}")
+    gcode = _out_code(grad_dtype)
+    need = lib().nvfp4_rms_norm_backward_workspace_bytes(rows, cols)
+    if need < 0:
+        _check(need, "nvfp4_rms_norm_backward")
+    with _on(dev, stream):
+        dx = h.new_empty((rows, cols))
+        dweight = torch.empty(cols, dtype=grad_dtype, device=dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+        _check(lib().nvfp4_rms_norm_backward(dy.data_ptr(), _dtype_code(dy), lddy, h.data_ptr(), _dtype_code(h), rows,
+                                             cols, ldh, rp, wp, wcode, _ptr(dh), lddh, dx.data_ptr(), max(cols, 1),
+                                             dweight.data_ptr(), gcode, _ptr(ws), need, _current_handle(dev)),
+               "nvfp4_rms_norm_backward")
+    return dx, dweight
 
 
 def _matvec(fn, what, w, x, out_dtype, out, stream):

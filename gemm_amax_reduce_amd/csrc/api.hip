@@ -154,6 +154,34 @@ int check_distill(const void *z, int z_dtype, int64_t tokens, int64_t vocab, int
   return NVFP4_OK;
 }
 
+// Does a matrix of the given pitch (bytes from row to row, and those of a row
+// that are its own) meet an input or the residual stream of an RMS norm?
+bool rms_meets(const nvfp4::RmsForward &a, const void *y, int64_t pitch, int64_t used) {
+  const int64_t xs = dtype_size(a.x_dtype), rs = dtype_size(a.r_dtype);
+  return overlap(a.x, a.ldx * xs, a.cols * xs, y, pitch, used, a.rows) ||
+         (a.res && (overlap(a.res, a.ldr * rs, a.cols * rs, y, pitch, used, a.rows) ||
+                    overlap(a.h, a.ldh * rs, a.cols * rs, y, pitch, used, a.rows)));
+}
+
+// What the two RMS norm calls share (all but y).
+int check_rms(const nvfp4::RmsForward &a) {
+  if (!dtype_ok(a.x_dtype) || !dtype_ok(a.w_dtype) || (a.res && !dtype_ok(a.r_dtype))) return NVFP4_ERR_ENUM;
+  if (a.cols < 1 || a.cols > kMaxNormCols || !matrix_ok(a.rows, a.cols, a.ldx)) return NVFP4_ERR_SHAPE;
+  if (a.res && (!matrix_ok(a.rows, a.cols, a.ldr) || !matrix_ok(a.rows, a.cols, a.ldh))) return NVFP4_ERR_SHAPE;
+  if (!(a.eps >= 0.0f) || a.eps > 3.0e38f) return NVFP4_ERR_VALUE;
+  if (a.rows > 0 && (!a.x || !a.rstd || (a.res && !a.h))) return NVFP4_ERR_NULL;
+  if (!aligned(a.x, dtype_size(a.x_dtype)) || !aligned(a.w, dtype_size(a.w_dtype)) || !aligned(a.rstd, 4))
+    return NVFP4_ERR_ALIGN;
+  if (!a.res) return NVFP4_OK;
+  const int64_t xs = dtype_size(a.x_dtype), rs = dtype_size(a.r_dtype);
+  if (!aligned(a.res, rs) || !aligned(a.h, rs)) return NVFP4_ERR_ALIGN;
+  // h may take the residual's place, and meets no input otherwise
+  if (overlap(a.x, a.ldx * xs, a.cols * xs, a.h, a.ldh * rs, a.cols * rs, a.rows)) return NVFP4_ERR_SHAPE;
+  const bool same = a.res == a.h && (a.ldr == a.ldh || a.rows <= 1);
+  if (!same && overlap(a.res, a.ldr * rs, a.cols * rs, a.h, a.ldh * rs, a.cols * rs, a.rows)) return NVFP4_ERR_SHAPE;
+  return NVFP4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -393,6 +421,65 @@ int nvfp4_layer_norm_backward(const void *dy, int dy_dtype, int64_t lddy, const 
   return hip_status(nvfp4::launch_layer_norm_backward(dy, dy_dtype, lddy, x, x_dtype, ldx, mean, rstd, weight, w_dtype,
                                                       dx, lddx, dweight, dbias, g_dtype, workspace, rows, cols,
                                                       (hipStream_t)hip_stream));
+}
+
+int nvfp4_rms_norm(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void *residual,
+                   int r_dtype, int64_t ldr, void *h, int64_t ldh, const void *weight, int w_dtype, float eps, void *y,
+                   int y_dtype, int64_t ldy, float *rstd, void *hip_stream) {
+  if (!dtype_ok(y_dtype)) return NVFP4_ERR_ENUM;
+  const nvfp4::RmsForward a = {x, x_dtype, rows, cols, ldx, residual, r_dtype, ldr, h, ldh, weight, w_dtype, eps, rstd};
+  const int st = check_rms(a);
+  if (st != NVFP4_OK) return st;
+  if (!matrix_ok(rows, cols, ldy)) return NVFP4_ERR_SHAPE;
+  if (rows > 0 && !y) return NVFP4_ERR_NULL;
+  if (!aligned(y, dtype_size(y_dtype))) return NVFP4_ERR_ALIGN;
+  if (rms_meets(a, y, ldy * dtype_size(y_dtype), cols * dtype_size(y_dtype))) return NVFP4_ERR_SHAPE;
+  return hip_status(nvfp4::launch_rms_norm(a, y, y_dtype, ldy, (hipStream_t)hip_stream));
+}
+
+int mxfp8_rms_norm(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void *residual,
+                   int r_dtype, int64_t ldr, void *h, int64_t ldh, const void *weight, int w_dtype, float eps,
+                   mxfp8_tensor *out, float *rstd, void *hip_stream) {
+  if (!out) return NVFP4_ERR_NULL;
+  const nvfp4::RmsForward a = {x, x_dtype, rows, cols, ldx, residual, r_dtype, ldr, h, ldh, weight, w_dtype, eps, rstd};
+  const int st = check_rms(a);
+  if (st != NVFP4_OK) return st;
+  if (cols % 32 != 0 || out->outer != rows || out->k != cols) return NVFP4_ERR_SHAPE;
+  if (rows > 0 && (!out->codes || !out->scales)) return NVFP4_ERR_NULL;
+  if (!aligned(out->codes, 16)) return NVFP4_ERR_ALIGN;
+  if (rms_meets(a, out->codes, cols, cols) || rms_meets(a, out->scales, cols / 32, cols / 32)) return NVFP4_ERR_SHAPE;
+  return hip_status(nvfp4::launch_rms_norm_mx8(a, out->codes, out->scales, (hipStream_t)hip_stream));
+}
+
+int64_t nvfp4_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  if (cols < 1 || cols > kMaxNormCols || !matrix_ok(rows, cols, cols)) return NVFP4_ERR_SHAPE;
+  return nvfp4::rms_norm_backward_workspace_bytes(rows, cols);
+}
+
+int nvfp4_rms_norm_backward(const void *dy, int dy_dtype, int64_t lddy, const void *h, int h_dtype, int64_t rows,
+                            int64_t cols, int64_t ldh, const float *rstd, const void *weight, int w_dtype,
+                            const void *dh, int64_t lddh, void *dx, int64_t lddx, void *dweight, int g_dtype,
+                            void *workspace, int64_t workspace_bytes, void *hip_stream) {
+  if (!dtype_ok(dy_dtype) || !dtype_ok(h_dtype) || !dtype_ok(w_dtype) || !dtype_ok(g_dtype)) return NVFP4_ERR_ENUM;
+  if (cols < 1 || cols > kMaxNormCols || !matrix_ok(rows, cols, ldh) || !matrix_ok(rows, cols, lddy) ||
+      !matrix_ok(rows, cols, lddx) || (dh && !matrix_ok(rows, cols, lddh)))
+    return NVFP4_ERR_SHAPE;
+  const int64_t need = nvfp4::rms_norm_backward_workspace_bytes(rows, cols);
+  if (workspace_bytes < need) return NVFP4_ERR_SHAPE;
+  if (rows > 0 && (!dy || !h || !rstd || !dx)) return NVFP4_ERR_NULL;
+  if (need > 0 && !workspace) return NVFP4_ERR_NULL;
+  if (!aligned(dy, dtype_size(dy_dtype)) || !aligned(h, dtype_size(h_dtype)) || !aligned(dx, dtype_size(h_dtype)) ||
+      !aligned(dh, dtype_size(h_dtype)) || !aligned(weight, dtype_size(w_dtype)) ||
+      !aligned(dweight, dtype_size(g_dtype)) || !aligned(rstd, 4) || !aligned(workspace, 16))
+    return NVFP4_ERR_ALIGN;
+  const int64_t hs = dtype_size(h_dtype), ds = dtype_size(dy_dtype);
+  if (overlap(dy, lddy * ds, cols * ds, dx, lddx * hs, cols * hs, rows) ||
+      overlap(h, ldh * hs, cols * hs, dx, lddx * hs, cols * hs, rows) ||
+      (dh && overlap(dh, lddh * hs, cols * hs, dx, lddx * hs, cols * hs, rows)))
+    return NVFP4_ERR_SHAPE;
+  return hip_status(nvfp4::launch_rms_norm_backward({dy, dy_dtype, lddy, h, h_dtype, rows, cols, ldh, rstd, weight,
+                                                     w_dtype, dh, lddh, dx, lddx, dweight, g_dtype, workspace},
+                                                    (hipStream_t)hip_stream));
 }
 
 int64_t nvfp4_matvec_workspace_bytes(int64_t n, int64_t k, int64_t tokens, int x_dtype) {

@@ -65,6 +65,47 @@ hipError_t launch_layer_norm_backward(const void *dy, int dy_dtype, int64_t lddy
                                       void *dx, int64_t lddx, void *dw, void *db, int g_dtype, void *workspace,
                                       int64_t rows, int64_t cols, hipStream_t stream);
 
+// RMS norm over rows: h = x + res in r_dtype (res null: h is x and is not
+// written), rstd, and y = h w rstd in f32 / bf16 or MXFP8 (cols % 32 == 0).
+// res and h may be the same matrix.  The backward workspace is
+// rms_norm_backward_workspace_bytes, 16-byte aligned; dh and dw may be null.
+struct RmsForward {
+  const void *x;
+  int x_dtype;
+  int64_t rows, cols, ldx;
+  const void *res;
+  int r_dtype;
+  int64_t ldr;
+  void *h;
+  int64_t ldh;
+  const void *w;
+  int w_dtype;
+  float eps;
+  float *rstd;
+};
+hipError_t launch_rms_norm(const RmsForward &a, void *y, int y_dtype, int64_t ldy, hipStream_t stream);
+hipError_t launch_rms_norm_mx8(const RmsForward &a, uint8_t *codes, uint8_t *scales, hipStream_t stream);
+struct RmsBackward {
+  const void *dy;
+  int dy_dtype;
+  int64_t lddy;
+  const void *h;
+  int h_dtype;
+  int64_t rows, cols, ldh;
+  const float *rstd;
+  const void *w;
+  int w_dtype;
+  const void *dh;              // in h_dtype, as dx
+  int64_t lddh;
+  void *dx;
+  int64_t lddx;
+  void *dw;
+  int g_dtype;
+  void *ws;
+};
+int64_t rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+hipError_t launch_rms_norm_backward(const RmsBackward &a, hipStream_t stream);
+
 // y[t][n] = sum_k x[t][k] w[n][k] with NVFP4 (mx = false) or MXFP4 weights.
 // ws: matvec_workspace_bytes, 16-byte aligned (none where that is 0).
 int64_t matvec_workspace_bytes(int64_t N, int64_t K, int64_t tokens, bool f32);

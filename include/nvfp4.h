@@ -425,6 +425,65 @@ int nvfp4_layer_norm_backward(const void *dy, int dy_dtype, int64_t lddy, const 
 int64_t nvfp4_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
 
 /*
+ * nvfp4_rms_norm -- root-mean-square norm of every row, after the addition of
+ * the residual stream where there is one:
+ *   h = x + residual,  r = 1 / sqrt(sum h^2 / cols + eps),  y = h weight r
+ *  x         : device, row-major [rows][ldx], x_dtype, ldx >= cols >= 1 (at
+ *              most 2^31 columns), aligned to its element only.
+ *  residual  : device, row-major [rows][ldr], r_dtype, or NULL (h is x then).
+ *  h         : device, row-major [rows][ldh], r_dtype: the sum, rounded to
+ *              nearest even; what is normed is h as stored.  May be `residual`
+ *              itself (same pointer and leading dimension).  Not used
+ *              without a residual.
+ *  weight    : device, w_dtype [cols]; NULL = 1.
+ *  eps       : >= 0 and finite (NVFP4_ERR_VALUE otherwise).
+ *  y         : device, row-major [rows][ldy], y_dtype (bf16 = nearest even of
+ *              the binary32 value, rounded once).
+ *  rstd      : device, f32 [rows], r for the backward pass.
+ * Sums are binary32 (a row whose squares pass its range has r = 0).  A row's
+ * non-finite values reach that row only.  Outputs must not overlap inputs or
+ * each other (NVFP4_ERR_SHAPE; rows of two may lie side by side in one
+ * buffer), but for h in the residual's place.  Deterministic.  Enqueues one
+ * kernel.
+ *
+ * mxfp8_rms_norm -- the same with y in MXFP8: the codes and scales that
+ * mxfp8_quantize forms, on axis 1, from the binary32 values (h weight) r where
+ * these are finite; the operand of mxfp8_gemm.  cols % 32 == 0;
+ * out->outer == rows, out->k == cols.
+ */
+int nvfp4_rms_norm(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void *residual,
+                   int r_dtype, int64_t ldr, void *h, int64_t ldh, const void *weight, int w_dtype, float eps, void *y,
+                   int y_dtype, int64_t ldy, float *rstd, void *hip_stream);
+int mxfp8_rms_norm(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void *residual,
+                   int r_dtype, int64_t ldr, void *h, int64_t ldh, const void *weight, int w_dtype, float eps,
+                   mxfp8_tensor *out, float *rstd, void *hip_stream);
+
+/*
+ * nvfp4_rms_norm_backward -- the gradients of nvfp4_rms_norm: with
+ * a = dy weight and n = h rstd,
+ *   dx = rstd (a - n sum(a n) / cols) + dh                  (h_dtype, [rows][lddx])
+ *   dweight = sum over rows of dy n                         (g_dtype, [cols])
+ *  h         : what was normed, h_dtype.  dx is the gradient of x and of the
+ *              residual alike.
+ *  dh        : the gradient that reaches h from the residual stream, h_dtype,
+ *              row-major [rows][lddh], or NULL (0).
+ *  dx        : must not overlap dy, h or dh (NVFP4_ERR_SHAPE).
+ *  dweight   : may be NULL; zeros when rows == 0.
+ *  workspace : device, at least nvfp4_rms_norm_backward_workspace_bytes
+ *              (rows, cols) bytes (0 for a few rows, NULL then allowed),
+ *              16-byte aligned, contents ignored and overwritten; calls that
+ *              share one must not overlap in time.
+ * The sums over rows are binary32 partial sums of fixed sets of rows, added
+ * in a fixed order: deterministic on one device.  The workspace size is
+ * NVFP4_ERR_SHAPE for sizes that the call itself refuses.
+ */
+int nvfp4_rms_norm_backward(const void *dy, int dy_dtype, int64_t lddy, const void *h, int h_dtype, int64_t rows,
+                            int64_t cols, int64_t ldh, const float *rstd, const void *weight, int w_dtype,
+                            const void *dh, int64_t lddh, void *dx, int64_t lddx, void *dweight, int g_dtype,
+                            void *workspace, int64_t workspace_bytes, void *hip_stream);
+int64_t nvfp4_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
  * nvfp4_matvec, mxfp4_matvec -- a few rows of unquantized activations times
  * a 4-bit weight matrix, the single-token form of the linear layer:
  *   y[t][n] = g sum_k x[t][k] e2m1(code[n][k]) e4m3(scale[n][k/16])       (NVFP4)
