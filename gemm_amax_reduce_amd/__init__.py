@@ -21,7 +21,8 @@ __all__ = ["NVFP4Tensor", "NVFP4Error", "nvfp4_quantize", "nvfp4_rht_quantize", 
            "mxfp8_gemm",
            "nvfp4_dequantize", "nvfp4_gemm", "nvfp4_gemm_ws", "nvfp4_gemm_noalloc", "gemm_workspace",
            "nvfp4_layer_norm", "nvfp4_layer_norm_backward", "nvfp4_rms_norm", "mxfp8_rms_norm",
-           "nvfp4_rms_norm_backward", "nvfp4_matvec", "mxfp4_matvec", "nvfp4_distill_topk",
+           "nvfp4_rms_norm_backward", "nvfp4_matvec", "mxfp4_matvec", "nvfp4_grouped_matmul", "mxfp4_grouped_matmul",
+           "nvfp4_grouped_wgrad", "nvfp4_distill_topk",
            "nvfp4_distill_topk_backward", "nvfp4_distill_topk_step",
            "lib", "LIB_PATH", "F32", "BF16", "RNE", "SR"]
 
@@ -55,7 +56,8 @@ EXPORTS = ("nvfp4_quantize", "nvfp4_rht_quantize", "nvfp4_amax", "nvfp4_quantize
            "nvfp4_layer_norm_workspace_bytes", "nvfp4_layer_norm_backward", "nvfp4_layer_norm_backward_workspace_bytes",
            "nvfp4_rms_norm", "mxfp8_rms_norm", "nvfp4_rms_norm_backward", "nvfp4_rms_norm_backward_workspace_bytes",
            "nvfp4_matvec", "mxfp4_matvec",
-           "nvfp4_matvec_workspace_bytes", "nvfp4_distill_topk", "nvfp4_distill_topk_backward",
+           "nvfp4_matvec_workspace_bytes", "nvfp4_grouped_matmul", "mxfp4_grouped_matmul",
+           "nvfp4_grouped_matmul_workspace_bytes", "nvfp4_grouped_wgrad", "nvfp4_distill_topk", "nvfp4_distill_topk_backward",
            "nvfp4_distill_topk_step", "nvfp4_distill_topk_workspace_bytes", "nvfp4_probe_mfma", "nvfp4_probe_philox", "nvfp4_status_string")
 
 
@@ -125,6 +127,15 @@ def lib() -> ctypes.CDLL:
         L.mxfp4_matvec.restype = ci
         L.nvfp4_matvec_workspace_bytes.argtypes = [i64, i64, i64, ci]
         L.nvfp4_matvec_workspace_bytes.restype = i64
+        groups = [ci, vp, ci, i64, i64, vp, ci, i64, vp, ci, i64, ci, vp, i64, vp]
+        L.nvfp4_grouped_matmul.argtypes = [pt] + groups
+        L.nvfp4_grouped_matmul.restype = ci
+        L.mxfp4_grouped_matmul.argtypes = [mt] + groups
+        L.mxfp4_grouped_matmul.restype = ci
+        L.nvfp4_grouped_matmul_workspace_bytes.argtypes = [i64, i64, i64, i64, ci]
+        L.nvfp4_grouped_matmul_workspace_bytes.restype = i64
+        L.nvfp4_grouped_wgrad.argtypes = [vp, ci, i64, vp, ci, i64, i64, i64, i64, vp, ci, i64, vp, ci, vp]
+        L.nvfp4_grouped_wgrad.restype = ci
         rows = [vp, ci, i64, i64, i64, vp, ci, vp, ci, i64, cf]       # logits, indices, teacher, temperature
         L.nvfp4_distill_topk.argtypes = rows + [vp, vp, vp, i64, vp]
         L.nvfp4_distill_topk.restype = ci
@@ -870,6 +881,90 @@ def mxfp4_matvec(w: MXFP4Tensor, x: torch.Tensor, out_dtype=None, out: torch.Ten
                  stream=None) -> torch.Tensor:
     """nvfp4_matvec with MXFP4 weights."""
     return _matvec(lib().mxfp4_matvec, "mxfp4_matvec", w, x, out_dtype, out, stream)
+
+
+def _group_args(offsets, device):
+    """(address, index bits, number of groups) of a vector of group offsets."""
+    if not isinstance(offsets, torch.Tensor) or offsets.dtype not in (torch.int32, torch.int64):
+        raise NVFP4Error("offsets must be an int32 or int64 tensor")
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise NVFP4Error(f"offsets must be a vector of the groups' ends behind a first start, got "
+                         f"{tuple(offsets.shape)}")
+    groups = offsets.shape[0] - 1
+    return (_vector(offsets, "offsets", offsets.dtype, groups + 1, device), 32 if offsets.dtype is torch.int32 else 64,
+            groups)
+
+
+def _grouped_matmul(fn, what, w, x, offsets, out_dtype, transposed, out, stream):
+    ldx = _require_matrix(x, "x")
+    dev = x.device
+    if w.device != dev:
+        raise NVFP4Error(f"weights on {w.device}, x on {dev}")
+    op, bits, experts = _group_args(offsets, dev)
+    rows, k = x.shape
+    stacked = w.k if transposed else w.outer
+    if stacked % experts:
+        raise NVFP4Error(f"a stack of {stacked} {'columns' if transposed else 'rows'} is not one of {experts} experts")
+    n, want = (w.outer, w.k // experts) if transposed else (w.outer // experts, w.k)
+    if k != want:
+        raise NVFP4Error(f"x must have {want} columns, got {k}")
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    code = _out_code(out_dtype)
+    cw, xcode = w._c(), _dtype_code(x)
+    need = lib().nvfp4_grouped_matmul_workspace_bytes(experts, n, k, rows, xcode)
+    if need < 0:
+        _check(need, what)
+    with _on(dev, stream):
+        y = torch.empty((rows, n), dtype=out_dtype, device=dev) if out is None else out
+        ldy = max(n, 1) if out is None else _require_matrix_out(y, rows, n, out_dtype, dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        _check(fn(ctypes.byref(cw), int(bool(transposed)), x.data_ptr(), xcode, rows, ldx, op, bits, experts,
+                  y.data_ptr(), code, ldy, int(out is None), _ptr(ws), need, _current_handle(dev)), what)
+    return y
+
+
+def nvfp4_grouped_matmul(w: NVFP4Tensor, x: torch.Tensor, offsets: torch.Tensor, out_dtype=None,
+                         transposed: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y [rows, N] = x . W_e^T for the rows offsets[e] .. offsets[e + 1] - 1 of
+    unquantized x [rows, K] (f32/bf16) and each expert's NVFP4 weights W_e
+    [N, K]: w is [experts * N, K], or with `transposed` [N, experts * K] (the
+    stack [experts * K, N] quantized on axis 0, for the data gradient).
+    offsets: int32/int64 [experts + 1] on the GPU, not decreasing.  Rows of no
+    group are zeros, and left as they are in a given `out`."""
+    return _grouped_matmul(lib().nvfp4_grouped_matmul, "nvfp4_grouped_matmul", w, x, offsets, out_dtype, transposed,
+                           out, stream)
+
+
+def mxfp4_grouped_matmul(w: MXFP4Tensor, x: torch.Tensor, offsets: torch.Tensor, out_dtype=None,
+                         transposed: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """nvfp4_grouped_matmul with MXFP4 weights."""
+    return _grouped_matmul(lib().mxfp4_grouped_matmul, "mxfp4_grouped_matmul", w, x, offsets, out_dtype, transposed,
+                           out, stream)
+
+
+def nvfp4_grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, grad_dtype=torch.float32,
+                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient [experts, N, K] of a stack of experts' weights in
+    `grad_dtype`: the sum of dy[t]^T x[t] over each group's rows of dy
+    [rows, N] and x [rows, K]."""
+    ldx = _require_matrix(x, "x")
+    dev = x.device
+    rows, k = x.shape
+    lddy = _require_matrix(dy, "dy", dev)
+    if dy.shape[0] != rows:
+        raise NVFP4Error(f"dy must have {rows} rows, got {dy.shape[0]}")
+    n = dy.shape[1]
+    op, bits, experts = _group_args(offsets, dev)
+    code = _out_code(grad_dtype)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((experts, n, k), dtype=grad_dtype, device=dev)
+        elif not isinstance(out, torch.Tensor) or tuple(out.shape) != (experts, n, k):
+            raise NVFP4Error(f"out must have shape ({experts}, {n}, {k})")
+        dp = _vector(out, "out", grad_dtype, experts * n * k, dev)
+        _check(lib().nvfp4_grouped_wgrad(dy.data_ptr(), _dtype_code(dy), lddy, x.data_ptr(), _dtype_code(x), ldx, rows, n,
+                                         k, op, bits, experts, dp, code, _current_handle(dev)), "nvfp4_grouped_wgrad")
+    return out
 
 
 def _distill_args(logits, indices, teacher, temperature):

@@ -182,6 +182,45 @@ int check_rms(const nvfp4::RmsForward &a) {
   return NVFP4_OK;
 }
 
+// Groups of rows and the grids of the kernels that walk them: at most 2^24 - 8
+// workgroups of 256 threads (a grid's threads are counted in 32 bits), of the
+// smallest tiles.
+constexpr int64_t kMaxGrid = (1LL << 24) - 8;
+constexpr int64_t kMaxGroups = 1LL << 20;
+inline bool grid_ok(int64_t a, int64_t b) { return a <= 0 || b <= kMaxGrid / a; }
+inline bool grouped_ok(int64_t experts, int64_t n, int64_t k, int64_t rows) {
+  return experts >= 1 && experts <= kMaxGroups && k <= kMaxGemmK && n <= kMaxMatvecRows &&
+         grid_ok((n + 127) / 128, rows / 32 + (experts < rows ? experts : rows));
+}
+// Do the bytes of two ranges meet?
+inline bool ranges_meet(const void *a, int64_t abytes, const void *b, int64_t bbytes) {
+  return overlap(a, abytes, abytes, b, bbytes, bbytes, 1);
+}
+inline int64_t span(int64_t rows, int64_t ld, int64_t cols, int64_t size) {
+  return rows > 0 && cols > 0 ? ((rows - 1) * ld + cols) * size : 0;
+}
+
+// What the grouped products share; outer, k: the stack as it is stored.
+int grouped_common(nvfp4::GroupedProduct p, int64_t outer, int64_t k, int64_t workspace_bytes, void *hip_stream) {
+  if (!dtype_ok(p.x_dtype) || !dtype_ok(p.y_dtype) || (p.index_bits != 32 && p.index_bits != 64)) return NVFP4_ERR_ENUM;
+  if (p.experts < 1 || p.experts > kMaxGroups) return NVFP4_ERR_SHAPE;
+  const int64_t block = p.mx ? 32 : 16;
+  p.n = p.transposed ? outer : outer / p.experts;
+  p.k = p.transposed ? k / p.experts : k;
+  if ((p.transposed ? k : outer) % p.experts != 0 || p.k % block != 0) return NVFP4_ERR_SHAPE;
+  if (!matrix_ok(p.rows, p.k, p.ldx) || !matrix_ok(p.rows, p.n, p.ldy) || !grouped_ok(p.experts, p.n, p.k, p.rows))
+    return NVFP4_ERR_SHAPE;
+  if (p.rows > 0 && p.n > 0 && (!p.y || !p.offsets || (p.k > 0 && !p.x))) return NVFP4_ERR_NULL;
+  const int64_t need = nvfp4::grouped_workspace_bytes(p.experts, p.n, p.k, p.rows, p.x_dtype == NVFP4_F32);
+  if (workspace_bytes < need) return NVFP4_ERR_SHAPE;
+  if (need > 0 && !p.ws) return NVFP4_ERR_NULL;
+  const int64_t xs = dtype_size(p.x_dtype), ys = dtype_size(p.y_dtype);
+  if (!aligned(p.x, xs) || !aligned(p.y, ys) || !aligned(p.offsets, p.index_bits / 8) || !aligned(p.ws, 16))
+    return NVFP4_ERR_ALIGN;
+  if (overlap(p.x, p.ldx * xs, p.k * xs, p.y, p.ldy * ys, p.n * ys, p.rows)) return NVFP4_ERR_SHAPE;
+  return hip_status(nvfp4::launch_grouped(p, (hipStream_t)hip_stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -506,6 +545,57 @@ int mxfp4_matvec(const mxfp4_tensor *w, const void *x, int x_dtype, int64_t toke
   if (!aligned(w->codes, 16)) return NVFP4_ERR_ALIGN;
   return matvec_common(true, w->codes, w->scales, nullptr, w->outer, w->k, x, x_dtype, tokens, ldx, y, y_dtype, ldy,
                        workspace, workspace_bytes, hip_stream);
+}
+
+int64_t nvfp4_grouped_matmul_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t rows, int x_dtype) {
+  if (!dtype_ok(x_dtype)) return NVFP4_ERR_ENUM;
+  if (n < 0 || k < 0 || k % 16 != 0 || rows < 0 || !matrix_ok(rows, k, k) || !matrix_ok(rows, n, n) ||
+      !grouped_ok(experts, n, k, rows))
+    return NVFP4_ERR_SHAPE;
+  return nvfp4::grouped_workspace_bytes(experts, n, k, rows, x_dtype == NVFP4_F32);
+}
+
+int nvfp4_grouped_matmul(const nvfp4_tensor *w, int transposed, const void *x, int x_dtype, int64_t rows, int64_t ldx,
+                         const void *offsets, int index_bits, int64_t experts, void *y, int y_dtype, int64_t ldy,
+                         int zero_rest, void *workspace, int64_t workspace_bytes, void *hip_stream) {
+  const int st = check_tensor(w);
+  if (st != NVFP4_OK) return st;
+  return grouped_common({false, transposed != 0, w->codes, w->scales, w->meta, experts, 0, 0, x, x_dtype, rows, ldx,
+                         offsets, index_bits, y, y_dtype, ldy, zero_rest, workspace},
+                        w->outer, w->k, workspace_bytes, hip_stream);
+}
+
+int mxfp4_grouped_matmul(const mxfp4_tensor *w, int transposed, const void *x, int x_dtype, int64_t rows, int64_t ldx,
+                         const void *offsets, int index_bits, int64_t experts, void *y, int y_dtype, int64_t ldy,
+                         int zero_rest, void *workspace, int64_t workspace_bytes, void *hip_stream) {
+  if (!w) return NVFP4_ERR_NULL;
+  if (w->outer < 0 || w->k < 0 || w->k % 32 != 0 || !count_ok(w->outer, w->k)) return NVFP4_ERR_SHAPE;
+  if (w->outer > 0 && w->k > 0 && (!w->codes || !w->scales)) return NVFP4_ERR_NULL;
+  if (!aligned(w->codes, 16)) return NVFP4_ERR_ALIGN;
+  return grouped_common({true, transposed != 0, w->codes, w->scales, nullptr, experts, 0, 0, x, x_dtype, rows, ldx,
+                         offsets, index_bits, y, y_dtype, ldy, zero_rest, workspace},
+                        w->outer, w->k, workspace_bytes, hip_stream);
+}
+
+int nvfp4_grouped_wgrad(const void *dy, int dy_dtype, int64_t lddy, const void *x, int x_dtype, int64_t ldx,
+                        int64_t rows, int64_t n, int64_t k, const void *offsets, int index_bits, int64_t experts,
+                        void *dw, int dw_dtype, void *hip_stream) {
+  if (!dtype_ok(dy_dtype) || !dtype_ok(x_dtype) || !dtype_ok(dw_dtype) || (index_bits != 32 && index_bits != 64))
+    return NVFP4_ERR_ENUM;
+  if (n < 0 || k < 0 || !matrix_ok(rows, n, lddy) || !matrix_ok(rows, k, ldx) || experts < 1 || experts > kMaxGroups ||
+      n > kMaxGrid * 128 || k > kMaxGrid * 128 || !grid_ok((n + 127) / 128, (k + 127) / 128) ||
+      !grid_ok((n + 127) / 128 * ((k + 127) / 128), experts))
+    return NVFP4_ERR_SHAPE;
+  if (n > 0 && k > 0 && (!dw || !offsets || (rows > 0 && (!dy || !x)))) return NVFP4_ERR_NULL;
+  const int64_t ds = dtype_size(dy_dtype), xs = dtype_size(x_dtype), ws = dtype_size(dw_dtype);
+  if (!aligned(dy, ds) || !aligned(x, xs) || !aligned(dw, ws) || !aligned(offsets, index_bits / 8))
+    return NVFP4_ERR_ALIGN;
+  if (ranges_meet(dy, span(rows, lddy, n, ds), dw, experts * n * k * ws) ||
+      ranges_meet(x, span(rows, ldx, k, xs), dw, experts * n * k * ws))
+    return NVFP4_ERR_SHAPE;
+  return hip_status(nvfp4::launch_grouped_wgrad({experts, n, k, dy, dy_dtype, lddy, x, x_dtype, rows, ldx, offsets,
+                                                 index_bits, dw, dw_dtype},
+                                                (hipStream_t)hip_stream));
 }
 
 int64_t nvfp4_distill_topk_workspace_bytes(int64_t tokens, int64_t vocab) {

@@ -1,0 +1,543 @@
+// grouped.hip -- matrix products grouped by expert for gfx950: rows of
+// unquantized activations, in ragged groups, each with 4-bit weights of its own
+//
+//   y[t][n] = g sum_k x[t][k] w_e[n][k]      for t in group e
+//
+// and the gradient of the weights, dw_e[n][k] = sum over t in group e of
+// dy[t][n] x[t][k].
+//
+// Weights are decoded to bf16, where e2m1(code) e4m3(scale) is exact, and
+// multiplied on the 32x32x16 bf16 MFMA with the weights as the A operand, so
+// that a lane ends up with 16 consecutive n of a token; float32 activations
+// are three bf16 parts.  A workgroup's tile is 128 NF weight rows (its four
+// waves have NF fragments of 32 each, so every weight is decoded by one wave)
+// by 32 MF tokens, which all of its waves read from LDS.
+#include "gemm_common.h"
+#include "groups.h"
+#include "nvfp4_kernels.h"
+#include "operands.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace nvfp4 {
+
+namespace {
+
+typedef uint32_t u32x4_a8 __attribute__((ext_vector_type(4), aligned(8)));
+typedef uint32_t u32x2_a8 __attribute__((ext_vector_type(2), aligned(8)));
+
+constexpr int kThreads = 256;
+constexpr int kStage = 128;                        // k of one LDS buffer
+constexpr int kXcds = 8;
+
+// Where a call's weights lie: expert e's row n starts at n * pitch + e * step
+// bytes of codes (experts one after the other, or side by side in each row).
+struct Stack {
+  const uint8_t *codes, *scales;
+  const float *meta;
+  int64_t N, K;
+  int64_t code_pitch, code_step, scale_pitch, scale_step;
+};
+
+template <typename X> struct Rows {
+  const X *p;
+  int64_t ld;
+};
+
+// 16 outputs n .. n + 15 of a token, none from N on.
+__device__ __forceinline__ void store16(void *y, int y_bf16, int64_t row, int64_t n, int64_t N, const float *v) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (y_bf16) {
+      Row8<uint16_t> q;
+      q.set(v + 8 * i);
+      store_row8(q, (uint16_t *)y + row, n + 8 * i, N);
+    } else {
+      Row8<float> q;
+      q.set(v + 8 * i);
+      store_row8(q, (float *)y + row, n + 8 * i, N);
+    }
+  }
+}
+
+// Zeros in the rows of y that no group has.
+__device__ void zero_rest(const Groups &g, void *y, int y_bf16, int64_t ldy, int64_t N) {
+  const int64_t first = g.at(0), last = max(g.at(g.count), first), rest = first + g.rows - last;
+  for (int64_t i = blockIdx.x; i < rest; i += gridDim.x) {
+    const int64_t row = (i < first ? i : last + i - first) * ldy;
+    for (int64_t n = threadIdx.x; n < N; n += blockDim.x) {
+      if (y_bf16) ((uint16_t *)y)[row + n] = 0;
+      else ((float *)y)[row + n] = 0.0f;
+    }
+  }
+}
+
+// XP: bf16 parts of an activation (1: bf16, 3: float32).
+template <bool MX, typename X, int NF, int MF>
+__global__ __launch_bounds__(kThreads, NF * MF >= 16 ? 1 : NF * MF >= 4 ? 2 : 4) void
+k_grouped(Stack w, Groups g, Rows<X> x, void *y, int y_bf16, int64_t ldy, int tiles_n, int fill) {
+  constexpr int kXP = sizeof(X) == 2 ? 1 : 3;
+  constexpr int BN = 128 * NF, BM = 32 * MF;
+  constexpr int kG = Scale<MX>::kPerByte, kSB = kStage / kG;        // scale bytes of a row and stage
+  constexpr int kCodes = BN * kStage / 2, kScales = BN * 8, kPart = BM * kStage * 2;
+  constexpr int kBuffer = kCodes + kScales + kXP * kPart;
+  constexpr int kCL = BN * 4 / kThreads;                            // 16-byte pieces of codes a thread loads
+  constexpr int kXL = BM * 16 / kThreads;                           // 8-element pieces of x
+  constexpr int kSL = (BN + kThreads - 1) / kThreads;               // scale rows
+  __shared__ __align__(16) char lds[2 * kBuffer];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 31, h = lane >> 5;
+
+  if (fill) zero_rest(g, y, y_bf16, ldy, w.N);
+  const int total = count_tiles(g, BM) * tiles_n;
+  // workgroups are dealt to the XCDs in turn: each gets a run of tiles
+  const int quota = (total + kXcds - 1) / kXcds, local = blockIdx.x / kXcds;
+  const int index = (int)(blockIdx.x % kXcds) * quota + local;
+  if (local >= quota || index >= total) return;
+  const GroupTile t = find_tile(g, BM, tiles_n, index);
+  if (t.e < 0) return;
+  // up to 8 tiles of tokens with one tile of weights after the other
+  const int per = 8 * tiles_n, first_m = t.local / per * 8, gsz = min(t.tiles - first_m, 8);
+  const int64_t m0 = t.begin + (int64_t)(first_m + t.local % per % gsz) * BM;
+  const int64_t n0 = (int64_t)(t.local % per / gsz) * BN;
+
+  const int stages = (int)((w.K + kStage - 1) / kStage);
+  const uint8_t *const codes = w.codes + t.e * w.code_step, *const scales = w.scales + t.e * w.scale_step;
+
+  // ---- from memory to registers
+  const uint8_t *crow[kCL], *srow[kSL];
+  const X *xrow[kXL];
+  bool live[kXL];
+#pragma unroll
+  for (int i = 0; i < kCL; ++i)
+    crow[i] = codes + min(n0 + (tid + i * kThreads) / 4, w.N - 1) * w.code_pitch + 16 * (tid & 3);
+#pragma unroll
+  for (int i = 0; i < kSL; ++i) srow[i] = scales + min(n0 + tid + i * kThreads, w.N - 1) * w.scale_pitch;
+#pragma unroll
+  for (int i = 0; i < kXL; ++i) {
+    const int64_t row = m0 + tid / 16 + 16 * i;
+    live[i] = row < t.end;
+    xrow[i] = x.p + min(row, t.end - 1) * x.ld + 8 * (tid & 15);
+  }
+  u32x4_t creg[kCL];
+  uint64_t sreg[kSL];
+  Row8<X> xreg[kXL];
+  const auto load = [&](int s) {
+    const int64_t k0 = (int64_t)s * kStage;
+    if (k0 + kStage <= w.K) {
+#pragma unroll
+      for (int i = 0; i < kCL; ++i) creg[i] = *reinterpret_cast<const u32x4_a8 *>(crow[i] + k0 / 2);
+#pragma unroll
+      for (int i = 0; i < kSL; ++i) {
+        sreg[i] = 0;
+        __builtin_memcpy(&sreg[i], srow[i] + k0 / kG, kSB);
+      }
+#pragma unroll
+      for (int i = 0; i < kXL; ++i) xreg[i].load(xrow[i] + k0);
+    } else {
+      // the last stage of K % 128 != 0: zeros past K (a scale of 1 for MXFP4)
+      const int64_t left = w.K - k0;
+#pragma unroll
+      for (int i = 0; i < kCL; ++i) {
+        const int at = 32 * (tid & 3);
+        u32x2_a8 lo = {0, 0}, hi = {0, 0};
+        if (at < left) lo = *reinterpret_cast<const u32x2_a8 *>(crow[i] + k0 / 2);
+        if (at + 16 < left) hi = *reinterpret_cast<const u32x2_a8 *>(crow[i] + k0 / 2 + 8);
+        creg[i] = (u32x4_t){lo[0], lo[1], hi[0], hi[1]};
+      }
+#pragma unroll
+      for (int i = 0; i < kSL; ++i) {
+        sreg[i] = MX ? 0x7F7F7F7F7F7F7F7Full : 0;
+        for (int b = 0; b < kSB; ++b)
+          if (b * kG < left) sreg[i] = (sreg[i] & ~(0xFFull << (8 * b))) | (uint64_t)srow[i][k0 / kG + b] << (8 * b);
+      }
+#pragma unroll
+      for (int i = 0; i < kXL; ++i) {
+        if (8 * (tid & 15) < left) xreg[i].load(xrow[i] + k0);
+        else xreg[i].zero();
+      }
+    }
+  };
+
+  // ---- from registers to LDS.  Codes: 4 pieces a row, piece c in slot
+  // c ^ (row / 16 % 4); x: 16 pieces a row, piece p in slot p ^ (row % 16): the
+  // 8 lanes of a 16-byte read that go together fall on all banks.
+  const auto put = [&](int s) {
+    char *const buf = lds + (s & 1) * kBuffer;
+#pragma unroll
+    for (int i = 0; i < kCL; ++i) {
+      const int row = (tid + i * kThreads) / 4;
+      *reinterpret_cast<u32x4_t *>(buf + row * 64 + 16 * ((tid & 3) ^ ((row >> 4) & 3))) = creg[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kSL; ++i)
+      if (BN % kThreads == 0 || tid + i * kThreads < BN)
+        *reinterpret_cast<uint64_t *>(buf + kCodes + (tid + i * kThreads) * 8) = sreg[i];
+#pragma unroll
+    for (int i = 0; i < kXL; ++i) {
+      const int row = tid / 16 + 16 * i;
+      char *const at = buf + kCodes + kScales + row * 256 + 16 * ((tid & 15) ^ (row & 15));
+      if constexpr (kXP == 1) {
+        *reinterpret_cast<u32x4_t *>(at) = live[i] ? (u32x4_t)xreg[i].r : (u32x4_t){0, 0, 0, 0};
+      } else {
+        if (!live[i]) xreg[i].zero();
+        const Parts q = split8((f32x4_t)xreg[i].a, (f32x4_t)xreg[i].b);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x4_t *>(at + p * kPart) = q.v[p];
+      }
+    }
+  };
+
+  // ---- a stage's products.  Row r of fragment f is weight row f * 32 +
+  // (r / 4 % 2) * 16 + r / 8 * 4 + r % 4 of the wave's, so that the lane's
+  // results of a fragment are 16 consecutive n.  A lane's 32 codes of a half
+  // stage are k 32 h .. 32 h + 31 of it, 8 an MFMA.
+  float16_t acc[NF][MF];
+#pragma unroll
+  for (int f = 0; f < NF; ++f)
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[f][m][i] = 0.0f;
+  const int wrow = wave * (32 * NF) + ((r >> 2) & 1) * 16 + (r >> 3) * 4 + (r & 3);
+  const auto half_stage = [&](int s, int sub) {
+    const char *const buf = lds + (s & 1) * kBuffer;
+    u32x4_t c[NF];
+    Scale<MX> sc[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      const int row = wrow + 32 * f;
+      c[f] = *reinterpret_cast<const u32x4_t *>(buf + row * 64 + 16 * ((2 * sub + h) ^ ((row >> 4) & 3)));
+      const char *const sp = buf + kCodes + row * 8 + (2 * sub + h) * (32 / kG);
+      if (MX) sc[f].raw = *reinterpret_cast<const uint8_t *>(sp);
+      else sc[f].raw = *reinterpret_cast<const uint16_t *>(sp);
+    }
+    // MXFP4 at a quarter: the largest scales' weights pass bf16's range
+    // otherwise; scales too near either end for the conversion's own go by
+    // products
+    bool far = false;
+    if constexpr (MX) {
+#pragma unroll
+      for (int f = 0; f < NF; ++f) far |= sc[f].raw - 3 >= 250;
+      far = __any(far);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      bf16x8_t a[NF];
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        if constexpr (MX) {
+          if (far) a[f] = decode8<false>(c[f][j], sc[f].quarter());
+          else a[f] = decode8<true>(c[f][j], __uint_as_float((sc[f].raw - 2) << 23));
+        } else {
+          a[f] = decode8<false>(c[f][j], j < 2 ? sc[f].lo() : sc[f].hi());
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < MF; ++m) {
+        const int row = 32 * m + r;
+        const char *const at = buf + kCodes + kScales + row * 256 + 16 * ((8 * sub + 4 * h + j) ^ (row & 15));
+#pragma unroll
+        for (int p = 0; p < kXP; ++p) {
+          const bf16x8_t b = *reinterpret_cast<const bf16x8_t *>(at + p * kPart);
+#pragma unroll
+          for (int f = 0; f < NF; ++f) acc[f][m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[f], b, acc[f][m], 0, 0, 0);
+        }
+      }
+    }
+  };
+
+  if (stages > 0) {
+    load(0);
+    put(0);
+    if (stages > 1) load(1);
+    __syncthreads();
+    for (int s = 0; s < stages; ++s) {
+      half_stage(s, 0);
+      half_stage(s, 1);
+      if (s + 1 < stages) put(s + 1);
+      if (s + 2 < stages) load(s + 2);
+      __syncthreads();
+    }
+  }
+
+  const float scale = MX ? 4.0f : w.K > 0 ? w.meta[1] : 0.0f;      // (g of no weights may be anything)
+#pragma unroll
+  for (int m = 0; m < MF; ++m) {
+    const int64_t row = m0 + 32 * m + r;
+    if (row >= t.end) continue;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = acc[f][m][i] * scale;
+      store16(y, y_bf16, row * ldy, n0 + wave * (32 * NF) + 32 * f + 16 * h, w.N, v);
+    }
+  }
+}
+
+// Weight rows and tokens of a tile, in fragments of 32 (times 4 waves).
+struct GroupedCut {
+  int nf, mf;
+};
+GroupedCut grouped_cut(const Stack &w, int experts, int64_t tokens, bool f32) {
+  const int64_t each = (tokens + experts - 1) / experts;      // rows of a group, on average
+  if (each <= 40) return {1, 1};
+  if (each <= 128 || f32) return {2, 2};
+  return {4, 4};
+}
+
+template <bool MX, typename X, int NF, int MF>
+hipError_t grouped(const Stack &w, const Groups &g, const Rows<X> &x, void *y, int y_bf16, int64_t ldy, int fill,
+                   hipStream_t stream) {
+  constexpr int BN = 128 * NF, BM = 32 * MF;
+  const int64_t tiles_n = (w.N + BN - 1) / BN, tiles_m = g.rows / BM + std::min<int64_t>(g.count, g.rows);
+  k_grouped<MX, X, NF, MF><<<(unsigned)((tiles_n * tiles_m + kXcds - 1) / kXcds * kXcds), kThreads, 0, stream>>>(
+      w, g, x, y, y_bf16, ldy, (int)tiles_n, fill);
+  return hipGetLastError();
+}
+template <bool MX, typename X>
+hipError_t grouped_x(const Stack &w, const Groups &g, const Rows<X> &x, void *y, int y_bf16, int64_t ldy, int fill,
+                     hipStream_t stream) {
+  const GroupedCut c = grouped_cut(w, g.count, g.rows, sizeof(X) == 4);
+  if (c.nf == 1) return grouped<MX, X, 1, 1>(w, g, x, y, y_bf16, ldy, fill, stream);
+  if constexpr (sizeof(X) == 2)
+    if (c.nf == 4) return grouped<MX, X, 4, 4>(w, g, x, y, y_bf16, ldy, fill, stream);
+  return grouped<MX, X, 2, 2>(w, g, x, y, y_bf16, ldy, fill, stream);
+}
+
+// ------------------------------------------------------ weight gradient --
+
+// Tokens run along the reduction here, and lie down the columns of both
+// operands: a stage's rows go to LDS as they are, and the lanes fetch columns
+// with transposing reads (16 lanes take 4 rows of 16 columns, and each leaves
+// with 4 rows of its own column).  Rows of LDS are 32 bytes longer than their
+// columns, so that the 4 rows of such a read fall on different banks.
+// A float32 operand is three bf16 parts, hi + mid + lo, rounded to nearest, of
+// which the products from hi hi to mid mid are taken; those left out are below
+// 2^-25 of the whole.
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+
+__device__ __forceinline__ Parts split8_nearest(const Row8<float> &q) {
+  float f[8], rest[8];
+  q.get(f);
+  Parts out;
+  float odd = 0.0f;                                // NaN if a part is not finite
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t p = pack_bf16(f[2 * i], f[2 * i + 1]);
+    out.v[0][i] = p;
+    rest[2 * i] = f[2 * i] - bf16_lo(p);
+    rest[2 * i + 1] = f[2 * i + 1] - bf16_hi(p);
+    odd += rest[2 * i] * 0.0f + rest[2 * i + 1] * 0.0f;
+    p = pack_bf16(rest[2 * i], rest[2 * i + 1]);
+    out.v[1][i] = p;
+    out.v[2][i] = pack_bf16(rest[2 * i] - bf16_lo(p), rest[2 * i + 1] - bf16_hi(p));
+  }
+  // (an Inf or NaN, or a value that rounds beyond bf16's largest)
+  if (odd != odd) return split8((f32x4_t)q.a, (f32x4_t)q.b);
+  return out;
+}
+
+// A workgroup's tile is 64 FN columns of dy (n) by 64 FK columns of x, two by
+// two waves; every group's tiles are written, zeros for a group without rows.
+template <typename D, typename X, int FN, int FK, int TOKENS>
+__global__ __launch_bounds__(kThreads) void k_grouped_wgrad(Groups g, Rows<D> dy, Rows<X> x, void *dw, int dw_bf16,
+                                                            int64_t N, int64_t K, int tiles_n, int tiles_k) {
+  constexpr int kDP = sizeof(D) == 2 ? 1 : 3, kXP = sizeof(X) == 2 ? 1 : 3;
+  constexpr int TN = 64 * FN, TK = 64 * FK;
+  constexpr int kRowD = TN * 2 + 32, kRowX = TK * 2 + 32;            // bytes of a row in LDS
+  constexpr int kPartD = TOKENS * kRowD, kPartX = TOKENS * kRowX;
+  constexpr int kBuffer = kDP * kPartD + kXP * kPartX;
+  constexpr int kDL = TOKENS * (TN / 8) / kThreads, kXL = TOKENS * (TK / 8) / kThreads;
+  __shared__ __align__(16) char lds[2 * kBuffer];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  const int tiles = tiles_n * tiles_k, total = tiles * g.count;
+  const int quota = (total + kXcds - 1) / kXcds;
+  const int index = (int)(blockIdx.x % kXcds) * quota + (int)(blockIdx.x / kXcds);
+  if ((int)(blockIdx.x / kXcds) >= quota || index >= total) return;
+  const int e = index / tiles, at = index % tiles;
+  const int per = 8 * tiles_k, first_n = at / per * 8, gsz = min(tiles_n - first_n, 8);
+  const int64_t n0 = (int64_t)(first_n + at % per % gsz) * TN, k0 = (int64_t)(at % per / gsz) * TK;
+  const int64_t begin = g.at(e), end = max(g.at(e + 1), begin);
+  const bool inside = n0 + TN <= N && k0 + TK <= K;
+  const int stages = (int)((end - begin + TOKENS - 1) / TOKENS);
+
+  Row8<D> dreg[kDL];
+  Row8<X> xreg[kXL];
+  const auto load = [&](int s) {
+    const int64_t t0 = begin + (int64_t)s * TOKENS;
+    if (inside && t0 + TOKENS <= end) {
+#pragma unroll
+      for (int i = 0; i < kDL; ++i) {
+        const int p = tid + i * kThreads;
+        dreg[i].load(dy.p + (t0 + p / (TN / 8)) * dy.ld + n0 + p % (TN / 8) * 8);
+      }
+#pragma unroll
+      for (int i = 0; i < kXL; ++i) {
+        const int p = tid + i * kThreads;
+        xreg[i].load(x.p + (t0 + p / (TK / 8)) * x.ld + k0 + p % (TK / 8) * 8);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kDL; ++i) {
+        const int p = tid + i * kThreads;
+        const int64_t row = t0 + p / (TN / 8);
+        load_row8(dreg[i], dy.p + row * dy.ld, n0 + p % (TN / 8) * 8, row < end ? N : 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kXL; ++i) {
+        const int p = tid + i * kThreads;
+        const int64_t row = t0 + p / (TK / 8);
+        load_row8(xreg[i], x.p + row * x.ld, k0 + p % (TK / 8) * 8, row < end ? K : 0);
+      }
+    }
+  };
+  const auto put_one = [&](char *to, int part, const auto &q) {
+    if constexpr (sizeof(q) == 16) {
+      *reinterpret_cast<u32x4_t *>(to) = q.r;
+    } else {
+      const Parts v = split8_nearest(q);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x4_t *>(to + p * part) = v.v[p];
+    }
+  };
+  const auto put = [&](int s) {
+    char *const buf = lds + (s & 1) * kBuffer;
+#pragma unroll
+    for (int i = 0; i < kDL; ++i) {
+      const int p = tid + i * kThreads;
+      put_one(buf + p / (TN / 8) * kRowD + p % (TN / 8) * 16, kPartD, dreg[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kXL; ++i) {
+      const int p = tid + i * kThreads;
+      put_one(buf + kDP * kPartD + p / (TK / 8) * kRowX + p % (TK / 8) * 16, kPartX, xreg[i]);
+    }
+  };
+
+  float16_t acc[FN][FK];
+#pragma unroll
+  for (int f = 0; f < FN; ++f)
+#pragma unroll
+    for (int q = 0; q < FK; ++q)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[f][q][i] = 0.0f;
+  // a lane's 8 rows (8 h .. 8 h + 7 of an MFMA's 16) of its column of a
+  // fragment of 32, by two reads; it names 4 columns of one row
+  const int col = 16 * ((lane >> 4) & 1) + 4 * (lane & 3), trow = 8 * (lane >> 5) + ((lane >> 2) & 3);
+  const auto column = [&](const char *from, int pitch) {
+    const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)from);
+    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(from + 4 * pitch));
+    return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  const auto products = [&](int s) {
+    const char *const dbuf = lds + (s & 1) * kBuffer + trow * kRowD + ((wave >> 1) * (32 * FN) + col) * 2;
+    const char *const xbuf = lds + (s & 1) * kBuffer + kDP * kPartD + trow * kRowX + ((wave & 1) * (32 * FK) + col) * 2;
+#pragma unroll
+    for (int ks = 0; ks < TOKENS / 16; ++ks) {
+      bf16x8_t a[kDP][FN], b[kXP][FK];
+#pragma unroll
+      for (int p = 0; p < kDP; ++p)
+#pragma unroll
+        for (int f = 0; f < FN; ++f) a[p][f] = column(dbuf + p * kPartD + ks * 16 * kRowD + f * 64, kRowD);
+#pragma unroll
+      for (int p = 0; p < kXP; ++p)
+#pragma unroll
+        for (int f = 0; f < FK; ++f) b[p][f] = column(xbuf + p * kPartX + ks * 16 * kRowX + f * 64, kRowX);
+#pragma unroll
+      for (int p = 0; p < kDP; ++p)
+#pragma unroll
+        for (int q = 0; q < kXP; ++q) {
+          if (p + q > 2) continue;
+#pragma unroll
+          for (int f = 0; f < FN; ++f)
+#pragma unroll
+            for (int k = 0; k < FK; ++k)
+              acc[f][k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[p][f], b[q][k], acc[f][k], 0, 0, 0);
+        }
+    }
+  };
+
+  if (stages > 0) {
+    load(0);
+    put(0);
+    if (stages > 1) load(1);
+    __syncthreads();
+    for (int s = 0; s < stages; ++s) {
+      products(s);
+      if (s + 1 < stages) put(s + 1);
+      if (s + 2 < stages) load(s + 2);
+      __syncthreads();
+    }
+  }
+
+  // register i of a fragment is row 8 (i / 4) + 4 h + i % 4, the lane its column
+  const int64_t base = (int64_t)e * N;
+#pragma unroll
+  for (int f = 0; f < FN; ++f)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int64_t n = n0 + (wave >> 1) * (32 * FN) + 32 * f + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
+      if (n >= N) continue;
+#pragma unroll
+      for (int q = 0; q < FK; ++q) {
+        const int64_t k = k0 + (wave & 1) * (32 * FK) + 32 * q + (lane & 31);
+        if (k >= K) continue;
+        if (dw_bf16) ((uint16_t *)dw)[(base + n) * K + k] = (uint16_t)pack_bf16(acc[f][q][i], 0.0f);
+        else ((float *)dw)[(base + n) * K + k] = acc[f][q][i];
+      }
+    }
+}
+
+template <typename D, typename X>
+hipError_t wgrad(const Groups &g, const Rows<D> &dy, const Rows<X> &x, void *dw, int dw_bf16, int64_t N, int64_t K,
+                 hipStream_t stream) {
+  constexpr bool narrow = sizeof(D) + sizeof(X) == 4;
+  constexpr int F = narrow ? 4 : 2, kTokens = narrow ? 64 : 32;
+  const int64_t tn = (N + 64 * F - 1) / (64 * F), tk = (K + 64 * F - 1) / (64 * F);
+  k_grouped_wgrad<D, X, F, F, kTokens><<<(unsigned)((tn * tk * g.count + kXcds - 1) / kXcds * kXcds), kThreads, 0, stream>>>(
+      g, dy, x, dw, dw_bf16, N, K, (int)tn, (int)tk);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_grouped_wgrad(const GroupedWgrad &p, hipStream_t stream) {
+  if (p.n == 0 || p.k == 0) return hipSuccess;
+  const Groups g = {p.offsets, p.index_bits == 64, (int)p.experts, p.rows};
+  const int b = p.dw_dtype == 1;
+  const auto run = [&](auto *d, auto *x) {
+    using D = std::remove_const_t<std::remove_pointer_t<decltype(d)>>;
+    using X = std::remove_const_t<std::remove_pointer_t<decltype(x)>>;
+    return wgrad<D, X>(g, {d, p.lddy}, {x, p.ldx}, p.dw, b, p.n, p.k, stream);
+  };
+  if (p.dy_dtype == 1 && p.x_dtype == 1) return run((const uint16_t *)p.dy, (const uint16_t *)p.x);
+  if (p.dy_dtype == 1) return run((const uint16_t *)p.dy, (const float *)p.x);
+  if (p.x_dtype == 1) return run((const float *)p.dy, (const uint16_t *)p.x);
+  return run((const float *)p.dy, (const float *)p.x);
+}
+
+int64_t grouped_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t rows, bool f32) { return 0; }
+
+hipError_t launch_grouped(const GroupedProduct &p, hipStream_t stream) {
+  if (p.n == 0 || p.rows == 0) return hipSuccess;
+  const int64_t block = p.mx ? 32 : 16, rows = p.transposed ? 1 : p.n;
+  const int64_t pitch = p.transposed ? p.experts * p.k : p.k, step = rows * p.k;
+  const Stack w = {p.codes, p.scales, p.meta, p.n, p.k, pitch / 2, step / 2, pitch / block, step / block};
+  const Groups g = {p.offsets, p.index_bits == 64, (int)p.experts, p.rows};
+  const int yb = p.y_dtype == 1;
+  if (p.x_dtype == 1) {
+    const Rows<uint16_t> x = {(const uint16_t *)p.x, p.ldx};
+    return p.mx ? grouped_x<true>(w, g, x, p.y, yb, p.ldy, p.fill, stream)
+                : grouped_x<false>(w, g, x, p.y, yb, p.ldy, p.fill, stream);
+  }
+  const Rows<float> x = {(const float *)p.x, p.ldx};
+  return p.mx ? grouped_x<true>(w, g, x, p.y, yb, p.ldy, p.fill, stream)
+              : grouped_x<false>(w, g, x, p.y, yb, p.ldy, p.fill, stream);
+}
+
+}  // namespace nvfp4

@@ -42,6 +42,7 @@
 #include "gemm_common.h"
 #include "nvfp4_device.h"
 #include "nvfp4_kernels.h"
+#include "operands.h"
 #include "row_common.h"
 
 #include <algorithm>
@@ -51,65 +52,12 @@ namespace nvfp4 {
 
 namespace {
 
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_a8 __attribute__((ext_vector_type(4), aligned(8)));
-typedef uint16_t u16_a1 __attribute__((aligned(1)));
 typedef uint32_t u32_a1 __attribute__((aligned(1)));
 typedef uint32_t u32x2_a1 __attribute__((ext_vector_type(2), aligned(1)));
 
 // ------------------------------------------------------------- operands --
-
-// The scales of a lane's 32 k, as loaded and as two factors (k 0-15, 16-31).
-template <bool MX> struct Scale;
-template <> struct Scale<false> {
-  static constexpr int kPerByte = 16;
-  uint32_t raw;
-  __device__ __forceinline__ void load(const uint8_t *p) { raw = *reinterpret_cast<const u16_a1 *>(p); }
-  __device__ __forceinline__ float lo() const { return __builtin_amdgcn_cvt_f32_fp8((int)raw, 0); }
-  __device__ __forceinline__ float hi() const { return __builtin_amdgcn_cvt_f32_fp8((int)raw, 1); }
-};
-template <> struct Scale<true> {
-  static constexpr int kPerByte = 32;
-  uint32_t raw;
-  __device__ __forceinline__ void load(const uint8_t *p) { raw = *p; }
-  // 2^(e - 127); e = 0 is the denormal 2^-127 and e = 255 NaN (both by the next bit below the exponent's)
-  __device__ __forceinline__ float lo() const {
-    return __uint_as_float(raw << 23 | (raw - 1 < 254 ? 0u : 0x00400000u));
-  }
-  __device__ __forceinline__ float hi() const { return lo(); }
-  // From 253 on a weight, at most 6 times as large, may pass bf16's range.  A
-  // quarter of the scale, 2^-129 to 2^125, keeps all weights in it (the
-  // smallest as denormals, exact).
-  static constexpr uint32_t kFar = 253;
-  __device__ __forceinline__ float quarter() const {
-    return raw == 255 ? lo() : __builtin_amdgcn_ldexpf(1.0f, (int)raw - 129);
-  }
-};
-
-// 8 codes (one word) as 8 bf16: NVFP4 codes times the block scale s (exact
-// in f32 and in bf16), MXFP4 by the conversion's own power-of-two scale.
-template <bool MX> __device__ __forceinline__ bf16x8_t decode8(uint32_t w, float s) {
-  u32x4_t v;
-  if (MX) {
-    v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
-    v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
-    v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
-    v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
-  } else {
-    const float2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
-    const float2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-    const float2_t c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
-    const float2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-    v[0] = pack_bf16(a.x * s, a.y * s);
-    v[1] = pack_bf16(b.x * s, b.y * s);
-    v[2] = pack_bf16(c.x * s, c.y * s);
-    v[3] = pack_bf16(d.x * s, d.y * s);
-  }
-  return __builtin_bit_cast(bf16x8_t, v);
-}
 
 // The same as 8 f16, where every q * S is exact, too: one conversion and one
 // packed product for two weights, half of what the bf16 form takes.
@@ -174,43 +122,6 @@ constexpr int kTurnBytes = 4096; // 16 columns x 128 k of bf16
 // columns a token, the parts hi, mid and lo, so that one MFMA serves five
 // tokens and the parts are added at the end.
 template <typename X> constexpr int columns() { return sizeof(X) == 2 ? 1 : 3; }
-
-// The three bf16 parts of 8 float32 values, a pair in each word.
-struct Parts {
-  u32x4_t v[3];
-};
-__device__ __forceinline__ Parts split8(const f32x4_t &a, const f32x4_t &b) {
-  constexpr uint32_t kHigh = 0xFFFF0000u;
-  const float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-  uint32_t hi[8];
-  float r[8];
-  float odd = 0.0f;                                  // NaN if a remainder is, so where an x is Inf or NaN
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    hi[i] = __float_as_uint(f[i]) & kHigh;
-    r[i] = f[i] - __uint_as_float(hi[i]);
-    odd += r[i];
-  }
-  if (odd != odd) {
-    // an Inf or NaN goes whole into the first part (with the quiet bit set
-    // for a NaN, whose payload may lie below), the others are 0 then
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (f[i] != f[i]) hi[i] |= 0x00400000u;
-      if ((__float_as_uint(f[i]) & 0x7F800000u) == 0x7F800000u) r[i] = 0.0f;
-    }
-  }
-  Parts out;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t r0 = __float_as_uint(r[2 * i]), r1 = __float_as_uint(r[2 * i + 1]);
-    const float lo0 = r[2 * i] - __uint_as_float(r0 & kHigh), lo1 = r[2 * i + 1] - __uint_as_float(r1 & kHigh);
-    out.v[0][i] = __builtin_amdgcn_perm(hi[2 * i + 1], hi[2 * i], 0x07060302u);
-    out.v[1][i] = __builtin_amdgcn_perm(r1, r0, 0x07060302u);
-    out.v[2][i] = __builtin_amdgcn_perm(__float_as_uint(lo1), __float_as_uint(lo0), 0x07060302u);
-  }
-  return out;
-}
 
 // A workgroup holds the columns of all its tokens over its range of K in
 // registers -- each wave a slice of SW steps -- and walks tiles of 16 weight

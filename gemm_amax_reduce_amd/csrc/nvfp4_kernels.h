@@ -113,6 +113,44 @@ hipError_t launch_matvec(bool mx, const uint8_t *codes, const uint8_t *scales, c
                          const void *x, int x_dtype, int64_t tokens, int64_t ldx, void *y, int y_dtype, int64_t ldy,
                          void *ws, hipStream_t stream);
 
+// y = x w_e^T for the rows of each group e, weights in NVFP4 or (mx) MXFP4:
+// [experts * n][k], or transposed [n][experts * k].  fill: zeros in the rows
+// that no group has.
+struct GroupedProduct {
+  bool mx, transposed;
+  const uint8_t *codes, *scales;
+  const float *meta;
+  int64_t experts, n, k;
+  const void *x;
+  int x_dtype;
+  int64_t rows, ldx;
+  const void *offsets;
+  int index_bits;
+  void *y;
+  int y_dtype;
+  int64_t ldy;
+  int fill;
+  void *ws;                    // grouped_workspace_bytes, 16-byte aligned
+};
+int64_t grouped_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t rows, bool f32);
+hipError_t launch_grouped(const GroupedProduct &p, hipStream_t stream);
+
+// dw[e] = the sum over the rows t of group e of dy[t] x[t]^T, [experts][n][k].
+struct GroupedWgrad {
+  int64_t experts, n, k;
+  const void *dy;
+  int dy_dtype;
+  int64_t lddy;
+  const void *x;
+  int x_dtype;
+  int64_t rows, ldx;
+  const void *offsets;
+  int index_bits;
+  void *dw;
+  int dw_dtype;
+};
+hipError_t launch_grouped_wgrad(const GroupedWgrad &p, hipStream_t stream);
+
 // Distillation from a teacher's top logits: with stats, loss and lse are
 // formed from z; without, lse is read.  dz (with weight) may be null when
 // stats is set.  workspace: distill_workspace_bytes, 8-byte aligned.

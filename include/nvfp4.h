@@ -513,6 +513,58 @@ int mxfp4_matvec(const mxfp4_tensor *w, const void *x, int x_dtype, int64_t toke
 int64_t nvfp4_matvec_workspace_bytes(int64_t n, int64_t k, int64_t tokens, int x_dtype);
 
 /*
+ * nvfp4_grouped_matmul, mxfp4_grouped_matmul -- matrix products grouped by
+ * expert: rows of unquantized activations in ragged groups, each with its own
+ * 4-bit weights (as nvfp4_matvec's), the layers of a mixture of experts:
+ *   y[t][n] = sum_k x[t][k] W_e[n][k]   for offsets[e] <= t < offsets[e + 1]
+ *  w       : the stack of all experts' weights, one tensor: with transposed
+ *            == 0 [outer = experts * N][k = K], expert after expert; with
+ *            transposed == 1 [outer = N][k = experts * K], expert e's columns
+ *            from e * K on, as the quantizers write the stack [experts * K][N]
+ *            on axis 0 -- the form for the data gradient dx = dy W.
+ *            K % 16 == 0 (MXFP4: 32).
+ *  x       : device, row-major [rows][ldx], x_dtype, ldx >= K, aligned to its
+ *            element only.
+ *  offsets : device, int32 or int64 (index_bits 32 or 64), [experts + 1],
+ *            not decreasing, 0 <= offsets[0] and offsets[experts] <= rows.
+ *            Not checked; values outside are taken as the nearest inside, and
+ *            where they decrease the result is unspecified (nothing outside
+ *            x and y is touched).  experts: 1 .. 2^20.
+ *  y       : device, row-major [rows][ldy], y_dtype, ldy >= N; must not
+ *            overlap x (NVFP4_ERR_SHAPE; their rows may lie side by side).
+ *  zero_rest : 0: rows of y that belong to no group are left as they are;
+ *            1: they become zeros.
+ *  workspace : device, at least nvfp4_grouped_matmul_workspace_bytes(experts,
+ *            N, K, rows, x_dtype) bytes (for both formats), 16-byte aligned,
+ *            contents ignored and overwritten; often 0, and NULL will do then.
+ *            Calls that share one must not overlap in time.
+ *  ceil(N / 128) * (rows / 32 + min(experts, rows)) <= 2^24 - 8, K <= 2^25 - 16.
+ * A group without rows costs nothing, and its weights are not read.  Weights
+ * and bf16 x enter the product exactly; a float32 x to within 2^-133 of its
+ * value.  Sums are binary32.  K == 0 gives zeros.  An MXFP4 scale of 255 is
+ * NaN.  Deterministic on one device.  Enqueues one kernel, or two where there
+ * is a workspace.
+ *
+ * nvfp4_grouped_wgrad -- the gradient of the experts' weights,
+ *   dw[e][n][k] = sum over offsets[e] <= t < offsets[e + 1] of dy[t][n] x[t][k]
+ * dw: device, dw_dtype [experts][n][k], written whole (zeros for a group
+ * without rows); must not overlap dy or x.  bf16 products are exact; with a
+ * float32 operand products are off by at most 2^-23 of their magnitude, and
+ * those with an infinity are infinite or NaN.  Sums are binary32.  experts * ceil(n / 128) * ceil(k / 128) <= 2^24 - 8.
+ * Deterministic.  Enqueues one kernel.
+ */
+int nvfp4_grouped_matmul(const nvfp4_tensor *w, int transposed, const void *x, int x_dtype, int64_t rows, int64_t ldx,
+                         const void *offsets, int index_bits, int64_t experts, void *y, int y_dtype, int64_t ldy,
+                         int zero_rest, void *workspace, int64_t workspace_bytes, void *hip_stream);
+int mxfp4_grouped_matmul(const mxfp4_tensor *w, int transposed, const void *x, int x_dtype, int64_t rows, int64_t ldx,
+                         const void *offsets, int index_bits, int64_t experts, void *y, int y_dtype, int64_t ldy,
+                         int zero_rest, void *workspace, int64_t workspace_bytes, void *hip_stream);
+int64_t nvfp4_grouped_matmul_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t rows, int x_dtype);
+int nvfp4_grouped_wgrad(const void *dy, int dy_dtype, int64_t lddy, const void *x, int x_dtype, int64_t ldx,
+                        int64_t rows, int64_t n, int64_t k, const void *offsets, int index_bits, int64_t experts,
+                        void *dw, int dw_dtype, void *hip_stream);
+
+/*
  * nvfp4_distill_topk -- the distillation loss of a student's logits against
  * a teacher's best logits, by which a model brought to 4 bits is trained:
  *   p    = softmax(teacher / temperature) over the row's valid entries
