@@ -22,7 +22,7 @@ __all__ = ["NVFP4Tensor", "NVFP4Error", "nvfp4_quantize", "nvfp4_rht_quantize", 
            "nvfp4_dequantize", "nvfp4_gemm", "nvfp4_gemm_ws", "nvfp4_gemm_noalloc", "gemm_workspace",
            "nvfp4_layer_norm", "nvfp4_layer_norm_backward", "nvfp4_rms_norm", "mxfp8_rms_norm",
            "nvfp4_rms_norm_backward", "nvfp4_matvec", "mxfp4_matvec", "nvfp4_grouped_matmul", "mxfp4_grouped_matmul",
-           "nvfp4_grouped_wgrad", "nvfp4_distill_topk",
+           "nvfp4_grouped_wgrad", "nvfp4_adapters", "nvfp4_adapters_backward", "nvfp4_distill_topk",
            "nvfp4_distill_topk_backward", "nvfp4_distill_topk_step",
            "lib", "LIB_PATH", "F32", "BF16", "RNE", "SR"]
 
@@ -57,7 +57,8 @@ EXPORTS = ("nvfp4_quantize", "nvfp4_rht_quantize", "nvfp4_amax", "nvfp4_quantize
            "nvfp4_rms_norm", "mxfp8_rms_norm", "nvfp4_rms_norm_backward", "nvfp4_rms_norm_backward_workspace_bytes",
            "nvfp4_matvec", "mxfp4_matvec",
            "nvfp4_matvec_workspace_bytes", "nvfp4_grouped_matmul", "mxfp4_grouped_matmul",
-           "nvfp4_grouped_matmul_workspace_bytes", "nvfp4_grouped_wgrad", "nvfp4_distill_topk", "nvfp4_distill_topk_backward",
+           "nvfp4_grouped_matmul_workspace_bytes", "nvfp4_grouped_wgrad", "nvfp4_adapters", "nvfp4_adapters_backward",
+           "nvfp4_adapters_backward_workspace_bytes", "nvfp4_distill_topk", "nvfp4_distill_topk_backward",
            "nvfp4_distill_topk_step", "nvfp4_distill_topk_workspace_bytes", "nvfp4_probe_mfma", "nvfp4_probe_philox", "nvfp4_status_string")
 
 
@@ -136,6 +137,14 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_grouped_matmul_workspace_bytes.restype = i64
         L.nvfp4_grouped_wgrad.argtypes = [vp, ci, i64, vp, ci, i64, i64, i64, i64, vp, ci, i64, vp, ci, vp]
         L.nvfp4_grouped_wgrad.restype = ci
+        low = [vp, vp, ci, i64, i64, i64, vp, vp, vp, ci, i64]               # adapters, scale, segments
+        L.nvfp4_adapters.argtypes = [vp, ci, i64, i64, i64] + low + [vp, ci, i64, vp, ci, i64, vp, vp]
+        L.nvfp4_adapters.restype = ci
+        L.nvfp4_adapters_backward.argtypes = ([vp, ci, i64, vp, ci, i64, i64, i64, vp] + low +
+                                              [vp, ci, i64, vp, ci, i64, vp, vp, ci, vp, i64, vp])
+        L.nvfp4_adapters_backward.restype = ci
+        L.nvfp4_adapters_backward_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, i64, ci]
+        L.nvfp4_adapters_backward_workspace_bytes.restype = i64
         rows = [vp, ci, i64, i64, i64, vp, ci, vp, ci, i64, cf]       # logits, indices, teacher, temperature
         L.nvfp4_distill_topk.argtypes = rows + [vp, vp, vp, i64, vp]
         L.nvfp4_distill_topk.restype = ci
@@ -965,6 +974,100 @@ def nvfp4_grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor
         _check(lib().nvfp4_grouped_wgrad(dy.data_ptr(), _dtype_code(dy), lddy, x.data_ptr(), _dtype_code(x), ldx, rows, n,
                                          k, op, bits, experts, dp, code, _current_handle(dev)), "nvfp4_grouped_wgrad")
     return out
+
+
+def _adapter_args(a, b, offsets, index, scale, device):
+    """Checks the adapters and their segments; returns (n, k, rank, the C
+    arguments from a to segments)."""
+    for t, name in ((a, "a"), (b, "b")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise NVFP4Error(f"{name} must be a 3-D tensor")
+    adapters, rank, k = a.shape
+    n = b.shape[1]
+    if b.shape[0] != adapters or b.shape[2] != rank:
+        raise NVFP4Error(f"b must have shape ({adapters}, N, {rank}), got {tuple(b.shape)}")
+    if b.dtype != a.dtype:
+        raise NVFP4Error(f"a and b must have the same dtype, got {a.dtype} and {b.dtype}")
+    code = _dtype_code(a)
+    op, bits, segments = _group_args(offsets, device)
+    if not isinstance(index, torch.Tensor) or index.dtype != offsets.dtype or tuple(index.shape) != (segments,):
+        raise NVFP4Error(f"index must be a vector of {segments} elements of offsets' dtype {offsets.dtype}")
+    sp = None if scale is None else _vector(scale, "scale", torch.float32, adapters, device)
+    return n, k, rank, [_vector(a, "a", a.dtype, adapters * rank * k, device),
+                        _vector(b, "b", b.dtype, adapters * n * rank, device), code, adapters, rank, n, sp, op,
+                        _vector(index, "index", index.dtype, segments, device), bits, segments]
+
+
+def _base_args(base, rows, cols, device):
+    """(address or None, dtype code, leading dimension)."""
+    if base is None:
+        return None, F32, max(cols, 1)
+    ld = _require_matrix(base, "base", device, (rows, cols))
+    return base.data_ptr(), _dtype_code(base), ld
+
+
+def nvfp4_adapters(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor, index: torch.Tensor,
+                   scale: torch.Tensor | None = None, base: torch.Tensor | None = None, out_dtype=None,
+                   out: torch.Tensor | None = None, stream=None):
+    """Low-rank adapters beside a shared projection: (y, u) with u = A x f32
+    [rows, rank] and y = base + scale B u, for the rows offsets[i] ..
+    offsets[i + 1] - 1 of x [rows, K] (f32/bf16) and adapter index[i] (-1 =
+    none: y = base, u = 0).  a [adapters, rank, K], b [adapters, N, rank]
+    (f32/bf16), scale f32 [adapters]; base [rows, N], the shared projection's
+    result, or None (0); offsets and index int32/int64 on the GPU.  y in
+    `out_dtype` (base's by default, else x's), new or in `out`, which may be
+    base (see include/nvfp4.h)."""
+    ldx = _require_matrix(x, "x")
+    dev = x.device
+    n, k, rank, weights = _adapter_args(a, b, offsets, index, scale, dev)
+    rows = x.shape[0]
+    if x.shape[1] != k:
+        raise NVFP4Error(f"x must have {k} columns, got {x.shape[1]}")
+    bp, bcode, ldb = _base_args(base, rows, n, dev)
+    if out_dtype is None:
+        out_dtype = (x if base is None else base).dtype
+    ycode = _out_code(out_dtype)
+    with _on(dev, stream):
+        y = torch.empty((rows, n), dtype=out_dtype, device=dev) if out is None else out
+        ldy = max(n, 1) if out is None else _require_matrix_out(y, rows, n, out_dtype, dev)
+        u = torch.empty((rows, rank), dtype=torch.float32, device=dev)
+        _check(lib().nvfp4_adapters(x.data_ptr(), _dtype_code(x), rows, k, ldx, *weights, bp, bcode, ldb, y.data_ptr(),
+                                    ycode, ldy, u.data_ptr(), _current_handle(dev)), "nvfp4_adapters")
+    return y, u
+
+
+def nvfp4_adapters_backward(dy: torch.Tensor, x: torch.Tensor, u: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+                            offsets: torch.Tensor, index: torch.Tensor, scale: torch.Tensor | None = None,
+                            base: torch.Tensor | None = None, grad_dtype=torch.float32,
+                            out: torch.Tensor | None = None, stream=None):
+    """The gradients of nvfp4_adapters: (dx, da, db).  dx [rows, K] in x's
+    dtype is base (the shared projection's own gradient, or 0) plus the
+    adapters' part, new or in `out`, which may be base; da and db in
+    `grad_dtype`, of a's and b's shapes."""
+    ldx = _require_matrix(x, "x")
+    dev = x.device
+    n, k, rank, weights = _adapter_args(a, b, offsets, index, scale, dev)
+    rows = x.shape[0]
+    if x.shape[1] != k:
+        raise NVFP4Error(f"x must have {k} columns, got {x.shape[1]}")
+    lddy = _require_matrix(dy, "dy", dev, (rows, n))
+    up = _vector(u, "u", torch.float32, rows * rank, dev)
+    bp, bcode, ldb = _base_args(base, rows, k, dev)
+    gcode = _out_code(grad_dtype)
+    need = lib().nvfp4_adapters_backward_workspace_bytes(rows, n, k, rank, a.shape[0], index.shape[0], weights[2])
+    if need < 0:
+        _check(need, "nvfp4_adapters_backward")
+    with _on(dev, stream):
+        dx = x.new_empty((rows, k)) if out is None else out
+        lddx = max(k, 1) if out is None else _require_matrix_out(dx, rows, k, x.dtype, dev)
+        da = torch.empty(a.shape, dtype=grad_dtype, device=dev)
+        db = torch.empty(b.shape, dtype=grad_dtype, device=dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        _check(lib().nvfp4_adapters_backward(dy.data_ptr(), _dtype_code(dy), lddy, x.data_ptr(), _dtype_code(x), rows, k,
+                                             ldx, up, *weights, bp, bcode, ldb, dx.data_ptr(), _dtype_code(dx), lddx,
+                                             da.data_ptr(), db.data_ptr(), gcode, _ptr(ws), need, _current_handle(dev)),
+               "nvfp4_adapters_backward")
+    return dx, da, db
 
 
 def _distill_args(logits, indices, teacher, temperature):

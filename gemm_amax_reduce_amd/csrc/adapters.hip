@@ -1,0 +1,547 @@
+// adapters.hip -- low-rank adapters of many requests at once, beside a shared
+// projection, for gfx950: rows come in segments (requests), each with an
+// adapter (A [r][K], B [N][r], scale s) or none,
+//
+//   u = A x,  y = base + s B u
+//
+// and the backward pass,
+//
+//   g = s B^T dy,  dx = base + A^T g,  dA = sum g x^T,  dB = sum s dy u^T.
+//
+// The rank is small, so each product reads its wide matrix once and is bound
+// by that: x and dy into r numbers a row (k_shrink), r numbers a row into base
+// and y (k_expand), and both matrices into sums over rows (k_grad).  u and g
+// are float32; every product runs on the bf16 MFMA with float32 operands as
+// three bf16 parts each (about what binary32 products keep).
+#include "groups.h"
+#include "nvfp4_kernels.h"
+#include "operands.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace nvfp4 {
+
+namespace {
+
+// The adapter of a segment: index[e], -1 where it names none.
+struct Segments {
+  Groups g;                // with the rows of no segment as the first and the last group
+  const void *index;
+  int adapters;
+  __device__ __forceinline__ int adapter(int e) const {
+    if (e < 1 || e >= g.count - 1) return -1;
+    const int64_t v = g.is64 ? ((const int64_t *)index)[e - 1] : (int64_t)((const int32_t *)index)[e - 1];
+    return v >= 0 && v < adapters ? (int)v : -1;
+  }
+};
+// The first segment from e on with that adapter and rows of its own between
+// `from` and `to`; count - 1 if there is none.
+__device__ __forceinline__ int next_of(const Segments &s, int adapter, int e, int64_t from, int64_t to) {
+  const int lane = threadIdx.x & 63;
+  for (; e < s.g.count - 1; e += 64) {
+    const int mine = e + lane;
+    bool hit = mine < s.g.count - 1 && s.adapter(mine) == adapter;
+    if (hit) hit = max(s.g.at(mine), from) < min(s.g.at(mine + 1), to);
+    const uint64_t found = __ballot(hit);
+    if (found) return __builtin_amdgcn_readfirstlane(e + (int)__builtin_ctzll(found));
+  }
+  return s.g.count - 1;
+}
+
+// --------------------------------------------------------------- shrink --
+
+// out[t][j] = scale sum_c x[t][c] w[a][j][c] for a tile of 16 rows, zeros for
+// those without an adapter.  The weights are the A operand of the 16x16x32
+// MFMA, so that a lane has 4 neighbouring ranks of a row; of 128 c a lane holds
+// 32 neighbours, 8 an MFMA.  The workgroup's waves take 128 c each in turn,
+// and their sums meet in LDS.
+constexpr int kChunk = 128;
+template <typename X, typename W, int RF>
+__global__ __launch_bounds__(RF > 4 ? 512 : 1024) void k_shrink(Segments s, const X *x, int64_t ldx, int64_t C, const W *w,
+                                                                int rank, const float *scale, float *out, int waves) {
+  extern __shared__ __align__(16) float sums[];        // [waves][16][16 RF]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row = lane & 15, quarter = lane >> 4;
+  const GroupTile t = find_tile(s.g, 16, 1, blockIdx.x);
+  if (t.e < 0) return;
+  const int64_t t0 = t.begin + 16 * (int64_t)t.local;
+  const int live = (int)min(t.end - t0, (int64_t)16);
+  const int a = s.adapter(t.e);
+  if (a < 0) {
+    for (int i = threadIdx.x; i < live * rank; i += 64 * waves) out[t0 * rank + i] = 0.0f;
+    return;
+  }
+  const X *xr = x + (t0 + min(row, live - 1)) * ldx;
+  const W *wr[RF];
+#pragma unroll
+  for (int f = 0; f < RF; ++f) wr[f] = w + ((int64_t)a * rank + min(16 * f + row, rank - 1)) * C;
+  f32x4_t acc[RF];
+#pragma unroll
+  for (int f = 0; f < RF; ++f) acc[f] = (f32x4_t){0, 0, 0, 0};
+  const auto step = [&](int64_t c0, auto whole) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t c = c0 + 32 * quarter + 8 * i;
+      Row8<X> xq;
+      Row8<W> wq[RF];
+      if (whole.value) xq.load(xr + c);
+      else load_row8(xq, xr, c, C);
+#pragma unroll
+      for (int f = 0; f < RF; ++f) {
+        if (whole.value) wq[f].load(wr[f] + c);
+        else load_row8(wq[f], wr[f], c, C);
+      }
+      Operand<X> xo;
+      xo.set(xq);
+#pragma unroll
+      for (int f = 0; f < RF; ++f) {
+        Operand<W> wo;
+        wo.set(wq[f]);
+        multiply16(acc[f], wo, xo);
+      }
+    }
+  };
+  int64_t c0 = (int64_t)wave * kChunk;
+#pragma unroll 2
+  for (; c0 + kChunk <= C; c0 += (int64_t)waves * kChunk) step(c0, std::true_type());
+  if (c0 < C) step(c0, std::false_type());
+  constexpr int kPitch = 16 * RF;
+#pragma unroll
+  for (int f = 0; f < RF; ++f)
+    *reinterpret_cast<f32x4_t *>(sums + (wave * 16 + row) * kPitch + 16 * f + 4 * quarter) = acc[f];
+  __syncthreads();
+  const float factor = scale ? scale[a] : 1.0f;
+  for (int i = threadIdx.x; i < live * rank; i += 64 * waves) {
+    const int at = i / rank * kPitch + i % rank;
+    float v = 0.0f;
+    for (int k = 0; k < waves; ++k) v += sums[k * 16 * kPitch + at];
+    out[t0 * rank + i] = v * factor;
+  }
+}
+
+// --------------------------------------------------------------- expand --
+
+// y[t][c] = base[t][c] + scale sum_j u[t][j] w[a][c][j] for 16 MT rows and 256
+// columns, 64 of them a wave.  The weights are the A operand with its rows
+// ordered so that a lane's results are 16 neighbouring columns of a row.
+template <typename W, int MT>
+__global__ __launch_bounds__(256) void k_expand(Segments s, const float *u, int rank, const W *w, const float *scale,
+                                                const void *base, int base_bf16, int64_t ldb, void *y, int y_bf16,
+                                                int64_t ldy, int64_t C, int tiles_c) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row = lane & 15, quarter = lane >> 4;
+  const GroupTile t = find_tile(s.g, 16 * MT, tiles_c, blockIdx.x);
+  if (t.e < 0) return;
+  const int64_t t0 = t.begin + 16 * MT * (int64_t)(t.local / tiles_c);
+  const int64_t c0 = (int64_t)(t.local % tiles_c) * 256 + 64 * wave, mine = c0 + 16 * quarter;
+  const int live = (int)min(t.end - t0, (int64_t)(16 * MT));
+  const int a = s.adapter(t.e);
+  if (c0 >= C || (a < 0 && base == y)) return;
+  float v[MT][16];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int64_t at = (t0 + min(16 * m + row, live - 1)) * ldb;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (!base) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[m][8 * i + j] = 0.0f;
+      } else if (base_bf16) {
+        Row8<uint16_t> q;
+        load_row8(q, (const uint16_t *)base + at, mine + 8 * i, C);
+        q.get(v[m] + 8 * i);
+      } else {
+        Row8<float> q;
+        load_row8(q, (const float *)base + at, mine + 8 * i, C);
+        q.get(v[m] + 8 * i);
+      }
+    }
+  }
+  if (a >= 0) {
+    f32x4_t acc[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int f = 0; f < 4; ++f) acc[m][f] = (f32x4_t){0, 0, 0, 0};
+    for (int j0 = 0; j0 < rank; j0 += 32) {
+      Operand<W> wo[4];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int64_t c = min(c0 + (row >> 2) * 16 + 4 * f + (row & 3), C - 1);
+        Row8<W> q;
+        load_row8(q, w + ((int64_t)a * C + c) * rank, j0 + 8 * quarter, rank);
+        wo[f].set(q);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        Row8<float> q;
+        load_row8(q, u + (t0 + min(16 * m + row, live - 1)) * rank, j0 + 8 * quarter, rank);
+        Operand<float> uo;
+        uo.set(q);
+#pragma unroll
+        for (int f = 0; f < 4; ++f) multiply16(acc[m][f], wo[f], uo);
+      }
+    }
+    const float factor = scale ? scale[a] : 1.0f;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[m][4 * f + i] = __builtin_fmaf(acc[m][f][i], factor, v[m][4 * f + i]);
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    if (16 * m + row >= live) continue;
+    const int64_t at = (t0 + 16 * m + row) * ldy;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (y_bf16) {
+        Row8<uint16_t> q;
+        q.set(v[m] + 8 * i);
+        store_row8(q, (uint16_t *)y + at, mine + 8 * i, C);
+      } else {
+        Row8<float> q;
+        q.set(v[m] + 8 * i);
+        store_row8(q, (float *)y + at, mine + 8 * i, C);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------ gradients --
+
+// Sums over the rows t of all segments of an adapter of x[t][c] g[t][j], x
+// with C columns, as [r][C] (dA) or, with TURN, [C][r] (dB).  Rows run along
+// the reduction: 32 of them a stage go to LDS as they lie and are fetched by
+// columns with transposing reads.  grid: (256 columns, adapters, shares of the
+// rows); with several shares partial sums go to partial[share][adapter][...].
+constexpr int kGradRows = 32, kGradCols = 256;
+template <typename X, int RF, bool TURN>
+__global__ __launch_bounds__(256) void k_grad(Segments s, const X *x, int64_t ldx, int64_t C, const float *g, int rank,
+                                              const float *scale, void *out, int out_bf16, float *partial) {
+  constexpr int kXP = Operand<X>::kParts;
+  constexpr int kRowX = kGradCols * 2 + 32, kRowG = 64 * RF + 32;
+  constexpr int kPartX = kGradRows * kRowX, kPartG = kGradRows * kRowG;
+  constexpr int kBuffer = kXP * kPartX + 3 * kPartG;
+  constexpr int kXL = kGradRows * (kGradCols / 8) / 256, kGL = (kGradRows * 4 * RF + 255) / 256;
+  __shared__ __align__(16) char lds[2 * kBuffer];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int a = blockIdx.y;
+  const int64_t c0 = (int64_t)blockIdx.x * kGradCols;
+  const int64_t from = s.g.rows * blockIdx.z / gridDim.z, to = s.g.rows * (blockIdx.z + 1) / gridDim.z;
+
+  // stages: 32 rows of a segment each
+  int e = next_of(s, a, 1, from, to);
+  int64_t at = 0, end = 0;
+  const auto enter = [&]() {
+    if (e < s.g.count - 1) {
+      at = max(s.g.at(e), from);
+      end = min(s.g.at(e + 1), to);
+    }
+  };
+  enter();
+  const auto more = [&]() { return e < s.g.count - 1; };
+  const auto advance = [&]() {
+    at += kGradRows;
+    if (at >= end) {
+      e = next_of(s, a, e + 1, from, to);
+      enter();
+    }
+  };
+  Row8<X> xr[kXL];
+  Row8<float> gr[kGL];
+  const auto load = [&]() {
+#pragma unroll
+    for (int i = 0; i < kXL; ++i) {
+      const int p = tid + i * 256;
+      const int64_t t = at + p / (kGradCols / 8);
+      load_row8(xr[i], x + t * ldx, c0 + p % (kGradCols / 8) * 8, t < end ? C : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kGL; ++i) {
+      const int p = tid + i * 256;
+      const int64_t t = at + p / (4 * RF);
+      load_row8(gr[i], g + t * rank, p % (4 * RF) * 8, t < end ? rank : 0);
+    }
+  };
+  const auto put = [&](int turn) {
+    char *const buf = lds + turn * kBuffer;
+#pragma unroll
+    for (int i = 0; i < kXL; ++i) {
+      const int p = tid + i * 256;
+      Operand<X> o;
+      o.set(xr[i]);
+#pragma unroll
+      for (int k = 0; k < kXP; ++k)
+        *reinterpret_cast<bf16x8_t *>(buf + k * kPartX + p / (kGradCols / 8) * kRowX + p % (kGradCols / 8) * 16) = o.v[k];
+    }
+#pragma unroll
+    for (int i = 0; i < kGL; ++i) {
+      const int p = tid + i * 256;
+      if (kGradRows * 4 * RF % 256 != 0 && p >= kGradRows * 4 * RF) continue;
+      Operand<float> o;
+      o.set(gr[i]);
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        *reinterpret_cast<bf16x8_t *>(buf + kXP * kPartX + k * kPartG + p / (4 * RF) * kRowG + p % (4 * RF) * 16) = o.v[k];
+    }
+  };
+  float16_t acc[RF][2];
+#pragma unroll
+  for (int f = 0; f < RF; ++f)
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[f][q][i] = 0.0f;
+  const int col = 16 * ((lane >> 4) & 1) + 4 * (lane & 3), trow = 8 * (lane >> 5) + ((lane >> 2) & 3);
+  const auto products = [&](int turn) {
+    const char *const xb = lds + turn * kBuffer + trow * kRowX + (64 * wave + col) * 2;
+    const char *const gb = lds + turn * kBuffer + kXP * kPartX + trow * kRowG + col * 2;
+#pragma unroll
+    for (int ks = 0; ks < kGradRows / 16; ++ks) {
+      bf16x8_t xo[kXP][2], go[3][RF];
+#pragma unroll
+      for (int p = 0; p < kXP; ++p)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) xo[p][q] = lds_column(xb + p * kPartX + ks * 16 * kRowX + q * 64, kRowX);
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int f = 0; f < RF; ++f) go[p][f] = lds_column(gb + p * kPartG + ks * 16 * kRowG + f * 64, kRowG);
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int k = 0; k < kXP; ++k) {
+          if (p + k > 2) continue;
+#pragma unroll
+          for (int f = 0; f < RF; ++f)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              acc[f][q] = TURN ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(xo[k][q], go[p][f], acc[f][q], 0, 0, 0)
+                               : __builtin_amdgcn_mfma_f32_32x32x16_bf16(go[p][f], xo[k][q], acc[f][q], 0, 0, 0);
+        }
+    }
+  };
+  if (more()) {
+    load();
+    int turn = 0;
+    put(0);
+    advance();
+    bool next = more();
+    if (next) load();
+    __syncthreads();
+    for (;;) {
+      products(turn);
+      if (!next) break;
+      put(turn ^ 1);
+      advance();
+      next = more();
+      if (next) load();
+      __syncthreads();
+      turn ^= 1;
+    }
+  }
+  const float factor = scale ? scale[a] : 1.0f;
+  const int64_t size = (int64_t)rank * C;
+  const int64_t first = gridDim.z > 1 ? ((int64_t)blockIdx.z * gridDim.y + a) * size : a * size;
+  // register i of a fragment is its row 8 (i / 4) + 4 h + i % 4, the lane its column
+#pragma unroll
+  for (int f = 0; f < RF; ++f)
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int down = 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3), over = lane & 31;
+        const int j = 32 * f + (TURN ? over : down);
+        const int64_t c = c0 + 64 * wave + 32 * q + (TURN ? down : over);
+        if (j >= rank || c >= C) continue;
+        const int64_t to_at = first + (TURN ? c * rank + j : j * C + c);
+        const float v = acc[f][q][i] * factor;
+        if (gridDim.z > 1) partial[to_at] = v;
+        else if (out_bf16) ((uint16_t *)out)[to_at] = (uint16_t)pack_bf16(v, 0.0f);
+        else ((float *)out)[to_at] = v;
+      }
+}
+
+// The shares' sums, in their order; zeros for an adapter that no segment has.
+__global__ __launch_bounds__(256) void k_grad_join(Segments s, const float *partial, int shares, int64_t size, void *out,
+                                                   int out_bf16) {
+  const int a = blockIdx.y;
+  const bool used = next_of(s, a, 1, 0, s.g.rows) < s.g.count - 1;
+  const int64_t all = size * s.adapters;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < size; i += (int64_t)gridDim.x * 256) {
+    float v = 0.0f;
+    if (used)
+      for (int z = 0; z < shares; ++z) v += partial[z * all + a * size + i];
+    if (out_bf16) ((uint16_t *)out)[a * size + i] = (uint16_t)pack_bf16(v, 0.0f);
+    else ((float *)out)[a * size + i] = v;
+  }
+}
+
+// out[a] = the transpose of in[a], [R][C], for the adapters that a segment has.
+template <typename W>
+__global__ __launch_bounds__(256) void k_turn(Segments s, const W *in, W *out, int64_t R, int64_t C, int tiles_r) {
+  __shared__ W tile[64][65];
+  const int a = blockIdx.y;
+  if (next_of(s, a, 1, 0, s.g.rows) == s.g.count - 1) return;
+  const int64_t r0 = (int64_t)(blockIdx.x % tiles_r) * 64, c0 = (int64_t)(blockIdx.x / tiles_r) * 64;
+  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+  for (int i = y; i < 64; i += 4)
+    if (r0 + i < R && c0 + x < C) tile[i][x] = in[((int64_t)a * R + r0 + i) * C + c0 + x];
+  __syncthreads();
+  for (int i = y; i < 64; i += 4)
+    if (c0 + i < C && r0 + x < R) out[((int64_t)a * C + c0 + i) * R + r0 + x] = tile[x][i];
+}
+
+// -------------------------------------------------------------- launches --
+
+template <typename X, typename W>
+void shrink(const Segments &s, const X *x, int64_t ldx, int64_t C, const W *w, int rank, const float *scale, float *out,
+            hipStream_t stream) {
+  const int64_t tiles = s.g.rows / 16 + std::min<int64_t>(s.g.count, s.g.rows);
+  const auto launch = [&](auto kernel, int rf) {
+    const int most = rf > 4 ? 8 : 16;
+    const int waves = (int)std::max<int64_t>(1, std::min<int64_t>(most, (C + kChunk - 1) / kChunk));
+    kernel<<<(unsigned)tiles, 64 * waves, (size_t)waves * 16 * 16 * rf * 4, stream>>>(s, x, ldx, C, w, rank, scale, out,
+                                                                                      waves);
+  };
+  if (rank <= 16) launch(k_shrink<X, W, 1>, 1);
+  else if (rank <= 32) launch(k_shrink<X, W, 2>, 2);
+  else if (rank <= 64) launch(k_shrink<X, W, 4>, 4);
+  else launch(k_shrink<X, W, 8>, 8);
+}
+
+template <typename W>
+void expand(const Segments &s, const float *u, int rank, const W *w, const float *scale, const void *base, int base_bf16,
+            int64_t ldb, void *y, int y_bf16, int64_t ldy, int64_t C, hipStream_t stream) {
+  const int tiles_c = (int)((C + 255) / 256);
+  const bool few = s.g.rows <= 32 * (int64_t)(s.g.count - 2);
+  const int64_t tile = few ? 16 : 64;
+  const int64_t tiles = s.g.rows / tile + std::min<int64_t>(s.g.count, s.g.rows);
+  const auto launch = [&](auto kernel) {
+    kernel<<<(unsigned)(tiles * tiles_c), 256, 0, stream>>>(s, u, rank, w, scale, base, base_bf16, ldb, y, y_bf16, ldy, C,
+                                                           tiles_c);
+  };
+  if (few) launch(k_expand<W, 1>);
+  else launch(k_expand<W, 4>);
+}
+
+// Shares of the rows that the gradient kernels cut a sum into: until there is
+// work for two rounds of the CUs, at least 256 rows each, and within 512 MB of
+// partial sums.
+int shares_of(int64_t rows, int64_t C, int64_t rank, int64_t adapters, int64_t segments) {
+  const int64_t work = (C + kGradCols - 1) / kGradCols * std::min(adapters, segments);
+  const int64_t want = std::min(2 * (int64_t)device_cus() / std::max<int64_t>(work, 1), rows / 256);
+  const int64_t room = ((int64_t)512 << 20) / std::max<int64_t>(1, adapters * rank * C * 4);
+  return (int)std::max<int64_t>(1, std::min(want, room));
+}
+
+template <typename X, bool TURN>
+void grad(const Segments &s, int64_t segments, const X *x, int64_t ldx, int64_t C, const float *g, int rank,
+          const float *scale, void *out, int out_bf16, float *partial, hipStream_t stream) {
+  const int shares = shares_of(s.g.rows, C, rank, s.adapters, segments);
+  const dim3 grid((unsigned)((C + kGradCols - 1) / kGradCols), (unsigned)s.adapters, (unsigned)shares);
+  const auto launch = [&](auto kernel) {
+    kernel<<<grid, 256, 0, stream>>>(s, x, ldx, C, g, rank, scale, out, out_bf16, partial);
+  };
+  if (rank <= 32) launch(k_grad<X, 1, TURN>);
+  else if (rank <= 64) launch(k_grad<X, 2, TURN>);
+  else launch(k_grad<X, 4, TURN>);
+  if (shares > 1) {
+    const int64_t size = rank * C;
+    k_grad_join<<<dim3((unsigned)std::min<int64_t>((size + 255) / 256, 1024), (unsigned)s.adapters), 256, 0, stream>>>(
+        s, partial, shares, size, out, out_bf16);
+  }
+}
+
+template <typename W>
+void turn(const Segments &s, const W *in, W *out, int64_t R, int64_t C, hipStream_t stream) {
+  const int64_t tr = (R + 63) / 64, tc = (C + 63) / 64;
+  k_turn<W><<<dim3((unsigned)(tr * tc), (unsigned)s.adapters), 256, 0, stream>>>(s, in, out, R, C, (int)tr);
+}
+
+int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
+
+// The backward pass' scratch memory: B and A turned, g, and the partial sums
+// (one after the other: dA's are added up before dB's are written).
+struct BackwardSpace {
+  int64_t b_turned, a_turned, g, partial, all;
+};
+BackwardSpace backward_space(int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters, int64_t segments,
+                             int64_t wsize) {
+  BackwardSpace s;
+  s.b_turned = 0;
+  s.a_turned = s.b_turned + round16(adapters * rank * n * wsize);
+  s.g = s.a_turned + round16(adapters * rank * k * wsize);
+  s.partial = s.g + round16(rows * rank * 4);
+  const auto need = [&](int64_t C) {
+    const int64_t shares = shares_of(rows, C, rank, adapters, segments);
+    return shares > 1 ? shares * adapters * rank * C * 4 : 0;
+  };
+  s.all = s.partial + std::max(need(n), need(k));
+  return s;
+}
+
+template <typename W> void forward_w(const AdapterForward &p, const Segments &s, hipStream_t stream) {
+  const W *a = (const W *)p.w.a, *b = (const W *)p.w.b;
+  const int rank = (int)p.w.rank;
+  if (p.x_dtype == 1) shrink(s, (const uint16_t *)p.x, p.ldx, p.w.k, a, rank, nullptr, p.u, stream);
+  else shrink(s, (const float *)p.x, p.ldx, p.w.k, a, rank, nullptr, p.u, stream);
+  if (p.w.n > 0)
+    expand(s, p.u, rank, b, p.w.scale, p.base, p.base_dtype == 1, p.ldb, p.y, p.y_dtype == 1, p.ldy, p.w.n, stream);
+}
+
+template <typename W> void backward_w(const AdapterBackward &p, const Segments &s, hipStream_t stream) {
+  const AdapterWeights &w = p.w;
+  const int rank = (int)w.rank, gb = p.g_dtype == 1;
+  const BackwardSpace at = backward_space(s.g.rows, w.n, w.k, rank, w.adapters, w.segments, sizeof(W));
+  char *const ws = (char *)p.ws;
+  W *const bt = (W *)(ws + at.b_turned), *const aT = (W *)(ws + at.a_turned);
+  float *const g = (float *)(ws + at.g), *const partial = (float *)(ws + at.partial);
+  if (s.g.rows > 0) {
+    if (w.n > 0) turn(s, (const W *)w.b, bt, w.n, rank, stream);
+    if (w.k > 0) turn(s, (const W *)w.a, aT, rank, w.k, stream);
+    if (p.dy_dtype == 1) shrink(s, (const uint16_t *)p.dy, p.lddy, w.n, bt, rank, w.scale, g, stream);
+    else shrink(s, (const float *)p.dy, p.lddy, w.n, bt, rank, w.scale, g, stream);
+    if (w.k > 0)
+      expand(s, g, rank, aT, nullptr, p.base, p.base_dtype == 1, p.ldb, p.dx, p.dx_dtype == 1, p.lddx, w.k, stream);
+  }
+  if (w.k > 0) {
+    if (p.x_dtype == 1) grad<uint16_t, false>(s, w.segments, (const uint16_t *)p.x, p.ldx, w.k, g, rank, nullptr, p.da, gb, partial, stream);
+    else grad<float, false>(s, w.segments, (const float *)p.x, p.ldx, w.k, g, rank, nullptr, p.da, gb, partial, stream);
+  }
+  if (w.n > 0) {
+    if (p.dy_dtype == 1) grad<uint16_t, true>(s, w.segments, (const uint16_t *)p.dy, p.lddy, w.n, p.u, rank, w.scale, p.db, gb, partial, stream);
+    else grad<float, true>(s, w.segments, (const float *)p.dy, p.lddy, w.n, p.u, rank, w.scale, p.db, gb, partial, stream);
+  }
+}
+
+Segments segments_of(const AdapterWeights &w, int64_t rows) {
+  return {{w.offsets, w.index_bits == 64, (int)w.segments + 2, rows, 1}, w.index, (int)w.adapters};
+}
+
+}  // namespace
+
+int64_t adapters_backward_workspace_bytes(int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters,
+                                          int64_t segments, int w_dtype) {
+  return backward_space(rows, n, k, rank, adapters, segments, w_dtype == 1 ? 2 : 4).all;
+}
+
+hipError_t launch_adapters(const AdapterForward &p, hipStream_t stream) {
+  if (p.rows == 0) return hipSuccess;
+  const Segments s = segments_of(p.w, p.rows);
+  if (p.w.w_dtype == 1) forward_w<uint16_t>(p, s, stream);
+  else forward_w<float>(p, s, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_adapters_backward(const AdapterBackward &p, hipStream_t stream) {
+  const Segments s = segments_of(p.w, p.rows);
+  if (p.w.w_dtype == 1) backward_w<uint16_t>(p, s, stream);
+  else backward_w<float>(p, s, stream);
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

@@ -221,6 +221,40 @@ int grouped_common(nvfp4::GroupedProduct p, int64_t outer, int64_t k, int64_t wo
   return hip_status(nvfp4::launch_grouped(p, (hipStream_t)hip_stream));
 }
 
+constexpr int64_t kMaxRank = 128;
+constexpr int64_t kMaxAdapters = 65535;      // the grid's y dimension
+// The adapters' own arguments, and the sizes that their launches take.
+int check_adapters(const nvfp4::AdapterWeights &w, int64_t rows) {
+  if (!dtype_ok(w.w_dtype) || (w.index_bits != 32 && w.index_bits != 64)) return NVFP4_ERR_ENUM;
+  if (rows < 0 || w.n < 0 || w.k < 0 || w.rank < 1 || w.rank > kMaxRank || w.adapters < 1 || w.adapters > kMaxAdapters ||
+      w.segments < 1 || w.segments > kMaxGroups)
+    return NVFP4_ERR_SHAPE;
+  const int64_t wide = w.n > w.k ? w.n : w.k;
+  if (wide > kMaxCount / (kMaxAdapters * kMaxRank) || wide > kMaxGrid * 64) return NVFP4_ERR_SHAPE;
+  const int64_t tiles = w.segments + 2 < rows ? w.segments + 2 : rows;
+  if (!grid_ok((wide + 255) / 256, rows / 16 + tiles) || !grid_ok((wide + 63) / 64, 2)) return NVFP4_ERR_SHAPE;
+  if (rows > 0 && (!w.offsets || !w.index || (w.k > 0 && !w.a) || (w.n > 0 && !w.b))) return NVFP4_ERR_NULL;
+  const uintptr_t ws = dtype_size(w.w_dtype);
+  if (!aligned(w.a, ws) || !aligned(w.b, ws) || !aligned(w.scale, 4) || !aligned(w.offsets, w.index_bits / 8) ||
+      !aligned(w.index, w.index_bits / 8))
+    return NVFP4_ERR_ALIGN;
+  return NVFP4_OK;
+}
+// The matrix that a low-rank product is added to, in y's place or apart from it.
+int check_base(const void *base, int base_dtype, int64_t ldb, const void *y, int y_dtype, int64_t ldy, int64_t rows,
+               int64_t cols) {
+  if (!dtype_ok(y_dtype) || (base && !dtype_ok(base_dtype))) return NVFP4_ERR_ENUM;
+  if (!matrix_ok(rows, cols, ldy) || (base && !matrix_ok(rows, cols, ldb))) return NVFP4_ERR_SHAPE;
+  if (rows > 0 && cols > 0 && !y) return NVFP4_ERR_NULL;
+  const int64_t ys = dtype_size(y_dtype);
+  if (!aligned(y, ys)) return NVFP4_ERR_ALIGN;
+  if (!base) return NVFP4_OK;
+  const int64_t bs = dtype_size(base_dtype);
+  if (!aligned(base, bs)) return NVFP4_ERR_ALIGN;
+  const bool same = base == y && base_dtype == y_dtype && (ldb == ldy || rows <= 1);
+  return !same && overlap(base, ldb * bs, cols * bs, y, ldy * ys, cols * ys, rows) ? NVFP4_ERR_SHAPE : NVFP4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -596,6 +630,76 @@ int nvfp4_grouped_wgrad(const void *dy, int dy_dtype, int64_t lddy, const void *
   return hip_status(nvfp4::launch_grouped_wgrad({experts, n, k, dy, dy_dtype, lddy, x, x_dtype, rows, ldx, offsets,
                                                  index_bits, dw, dw_dtype},
                                                 (hipStream_t)hip_stream));
+}
+
+int nvfp4_adapters(const void *x, int x_dtype, int64_t rows, int64_t k, int64_t ldx, const void *a, const void *b,
+                   int w_dtype, int64_t adapters, int64_t rank, int64_t n, const float *scale, const void *offsets,
+                   const void *index, int index_bits, int64_t segments, const void *base, int base_dtype, int64_t ldb,
+                   void *y, int y_dtype, int64_t ldy, float *u, void *hip_stream) {
+  const nvfp4::AdapterWeights w = {a, b, w_dtype, adapters, rank, n, k, scale, offsets, index, index_bits, segments};
+  if (!dtype_ok(x_dtype)) return NVFP4_ERR_ENUM;
+  int st = check_adapters(w, rows);
+  if (st != NVFP4_OK) return st;
+  if (!matrix_ok(rows, k, ldx)) return NVFP4_ERR_SHAPE;
+  st = check_base(base, base_dtype, ldb, y, y_dtype, ldy, rows, n);
+  if (st != NVFP4_OK) return st;
+  if (rows > 0 && (!u || (k > 0 && !x))) return NVFP4_ERR_NULL;
+  const int64_t xs = dtype_size(x_dtype), ys = dtype_size(y_dtype);
+  if (!aligned(x, xs) || !aligned(u, 4)) return NVFP4_ERR_ALIGN;
+  if (overlap(x, ldx * xs, k * xs, y, ldy * ys, n * ys, rows) ||
+      ranges_meet(x, span(rows, ldx, k, xs), u, rows * rank * 4) ||
+      ranges_meet(y, span(rows, ldy, n, ys), u, rows * rank * 4) ||
+      (base && ranges_meet(base, span(rows, ldb, n, dtype_size(base_dtype)), u, rows * rank * 4)))
+    return NVFP4_ERR_SHAPE;
+  return hip_status(nvfp4::launch_adapters({w, x, x_dtype, rows, ldx, base, base_dtype, ldb, y, y_dtype, ldy, u},
+                                           (hipStream_t)hip_stream));
+}
+
+int64_t nvfp4_adapters_backward_workspace_bytes(int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters,
+                                                int64_t segments, int w_dtype) {
+  const nvfp4::AdapterWeights w = {&rows, &rows, w_dtype, adapters, rank, n, k, nullptr, &rows, &rows, 32, segments};
+  const int st = check_adapters(w, rows);
+  if (st != NVFP4_OK && st != NVFP4_ERR_ALIGN) return st;
+  return nvfp4::adapters_backward_workspace_bytes(rows, n, k, rank, adapters, segments, w_dtype);
+}
+
+int nvfp4_adapters_backward(const void *dy, int dy_dtype, int64_t lddy, const void *x, int x_dtype, int64_t rows,
+                            int64_t k, int64_t ldx, const float *u, const void *a, const void *b, int w_dtype,
+                            int64_t adapters, int64_t rank, int64_t n, const float *scale, const void *offsets,
+                            const void *index, int index_bits, int64_t segments, const void *base, int base_dtype,
+                            int64_t ldb, void *dx, int dx_dtype, int64_t lddx, void *da, void *db, int g_dtype,
+                            void *workspace, int64_t workspace_bytes, void *hip_stream) {
+  const nvfp4::AdapterWeights w = {a, b, w_dtype, adapters, rank, n, k, scale, offsets, index, index_bits, segments};
+  if (!dtype_ok(dy_dtype) || !dtype_ok(x_dtype) || !dtype_ok(g_dtype)) return NVFP4_ERR_ENUM;
+  int st = check_adapters(w, rows);
+  if (st != NVFP4_OK) return st;
+  if (!matrix_ok(rows, k, ldx) || !matrix_ok(rows, n, lddy)) return NVFP4_ERR_SHAPE;
+  st = check_base(base, base_dtype, ldb, dx, dx_dtype, lddx, rows, k);
+  if (st != NVFP4_OK) return st;
+  if (rows > 0 && (!u || (k > 0 && !x) || (n > 0 && !dy))) return NVFP4_ERR_NULL;
+  if ((k > 0 && !da) || (n > 0 && !db) || !offsets || !index) return NVFP4_ERR_NULL;
+  const int64_t need = nvfp4::adapters_backward_workspace_bytes(rows, n, k, rank, adapters, segments, w_dtype);
+  if (workspace_bytes < need) return NVFP4_ERR_SHAPE;
+  if (need > 0 && !workspace) return NVFP4_ERR_NULL;
+  const int64_t xs = dtype_size(x_dtype), ds = dtype_size(dy_dtype), os = dtype_size(dx_dtype), gs = dtype_size(g_dtype);
+  if (!aligned(x, xs) || !aligned(dy, ds) || !aligned(u, 4) || !aligned(da, gs) || !aligned(db, gs) ||
+      !aligned(workspace, 16))
+    return NVFP4_ERR_ALIGN;
+  if (overlap(x, ldx * xs, k * xs, dx, lddx * os, k * os, rows) ||
+      ranges_meet(dy, span(rows, lddy, n, ds), dx, span(rows, lddx, k, os)))
+    return NVFP4_ERR_SHAPE;
+  // the weights' gradients meet neither each other nor a matrix
+  const struct { const void *p; int64_t bytes; } out[] = {{da, adapters * rank * k * gs}, {db, adapters * rank * n * gs}},
+      in[] = {{x, span(rows, ldx, k, xs)}, {dy, span(rows, lddy, n, ds)}, {dx, span(rows, lddx, k, os)},
+              {u, rows * rank * 4}, {a, adapters * rank * k * (int64_t)dtype_size(w_dtype)},
+              {b, adapters * rank * n * (int64_t)dtype_size(w_dtype)}};
+  if (ranges_meet(da, out[0].bytes, db, out[1].bytes)) return NVFP4_ERR_SHAPE;
+  for (const auto &o : out)
+    for (const auto &i : in)
+      if (ranges_meet(o.p, o.bytes, i.p, i.bytes)) return NVFP4_ERR_SHAPE;
+  return hip_status(nvfp4::launch_adapters_backward({w, dy, dy_dtype, lddy, x, x_dtype, rows, ldx, u, base, base_dtype,
+                                                     ldb, dx, dx_dtype, lddx, da, db, g_dtype, workspace},
+                                                    (hipStream_t)hip_stream));
 }
 
 int64_t nvfp4_distill_topk_workspace_bytes(int64_t tokens, int64_t vocab) {

@@ -314,33 +314,8 @@ hipError_t grouped_x(const Stack &w, const Groups &g, const Rows<X> &x, void *y,
 // with transposing reads (16 lanes take 4 rows of 16 columns, and each leaves
 // with 4 rows of its own column).  Rows of LDS are 32 bytes longer than their
 // columns, so that the 4 rows of such a read fall on different banks.
-// A float32 operand is three bf16 parts, hi + mid + lo, rounded to nearest, of
-// which the products from hi hi to mid mid are taken; those left out are below
-// 2^-25 of the whole.
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
-
-__device__ __forceinline__ Parts split8_nearest(const Row8<float> &q) {
-  float f[8], rest[8];
-  q.get(f);
-  Parts out;
-  float odd = 0.0f;                                // NaN if a part is not finite
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t p = pack_bf16(f[2 * i], f[2 * i + 1]);
-    out.v[0][i] = p;
-    rest[2 * i] = f[2 * i] - bf16_lo(p);
-    rest[2 * i + 1] = f[2 * i + 1] - bf16_hi(p);
-    odd += rest[2 * i] * 0.0f + rest[2 * i + 1] * 0.0f;
-    p = pack_bf16(rest[2 * i], rest[2 * i + 1]);
-    out.v[1][i] = p;
-    out.v[2][i] = pack_bf16(rest[2 * i] - bf16_lo(p), rest[2 * i + 1] - bf16_hi(p));
-  }
-  // (an Inf or NaN, or a value that rounds beyond bf16's largest)
-  if (odd != odd) return split8((f32x4_t)q.a, (f32x4_t)q.b);
-  return out;
-}
-
+// Of the parts of two float32 operands the products from hi hi to mid mid are
+// taken; those left out are below 2^-25 of the whole.
 // A workgroup's tile is 64 FN columns of dy (n) by 64 FK columns of x, two by
 // two waves; every group's tiles are written, zeros for a group without rows.
 template <typename D, typename X, int FN, int FK, int TOKENS>
@@ -429,11 +404,6 @@ __global__ __launch_bounds__(kThreads) void k_grouped_wgrad(Groups g, Rows<D> dy
   // a lane's 8 rows (8 h .. 8 h + 7 of an MFMA's 16) of its column of a
   // fragment of 32, by two reads; it names 4 columns of one row
   const int col = 16 * ((lane >> 4) & 1) + 4 * (lane & 3), trow = 8 * (lane >> 5) + ((lane >> 2) & 3);
-  const auto column = [&](const char *from, int pitch) {
-    const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)from);
-    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(from + 4 * pitch));
-    return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-  };
   const auto products = [&](int s) {
     const char *const dbuf = lds + (s & 1) * kBuffer + trow * kRowD + ((wave >> 1) * (32 * FN) + col) * 2;
     const char *const xbuf = lds + (s & 1) * kBuffer + kDP * kPartD + trow * kRowX + ((wave & 1) * (32 * FK) + col) * 2;
@@ -443,11 +413,11 @@ __global__ __launch_bounds__(kThreads) void k_grouped_wgrad(Groups g, Rows<D> dy
 #pragma unroll
       for (int p = 0; p < kDP; ++p)
 #pragma unroll
-        for (int f = 0; f < FN; ++f) a[p][f] = column(dbuf + p * kPartD + ks * 16 * kRowD + f * 64, kRowD);
+        for (int f = 0; f < FN; ++f) a[p][f] = lds_column(dbuf + p * kPartD + ks * 16 * kRowD + f * 64, kRowD);
 #pragma unroll
       for (int p = 0; p < kXP; ++p)
 #pragma unroll
-        for (int f = 0; f < FK; ++f) b[p][f] = column(xbuf + p * kPartX + ks * 16 * kRowX + f * 64, kRowX);
+        for (int f = 0; f < FK; ++f) b[p][f] = lds_column(xbuf + p * kPartX + ks * 16 * kRowX + f * 64, kRowX);
 #pragma unroll
       for (int p = 0; p < kDP; ++p)
 #pragma unroll
@@ -508,7 +478,7 @@ hipError_t wgrad(const Groups &g, const Rows<D> &dy, const Rows<X> &x, void *dw,
 
 hipError_t launch_grouped_wgrad(const GroupedWgrad &p, hipStream_t stream) {
   if (p.n == 0 || p.k == 0) return hipSuccess;
-  const Groups g = {p.offsets, p.index_bits == 64, (int)p.experts, p.rows};
+  const Groups g = {p.offsets, p.index_bits == 64, (int)p.experts, p.rows, 0};
   const int b = p.dw_dtype == 1;
   const auto run = [&](auto *d, auto *x) {
     using D = std::remove_const_t<std::remove_pointer_t<decltype(d)>>;
@@ -528,7 +498,7 @@ hipError_t launch_grouped(const GroupedProduct &p, hipStream_t stream) {
   const int64_t block = p.mx ? 32 : 16, rows = p.transposed ? 1 : p.n;
   const int64_t pitch = p.transposed ? p.experts * p.k : p.k, step = rows * p.k;
   const Stack w = {p.codes, p.scales, p.meta, p.n, p.k, pitch / 2, step / 2, pitch / block, step / block};
-  const Groups g = {p.offsets, p.index_bits == 64, (int)p.experts, p.rows};
+  const Groups g = {p.offsets, p.index_bits == 64, (int)p.experts, p.rows, 0};
   const int yb = p.y_dtype == 1;
   if (p.x_dtype == 1) {
     const Rows<uint16_t> x = {(const uint16_t *)p.x, p.ldx};

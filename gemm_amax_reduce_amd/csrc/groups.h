@@ -9,13 +9,21 @@
 
 namespace nvfp4 {
 
+// With `cover` the rows in front and behind are groups of their own, the first
+// and the last of `count`.
 struct Groups {
   const void *offsets;
   int is64;
   int count;
   int64_t rows;
-  // offsets[i], kept inside the matrix whatever is stored there
+  int cover;
+  // where group i begins (i == count: where the last one ends), kept inside the
+  // matrix whatever is stored there
   __device__ __forceinline__ int64_t at(int i) const {
+    if (cover) {
+      if (i == 0 || i == count) return i ? rows : 0;
+      i -= 1;
+    }
     const int64_t v = is64 ? ((const int64_t *)offsets)[i] : (int64_t)((const int32_t *)offsets)[i];
     return min(max(v, (int64_t)0), rows);
   }

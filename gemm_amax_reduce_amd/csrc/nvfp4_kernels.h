@@ -151,6 +151,57 @@ struct GroupedWgrad {
 };
 hipError_t launch_grouped_wgrad(const GroupedWgrad &p, hipStream_t stream);
 
+// Low-rank adapters of the segments of rows that offsets and index give:
+// a [adapters][rank][k], b [adapters][n][rank], scale [adapters] (null = 1).
+struct AdapterWeights {
+  const void *a, *b;
+  int w_dtype;
+  int64_t adapters, rank, n, k;
+  const float *scale;
+  const void *offsets, *index;
+  int index_bits;
+  int64_t segments;
+};
+// u = A x, y = base + scale B u (base null = 0; y itself may be base).
+struct AdapterForward {
+  AdapterWeights w;
+  const void *x;
+  int x_dtype;
+  int64_t rows, ldx;
+  const void *base;
+  int base_dtype;
+  int64_t ldb;
+  void *y;
+  int y_dtype;
+  int64_t ldy;
+  float *u;
+};
+// dx = base + A^T g with g = scale B^T dy, da = sum g x^T, db = sum scale dy u^T
+// (in g_dtype).  ws: adapters_backward_workspace_bytes, 16-byte aligned.
+struct AdapterBackward {
+  AdapterWeights w;
+  const void *dy;
+  int dy_dtype;
+  int64_t lddy;
+  const void *x;
+  int x_dtype;
+  int64_t rows, ldx;
+  const float *u;
+  const void *base;
+  int base_dtype;
+  int64_t ldb;
+  void *dx;
+  int dx_dtype;
+  int64_t lddx;
+  void *da, *db;
+  int g_dtype;
+  void *ws;
+};
+int64_t adapters_backward_workspace_bytes(int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters,
+                                          int64_t segments, int w_dtype);
+hipError_t launch_adapters(const AdapterForward &p, hipStream_t stream);
+hipError_t launch_adapters_backward(const AdapterBackward &p, hipStream_t stream);
+
 // Distillation from a teacher's top logits: with stats, loss and lse are
 // formed from z; without, lse is read.  dz (with weight) may be null when
 // stats is set.  workspace: distill_workspace_bytes, 8-byte aligned.

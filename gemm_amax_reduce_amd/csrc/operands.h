@@ -98,4 +98,65 @@ __device__ __forceinline__ Parts split8(const f32x4_t &a, const f32x4_t &b) {
   return out;
 }
 
+// The same with hi and mid rounded to nearest: what is left over after two
+// parts is at most 2^-17 of the value (2^-15 above, on one side).
+__device__ __forceinline__ Parts split8_nearest(const Row8<float> &q) {
+  float f[8], rest[8];
+  q.get(f);
+  Parts out;
+  float odd = 0.0f;                                // NaN if a part is not finite
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t p = pack_bf16(f[2 * i], f[2 * i + 1]);
+    out.v[0][i] = p;
+    rest[2 * i] = f[2 * i] - bf16_lo(p);
+    rest[2 * i + 1] = f[2 * i + 1] - bf16_hi(p);
+    odd += rest[2 * i] * 0.0f + rest[2 * i + 1] * 0.0f;
+    p = pack_bf16(rest[2 * i], rest[2 * i + 1]);
+    out.v[1][i] = p;
+    out.v[2][i] = pack_bf16(rest[2 * i] - bf16_lo(p), rest[2 * i + 1] - bf16_hi(p));
+  }
+  // (an Inf or NaN, or a value that rounds beyond bf16's largest)
+  if (odd != odd) return split8((f32x4_t)q.a, (f32x4_t)q.b);
+  return out;
+}
+
+// 8 rows of a lane's column, from rows of bf16 in LDS `pitch` bytes apart, by
+// two transposing reads: 16 lanes name 4 rows of 16 columns (each 4 columns of
+// one row) and leave with those rows of a column each; the second read takes
+// the next 4 rows.
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+__device__ __forceinline__ bf16x8_t lds_column(const char *from, int pitch) {
+  const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)from);
+  const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(from + 4 * pitch));
+  return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// 8 elements as MFMA operands: a bf16 value, or the parts of a float32 one.
+template <typename T> struct Operand;
+template <> struct Operand<uint16_t> {
+  static constexpr int kParts = 1;
+  bf16x8_t v[1];
+  __device__ __forceinline__ void set(const Row8<uint16_t> &q) { v[0] = __builtin_bit_cast(bf16x8_t, (u32x4_t)q.r); }
+};
+template <> struct Operand<float> {
+  static constexpr int kParts = 3;
+  bf16x8_t v[3];
+  __device__ __forceinline__ void set(const Row8<float> &q) {
+    const Parts p = split8_nearest(q);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v[i] = __builtin_bit_cast(bf16x8_t, p.v[i]);
+  }
+};
+// acc += the product of two operands (of the parts those that count).
+template <typename A, typename B>
+__device__ __forceinline__ void multiply16(f32x4_t &acc, const Operand<A> &a, const Operand<B> &b) {
+#pragma unroll
+  for (int p = 0; p < Operand<A>::kParts; ++p)
+#pragma unroll
+    for (int q = 0; q < Operand<B>::kParts; ++q)
+      if (p + q < 3) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[p], b.v[q], acc, 0, 0, 0);
+}
+
 }  // namespace nvfp4

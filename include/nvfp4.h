@@ -565,6 +565,65 @@ int nvfp4_grouped_wgrad(const void *dy, int dy_dtype, int64_t lddy, const void *
                         void *dw, int dw_dtype, void *hip_stream);
 
 /*
+ * nvfp4_adapters -- low-rank adapters of many requests at once, beside a
+ * projection that they share (its weights 4-bit and frozen, say, its result
+ * from nvfp4_matvec or nvfp4_gemm):
+ *   u[t] = A_a x[t],   y[t] = base[t] + scale_a B_a u[t]
+ * for the rows offsets[i] <= t < offsets[i + 1] of segment i (a request) and
+ * its adapter a = index[i].
+ *  x       : device, row-major [rows][ldx], x_dtype, ldx >= k, aligned to its
+ *            element only.
+ *  a, b    : device, w_dtype, contiguous: a [adapters][rank][k],
+ *            b [adapters][n][rank].  1 <= rank <= 128, 1 <= adapters <= 65535.
+ *            Adapters of a smaller rank are filled up with zeros.
+ *  scale   : device, f32 [adapters]; NULL = 1.
+ *  offsets : device, [segments + 1] of int32 or int64 (index_bits 32 or 64),
+ *            not decreasing, 0 <= offsets[0] and offsets[segments] <= rows.
+ *            Not checked; values outside are taken as the nearest inside, and
+ *            where they decrease the result is unspecified (nothing outside
+ *            the outputs is written).  1 <= segments <= 2^20.
+ *  index   : device, [segments], of the same type.  A segment whose index lies
+ *            outside [0, adapters) (-1, say) has no adapter.
+ *  base    : device, row-major [rows][ldb], base_dtype, or NULL (zeros).
+ *  y       : device, row-major [rows][ldy], y_dtype, written whole: rows
+ *            without an adapter (those of no segment too) are base.  May be
+ *            `base` itself (same pointer, type and leading dimension); must
+ *            not overlap it otherwise, nor x (NVFP4_ERR_SHAPE).
+ *  u       : device, f32 [rows][rank], written whole (zeros without an
+ *            adapter), for the backward pass.
+ *  ceil(max(n, k) / 256) * (rows / 16 + min(segments + 2, rows)) <= 2^24 - 8.
+ * bf16 operands enter the products exactly; a product of two float32 values
+ * is off by at most 2^-23 of its magnitude, and one with an infinity infinite
+ * or NaN.  Sums are binary32.  Deterministic.  Enqueues two kernels.
+ *
+ * nvfp4_adapters_backward -- with g[t] = scale_a B_a^T dy[t]:
+ *   dx[t] = base[t] + A_a^T g[t]                             (dx_dtype)
+ *   da[a] = sum of g[t] x[t]^T, db[a] = scale_a sum of dy[t] u[t]^T
+ * over the rows of all segments of adapter a (g_dtype, zeros for an adapter
+ * that no segment has).  base is what the shared projection gives, dx written
+ * whole as y is above.  u: the forward call's.
+ *  workspace : device, at least nvfp4_adapters_backward_workspace_bytes(rows,
+ *            n, k, rank, adapters, segments, w_dtype) bytes, 16-byte aligned,
+ *            contents ignored and overwritten; calls that share one must not
+ *            overlap in time.
+ * Outputs must not overlap inputs or each other (NVFP4_ERR_SHAPE), but for dx
+ * in base's place.  Sums over rows are binary32, in a fixed order:
+ * deterministic on one device.
+ */
+int nvfp4_adapters(const void *x, int x_dtype, int64_t rows, int64_t k, int64_t ldx, const void *a, const void *b,
+                   int w_dtype, int64_t adapters, int64_t rank, int64_t n, const float *scale, const void *offsets,
+                   const void *index, int index_bits, int64_t segments, const void *base, int base_dtype, int64_t ldb,
+                   void *y, int y_dtype, int64_t ldy, float *u, void *hip_stream);
+int nvfp4_adapters_backward(const void *dy, int dy_dtype, int64_t lddy, const void *x, int x_dtype, int64_t rows,
+                            int64_t k, int64_t ldx, const float *u, const void *a, const void *b, int w_dtype,
+                            int64_t adapters, int64_t rank, int64_t n, const float *scale, const void *offsets,
+                            const void *index, int index_bits, int64_t segments, const void *base, int base_dtype,
+                            int64_t ldb, void *dx, int dx_dtype, int64_t lddx, void *da, void *db, int g_dtype,
+                            void *workspace, int64_t workspace_bytes, void *hip_stream);
+int64_t nvfp4_adapters_backward_workspace_bytes(int64_t rows, int64_t n, int64_t k, int64_t rank, int64_t adapters,
+                                                int64_t segments, int w_dtype);
+
+/*
  * nvfp4_distill_topk -- the distillation loss of a student's logits against
  * a teacher's best logits, by which a model brought to 4 bits is trained:
  *   p    = softmax(teacher / temperature) over the row's valid entries
