@@ -618,7 +618,7 @@ int nvfp4_grouped_wgrad(const void *dy, int dy_dtype, int64_t lddy, const void *
     return NVFP4_ERR_ENUM;
   if (n < 0 || k < 0 || !matrix_ok(rows, n, lddy) || !matrix_ok(rows, k, ldx) || experts < 1 || experts > kMaxGroups ||
       n > kMaxGrid * 128 || k > kMaxGrid * 128 || !grid_ok((n + 127) / 128, (k + 127) / 128) ||
-      !grid_ok((n + 127) / 128 * ((k + 127) / 128), experts))
+      !grid_ok((n + 127) / 128 * ((k + 127) / 128) + 7, experts))
     return NVFP4_ERR_SHAPE;
   if (n > 0 && k > 0 && (!dw || !offsets || (rows > 0 && (!dy || !x)))) return NVFP4_ERR_NULL;
   const int64_t ds = dtype_size(dy_dtype), xs = dtype_size(x_dtype), ws = dtype_size(dw_dtype);

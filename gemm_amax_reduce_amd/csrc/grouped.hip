@@ -277,6 +277,244 @@ k_grouped(Stack w, Groups g, Rows<X> x, void *y, int y_bf16, int64_t ldy, int ti
   }
 }
 
+// ------------------------------------------------- bf16, larger groups --
+
+// The same tiles with both operands copied to LDS by DMA, a stage ahead, and
+// the work of a K step (the 16 k of an MFMA) in a fixed order: each MFMA is
+// followed by its share of decoding the next step's weights, so that one wave a
+// SIMD keeps the matrix pipe busy.  A stage's copies go out over the first four
+// of its eight steps; in the last one the wave waits for those of the stage
+// behind, meets the others, and reads from it.
+//
+// x rows of a multiple of 4 bytes, from an address of one (the range check that
+// makes rows past the group zeros works by words).
+constexpr int wait_vm(int n) { return (n & 15) | (n >> 4) << 14 | 0x0F70; }
+// A wait for those counts, and the workgroup's barrier.
+template <int COUNTS> __device__ __forceinline__ void meet() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(COUNTS);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <bool MX, int NF, int MF>
+__global__ __launch_bounds__(kThreads, NF * MF >= 16 ? 1 : 2) void
+k_grouped_dma(Stack w, Groups g, Rows<uint16_t> x, void *y, int y_bf16, int64_t ldy, int tiles_n, int fill) {
+  constexpr int BN = 128 * NF, BM = 32 * MF;
+  constexpr int kG = Scale<MX>::kPerByte, kSB = kStage / kG;
+  constexpr int kCodes = BN * kStage / 2, kScales = BN * 8, kBuffer = kCodes + kScales + BM * kStage * 2;
+  constexpr int kCL = BN / 64, kXL = BM / 16;        // DMA instructions a wave and stage: 16 rows of codes, 4 of x each
+  constexpr int kSL = (BN + kThreads - 1) / kThreads;
+  __shared__ __align__(16) uint8_t lds[2 * kBuffer];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 31, h = lane >> 5;
+
+  if (fill) zero_rest(g, y, y_bf16, ldy, w.N);
+  const int total = count_tiles(g, BM) * tiles_n;
+  const int quota = (total + kXcds - 1) / kXcds, local = blockIdx.x / kXcds;
+  const int index = (int)(blockIdx.x % kXcds) * quota + local;
+  if (local >= quota || index >= total) return;
+  const GroupTile t = find_tile(g, BM, tiles_n, index);
+  if (t.e < 0) return;
+  const int per = 8 * tiles_n, first_m = t.local / per * 8, gsz = min(t.tiles - first_m, 8);
+  const int64_t m0 = t.begin + (int64_t)(first_m + t.local % per % gsz) * BM;
+  const int64_t n0 = (int64_t)(t.local % per / gsz) * BN;
+  const int stages = (int)((w.K + kStage - 1) / kStage);
+
+  // ---- copies.  Codes: lane l takes row l / 4, slot l % 4, which holds piece
+  // (l % 4) ^ (row / 16 % 4); x: row l / 16, slot l % 16, which holds piece
+  // (l % 16) ^ (row % 16).  A wave's instructions are BN / 4 rows of codes and
+  // BM / 4 of x, from views of the tile's own rows.
+  const uint32_t cp = (uint32_t)w.code_pitch, xp = (uint32_t)(x.ld * 2), kb = (uint32_t)w.K;
+  const __amdgpu_buffer_rsrc_t cview =
+      make_rsrc(w.codes + t.e * w.code_step + n0 * w.code_pitch,
+                (uint32_t)(min((int64_t)BN, w.N - n0) - 1) * cp + kb / 2);
+  const __amdgpu_buffer_rsrc_t xview =
+      make_rsrc(x.p + m0 * x.ld, (uint32_t)(min((int64_t)BM, t.end - m0) - 1) * xp + kb * 2);
+  const uint32_t crow = (uint32_t)(wave * (BN / 4) + (lane >> 2)) * cp, cpiece = (uint32_t)lane & 3;
+  const uint32_t xrow = (uint32_t)(wave * (BM / 4) + (lane >> 4)) * xp, xpiece = (uint32_t)(lane & 15) ^ (lane >> 4);
+  const uint8_t *srow[kSL];
+#pragma unroll
+  for (int i = 0; i < kSL; ++i)
+    srow[i] = w.scales + t.e * w.scale_step + min(n0 + tid + i * kThreads, w.N - 1) * w.scale_pitch;
+  uint64_t sreg[kSL];
+  // part q of 4 of stage s (nothing past the last one)
+  const auto copy = [&](int s, int q) {
+    uint8_t *const buf = lds + (s & 1) * kBuffer;
+    const uint32_t k0 = (uint32_t)s * kStage;
+    const bool in = s < stages;
+#pragma unroll
+    for (int i = q * kCL / 4; i < (q + 1) * kCL / 4; ++i) {
+      const uint32_t piece = cpiece ^ (uint32_t)((wave * (BN / 64) + i) & 3);
+      const uint32_t at = !in || k0 + 32 * piece < kb ? crow + 16 * piece : kOutOfRange;
+      dma16(cview, buf + (wave * (BN / 4) + 16 * i) * 64, at, in ? 16u * i * cp + k0 / 2 : kOutOfRange);
+    }
+#pragma unroll
+    for (int i = q * kXL / 4; i < (q + 1) * kXL / 4; ++i) {
+      const uint32_t piece = xpiece ^ (uint32_t)((wave * (BM / 4) + 4 * i) & 15);
+      const uint32_t at = !in || k0 + 8 * piece < kb ? xrow + 16 * piece : kOutOfRange;
+      dma16(xview, buf + kCodes + kScales + (wave * (BM / 4) + 4 * i) * 256, at, in ? 4u * i * xp + k0 * 2 : kOutOfRange);
+    }
+    if (q == 0 && in) {
+      if ((int64_t)k0 + kStage <= w.K) {
+#pragma unroll
+        for (int i = 0; i < kSL; ++i) {
+          sreg[i] = 0;
+          __builtin_memcpy(&sreg[i], srow[i] + k0 / kG, kSB);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kSL; ++i) {
+          sreg[i] = MX ? 0x7F7F7F7F7F7F7F7Full : 0;
+          for (int b = 0; b < kSB; ++b)
+            if (k0 + b * kG < kb)
+              sreg[i] = (sreg[i] & ~(0xFFull << (8 * b))) | (uint64_t)srow[i][k0 / kG + b] << (8 * b);
+        }
+      }
+    }
+  };
+  const auto put_scales = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < kSL; ++i)
+      if (BN % kThreads == 0 || tid + i * kThreads < BN)
+        *reinterpret_cast<uint64_t *>(lds + (s & 1) * kBuffer + kCodes + (tid + i * kThreads) * 8) = sreg[i];
+  };
+
+  // ---- operands.  Half stage p (0, 1) of a stage is four K steps.
+  float16_t acc[NF][MF];
+#pragma unroll
+  for (int f = 0; f < NF; ++f)
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[f][m][i] = 0.0f;
+  const int wrow = wave * (32 * NF) + ((r >> 2) & 1) * 16 + (r >> 3) * 4 + (r & 3);
+  u32x4_t c[2][NF];
+  Scale<MX> sc[2][NF];
+  bool far[2] = {false, false};
+  bf16x8_t a[2][NF], b[2][MF];
+  const auto read_codes = [&](int s, int p) {
+    const uint8_t *const buf = lds + (s & 1) * kBuffer;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      const int row = wrow + 32 * f;
+      c[p][f] = *reinterpret_cast<const u32x4_t *>(buf + row * 64 + 16 * ((2 * p + h) ^ ((row >> 4) & 3)));
+      const uint8_t *const sp = buf + kCodes + row * 8 + (2 * p + h) * (32 / kG);
+      if (MX) sc[p][f].raw = *sp;
+      else sc[p][f].raw = *reinterpret_cast<const uint16_t *>(sp);
+    }
+  };
+  const auto read_x = [&](int s, int p, int j, int into) {
+    const uint8_t *const buf = lds + (s & 1) * kBuffer + kCodes + kScales;
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+      b[into][m] = *reinterpret_cast<const bf16x8_t *>(buf + (32 * m + r) * 256 + 16 * ((8 * p + 4 * h + j) ^ (r & 15)));
+  };
+  const auto check_far = [&](int p) {
+    if constexpr (MX) {
+      bool any = false;
+#pragma unroll
+      for (int f = 0; f < NF; ++f) any |= sc[p][f].raw - 3 >= 250;
+      far[p] = __any(any);
+    }
+  };
+  // a quarter of a fragment's 8 weights (MXFP4: all of them for quarter 0)
+  const auto decode = [&](int p, int j, int f, int quarter, int into) {
+    if constexpr (MX) {
+      if (quarter) return;
+      if (far[p]) a[into][f] = decode8<false>(c[p][f][j], sc[p][f].quarter());
+      else a[into][f] = decode8<true>(c[p][f][j], __uint_as_float((sc[p][f].raw - 2) << 23));
+    } else {
+      const float s = j < 2 ? sc[p][f].lo() : sc[p][f].hi();
+      const uint32_t code = c[p][f][j];
+      const float2_t v = quarter == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 0)
+                         : quarter == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 1)
+                         : quarter == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 2)
+                                        : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 3);
+      const bf16x2_t q = __builtin_convertvector((f32x2_t){v.x * s, v.y * s}, bf16x2_t);
+      a[into][f][2 * quarter] = q[0];
+      a[into][f][2 * quarter + 1] = q[1];
+    }
+  };
+  constexpr int NU = NF * MF, ND = 4 * NF;           // MFMAs and quarters to decode of a K step
+  // K step j of half p of stage s: operands of `cur` are there; the next step's
+  // go to the other.
+  const auto step = [&](int s, auto half, auto kstep) {
+    constexpr int p = decltype(half)::value, j = decltype(kstep)::value;
+    constexpr int cur = j & 1, nxt = cur ^ 1, np = j == 3 ? p ^ 1 : p, nj = (j + 1) & 3;
+    if constexpr (p == 1 && j == 3) {
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(wait_vm(0));       // this wave's copies of the next stage
+      put_scales(s + 1);
+      __syncthreads();
+      read_codes(s + 1, 0);
+      read_x(s + 1, 0, 0, nxt);
+    } else {
+      if constexpr (p == 0) copy(s + 1, j);
+      if constexpr (p == 0 && j == 2) read_codes(s, 1);
+      read_x(s, np, nj, nxt);
+    }
+    constexpr int kLag = j == 3 && NU >= 4 ? NU / 4 : 0;      // codes just read are not there yet
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      const int m = i / NF, f = (m & 1) ? NF - 1 - i % NF : i % NF;
+      acc[f][m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[cur][f], b[cur][m], acc[f][m], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (j == 3 && i == kLag) check_far(np);
+      if (i >= kLag) {
+        const int d0 = (i - kLag) * ND / (NU - kLag), d1 = (i - kLag + 1) * ND / (NU - kLag);
+#pragma unroll
+        for (int d = d0; d < d1; ++d) decode(np, nj, d / 4, d % 4, nxt);
+      }
+    }
+  };
+
+  if (stages > 0) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) copy(0, q);
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));
+    put_scales(0);
+    __syncthreads();
+    read_codes(0, 0);
+    read_x(0, 0, 0, 0);
+    check_far(0);
+#pragma unroll
+    for (int d = 0; d < ND; ++d) decode(0, 0, d / 4, d % 4, 0);
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I3 = std::integral_constant<int, 3>;
+    for (int s = 0; s < stages; ++s) {
+      step(s, I0{}, I0{});
+      step(s, I0{}, I1{});
+      step(s, I0{}, I2{});
+      step(s, I0{}, I3{});
+      step(s, I1{}, I0{});
+      step(s, I1{}, I1{});
+      step(s, I1{}, I2{});
+      step(s, I1{}, I3{});
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  const float scale = MX ? 4.0f : w.K > 0 ? w.meta[1] : 0.0f;
+#pragma unroll
+  for (int m = 0; m < MF; ++m) {
+    const int64_t row = m0 + 32 * m + r;
+    if (row >= t.end) continue;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = acc[f][m][i] * scale;
+      store16(y, y_bf16, row * ldy, n0 + wave * (32 * NF) + 32 * f + 16 * h, w.N, v);
+    }
+  }
+}
+
 // Weight rows and tokens of a tile, in fragments of 32 (times 4 waves).
 struct GroupedCut {
   int nf, mf;
@@ -293,8 +531,15 @@ hipError_t grouped(const Stack &w, const Groups &g, const Rows<X> &x, void *y, i
                    hipStream_t stream) {
   constexpr int BN = 128 * NF, BM = 32 * MF;
   const int64_t tiles_n = (w.N + BN - 1) / BN, tiles_m = g.rows / BM + std::min<int64_t>(g.count, g.rows);
-  k_grouped<MX, X, NF, MF><<<(unsigned)((tiles_n * tiles_m + kXcds - 1) / kXcds * kXcds), kThreads, 0, stream>>>(
-      w, g, x, y, y_bf16, ldy, (int)tiles_n, fill);
+  const unsigned grid = (unsigned)((tiles_n * tiles_m + kXcds - 1) / kXcds * kXcds);
+  if constexpr (sizeof(X) == 2 && NF > 1) {
+    // copies by DMA: words, and offsets inside a tile below 2^31
+    if ((uintptr_t)x.p % 4 == 0 && x.ld % 2 == 0 && x.ld < (1LL << 22) && w.code_pitch < (1LL << 21)) {
+      k_grouped_dma<MX, NF, MF><<<grid, kThreads, 0, stream>>>(w, g, x, y, y_bf16, ldy, (int)tiles_n, fill);
+      return hipGetLastError();
+    }
+  }
+  k_grouped<MX, X, NF, MF><<<grid, kThreads, 0, stream>>>(w, g, x, y, y_bf16, ldy, (int)tiles_n, fill);
   return hipGetLastError();
 }
 template <bool MX, typename X>
@@ -312,10 +557,14 @@ hipError_t grouped_x(const Stack &w, const Groups &g, const Rows<X> &x, void *y,
 // Tokens run along the reduction here, and lie down the columns of both
 // operands: a stage's rows go to LDS as they are, and the lanes fetch columns
 // with transposing reads (16 lanes take 4 rows of 16 columns, and each leaves
-// with 4 rows of its own column).  Rows of LDS are 32 bytes longer than their
-// columns, so that the 4 rows of such a read fall on different banks.
+// with 4 rows of its own column).  Rows of LDS are 64 bytes longer than their
+// columns, so that the 4 rows of two such neighbours fall on different banks.
 // Of the parts of two float32 operands the products from hi hi to mid mid are
 // taken; those left out are below 2^-25 of the whole.
+// Tiles of a group that an XCD takes: a run of an eighth of every group's, since
+// groups differ in length.  The grid has this for each XCD and group.
+__host__ __device__ __forceinline__ int wgrad_quota(int tiles) { return (tiles + kXcds - 1) / kXcds; }
+
 // A workgroup's tile is 64 FN columns of dy (n) by 64 FK columns of x, two by
 // two waves; every group's tiles are written, zeros for a group without rows.
 template <typename D, typename X, int FN, int FK, int TOKENS>
@@ -323,18 +572,16 @@ __global__ __launch_bounds__(kThreads) void k_grouped_wgrad(Groups g, Rows<D> dy
                                                             int64_t N, int64_t K, int tiles_n, int tiles_k) {
   constexpr int kDP = sizeof(D) == 2 ? 1 : 3, kXP = sizeof(X) == 2 ? 1 : 3;
   constexpr int TN = 64 * FN, TK = 64 * FK;
-  constexpr int kRowD = TN * 2 + 32, kRowX = TK * 2 + 32;            // bytes of a row in LDS
+  constexpr int kRowD = TN * 2 + 64, kRowX = TK * 2 + 64;            // bytes of a row in LDS
   constexpr int kPartD = TOKENS * kRowD, kPartX = TOKENS * kRowX;
   constexpr int kBuffer = kDP * kPartD + kXP * kPartX;
   constexpr int kDL = TOKENS * (TN / 8) / kThreads, kXL = TOKENS * (TK / 8) / kThreads;
   __shared__ __align__(16) char lds[2 * kBuffer];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  const int tiles = tiles_n * tiles_k, total = tiles * g.count;
-  const int quota = (total + kXcds - 1) / kXcds;
-  const int index = (int)(blockIdx.x % kXcds) * quota + (int)(blockIdx.x / kXcds);
-  if ((int)(blockIdx.x / kXcds) >= quota || index >= total) return;
-  const int e = index / tiles, at = index % tiles;
+  const int tiles = tiles_n * tiles_k, quota = wgrad_quota(tiles);
+  const int e = blockIdx.x / kXcds / quota, at = (int)(blockIdx.x % kXcds) * quota + (int)(blockIdx.x / kXcds) % quota;
+  if (at >= tiles) return;
   const int per = 8 * tiles_k, first_n = at / per * 8, gsz = min(tiles_n - first_n, 8);
   const int64_t n0 = (int64_t)(first_n + at % per % gsz) * TN, k0 = (int64_t)(at % per / gsz) * TK;
   const int64_t begin = g.at(e), end = max(g.at(e + 1), begin);
@@ -463,14 +710,195 @@ __global__ __launch_bounds__(kThreads) void k_grouped_wgrad(Groups g, Rows<D> dy
     }
 }
 
+// The 4 x 4 transpose over the lanes of a quad and four registers: lane j is
+// left with the j-th register of each of them.
+__device__ __forceinline__ f32x4_t quad_turn(float a, float b, float c, float d) {
+  const int lane = threadIdx.x;
+  const bool odd = lane & 1, high = lane & 2;
+  // lanes 1 apart, then 2 (every exchange by all lanes, the choice after it)
+  const float an = dpp<0xB1>(a), bn = dpp<0xB1>(b), cn = dpp<0xB1>(c), dn = dpp<0xB1>(d);
+  const float a1 = odd ? bn : a, b1 = odd ? b : an, c1 = odd ? dn : c, d1 = odd ? d : cn;
+  const float af = dpp<0x4E>(a1), bf = dpp<0x4E>(b1), cf = dpp<0x4E>(c1), df = dpp<0x4E>(d1);
+  return (f32x4_t){high ? cf : a1, high ? df : b1, high ? c1 : af, high ? d1 : bf};
+}
+// 4 neighbouring elements k .. k + 3 of a row of K.
+__device__ __forceinline__ void store4(void *out, int bf16, int64_t row, int64_t k, int64_t K, const f32x4_t &v) {
+  if (k + 4 <= K) {
+    if (bf16) *reinterpret_cast<u32x2_a2 *>((uint16_t *)out + row + k) = (u32x2_a2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    else *reinterpret_cast<f32x4_a4 *>((float *)out + row + k) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      if (k + i >= K) continue;
+      if (bf16) ((uint16_t *)out)[row + k + i] = (uint16_t)pack_bf16(v[i], 0.0f);
+      else ((float *)out)[row + k + i] = v[i];
+    }
+  }
+}
+
+// bf16 operands of whole words: tiles of 128 columns of dy by 256 of x, two
+// workgroups a CU, so that one multiplies while the other stores; copied to
+// LDS by DMA two stages of 32 tokens ahead, the columns of the next 16 tokens
+// fetched between the MFMAs of these.  Chunk c (32 bytes, 16 columns) of row t
+// lies in place c ^ (2 (t % 4)), so that the 4 rows of a transposing read's
+// two neighbouring chunks fall on different banks.
+constexpr int kWgTokens = 32, kWgRing = 3, kWgRowD = 256, kWgRowX = 512;
+constexpr int kWgStageD = kWgTokens * kWgRowD, kWgStage = kWgStageD + kWgTokens * kWgRowX;
+constexpr int kWgCopies = kWgStage / 4096;         // DMA instructions a wave and stage
+// One of the two half stages of 16 tokens: `from` is where the operands of the
+// next one lie (the stage itself, or the one behind), `to` where this stage's
+// copies go, which is another place of the ring.  (Two pointers that do not
+// meet: a transposing read would else wait for every copy under way.)
+struct WgOperands {
+  bf16x8_t a[2][2], b[2][4];
+};
+struct WgCopy {
+  __amdgpu_buffer_rsrc_t dv, xv;
+  uint32_t dat, xat[2], dp, xp;              // lane offsets (x: of even and odd instructions), a row's bytes
+  int wave;
+  // copy i of 6 of a stage at `to`: 4 rows of dy, or 2 of x; a wave's are 8 rows
+  __device__ __forceinline__ void run(int i, uint8_t *to) const {
+    if (i < 2)
+      dma16(dv, to + (8 * wave + 4 * i) * kWgRowD, dat, (uint32_t)(8 * wave + 4 * i) * dp);
+    else
+      dma16(xv, to + kWgStageD + (8 * wave + 2 * (i - 2)) * kWgRowX, xat[i & 1], (uint32_t)(8 * wave + 2 * (i - 2)) * xp);
+  }
+};
+template <int P>
+__device__ __forceinline__ void wg_half(const char *__restrict__ from, uint8_t *__restrict__ to, float16_t (&acc)[2][4],
+                                        WgOperands &o, const uint32_t (&dat)[2], const uint32_t (&xat)[4],
+                                        const WgCopy &c) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    __builtin_amdgcn_sched_barrier(0);
+    const int f = i / 4, q = (f & 1) ? 3 - i % 4 : i % 4;
+    acc[f][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.a[P][f], o.b[P][q], acc[f][q], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (i < 2) o.a[P ^ 1][i] = lds_column(from + dat[i], kWgRowD);
+    else if (i < 6) o.b[P ^ 1][i - 2] = lds_column(from + xat[i - 2], kWgRowX);
+    if (P == 0 && i >= 2) c.run(i - 2, to);
+  }
+}
+__global__ __launch_bounds__(kThreads, 2) void k_grouped_wgrad_dma(Groups g, Rows<uint16_t> dy, Rows<uint16_t> x, void *dw,
+                                                                   int dw_bf16, int64_t N, int64_t K, int tiles_n,
+                                                                   int tiles_k) {
+  __shared__ __align__(16) uint8_t lds[kWgRing * kWgStage];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tiles = tiles_n * tiles_k, quota = wgrad_quota(tiles);
+  const int e = blockIdx.x / kXcds / quota, at = (int)(blockIdx.x % kXcds) * quota + (int)(blockIdx.x / kXcds) % quota;
+  if (at >= tiles) return;
+  const int per = 16 * tiles_k, first_n = at / per * 16, gsz = min(tiles_n - first_n, 16);
+  const int64_t n0 = (int64_t)(first_n + at % per % gsz) * 128, k0 = (int64_t)(at % per / gsz) * 256;
+  const int64_t begin = uniform64(g.at(e)), end = max(uniform64(g.at(e + 1)), begin);
+  const int stages = (int)((end - begin + kWgTokens - 1) / kWgTokens);
+
+  // an instruction copies 1 KB: 4 rows of dy, lane l slot l % 16 (16 bytes) of
+  // row l / 16, or 2 of x, slot l % 32 of row l / 32
+  WgCopy c;
+  c.wave = wave;
+  c.dp = (uint32_t)(dy.ld * 2);
+  c.xp = (uint32_t)(x.ld * 2);
+  c.dat = (uint32_t)(lane >> 4) * c.dp + 16 * (uint32_t)((lane & 15) ^ (4 * (lane >> 4)));
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    c.xat[i] = (uint32_t)(lane >> 5) * c.xp + 16 * (uint32_t)((lane & 31) ^ (4 * (2 * i + (lane >> 5))));
+  const auto aim = [&](int s) {
+    const int64_t t0 = begin + (int64_t)s * kWgTokens, rows = min(end - t0, (int64_t)kWgTokens);
+    const auto view = [&](const Rows<uint16_t> &m, uint32_t pitch, int64_t c0, int64_t cols, int64_t most) {
+      return make_rsrc(m.p + (rows > 0 ? t0 * m.ld + c0 : 0),
+                       rows > 0 ? (uint32_t)(rows - 1) * pitch + (uint32_t)min(cols - c0, most) * 2 : 0u);
+    };
+    c.dv = view(dy, c.dp, n0, N, 128);
+    c.xv = view(x, c.xp, k0, K, 256);
+  };
+
+  float16_t acc[2][4];
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[f][q][i] = 0.0f;
+  // the lane's 4 columns of one row of a transposing read, for each fragment
+  const int trow = 8 * (lane >> 5) + ((lane >> 2) & 3), turn = 2 * ((lane >> 2) & 3);
+  uint32_t dat[2], xat[4];
+#pragma unroll
+  for (int f = 0; f < 4; ++f) {
+    const int chunk = 2 * f + ((lane >> 4) & 1);
+    if (f < 2) dat[f] = trow * kWgRowD + 32 * (((wave >> 1) * 4 + chunk) ^ turn) + 8 * (lane & 3);
+    xat[f] = kWgStageD + trow * kWgRowX + 32 * (((wave & 1) * 8 + chunk) ^ turn) + 8 * (lane & 3);
+  }
+  // (a half stage's operands lie 16 rows on, of both matrices)
+  uint32_t dat1[2], xat1[4];
+#pragma unroll
+  for (int f = 0; f < 4; ++f) {
+    if (f < 2) dat1[f] = dat[f] + 16 * kWgRowD;
+    xat1[f] = xat[f] + 16 * kWgRowX;
+  }
+  WgOperands o;
+  if (stages > 0) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      aim(s);
+#pragma unroll
+      for (int i = 0; i < kWgCopies; ++i) c.run(i, lds + s * kWgStage);
+    }
+    meet<(wait_vm(kWgCopies) & ~0x0F00)>();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < 2) o.a[0][i] = lds_column((const char *)lds + dat[i], kWgRowD);
+      o.b[0][i] = lds_column((const char *)lds + xat[i], kWgRowX);
+    }
+    int now = 0, next = kWgStage, free = 2 * kWgStage;           // places of this stage, the next, and the one behind it
+    for (int s = 0; s < stages; ++s) {
+      aim(s + 2);
+      wg_half<0>((const char *)lds + now, lds + free, acc, o, dat1, xat1, c);
+      // this wave's copies of the next stage (those of one more stay under way,
+      // which a fence would wait for) and its reads of this one
+      meet<(wait_vm(kWgCopies) & ~0x0F00)>();
+      wg_half<1>((const char *)lds + next, lds + free, acc, o, dat, xat, c);
+      const int was = now;
+      now = next;
+      next = free;
+      free = was;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));        // nothing is left that writes LDS
+  }
+  // register i of a fragment is row 8 (i / 4) + 4 h + i % 4, the lane its
+  // column; turned over the quads a lane has 4 neighbours of fragment lane % 4
+  // (stores of 16 bytes a lane, whole lines: with 4 the wave's 128 of them held
+  // the copies of the CU's other workgroup up, 530 -> 480 us)
+  const int64_t base = (int64_t)e * N, k = k0 + (wave & 1) * 128 + 32 * (lane & 3) + (lane & 28);
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int64_t n = n0 + (wave >> 1) * 64 + 32 * f + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
+      const f32x4_t v = quad_turn(acc[f][0][i], acc[f][1][i], acc[f][2][i], acc[f][3][i]);
+      if (n < N && k < K) store4(dw, dw_bf16, (base + n) * K, k, K, v);
+    }
+}
+
 template <typename D, typename X>
 hipError_t wgrad(const Groups &g, const Rows<D> &dy, const Rows<X> &x, void *dw, int dw_bf16, int64_t N, int64_t K,
                  hipStream_t stream) {
   constexpr bool narrow = sizeof(D) + sizeof(X) == 4;
-  constexpr int F = narrow ? 4 : 2, kTokens = narrow ? 64 : 32;
+  constexpr int F = narrow ? 4 : 2, kTokens = narrow ? 64 : 16;
   const int64_t tn = (N + 64 * F - 1) / (64 * F), tk = (K + 64 * F - 1) / (64 * F);
-  k_grouped_wgrad<D, X, F, F, kTokens><<<(unsigned)((tn * tk * g.count + kXcds - 1) / kXcds * kXcds), kThreads, 0, stream>>>(
-      g, dy, x, dw, dw_bf16, N, K, (int)tn, (int)tk);
+  const unsigned grid = (unsigned)(wgrad_quota((int)(tn * tk)) * kXcds * g.count);
+  if constexpr (narrow) {
+    const auto words = [](const Rows<uint16_t> &m, int64_t cols) {
+      return (uintptr_t)m.p % 4 == 0 && m.ld % 2 == 0 && cols % 2 == 0 && m.ld < (1LL << 24);
+    };
+    if (words(dy, N) && words(x, K)) {
+      const int64_t rows = (N + 127) / 128;
+      k_grouped_wgrad_dma<<<(unsigned)(wgrad_quota((int)(rows * tk)) * kXcds * g.count), kThreads, 0, stream>>>(
+          g, dy, x, dw, dw_bf16, N, K, (int)rows, (int)tk);
+      return hipGetLastError();
+    }
+  }
+  k_grouped_wgrad<D, X, F, F, kTokens><<<grid, kThreads, 0, stream>>>(g, dy, x, dw, dw_bf16, N, K, (int)tn, (int)tk);
   return hipGetLastError();
 }
 

@@ -41,6 +41,10 @@ struct GroupTile {
 // The id-th of all tiles (units for each tile of rows), counted over the
 // groups in their order, found by a wave 64 groups at a time; `total` becomes
 // the number of all of them.  Every lane has the result.
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+}
 __device__ __forceinline__ int wave_total(int v) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
@@ -70,15 +74,15 @@ __device__ __forceinline__ GroupTile find_tile(const Groups &g, int tile, int un
       const int v = __shfl_up(sum, off, 64);
       if (lane >= off) sum += v;
     }
-    const int all = __shfl(sum, 63, 64);
+    const int all = __builtin_amdgcn_readfirstlane(__shfl(sum, 63, 64));      // (uniform, so that the branch is)
     if (index < before + all) {
       const uint64_t past = __ballot(before + sum > index);
       const int who = __builtin_ctzll(past);
       t.e = __builtin_amdgcn_readfirstlane(e0 + who);
       t.tiles = __builtin_amdgcn_readfirstlane(__shfl(tiles, who, 64));
       t.local = __builtin_amdgcn_readfirstlane(index - before - (__shfl(sum, who, 64) - t.tiles * units));
-      t.begin = g.at(t.e);
-      t.end = g.at(t.e + 1);
+      t.begin = uniform64(g.at(t.e));
+      t.end = uniform64(g.at(t.e + 1));
       return t;
     }
     before += all;

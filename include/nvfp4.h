@@ -550,7 +550,7 @@ int64_t nvfp4_matvec_workspace_bytes(int64_t n, int64_t k, int64_t tokens, int x
  * dw: device, dw_dtype [experts][n][k], written whole (zeros for a group
  * without rows); must not overlap dy or x.  bf16 products are exact; with a
  * float32 operand products are off by at most 2^-23 of their magnitude, and
- * those with an infinity are infinite or NaN.  Sums are binary32.  experts * ceil(n / 128) * ceil(k / 128) <= 2^24 - 8.
+ * those with an infinity are infinite or NaN.  Sums are binary32.  experts * (ceil(n / 128) * ceil(k / 128) + 7) <= 2^24 - 8.
  * Deterministic.  Enqueues one kernel.
  */
 int nvfp4_grouped_matmul(const nvfp4_tensor *w, int transposed, const void *x, int x_dtype, int64_t rows, int64_t ldx,
