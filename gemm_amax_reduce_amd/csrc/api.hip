@@ -187,6 +187,9 @@ int check_rms(const nvfp4::RmsForward &a) {
 // smallest tiles.
 constexpr int64_t kMaxGrid = (1LL << 24) - 8;
 constexpr int64_t kMaxGroups = 1LL << 20;
+// A row of a stack of experts' weights: 16 of them, K / 2 bytes each, are
+// addressed with 32-bit buffer offsets below 2^31.
+constexpr int64_t kMaxStackK = (1LL << 28) - 32;
 inline bool grid_ok(int64_t a, int64_t b) { return a <= 0 || b <= kMaxGrid / a; }
 inline bool grouped_ok(int64_t experts, int64_t n, int64_t k, int64_t rows) {
   return experts >= 1 && experts <= kMaxGroups && k <= kMaxGemmK && n <= kMaxMatvecRows &&
@@ -207,7 +210,7 @@ int grouped_common(nvfp4::GroupedProduct p, int64_t outer, int64_t k, int64_t wo
   const int64_t block = p.mx ? 32 : 16;
   p.n = p.transposed ? outer : outer / p.experts;
   p.k = p.transposed ? k / p.experts : k;
-  if ((p.transposed ? k : outer) % p.experts != 0 || p.k % block != 0) return NVFP4_ERR_SHAPE;
+  if ((p.transposed ? k : outer) % p.experts != 0 || p.k % block != 0 || k > kMaxStackK) return NVFP4_ERR_SHAPE;
   if (!matrix_ok(p.rows, p.k, p.ldx) || !matrix_ok(p.rows, p.n, p.ldy) || !grouped_ok(p.experts, p.n, p.k, p.rows))
     return NVFP4_ERR_SHAPE;
   if (p.rows > 0 && p.n > 0 && (!p.y || !p.offsets || (p.k > 0 && !p.x))) return NVFP4_ERR_NULL;

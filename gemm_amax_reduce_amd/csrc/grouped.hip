@@ -73,221 +73,32 @@ __device__ void zero_rest(const Groups &g, void *y, int y_bf16, int64_t ldy, int
   }
 }
 
-// XP: bf16 parts of an activation (1: bf16, 3: float32).
-template <bool MX, typename X, int NF, int MF>
-__global__ __launch_bounds__(kThreads, NF * MF >= 16 ? 1 : NF * MF >= 4 ? 2 : 4) void
-k_grouped(Stack w, Groups g, Rows<X> x, void *y, int y_bf16, int64_t ldy, int tiles_n, int fill) {
-  constexpr int kXP = sizeof(X) == 2 ? 1 : 3;
-  constexpr int BN = 128 * NF, BM = 32 * MF;
-  constexpr int kG = Scale<MX>::kPerByte, kSB = kStage / kG;        // scale bytes of a row and stage
-  constexpr int kCodes = BN * kStage / 2, kScales = BN * 8, kPart = BM * kStage * 2;
-  constexpr int kBuffer = kCodes + kScales + kXP * kPart;
-  constexpr int kCL = BN * 4 / kThreads;                            // 16-byte pieces of codes a thread loads
-  constexpr int kXL = BM * 16 / kThreads;                           // 8-element pieces of x
-  constexpr int kSL = (BN + kThreads - 1) / kThreads;               // scale rows
-  __shared__ __align__(16) char lds[2 * kBuffer];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 31, h = lane >> 5;
-
-  if (fill) zero_rest(g, y, y_bf16, ldy, w.N);
-  const int total = count_tiles(g, BM) * tiles_n;
-  // workgroups are dealt to the XCDs in turn: each gets a run of tiles
-  const int quota = (total + kXcds - 1) / kXcds, local = blockIdx.x / kXcds;
-  const int index = (int)(blockIdx.x % kXcds) * quota + local;
-  if (local >= quota || index >= total) return;
-  const GroupTile t = find_tile(g, BM, tiles_n, index);
-  if (t.e < 0) return;
-  // up to 8 tiles of tokens with one tile of weights after the other
-  const int per = 8 * tiles_n, first_m = t.local / per * 8, gsz = min(t.tiles - first_m, 8);
-  const int64_t m0 = t.begin + (int64_t)(first_m + t.local % per % gsz) * BM;
-  const int64_t n0 = (int64_t)(t.local % per / gsz) * BN;
-
-  const int stages = (int)((w.K + kStage - 1) / kStage);
-  const uint8_t *const codes = w.codes + t.e * w.code_step, *const scales = w.scales + t.e * w.scale_step;
-
-  // ---- from memory to registers
-  const uint8_t *crow[kCL], *srow[kSL];
-  const X *xrow[kXL];
-  bool live[kXL];
-#pragma unroll
-  for (int i = 0; i < kCL; ++i)
-    crow[i] = codes + min(n0 + (tid + i * kThreads) / 4, w.N - 1) * w.code_pitch + 16 * (tid & 3);
-#pragma unroll
-  for (int i = 0; i < kSL; ++i) srow[i] = scales + min(n0 + tid + i * kThreads, w.N - 1) * w.scale_pitch;
-#pragma unroll
-  for (int i = 0; i < kXL; ++i) {
-    const int64_t row = m0 + tid / 16 + 16 * i;
-    live[i] = row < t.end;
-    xrow[i] = x.p + min(row, t.end - 1) * x.ld + 8 * (tid & 15);
-  }
-  u32x4_t creg[kCL];
-  uint64_t sreg[kSL];
-  Row8<X> xreg[kXL];
-  const auto load = [&](int s) {
-    const int64_t k0 = (int64_t)s * kStage;
-    if (k0 + kStage <= w.K) {
-#pragma unroll
-      for (int i = 0; i < kCL; ++i) creg[i] = *reinterpret_cast<const u32x4_a8 *>(crow[i] + k0 / 2);
-#pragma unroll
-      for (int i = 0; i < kSL; ++i) {
-        sreg[i] = 0;
-        __builtin_memcpy(&sreg[i], srow[i] + k0 / kG, kSB);
-      }
-#pragma unroll
-      for (int i = 0; i < kXL; ++i) xreg[i].load(xrow[i] + k0);
+// Activations as the kernel copies them: bf16 rows of whole words.  Where a
+// call's own are not (float32, or rows at odd places), they are brought to
+// that first: [parts][rows][K] in the workspace.
+template <typename X>
+__global__ __launch_bounds__(256) void k_parts(const X *x, int64_t ldx, int64_t rows, int64_t K, uint16_t *out) {
+  const int64_t pieces = K / 8, all = rows * pieces;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    const int64_t at = i / pieces * K + i % pieces * 8;
+    Row8<X> q;
+    q.load(x + i / pieces * ldx + i % pieces * 8);
+    if constexpr (sizeof(X) == 2) {
+      *reinterpret_cast<u32x4_t *>(out + at) = q.r;
     } else {
-      // the last stage of K % 128 != 0: zeros past K (a scale of 1 for MXFP4)
-      const int64_t left = w.K - k0;
+      const Parts p = split8((f32x4_t)q.a, (f32x4_t)q.b);
 #pragma unroll
-      for (int i = 0; i < kCL; ++i) {
-        const int at = 32 * (tid & 3);
-        u32x2_a8 lo = {0, 0}, hi = {0, 0};
-        if (at < left) lo = *reinterpret_cast<const u32x2_a8 *>(crow[i] + k0 / 2);
-        if (at + 16 < left) hi = *reinterpret_cast<const u32x2_a8 *>(crow[i] + k0 / 2 + 8);
-        creg[i] = (u32x4_t){lo[0], lo[1], hi[0], hi[1]};
-      }
-#pragma unroll
-      for (int i = 0; i < kSL; ++i) {
-        sreg[i] = MX ? 0x7F7F7F7F7F7F7F7Full : 0;
-        for (int b = 0; b < kSB; ++b)
-          if (b * kG < left) sreg[i] = (sreg[i] & ~(0xFFull << (8 * b))) | (uint64_t)srow[i][k0 / kG + b] << (8 * b);
-      }
-#pragma unroll
-      for (int i = 0; i < kXL; ++i) {
-        if (8 * (tid & 15) < left) xreg[i].load(xrow[i] + k0);
-        else xreg[i].zero();
-      }
-    }
-  };
-
-  // ---- from registers to LDS.  Codes: 4 pieces a row, piece c in slot
-  // c ^ (row / 16 % 4); x: 16 pieces a row, piece p in slot p ^ (row % 16): the
-  // 8 lanes of a 16-byte read that go together fall on all banks.
-  const auto put = [&](int s) {
-    char *const buf = lds + (s & 1) * kBuffer;
-#pragma unroll
-    for (int i = 0; i < kCL; ++i) {
-      const int row = (tid + i * kThreads) / 4;
-      *reinterpret_cast<u32x4_t *>(buf + row * 64 + 16 * ((tid & 3) ^ ((row >> 4) & 3))) = creg[i];
-    }
-#pragma unroll
-    for (int i = 0; i < kSL; ++i)
-      if (BN % kThreads == 0 || tid + i * kThreads < BN)
-        *reinterpret_cast<uint64_t *>(buf + kCodes + (tid + i * kThreads) * 8) = sreg[i];
-#pragma unroll
-    for (int i = 0; i < kXL; ++i) {
-      const int row = tid / 16 + 16 * i;
-      char *const at = buf + kCodes + kScales + row * 256 + 16 * ((tid & 15) ^ (row & 15));
-      if constexpr (kXP == 1) {
-        *reinterpret_cast<u32x4_t *>(at) = live[i] ? (u32x4_t)xreg[i].r : (u32x4_t){0, 0, 0, 0};
-      } else {
-        if (!live[i]) xreg[i].zero();
-        const Parts q = split8((f32x4_t)xreg[i].a, (f32x4_t)xreg[i].b);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x4_t *>(at + p * kPart) = q.v[p];
-      }
-    }
-  };
-
-  // ---- a stage's products.  Row r of fragment f is weight row f * 32 +
-  // (r / 4 % 2) * 16 + r / 8 * 4 + r % 4 of the wave's, so that the lane's
-  // results of a fragment are 16 consecutive n.  A lane's 32 codes of a half
-  // stage are k 32 h .. 32 h + 31 of it, 8 an MFMA.
-  float16_t acc[NF][MF];
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-#pragma unroll
-    for (int m = 0; m < MF; ++m)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[f][m][i] = 0.0f;
-  const int wrow = wave * (32 * NF) + ((r >> 2) & 1) * 16 + (r >> 3) * 4 + (r & 3);
-  const auto half_stage = [&](int s, int sub) {
-    const char *const buf = lds + (s & 1) * kBuffer;
-    u32x4_t c[NF];
-    Scale<MX> sc[NF];
-#pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      const int row = wrow + 32 * f;
-      c[f] = *reinterpret_cast<const u32x4_t *>(buf + row * 64 + 16 * ((2 * sub + h) ^ ((row >> 4) & 3)));
-      const char *const sp = buf + kCodes + row * 8 + (2 * sub + h) * (32 / kG);
-      if (MX) sc[f].raw = *reinterpret_cast<const uint8_t *>(sp);
-      else sc[f].raw = *reinterpret_cast<const uint16_t *>(sp);
-    }
-    // MXFP4 at a quarter: the largest scales' weights pass bf16's range
-    // otherwise; scales too near either end for the conversion's own go by
-    // products
-    bool far = false;
-    if constexpr (MX) {
-#pragma unroll
-      for (int f = 0; f < NF; ++f) far |= sc[f].raw - 3 >= 250;
-      far = __any(far);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      bf16x8_t a[NF];
-#pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        if constexpr (MX) {
-          if (far) a[f] = decode8<false>(c[f][j], sc[f].quarter());
-          else a[f] = decode8<true>(c[f][j], __uint_as_float((sc[f].raw - 2) << 23));
-        } else {
-          a[f] = decode8<false>(c[f][j], j < 2 ? sc[f].lo() : sc[f].hi());
-        }
-      }
-#pragma unroll
-      for (int m = 0; m < MF; ++m) {
-        const int row = 32 * m + r;
-        const char *const at = buf + kCodes + kScales + row * 256 + 16 * ((8 * sub + 4 * h + j) ^ (row & 15));
-#pragma unroll
-        for (int p = 0; p < kXP; ++p) {
-          const bf16x8_t b = *reinterpret_cast<const bf16x8_t *>(at + p * kPart);
-#pragma unroll
-          for (int f = 0; f < NF; ++f) acc[f][m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[f], b, acc[f][m], 0, 0, 0);
-        }
-      }
-    }
-  };
-
-  if (stages > 0) {
-    load(0);
-    put(0);
-    if (stages > 1) load(1);
-    __syncthreads();
-    for (int s = 0; s < stages; ++s) {
-      half_stage(s, 0);
-      half_stage(s, 1);
-      if (s + 1 < stages) put(s + 1);
-      if (s + 2 < stages) load(s + 2);
-      __syncthreads();
-    }
-  }
-
-  const float scale = MX ? 4.0f : w.K > 0 ? w.meta[1] : 0.0f;      // (g of no weights may be anything)
-#pragma unroll
-  for (int m = 0; m < MF; ++m) {
-    const int64_t row = m0 + 32 * m + r;
-    if (row >= t.end) continue;
-#pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      float v[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = acc[f][m][i] * scale;
-      store16(y, y_bf16, row * ldy, n0 + wave * (32 * NF) + 32 * f + 16 * h, w.N, v);
+      for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x4_t *>(out + k * rows * K + at) = p.v[k];
     }
   }
 }
 
-// ------------------------------------------------- bf16, larger groups --
-
-// The same tiles with both operands copied to LDS by DMA, a stage ahead, and
-// the work of a K step (the 16 k of an MFMA) in a fixed order: each MFMA is
-// followed by its share of decoding the next step's weights, so that one wave a
-// SIMD keeps the matrix pipe busy.  A stage's copies go out over the first four
-// of its eight steps; in the last one the wave waits for those of the stage
-// behind, meets the others, and reads from it.
-//
-// x rows of a multiple of 4 bytes, from an address of one (the range check that
-// makes rows past the group zeros works by words).
+// Both operands are copied to LDS by DMA, a stage ahead, and the work of a K
+// step (the 16 k of an MFMA) goes in a fixed order: each MFMA is followed by
+// its share of decoding the next step's weights, so that one wave a SIMD keeps
+// the matrix pipe busy.  A stage's copies go out over the first four of its
+// eight steps; in the last one the wave waits for those of the stage behind,
+// meets the others, and reads from it.
 constexpr int wait_vm(int n) { return (n & 15) | (n >> 4) << 14 | 0x0F70; }
 // A wait for those counts, and the workgroup's barrier.
 template <int COUNTS> __device__ __forceinline__ void meet() {
@@ -299,15 +110,20 @@ template <int COUNTS> __device__ __forceinline__ void meet() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <bool MX, int NF, int MF>
-__global__ __launch_bounds__(kThreads, NF * MF >= 16 ? 1 : 2) void
-k_grouped_dma(Stack w, Groups g, Rows<uint16_t> x, void *y, int y_bf16, int64_t ldy, int tiles_n, int fill) {
-  constexpr int BN = 128 * NF, BM = 32 * MF;
+// XP: parts of x (3: float32), `part` elements apart.
+template <bool MX, int XP, int WAVES, int NF, int MF>
+__global__ __launch_bounds__(64 * WAVES, WAVES == 4 && NF * MF * XP < 12 ? 2 : 1) void
+k_grouped(Stack w, Groups g, Rows<uint16_t> x, int64_t part, void *y, int y_bf16, int64_t ldy, int tiles_n, int fill) {
+  constexpr int BN = 32 * WAVES * NF, BM = 32 * MF;
   constexpr int kG = Scale<MX>::kPerByte, kSB = kStage / kG;
-  constexpr int kCodes = BN * kStage / 2, kScales = BN * 8, kBuffer = kCodes + kScales + BM * kStage * 2;
-  constexpr int kCL = BN / 64, kXL = BM / 16;        // DMA instructions a wave and stage: 16 rows of codes, 4 of x each
-  constexpr int kSL = (BN + kThreads - 1) / kThreads;
-  __shared__ __align__(16) uint8_t lds[2 * kBuffer];
+  constexpr int kCodes = BN * kStage / 2, kScales = BN * 8, kPart = BM * kStage * 2, kBuffer = kCodes + kScales + XP * kPart;
+  // DMA instructions a wave and stage: 16 rows of codes, 4 of a part of x each
+  constexpr int kCL = BN / WAVES / 16, kXL = BM / WAVES / 4;
+  constexpr int kSL = NF / 2;                        // weight rows of a lane, whose scales it fetches: its wave's own
+  static_assert(kXL >= 1 && kSL >= 1, "a wave copies whole instructions");
+  // (one array for all: with two of them every read would wait for the copies
+  // under way)
+  __shared__ __align__(16) uint8_t lds[2 * kBuffer + 4 * WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5;
 
@@ -328,36 +144,42 @@ k_grouped_dma(Stack w, Groups g, Rows<uint16_t> x, void *y, int y_bf16, int64_t 
   // (l % 16) ^ (row % 16).  A wave's instructions are BN / 4 rows of codes and
   // BM / 4 of x, from views of the tile's own rows.
   const uint32_t cp = (uint32_t)w.code_pitch, xp = (uint32_t)(x.ld * 2), kb = (uint32_t)w.K;
-  const __amdgpu_buffer_rsrc_t cview =
-      make_rsrc(w.codes + t.e * w.code_step + n0 * w.code_pitch,
-                (uint32_t)(min((int64_t)BN, w.N - n0) - 1) * cp + kb / 2);
-  const __amdgpu_buffer_rsrc_t xview =
-      make_rsrc(x.p + m0 * x.ld, (uint32_t)(min((int64_t)BM, t.end - m0) - 1) * xp + kb * 2);
-  const uint32_t crow = (uint32_t)(wave * (BN / 4) + (lane >> 2)) * cp, cpiece = (uint32_t)lane & 3;
-  const uint32_t xrow = (uint32_t)(wave * (BM / 4) + (lane >> 4)) * xp, xpiece = (uint32_t)(lane & 15) ^ (lane >> 4);
+  // (codes: a view for each instruction's 16 rows, whose offsets stay small
+  // however long the stack's rows are)
+  const auto cview = [&](int i) {
+    const int64_t row = n0 + wave * (BN / WAVES) + 16 * i, rows = min(w.N - row, (int64_t)16);
+    return make_rsrc(w.codes + t.e * w.code_step + row * w.code_pitch, rows > 0 ? (uint32_t)(rows - 1) * cp + kb / 2 : 0u);
+  };
+  const int64_t xfirst = m0 + wave * (BM / WAVES), xrows = min(t.end - xfirst, (int64_t)(BM / WAVES));
+  const auto xview = [&](int p) {
+    return make_rsrc(x.p + p * part + xfirst * x.ld, xrows > 0 ? (uint32_t)(xrows - 1) * xp + kb * 2 : 0u);
+  };
+  const uint32_t crow = (uint32_t)(lane >> 2) * cp, cpiece = (uint32_t)lane & 3;
+  const uint32_t xrow = (uint32_t)(lane >> 4) * xp, xpiece = (uint32_t)(lane & 15) ^ (lane >> 4);
   const uint8_t *srow[kSL];
 #pragma unroll
   for (int i = 0; i < kSL; ++i)
-    srow[i] = w.scales + t.e * w.scale_step + min(n0 + tid + i * kThreads, w.N - 1) * w.scale_pitch;
+    srow[i] = w.scales + t.e * w.scale_step + min(n0 + wave * (32 * NF) + lane + 64 * i, w.N - 1) * w.scale_pitch;
   uint64_t sreg[kSL];
-  // part q of 4 of stage s (nothing past the last one)
-  const auto copy = [&](int s, int q) {
+  // instruction u of a stage's kC copies (nothing past the last stage); the
+  // scales, by way of registers, with the first
+  constexpr int kC = kCL + XP * kXL;
+  const auto copy = [&](int s, int u) {
     uint8_t *const buf = lds + (s & 1) * kBuffer;
     const uint32_t k0 = (uint32_t)s * kStage;
     const bool in = s < stages;
-#pragma unroll
-    for (int i = q * kCL / 4; i < (q + 1) * kCL / 4; ++i) {
-      const uint32_t piece = cpiece ^ (uint32_t)((wave * (BN / 64) + i) & 3);
+    if (u < kCL) {
+      const uint32_t piece = cpiece ^ (uint32_t)((wave * (BN / WAVES / 16) + u) & 3);
       const uint32_t at = !in || k0 + 32 * piece < kb ? crow + 16 * piece : kOutOfRange;
-      dma16(cview, buf + (wave * (BN / 4) + 16 * i) * 64, at, in ? 16u * i * cp + k0 / 2 : kOutOfRange);
-    }
-#pragma unroll
-    for (int i = q * kXL / 4; i < (q + 1) * kXL / 4; ++i) {
-      const uint32_t piece = xpiece ^ (uint32_t)((wave * (BM / 4) + 4 * i) & 15);
+      dma16(cview(u), buf + (wave * (BN / WAVES) + 16 * u) * 64, at, in ? k0 / 2 : kOutOfRange);
+    } else {
+      const int p = (u - kCL) / kXL, i = (u - kCL) % kXL;
+      const uint32_t piece = xpiece ^ (uint32_t)((wave * (BM / WAVES) + 4 * i) & 15);
       const uint32_t at = !in || k0 + 8 * piece < kb ? xrow + 16 * piece : kOutOfRange;
-      dma16(xview, buf + kCodes + kScales + (wave * (BM / 4) + 4 * i) * 256, at, in ? 4u * i * xp + k0 * 2 : kOutOfRange);
+      dma16(xview(p), buf + kCodes + kScales + p * kPart + (wave * (BM / WAVES) + 4 * i) * 256, at,
+            in ? 4u * i * xp + k0 * 2 : kOutOfRange);
     }
-    if (q == 0 && in) {
+    if (u == 0 && in) {
       if ((int64_t)k0 + kStage <= w.K) {
 #pragma unroll
         for (int i = 0; i < kSL; ++i) {
@@ -378,23 +200,15 @@ k_grouped_dma(Stack w, Groups g, Rows<uint16_t> x, void *y, int y_bf16, int64_t 
   const auto put_scales = [&](int s) {
 #pragma unroll
     for (int i = 0; i < kSL; ++i)
-      if (BN % kThreads == 0 || tid + i * kThreads < BN)
-        *reinterpret_cast<uint64_t *>(lds + (s & 1) * kBuffer + kCodes + (tid + i * kThreads) * 8) = sreg[i];
+      *reinterpret_cast<uint64_t *>(lds + (s & 1) * kBuffer + kCodes + (wave * (32 * NF) + lane + 64 * i) * 8) = sreg[i];
   };
 
   // ---- operands.  Half stage p (0, 1) of a stage is four K steps.
   float16_t acc[NF][MF];
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-#pragma unroll
-    for (int m = 0; m < MF; ++m)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[f][m][i] = 0.0f;
   const int wrow = wave * (32 * NF) + ((r >> 2) & 1) * 16 + (r >> 3) * 4 + (r & 3);
   u32x4_t c[2][NF];
   Scale<MX> sc[2][NF];
-  bool far[2] = {false, false};
-  bf16x8_t a[2][NF], b[2][MF];
+  bf16x8_t a[2][NF], b[2][XP][MF];
   const auto read_codes = [&](int s, int p) {
     const uint8_t *const buf = lds + (s & 1) * kBuffer;
 #pragma unroll
@@ -406,26 +220,32 @@ k_grouped_dma(Stack w, Groups g, Rows<uint16_t> x, void *y, int y_bf16, int64_t 
       else sc[p][f].raw = *reinterpret_cast<const uint16_t *>(sp);
     }
   };
-  const auto read_x = [&](int s, int p, int j, int into) {
+  const auto read_x = [&](int s, int p, int j, int u, int into) {
     const uint8_t *const buf = lds + (s & 1) * kBuffer + kCodes + kScales;
-#pragma unroll
-    for (int m = 0; m < MF; ++m)
-      b[into][m] = *reinterpret_cast<const bf16x8_t *>(buf + (32 * m + r) * 256 + 16 * ((8 * p + 4 * h + j) ^ (r & 15)));
-  };
-  const auto check_far = [&](int p) {
-    if constexpr (MX) {
-      bool any = false;
-#pragma unroll
-      for (int f = 0; f < NF; ++f) any |= sc[p][f].raw - 3 >= 250;
-      far[p] = __any(any);
-    }
+    const int k = u / MF, m = u % MF;
+    b[into][k][m] = *reinterpret_cast<const bf16x8_t *>(buf + k * kPart + (32 * m + r) * 256 +
+                                                        16 * ((8 * p + 4 * h + j) ^ (r & 15)));
   };
   // a quarter of a fragment's 8 weights (MXFP4: all of them for quarter 0)
-  const auto decode = [&](int p, int j, int f, int quarter, int into) {
+  // MXFP4 weights are decoded at a quarter: those of the largest scales would
+  // pass bf16's range.  Where a scale lies too near either end for the
+  // conversion's own (and is not that of zeros), the tile is done once more, FAR,
+  // by products.
+  uint32_t ends = 0;
+  const auto check = [&](int p) {
+    if constexpr (MX) {
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        const uint32_t raw = sc[p][f].raw, any = (c[p][f][0] | c[p][f][1] | c[p][f][2] | c[p][f][3]) & 0x77777777u;
+        ends |= raw >= 253 ? 1u : raw < 3 ? any : 0u;
+      }
+    }
+  };
+  const auto decode = [&](int p, int j, int f, int quarter, int into, auto far) {
     if constexpr (MX) {
       if (quarter) return;
-      if (far[p]) a[into][f] = decode8<false>(c[p][f][j], sc[p][f].quarter());
-      else a[into][f] = decode8<true>(c[p][f][j], __uint_as_float((sc[p][f].raw - 2) << 23));
+      if constexpr (far.value) a[into][f] = decode8<false>(c[p][f][j], sc[p][f].quarter());
+      else a[into][f] = decode8<true>(c[p][f][j], __uint_as_float((max(sc[p][f].raw, 3u) - 2) << 23));
     } else {
       const float s = j < 2 ? sc[p][f].lo() : sc[p][f].hi();
       const uint32_t code = c[p][f][j];
@@ -438,10 +258,10 @@ k_grouped_dma(Stack w, Groups g, Rows<uint16_t> x, void *y, int y_bf16, int64_t 
       a[into][f][2 * quarter + 1] = q[1];
     }
   };
-  constexpr int NU = NF * MF, ND = 4 * NF;           // MFMAs and quarters to decode of a K step
+  constexpr int NU = NF * MF * XP, ND = 4 * NF;      // MFMAs and quarters to decode of a K step
   // K step j of half p of stage s: operands of `cur` are there; the next step's
   // go to the other.
-  const auto step = [&](int s, auto half, auto kstep) {
+  const auto step = [&](int s, auto half, auto kstep, auto far) {
     constexpr int p = decltype(half)::value, j = decltype(kstep)::value;
     constexpr int cur = j & 1, nxt = cur ^ 1, np = j == 3 ? p ^ 1 : p, nj = (j + 1) & 3;
     if constexpr (p == 1 && j == 3) {
@@ -450,54 +270,90 @@ k_grouped_dma(Stack w, Groups g, Rows<uint16_t> x, void *y, int y_bf16, int64_t 
       put_scales(s + 1);
       __syncthreads();
       read_codes(s + 1, 0);
-      read_x(s + 1, 0, 0, nxt);
-    } else {
-      if constexpr (p == 0) copy(s + 1, j);
-      if constexpr (p == 0 && j == 2) read_codes(s, 1);
-      read_x(s, np, nj, nxt);
+    } else if constexpr (p == 0 && j == 2) {
+      read_codes(s, 1);
     }
     constexpr int kLag = j == 3 && NU >= 4 ? NU / 4 : 0;      // codes just read are not there yet
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       __builtin_amdgcn_sched_barrier(0);
-      const int m = i / NF, f = (m & 1) ? NF - 1 - i % NF : i % NF;
-      acc[f][m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[cur][f], b[cur][m], acc[f][m], 0, 0, 0);
+      // snake order: one operand stays the same to the next MFMA
+      const int k = i / (NF * MF), m = i / NF % MF, f = (m & 1) ? NF - 1 - i % NF : i % NF;
+      acc[f][m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[cur][f], b[cur][k][m], acc[f][m], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
-      if (j == 3 && i == kLag) check_far(np);
+      // the next step's x in the first half of the step, copies over all of it
+      constexpr int kHalf = (NU + 1) / 2;
+      if (i < kHalf) {
+#pragma unroll
+        for (int u = i * XP * MF / kHalf; u < (i + 1) * XP * MF / kHalf; ++u)
+          read_x(p == 1 && j == 3 ? s + 1 : s, np, nj, u, nxt);
+      }
+      if (p == 0) {
+#pragma unroll
+        for (int u = (j * NU + i) * kC / (4 * NU); u < (j * NU + i + 1) * kC / (4 * NU); ++u) copy(s + 1, u);
+      }
+      if (j == 3 && i == kLag && !far.value) check(np);
       if (i >= kLag) {
         const int d0 = (i - kLag) * ND / (NU - kLag), d1 = (i - kLag + 1) * ND / (NU - kLag);
 #pragma unroll
-        for (int d = d0; d < d1; ++d) decode(np, nj, d / 4, d % 4, nxt);
+        for (int d = d0; d < d1; ++d) decode(np, nj, d / 4, d % 4, nxt, far);
       }
     }
   };
 
-  if (stages > 0) {
+  const auto run = [&](auto far) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) copy(0, q);
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int m = 0; m < MF; ++m)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[f][m][i] = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kC; ++u) copy(0, u);
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
     put_scales(0);
     __syncthreads();
     read_codes(0, 0);
-    read_x(0, 0, 0, 0);
-    check_far(0);
 #pragma unroll
-    for (int d = 0; d < ND; ++d) decode(0, 0, d / 4, d % 4, 0);
+    for (int u = 0; u < XP * MF; ++u) read_x(0, 0, 0, u, 0);
+    if (!far.value) check(0);
+#pragma unroll
+    for (int d = 0; d < ND; ++d) decode(0, 0, d / 4, d % 4, 0, far);
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
     using I2 = std::integral_constant<int, 2>;
     using I3 = std::integral_constant<int, 3>;
     for (int s = 0; s < stages; ++s) {
-      step(s, I0{}, I0{});
-      step(s, I0{}, I1{});
-      step(s, I0{}, I2{});
-      step(s, I0{}, I3{});
-      step(s, I1{}, I0{});
-      step(s, I1{}, I1{});
-      step(s, I1{}, I2{});
-      step(s, I1{}, I3{});
+      step(s, I0{}, I0{}, far);
+      step(s, I0{}, I1{}, far);
+      step(s, I0{}, I2{}, far);
+      step(s, I0{}, I3{}, far);
+      step(s, I1{}, I0{}, far);
+      step(s, I1{}, I1{}, far);
+      step(s, I1{}, I2{}, far);
+      step(s, I1{}, I3{}, far);
     }
     __builtin_amdgcn_sched_barrier(0);
+  };
+  if (stages == 0) {
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int m = 0; m < MF; ++m)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[f][m][i] = 0.0f;
+  } else {
+    run(std::false_type());
+    if constexpr (MX) {
+      uint32_t *const far = reinterpret_cast<uint32_t *>(lds + 2 * kBuffer);
+      const bool any = __any(ends != 0);
+      if (lane == 0) far[wave] = any;
+      __syncthreads();
+      uint32_t all = 0;
+#pragma unroll
+      for (int i = 0; i < WAVES; ++i) all |= far[i];
+      if (__builtin_amdgcn_readfirstlane(all)) run(std::true_type());
+    }
   }
 
   const float scale = MX ? 4.0f : w.K > 0 ? w.meta[1] : 0.0f;
@@ -515,41 +371,41 @@ k_grouped_dma(Stack w, Groups g, Rows<uint16_t> x, void *y, int y_bf16, int64_t 
   }
 }
 
-// Weight rows and tokens of a tile, in fragments of 32 (times 4 waves).
-struct GroupedCut {
-  int nf, mf;
-};
-GroupedCut grouped_cut(const Stack &w, int experts, int64_t tokens, bool f32) {
-  const int64_t each = (tokens + experts - 1) / experts;      // rows of a group, on average
-  if (each <= 40) return {1, 1};
-  if (each <= 128 || f32) return {2, 2};
-  return {4, 4};
-}
-
-template <bool MX, typename X, int NF, int MF>
-hipError_t grouped(const Stack &w, const Groups &g, const Rows<X> &x, void *y, int y_bf16, int64_t ldy, int fill,
-                   hipStream_t stream) {
-  constexpr int BN = 128 * NF, BM = 32 * MF;
+template <bool MX, int XP, int WAVES, int NF, int MF>
+hipError_t grouped(const Stack &w, const Groups &g, const Rows<uint16_t> &x, int64_t part, void *y, int y_bf16, int64_t ldy,
+                   int fill, hipStream_t stream) {
+  constexpr int BN = 32 * WAVES * NF, BM = 32 * MF;
   const int64_t tiles_n = (w.N + BN - 1) / BN, tiles_m = g.rows / BM + std::min<int64_t>(g.count, g.rows);
-  const unsigned grid = (unsigned)((tiles_n * tiles_m + kXcds - 1) / kXcds * kXcds);
-  if constexpr (sizeof(X) == 2 && NF > 1) {
-    // copies by DMA: words, and offsets inside a tile below 2^31
-    if ((uintptr_t)x.p % 4 == 0 && x.ld % 2 == 0 && x.ld < (1LL << 22) && w.code_pitch < (1LL << 21)) {
-      k_grouped_dma<MX, NF, MF><<<grid, kThreads, 0, stream>>>(w, g, x, y, y_bf16, ldy, (int)tiles_n, fill);
-      return hipGetLastError();
-    }
-  }
-  k_grouped<MX, X, NF, MF><<<grid, kThreads, 0, stream>>>(w, g, x, y, y_bf16, ldy, (int)tiles_n, fill);
+  k_grouped<MX, XP, WAVES, NF, MF><<<(unsigned)((tiles_n * tiles_m + kXcds - 1) / kXcds * kXcds), 64 * WAVES, 0, stream>>>(
+      w, g, x, part, y, y_bf16, ldy, (int)tiles_n, fill);
   return hipGetLastError();
 }
-template <bool MX, typename X>
-hipError_t grouped_x(const Stack &w, const Groups &g, const Rows<X> &x, void *y, int y_bf16, int64_t ldy, int fill,
-                     hipStream_t stream) {
-  const GroupedCut c = grouped_cut(w, g.count, g.rows, sizeof(X) == 4);
-  if (c.nf == 1) return grouped<MX, X, 1, 1>(w, g, x, y, y_bf16, ldy, fill, stream);
-  if constexpr (sizeof(X) == 2)
-    if (c.nf == 4) return grouped<MX, X, 4, 4>(w, g, x, y, y_bf16, ldy, fill, stream);
-  return grouped<MX, X, 2, 2>(w, g, x, y, y_bf16, ldy, fill, stream);
+
+// Whether a call's x is copied from where it lies.
+bool copied_as_is(const void *x, int64_t ldx, bool f32) {
+  return !f32 && (uintptr_t)x % 4 == 0 && ldx % 2 == 0 && ldx < (1LL << 24);
+}
+
+template <bool MX>
+hipError_t grouped_tiles(const GroupedProduct &p, const Stack &w, const Groups &g, hipStream_t stream) {
+  const bool f32 = p.x_dtype == 0;
+  Rows<uint16_t> x = {(const uint16_t *)p.x, p.ldx};
+  const int64_t part = p.rows * p.k;
+  if (p.k > 0 && !copied_as_is(p.x, p.ldx, f32)) {
+    const unsigned grid = (unsigned)std::min<int64_t>((part / 8 + 255) / 256, 1 << 14);
+    if (f32) k_parts<<<grid, 256, 0, stream>>>((const float *)p.x, p.ldx, p.rows, p.k, (uint16_t *)p.ws);
+    else k_parts<<<grid, 256, 0, stream>>>((const uint16_t *)p.x, p.ldx, p.rows, p.k, (uint16_t *)p.ws);
+    x = {(const uint16_t *)p.ws, p.k};
+  }
+  const int yb = p.y_dtype == 1;
+  const int64_t each = (p.rows + p.experts - 1) / p.experts;      // rows of a group, on average
+  if (f32) {
+    if (each <= 48) return grouped<MX, 3, 4, 2, 1>(w, g, x, part, p.y, yb, p.ldy, p.fill, stream);
+    return grouped<MX, 3, 4, 2, 2>(w, g, x, part, p.y, yb, p.ldy, p.fill, stream);
+  }
+  if (each <= 48) return grouped<MX, 1, 4, 2, 1>(w, g, x, part, p.y, yb, p.ldy, p.fill, stream);
+  if (each <= 128) return grouped<MX, 1, 4, 2, 2>(w, g, x, part, p.y, yb, p.ldy, p.fill, stream);
+  return grouped<MX, 1, 8, 2, 4>(w, g, x, part, p.y, yb, p.ldy, p.fill, stream);
 }
 
 // ------------------------------------------------------ weight gradient --
@@ -919,23 +775,22 @@ hipError_t launch_grouped_wgrad(const GroupedWgrad &p, hipStream_t stream) {
   return run((const float *)p.dy, (const float *)p.x);
 }
 
-int64_t grouped_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t rows, bool f32) { return 0; }
+int64_t grouped_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t rows, bool f32) {
+  if (n == 0 || rows == 0 || k == 0) return 0;
+  if (grouped_by_tiles(experts, k, rows)) return grouped_tiles_workspace_bytes(experts, n, k, rows, f32);
+  // (a bf16 x may lie at any place: room for a copy)
+  return rows * k * (f32 ? 6 : 2);
+}
 
 hipError_t launch_grouped(const GroupedProduct &p, hipStream_t stream) {
   if (p.n == 0 || p.rows == 0) return hipSuccess;
   const int64_t block = p.mx ? 32 : 16, rows = p.transposed ? 1 : p.n;
   const int64_t pitch = p.transposed ? p.experts * p.k : p.k, step = rows * p.k;
   const Stack w = {p.codes, p.scales, p.meta, p.n, p.k, pitch / 2, step / 2, pitch / block, step / block};
+  if (grouped_by_tiles(p.experts, p.k, p.rows))
+    return launch_grouped_tiles(p, w.code_pitch, w.code_step, w.scale_pitch, w.scale_step, stream);
   const Groups g = {p.offsets, p.index_bits == 64, (int)p.experts, p.rows, 0};
-  const int yb = p.y_dtype == 1;
-  if (p.x_dtype == 1) {
-    const Rows<uint16_t> x = {(const uint16_t *)p.x, p.ldx};
-    return p.mx ? grouped_x<true>(w, g, x, p.y, yb, p.ldy, p.fill, stream)
-                : grouped_x<false>(w, g, x, p.y, yb, p.ldy, p.fill, stream);
-  }
-  const Rows<float> x = {(const float *)p.x, p.ldx};
-  return p.mx ? grouped_x<true>(w, g, x, p.y, yb, p.ldy, p.fill, stream)
-              : grouped_x<false>(w, g, x, p.y, yb, p.ldy, p.fill, stream);
+  return p.mx ? grouped_tiles<true>(p, w, g, stream) : grouped_tiles<false>(p, w, g, stream);
 }
 
 }  // namespace nvfp4

@@ -40,6 +40,7 @@
 // (6.5 TB/s) and 59.1; 8 bf16 tokens 20480 x 5120 17.3; f32, NVFP4, 16 tokens
 // 20480 x 5120 (three slabs) 29.6, 8 tokens 131075 x 5120 (two slabs) 111.
 #include "gemm_common.h"
+#include "groups.h"
 #include "nvfp4_device.h"
 #include "nvfp4_kernels.h"
 #include "operands.h"
@@ -133,11 +134,32 @@ template <typename X> constexpr int columns() { return sizeof(X) == 2 ? 1 : 3; }
 // and an extra wave adds and stores them meanwhile.  With more than
 // one range of K (gridDim.z) the sums go to `partial` [z][token][n] instead.
 // SL: 16-column slabs; grid: (tile walkers, tokens / 16, ranges of K).
-template <bool MX, typename X, int SL, int SW, bool HELPER>
+//
+// With groups (of tokens, each with weights of its own) the grid's y counts the
+// groups' tiles of up to as many tokens as the slabs hold.
+struct OneWeight {};
+struct Experts {
+  Groups g;
+  int64_t code_pitch, code_step, scale_pitch, scale_step;      // bytes from row to row, from expert to expert
+  int fill;                                                    // zeros in the rows of no group
+};
+// Zeros in the rows of y that no group has, by all of the grid's workgroups.
+__device__ void zero_other_rows(const Groups &g, void *y, int y_bf16, int64_t ldy, int64_t N, int64_t block,
+                                int64_t blocks) {
+  const int64_t first = g.at(0), last = max(g.at(g.count), first), rest = first + g.rows - last;
+  for (int64_t i = block; i < rest; i += blocks)
+    for (int64_t n = threadIdx.x; n < N; n += blockDim.x) store_y(y, y_bf16, (i < first ? i : last + i - first) * ldy + n, 0.0f);
+}
+// Tokens that the slabs' columns hold.
+template <typename X> constexpr int slab_tokens(int slabs) { return sizeof(X) == 2 ? 16 : 16 * slabs / 3; }
+
+template <bool MX, typename X, int SL, int SW, bool HELPER, typename G>
 __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *codes, const uint8_t *scales,
                                                                  const float *meta, int64_t N, int64_t K, const X *x,
                                                                  int64_t tokens, int64_t ldx, void *y, int y_bf16,
-                                                                 int64_t ldy, float *partial, int waves, int long_walk) {
+                                                                 int64_t ldy, float *partial, int waves, int long_walk,
+                                                                 G groups) {
+  constexpr bool kGrouped = std::is_same<G, Experts>::value;
   constexpr int kC = columns<X>();
   constexpr int kG = Scale<MX>::kPerByte;
   constexpr int kSB = SW * kStepK / kG;              // scale bytes of a slice's row
@@ -145,8 +167,23 @@ __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *
   extern __shared__ __align__(16) char lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, quarter = lane >> 4;
-  const int64_t t0 = (int64_t)blockIdx.y * kTokens;
-  const int live = (int)min(tokens - t0, (int64_t)kTokens);
+  int64_t t0 = (int64_t)blockIdx.y * kTokens;
+  int live = (int)min(tokens - t0, (int64_t)kTokens);
+  int64_t code_pitch = K / 2, scale_pitch = K / kG;
+  if constexpr (kGrouped) {
+    if (groups.fill && !partial)
+      zero_other_rows(groups.g, y, y_bf16, ldy, N, blockIdx.y * (int64_t)gridDim.x + blockIdx.x,
+                      (int64_t)gridDim.y * gridDim.x);
+    constexpr int kMost = slab_tokens<X>(SL);
+    const GroupTile tile = find_tile(groups.g, kMost, 1, blockIdx.y);
+    if (tile.e < 0) return;
+    t0 = tile.begin + (int64_t)tile.local * kMost;
+    live = (int)min(tile.end - t0, (int64_t)kMost);
+    codes += tile.e * groups.code_step;
+    scales += tile.e * groups.scale_step;
+    code_pitch = groups.code_pitch;
+    scale_pitch = groups.scale_pitch;
+  }
   // a range's own k begin at `own`; one that would have only 16 of them (half a
   // lane's load, NVFP4) starts 16 before, and meets zeros there
   const int64_t own = (int64_t)blockIdx.z * waves * (SW * kStepK), kz = MX ? own : min(own, K - 32);
@@ -204,10 +241,12 @@ __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *
   const auto load_codes = [&](u32x4_t *c, int64_t tile) {
     const int64_t n0 = min(tile, tiles - 1) * 16;
     const uint32_t rows = tile < tiles ? (uint32_t)min(N - n0, (int64_t)16) : 0u;
-    const __amdgpu_buffer_rsrc_t view = make_rsrc(codes + n0 * (K / 2), rows * (uint32_t)(K / 2));
+    const __amdgpu_buffer_rsrc_t view =
+        make_rsrc(codes + n0 * code_pitch, kGrouped ? rows ? (rows - 1) * (uint32_t)code_pitch + (uint32_t)(K / 2) : 0u
+                                                    : rows * (uint32_t)(K / 2));
 #pragma unroll
     for (int s = 0; s < SW; ++s)
-      c[s] = __builtin_amdgcn_raw_buffer_load_b128(view, (uint32_t)row * (uint32_t)(K / 2) + k[s] / 2, 0, 0);
+      c[s] = __builtin_amdgcn_raw_buffer_load_b128(view, (uint32_t)row * (uint32_t)code_pitch + k[s] / 2, 0, 0);
   };
   // scales: piece `sp` of row `sr` of the tile's runs of waves * kSB bytes;
   // a piece that passes the row's end is fetched from before it and shifted
@@ -222,7 +261,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void k_matvec_tile(const uint8_t *
     const int64_t n0 = tile * 16;
     const uint32_t r = min((uint32_t)sr, (uint32_t)min(N - 1 - n0, (int64_t)15));
     uint64_t v = 0;
-    const uint8_t *p = scales + n0 * row_bytes + (r * (uint32_t)row_bytes + sfrom);
+    const uint8_t *p = scales + n0 * scale_pitch + (r * (uint32_t)scale_pitch + sfrom);
     __builtin_memcpy(&v, p, kPiece);
     return v;
   };
@@ -485,6 +524,22 @@ __global__ __launch_bounds__(256) void k_matvec_join(const float *partial, int r
   }
 }
 
+// The same for the rows of groups; those of none become zeros or stay.
+__global__ __launch_bounds__(256) void k_grouped_join(const float *partial, int ranges, const float *meta, int64_t N,
+                                                      int64_t tokens, void *y, int y_bf16, int64_t ldy, Experts groups) {
+  const float g = meta ? meta[1] : 1.0f;
+  const int64_t first = groups.g.at(0), last = groups.g.at(groups.g.count);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < N * tokens; i += (int64_t)gridDim.x * 256) {
+    const int64_t t = i / N;
+    const bool own = t >= first && t < last;
+    if (!own && !groups.fill) continue;
+    float sum = 0.0f;
+    if (own)
+      for (int z = 0; z < ranges; ++z) sum += partial[z * tokens * N + i];
+    store_y(y, y_bf16, t * ldy + i % N, own ? sum * g : 0.0f);
+  }
+}
+
 // K below 128, where a row has less than a step's codes: one thread an output.
 constexpr int64_t kShortK = 128;
 template <bool MX, typename X>
@@ -710,9 +765,8 @@ k_matvec_row(const uint8_t *codes, const uint8_t *scales, const float *meta, int
 struct Cut {
   int sl, sw, waves, ranges, walkers, long_walk;
 };
-Cut cut_for(int64_t N, int64_t K, int64_t tokens, bool f32) {
+Cut cut_of(int64_t N, int64_t K, int cols, int64_t blocks) {
   Cut c;
-  const int cols = (int)std::min<int64_t>(tokens, kTokens) * (f32 ? 3 : 1);
   c.sl = (cols + 15) / 16;
   c.sw = c.sl == 1 ? 4 : 2;
   const int64_t slices = (K + c.sw * kStepK - 1) / (c.sw * kStepK);
@@ -720,7 +774,7 @@ Cut cut_for(int64_t N, int64_t K, int64_t tokens, bool f32) {
   c.ranges = (int)((slices + most - 1) / most);
   c.waves = (int)((slices + c.ranges - 1) / c.ranges);       // (the last range has a slice at least: waves <= most)
   // one round of workgroups: as many as fit the CUs' waves, the tiles dealt evenly
-  const int64_t tiles = (N + 15) / 16, blocks = (tokens + kTokens - 1) / kTokens;
+  const int64_t tiles = (N + 15) / 16;
   const int64_t room = (int64_t)device_cus() * (kTileWaves / (c.waves + has_helper(c.waves, c.sl)));
   const int64_t want = std::min(tiles, std::max<int64_t>(1, room / (c.ranges * blocks)));
   const int64_t per = (tiles + want - 1) / want;
@@ -729,6 +783,9 @@ Cut cut_for(int64_t N, int64_t K, int64_t tokens, bool f32) {
   // fifth less a tile: 131075 x 5120 90 -> 77 us, 20480 x 5120 18.4 -> 19.7)
   c.long_walk = per >= 8;
   return c;
+}
+Cut cut_for(int64_t N, int64_t K, int64_t tokens, bool f32) {
+  return cut_of(N, K, (int)std::min<int64_t>(tokens, kTokens) * (f32 ? 3 : 1), (tokens + kTokens - 1) / kTokens);
 }
 
 // What every launch of a product passes on.
@@ -745,18 +802,25 @@ template <typename X> struct Product {
   hipStream_t stream;
 };
 
-template <bool MX, int SL, int SW, typename X> void tile(const Cut &c, const Product<X> &p) {
-  const dim3 grid((unsigned)c.walkers, (unsigned)((p.tokens + kTokens - 1) / kTokens), (unsigned)c.ranges);
+template <bool MX, int SL, int SW, typename X, typename G>
+void tile(const Cut &c, const Product<X> &p, int64_t blocks, const G &groups) {
+  const dim3 grid((unsigned)c.walkers, (unsigned)blocks, (unsigned)c.ranges);
   const size_t run = c.waves * SW * kStepK / Scale<MX>::kPerByte;       // scale bytes of a row
   const size_t lds =
       std::max<size_t>(c.waves * SL * kTurnBytes, 2 * max_waves(SL) * SL * 64 * sizeof(f32x4_t) + 32 * (run + 4));
   float *partial = c.ranges > 1 ? (float *)p.ws : nullptr;
   const auto launch = [&](auto kernel, int waves) {
     kernel<<<grid, 64 * waves, lds, p.stream>>>(p.codes, p.scales, p.meta, p.N, p.K, p.x, p.tokens, p.ldx, p.y, p.y_bf16,
-                                                p.ldy, partial, c.waves, c.long_walk);
+                                                p.ldy, partial, c.waves, c.long_walk, groups);
   };
-  if (has_helper(c.waves, SL)) launch(k_matvec_tile<MX, X, SL, SW, true>, c.waves + 1);
-  else if constexpr (SL == 1) launch(k_matvec_tile<MX, X, SL, SW, false>, c.waves);
+  if (has_helper(c.waves, SL)) launch(k_matvec_tile<MX, X, SL, SW, true, G>, c.waves + 1);
+  else if constexpr (SL == 1) launch(k_matvec_tile<MX, X, SL, SW, false, G>, c.waves);
+  if constexpr (std::is_same<G, Experts>::value) {
+    if (partial)
+      k_grouped_join<<<(unsigned)std::min(kFlatGrid, (p.N * p.tokens + 255) / 256), 256, 0, p.stream>>>(
+          partial, c.ranges, MX ? nullptr : p.meta, p.N, p.tokens, p.y, p.y_bf16, p.ldy, groups);
+    return;
+  }
   if (partial)
     k_matvec_join<<<(unsigned)std::min(kFlatGrid, (p.N * p.tokens + 255) / 256), 256, 0, p.stream>>>(
         partial, c.ranges, MX ? nullptr : p.meta, p.N, p.tokens, p.y, p.y_bf16, p.ldy);
@@ -822,12 +886,63 @@ template <bool MX, typename X> void matvec(const Product<X> &p) {
                                                      p.y_bf16, p.ldy);
   } else {
     const Cut c = cut_for(p.N, p.K, p.tokens, sizeof(X) == 4);
-    if (c.sl == 1) tile<MX, 1, 4>(c, p);
-    else if constexpr (sizeof(X) == 4) c.sl == 2 ? tile<MX, 2, 2>(c, p) : tile<MX, 3, 2>(c, p);
+    const int64_t blocks = (p.tokens + kTokens - 1) / kTokens;
+    if (c.sl == 1) tile<MX, 1, 4>(c, p, blocks, OneWeight());
+    else if constexpr (sizeof(X) == 4)
+      c.sl == 2 ? tile<MX, 2, 2>(c, p, blocks, OneWeight()) : tile<MX, 3, 2>(c, p, blocks, OneWeight());
   }
 }
 
+// Groups of few rows: the tiles of 16 weight rows, one walk over an expert's
+// for up to as many tokens as the slabs hold (float32: 5, 10 or 16, by the
+// groups' average).
+struct GroupedCut {
+  Cut cut;
+  int64_t blocks;
+};
+GroupedCut grouped_cut(int64_t experts, int64_t N, int64_t K, int64_t rows, bool f32) {
+  const int64_t groups = std::min(experts, rows), each = (rows + groups - 1) / groups;
+  const int most = !f32 ? 16 : each <= 3 ? 5 : each <= 8 ? 10 : 16;
+  GroupedCut c;
+  c.blocks = rows / (f32 ? 16 * ((3 * most + 15) / 16) / 3 : 16) + groups;
+  c.cut = cut_of(N, K, f32 ? 3 * most : 16, c.blocks);
+  return c;
+}
+
 }  // namespace
+
+// Whether a grouped product goes by the tiles for few tokens.
+bool grouped_by_tiles(int64_t experts, int64_t K, int64_t rows) {
+  const int64_t groups = std::min(experts, rows);
+  return K >= kShortK && rows <= 24 * groups && rows / 5 + groups <= 65535;
+}
+int64_t grouped_tiles_workspace_bytes(int64_t experts, int64_t N, int64_t K, int64_t rows, bool f32) {
+  const GroupedCut c = grouped_cut(experts, N, K, rows, f32);
+  return c.cut.ranges > 1 ? 4 * c.cut.ranges * rows * N : 0;
+}
+hipError_t launch_grouped_tiles(const GroupedProduct &g, int64_t code_pitch, int64_t code_step, int64_t scale_pitch,
+                                int64_t scale_step, hipStream_t stream) {
+  const Experts experts = {{g.offsets, g.index_bits == 64, (int)g.experts, g.rows, 0}, code_pitch, code_step,
+                           scale_pitch, scale_step, g.fill};
+  const GroupedCut c = grouped_cut(g.experts, g.n, g.k, g.rows, g.x_dtype == 0);
+  const auto run = [&](auto *xt, auto mx) {
+    using X = std::remove_const_t<std::remove_pointer_t<decltype(xt)>>;
+    constexpr bool MX = decltype(mx)::value;
+    const Product<X> p = {g.codes, g.scales, g.meta, g.n, g.k, xt, g.rows, g.ldx, g.y, g.y_dtype == 1, g.ldy, g.ws, stream};
+    if constexpr (sizeof(X) == 2) {
+      tile<MX, 1, 4>(c.cut, p, c.blocks, experts);
+    } else {
+      if (c.cut.sl == 1) tile<MX, 1, 4>(c.cut, p, c.blocks, experts);
+      else if (c.cut.sl == 2) tile<MX, 2, 2>(c.cut, p, c.blocks, experts);
+      else tile<MX, 3, 2>(c.cut, p, c.blocks, experts);
+    }
+  };
+  with_flag(g.mx, [&](auto mx) {
+    if (g.x_dtype == 1) run((const uint16_t *)g.x, mx);
+    else run((const float *)g.x, mx);
+  });
+  return hipGetLastError();
+}
 
 int64_t matvec_workspace_bytes(int64_t N, int64_t K, int64_t tokens, bool f32) {
   if (N <= 0 || tokens <= 0 || K < kShortK || by_rows(N, K, tokens, f32)) return 0;

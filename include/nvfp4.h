@@ -536,9 +536,10 @@ int64_t nvfp4_matvec_workspace_bytes(int64_t n, int64_t k, int64_t tokens, int x
  *            1: they become zeros.
  *  workspace : device, at least nvfp4_grouped_matmul_workspace_bytes(experts,
  *            N, K, rows, x_dtype) bytes (for both formats), 16-byte aligned,
- *            contents ignored and overwritten; often 0, and NULL will do then.
+ *            contents ignored and overwritten; may be 0, and NULL will do then.
  *            Calls that share one must not overlap in time.
- *  ceil(N / 128) * (rows / 32 + min(experts, rows)) <= 2^24 - 8, K <= 2^25 - 16.
+ *  ceil(N / 128) * (rows / 32 + min(experts, rows)) <= 2^24 - 8, K <= 2^25 - 16,
+ *  w's k <= 2^28 - 32.
  * A group without rows costs nothing, and its weights are not read.  Weights
  * and bf16 x enter the product exactly; a float32 x to within 2^-133 of its
  * value.  Sums are binary32.  K == 0 gives zeros.  An MXFP4 scale of 255 is
