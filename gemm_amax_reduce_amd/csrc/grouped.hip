@@ -398,14 +398,34 @@ hipError_t grouped_tiles(const GroupedProduct &p, const Stack &w, const Groups &
     x = {(const uint16_t *)p.ws, p.k};
   }
   const int yb = p.y_dtype == 1;
-  const int64_t each = (p.rows + p.experts - 1) / p.experts;      // rows of a group, on average
+  const int64_t groups = std::min(p.experts, p.rows), each = (p.rows + groups - 1) / groups;
   if (f32) {
-    if (each <= 48) return grouped<MX, 3, 4, 2, 1>(w, g, x, part, p.y, yb, p.ldy, p.fill, stream);
+    // tiles of 512 x 32 against 256 x 64, us, 24 groups of 5120 x 1280: 64 rows
+    // each 86 / 80, as many on average with few groups alike 113 / 128, 256 each
+    // 315 / 288
+    if (each <= 96) return grouped<MX, 3, 8, 2, 1>(w, g, x, part, p.y, yb, p.ldy, p.fill, stream);
     return grouped<MX, 3, 4, 2, 2>(w, g, x, part, p.y, yb, p.ldy, p.fill, stream);
   }
-  if (each <= 48) return grouped<MX, 1, 4, 2, 1>(w, g, x, part, p.y, yb, p.ldy, p.fill, stream);
-  if (each <= 128) return grouped<MX, 1, 4, 2, 2>(w, g, x, part, p.y, yb, p.ldy, p.fill, stream);
-  return grouped<MX, 1, 8, 2, 4>(w, g, x, part, p.y, yb, p.ldy, p.fill, stream);
+  // tiles of 512 x 128 where groups fill them and there are some for most CUs,
+  // else of 256 x 64; us, 16 groups of 4096 x 4096 of unlike sizes, 64 rows on
+  // average 98 / 81, 96 97 / 122, 128 104 / 125, 512 308 / 339
+  const int64_t large = (w.N + 511) / 512 * (p.rows / 128 + groups / 2);
+  if (each > 80 && 8 * large >= 5 * device_cus())
+    return grouped<MX, 1, 8, 2, 4>(w, g, x, part, p.y, yb, p.ldy, p.fill, stream);
+  return grouped<MX, 1, 4, 2, 2>(w, g, x, part, p.y, yb, p.ldy, p.fill, stream);
+}
+
+// Whether a product goes by the matvec's tiles, which read the weights once for
+// every 16 rows of a group, at some 6 TB/s from whichever memory holds them,
+// behind a start of 6 us; the tiles here take some 1.5 us a stage of 128 k for
+// every two a CU.  us, 16 groups of 4096 x 4096, 4 rows each on average 38 /
+// 54, 16 50 / 56, 32 71 / 80, 64 110 / 81.
+bool by_matvec_tiles(int64_t experts, int64_t n, int64_t k, int64_t rows) {
+  if (!grouped_tiles_fit(experts, k, rows)) return false;
+  const int64_t groups = std::min(experts, rows);
+  const double reads = (double)(rows / 16 + groups) * n * k * 0.53 / 6.0e6;
+  const double rounds = std::max(1.0, (double)((n + 255) / 256) * (rows / 64 + groups / 2) / (2 * device_cus()));
+  return reads < rounds * 1.5 * ((k + kStage - 1) / kStage);
 }
 
 // ------------------------------------------------------ weight gradient --
@@ -777,7 +797,7 @@ hipError_t launch_grouped_wgrad(const GroupedWgrad &p, hipStream_t stream) {
 
 int64_t grouped_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t rows, bool f32) {
   if (n == 0 || rows == 0 || k == 0) return 0;
-  if (grouped_by_tiles(experts, k, rows)) return grouped_tiles_workspace_bytes(experts, n, k, rows, f32);
+  if (by_matvec_tiles(experts, n, k, rows)) return grouped_tiles_workspace_bytes(experts, n, k, rows, f32);
   // (a bf16 x may lie at any place: room for a copy)
   return rows * k * (f32 ? 6 : 2);
 }
@@ -787,7 +807,7 @@ hipError_t launch_grouped(const GroupedProduct &p, hipStream_t stream) {
   const int64_t block = p.mx ? 32 : 16, rows = p.transposed ? 1 : p.n;
   const int64_t pitch = p.transposed ? p.experts * p.k : p.k, step = rows * p.k;
   const Stack w = {p.codes, p.scales, p.meta, p.n, p.k, pitch / 2, step / 2, pitch / block, step / block};
-  if (grouped_by_tiles(p.experts, p.k, p.rows))
+  if (by_matvec_tiles(p.experts, p.n, p.k, p.rows))
     return launch_grouped_tiles(p, w.code_pitch, w.code_step, w.scale_pitch, w.scale_step, stream);
   const Groups g = {p.offsets, p.index_bits == 64, (int)p.experts, p.rows, 0};
   return p.mx ? grouped_tiles<true>(p, w, g, stream) : grouped_tiles<false>(p, w, g, stream);

@@ -911,10 +911,10 @@ GroupedCut grouped_cut(int64_t experts, int64_t N, int64_t K, int64_t rows, bool
 
 }  // namespace
 
-// Whether a grouped product goes by the tiles for few tokens.
-bool grouped_by_tiles(int64_t experts, int64_t K, int64_t rows) {
-  const int64_t groups = std::min(experts, rows);
-  return K >= kShortK && rows <= 24 * groups && rows / 5 + groups <= 65535;
+// Whether the tiles can take a grouped product (a row holds a step's codes, the
+// grid's y the groups' tiles).
+bool grouped_tiles_fit(int64_t experts, int64_t K, int64_t rows) {
+  return K >= kShortK && rows / 5 + std::min(experts, rows) <= 65535;
 }
 int64_t grouped_tiles_workspace_bytes(int64_t experts, int64_t N, int64_t K, int64_t rows, bool f32) {
   const GroupedCut c = grouped_cut(experts, N, K, rows, f32);

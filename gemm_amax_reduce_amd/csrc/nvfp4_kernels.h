@@ -135,9 +135,9 @@ struct GroupedProduct {
 int64_t grouped_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t rows, bool f32);
 hipError_t launch_grouped(const GroupedProduct &p, hipStream_t stream);
 
-// The form for groups of few rows (which calls take it; pitches and steps in
-// bytes from row to row and from expert to expert).
-bool grouped_by_tiles(int64_t experts, int64_t k, int64_t rows);
+// The form for groups of few rows, where it fits (pitches and steps in bytes
+// from row to row and from expert to expert).
+bool grouped_tiles_fit(int64_t experts, int64_t k, int64_t rows);
 int64_t grouped_tiles_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t rows, bool f32);
 hipError_t launch_grouped_tiles(const GroupedProduct &p, int64_t code_pitch, int64_t code_step, int64_t scale_pitch,
                                 int64_t scale_step, hipStream_t stream);
