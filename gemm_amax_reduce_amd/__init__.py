@@ -57,7 +57,8 @@ EXPORTS = ("nvfp4_quantize", "nvfp4_rht_quantize", "nvfp4_amax", "nvfp4_quantize
            "nvfp4_rms_norm", "mxfp8_rms_norm", "nvfp4_rms_norm_backward", "nvfp4_rms_norm_backward_workspace_bytes",
            "nvfp4_matvec", "mxfp4_matvec",
            "nvfp4_matvec_workspace_bytes", "nvfp4_grouped_matmul", "mxfp4_grouped_matmul",
-           "nvfp4_grouped_matmul_workspace_bytes", "nvfp4_grouped_wgrad", "nvfp4_adapters", "nvfp4_adapters_backward",
+           "nvfp4_grouped_matmul_workspace_bytes", "nvfp4_grouped_wgrad", "nvfp4_grouped_wgrad_workspace_bytes",
+           "nvfp4_adapters", "nvfp4_adapters_backward",
            "nvfp4_adapters_backward_workspace_bytes", "nvfp4_distill_topk", "nvfp4_distill_topk_backward",
            "nvfp4_distill_topk_step", "nvfp4_distill_topk_workspace_bytes", "nvfp4_probe_mfma", "nvfp4_probe_philox", "nvfp4_status_string")
 
@@ -135,8 +136,10 @@ def lib() -> ctypes.CDLL:
         L.mxfp4_grouped_matmul.restype = ci
         L.nvfp4_grouped_matmul_workspace_bytes.argtypes = [i64, i64, i64, i64, ci]
         L.nvfp4_grouped_matmul_workspace_bytes.restype = i64
-        L.nvfp4_grouped_wgrad.argtypes = [vp, ci, i64, vp, ci, i64, i64, i64, i64, vp, ci, i64, vp, ci, vp]
+        L.nvfp4_grouped_wgrad.argtypes = [vp, ci, i64, vp, ci, i64, i64, i64, i64, vp, ci, i64, vp, ci, vp, i64, vp]
         L.nvfp4_grouped_wgrad.restype = ci
+        L.nvfp4_grouped_wgrad_workspace_bytes.argtypes = [i64, i64, i64, i64, ci, ci]
+        L.nvfp4_grouped_wgrad_workspace_bytes.restype = i64
         low = [vp, vp, ci, i64, i64, i64, vp, vp, vp, ci, i64]               # adapters, scale, segments
         L.nvfp4_adapters.argtypes = [vp, ci, i64, i64, i64] + low + [vp, ci, i64, vp, ci, i64, vp, vp]
         L.nvfp4_adapters.restype = ci
@@ -965,14 +968,19 @@ def nvfp4_grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor
     n = dy.shape[1]
     op, bits, experts = _group_args(offsets, dev)
     code = _out_code(grad_dtype)
+    need = lib().nvfp4_grouped_wgrad_workspace_bytes(experts, n, k, rows, _dtype_code(dy), _dtype_code(x))
+    if need < 0:
+        _check(need, "nvfp4_grouped_wgrad")
     with _on(dev, stream):
         if out is None:
             out = torch.empty((experts, n, k), dtype=grad_dtype, device=dev)
         elif not isinstance(out, torch.Tensor) or tuple(out.shape) != (experts, n, k):
             raise NVFP4Error(f"out must have shape ({experts}, {n}, {k})")
         dp = _vector(out, "out", grad_dtype, experts * n * k, dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         _check(lib().nvfp4_grouped_wgrad(dy.data_ptr(), _dtype_code(dy), lddy, x.data_ptr(), _dtype_code(x), ldx, rows, n,
-                                         k, op, bits, experts, dp, code, _current_handle(dev)), "nvfp4_grouped_wgrad")
+                                         k, op, bits, experts, dp, code, _ptr(ws), need, _current_handle(dev)),
+               "nvfp4_grouped_wgrad")
     return out
 
 

@@ -195,6 +195,11 @@ inline bool grouped_ok(int64_t experts, int64_t n, int64_t k, int64_t rows) {
   return experts >= 1 && experts <= kMaxGroups && k <= kMaxGemmK && n <= kMaxMatvecRows &&
          grid_ok((n + 127) / 128, rows / 32 + (experts < rows ? experts : rows));
 }
+inline bool wgrad_ok(int64_t experts, int64_t n, int64_t k, int64_t rows) {
+  return n >= 0 && k >= 0 && rows >= 0 && experts >= 1 && experts <= kMaxGroups && n <= kMaxGrid * 128 && k <= kMaxGrid * 128 &&
+         grid_ok((n + 127) / 128, (k + 127) / 128) && grid_ok((n + 127) / 128 * ((k + 127) / 128) + 7, experts) &&
+         count_ok(rows, n + 8) && count_ok(rows, k + 8);
+}
 // Do the bytes of two ranges meet?
 inline bool ranges_meet(const void *a, int64_t abytes, const void *b, int64_t bbytes) {
   return overlap(a, abytes, abytes, b, bbytes, bbytes, 1);
@@ -614,24 +619,33 @@ int mxfp4_grouped_matmul(const mxfp4_tensor *w, int transposed, const void *x, i
                         w->outer, w->k, workspace_bytes, hip_stream);
 }
 
+int64_t nvfp4_grouped_wgrad_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t rows, int dy_dtype,
+                                            int x_dtype) {
+  if (!dtype_ok(dy_dtype) || !dtype_ok(x_dtype)) return NVFP4_ERR_ENUM;
+  if (!wgrad_ok(experts, n, k, rows)) return NVFP4_ERR_SHAPE;
+  return nvfp4::grouped_wgrad_workspace_bytes(experts, n, k, rows, dy_dtype == NVFP4_F32, x_dtype == NVFP4_F32);
+}
+
 int nvfp4_grouped_wgrad(const void *dy, int dy_dtype, int64_t lddy, const void *x, int x_dtype, int64_t ldx,
                         int64_t rows, int64_t n, int64_t k, const void *offsets, int index_bits, int64_t experts,
-                        void *dw, int dw_dtype, void *hip_stream) {
+                        void *dw, int dw_dtype, void *workspace, int64_t workspace_bytes, void *hip_stream) {
   if (!dtype_ok(dy_dtype) || !dtype_ok(x_dtype) || !dtype_ok(dw_dtype) || (index_bits != 32 && index_bits != 64))
     return NVFP4_ERR_ENUM;
-  if (n < 0 || k < 0 || !matrix_ok(rows, n, lddy) || !matrix_ok(rows, k, ldx) || experts < 1 || experts > kMaxGroups ||
-      n > kMaxGrid * 128 || k > kMaxGrid * 128 || !grid_ok((n + 127) / 128, (k + 127) / 128) ||
-      !grid_ok((n + 127) / 128 * ((k + 127) / 128) + 7, experts))
-    return NVFP4_ERR_SHAPE;
+  if (!wgrad_ok(experts, n, k, rows) || !matrix_ok(rows, n, lddy) || !matrix_ok(rows, k, ldx)) return NVFP4_ERR_SHAPE;
   if (n > 0 && k > 0 && (!dw || !offsets || (rows > 0 && (!dy || !x)))) return NVFP4_ERR_NULL;
+  const int64_t need =
+      nvfp4::grouped_wgrad_workspace_bytes(experts, n, k, rows, dy_dtype == NVFP4_F32, x_dtype == NVFP4_F32);
+  if (workspace_bytes < need) return NVFP4_ERR_SHAPE;
+  if (need > 0 && !workspace) return NVFP4_ERR_NULL;
   const int64_t ds = dtype_size(dy_dtype), xs = dtype_size(x_dtype), ws = dtype_size(dw_dtype);
-  if (!aligned(dy, ds) || !aligned(x, xs) || !aligned(dw, ws) || !aligned(offsets, index_bits / 8))
+  if (!aligned(dy, ds) || !aligned(x, xs) || !aligned(dw, ws) || !aligned(offsets, index_bits / 8) ||
+      !aligned(workspace, 16))
     return NVFP4_ERR_ALIGN;
   if (ranges_meet(dy, span(rows, lddy, n, ds), dw, experts * n * k * ws) ||
       ranges_meet(x, span(rows, ldx, k, xs), dw, experts * n * k * ws))
     return NVFP4_ERR_SHAPE;
   return hip_status(nvfp4::launch_grouped_wgrad({experts, n, k, dy, dy_dtype, lddy, x, x_dtype, rows, ldx, offsets,
-                                                 index_bits, dw, dw_dtype},
+                                                 index_bits, dw, dw_dtype, workspace},
                                                 (hipStream_t)hip_stream));
 }
 

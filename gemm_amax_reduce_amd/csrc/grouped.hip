@@ -431,160 +431,49 @@ bool by_matvec_tiles(int64_t experts, int64_t n, int64_t k, int64_t rows) {
 // ------------------------------------------------------ weight gradient --
 
 // Tokens run along the reduction here, and lie down the columns of both
-// operands: a stage's rows go to LDS as they are, and the lanes fetch columns
-// with transposing reads (16 lanes take 4 rows of 16 columns, and each leaves
-// with 4 rows of its own column).  Rows of LDS are 64 bytes longer than their
-// columns, so that the 4 rows of two such neighbours fall on different banks.
-// Of the parts of two float32 operands the products from hi hi to mid mid are
-// taken; those left out are below 2^-25 of the whole.
-// Tiles of a group that an XCD takes: a run of an eighth of every group's, since
-// groups differ in length.  The grid has this for each XCD and group.
-__host__ __device__ __forceinline__ int wgrad_quota(int tiles) { return (tiles + kXcds - 1) / kXcds; }
+// operands: a stage's rows go to LDS as they are, by DMA, and the lanes fetch
+// columns with transposing reads (16 lanes take 4 rows of 16 columns, and each
+// leaves with 4 rows of its own column), those of the next 16 tokens between the
+// MFMAs of these.  Chunk c (32 bytes, 16 columns) of row t lies in place
+// c ^ (2 (t % 4)), so that the 4 rows of a transposing read's two neighbouring
+// chunks fall on different banks.  Of the parts of two float32 operands the
+// products from hi hi to mid mid are taken; those left out are below 2^-25 of
+// the whole.
+//
+// Two workgroups a CU, so that one multiplies while the other stores: tiles of
+// 128 columns of dy by 256 of x and stages of 32 tokens for bf16, 128 by 128
+// and 16 tokens for the parts of float32.
 
-// A workgroup's tile is 64 FN columns of dy (n) by 64 FK columns of x, two by
-// two waves; every group's tiles are written, zeros for a group without rows.
-template <typename D, typename X, int FN, int FK, int TOKENS>
-__global__ __launch_bounds__(kThreads) void k_grouped_wgrad(Groups g, Rows<D> dy, Rows<X> x, void *dw, int dw_bf16,
-                                                            int64_t N, int64_t K, int tiles_n, int tiles_k) {
-  constexpr int kDP = sizeof(D) == 2 ? 1 : 3, kXP = sizeof(X) == 2 ? 1 : 3;
-  constexpr int TN = 64 * FN, TK = 64 * FK;
-  constexpr int kRowD = TN * 2 + 64, kRowX = TK * 2 + 64;            // bytes of a row in LDS
-  constexpr int kPartD = TOKENS * kRowD, kPartX = TOKENS * kRowX;
-  constexpr int kBuffer = kDP * kPartD + kXP * kPartX;
-  constexpr int kDL = TOKENS * (TN / 8) / kThreads, kXL = TOKENS * (TK / 8) / kThreads;
-  __shared__ __align__(16) char lds[2 * kBuffer];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-
-  const int tiles = tiles_n * tiles_k, quota = wgrad_quota(tiles);
-  const int e = blockIdx.x / kXcds / quota, at = (int)(blockIdx.x % kXcds) * quota + (int)(blockIdx.x / kXcds) % quota;
-  if (at >= tiles) return;
-  const int per = 8 * tiles_k, first_n = at / per * 8, gsz = min(tiles_n - first_n, 8);
-  const int64_t n0 = (int64_t)(first_n + at % per % gsz) * TN, k0 = (int64_t)(at % per / gsz) * TK;
-  const int64_t begin = g.at(e), end = max(g.at(e + 1), begin);
-  const bool inside = n0 + TN <= N && k0 + TK <= K;
-  const int stages = (int)((end - begin + TOKENS - 1) / TOKENS);
-
-  Row8<D> dreg[kDL];
-  Row8<X> xreg[kXL];
-  const auto load = [&](int s) {
-    const int64_t t0 = begin + (int64_t)s * TOKENS;
-    if (inside && t0 + TOKENS <= end) {
-#pragma unroll
-      for (int i = 0; i < kDL; ++i) {
-        const int p = tid + i * kThreads;
-        dreg[i].load(dy.p + (t0 + p / (TN / 8)) * dy.ld + n0 + p % (TN / 8) * 8);
-      }
-#pragma unroll
-      for (int i = 0; i < kXL; ++i) {
-        const int p = tid + i * kThreads;
-        xreg[i].load(x.p + (t0 + p / (TK / 8)) * x.ld + k0 + p % (TK / 8) * 8);
-      }
+// Operands as the kernel copies them: rows of whole words.  Others are brought
+// to that first: [parts][rows][round8(cols)] in the workspace, zeros behind a
+// row's end.
+int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
+template <typename X>
+__global__ __launch_bounds__(256) void k_pad(const X *x, int64_t ldx, int64_t rows, int64_t cols, uint16_t *out) {
+  const int64_t pieces = (cols + 7) / 8, all = rows * pieces;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    Row8<X> q;
+    load_row8(q, x + i / pieces * ldx, i % pieces * 8, cols);
+    if constexpr (sizeof(X) == 2) {
+      *reinterpret_cast<u32x4_t *>(out + i * 8) = q.r;
     } else {
+      const Parts p = split8_nearest(q);
 #pragma unroll
-      for (int i = 0; i < kDL; ++i) {
-        const int p = tid + i * kThreads;
-        const int64_t row = t0 + p / (TN / 8);
-        load_row8(dreg[i], dy.p + row * dy.ld, n0 + p % (TN / 8) * 8, row < end ? N : 0);
-      }
-#pragma unroll
-      for (int i = 0; i < kXL; ++i) {
-        const int p = tid + i * kThreads;
-        const int64_t row = t0 + p / (TK / 8);
-        load_row8(xreg[i], x.p + row * x.ld, k0 + p % (TK / 8) * 8, row < end ? K : 0);
-      }
-    }
-  };
-  const auto put_one = [&](char *to, int part, const auto &q) {
-    if constexpr (sizeof(q) == 16) {
-      *reinterpret_cast<u32x4_t *>(to) = q.r;
-    } else {
-      const Parts v = split8_nearest(q);
-#pragma unroll
-      for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x4_t *>(to + p * part) = v.v[p];
-    }
-  };
-  const auto put = [&](int s) {
-    char *const buf = lds + (s & 1) * kBuffer;
-#pragma unroll
-    for (int i = 0; i < kDL; ++i) {
-      const int p = tid + i * kThreads;
-      put_one(buf + p / (TN / 8) * kRowD + p % (TN / 8) * 16, kPartD, dreg[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kXL; ++i) {
-      const int p = tid + i * kThreads;
-      put_one(buf + kDP * kPartD + p / (TK / 8) * kRowX + p % (TK / 8) * 16, kPartX, xreg[i]);
-    }
-  };
-
-  float16_t acc[FN][FK];
-#pragma unroll
-  for (int f = 0; f < FN; ++f)
-#pragma unroll
-    for (int q = 0; q < FK; ++q)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[f][q][i] = 0.0f;
-  // a lane's 8 rows (8 h .. 8 h + 7 of an MFMA's 16) of its column of a
-  // fragment of 32, by two reads; it names 4 columns of one row
-  const int col = 16 * ((lane >> 4) & 1) + 4 * (lane & 3), trow = 8 * (lane >> 5) + ((lane >> 2) & 3);
-  const auto products = [&](int s) {
-    const char *const dbuf = lds + (s & 1) * kBuffer + trow * kRowD + ((wave >> 1) * (32 * FN) + col) * 2;
-    const char *const xbuf = lds + (s & 1) * kBuffer + kDP * kPartD + trow * kRowX + ((wave & 1) * (32 * FK) + col) * 2;
-#pragma unroll
-    for (int ks = 0; ks < TOKENS / 16; ++ks) {
-      bf16x8_t a[kDP][FN], b[kXP][FK];
-#pragma unroll
-      for (int p = 0; p < kDP; ++p)
-#pragma unroll
-        for (int f = 0; f < FN; ++f) a[p][f] = lds_column(dbuf + p * kPartD + ks * 16 * kRowD + f * 64, kRowD);
-#pragma unroll
-      for (int p = 0; p < kXP; ++p)
-#pragma unroll
-        for (int f = 0; f < FK; ++f) b[p][f] = lds_column(xbuf + p * kPartX + ks * 16 * kRowX + f * 64, kRowX);
-#pragma unroll
-      for (int p = 0; p < kDP; ++p)
-#pragma unroll
-        for (int q = 0; q < kXP; ++q) {
-          if (p + q > 2) continue;
-#pragma unroll
-          for (int f = 0; f < FN; ++f)
-#pragma unroll
-            for (int k = 0; k < FK; ++k)
-              acc[f][k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[p][f], b[q][k], acc[f][k], 0, 0, 0);
-        }
-    }
-  };
-
-  if (stages > 0) {
-    load(0);
-    put(0);
-    if (stages > 1) load(1);
-    __syncthreads();
-    for (int s = 0; s < stages; ++s) {
-      products(s);
-      if (s + 1 < stages) put(s + 1);
-      if (s + 2 < stages) load(s + 2);
-      __syncthreads();
+      for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x4_t *>(out + (k * all + i) * 8) = p.v[k];
     }
   }
-
-  // register i of a fragment is row 8 (i / 4) + 4 h + i % 4, the lane its column
-  const int64_t base = (int64_t)e * N;
-#pragma unroll
-  for (int f = 0; f < FN; ++f)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int64_t n = n0 + (wave >> 1) * (32 * FN) + 32 * f + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
-      if (n >= N) continue;
-#pragma unroll
-      for (int q = 0; q < FK; ++q) {
-        const int64_t k = k0 + (wave & 1) * (32 * FK) + 32 * q + (lane & 31);
-        if (k >= K) continue;
-        if (dw_bf16) ((uint16_t *)dw)[(base + n) * K + k] = (uint16_t)pack_bf16(acc[f][q][i], 0.0f);
-        else ((float *)dw)[(base + n) * K + k] = acc[f][q][i];
-      }
-    }
 }
+
+// A matrix as the kernel copies it, with an even number of columns; its parts
+// lie `part` elements apart.
+struct Operand16 {
+  const uint16_t *p;
+  int64_t ld, cols, part;
+};
+
+// The tiles of a group that an XCD takes: a run of an eighth of every group's,
+// since groups differ in length.  The grid has this for each XCD and group.
+__host__ __device__ __forceinline__ int wgrad_quota(int tiles) { return (tiles + kXcds - 1) / kXcds; }
 
 // The 4 x 4 transpose over the lanes of a quad and four registers: lane j is
 // left with the j-th register of each of them.
@@ -597,202 +486,302 @@ __device__ __forceinline__ f32x4_t quad_turn(float a, float b, float c, float d)
   const float af = dpp<0x4E>(a1), bf = dpp<0x4E>(b1), cf = dpp<0x4E>(c1), df = dpp<0x4E>(d1);
   return (f32x4_t){high ? cf : a1, high ? df : b1, high ? c1 : af, high ? d1 : bf};
 }
-// 4 neighbouring elements k .. k + 3 of a row of K.
-__device__ __forceinline__ void store4(void *out, int bf16, int64_t row, int64_t k, int64_t K, const f32x4_t &v) {
-  if (k + 4 <= K) {
+// N (2 or 4) neighbouring elements k .. of a row of K.
+template <int N>
+__device__ __forceinline__ void store_run(void *out, int bf16, int64_t row, int64_t k, int64_t K, const f32x4_t &v) {
+  if (N == 4 && k + 4 <= K) {
     if (bf16) *reinterpret_cast<u32x2_a2 *>((uint16_t *)out + row + k) = (u32x2_a2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
     else *reinterpret_cast<f32x4_a4 *>((float *)out + row + k) = v;
-  } else {
+    return;
+  }
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      if (k + i >= K) continue;
-      if (bf16) ((uint16_t *)out)[row + k + i] = (uint16_t)pack_bf16(v[i], 0.0f);
-      else ((float *)out)[row + k + i] = v[i];
-    }
+  for (int i = 0; i < N; ++i) {
+    if (k + i >= K) continue;
+    if (bf16) ((uint16_t *)out)[row + k + i] = (uint16_t)pack_bf16(v[i], 0.0f);
+    else ((float *)out)[row + k + i] = v[i];
   }
 }
 
-// bf16 operands of whole words: tiles of 128 columns of dy by 256 of x, two
-// workgroups a CU, so that one multiplies while the other stores; copied to
-// LDS by DMA two stages of 32 tokens ahead, the columns of the next 16 tokens
-// fetched between the MFMAs of these.  Chunk c (32 bytes, 16 columns) of row t
-// lies in place c ^ (2 (t % 4)), so that the 4 rows of a transposing read's
-// two neighbouring chunks fall on different banks.
-constexpr int kWgTokens = 32, kWgRing = 3, kWgRowD = 256, kWgRowX = 512;
-constexpr int kWgStageD = kWgTokens * kWgRowD, kWgStage = kWgStageD + kWgTokens * kWgRowX;
-constexpr int kWgCopies = kWgStage / 4096;         // DMA instructions a wave and stage
-// One of the two half stages of 16 tokens: `from` is where the operands of the
-// next one lie (the stage itself, or the one behind), `to` where this stage's
-// copies go, which is another place of the ring.  (Two pointers that do not
-// meet: a transposing read would else wait for every copy under way.)
-struct WgOperands {
-  bf16x8_t a[2][2], b[2][4];
-};
-struct WgCopy {
-  __amdgpu_buffer_rsrc_t dv, xv;
-  uint32_t dat, xat[2], dp, xp;              // lane offsets (x: of even and odd instructions), a row's bytes
-  int wave;
-  // copy i of 6 of a stage at `to`: 4 rows of dy, or 2 of x; a wave's are 8 rows
-  __device__ __forceinline__ void run(int i, uint8_t *to) const {
-    if (i < 2)
-      dma16(dv, to + (8 * wave + 4 * i) * kWgRowD, dat, (uint32_t)(8 * wave + 4 * i) * dp);
-    else
-      dma16(xv, to + kWgStageD + (8 * wave + 2 * (i - 2)) * kWgRowX, xat[i & 1], (uint32_t)(8 * wave + 2 * (i - 2)) * xp);
-  }
-};
-template <int P>
-__device__ __forceinline__ void wg_half(const char *__restrict__ from, uint8_t *__restrict__ to, float16_t (&acc)[2][4],
-                                        WgOperands &o, const uint32_t (&dat)[2], const uint32_t (&xat)[4],
-                                        const WgCopy &c) {
+// DP, XP: parts of dy and x; FK: fragments of 32 columns of x a wave (the tile
+// is two waves of 64 columns of dy by two of 32 FK of x).
+template <int DP, int XP, int FK, int TOKENS> struct Wgrad {
+  static constexpr int kTK = 64 * FK, kRing = 3;
+  static constexpr int kRowD = 256, kRowX = 2 * kTK;                  // bytes of a row in LDS
+  static constexpr int kPartD = TOKENS * kRowD, kPartX = TOKENS * kRowX;
+  static constexpr int kX = DP * kPartD, kStage = kX + XP * kPartX;
+  // DMA instructions (1 KB: 4 rows of 256 bytes, or 2 of 512) a wave: of a
+  // part, of a stage; a wave copies TOKENS / 4 rows
+  static constexpr int kID = kPartD / 4096, kIX = kPartX / 4096, kCopies = DP * kID + XP * kIX;
+  static constexpr int kPairs = DP * XP == 9 ? 6 : DP * XP;           // products of parts that count
+  static constexpr int kMfma = kPairs * 2 * FK, kReads = 2 * DP + FK * XP;
+
+  struct Operands {
+    bf16x8_t a[2][DP][2], b[2][XP][FK];
+  };
+  struct Copy {
+    __amdgpu_buffer_rsrc_t dv[DP], xv[XP];
+    uint32_t dat, xat[2], dp, xp;            // lane offsets (x: of even and odd instructions), a row's bytes
+    int wave;
+    // copy u of a stage at `to`
+    __device__ __forceinline__ void run(int u, uint8_t *to) const {
+      const int row = wave * (TOKENS / 4);
+      if (u < DP * kID) {
+        const int p = u / kID, r = row + 4 * (u % kID);
+        dma16(dv[p], to + p * kPartD + r * kRowD, dat, (uint32_t)r * dp);
+      } else {
+        const int p = (u - DP * kID) / kIX, i = (u - DP * kID) % kIX, r = row + 1024 / kRowX * i;
+        dma16(xv[p], to + kX + p * kPartX + r * kRowX, xat[i & 1], (uint32_t)r * xp);
+      }
+    }
+  };
+  // The MFMAs of 16 tokens, whose operands are set P: `from` is where those of
+  // the next 16 lie, `to` where copies go, which is another place of the ring.
+  // (Two pointers that do not meet: a transposing read would else wait for every
+  // copy under way.)
+  template <int P, bool COPY>
+  static __device__ __forceinline__ void step(const char *__restrict__ from, uint8_t *__restrict__ to,
+                                              float16_t (&acc)[2][FK], Operands &o, const uint32_t (&dat)[2],
+                                              const uint32_t (&xat)[FK], const Copy &c) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    __builtin_amdgcn_sched_barrier(0);
-    const int f = i / 4, q = (f & 1) ? 3 - i % 4 : i % 4;
-    acc[f][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.a[P][f], o.b[P][q], acc[f][q], 0, 0, 0);
-    __builtin_amdgcn_sched_barrier(0);
-    if (i < 2) o.a[P ^ 1][i] = lds_column(from + dat[i], kWgRowD);
-    else if (i < 6) o.b[P ^ 1][i - 2] = lds_column(from + xat[i - 2], kWgRowX);
-    if (P == 0 && i >= 2) c.run(i - 2, to);
+    for (int i = 0; i < kMfma; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      // pairs of parts (0 0) (0 1) (0 2) (1 0) (1 1) (2 0), as far as there are parts
+      const int pair = i / (2 * FK), u = i % (2 * FK), f = u / FK, q = (f & 1) ? FK - 1 - u % FK : u % FK;
+      const int p = XP == 1 ? pair : DP == 1 ? 0 : pair < 3 ? 0 : pair < 5 ? 1 : 2;
+      const int k = XP == 1 ? 0 : DP == 1 ? pair : pair < 3 ? pair : pair < 5 ? pair - 3 : 0;
+      acc[f][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.a[P][p][f], o.b[P][k][q], acc[f][q], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      // the reads in the first three quarters, the copies after the first two MFMAs
+      constexpr int kSlots = kMfma * 3 / 4;
+      if (i < kSlots) {
+#pragma unroll
+        for (int r = i * kReads / kSlots; r < (i + 1) * kReads / kSlots; ++r) {
+          if (r < 2 * DP) o.a[P ^ 1][r / 2][r % 2] = lds_column(from + r / 2 * kPartD + dat[r % 2], kRowD);
+          else o.b[P ^ 1][(r - 2 * DP) / FK][(r - 2 * DP) % FK] =
+                   lds_column(from + (r - 2 * DP) / FK * kPartX + xat[(r - 2 * DP) % FK], kRowX);
+        }
+      }
+      if (COPY && i >= 2) {
+#pragma unroll
+        for (int r = (i - 2) * kCopies / (kMfma - 2); r < (i - 1) * kCopies / (kMfma - 2); ++r) c.run(r, to);
+      }
+    }
   }
-}
-__global__ __launch_bounds__(kThreads, 2) void k_grouped_wgrad_dma(Groups g, Rows<uint16_t> dy, Rows<uint16_t> x, void *dw,
-                                                                   int dw_bf16, int64_t N, int64_t K, int tiles_n,
-                                                                   int tiles_k) {
-  __shared__ __align__(16) uint8_t lds[kWgRing * kWgStage];
+};
+
+// Every group's tiles are written, zeros for a group without rows; with several
+// shares of a group's tokens (gridDim.y) the sums go to partial[share] instead.
+template <int DP, int XP, int FK, int TOKENS>
+__global__ __launch_bounds__(kThreads, 2) void k_grouped_wgrad(Groups g, Operand16 dy, Operand16 x, void *dw, int dw_bf16,
+                                                               float *partial, int64_t N, int64_t K, int tiles_n,
+                                                               int tiles_k) {
+  using W = Wgrad<DP, XP, FK, TOKENS>;
+  __shared__ __align__(16) uint8_t lds[W::kRing * W::kStage];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tiles = tiles_n * tiles_k, quota = wgrad_quota(tiles);
   const int e = blockIdx.x / kXcds / quota, at = (int)(blockIdx.x % kXcds) * quota + (int)(blockIdx.x / kXcds) % quota;
   if (at >= tiles) return;
   const int per = 16 * tiles_k, first_n = at / per * 16, gsz = min(tiles_n - first_n, 16);
-  const int64_t n0 = (int64_t)(first_n + at % per % gsz) * 128, k0 = (int64_t)(at % per / gsz) * 256;
-  const int64_t begin = uniform64(g.at(e)), end = max(uniform64(g.at(e + 1)), begin);
-  const int stages = (int)((end - begin + kWgTokens - 1) / kWgTokens);
+  const int64_t n0 = (int64_t)(first_n + at % per % gsz) * 128, k0 = (int64_t)(at % per / gsz) * W::kTK;
+  int64_t begin = uniform64(g.at(e)), end = max(uniform64(g.at(e + 1)), begin);
+  if (gridDim.y > 1) {
+    // a share is a run of whole stages
+    const int64_t all = (end - begin + TOKENS - 1) / TOKENS, from = all * blockIdx.y / gridDim.y, to = all * (blockIdx.y + 1) / gridDim.y;
+    end = min(end, begin + to * TOKENS);
+    begin = min(begin + from * TOKENS, end);
+  }
+  const int stages = (int)((end - begin + TOKENS - 1) / TOKENS);
 
-  // an instruction copies 1 KB: 4 rows of dy, lane l slot l % 16 (16 bytes) of
-  // row l / 16, or 2 of x, slot l % 32 of row l / 32
-  WgCopy c;
+  typename W::Copy c;
   c.wave = wave;
   c.dp = (uint32_t)(dy.ld * 2);
   c.xp = (uint32_t)(x.ld * 2);
+  // lane l copies slot l % 16 (16 bytes) of row l / 16, or l % 32 of row l / 32
   c.dat = (uint32_t)(lane >> 4) * c.dp + 16 * (uint32_t)((lane & 15) ^ (4 * (lane >> 4)));
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    c.xat[i] = (uint32_t)(lane >> 5) * c.xp + 16 * (uint32_t)((lane & 31) ^ (4 * (2 * i + (lane >> 5))));
+    c.xat[i] = FK == 4 ? (uint32_t)(lane >> 5) * c.xp + 16 * (uint32_t)((lane & 31) ^ (4 * (2 * i + (lane >> 5))))
+                       : (uint32_t)(lane >> 4) * c.xp + 16 * (uint32_t)((lane & 15) ^ (4 * (lane >> 4)));
   const auto aim = [&](int s) {
-    const int64_t t0 = begin + (int64_t)s * kWgTokens, rows = min(end - t0, (int64_t)kWgTokens);
-    const auto view = [&](const Rows<uint16_t> &m, uint32_t pitch, int64_t c0, int64_t cols, int64_t most) {
-      return make_rsrc(m.p + (rows > 0 ? t0 * m.ld + c0 : 0),
-                       rows > 0 ? (uint32_t)(rows - 1) * pitch + (uint32_t)min(cols - c0, most) * 2 : 0u);
+    const int64_t t0 = begin + (int64_t)s * TOKENS, rows = min(end - t0, (int64_t)TOKENS);
+    const auto view = [&](const Operand16 &m, int p, uint32_t pitch, int64_t c0, int64_t most) {
+      return make_rsrc(m.p + (rows > 0 ? p * m.part + t0 * m.ld + c0 : 0),
+                       rows > 0 ? (uint32_t)(rows - 1) * pitch + (uint32_t)most * 2 : 0u);
     };
-    c.dv = view(dy, c.dp, n0, N, 128);
-    c.xv = view(x, c.xp, k0, K, 256);
+#pragma unroll
+    for (int p = 0; p < DP; ++p) c.dv[p] = view(dy, p, c.dp, n0, min(dy.cols - n0, (int64_t)128));
+#pragma unroll
+    for (int p = 0; p < XP; ++p) c.xv[p] = view(x, p, c.xp, k0, min(x.cols - k0, (int64_t)W::kTK));
   };
 
-  float16_t acc[2][4];
+  float16_t acc[2][FK];
 #pragma unroll
   for (int f = 0; f < 2; ++f)
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < FK; ++q)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[f][q][i] = 0.0f;
-  // the lane's 4 columns of one row of a transposing read, for each fragment
+  // the lane's 4 columns of one row of a transposing read, for each fragment, in
+  // the first 16 tokens of a stage and the second
   const int trow = 8 * (lane >> 5) + ((lane >> 2) & 3), turn = 2 * ((lane >> 2) & 3);
-  uint32_t dat[2], xat[4];
+  uint32_t dat[2][2], xat[2][FK];
 #pragma unroll
-  for (int f = 0; f < 4; ++f) {
-    const int chunk = 2 * f + ((lane >> 4) & 1);
-    if (f < 2) dat[f] = trow * kWgRowD + 32 * (((wave >> 1) * 4 + chunk) ^ turn) + 8 * (lane & 3);
-    xat[f] = kWgStageD + trow * kWgRowX + 32 * (((wave & 1) * 8 + chunk) ^ turn) + 8 * (lane & 3);
-  }
-  // (a half stage's operands lie 16 rows on, of both matrices)
-  uint32_t dat1[2], xat1[4];
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-  for (int f = 0; f < 4; ++f) {
-    if (f < 2) dat1[f] = dat[f] + 16 * kWgRowD;
-    xat1[f] = xat[f] + 16 * kWgRowX;
-  }
-  WgOperands o;
+    for (int f = 0; f < FK; ++f) {
+      const int chunk = 2 * f + ((lane >> 4) & 1);
+      if (f < 2) dat[h][f] = (trow + 16 * h) * W::kRowD + 32 * (((wave >> 1) * 4 + chunk) ^ turn) + 8 * (lane & 3);
+      xat[h][f] = W::kX + (trow + 16 * h) * W::kRowX + 32 * (((wave & 1) * 2 * FK + chunk) ^ turn) + 8 * (lane & 3);
+    }
+  typename W::Operands o;
   if (stages > 0) {
+    const auto place = [&](int turn_of) { return lds + turn_of * W::kStage; };
+    constexpr int kLead = TOKENS == 32 ? 2 : 3;          // stages copied before the first is used
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kLead; ++s) {
       aim(s);
 #pragma unroll
-      for (int i = 0; i < kWgCopies; ++i) c.run(i, lds + s * kWgStage);
+      for (int i = 0; i < W::kCopies; ++i) c.run(i, place(s));
     }
-    meet<(wait_vm(kWgCopies) & ~0x0F00)>();
+    constexpr int kStay = wait_vm((kLead - 1) * W::kCopies) & ~0x0F00;
+    meet<kStay>();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i < 2) o.a[0][i] = lds_column((const char *)lds + dat[i], kWgRowD);
-      o.b[0][i] = lds_column((const char *)lds + xat[i], kWgRowX);
-    }
-    int now = 0, next = kWgStage, free = 2 * kWgStage;           // places of this stage, the next, and the one behind it
-    for (int s = 0; s < stages; ++s) {
-      aim(s + 2);
-      wg_half<0>((const char *)lds + now, lds + free, acc, o, dat1, xat1, c);
-      // this wave's copies of the next stage (those of one more stay under way,
-      // which a fence would wait for) and its reads of this one
-      meet<(wait_vm(kWgCopies) & ~0x0F00)>();
-      wg_half<1>((const char *)lds + next, lds + free, acc, o, dat, xat, c);
+    for (int p = 0; p < DP; ++p)
+#pragma unroll
+      for (int f = 0; f < 2; ++f) o.a[0][p][f] = lds_column((const char *)lds + p * W::kPartD + dat[0][f], W::kRowD);
+#pragma unroll
+    for (int p = 0; p < XP; ++p)
+#pragma unroll
+      for (int f = 0; f < FK; ++f) o.b[0][p][f] = lds_column((const char *)lds + p * W::kPartX + xat[0][f], W::kRowX);
+    int now = 0, next = 1, last = 2;             // places of this stage, the next, and the one behind it
+    const auto move = [&]() {
       const int was = now;
       now = next;
-      next = free;
-      free = was;
+      next = last;
+      last = was;
+    };
+    if constexpr (TOKENS == 32) {
+      for (int s = 0; s < stages; ++s) {
+        aim(s + 2);
+        W::template step<0, true>((const char *)place(now), place(last), acc, o, dat[1], xat[1], c);
+        // this wave's copies of the next stage (those of one more stay under way,
+        // which a fence would wait for) and its reads of this one
+        meet<(wait_vm(W::kCopies) & ~0x0F00)>();
+        W::template step<1, false>((const char *)place(next), place(last), acc, o, dat[0], xat[0], c);
+        move();
+      }
+    } else {
+      // (the stage's own operands are in registers: its place takes the copies)
+      for (int s = 0; s < stages; s += 2) {
+        meet<(wait_vm(W::kCopies) & ~0x0F00)>();
+        aim(s + 3);
+        W::template step<0, true>((const char *)place(next), place(now), acc, o, dat[0], xat[0], c);
+        move();
+        if (s + 1 >= stages) break;
+        meet<(wait_vm(W::kCopies) & ~0x0F00)>();
+        aim(s + 4);
+        W::template step<1, true>((const char *)place(next), place(now), acc, o, dat[0], xat[0], c);
+        move();
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(wait_vm(0));        // nothing is left that writes LDS
   }
   // register i of a fragment is row 8 (i / 4) + 4 h + i % 4, the lane its
-  // column; turned over the quads a lane has 4 neighbours of fragment lane % 4
-  // (stores of 16 bytes a lane, whole lines: with 4 the wave's 128 of them held
-  // the copies of the CU's other workgroup up, 530 -> 480 us)
-  const int64_t base = (int64_t)e * N, k = k0 + (wave & 1) * 128 + 32 * (lane & 3) + (lane & 28);
+  // column; turned over the quads (pairs) a lane has neighbours of fragment
+  // lane % 4 (stores of 16 bytes a lane, whole lines: with 4 the wave's 128 of
+  // them held up the copies of the CU's other workgroup, 8192 rows of 8 experts
+  // 5120 x 5120 530 -> 490 us)
+  const bool split = gridDim.y > 1;
+  void *const out = split ? (void *)(partial + (int64_t)blockIdx.y * g.count * N * K) : dw;
+  const int bf16 = split ? 0 : dw_bf16;
+  const int64_t base = (int64_t)e * N;
 #pragma unroll
   for (int f = 0; f < 2; ++f)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int64_t n = n0 + (wave >> 1) * 64 + 32 * f + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
-      const f32x4_t v = quad_turn(acc[f][0][i], acc[f][1][i], acc[f][2][i], acc[f][3][i]);
-      if (n < N && k < K) store4(dw, dw_bf16, (base + n) * K, k, K, v);
+      if constexpr (FK == 4) {
+        const int64_t k = k0 + (wave & 1) * 128 + 32 * (lane & 3) + (lane & 28);
+        const f32x4_t v = quad_turn(acc[f][0][i], acc[f][1][i], acc[f][2][i], acc[f][3][i]);
+        if (n < N && k < K) store_run<4>(out, bf16, (base + n) * K, k, K, v);
+      } else {
+        // two fragments: rows n and n + 1 of the pair (i, i + 1) make the quad's four
+        if (i & 1) continue;
+        const f32x4_t v = quad_turn(acc[f][0][i], acc[f][1][i], acc[f][0][i + 1], acc[f][1][i + 1]);
+        const int64_t m = n + ((lane >> 1) & 1), k = k0 + (wave & 1) * 64 + 32 * (lane & 1) + (lane & 28);
+        if (m < N && k < K) store_run<4>(out, bf16, (base + m) * K, k, K, v);
+      }
     }
 }
 
-template <typename D, typename X>
-hipError_t wgrad(const Groups &g, const Rows<D> &dy, const Rows<X> &x, void *dw, int dw_bf16, int64_t N, int64_t K,
-                 hipStream_t stream) {
-  constexpr bool narrow = sizeof(D) + sizeof(X) == 4;
-  constexpr int F = narrow ? 4 : 2, kTokens = narrow ? 64 : 16;
-  const int64_t tn = (N + 64 * F - 1) / (64 * F), tk = (K + 64 * F - 1) / (64 * F);
-  const unsigned grid = (unsigned)(wgrad_quota((int)(tn * tk)) * kXcds * g.count);
-  if constexpr (narrow) {
-    const auto words = [](const Rows<uint16_t> &m, int64_t cols) {
-      return (uintptr_t)m.p % 4 == 0 && m.ld % 2 == 0 && cols % 2 == 0 && m.ld < (1LL << 24);
-    };
-    if (words(dy, N) && words(x, K)) {
-      const int64_t rows = (N + 127) / 128;
-      k_grouped_wgrad_dma<<<(unsigned)(wgrad_quota((int)(rows * tk)) * kXcds * g.count), kThreads, 0, stream>>>(
-          g, dy, x, dw, dw_bf16, N, K, (int)rows, (int)tk);
-      return hipGetLastError();
-    }
+// The shares' sums, in their order.
+__global__ __launch_bounds__(256) void k_wgrad_join(const float *partial, int shares, int64_t size, void *dw, int dw_bf16) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < size; i += (int64_t)gridDim.x * 256) {
+    float v = 0.0f;
+    for (int z = 0; z < shares; ++z) v += partial[z * size + i];
+    if (dw_bf16) ((uint16_t *)dw)[i] = (uint16_t)pack_bf16(v, 0.0f);
+    else ((float *)dw)[i] = v;
   }
-  k_grouped_wgrad<D, X, F, F, kTokens><<<grid, kThreads, 0, stream>>>(g, dy, x, dw, dw_bf16, N, K, (int)tn, (int)tk);
+}
+
+// Shares of the tokens: until there is work for two workgroups a CU, at least
+// 128 tokens of an average group each.
+int wgrad_shares(int64_t experts, int64_t n, int64_t k, int64_t rows, bool narrow) {
+  const int64_t tk = narrow ? 256 : 128, tiles = (n + 127) / 128 * ((k + tk - 1) / tk);
+  const int64_t groups = std::max<int64_t>(1, std::min(experts, rows));
+  const int64_t want = std::min(2 * (int64_t)device_cus() / (tiles * groups), rows / groups / 128);
+  return (int)std::min<int64_t>(std::max<int64_t>(want, 1), 64);
+}
+// Whether a matrix is copied from where it lies.
+bool words(const void *p, int64_t ld, int64_t cols, bool f32) {
+  return !f32 && (uintptr_t)p % 4 == 0 && ld % 2 == 0 && cols % 2 == 0 && ld < (1LL << 24);
+}
+
+template <int DP, int XP> hipError_t wgrad(const GroupedWgrad &p, hipStream_t stream) {
+  constexpr bool narrow = DP * XP == 1;
+  constexpr int FK = narrow ? 4 : 2, kTokens = narrow ? 32 : 16;
+  const int shares = wgrad_shares(p.experts, p.n, p.k, p.rows, narrow);
+  float *const partial = (float *)p.ws;
+  uint16_t *space = (uint16_t *)((char *)p.ws + (shares > 1 ? 4 * shares * p.experts * p.n * p.k : 0));
+  space += (8 - (uintptr_t)space / 2 % 8) % 8;
+  const auto ready = [&](const void *m, int64_t ld, int64_t cols, bool f32) {
+    if (p.rows == 0 || words(m, ld, cols, f32)) return Operand16{(const uint16_t *)m, ld, cols, 0};
+    const int64_t padded = round8(cols), pieces = p.rows * padded / 8;
+    const unsigned grid = (unsigned)std::min<int64_t>((pieces + 255) / 256, 1 << 14);
+    if (f32) k_pad<<<grid, 256, 0, stream>>>((const float *)m, ld, p.rows, cols, space);
+    else k_pad<<<grid, 256, 0, stream>>>((const uint16_t *)m, ld, p.rows, cols, space);
+    const Operand16 o = {space, padded, padded, p.rows * padded};
+    space += (f32 ? 3 : 1) * p.rows * padded;
+    return o;
+  };
+  const Operand16 dy = ready(p.dy, p.lddy, p.n, DP == 3), x = ready(p.x, p.ldx, p.k, XP == 3);
+  const Groups g = {p.offsets, p.index_bits == 64, (int)p.experts, p.rows, 0};
+  const int64_t tn = (p.n + 127) / 128, tk = (p.k + 64 * FK - 1) / (64 * FK);
+  const dim3 grid((unsigned)(wgrad_quota((int)(tn * tk)) * kXcds * p.experts), (unsigned)shares);
+  k_grouped_wgrad<DP, XP, FK, kTokens><<<grid, kThreads, 0, stream>>>(g, dy, x, p.dw, p.dw_dtype == 1, partial, p.n, p.k,
+                                                                     (int)tn, (int)tk);
+  if (shares > 1) {
+    const int64_t size = p.experts * p.n * p.k;
+    k_wgrad_join<<<(unsigned)std::min<int64_t>((size + 255) / 256, 1 << 14), 256, 0, stream>>>(partial, shares, size, p.dw,
+                                                                                             p.dw_dtype == 1);
+  }
   return hipGetLastError();
 }
 
 }  // namespace
 
+int64_t grouped_wgrad_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t rows, bool dy_f32, bool x_f32) {
+  if (n == 0 || k == 0) return 0;
+  const int shares = wgrad_shares(experts, n, k, rows, !dy_f32 && !x_f32);
+  // (a bf16 matrix may lie at any place: room for a copy)
+  return (shares > 1 ? 4 * shares * experts * n * k + 16 : 0) +
+         2 * rows * (round8(n) * (dy_f32 ? 3 : 1) + round8(k) * (x_f32 ? 3 : 1));
+}
 hipError_t launch_grouped_wgrad(const GroupedWgrad &p, hipStream_t stream) {
   if (p.n == 0 || p.k == 0) return hipSuccess;
-  const Groups g = {p.offsets, p.index_bits == 64, (int)p.experts, p.rows, 0};
-  const int b = p.dw_dtype == 1;
-  const auto run = [&](auto *d, auto *x) {
-    using D = std::remove_const_t<std::remove_pointer_t<decltype(d)>>;
-    using X = std::remove_const_t<std::remove_pointer_t<decltype(x)>>;
-    return wgrad<D, X>(g, {d, p.lddy}, {x, p.ldx}, p.dw, b, p.n, p.k, stream);
-  };
-  if (p.dy_dtype == 1 && p.x_dtype == 1) return run((const uint16_t *)p.dy, (const uint16_t *)p.x);
-  if (p.dy_dtype == 1) return run((const uint16_t *)p.dy, (const float *)p.x);
-  if (p.x_dtype == 1) return run((const float *)p.dy, (const uint16_t *)p.x);
-  return run((const float *)p.dy, (const float *)p.x);
+  if (p.dy_dtype == 1) return p.x_dtype == 1 ? wgrad<1, 1>(p, stream) : wgrad<1, 3>(p, stream);
+  return p.x_dtype == 1 ? wgrad<3, 1>(p, stream) : wgrad<3, 3>(p, stream);
 }
 
 int64_t grouped_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t rows, bool f32) {

@@ -155,7 +155,9 @@ struct GroupedWgrad {
   int index_bits;
   void *dw;
   int dw_dtype;
+  void *ws;                    // grouped_wgrad_workspace_bytes, 16-byte aligned
 };
+int64_t grouped_wgrad_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t rows, bool dy_f32, bool x_f32);
 hipError_t launch_grouped_wgrad(const GroupedWgrad &p, hipStream_t stream);
 
 // Low-rank adapters of the segments of rows that offsets and index give:

@@ -548,11 +548,19 @@ int64_t nvfp4_matvec_workspace_bytes(int64_t n, int64_t k, int64_t tokens, int x
  *
  * nvfp4_grouped_wgrad -- the gradient of the experts' weights,
  *   dw[e][n][k] = sum over offsets[e] <= t < offsets[e + 1] of dy[t][n] x[t][k]
- * dw: device, dw_dtype [experts][n][k], written whole (zeros for a group
- * without rows); must not overlap dy or x.  bf16 products are exact; with a
- * float32 operand products are off by at most 2^-23 of their magnitude, and
- * those with an infinity are infinite or NaN.  Sums are binary32.  experts * (ceil(n / 128) * ceil(k / 128) + 7) <= 2^24 - 8.
- * Deterministic.  Enqueues one kernel.
+ *  dw        : device, dw_dtype [experts][n][k], written whole (zeros for a
+ *              group without rows); must not overlap dy or x.
+ *  workspace : device, at least nvfp4_grouped_wgrad_workspace_bytes(experts, n,
+ *              k, rows, dy_dtype, x_dtype) bytes, 16-byte aligned, contents
+ *              ignored and overwritten.  Calls that share one must not overlap
+ *              in time.
+ *  experts * (ceil(n / 128) * ceil(k / 128) + 7) <= 2^24 - 8.
+ * bf16 products are exact; with a float32 operand products are off by at most
+ * 2^-23 of their magnitude, and those with an infinity are infinite or NaN.
+ * Sums are binary32, in a fixed order: deterministic on one device.  Enqueues
+ * one kernel, one more for each operand that is float32 or not of whole words
+ * (an odd number of columns, rows at odd places), and one where few tiles share
+ * long groups.
  */
 int nvfp4_grouped_matmul(const nvfp4_tensor *w, int transposed, const void *x, int x_dtype, int64_t rows, int64_t ldx,
                          const void *offsets, int index_bits, int64_t experts, void *y, int y_dtype, int64_t ldy,
@@ -563,7 +571,9 @@ int mxfp4_grouped_matmul(const mxfp4_tensor *w, int transposed, const void *x, i
 int64_t nvfp4_grouped_matmul_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t rows, int x_dtype);
 int nvfp4_grouped_wgrad(const void *dy, int dy_dtype, int64_t lddy, const void *x, int x_dtype, int64_t ldx,
                         int64_t rows, int64_t n, int64_t k, const void *offsets, int index_bits, int64_t experts,
-                        void *dw, int dw_dtype, void *hip_stream);
+                        void *dw, int dw_dtype, void *workspace, int64_t workspace_bytes, void *hip_stream);
+int64_t nvfp4_grouped_wgrad_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t rows, int dy_dtype,
+                                            int x_dtype);
 
 /*
  * nvfp4_adapters -- low-rank adapters of many requests at once, beside a

@@ -325,3 +325,19 @@ def test_streams_and_graphs(sizes):
         assert torch.equal(y, nv.nvfp4_grouped_matmul(w, x, offsets))
         assert torch.equal(dw, nv.nvfp4_grouped_wgrad(dy, x, offsets))
         offsets[1:-1] = offsets[1:-1].flip(0).sort().values // 2
+
+
+@pytest.mark.parametrize("n,k,sizes", [(128, 128, [2735]), (144, 4411, [1000, 524]), (2, 6, [5000, 0, 3]),
+                                       (130, 258, [900, 33, 900])])
+@pytest.mark.parametrize("dd,xd", [("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("pad", [0, 1])
+def test_wgrad_of_few_tiles(n, k, sizes, dd, xd, pad):
+    """Long groups of a small gradient, whose tokens are shared out."""
+    rows = sum(sizes) + 4
+    dy, x = matrix(whole_numbers(rows, n, n, DT[dd]), DT[dd], pad, pad), matrix(whole_numbers(rows, k, k, DT[xd]), DT[xd], pad)
+    dy[:3], x[-1] = float("nan"), float("nan")
+    dw = nv.nvfp4_grouped_wgrad(dy, x, offsets_of(sizes, first=3))
+    at = 3
+    for e, size in enumerate(sizes):
+        assert torch.equal(dw[e].double(), dy[at:at + size].double().t() @ x[at:at + size].double()), e
+        at += size
