@@ -51,71 +51,90 @@ __device__ __forceinline__ int next_of(const Segments &s, int adapter, int e, in
 
 // --------------------------------------------------------------- shrink --
 
-// out[t][j] = scale sum_c x[t][c] w[a][j][c] for a tile of 16 rows, zeros for
-// those without an adapter.  The weights are the A operand of the 16x16x32
-// MFMA, so that a lane has 4 neighbouring ranks of a row; of 128 c a lane holds
-// 32 neighbours, 8 an MFMA.  The workgroup's waves take 128 c each in turn,
-// and their sums meet in LDS.
+// out[t][j] = scale sum_c x[t][c] w[a][j][c] for a tile of 16 MT rows, zeros
+// for those without an adapter.  The weights are the A operand of the 16x16x32
+// MFMA, so that a lane has 4 neighbouring ranks of a row; 4 lanes hold 64 bytes
+// of a row in one piece.  The workgroup's waves take 128 c each in turn, and
+// their sums meet in LDS.
 constexpr int kChunk = 128;
-template <typename X, typename W, int RF>
-__global__ __launch_bounds__(RF > 4 ? 512 : 1024) void k_shrink(Segments s, const X *x, int64_t ldx, int64_t C, const W *w,
+template <typename X, typename W, int RF, int MT>
+__global__ __launch_bounds__(RF * MT > 4 ? 512 : 1024) void k_shrink(Segments s, const X *x, int64_t ldx, int64_t C, const W *w,
                                                                 int rank, const float *scale, float *out, int waves) {
-  extern __shared__ __align__(16) float sums[];        // [waves][16][16 RF]
+  extern __shared__ __align__(16) float sums[];        // [waves][16 MT][16 RF]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, quarter = lane >> 4;
-  const GroupTile t = find_tile(s.g, 16, 1, blockIdx.x);
+  const GroupTile t = find_tile(s.g, 16 * MT, 1, blockIdx.x);
   if (t.e < 0) return;
-  const int64_t t0 = t.begin + 16 * (int64_t)t.local;
-  const int live = (int)min(t.end - t0, (int64_t)16);
+  const int64_t t0 = t.begin + 16 * MT * (int64_t)t.local;
+  const int live = (int)min(t.end - t0, (int64_t)(16 * MT));
   const int a = s.adapter(t.e);
   if (a < 0) {
     for (int i = threadIdx.x; i < live * rank; i += 64 * waves) out[t0 * rank + i] = 0.0f;
     return;
   }
-  const X *xr = x + (t0 + min(row, live - 1)) * ldx;
+  const X *xr[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) xr[m] = x + (t0 + min(16 * m + row, live - 1)) * ldx;
   const W *wr[RF];
 #pragma unroll
   for (int f = 0; f < RF; ++f) wr[f] = w + ((int64_t)a * rank + min(16 * f + row, rank - 1)) * C;
-  f32x4_t acc[RF];
+  f32x4_t acc[MT][RF];
 #pragma unroll
-  for (int f = 0; f < RF; ++f) acc[f] = (f32x4_t){0, 0, 0, 0};
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int f = 0; f < RF; ++f) acc[m][f] = (f32x4_t){0, 0, 0, 0};
+  // (as many loads as the registers hold go out together)
+  constexpr int kTogether = (MT * sizeof(X) + RF * sizeof(W)) > 16 ? (MT * sizeof(X) + RF * sizeof(W)) > 32 ? 1 : 2 : 4;
   const auto step = [&](int64_t c0, auto whole) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t c = c0 + 32 * quarter + 8 * i;
-      Row8<X> xq;
-      Row8<W> wq[RF];
-      if (whole.value) xq.load(xr + c);
-      else load_row8(xq, xr, c, C);
+    for (int i0 = 0; i0 < 4; i0 += kTogether) {
+      Row8<X> xq[kTogether][MT];
+      Row8<W> wq[kTogether][RF];
 #pragma unroll
-      for (int f = 0; f < RF; ++f) {
-        if (whole.value) wq[f].load(wr[f] + c);
-        else load_row8(wq[f], wr[f], c, C);
+      for (int i = 0; i < kTogether; ++i) {
+        const int64_t c = c0 + 32 * (i0 + i) + 8 * quarter;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if (whole.value) xq[i][m].load(xr[m] + c);
+          else load_row8(xq[i][m], xr[m], c, C);
+        }
+#pragma unroll
+        for (int f = 0; f < RF; ++f) {
+          if (whole.value) wq[i][f].load(wr[f] + c);
+          else load_row8(wq[i][f], wr[f], c, C);
+        }
       }
-      Operand<X> xo;
-      xo.set(xq);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int f = 0; f < RF; ++f) {
-        Operand<W> wo;
-        wo.set(wq[f]);
-        multiply16(acc[f], wo, xo);
+      for (int i = 0; i < kTogether; ++i) {
+        Operand<X> xo[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) xo[m].set(xq[i][m]);
+#pragma unroll
+        for (int f = 0; f < RF; ++f) {
+          Operand<W> wo;
+          wo.set(wq[i][f]);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) multiply16(acc[m][f], wo, xo[m]);
+        }
       }
     }
   };
   int64_t c0 = (int64_t)wave * kChunk;
-#pragma unroll 2
   for (; c0 + kChunk <= C; c0 += (int64_t)waves * kChunk) step(c0, std::true_type());
   if (c0 < C) step(c0, std::false_type());
   constexpr int kPitch = 16 * RF;
 #pragma unroll
-  for (int f = 0; f < RF; ++f)
-    *reinterpret_cast<f32x4_t *>(sums + (wave * 16 + row) * kPitch + 16 * f + 4 * quarter) = acc[f];
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int f = 0; f < RF; ++f)
+      *reinterpret_cast<f32x4_t *>(sums + (wave * 16 * MT + 16 * m + row) * kPitch + 16 * f + 4 * quarter) = acc[m][f];
   __syncthreads();
   const float factor = scale ? scale[a] : 1.0f;
   for (int i = threadIdx.x; i < live * rank; i += 64 * waves) {
     const int at = i / rank * kPitch + i % rank;
     float v = 0.0f;
-    for (int k = 0; k < waves; ++k) v += sums[k * 16 * kPitch + at];
+    for (int k = 0; k < waves; ++k) v += sums[k * 16 * MT * kPitch + at];
     out[t0 * rank + i] = v * factor;
   }
 }
@@ -124,72 +143,96 @@ __global__ __launch_bounds__(RF > 4 ? 512 : 1024) void k_shrink(Segments s, cons
 
 // y[t][c] = base[t][c] + scale sum_j u[t][j] w[a][c][j] for 16 MT rows and 256
 // columns, 64 of them a wave.  The weights are the A operand with its rows
-// ordered so that a lane's results are 16 neighbouring columns of a row.
-template <typename W, int MT>
+// ordered so that a lane's results are two runs of 8 columns of a row, and 4
+// lanes hold 64 bytes of it (bf16) in one piece.
+//
+// Loads are whole and unconditional wherever the columns (the ranks) allow it,
+// by a choice that the wave makes as one: what a branch leaves zero in some lanes
+// would wait for the loads of the others.
+template <typename T>
+__device__ __forceinline__ void load_ranks(Row8<T> &q, const T *row, int at, int rank, bool eights) {
+  if (eights) {
+    q.load(row + (at < rank ? at : 0));
+  } else {
+    load_row8(q, row, at, rank);
+  }
+}
+template <typename T> __device__ __forceinline__ void zero_unless(Row8<T> &q, bool keep) {
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q.r[i] = keep ? q.r[i] : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      q.a[i] = keep ? q.a[i] : 0.0f;
+      q.b[i] = keep ? q.b[i] : 0.0f;
+    }
+  }
+}
+
+// BASE: 0 none, 1 f32, 2 bf16.
+template <typename W, int MT, int BASE>
 __global__ __launch_bounds__(256) void k_expand(Segments s, const float *u, int rank, const W *w, const float *scale,
-                                                const void *base, int base_bf16, int64_t ldb, void *y, int y_bf16,
-                                                int64_t ldy, int64_t C, int tiles_c) {
+                                                const void *base, int64_t ldb, void *y, int y_bf16, int64_t ldy, int64_t C,
+                                                int tiles_c) {
+  using B = std::conditional_t<BASE == 2, uint16_t, float>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, quarter = lane >> 4;
   const GroupTile t = find_tile(s.g, 16 * MT, tiles_c, blockIdx.x);
   if (t.e < 0) return;
   const int64_t t0 = t.begin + 16 * MT * (int64_t)(t.local / tiles_c);
-  const int64_t c0 = (int64_t)(t.local % tiles_c) * 256 + 64 * wave, mine = c0 + 16 * quarter;
+  const int64_t c0 = (int64_t)(t.local % tiles_c) * 256 + 64 * wave, mine = c0 + 8 * quarter;
   const int live = (int)min(t.end - t0, (int64_t)(16 * MT));
-  const int a = s.adapter(t.e);
+  const int a = __builtin_amdgcn_readfirstlane(s.adapter(t.e));
   if (c0 >= C || (a < 0 && base == y)) return;
-  float v[MT][16];
+  const bool inside = c0 + 64 <= C, eights = rank % 8 == 0;
+  Row8<B> bq[BASE ? MT : 1][2];
+  if constexpr (BASE != 0) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int64_t at = (t0 + min(16 * m + row, live - 1)) * ldb;
+    for (int m = 0; m < MT; ++m) {
+      const B *at = (const B *)base + (t0 + min(16 * m + row, live - 1)) * ldb;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (!base) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[m][8 * i + j] = 0.0f;
-      } else if (base_bf16) {
-        Row8<uint16_t> q;
-        load_row8(q, (const uint16_t *)base + at, mine + 8 * i, C);
-        q.get(v[m] + 8 * i);
-      } else {
-        Row8<float> q;
-        load_row8(q, (const float *)base + at, mine + 8 * i, C);
-        q.get(v[m] + 8 * i);
+      for (int i = 0; i < 2; ++i) {
+        if (inside) bq[m][i].load(at + mine + 32 * i);
+        else load_row8(bq[m][i], at, mine + 32 * i, C);
       }
     }
   }
+  f32x4_t acc[MT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int f = 0; f < 4; ++f) acc[m][f] = (f32x4_t){0, 0, 0, 0};
+  float factor = 0.0f;
   if (a >= 0) {
-    f32x4_t acc[MT][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int f = 0; f < 4; ++f) acc[m][f] = (f32x4_t){0, 0, 0, 0};
+    factor = scale ? scale[a] : 1.0f;
     for (int j0 = 0; j0 < rank; j0 += 32) {
+      const int j = j0 + 8 * quarter;
+      Row8<W> wq[4];
+      Row8<float> uq[MT];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int64_t c = min(c0 + 32 * (f >> 1) + 8 * (row >> 2) + 4 * (f & 1) + (row & 3), C - 1);
+        load_ranks(wq[f], w + ((int64_t)a * C + c) * rank, j, rank, eights);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) load_ranks(uq[m], u + (t0 + min(16 * m + row, live - 1)) * rank, j, rank, eights);
+      __builtin_amdgcn_sched_barrier(0);
       Operand<W> wo[4];
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
-        const int64_t c = min(c0 + (row >> 2) * 16 + 4 * f + (row & 3), C - 1);
-        Row8<W> q;
-        load_row8(q, w + ((int64_t)a * C + c) * rank, j0 + 8 * quarter, rank);
-        wo[f].set(q);
+        zero_unless(wq[f], j < rank);
+        wo[f].set(wq[f]);
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        Row8<float> q;
-        load_row8(q, u + (t0 + min(16 * m + row, live - 1)) * rank, j0 + 8 * quarter, rank);
+        zero_unless(uq[m], j < rank);
         Operand<float> uo;
-        uo.set(q);
+        uo.set(uq[m]);
 #pragma unroll
         for (int f = 0; f < 4; ++f) multiply16(acc[m][f], wo[f], uo);
       }
     }
-    const float factor = scale ? scale[a] : 1.0f;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int f = 0; f < 4; ++f)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[m][4 * f + i] = __builtin_fmaf(acc[m][f][i], factor, v[m][4 * f + i]);
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
@@ -197,14 +240,27 @@ __global__ __launch_bounds__(256) void k_expand(Segments s, const float *u, int 
     const int64_t at = (t0 + 16 * m + row) * ldy;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      float v[8];
+      if constexpr (BASE != 0) {
+        bq[m][i].get(v);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+      }
+      if (a >= 0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = __builtin_fmaf(acc[m][2 * i + k / 4][k % 4], factor, v[k]);
+      }
       if (y_bf16) {
         Row8<uint16_t> q;
-        q.set(v[m] + 8 * i);
-        store_row8(q, (uint16_t *)y + at, mine + 8 * i, C);
+        q.set(v);
+        if (inside) q.store((uint16_t *)y + at + mine + 32 * i);
+        else store_row8(q, (uint16_t *)y + at, mine + 32 * i, C);
       } else {
         Row8<float> q;
-        q.set(v[m] + 8 * i);
-        store_row8(q, (float *)y + at, mine + 8 * i, C);
+        q.set(v);
+        if (inside) q.store((float *)y + at + mine + 32 * i);
+        else store_row8(q, (float *)y + at, mine + 32 * i, C);
       }
     }
   }
@@ -400,32 +456,37 @@ __global__ __launch_bounds__(256) void k_turn(Segments s, const W *in, W *out, i
 template <typename X, typename W>
 void shrink(const Segments &s, const X *x, int64_t ldx, int64_t C, const W *w, int rank, const float *scale, float *out,
             hipStream_t stream) {
-  const int64_t tiles = s.g.rows / 16 + std::min<int64_t>(s.g.count, s.g.rows);
+  // 32 rows a tile where 16 would make more than two rounds of the CUs
+  const bool pairs = s.g.rows > 16 * 2 * (int64_t)device_cus() && rank <= 64;
+  const int64_t tile = pairs ? 32 : 16, tiles = s.g.rows / tile + std::min<int64_t>(s.g.count, s.g.rows);
   const auto launch = [&](auto kernel, int rf) {
-    const int most = rf > 4 ? 8 : 16;
+    const int most = rf * (pairs ? 2 : 1) > 4 ? 8 : 16;
     const int waves = (int)std::max<int64_t>(1, std::min<int64_t>(most, (C + kChunk - 1) / kChunk));
-    kernel<<<(unsigned)tiles, 64 * waves, (size_t)waves * 16 * 16 * rf * 4, stream>>>(s, x, ldx, C, w, rank, scale, out,
-                                                                                      waves);
+    kernel<<<(unsigned)tiles, 64 * waves, (size_t)waves * tile * 16 * rf * 4, stream>>>(s, x, ldx, C, w, rank, scale, out,
+                                                                                       waves);
   };
-  if (rank <= 16) launch(k_shrink<X, W, 1>, 1);
-  else if (rank <= 32) launch(k_shrink<X, W, 2>, 2);
-  else if (rank <= 64) launch(k_shrink<X, W, 4>, 4);
-  else launch(k_shrink<X, W, 8>, 8);
+  if (rank <= 16) pairs ? launch(k_shrink<X, W, 1, 2>, 1) : launch(k_shrink<X, W, 1, 1>, 1);
+  else if (rank <= 32) pairs ? launch(k_shrink<X, W, 2, 2>, 2) : launch(k_shrink<X, W, 2, 1>, 2);
+  else if (rank <= 64) pairs ? launch(k_shrink<X, W, 4, 2>, 4) : launch(k_shrink<X, W, 4, 1>, 4);
+  else launch(k_shrink<X, W, 8, 1>, 8);
 }
 
 template <typename W>
 void expand(const Segments &s, const float *u, int rank, const W *w, const float *scale, const void *base, int base_bf16,
             int64_t ldb, void *y, int y_bf16, int64_t ldy, int64_t C, hipStream_t stream) {
   const int tiles_c = (int)((C + 255) / 256);
-  const bool few = s.g.rows <= 32 * (int64_t)(s.g.count - 2);
-  const int64_t tile = few ? 16 : 64;
+  const bool few = s.g.rows <= 16 * (int64_t)(s.g.count - 2);
+  const int64_t tile = few ? 16 : 32;
   const int64_t tiles = s.g.rows / tile + std::min<int64_t>(s.g.count, s.g.rows);
   const auto launch = [&](auto kernel) {
-    kernel<<<(unsigned)(tiles * tiles_c), 256, 0, stream>>>(s, u, rank, w, scale, base, base_bf16, ldb, y, y_bf16, ldy, C,
-                                                           tiles_c);
+    kernel<<<(unsigned)(tiles * tiles_c), 256, 0, stream>>>(s, u, rank, w, scale, base, ldb, y, y_bf16, ldy, C, tiles_c);
   };
-  if (few) launch(k_expand<W, 1>);
-  else launch(k_expand<W, 4>);
+  with_flag(few, [&](auto f) {
+    constexpr int MT = f.value ? 1 : 2;
+    if (!base) launch(k_expand<W, MT, 0>);
+    else if (base_bf16) launch(k_expand<W, MT, 2>);
+    else launch(k_expand<W, MT, 1>);
+  });
 }
 
 // Shares of the rows that the gradient kernels cut a sum into: until there is
