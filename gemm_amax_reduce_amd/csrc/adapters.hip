@@ -13,6 +13,7 @@
 // and y (k_expand), and both matrices into sums over rows (k_grad).  u and g
 // are float32; every product runs on the bf16 MFMA with float32 operands as
 // three bf16 parts each (about what binary32 products keep).
+#include "gemm_common.h"
 #include "groups.h"
 #include "nvfp4_kernels.h"
 #include "operands.h"
@@ -35,14 +36,14 @@ struct Segments {
     return v >= 0 && v < adapters ? (int)v : -1;
   }
 };
-// The first segment from e on with that adapter and rows of its own between
-// `from` and `to`; count - 1 if there is none.
-__device__ __forceinline__ int next_of(const Segments &s, int adapter, int e, int64_t from, int64_t to) {
+// The first segment from e on with that adapter and rows of its own; count - 1
+// if there is none.
+__device__ __forceinline__ int next_of(const Segments &s, int adapter, int e) {
   const int lane = threadIdx.x & 63;
   for (; e < s.g.count - 1; e += 64) {
     const int mine = e + lane;
     bool hit = mine < s.g.count - 1 && s.adapter(mine) == adapter;
-    if (hit) hit = max(s.g.at(mine), from) < min(s.g.at(mine + 1), to);
+    if (hit) hit = s.g.size(mine) > 0;
     const uint64_t found = __ballot(hit);
     if (found) return __builtin_amdgcn_readfirstlane(e + (int)__builtin_ctzll(found));
   }
@@ -270,80 +271,121 @@ __global__ __launch_bounds__(256) void k_expand(Segments s, const float *u, int 
 
 // Sums over the rows t of all segments of an adapter of x[t][c] g[t][j], x
 // with C columns, as [r][C] (dA) or, with TURN, [C][r] (dB).  Rows run along
-// the reduction: 32 of them a stage go to LDS as they lie and are fetched by
-// columns with transposing reads.  grid: (256 columns, adapters, shares of the
-// rows); with several shares partial sums go to partial[share][adapter][...].
+// the reduction: 32 of them a stage, of a segment, go to LDS as they lie, and
+// the lanes fetch 8 rows of a column: by transposing reads where they are bf16
+// (two 32-byte chunks of a row trade places by row, as in the grouped weight
+// gradient), else, and g always, by 8 reads whose lanes are neighbours.
+// grid: (256 columns, adapters, shares of the rows); with several shares
+// partial sums go to partial[share][adapter][...].
+//
+// x of whole words goes to LDS by DMA, two stages ahead; x at odd places by way
+// of registers, one stage ahead.
 constexpr int kGradRows = 32, kGradCols = 256;
-template <typename X, int RF, bool TURN>
+template <typename X, int RF, bool DMA> struct Grad {
+  static constexpr int kRowX = kGradCols * sizeof(X), kX = kGradRows * kRowX;
+  static constexpr int kG = kGradRows * 32 * RF * 4 + 256;            // g's rows lie together, a rank apart
+  static constexpr int kStage = kX + kG, kRing = DMA ? (2 * 3 * kStage <= 160 * 1024 || 3 * kStage <= 160 * 1024 ? 3 : 2) : 2;
+  // DMA instructions (1 KB) a wave and stage: a wave copies 8 rows of x
+  static constexpr int kIX = kX / 4096, kRows = 1024 / kRowX;
+};
+// Where a stage lies: rows at .. at + 31 of a segment that ends at `end`.
+struct GradStage {
+  int64_t at, end;
+};
+
+template <typename X, int RF, bool TURN, bool DMA>
 __global__ __launch_bounds__(256) void k_grad(Segments s, const X *x, int64_t ldx, int64_t C, const float *g, int rank,
                                               const float *scale, void *out, int out_bf16, float *partial) {
+  using T = Grad<X, RF, DMA>;
+  constexpr bool kWide = sizeof(X) == 4;
   constexpr int kXP = Operand<X>::kParts;
-  constexpr int kRowX = kGradCols * 2 + 32, kRowG = 64 * RF + 32;
-  constexpr int kPartX = kGradRows * kRowX, kPartG = kGradRows * kRowG;
-  constexpr int kBuffer = kXP * kPartX + 3 * kPartG;
-  constexpr int kXL = kGradRows * (kGradCols / 8) / 256, kGL = (kGradRows * 4 * RF + 255) / 256;
-  __shared__ __align__(16) char lds[2 * kBuffer];
+  __shared__ __align__(16) uint8_t lds[T::kRing * T::kStage];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int a = blockIdx.y;
   const int64_t c0 = (int64_t)blockIdx.x * kGradCols;
-  const int64_t from = s.g.rows * blockIdx.z / gridDim.z, to = s.g.rows * (blockIdx.z + 1) / gridDim.z;
 
-  // stages: 32 rows of a segment each
-  int e = next_of(s, a, 1, from, to);
-  int64_t at = 0, end = 0;
+  // the stages one after the other, every gridDim.z-th of the adapter's; past the
+  // last one, empty ones
+  const int shares = gridDim.z;
+  int e = next_of(s, a, 1), before = 0;             // stages of earlier segments, modulo the shares
+  GradStage now = {0, 0};
   const auto enter = [&]() {
-    if (e < s.g.count - 1) {
-      at = max(s.g.at(e), from);
-      end = min(s.g.at(e + 1), to);
+    for (; e < s.g.count - 1; e = next_of(s, a, e + 1)) {
+      const int64_t begin = uniform64(s.g.at(e)), end = uniform64(s.g.at(e + 1));
+      const int skip = ((int)blockIdx.z - before + shares) % shares;
+      now = {begin + (int64_t)skip * kGradRows, end};
+      if (now.at < end) return;
+      before = (int)((before + (end - begin + kGradRows - 1) / kGradRows) % shares);
     }
+    now = {0, 0};
   };
   enter();
-  const auto more = [&]() { return e < s.g.count - 1; };
   const auto advance = [&]() {
-    at += kGradRows;
-    if (at >= end) {
-      e = next_of(s, a, e + 1, from, to);
-      enter();
+    if (now.at >= now.end) return;
+    now.at += (int64_t)shares * kGradRows;
+    if (now.at < now.end) return;
+    before = (int)((before + (uniform64(s.g.size(e)) + kGradRows - 1) / kGradRows) % shares);
+    e = next_of(s, a, e + 1);
+    enter();
+  };
+
+  // ---- into LDS
+  const uint32_t xp = (uint32_t)(ldx * sizeof(X));
+  // lane l copies 16 bytes, l % kPer of row l / kPer; bf16 chunks (32 bytes)
+  // turned by 2 (row % 4)
+  constexpr int kPer = T::kRowX / 16 < 64 ? T::kRowX / 16 : 64;
+  uint32_t xat[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    xat[i] = kWide ? 16 * (uint32_t)lane : (uint32_t)(lane / kPer) * xp + 16 * (uint32_t)((lane % kPer) ^ (4 * (2 * i + lane / kPer)));
+  const auto copy = [&](uint8_t *buf) {
+    const int64_t rows = min(now.end - now.at, (int64_t)kGradRows), cols = min(C - c0, (int64_t)kGradCols);
+    const __amdgpu_buffer_rsrc_t xv = make_rsrc(x + (rows > 0 ? now.at * ldx + c0 : 0),
+                                                rows > 0 ? (uint32_t)(rows - 1) * xp + (uint32_t)(cols * sizeof(X)) : 0u);
+    const __amdgpu_buffer_rsrc_t gv = make_rsrc(g + (rows > 0 ? now.at * rank : 0), rows > 0 ? (uint32_t)rows * rank * 4 : 0u);
+#pragma unroll
+    for (int i = 0; i < T::kIX; ++i) {
+      const int r = 8 * wave + i * T::kRows;
+      dma16(xv, buf + r * T::kRowX, xat[i & 1], (uint32_t)r * xp);
+    }
+    // g's 128 rank bytes, a KB an instruction, the same number for each wave
+#pragma unroll
+    for (int i = 0; i < RF; ++i) {
+      const uint32_t at = (uint32_t)(4 * i + wave) * 1024;
+      dma16(gv, buf + T::kX + at, 16 * (uint32_t)lane, at);
     }
   };
-  Row8<X> xr[kXL];
-  Row8<float> gr[kGL];
+  // (bf16 at odd places)
+  constexpr int kXL = kGradRows * (kGradCols / 8) / 256, kGL = kGradRows * 32 * RF / 256;
+  Row8<X> xr[DMA ? 1 : kXL];
+  float gr[DMA ? 1 : kGL];
   const auto load = [&]() {
+    if constexpr (!DMA) {
 #pragma unroll
-    for (int i = 0; i < kXL; ++i) {
-      const int p = tid + i * 256;
-      const int64_t t = at + p / (kGradCols / 8);
-      load_row8(xr[i], x + t * ldx, c0 + p % (kGradCols / 8) * 8, t < end ? C : 0);
-    }
+      for (int i = 0; i < kXL; ++i) {
+        const int p = tid + i * 256;
+        const int64_t t = now.at + p / (kGradCols / 8);
+        load_row8(xr[i], x + t * ldx, c0 + p % (kGradCols / 8) * 8, t < now.end ? C : 0);
+      }
 #pragma unroll
-    for (int i = 0; i < kGL; ++i) {
-      const int p = tid + i * 256;
-      const int64_t t = at + p / (4 * RF);
-      load_row8(gr[i], g + t * rank, p % (4 * RF) * 8, t < end ? rank : 0);
-    }
-  };
-  const auto put = [&](int turn) {
-    char *const buf = lds + turn * kBuffer;
-#pragma unroll
-    for (int i = 0; i < kXL; ++i) {
-      const int p = tid + i * 256;
-      Operand<X> o;
-      o.set(xr[i]);
-#pragma unroll
-      for (int k = 0; k < kXP; ++k)
-        *reinterpret_cast<bf16x8_t *>(buf + k * kPartX + p / (kGradCols / 8) * kRowX + p % (kGradCols / 8) * 16) = o.v[k];
-    }
-#pragma unroll
-    for (int i = 0; i < kGL; ++i) {
-      const int p = tid + i * 256;
-      if (kGradRows * 4 * RF % 256 != 0 && p >= kGradRows * 4 * RF) continue;
-      Operand<float> o;
-      o.set(gr[i]);
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-        *reinterpret_cast<bf16x8_t *>(buf + kXP * kPartX + k * kPartG + p / (4 * RF) * kRowG + p % (4 * RF) * 16) = o.v[k];
+      for (int i = 0; i < kGL; ++i) {
+        const int64_t p = tid + i * 256;
+        gr[i] = p < min(now.end - now.at, (int64_t)kGradRows) * rank ? g[now.at * rank + p] : 0.0f;
+      }
     }
   };
+  const auto put = [&](uint8_t *buf) {
+    if constexpr (!DMA) {
+#pragma unroll
+      for (int i = 0; i < kXL; ++i) {
+        const int p = tid + i * 256, r = p / (kGradCols / 8), c = p % (kGradCols / 8);
+        *reinterpret_cast<u32x4_t *>(buf + r * T::kRowX + 16 * (c ^ (4 * (r & 3)))) = xr[i].r;
+      }
+#pragma unroll
+      for (int i = 0; i < kGL; ++i) *reinterpret_cast<float *>(buf + T::kX + 4 * (tid + i * 256)) = gr[i];
+    }
+  };
+
   float16_t acc[RF][2];
 #pragma unroll
   for (int f = 0; f < RF; ++f)
@@ -351,21 +393,35 @@ __global__ __launch_bounds__(256) void k_grad(Segments s, const X *x, int64_t ld
     for (int q = 0; q < 2; ++q)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[f][q][i] = 0.0f;
-  const int col = 16 * ((lane >> 4) & 1) + 4 * (lane & 3), trow = 8 * (lane >> 5) + ((lane >> 2) & 3);
-  const auto products = [&](int turn) {
-    const char *const xb = lds + turn * kBuffer + trow * kRowX + (64 * wave + col) * 2;
-    const char *const gb = lds + turn * kBuffer + kXP * kPartX + trow * kRowG + col * 2;
+  const int r = lane & 31, h = lane >> 5;
+  uint32_t xcol[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int chunk = 4 * wave + 2 * q + ((lane >> 4) & 1);
+    xcol[q] = kWide ? 8 * h * T::kRowX + 4 * (64 * wave + 32 * q + r)
+                    : (8 * h + ((lane >> 2) & 3)) * T::kRowX + 32 * (chunk ^ (2 * ((lane >> 2) & 3))) + 8 * (lane & 3);
+  }
+  const auto eight = [&](const char *p, int pitch) {
+    Row8<float> q;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const float *>(p + i * pitch);
+    q.set(v);
+    return q;
+  };
+  const auto products = [&](const char *buf) {
 #pragma unroll
     for (int ks = 0; ks < kGradRows / 16; ++ks) {
-      bf16x8_t xo[kXP][2], go[3][RF];
+      Operand<X> xo[2];
+      Operand<float> go[RF];
 #pragma unroll
-      for (int p = 0; p < kXP; ++p)
+      for (int q = 0; q < 2; ++q) {
+        const char *at = buf + xcol[q] + ks * 16 * T::kRowX;
+        if constexpr (kWide) xo[q].set(eight(at, T::kRowX));
+        else xo[q].v[0] = lds_column(at, T::kRowX);
+      }
 #pragma unroll
-        for (int q = 0; q < 2; ++q) xo[p][q] = lds_column(xb + p * kPartX + ks * 16 * kRowX + q * 64, kRowX);
-#pragma unroll
-      for (int p = 0; p < 3; ++p)
-#pragma unroll
-        for (int f = 0; f < RF; ++f) go[p][f] = lds_column(gb + p * kPartG + ks * 16 * kRowG + f * 64, kRowG);
+      for (int f = 0; f < RF; ++f) go[f].set(eight(buf + T::kX + ((16 * ks + 8 * h) * rank + 32 * f + r) * 4, rank * 4));
 #pragma unroll
       for (int p = 0; p < 3; ++p)
 #pragma unroll
@@ -375,28 +431,54 @@ __global__ __launch_bounds__(256) void k_grad(Segments s, const X *x, int64_t ld
           for (int f = 0; f < RF; ++f)
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-              acc[f][q] = TURN ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(xo[k][q], go[p][f], acc[f][q], 0, 0, 0)
-                               : __builtin_amdgcn_mfma_f32_32x32x16_bf16(go[p][f], xo[k][q], acc[f][q], 0, 0, 0);
+              acc[f][q] = TURN ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(xo[q].v[k], go[f].v[p], acc[f][q], 0, 0, 0)
+                               : __builtin_amdgcn_mfma_f32_32x32x16_bf16(go[f].v[p], xo[q].v[k], acc[f][q], 0, 0, 0);
         }
     }
   };
-  if (more()) {
-    load();
-    int turn = 0;
-    put(0);
-    advance();
-    bool next = more();
-    if (next) load();
-    __syncthreads();
-    for (;;) {
-      products(turn);
-      if (!next) break;
-      put(turn ^ 1);
+  if (now.at < now.end) {
+    if constexpr (DMA) {
+      constexpr int kCopies = T::kIX + RF, kAhead = T::kRing - 1;
+      GradStage at[T::kRing];                       // the stages in the ring
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        at[i] = now;
+        copy(lds + i * T::kStage);
+        advance();
+      }
+      int place = 0;
+      while (at[0].at < at[0].end) {
+        // this wave's copies of the stage (those behind it stay under way), and
+        // every wave past its reads of the one before
+        meet<(wait_vm((kAhead - 1) * kCopies) & ~0x0F00)>();
+        const int free = place == 0 ? T::kRing - 1 : place - 1;
+        at[kAhead] = now;
+        copy(lds + free * T::kStage);
+        advance();
+        products((const char *)lds + place * T::kStage);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) at[i] = at[i + 1];
+        place = place + 1 == T::kRing ? 0 : place + 1;
+      }
+      __builtin_amdgcn_s_waitcnt(wait_vm(0));       // nothing is left that writes LDS
+    } else {
+      int turn = 0;
+      load();
+      put(lds);
       advance();
-      next = more();
+      bool next = now.at < now.end;
       if (next) load();
       __syncthreads();
-      turn ^= 1;
+      for (;;) {
+        products((const char *)lds + turn * T::kStage);
+        if (!next) break;
+        put(lds + (turn ^ 1) * T::kStage);
+        advance();
+        next = now.at < now.end;
+        if (next) load();
+        __syncthreads();
+        turn ^= 1;
+      }
     }
   }
   const float factor = scale ? scale[a] : 1.0f;
@@ -425,7 +507,7 @@ __global__ __launch_bounds__(256) void k_grad(Segments s, const X *x, int64_t ld
 __global__ __launch_bounds__(256) void k_grad_join(Segments s, const float *partial, int shares, int64_t size, void *out,
                                                    int out_bf16) {
   const int a = blockIdx.y;
-  const bool used = next_of(s, a, 1, 0, s.g.rows) < s.g.count - 1;
+  const bool used = next_of(s, a, 1) < s.g.count - 1;
   const int64_t all = size * s.adapters;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < size; i += (int64_t)gridDim.x * 256) {
     float v = 0.0f;
@@ -441,7 +523,7 @@ template <typename W>
 __global__ __launch_bounds__(256) void k_turn(Segments s, const W *in, W *out, int64_t R, int64_t C, int tiles_r) {
   __shared__ W tile[64][65];
   const int a = blockIdx.y;
-  if (next_of(s, a, 1, 0, s.g.rows) == s.g.count - 1) return;
+  if (next_of(s, a, 1) == s.g.count - 1) return;
   const int64_t r0 = (int64_t)(blockIdx.x % tiles_r) * 64, c0 = (int64_t)(blockIdx.x / tiles_r) * 64;
   const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
   for (int i = y; i < 64; i += 4)
@@ -507,9 +589,14 @@ void grad(const Segments &s, int64_t segments, const X *x, int64_t ldx, int64_t 
   const auto launch = [&](auto kernel) {
     kernel<<<grid, 256, 0, stream>>>(s, x, ldx, C, g, rank, scale, out, out_bf16, partial);
   };
-  if (rank <= 32) launch(k_grad<X, 1, TURN>);
-  else if (rank <= 64) launch(k_grad<X, 2, TURN>);
-  else launch(k_grad<X, 4, TURN>);
+  const bool words = (uintptr_t)x % 4 == 0 && ldx * sizeof(X) % 4 == 0 && C * sizeof(X) % 4 == 0 && ldx < (1LL << 24);
+  const auto of_rank = [&](auto dma) {
+    if (rank <= 32) launch(k_grad<X, 1, TURN, dma.value>);
+    else if (rank <= 64) launch(k_grad<X, 2, TURN, dma.value>);
+    else launch(k_grad<X, 4, TURN, dma.value>);
+  };
+  if constexpr (sizeof(X) == 2) with_flag(words, of_rank);
+  else of_rank(std::true_type());
   if (shares > 1) {
     const int64_t size = rank * C;
     k_grad_join<<<dim3((unsigned)std::min<int64_t>((size + 255) / 256, 1024), (unsigned)s.adapters), 256, 0, stream>>>(

@@ -25,6 +25,19 @@ __device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t v, uint8_t *dst, uin
   __builtin_amdgcn_raw_ptr_buffer_load_lds(v, (__attribute__((address_space(3))) void *)dst, 4, voff, soff, 0, 0);
 }
 
+// The s_waitcnt operand that waits until n vector memory operations are left
+// (& ~0x0F00: and no LDS operation).
+constexpr int wait_vm(int n) { return (n & 15) | (n >> 4) << 14 | 0x0F70; }
+// A wait for those counts, and the workgroup's barrier.
+template <int COUNTS> __device__ __forceinline__ void meet() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(COUNTS);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
   uint32_t u = __float_as_uint(f);
   return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);

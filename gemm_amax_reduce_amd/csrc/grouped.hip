@@ -99,17 +99,6 @@ __global__ __launch_bounds__(256) void k_parts(const X *x, int64_t ldx, int64_t 
 // the matrix pipe busy.  A stage's copies go out over the first four of its
 // eight steps; in the last one the wave waits for those of the stage behind,
 // meets the others, and reads from it.
-constexpr int wait_vm(int n) { return (n & 15) | (n >> 4) << 14 | 0x0F70; }
-// A wait for those counts, and the workgroup's barrier.
-template <int COUNTS> __device__ __forceinline__ void meet() {
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(COUNTS);
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
-
 // XP: parts of x (3: float32), `part` elements apart.
 template <bool MX, int XP, int WAVES, int NF, int MF>
 __global__ __launch_bounds__(64 * WAVES, WAVES == 4 && NF * MF * XP < 12 ? 2 : 1) void
