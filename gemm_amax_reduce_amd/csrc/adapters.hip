@@ -518,19 +518,37 @@ __global__ __launch_bounds__(256) void k_grad_join(Segments s, const float *part
   }
 }
 
-// out[a] = the transpose of in[a], [R][C], for the adapters that a segment has.
+// B as [r][N] and A as [K][r] for the adapters that a segment has: kTurn of the
+// long side and the whole rank a workgroup, B's workgroups first, read and
+// written as they lie.
+constexpr int kTurn = 64;
 template <typename W>
-__global__ __launch_bounds__(256) void k_turn(Segments s, const W *in, W *out, int64_t R, int64_t C, int tiles_r) {
-  __shared__ W tile[64][65];
-  const int a = blockIdx.y;
-  if (next_of(s, a, 1) == s.g.count - 1) return;
-  const int64_t r0 = (int64_t)(blockIdx.x % tiles_r) * 64, c0 = (int64_t)(blockIdx.x / tiles_r) * 64;
-  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-  for (int i = y; i < 64; i += 4)
-    if (r0 + i < R && c0 + x < C) tile[i][x] = in[((int64_t)a * R + r0 + i) * C + c0 + x];
+__global__ __launch_bounds__(256) void k_turn(Segments s, const W *b, W *b_turned, int64_t N, const W *a, W *a_turned,
+                                              int64_t K, int rank) {
+  extern __shared__ __align__(16) uint8_t turn_lds[];
+  W *const tile = reinterpret_cast<W *>(turn_lds);       // [rank][kTurn + 1]
+  const int adapter = blockIdx.y;
+  if (next_of(s, adapter, 1) == s.g.count - 1) return;
+  const int blocks_b = (int)((N + kTurn - 1) / kTurn);
+  const bool first = (int)blockIdx.x < blocks_b;
+  const int64_t L = first ? N : K, at = (int64_t)(first ? blockIdx.x : blockIdx.x - blocks_b) * kTurn;
+  const int live = (int)min(L - at, (int64_t)kTurn);
+  const int64_t base = (int64_t)adapter * rank * L;
+  if (first) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < live * rank; i += 256) tile[i % rank * (kTurn + 1) + i / rank] = b[base + at * rank + i];
+  } else {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < kTurn * rank; i += 256)
+      if (i % kTurn < live) tile[i / kTurn * (kTurn + 1) + i % kTurn] = a[base + i / kTurn * L + at + i % kTurn];
+  }
   __syncthreads();
-  for (int i = y; i < 64; i += 4)
-    if (c0 + i < C && r0 + x < R) out[((int64_t)a * C + c0 + i) * R + r0 + x] = tile[x][i];
+  if (first) {
+    for (int i = threadIdx.x; i < kTurn * rank; i += 256)
+      if (i % kTurn < live) b_turned[base + i / kTurn * L + at + i % kTurn] = tile[i / kTurn * (kTurn + 1) + i % kTurn];
+  } else {
+    for (int i = threadIdx.x; i < live * rank; i += 256) a_turned[base + at * rank + i] = tile[i % rank * (kTurn + 1) + i / rank];
+  }
 }
 
 // -------------------------------------------------------------- launches --
@@ -543,7 +561,8 @@ void shrink(const Segments &s, const X *x, int64_t ldx, int64_t C, const W *w, i
   const int64_t tile = pairs ? 32 : 16, tiles = s.g.rows / tile + std::min<int64_t>(s.g.count, s.g.rows);
   const auto launch = [&](auto kernel, int rf) {
     const int most = rf * (pairs ? 2 : 1) > 4 ? 8 : 16;
-    const int waves = (int)std::max<int64_t>(1, std::min<int64_t>(most, (C + kChunk - 1) / kChunk));
+    const int64_t chunks = std::max<int64_t>(1, (C + kChunk - 1) / kChunk), rounds = (chunks + most - 1) / most;
+    const int waves = (int)((chunks + rounds - 1) / rounds);
     kernel<<<(unsigned)tiles, 64 * waves, (size_t)waves * tile * 16 * rf * 4, stream>>>(s, x, ldx, C, w, rank, scale, out,
                                                                                        waves);
   };
@@ -604,12 +623,6 @@ void grad(const Segments &s, int64_t segments, const X *x, int64_t ldx, int64_t 
   }
 }
 
-template <typename W>
-void turn(const Segments &s, const W *in, W *out, int64_t R, int64_t C, hipStream_t stream) {
-  const int64_t tr = (R + 63) / 64, tc = (C + 63) / 64;
-  k_turn<W><<<dim3((unsigned)(tr * tc), (unsigned)s.adapters), 256, 0, stream>>>(s, in, out, R, C, (int)tr);
-}
-
 int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 
 // The backward pass' scratch memory: B and A turned, g, and the partial sums
@@ -649,8 +662,10 @@ template <typename W> void backward_w(const AdapterBackward &p, const Segments &
   W *const bt = (W *)(ws + at.b_turned), *const aT = (W *)(ws + at.a_turned);
   float *const g = (float *)(ws + at.g), *const partial = (float *)(ws + at.partial);
   if (s.g.rows > 0) {
-    if (w.n > 0) turn(s, (const W *)w.b, bt, w.n, rank, stream);
-    if (w.k > 0) turn(s, (const W *)w.a, aT, rank, w.k, stream);
+    const int64_t blocks = (w.n + kTurn - 1) / kTurn + (w.k + kTurn - 1) / kTurn;
+    if (blocks > 0)
+      k_turn<W><<<dim3((unsigned)blocks, (unsigned)w.adapters), 256, sizeof(W) * rank * (kTurn + 1), stream>>>(
+          s, (const W *)w.b, bt, w.n, (const W *)w.a, aT, w.k, rank);
     if (p.dy_dtype == 1) shrink(s, (const uint16_t *)p.dy, p.lddy, w.n, bt, rank, w.scale, g, stream);
     else shrink(s, (const float *)p.dy, p.lddy, w.n, bt, rank, w.scale, g, stream);
     if (w.k > 0)
