@@ -142,8 +142,8 @@ __global__ __launch_bounds__(RF * MT > 4 ? 512 : 1024) void k_shrink(Segments s,
 
 // --------------------------------------------------------------- expand --
 
-// y[t][c] = base[t][c] + scale sum_j u[t][j] w[a][c][j] for 16 MT rows and 256
-// columns, 64 of them a wave.  The weights are the A operand with its rows
+// y[t][c] = base[t][c] + scale sum_j u[t][j] w[a][c][j] for 16 MT rows and
+// `spans` times 256 columns, 64 of them a wave.  The weights are the A operand with its rows
 // ordered so that a lane's results are two runs of 8 columns of a row, and 4
 // lanes hold 64 bytes of it (bf16) in one piece.
 //
@@ -175,93 +175,97 @@ template <typename T> __device__ __forceinline__ void zero_unless(Row8<T> &q, bo
 template <typename W, int MT, int BASE>
 __global__ __launch_bounds__(256) void k_expand(Segments s, const float *u, int rank, const W *w, const float *scale,
                                                 const void *base, int64_t ldb, void *y, int y_bf16, int64_t ldy, int64_t C,
-                                                int tiles_c) {
+                                                int tiles_c, int spans) {
   using B = std::conditional_t<BASE == 2, uint16_t, float>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, quarter = lane >> 4;
   const GroupTile t = find_tile(s.g, 16 * MT, tiles_c, blockIdx.x);
   if (t.e < 0) return;
   const int64_t t0 = t.begin + 16 * MT * (int64_t)(t.local / tiles_c);
-  const int64_t c0 = (int64_t)(t.local % tiles_c) * 256 + 64 * wave, mine = c0 + 8 * quarter;
   const int live = (int)min(t.end - t0, (int64_t)(16 * MT));
   const int a = __builtin_amdgcn_readfirstlane(s.adapter(t.e));
-  if (c0 >= C || (a < 0 && base == y)) return;
-  const bool inside = c0 + 64 <= C, eights = rank % 8 == 0;
-  Row8<B> bq[BASE ? MT : 1][2];
-  if constexpr (BASE != 0) {
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const B *at = (const B *)base + (t0 + min(16 * m + row, live - 1)) * ldb;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (inside) bq[m][i].load(at + mine + 32 * i);
-        else load_row8(bq[m][i], at, mine + 32 * i, C);
-      }
-    }
-  }
-  f32x4_t acc[MT][4];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int f = 0; f < 4; ++f) acc[m][f] = (f32x4_t){0, 0, 0, 0};
-  float factor = 0.0f;
-  if (a >= 0) {
-    factor = scale ? scale[a] : 1.0f;
-    for (int j0 = 0; j0 < rank; j0 += 32) {
-      const int j = j0 + 8 * quarter;
-      Row8<W> wq[4];
-      Row8<float> uq[MT];
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        const int64_t c = min(c0 + 32 * (f >> 1) + 8 * (row >> 2) + 4 * (f & 1) + (row & 3), C - 1);
-        load_ranks(wq[f], w + ((int64_t)a * C + c) * rank, j, rank, eights);
-      }
-#pragma unroll
-      for (int m = 0; m < MT; ++m) load_ranks(uq[m], u + (t0 + min(16 * m + row, live - 1)) * rank, j, rank, eights);
-      __builtin_amdgcn_sched_barrier(0);
-      Operand<W> wo[4];
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        zero_unless(wq[f], j < rank);
-        wo[f].set(wq[f]);
-      }
+  if (a < 0 && base == y) return;
+  const float factor = a >= 0 && scale ? scale[a] : 1.0f;
+  const bool eights = rank % 8 == 0;
+  int64_t c0 = (int64_t)(t.local % tiles_c) * spans * 256 + 64 * wave;
+  const int64_t end = min(C, c0 + spans * 256);
+  for (; c0 < end; c0 += 256) {
+    const int64_t mine = c0 + 8 * quarter;
+    const bool inside = c0 + 64 <= C;
+    Row8<B> bq[BASE ? MT : 1][2];
+    if constexpr (BASE != 0) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        zero_unless(uq[m], j < rank);
-        Operand<float> uo;
-        uo.set(uq[m]);
+        const B *at = (const B *)base + (t0 + min(16 * m + row, live - 1)) * ldb;
 #pragma unroll
-        for (int f = 0; f < 4; ++f) multiply16(acc[m][f], wo[f], uo);
+        for (int i = 0; i < 2; ++i) {
+          if (inside) bq[m][i].load(at + mine + 32 * i);
+          else load_row8(bq[m][i], at, mine + 32 * i, C);
+        }
       }
     }
-  }
+    f32x4_t acc[MT][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    if (16 * m + row >= live) continue;
-    const int64_t at = (t0 + 16 * m + row) * ldy;
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float v[8];
-      if constexpr (BASE != 0) {
-        bq[m][i].get(v);
-      } else {
+      for (int f = 0; f < 4; ++f) acc[m][f] = (f32x4_t){0, 0, 0, 0};
+    if (a >= 0) {
+      for (int j0 = 0; j0 < rank; j0 += 32) {
+        const int j = j0 + 8 * quarter;
+        Row8<W> wq[4];
+        Row8<float> uq[MT];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+        for (int f = 0; f < 4; ++f) {
+          const int64_t c = min(c0 + 32 * (f >> 1) + 8 * (row >> 2) + 4 * (f & 1) + (row & 3), C - 1);
+          load_ranks(wq[f], w + ((int64_t)a * C + c) * rank, j, rank, eights);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) load_ranks(uq[m], u + (t0 + min(16 * m + row, live - 1)) * rank, j, rank, eights);
+        __builtin_amdgcn_sched_barrier(0);
+        Operand<W> wo[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          zero_unless(wq[f], j < rank);
+          wo[f].set(wq[f]);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          zero_unless(uq[m], j < rank);
+          Operand<float> uo;
+          uo.set(uq[m]);
+#pragma unroll
+          for (int f = 0; f < 4; ++f) multiply16(acc[m][f], wo[f], uo);
+        }
       }
-      if (a >= 0) {
+    }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = __builtin_fmaf(acc[m][2 * i + k / 4][k % 4], factor, v[k]);
-      }
-      if (y_bf16) {
-        Row8<uint16_t> q;
-        q.set(v);
-        if (inside) q.store((uint16_t *)y + at + mine + 32 * i);
-        else store_row8(q, (uint16_t *)y + at, mine + 32 * i, C);
-      } else {
-        Row8<float> q;
-        q.set(v);
-        if (inside) q.store((float *)y + at + mine + 32 * i);
-        else store_row8(q, (float *)y + at, mine + 32 * i, C);
+    for (int m = 0; m < MT; ++m) {
+      if (16 * m + row >= live) continue;
+      const int64_t at = (t0 + 16 * m + row) * ldy;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float v[8];
+        if constexpr (BASE != 0) {
+          bq[m][i].get(v);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+        }
+        if (a >= 0) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = __builtin_fmaf(acc[m][2 * i + k / 4][k % 4], factor, v[k]);
+        }
+        if (y_bf16) {
+          Row8<uint16_t> q;
+          q.set(v);
+          if (inside) q.store((uint16_t *)y + at + mine + 32 * i);
+          else store_row8(q, (uint16_t *)y + at, mine + 32 * i, C);
+        } else {
+          Row8<float> q;
+          q.set(v);
+          if (inside) q.store((float *)y + at + mine + 32 * i);
+          else store_row8(q, (float *)y + at, mine + 32 * i, C);
+        }
       }
     }
   }
@@ -575,12 +579,17 @@ void shrink(const Segments &s, const X *x, int64_t ldx, int64_t C, const W *w, i
 template <typename W>
 void expand(const Segments &s, const float *u, int rank, const W *w, const float *scale, const void *base, int base_bf16,
             int64_t ldb, void *y, int y_bf16, int64_t ldy, int64_t C, hipStream_t stream) {
-  const int tiles_c = (int)((C + 255) / 256);
   const bool few = s.g.rows <= 16 * (int64_t)(s.g.count - 2);
   const int64_t tile = few ? 16 : 32;
-  const int64_t tiles = s.g.rows / tile + std::min<int64_t>(s.g.count, s.g.rows);
+  const int64_t tiles = s.g.rows / tile + std::min<int64_t>(s.g.count, s.g.rows), across = (C + 255) / 256;
+  // several spans a workgroup where the CUs have 8 workgroups each without: finding
+  // the rows is paid once (4099 rows of 20480 columns: 138 us a call with one span,
+  // 132 with four, 136 with eight)
+  const int spans = (int)std::max<int64_t>(1, std::min<int64_t>(4, tiles * across / (8 * (int64_t)device_cus())));
+  const int tiles_c = (int)((across + spans - 1) / spans);
   const auto launch = [&](auto kernel) {
-    kernel<<<(unsigned)(tiles * tiles_c), 256, 0, stream>>>(s, u, rank, w, scale, base, ldb, y, y_bf16, ldy, C, tiles_c);
+    kernel<<<(unsigned)(tiles * tiles_c), 256, 0, stream>>>(s, u, rank, w, scale, base, ldb, y, y_bf16, ldy, C, tiles_c,
+                                                            spans);
   };
   with_flag(few, [&](auto f) {
     constexpr int MT = f.value ? 1 : 2;
