@@ -515,10 +515,9 @@ template <typename X, typename Y> void forward_x(const RmsForward &a, const Out<
   else forward<X, float, Y, true>(a, out, stream);
 }
 template <typename Y> hipError_t forward_y(const RmsForward &a, const Out<Y> &out, hipStream_t stream) {
-  if (a.rows > 0) {
-    if (a.x_dtype == 1) forward_x<uint16_t>(a, out, stream);
-    else forward_x<float>(a, out, stream);
-  }
+  if (a.rows == 0) return hipSuccess;
+  if (a.x_dtype == 1) forward_x<uint16_t>(a, out, stream);
+  else forward_x<float>(a, out, stream);
   return hipGetLastError();
 }
 
