@@ -9,9 +9,26 @@
 // Weights are decoded to bf16, where e2m1(code) e4m3(scale) is exact, and
 // multiplied on the 32x32x16 bf16 MFMA with the weights as the A operand, so
 // that a lane ends up with 16 consecutive n of a token; float32 activations
-// are three bf16 parts.  A workgroup's tile is 128 NF weight rows (its four
-// waves have NF fragments of 32 each, so every weight is decoded by one wave)
-// by 32 MF tokens, which all of its waves read from LDS.
+// are three bf16 parts, made once per call (k_parts).  A workgroup's tile is
+// 32 NF weight rows a wave, so that every weight is decoded by one wave, by 32
+// MF tokens, which all of its waves read from LDS; codes, scales and tokens are
+// copied there by DMA a stage ahead, and the decoding lies between the MFMAs.
+// Groups of few rows take the matrix-vector product's tiles instead
+// (grouped_tiles_fit, in matvec.hip), which read the weights once and are bound
+// by that.
+//
+// Bound by the matrix pipe where groups are long: 4096 rows of 8 experts
+// 20480 x 5120 in bf16 take 819 us (NVFP4; 1050 TFLOP/s, a large bf16 product of
+// the library reaches 1425), of which partly filled tiles at the groups' ends
+// are an eighth, decoding a tenth and the LDS traffic of the copies a fifth.
+// 1531 float32 rows of 24 experts transposed, 5120 x 1280 (three products each):
+// 103 us and 7.5 for the parts.
+//
+// The weight gradient has tokens along the reduction: both operands lie in LDS
+// as they come, by DMA three stages deep, and reach the lanes by transposing
+// reads.  8192 rows of 8 experts 5120 x 5120 in bf16: 498 us (863 TFLOP/s);
+// float32 operands go as three parts each, six products (777 rows of 16 experts
+// 1283 x 2050: 70 us, 168 MB of results among them, and 14 for the parts).
 #include "gemm_common.h"
 #include "groups.h"
 #include "nvfp4_kernels.h"
@@ -437,6 +454,7 @@ bool by_matvec_tiles(int64_t experts, int64_t n, int64_t k, int64_t rows) {
 // to that first: [parts][rows][round8(cols)] in the workspace, zeros behind a
 // row's end.
 int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
+// (1.5 TB/s at 777 rows, where its start counts: 6 to 8 us)
 template <typename X>
 __global__ __launch_bounds__(256) void k_pad(const X *x, int64_t ldx, int64_t rows, int64_t cols, uint16_t *out) {
   const int64_t pieces = (cols + 7) / 8, all = rows * pieces;

@@ -136,7 +136,9 @@ template <typename X> constexpr int columns() { return sizeof(X) == 2 ? 1 : 3; }
 // SL: 16-column slabs; grid: (tile walkers, tokens / 16, ranges of K).
 //
 // With groups (of tokens, each with weights of its own) the grid's y counts the
-// groups' tiles of up to as many tokens as the slabs hold.
+// groups' tiles of up to as many tokens as the slabs hold.  16 rows over 32
+// experts of MXFP4 2048 x 5120: 19.5 us for the weights of some 12 experts (66
+// MB) in one wave of workgroups, 3.4 TB/s behind a start of 6 us.
 struct OneWeight {};
 struct Experts {
   Groups g;
