@@ -364,7 +364,13 @@ __global__ __launch_bounds__(256) void k_grad(Segments s, const X *x, int64_t ld
 #pragma unroll
     for (int i = 0; i < T::kIX; ++i) {
       const int r = 8 * wave + i * T::kRows;
-      dma16(xv, buf + r * T::kRowX, xat[i & 1], (uint32_t)r * xp);
+      if constexpr (kWide) {
+        // (a view for each row, wherever it lies)
+        const bool in = r < rows;
+        dma16(make_rsrc(x + (in ? (now.at + r) * ldx + c0 : 0), in ? (uint32_t)cols * 4 : 0u), buf + r * T::kRowX, xat[0], 0);
+      } else {
+        dma16(xv, buf + r * T::kRowX, xat[i & 1], (uint32_t)r * xp);
+      }
     }
     // g's 128 rank bytes, a KB an instruction, the same number for each wave
 #pragma unroll

@@ -196,7 +196,7 @@ inline bool grouped_ok(int64_t experts, int64_t n, int64_t k, int64_t rows) {
          grid_ok((n + 127) / 128, rows / 32 + (experts < rows ? experts : rows));
 }
 inline bool wgrad_ok(int64_t experts, int64_t n, int64_t k, int64_t rows) {
-  return n >= 0 && k >= 0 && rows >= 0 && experts >= 1 && experts <= kMaxGroups && n <= kMaxGrid * 128 && k <= kMaxGrid * 128 &&
+  return n >= 0 && k >= 0 && rows >= 0 && experts >= 1 && experts <= kMaxGroups && n <= kMaxGemmK && k <= kMaxGemmK &&
          grid_ok((n + 127) / 128, (k + 127) / 128) && grid_ok((n + 127) / 128 * ((k + 127) / 128) + 7, experts) &&
          count_ok(rows, n + 8) && count_ok(rows, k + 8);
 }

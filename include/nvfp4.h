@@ -554,7 +554,7 @@ int64_t nvfp4_matvec_workspace_bytes(int64_t n, int64_t k, int64_t tokens, int x
  *              k, rows, dy_dtype, x_dtype) bytes, 16-byte aligned, contents
  *              ignored and overwritten.  Calls that share one must not overlap
  *              in time.
- *  experts * (ceil(n / 128) * ceil(k / 128) + 7) <= 2^24 - 8.
+ *  n, k <= 2^25 - 16, experts * (ceil(n / 128) * ceil(k / 128) + 7) <= 2^24 - 8.
  * bf16 products are exact; with a float32 operand products are off by at most
  * 2^-23 of their magnitude, and those with an infinity are infinite or NaN.
  * Sums are binary32, in a fixed order: deterministic on one device.  Enqueues

@@ -165,7 +165,8 @@ WGRAD = dict(dy=FAKE, dyd=1, lddy=48, x=2 * FAKE, xd=1, ldx=64, rows=40, n=48, k
 @pytest.mark.parametrize("bad,status", [
     (dict(dyd=2), ENUM), (dict(xd=2), ENUM), (dict(dwd=2), ENUM), (dict(bits=8), ENUM), (dict(lddy=47), SHAPE),
     (dict(ldx=63), SHAPE), (dict(rows=-1), SHAPE), (dict(n=-1), SHAPE), (dict(k=-1), SHAPE), (dict(experts=0), SHAPE),
-    (dict(experts=(1 << 20) + 1), SHAPE), (dict(experts=1 << 20, n=1 << 12, lddy=1 << 12), SHAPE), (dict(dy=None), NULL),
+    (dict(experts=(1 << 20) + 1), SHAPE),
+    (dict(n=1 << 25, lddy=1 << 25), SHAPE), (dict(k=1 << 25, ldx=1 << 25), SHAPE), (dict(experts=1 << 20, n=1 << 12, lddy=1 << 12), SHAPE), (dict(dy=None), NULL),
     (dict(x=None), NULL), (dict(dw=None), NULL), (dict(off=None), NULL), (dict(dy=FAKE + 1), ALIGN),
     (dict(dw=3 * FAKE + 2), ALIGN), (dict(off=FAKE + 2), ALIGN), (dict(ws=FAKE + 8), ALIGN), (dict(dw=FAKE), SHAPE),
     (dict(dw=2 * FAKE - 4), SHAPE), (dict(dyd=0, lddy=48, bytes=0), SHAPE), (dict(dyd=0, ws=None), NULL), (dict(), HIP),

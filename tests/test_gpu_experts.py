@@ -323,6 +323,13 @@ def test_captured_and_replayed():
         want = step()
 
 
+def test_tensors_stay_plain():
+    """Nothing is left on parameters or inputs that would be saved with them."""
+    step, x, r, _, _ = _chain()
+    step()
+    assert not vars(x) and not vars(r)
+
+
 def test_capture_beside_an_eager_graph_is_refused():
     layer = E.NVFP4Experts(2, 32, 32, device="cuda")
     x = torch.randn((8, 32), device="cuda", dtype=torch.bfloat16)
