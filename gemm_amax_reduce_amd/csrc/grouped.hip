@@ -454,19 +454,26 @@ bool by_matvec_tiles(int64_t experts, int64_t n, int64_t k, int64_t rows) {
 // to that first: [parts][rows][round8(cols)] in the workspace, zeros behind a
 // row's end.
 int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
-// (1.5 TB/s at 777 rows, where its start counts: 6 to 8 us)
+// (Both operands in one launch where they are of one type: its start counts.)
+template <typename X> struct Pad {
+  const X *x;
+  int64_t ld, cols;
+  uint16_t *out;
+};
 template <typename X>
-__global__ __launch_bounds__(256) void k_pad(const X *x, int64_t ldx, int64_t rows, int64_t cols, uint16_t *out) {
-  const int64_t pieces = (cols + 7) / 8, all = rows * pieces;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+__global__ __launch_bounds__(256) void k_pad(Pad<X> first, Pad<X> second, int64_t rows) {
+  const int64_t before = rows * ((first.cols + 7) / 8), every = before + rows * ((second.cols + 7) / 8);
+  for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < every; j += (int64_t)gridDim.x * 256) {
+    const Pad<X> m = j < before ? first : second;
+    const int64_t pieces = (m.cols + 7) / 8, all = rows * pieces, i = j < before ? j : j - before;
     Row8<X> q;
-    load_row8(q, x + i / pieces * ldx, i % pieces * 8, cols);
+    load_row8(q, m.x + i / pieces * m.ld, i % pieces * 8, m.cols);
     if constexpr (sizeof(X) == 2) {
-      *reinterpret_cast<u32x4_t *>(out + i * 8) = q.r;
+      *reinterpret_cast<u32x4_t *>(m.out + i * 8) = q.r;
     } else {
       const Parts p = split8_nearest(q);
 #pragma unroll
-      for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x4_t *>(out + (k * all + i) * 8) = p.v[k];
+      for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x4_t *>(m.out + (k * all + i) * 8) = p.v[k];
     }
   }
 }
@@ -754,15 +761,24 @@ template <int DP, int XP> hipError_t wgrad(const GroupedWgrad &p, hipStream_t st
   space += (8 - (uintptr_t)space / 2 % 8) % 8;
   const auto ready = [&](const void *m, int64_t ld, int64_t cols, bool f32) {
     if (p.rows == 0 || words(m, ld, cols, f32)) return Operand16{(const uint16_t *)m, ld, cols, 0};
-    const int64_t padded = round8(cols), pieces = p.rows * padded / 8;
-    const unsigned grid = (unsigned)std::min<int64_t>((pieces + 255) / 256, 1 << 14);
-    if (f32) k_pad<<<grid, 256, 0, stream>>>((const float *)m, ld, p.rows, cols, space);
-    else k_pad<<<grid, 256, 0, stream>>>((const uint16_t *)m, ld, p.rows, cols, space);
+    const int64_t padded = round8(cols);
     const Operand16 o = {space, padded, padded, p.rows * padded};
     space += (f32 ? 3 : 1) * p.rows * padded;
     return o;
   };
   const Operand16 dy = ready(p.dy, p.lddy, p.n, DP == 3), x = ready(p.x, p.ldx, p.k, XP == 3);
+  // an operand that is where it was takes no part
+  const auto pad = [&](auto zero, bool with_dy, bool with_x) {
+    using T = decltype(zero);
+    Pad<T> a = {(const T *)p.dy, p.lddy, p.n, (uint16_t *)dy.p}, b = {(const T *)p.x, p.ldx, p.k, (uint16_t *)x.p};
+    if (!with_dy || dy.p == p.dy) a.cols = 0;
+    if (!with_x || x.p == p.x) b.cols = 0;
+    const int64_t pieces = p.rows * (round8(a.cols) + round8(b.cols)) / 8;
+    if (pieces > 0)
+      k_pad<<<(unsigned)std::min<int64_t>((pieces + 255) / 256, 1 << 14), 256, 0, stream>>>(a, b, p.rows);
+  };
+  pad(0.0f, DP == 3, XP == 3);
+  pad((uint16_t)0, DP == 1, XP == 1);
   const Groups g = {p.offsets, p.index_bits == 64, (int)p.experts, p.rows, 0};
   const int64_t tn = (p.n + 127) / 128, tk = (p.k + 64 * FK - 1) / (64 * FK);
   const dim3 grid((unsigned)(wgrad_quota((int)(tn * tk)) * kXcds * p.experts), (unsigned)shares);
