@@ -18,17 +18,18 @@
 // by that.
 //
 // Bound by the matrix pipe where groups are long: 4096 rows of 8 experts
-// 20480 x 5120 in bf16 take 819 us (NVFP4; 1050 TFLOP/s, a large bf16 product of
+// 20480 x 5120 in bf16 take 800 us (NVFP4; 1075 TFLOP/s, a large bf16 product of
 // the library reaches 1425), of which partly filled tiles at the groups' ends
 // are an eighth, decoding a tenth and the LDS traffic of the copies a fifth.
 // 1531 float32 rows of 24 experts transposed, 5120 x 1280 (three products each):
-// 103 us and 7.5 for the parts.
+// 101 us, bound by copies that are one stage ahead (60 KB a CU on their way), and
+// 7.5 for the parts.
 //
 // The weight gradient has tokens along the reduction: both operands lie in LDS
 // as they come, by DMA three stages deep, and reach the lanes by transposing
 // reads.  8192 rows of 8 experts 5120 x 5120 in bf16: 498 us (863 TFLOP/s);
 // float32 operands go as three parts each, six products (777 rows of 16 experts
-// 1283 x 2050: 70 us, 168 MB of results among them, and 14 for the parts).
+// 1283 x 2050: 63 to 71 us, 168 MB of results among them, and 9 to 11 for the parts).
 #include "gemm_common.h"
 #include "groups.h"
 #include "nvfp4_kernels.h"
@@ -454,7 +455,8 @@ bool by_matvec_tiles(int64_t experts, int64_t n, int64_t k, int64_t rows) {
 // to that first: [parts][rows][round8(cols)] in the workspace, zeros behind a
 // row's end.
 int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
-// (Both operands in one launch where they are of one type: its start counts.)
+// Both operands in one launch where they are of one type: its start counts (777
+// rows of 1283 and 2050 columns in two launches 14 us, in one 9 to 11).
 template <typename X> struct Pad {
   const X *x;
   int64_t ld, cols;
