@@ -338,6 +338,8 @@ __global__ __launch_bounds__(256) void k_grad(Segments s, const X *x, int64_t ld
     now = {0, 0};
   };
   enter();
+  // (one without rows leaves zeros, whatever its scale)
+  const float factor = scale && now.at < now.end ? scale[a] : 1.0f;
   const auto advance = [&]() {
     if (now.at >= now.end) return;
     now.at += (int64_t)shares * kGradRows;
@@ -505,7 +507,6 @@ __global__ __launch_bounds__(256) void k_grad(Segments s, const X *x, int64_t ld
       }
     }
   }
-  const float factor = scale ? scale[a] : 1.0f;
   const int64_t size = (int64_t)rank * C;
   const int64_t first = gridDim.z > 1 ? ((int64_t)blockIdx.z * gridDim.y + a) * size : a * size;
   // register i of a fragment is its row 8 (i / 4) + 4 h + i % 4, the lane its column

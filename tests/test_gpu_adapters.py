@@ -219,6 +219,36 @@ def test_rows_without_an_adapter_may_hold_anything():
     assert torch.all(got[2][1] == 0) and torch.all(got[2][3] == 0) and torch.all(got[3][1] == 0)
 
 
+@pytest.mark.parametrize("rows", [3, 600, 2000])
+@pytest.mark.parametrize("rank", [8, 40, 100])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_the_scale_of_an_unused_adapter_reaches_nothing(rows, rank, dt):
+    """Scales of NaN and Inf where no segment has the adapter, or an empty one
+    has it: zeros, and the others' results unchanged.  Below 512 rows a sum
+    over them is one share, above it is cut."""
+    x, dy, a, b, scale, offsets, which = setup([rows, 0], [1, 3], 0, 1, 90, 70, rank, 5, dt, dt, 6)
+    u = nv.nvfp4_adapters(x, a, b, offsets, which, scale)[1]
+    want = nv.nvfp4_adapters(x, a, b, offsets, which, scale)[0], *nv.nvfp4_adapters_backward(
+        dy, x, u, a, b, offsets, which, scale)
+    scale[0], scale[2], scale[3], scale[4] = float("nan"), float("inf"), float("nan"), float("-inf")
+    got = nv.nvfp4_adapters(x, a, b, offsets, which, scale)[0], *nv.nvfp4_adapters_backward(
+        dy, x, u, a, b, offsets, which, scale)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    for unused in (0, 2, 3, 4):
+        assert torch.all(got[2][unused] == 0) and torch.all(got[3][unused] == 0)
+
+
+def test_an_infinite_scale_with_an_idle_share():
+    """An adapter of one stage of rows beside one of many, whose sums are cut:
+    the shares without rows of it add zeros to its infinite gradient."""
+    x, dy, a, b, scale, offsets, which = setup([20, 700], [0, 1], 0, 0, 90, 70, 8, 2, "bf16", "bf16", 7)
+    u = nv.nvfp4_adapters(x, a, b, offsets, which, scale)[1]
+    want = nv.nvfp4_adapters_backward(dy, x, u, a, b, offsets, which, scale)[2]
+    scale[0] = float("inf")
+    db = nv.nvfp4_adapters_backward(dy, x, u, a, b, offsets, which, scale)[2]
+    assert torch.equal(db[1], want[1]) and torch.isinf(db[0]).all() and torch.equal(db[0] > 0, want[0] > 0)
+
+
 def test_empty():
     a, b = torch.ones((2, 4, 16), device="cuda"), torch.ones((2, 8, 4), device="cuda")
     offsets, index = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
