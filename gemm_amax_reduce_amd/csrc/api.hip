@@ -7,6 +7,8 @@
 #include <float.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 namespace {
 
 // Size limits of the launch geometry (each documented in nvfp4.h).
@@ -154,13 +156,44 @@ int check_distill(const void *z, int z_dtype, int64_t tokens, int64_t vocab, int
   return NVFP4_OK;
 }
 
-// Does a matrix of the given pitch (bytes from row to row, and those of a row
-// that are its own) meet an input or the residual stream of an RMS norm?
-bool rms_meets(const nvfp4::RmsForward &a, const void *y, int64_t pitch, int64_t used) {
-  const int64_t xs = dtype_size(a.x_dtype), rs = dtype_size(a.r_dtype);
-  return overlap(a.x, a.ldx * xs, a.cols * xs, y, pitch, used, a.rows) ||
-         (a.res && (overlap(a.res, a.ldr * rs, a.cols * rs, y, pitch, used, a.rows) ||
-                    overlap(a.h, a.ldh * rs, a.cols * rs, y, pitch, used, a.rows)));
+// The bytes of an argument: `rows` times `used` of them, `pitch` apart (one row:
+// a block).  Absent ones are empty.
+struct Area {
+  const void *p;
+  int64_t rows, pitch, used;
+  bool empty() const { return !p || rows <= 0 || used <= 0; }
+  uintptr_t begin() const { return (uintptr_t)p; }
+  uintptr_t end() const { return begin() + (uintptr_t)((rows - 1) * pitch + used); }
+};
+inline Area matrix(const void *p, int dtype, int64_t rows, int64_t cols, int64_t ld) {
+  const int64_t size = dtype_size(dtype);
+  return {p, rows, ld * size, cols * size};
+}
+inline Area block(const void *p, int64_t bytes) { return {p, 1, bytes, bytes}; }
+// Do two of them meet?  (Exact where they have one pitch, or one is a block,
+// which may lie in the other's gaps.)
+bool meet(const Area &a, const Area &b) {
+  if (a.empty() || b.empty() || a.begin() >= b.end() || b.begin() >= a.end()) return false;
+  if (a.rows == 1 && b.rows == 1) return true;
+  if (a.rows > 1 && b.rows > 1) {
+    if (a.pitch != b.pitch) return true;
+    const int64_t d = ((int64_t)(b.begin() - a.begin()) % a.pitch + a.pitch) % a.pitch;
+    return d < a.used || d + b.used > a.pitch;
+  }
+  const Area &m = a.rows > 1 ? a : b, &one = a.rows > 1 ? b : a;
+  if (one.begin() < m.begin()) return true;                  // it reaches the first row
+  const int64_t at = (int64_t)(one.begin() - m.begin()) % m.pitch;
+  return at < m.used || at + one.used > m.pitch;
+}
+// Do outputs meet inputs, or each other?
+bool any_meet(std::initializer_list<Area> outs, std::initializer_list<Area> ins) {
+  for (const Area *o = outs.begin(); o != outs.end(); ++o) {
+    for (const Area &i : ins)
+      if (meet(*o, i)) return true;
+    for (const Area *other = outs.begin(); other != o; ++other)
+      if (meet(*o, *other)) return true;
+  }
+  return false;
 }
 
 // What the two RMS norm calls share (all but y).
@@ -172,14 +205,18 @@ int check_rms(const nvfp4::RmsForward &a) {
   if (a.rows > 0 && (!a.x || !a.rstd || (a.res && !a.h))) return NVFP4_ERR_NULL;
   if (!aligned(a.x, dtype_size(a.x_dtype)) || !aligned(a.w, dtype_size(a.w_dtype)) || !aligned(a.rstd, 4))
     return NVFP4_ERR_ALIGN;
-  if (!a.res) return NVFP4_OK;
-  const int64_t xs = dtype_size(a.x_dtype), rs = dtype_size(a.r_dtype);
-  if (!aligned(a.res, rs) || !aligned(a.h, rs)) return NVFP4_ERR_ALIGN;
-  // h may take the residual's place, and meets no input otherwise
-  if (overlap(a.x, a.ldx * xs, a.cols * xs, a.h, a.ldh * rs, a.cols * rs, a.rows)) return NVFP4_ERR_SHAPE;
-  const bool same = a.res == a.h && (a.ldr == a.ldh || a.rows <= 1);
-  if (!same && overlap(a.res, a.ldr * rs, a.cols * rs, a.h, a.ldh * rs, a.cols * rs, a.rows)) return NVFP4_ERR_SHAPE;
+  if (a.res && (!aligned(a.res, dtype_size(a.r_dtype)) || !aligned(a.h, dtype_size(a.r_dtype)))) return NVFP4_ERR_ALIGN;
   return NVFP4_OK;
+}
+// Do its outputs (y, or codes and scales, y0 and y1) meet inputs or each other?
+// h may take the residual's place.
+bool rms_meets(const nvfp4::RmsForward &a, const Area &y0, const Area &y1) {
+  const Area x = matrix(a.x, a.x_dtype, a.rows, a.cols, a.ldx), w = block(a.w, a.cols * dtype_size(a.w_dtype)),
+             rstd = block(a.rstd, a.rows * 4);
+  if (!a.res) return any_meet({y0, y1, rstd}, {x, w});
+  const Area res = matrix(a.res, a.r_dtype, a.rows, a.cols, a.ldr), h = matrix(a.h, a.r_dtype, a.rows, a.cols, a.ldh);
+  const bool same = a.res == a.h && (a.ldr == a.ldh || a.rows <= 1);
+  return any_meet({y0, y1, rstd, h}, {x, w}) || any_meet({y0, y1, rstd}, {res}) || (!same && meet(h, res));
 }
 
 // Groups of rows and the grids of the kernels that walk them: at most 2^24 - 8
@@ -199,13 +236,6 @@ inline bool wgrad_ok(int64_t experts, int64_t n, int64_t k, int64_t rows) {
   return n >= 0 && k >= 0 && rows >= 0 && experts >= 1 && experts <= kMaxGroups && n <= kMaxGemmK && k <= kMaxGemmK &&
          grid_ok((n + 127) / 128, (k + 127) / 128) && grid_ok((n + 127) / 128 * ((k + 127) / 128) + 7, experts) &&
          count_ok(rows, n + 8) && count_ok(rows, k + 8);
-}
-// Do the bytes of two ranges meet?
-inline bool ranges_meet(const void *a, int64_t abytes, const void *b, int64_t bbytes) {
-  return overlap(a, abytes, abytes, b, bbytes, bbytes, 1);
-}
-inline int64_t span(int64_t rows, int64_t ld, int64_t cols, int64_t size) {
-  return rows > 0 && cols > 0 ? ((rows - 1) * ld + cols) * size : 0;
 }
 
 // What the grouped products share; outer, k: the stack as it is stored.
@@ -260,7 +290,16 @@ int check_base(const void *base, int base_dtype, int64_t ldb, const void *y, int
   const int64_t bs = dtype_size(base_dtype);
   if (!aligned(base, bs)) return NVFP4_ERR_ALIGN;
   const bool same = base == y && base_dtype == y_dtype && (ldb == ldy || rows <= 1);
-  return !same && overlap(base, ldb * bs, cols * bs, y, ldy * ys, cols * ys, rows) ? NVFP4_ERR_SHAPE : NVFP4_OK;
+  return !same && meet(matrix(base, base_dtype, rows, cols, ldb), matrix(y, y_dtype, rows, cols, ldy)) ? NVFP4_ERR_SHAPE
+                                                                                                       : NVFP4_OK;
+}
+// Do outputs meet the adapters' own arguments, the inputs given, or each other?
+bool adapters_meet(const nvfp4::AdapterWeights &w, std::initializer_list<Area> outs, std::initializer_list<Area> ins) {
+  const int64_t ws = dtype_size(w.w_dtype), bits = w.index_bits / 8;
+  return any_meet(outs, {block(w.a, w.adapters * w.rank * w.k * ws), block(w.b, w.adapters * w.n * w.rank * ws),
+                         block(w.scale, w.adapters * 4), block(w.offsets, (w.segments + 1) * bits),
+                         block(w.index, w.segments * bits)}) ||
+         any_meet(outs, ins);
 }
 
 }  // namespace
@@ -514,7 +553,7 @@ int nvfp4_rms_norm(const void *x, int x_dtype, int64_t rows, int64_t cols, int64
   if (!matrix_ok(rows, cols, ldy)) return NVFP4_ERR_SHAPE;
   if (rows > 0 && !y) return NVFP4_ERR_NULL;
   if (!aligned(y, dtype_size(y_dtype))) return NVFP4_ERR_ALIGN;
-  if (rms_meets(a, y, ldy * dtype_size(y_dtype), cols * dtype_size(y_dtype))) return NVFP4_ERR_SHAPE;
+  if (rms_meets(a, matrix(y, y_dtype, rows, cols, ldy), Area{})) return NVFP4_ERR_SHAPE;
   return hip_status(nvfp4::launch_rms_norm(a, y, y_dtype, ldy, (hipStream_t)hip_stream));
 }
 
@@ -528,7 +567,7 @@ int mxfp8_rms_norm(const void *x, int x_dtype, int64_t rows, int64_t cols, int64
   if (cols % 32 != 0 || out->outer != rows || out->k != cols) return NVFP4_ERR_SHAPE;
   if (rows > 0 && (!out->codes || !out->scales)) return NVFP4_ERR_NULL;
   if (!aligned(out->codes, 16)) return NVFP4_ERR_ALIGN;
-  if (rms_meets(a, out->codes, cols, cols) || rms_meets(a, out->scales, cols / 32, cols / 32)) return NVFP4_ERR_SHAPE;
+  if (rms_meets(a, block(out->codes, rows * cols), block(out->scales, rows * (cols / 32)))) return NVFP4_ERR_SHAPE;
   return hip_status(nvfp4::launch_rms_norm_mx8(a, out->codes, out->scales, (hipStream_t)hip_stream));
 }
 
@@ -553,10 +592,9 @@ int nvfp4_rms_norm_backward(const void *dy, int dy_dtype, int64_t lddy, const vo
       !aligned(dh, dtype_size(h_dtype)) || !aligned(weight, dtype_size(w_dtype)) ||
       !aligned(dweight, dtype_size(g_dtype)) || !aligned(rstd, 4) || !aligned(workspace, 16))
     return NVFP4_ERR_ALIGN;
-  const int64_t hs = dtype_size(h_dtype), ds = dtype_size(dy_dtype);
-  if (overlap(dy, lddy * ds, cols * ds, dx, lddx * hs, cols * hs, rows) ||
-      overlap(h, ldh * hs, cols * hs, dx, lddx * hs, cols * hs, rows) ||
-      (dh && overlap(dh, lddh * hs, cols * hs, dx, lddx * hs, cols * hs, rows)))
+  if (any_meet({matrix(dx, h_dtype, rows, cols, lddx), block(dweight, cols * dtype_size(g_dtype))},
+               {matrix(dy, dy_dtype, rows, cols, lddy), matrix(h, h_dtype, rows, cols, ldh),
+                matrix(dh, h_dtype, rows, cols, lddh), block(rstd, rows * 4), block(weight, cols * dtype_size(w_dtype))}))
     return NVFP4_ERR_SHAPE;
   return hip_status(nvfp4::launch_rms_norm_backward({dy, dy_dtype, lddy, h, h_dtype, rows, cols, ldh, rstd, weight,
                                                      w_dtype, dh, lddh, dx, lddx, dweight, g_dtype, workspace},
@@ -637,12 +675,12 @@ int nvfp4_grouped_wgrad(const void *dy, int dy_dtype, int64_t lddy, const void *
       nvfp4::grouped_wgrad_workspace_bytes(experts, n, k, rows, dy_dtype == NVFP4_F32, x_dtype == NVFP4_F32);
   if (workspace_bytes < need) return NVFP4_ERR_SHAPE;
   if (need > 0 && !workspace) return NVFP4_ERR_NULL;
-  const int64_t ds = dtype_size(dy_dtype), xs = dtype_size(x_dtype), ws = dtype_size(dw_dtype);
-  if (!aligned(dy, ds) || !aligned(x, xs) || !aligned(dw, ws) || !aligned(offsets, index_bits / 8) ||
-      !aligned(workspace, 16))
+  const int64_t ws = dtype_size(dw_dtype);
+  if (!aligned(dy, dtype_size(dy_dtype)) || !aligned(x, dtype_size(x_dtype)) || !aligned(dw, ws) ||
+      !aligned(offsets, index_bits / 8) || !aligned(workspace, 16))
     return NVFP4_ERR_ALIGN;
-  if (ranges_meet(dy, span(rows, lddy, n, ds), dw, experts * n * k * ws) ||
-      ranges_meet(x, span(rows, ldx, k, xs), dw, experts * n * k * ws))
+  if (any_meet({block(dw, experts * n * k * ws)},
+               {matrix(dy, dy_dtype, rows, n, lddy), matrix(x, x_dtype, rows, k, ldx)}))
     return NVFP4_ERR_SHAPE;
   return hip_status(nvfp4::launch_grouped_wgrad({experts, n, k, dy, dy_dtype, lddy, x, x_dtype, rows, ldx, offsets,
                                                  index_bits, dw, dw_dtype, workspace},
@@ -661,12 +699,10 @@ int nvfp4_adapters(const void *x, int x_dtype, int64_t rows, int64_t k, int64_t 
   st = check_base(base, base_dtype, ldb, y, y_dtype, ldy, rows, n);
   if (st != NVFP4_OK) return st;
   if (rows > 0 && (!u || (k > 0 && !x))) return NVFP4_ERR_NULL;
-  const int64_t xs = dtype_size(x_dtype), ys = dtype_size(y_dtype);
-  if (!aligned(x, xs) || !aligned(u, 4)) return NVFP4_ERR_ALIGN;
-  if (overlap(x, ldx * xs, k * xs, y, ldy * ys, n * ys, rows) ||
-      ranges_meet(x, span(rows, ldx, k, xs), u, rows * rank * 4) ||
-      ranges_meet(y, span(rows, ldy, n, ys), u, rows * rank * 4) ||
-      (base && ranges_meet(base, span(rows, ldb, n, dtype_size(base_dtype)), u, rows * rank * 4)))
+  if (!aligned(x, dtype_size(x_dtype)) || !aligned(u, 4)) return NVFP4_ERR_ALIGN;
+  const Area au = block(u, rows * rank * 4);
+  if (adapters_meet(w, {matrix(y, y_dtype, rows, n, ldy), au}, {matrix(x, x_dtype, rows, k, ldx)}) ||
+      meet(au, matrix(base, base_dtype, rows, n, ldb)))
     return NVFP4_ERR_SHAPE;
   return hip_status(nvfp4::launch_adapters({w, x, x_dtype, rows, ldx, base, base_dtype, ldb, y, y_dtype, ldy, u},
                                            (hipStream_t)hip_stream));
@@ -698,22 +734,16 @@ int nvfp4_adapters_backward(const void *dy, int dy_dtype, int64_t lddy, const vo
   const int64_t need = nvfp4::adapters_backward_workspace_bytes(rows, n, k, rank, adapters, segments, w_dtype);
   if (workspace_bytes < need) return NVFP4_ERR_SHAPE;
   if (need > 0 && !workspace) return NVFP4_ERR_NULL;
-  const int64_t xs = dtype_size(x_dtype), ds = dtype_size(dy_dtype), os = dtype_size(dx_dtype), gs = dtype_size(g_dtype);
-  if (!aligned(x, xs) || !aligned(dy, ds) || !aligned(u, 4) || !aligned(da, gs) || !aligned(db, gs) ||
-      !aligned(workspace, 16))
+  const int64_t gs = dtype_size(g_dtype);
+  if (!aligned(x, dtype_size(x_dtype)) || !aligned(dy, dtype_size(dy_dtype)) || !aligned(u, 4) || !aligned(da, gs) ||
+      !aligned(db, gs) || !aligned(workspace, 16))
     return NVFP4_ERR_ALIGN;
-  if (overlap(x, ldx * xs, k * xs, dx, lddx * os, k * os, rows) ||
-      ranges_meet(dy, span(rows, lddy, n, ds), dx, span(rows, lddx, k, os)))
+  const Area ada = block(da, adapters * rank * k * gs), adb = block(db, adapters * rank * n * gs),
+             abase = matrix(base, base_dtype, rows, k, ldb);
+  if (adapters_meet(w, {matrix(dx, dx_dtype, rows, k, lddx), ada, adb},
+                    {matrix(x, x_dtype, rows, k, ldx), matrix(dy, dy_dtype, rows, n, lddy), block(u, rows * rank * 4)}) ||
+      any_meet({ada, adb}, {abase}))
     return NVFP4_ERR_SHAPE;
-  // the weights' gradients meet neither each other nor a matrix
-  const struct { const void *p; int64_t bytes; } out[] = {{da, adapters * rank * k * gs}, {db, adapters * rank * n * gs}},
-      in[] = {{x, span(rows, ldx, k, xs)}, {dy, span(rows, lddy, n, ds)}, {dx, span(rows, lddx, k, os)},
-              {u, rows * rank * 4}, {a, adapters * rank * k * (int64_t)dtype_size(w_dtype)},
-              {b, adapters * rank * n * (int64_t)dtype_size(w_dtype)}};
-  if (ranges_meet(da, out[0].bytes, db, out[1].bytes)) return NVFP4_ERR_SHAPE;
-  for (const auto &o : out)
-    for (const auto &i : in)
-      if (ranges_meet(o.p, o.bytes, i.p, i.bytes)) return NVFP4_ERR_SHAPE;
   return hip_status(nvfp4::launch_adapters_backward({w, dy, dy_dtype, lddy, x, x_dtype, rows, ldx, u, base, base_dtype,
                                                      ldb, dx, dx_dtype, lddx, da, db, g_dtype, workspace},
                                                     (hipStream_t)hip_stream));

@@ -467,8 +467,9 @@ int mxfp8_rms_norm(const void *x, int x_dtype, int64_t rows, int64_t cols, int64
  *              residual alike.
  *  dh        : the gradient that reaches h from the residual stream, h_dtype,
  *              row-major [rows][lddh], or NULL (0).
- *  dx        : must not overlap dy, h or dh (NVFP4_ERR_SHAPE).
- *  dweight   : may be NULL; zeros when rows == 0.
+ *  dx, dweight : must not overlap inputs or each other (NVFP4_ERR_SHAPE; rows
+ *              of dx may lie in the gaps of dy, h or dh).  dweight may be
+ *              NULL; zeros when rows == 0.
  *  workspace : device, at least nvfp4_rms_norm_backward_workspace_bytes
  *              (rows, cols) bytes (0 for a few rows, NULL then allowed),
  *              16-byte aligned, contents ignored and overwritten; calls that
@@ -598,11 +599,12 @@ int64_t nvfp4_grouped_wgrad_workspace_bytes(int64_t experts, int64_t n, int64_t 
  *  base    : device, row-major [rows][ldb], base_dtype, or NULL (zeros).
  *  y       : device, row-major [rows][ldy], y_dtype, written whole: rows
  *            without an adapter (those of no segment too) are base.  May be
- *            `base` itself (same pointer, type and leading dimension); must
- *            not overlap it otherwise, nor x (NVFP4_ERR_SHAPE).
+ *            `base` itself (same pointer, type and leading dimension).
  *  u       : device, f32 [rows][rank], written whole (zeros without an
  *            adapter), for the backward pass.
  *  ceil(max(n, k) / 256) * (rows / 16 + min(segments + 2, rows)) <= 2^24 - 8.
+ * Outputs must not overlap inputs or each other (NVFP4_ERR_SHAPE), but for y
+ * in base's place.
  * bf16 operands enter the products exactly; a product of two float32 values
  * is off by at most 2^-23 of its magnitude, and one with an infinity infinite
  * or NaN.  Sums are binary32.  Deterministic.  Enqueues two kernels.

@@ -248,6 +248,101 @@ def test_adapters_backward_workspace(L):
     assert _call(L.nvfp4_adapters_backward, ADAPT_BACK, bytes=need) == HIP
 
 
+# ----------------------------------------------- outputs that meet something
+
+APART = {
+    "rms": (RMS, dict(y="x res h w rstd", h="x w", rstd="x res h w y")),
+    "rms_back": (dict(RMS_BACK, rstd=6 * FAKE, w=7 * FAKE, ws=8 * FAKE),
+                 dict(dx="dy h dh rstd w dw", dw="dy h dh rstd w dx")),
+    "adapters": (dict(ADAPT, scale=7 * FAKE, off=8 * FAKE, index=9 * FAKE),
+                 dict(y="x a b scale off index u", u="x a b scale off index base y")),
+    "adapters_back": (dict(ADAPT_BACK, scale=10 * FAKE, off=11 * FAKE, index=12 * FAKE, ws=13 * FAKE),
+                      dict(dx="dy x u a b scale off index da db", da="dy x u a b scale off index base dx db",
+                           db="dy x u a b scale off index base dx da")),
+}
+CALLS = {"rms": "nvfp4_rms_norm", "rms_back": "nvfp4_rms_norm_backward", "adapters": "nvfp4_adapters",
+         "adapters_back": "nvfp4_adapters_backward"}
+
+
+@_no_gpu
+@pytest.mark.parametrize("which,out,other", [(which, out, other) for which, (_, pairs) in APART.items()
+                                             for out, others in pairs.items() for other in others.split()])
+def test_outputs_do_not_meet(L, which, out, other):
+    """Each output at another argument's place, and 8 bytes in front of it; with
+    all of them a megabyte apart the call gets as far as its launch."""
+    good = APART[which][0]
+    fn = getattr(L, CALLS[which])
+    assert _call(fn, good) == HIP
+    assert _call(fn, good, **{out: good[other]}) == SHAPE
+    assert _call(fn, good, **{out: good[other] - 8}) == SHAPE
+
+
+@_no_gpu
+@pytest.mark.parametrize("other", ["x", "res", "h", "w", "rstd"])
+@pytest.mark.parametrize("out", ["codes", "scales"])
+def test_mx8_outputs_do_not_meet(L, out, other):
+    good = {**RMS, "w": 8 * FAKE, "rstd": 6 * FAKE}
+    args = [v for k, v in good.items() if k not in ("y", "yd", "ldy", "rstd", "stream")]
+    call = lambda **t: L.mxfp8_rms_norm(*args, ctypes.byref(_mx8(**t)), good["rstd"], None)
+    assert call() == HIP
+    assert call(**{out: good[other]}) == SHAPE
+    assert call(codes=4 * FAKE, scales=4 * FAKE + 255) == SHAPE and call(codes=4 * FAKE, scales=4 * FAKE + 256) == HIP
+    assert call(codes=4 * FAKE, scales=4 * FAKE - 7) == SHAPE and call(codes=4 * FAKE, scales=4 * FAKE - 8) == HIP
+
+
+@_no_gpu
+@pytest.mark.parametrize("rows", [1, 2, 4])
+@pytest.mark.parametrize("ld", [4, 9, 40])
+def test_a_block_in_the_gaps_of_a_matrix(L, rows, ld):
+    """u (a block of rows * rank * 4 bytes) at every place around dx [rows][ld]
+    of 4 float32 columns: refused where elements meet, and there alone."""
+    k, rank = 4, 3
+    dx = {FAKE + 4 * (r * ld + c) for r in range(rows) for c in range(k)}
+    good = dict(ADAPT_BACK, rows=rows, k=k, ldx=k, rank=rank, n=2, lddy=2, dyd=0, xd=0, base=None, dx=FAKE, dxd=0, lddx=ld,
+                a=20 * FAKE, b=21 * FAKE, scale=None, off=22 * FAKE, index=23 * FAKE, ws=24 * FAKE)
+    for shift in range(-4 * (rows * rank + 2), 4 * (rows * ld + 2), 4):
+        u = {FAKE + shift + 4 * i for i in range(rows * rank)}
+        assert _call(L.nvfp4_adapters_backward, good, u=FAKE + shift) == (SHAPE if u & dx else HIP), shift
+
+
+@_no_gpu
+@pytest.mark.parametrize("rows", [1, 3])
+def test_matrices_side_by_side(L, rows):
+    """y against h, and dx against dy, in one buffer: refused where elements
+    meet (of two pitches, where the whole ranges do)."""
+    cols = 5
+    for ldh, ldy in ((5, 5), (12, 12), (12, 9)):
+        at = lambda p, ld: {p + 4 * (r * ld + c) for r in range(rows) for c in range(cols)}
+        for shift in range(-4 * 40, 4 * 40, 4):
+            meets = bool(at(FAKE, ldh) & at(FAKE + shift, ldy))
+            fwd = _call(L.nvfp4_rms_norm, RMS, rows=rows, cols=cols, ldx=cols, x=9 * FAKE, w=None, ldr=cols, h=FAKE, ldh=ldh,
+                        y=FAKE + shift, yd=0, ldy=ldy)
+            back = _call(L.nvfp4_rms_norm_backward, RMS_BACK, rows=rows, cols=cols, rstd=6 * FAKE, w=None, hd=0, ldh=cols,
+                         dh=None, dy=FAKE, dyd=0, lddy=ldh, dx=FAKE + shift, lddx=ldy)
+            for got in (fwd, back):
+                if meets or ldh == ldy:
+                    assert got == (SHAPE if meets else HIP), (ldh, ldy, shift)
+                else:
+                    assert got in (SHAPE, HIP)
+
+
+@pytest.mark.gpu
+def test_gradients_in_the_place_of_u_are_refused():
+    x, dy = torch.randn((6, 8), device="cuda"), torch.randn((6, 40), device="cuda")
+    a, b = torch.randn((2, 8, 8), device="cuda"), torch.randn((2, 40, 8), device="cuda")
+    off, index = torch.tensor([0, 4, 6], device="cuda"), torch.tensor([1, 0], device="cuda")
+    y, u = nv.nvfp4_adapters(x, a, b, off, index)
+    with pytest.raises(nv.NVFP4Error, match="shape"):
+        nv.nvfp4_adapters_backward(dy, x, u, a, b, off, index, out=u)
+    with pytest.raises(nv.NVFP4Error, match="shape"):
+        nv.nvfp4_adapters(x, a, b, off, index, out=b.view(-1)[:240].view(6, 40))
+    wide = torch.zeros((6, 100), device="cuda")
+    wide[:, 60:] = dy                                          # dx beside dy in one buffer
+    want = nv.nvfp4_adapters_backward(dy, x, u, a, b, off, index)
+    got = nv.nvfp4_adapters_backward(wide[:, 60:], x, u, a, b, off, index, out=wide[:, 3:11])
+    assert all(torch.equal(p, q) for p, q in zip(got, want)) and torch.equal(wide[:, 60:], dy)
+
+
 # ------------------------------------------------------- binding and modules
 
 
