@@ -12,7 +12,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import NVFP4Error, nvfp4_adapters, nvfp4_adapters_backward
-from .capture import note_leaves
+from .capture import LeafFunction
 
 
 def _rows(t: torch.Tensor) -> torch.Tensor:
@@ -20,12 +20,11 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
     return t.contiguous() if t.stride(1) != 1 or t.stride(0) < t.shape[1] else t
 
 
-class AdaptersFunction(torch.autograd.Function):
+class AdaptersFunction(LeafFunction):
     """y [tokens, out] of x [tokens, in] and base [tokens, out] (or None)."""
 
     @staticmethod
     def forward(ctx, x, a, b, base, scale, offsets, index):
-        note_leaves(ctx, x, a, b, base)
         x, a, b = _rows(x), a.contiguous(), b.contiguous()
         offsets, index = offsets.contiguous(), index.contiguous()
         y, u = nvfp4_adapters(x, a, b, offsets, index, scale, None if base is None else _rows(base))

@@ -16,7 +16,7 @@ from torch.autograd.function import once_differentiable
 
 from . import (NVFP4Error, NVFP4Tensor, nvfp4_grouped_matmul, nvfp4_grouped_wgrad, nvfp4_quantize,
                nvfp4_quantize_dual)
-from .capture import note_leaves
+from .capture import LeafFunction
 from .head import RMSNorm, _matrix
 
 
@@ -32,13 +32,12 @@ def group_by_expert(choice: torch.Tensor, experts: int):
     return order, offsets
 
 
-class NVFP4ExpertsFunction(torch.autograd.Function):
+class NVFP4ExpertsFunction(LeafFunction):
     """y [rows, out] of grouped rows x [rows, in], W [experts, out, in]; rows
     of no group are zeros."""
 
     @staticmethod
     def forward(ctx, x, weight, offsets):
-        note_leaves(ctx, x, weight)
         x, offsets = _matrix(x), offsets.contiguous()
         stack = weight.contiguous().reshape(-1, weight.shape[2])
         ctx.qw0 = None

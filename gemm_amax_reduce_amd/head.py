@@ -23,7 +23,7 @@ from . import (NVFP4Error, NVFP4Tensor, nvfp4_distill_topk, nvfp4_distill_topk_b
                nvfp4_layer_norm, nvfp4_layer_norm_backward, nvfp4_matvec, nvfp4_quantize, nvfp4_quantize_amax,
                nvfp4_rms_norm, nvfp4_rms_norm_backward)
 from .adapters import LowRankAdapters
-from .capture import note_leaves
+from .capture import LeafFunction
 from .linear import NVFP4Linear
 
 # Up to this many rows are answered by the matrix-vector form, which reads
@@ -60,13 +60,12 @@ class LayerNormFunction(torch.autograd.Function):
         return dx, dw if weight is not None else None, db if ctx.has_bias else None, None
 
 
-class RMSNormFunction(torch.autograd.Function):
+class RMSNormFunction(LeafFunction):
     """y = RMS norm of the rows of x [tokens, features] in x's dtype, or with a
     residual (y, h) of h = x + residual, in the residual's dtype."""
 
     @staticmethod
     def forward(ctx, x, residual, weight, eps: float):
-        note_leaves(ctx, x, residual, weight)
         x = _matrix(x)
         ctx.x_dtype, ctx.has_residual = x.dtype, residual is not None
         if residual is None:

@@ -1,0 +1,60 @@
+"""The guard of captured autograd functions, on the CPU: a stand-in function, and
+a flag in the place of the stream's state."""
+import pytest
+import torch
+
+import gemm_amax_reduce_amd as nv
+from gemm_amax_reduce_amd import capture
+
+
+class Twice(capture.LeafFunction):
+    @staticmethod
+    def forward(ctx, x, w):
+        return x * w
+
+    @staticmethod
+    def backward(ctx, dy):
+        return dy, dy
+
+
+@pytest.fixture
+def capturing(monkeypatch):
+    flag = [False]
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: flag[0])
+    return flag
+
+
+def test_beside_an_eager_graph(capturing):
+    x, w = torch.ones(3, requires_grad=True), torch.ones(3, requires_grad=True)
+    alive = Twice.apply(x, w)
+    capturing[0] = True
+    with pytest.raises(nv.NVFP4Error, match="still lives"):
+        Twice.apply(torch.ones(3), w)
+    with pytest.raises(nv.NVFP4Error, match="still lives"):
+        Twice.apply(x.view(3, 1), torch.ones(3, 1))
+    other = torch.ones(3, requires_grad=True)
+    Twice.apply(torch.ones(3), other)                              # another leaf
+    del alive
+    y = Twice.apply(x, w)
+    y.sum().backward()
+    assert torch.equal(x.grad, torch.ones(3))
+
+
+def test_without_gradients(capturing):
+    """Parameters need gradients, but no node is recorded."""
+    x, w = torch.ones(3, requires_grad=True), torch.ones(3, requires_grad=True)
+    alive = Twice.apply(x, w)
+    capturing[0] = True
+    with torch.no_grad():
+        assert not Twice.apply(x, w).requires_grad
+    with torch.inference_mode():
+        Twice.apply(x, w)
+    assert not Twice.apply(x.detach(), w.detach()).requires_grad
+    capturing[0] = False
+    with torch.no_grad():
+        quiet = Twice.apply(x, w)
+    del alive
+    capturing[0] = True
+    Twice.apply(x, w)                                              # no graph is left beside
+    assert quiet.grad_fn is None

@@ -348,3 +348,39 @@ def test_capture_beside_an_eager_graph_is_refused():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(grad, nv.nvfp4_grouped_wgrad(torch.ones_like(y), x, offsets, torch.bfloat16))
+
+
+def test_answers_are_captured_beside_an_eager_graph():
+    """Without gradients no node is recorded, and a training output may live on."""
+    torch.manual_seed(8)
+    block = E.NVFP4ExpertBlock(4, 2, 64, 64, device="cuda")
+    low = LowRankAdapters(2, 64, 64, 4, device="cuda")
+    torch.nn.init.normal_(low.b)
+    x, r = (torch.randn((24, 64), device="cuda", dtype=torch.bfloat16).requires_grad_(True) for _ in range(2))
+    offsets, index = torch.tensor([0, 10, 24], device="cuda"), torch.tensor([1, 0], device="cuda")
+    at = torch.tensor([0, 5, 9, 20, 24], device="cuda")
+
+    def run(packed=None):
+        n, h = block.norm(x, r)
+        return [low(n, h, offsets, index), block.up(n, at, packed)]
+
+    alive = run()                                                  # an eager graph of every parameter
+    packed = block.pack()
+    with torch.no_grad():
+        want = run(packed[0])
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            run(packed[0])
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = run(packed[0])
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+        with torch.no_grad():
+            x.copy_(torch.randn_like(x))
+            want = run(packed[0])
+    assert all(t.grad_fn is not None for t in alive)
