@@ -413,17 +413,27 @@ def nvfp4_gemm(a: NVFP4Tensor, b: NVFP4Tensor, out_dtype=torch.float32, out: tor
 _workspaces: dict = {}
 
 
+
+
 def gemm_workspace(device=None, stream=None) -> torch.Tensor:
     """The split-tail GEMM workspace for one (device, stream): allocated
     zero-filled on first use and kept (the kernel leaves it zero-filled).
     Calls on one stream run in order, so a workspace per stream is never
     used by two calls at once."""
     device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if stream is not None:
+        with torch.cuda.stream(stream):          # its memory and its clearing are that stream's
+            return _stream_workspace(device, stream)
+    with torch.cuda.device(device):
+        return _stream_workspace(device, torch.cuda.current_stream(device))
+
+
+def _stream_workspace(device, s) -> torch.Tensor:
+    size = int(lib().nvfp4_gemm_workspace_bytes())
     key = (device, int(s.cuda_stream))
     ws = _workspaces.get(key)
     if ws is None:
-        ws = torch.zeros(int(lib().nvfp4_gemm_workspace_bytes()), dtype=torch.uint8, device=device)
+        ws = torch.zeros(size, dtype=torch.uint8, device=device)
         _workspaces[key] = ws
     return ws
 
