@@ -413,13 +413,17 @@ def nvfp4_gemm(a: NVFP4Tensor, b: NVFP4Tensor, out_dtype=torch.float32, out: tor
 _workspaces: dict = {}
 
 
+# of it, what the kernel needs zero-filled (its flags)
+_WORKSPACE_FLAGS = 1 << 16
 
 
 def gemm_workspace(device=None, stream=None) -> torch.Tensor:
     """The split-tail GEMM workspace for one (device, stream): allocated
     zero-filled on first use and kept (the kernel leaves it zero-filled).
     Calls on one stream run in order, so a workspace per stream is never
-    used by two calls at once."""
+    used by two calls at once.  Under capture it is a new one, its flags
+    cleared by the graph itself, and is not kept: graphs captured on one stream
+    may be replayed in any order, on any streams."""
     device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     if stream is not None:
         with torch.cuda.stream(stream):          # its memory and its clearing are that stream's
@@ -430,6 +434,10 @@ def gemm_workspace(device=None, stream=None) -> torch.Tensor:
 
 def _stream_workspace(device, s) -> torch.Tensor:
     size = int(lib().nvfp4_gemm_workspace_bytes())
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(size, dtype=torch.uint8, device=device)
+        ws[:_WORKSPACE_FLAGS].zero_()
+        return ws
     key = (device, int(s.cuda_stream))
     ws = _workspaces.get(key)
     if ws is None:

@@ -1,11 +1,39 @@
 """The workspace that nvfp4_gemm_ws takes by itself: one for each stream, cleared
-in that stream's order."""
+in that stream's order, and one of its own for every captured call."""
 import pytest
 import torch
 
 import gemm_amax_reduce_amd as nv
 
 pytestmark = pytest.mark.gpu
+
+
+def test_captured_graphs_share_none():
+    """Neither a graph whose clearing is only captured, nor two graphs, may
+    leave theirs to another call."""
+    a, b = (nv.nvfp4_quantize(torch.randn((n, 128), device="cuda")) for n in (300, 200))
+    want = nv.nvfp4_gemm_ws(a, b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    before = {k: v.data_ptr() for k, v in nv._workspaces.items()}
+    held, graphs, outs = [], [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            held.append(nv.gemm_workspace())
+            outs.append(nv.nvfp4_gemm_ws(a, b))
+        graphs.append(graph)
+    assert {k: v.data_ptr() for k, v in nv._workspaces.items()} == before
+    assert len({t.data_ptr() for t in held} | set(before.values())) == 2 + len(set(before.values()))
+    for _ in range(3):
+        for graph, out in zip(graphs[::-1], outs[::-1]):
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+            assert torch.equal(nv.nvfp4_gemm_ws(a, b), want)
+    for t in held:
+        assert torch.all(t[:1 << 16] == 0)
 
 
 def test_cleared_in_its_streams_order():
