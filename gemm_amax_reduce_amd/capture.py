@@ -6,7 +6,9 @@ the stream of the first.  A backward pass captured while an eager graph of the
 same leaf lives would make the captured stream wait for that other stream, and
 the process ends inside autograd's worker thread.  So each function here notes
 its node and the leaves that it starts from, and refuses to be captured beside
-an eager one.  Without gradients no node is recorded, and nothing is refused.
+an eager one: some at once, others, whose forward pass alone may be captured
+there, in their backward pass.  Without gradients no node is recorded, and
+nothing is refused.
 """
 from __future__ import annotations
 
@@ -29,10 +31,28 @@ def _leaves(args):
     return [t for t in tensors if t.is_leaf and t.requires_grad]
 
 
+def _lives_beside(leaves) -> bool:
+    """Whether a node noted outside a capture still lives at one of them."""
+    return any(t is noted() for node in list(_eager) for noted in node.leaves for t in leaves)
+
+
+def _refuse():
+    raise NVFP4Error("a graph of this parameter or input, made outside the capture, still lives: delete its outputs "
+                     "before the capture")
+
+
+def refuse_beside(ctx) -> None:
+    """For the backward pass of a LateLeafFunction."""
+    if getattr(ctx, "beside", False) and _capturing():
+        _refuse()
+
+
 class LeafFunction(torch.autograd.Function):
     """An autograd function whose nodes are noted; under capture, apply raises
     NVFP4Error if a node noted outside a capture still lives at a leaf of the
     call's."""
+
+    late = False
 
     @classmethod
     def apply(cls, *args):
@@ -41,15 +61,24 @@ class LeafFunction(torch.autograd.Function):
         leaves = _leaves(args) if torch.is_grad_enabled() else []
         if not leaves:
             return super().apply(*args)
-        if _capturing():
-            for node in list(_eager):
-                noted = [leaf() for leaf in node.leaves]
-                if any(t is leaf for t in leaves for leaf in noted):
-                    raise NVFP4Error("a graph of this parameter or input, made outside the capture, still lives: "
-                                     "delete its outputs before the capture")
-            return super().apply(*args)
+        capturing = _capturing()
+        beside = capturing and _lives_beside(leaves)
+        if beside and not cls.late:
+            _refuse()
         out = super().apply(*args)
         node = (out[0] if isinstance(out, tuple) else out).grad_fn
-        node.leaves = [weakref.ref(t) for t in leaves]
-        _eager.add(node)
+        if capturing:
+            # (the accumulator stays the eager graph's, also where that is gone by
+            # the backward pass: this graph holds it)
+            node.beside = beside
+        else:
+            node.leaves = [weakref.ref(t) for t in leaves]
+            _eager.add(node)
         return out
+
+
+class LateLeafFunction(LeafFunction):
+    """The same for a function whose forward pass may be captured beside an eager
+    graph; its backward pass begins with refuse_beside."""
+
+    late = True

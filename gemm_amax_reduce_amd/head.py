@@ -23,7 +23,7 @@ from . import (NVFP4Error, NVFP4Tensor, nvfp4_distill_topk, nvfp4_distill_topk_b
                nvfp4_layer_norm, nvfp4_layer_norm_backward, nvfp4_matvec, nvfp4_quantize, nvfp4_quantize_amax,
                nvfp4_rms_norm, nvfp4_rms_norm_backward)
 from .adapters import LowRankAdapters
-from .capture import LeafFunction
+from .capture import LateLeafFunction, LeafFunction, refuse_beside
 from .linear import NVFP4Linear
 
 # Up to this many rows are answered by the matrix-vector form, which reads
@@ -39,7 +39,7 @@ def _matrix(x: torch.Tensor) -> torch.Tensor:
     return x
 
 
-class LayerNormFunction(torch.autograd.Function):
+class LayerNormFunction(LateLeafFunction):
     """y = layer norm of the rows of x [tokens, features], in x's dtype."""
 
     @staticmethod
@@ -54,6 +54,7 @@ class LayerNormFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
+        refuse_beside(ctx)
         x, mean, rstd, weight = ctx.saved_tensors
         grad_dtype = weight.dtype if weight is not None else ctx.bias_dtype or torch.float32
         dx, dw, db = nvfp4_layer_norm_backward(dy.contiguous(), x, mean, rstd, weight, grad_dtype=grad_dtype)
@@ -86,7 +87,7 @@ class RMSNormFunction(LeafFunction):
         return (dx.to(ctx.x_dtype), dx if ctx.has_residual else None, dw if weight is not None else None, None)
 
 
-class DistillTopKFunction(torch.autograd.Function):
+class DistillTopKFunction(LateLeafFunction):
     """Per-token distillation losses [tokens] of logits [tokens, vocab]; the
     gradient takes any upstream gradient of the losses."""
 
@@ -101,6 +102,7 @@ class DistillTopKFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dloss):
+        refuse_beside(ctx)
         logits, indices, teacher, lse = ctx.saved_tensors
         dz = nvfp4_distill_topk_backward(logits, indices, teacher, lse, dloss.contiguous(),
                                          temperature=ctx.temperature)

@@ -25,13 +25,14 @@ from __future__ import annotations
 import torch
 
 from . import (nvfp4_gemm_ws, nvfp4_quantize, nvfp4_quantize_dual, NVFP4Error)
+from .capture import LateLeafFunction, refuse_beside
 
 
 def _out_dtype(t: torch.Tensor) -> torch.dtype:
     return torch.bfloat16 if t.dtype == torch.bfloat16 else torch.float32
 
 
-class NVFP4LinearFunction(torch.autograd.Function):
+class NVFP4LinearFunction(LateLeafFunction):
     """y = x W^T for x [tokens, in], W [out, in]; returns y in x's dtype."""
 
     @staticmethod
@@ -62,6 +63,7 @@ class NVFP4LinearFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
+        refuse_beside(ctx)
         dy = dy.contiguous().to(ctx.x_dtype)
         # dy along its columns (data gradient) and, transformed, along its
         # rows (weight gradient); distinct Philox offsets keep the two draws

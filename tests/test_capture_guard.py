@@ -17,6 +17,17 @@ class Twice(capture.LeafFunction):
         return dy, dy
 
 
+class LateTwice(capture.LateLeafFunction):
+    @staticmethod
+    def forward(ctx, x, w):
+        return x * w
+
+    @staticmethod
+    def backward(ctx, dy):
+        capture.refuse_beside(ctx)
+        return dy, dy
+
+
 @pytest.fixture
 def capturing(monkeypatch):
     flag = [False]
@@ -58,3 +69,48 @@ def test_without_gradients(capturing):
     capturing[0] = True
     Twice.apply(x, w)                                              # no graph is left beside
     assert quiet.grad_fn is None
+
+
+def test_forward_alone_beside_an_eager_graph(capturing):
+    """The backward pass is what may not be captured there, and that holds when
+    the eager graph is gone by then."""
+    x, w = torch.ones(3, requires_grad=True), torch.ones(3, requires_grad=True)
+    alive = LateTwice.apply(x, w)
+    capturing[0] = True
+    y, again = LateTwice.apply(x, w), LateTwice.apply(x, w)
+    with pytest.raises(nv.NVFP4Error, match="still lives"):
+        y.sum().backward()
+    assert x.grad is None
+    del alive
+    with pytest.raises(nv.NVFP4Error, match="still lives"):
+        again.sum().backward()
+    capturing[0] = False
+    LateTwice.apply(x, w).sum().backward()
+    x.grad = w.grad = None
+    capturing[0] = True
+    LateTwice.apply(x, w).sum().backward()                         # no graph is left beside
+    assert torch.equal(x.grad, torch.ones(3))
+
+
+def test_either_function_sees_the_others_graph(capturing):
+    w = torch.ones(3, requires_grad=True)
+    alive = LateTwice.apply(torch.ones(3), w)
+    capturing[0] = True
+    with pytest.raises(nv.NVFP4Error, match="still lives"):
+        Twice.apply(torch.ones(3), w)
+    del alive
+    capturing[0] = False
+    alive = Twice.apply(torch.ones(3), w)
+    capturing[0] = True
+    y = LateTwice.apply(torch.ones(3), w)
+    with pytest.raises(nv.NVFP4Error, match="still lives"):
+        y.sum().backward()
+    assert alive.grad_fn is not None
+
+
+def test_functions_of_the_package():
+    from gemm_amax_reduce_amd import adapters, experts, head, linear
+    for function in (adapters.AdaptersFunction, experts.NVFP4ExpertsFunction, head.RMSNormFunction):
+        assert issubclass(function, capture.LeafFunction) and not function.late
+    for function in (head.LayerNormFunction, head.DistillTopKFunction, linear.NVFP4LinearFunction):
+        assert issubclass(function, capture.LateLeafFunction)

@@ -384,3 +384,62 @@ def test_answers_are_captured_beside_an_eager_graph():
             x.copy_(torch.randn_like(x))
             want = run(packed[0])
     assert all(t.grad_fn is not None for t in alive)
+
+
+@pytest.mark.parametrize("norm", ["layer", "rms"])
+def test_a_head_captured_beside_an_eager_graph(norm):
+    """Norm, 4-bit projection and loss: the forward pass is captured beside a
+    live eager graph (without the gradient of an RMS norm, which is refused at
+    once), the backward pass is refused until that is gone."""
+    torch.manual_seed(9)
+    head = H.NVFP4Head(64, 96, device="cuda", norm=norm)
+    head.proj.requires_grad_(False)                                # (its rounding draws anew in every call)
+    x = torch.randn((32, 64), device="cuda", dtype=torch.bfloat16, requires_grad=norm == "layer")
+    at, teacher = torch.randint(0, 96, (32, 4), device="cuda"), torch.randn((32, 4), device="cuda")
+    leaves = [head.norm.weight] + ([x] if norm == "layer" else [])
+
+    def forward():
+        return H.distill_topk_loss(head.proj(head.norm(x)), at, teacher)
+
+    alive = forward()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(nv.NVFP4Error, match="still lives"):
+        with torch.cuda.graph(graph):
+            loss = forward()
+            assert norm == "layer"
+            torch.autograd.grad(loss, leaves)
+    if norm == "layer":
+        del loss
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            loss = forward()
+        for _ in range(2):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(loss, alive)
+        del loss, graph
+    del alive
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        forward()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = torch.autograd.grad(forward(), leaves)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.isfinite(g).all() and g.abs().max() > 0 for g in got)
+
+
+def test_a_layer_captured_beside_the_graph_of_another():
+    """The eager graph is a layer norm's, the captured function an RMS norm of
+    the same x."""
+    x = torch.randn((8, 64), device="cuda", requires_grad=True)
+    layer, rms = H.LayerNorm(64, device="cuda", dtype=torch.float32), H.RMSNorm(64, device="cuda", dtype=torch.float32)
+    alive = layer(x)
+    with pytest.raises(nv.NVFP4Error, match="still lives"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            rms(x)
+    assert alive.grad_fn is not None
