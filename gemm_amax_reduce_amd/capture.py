@@ -12,6 +12,7 @@ nothing is refused.
 """
 from __future__ import annotations
 
+import threading
 import weakref
 
 import torch
@@ -19,6 +20,7 @@ import torch
 from . import NVFP4Error
 
 _eager = weakref.WeakSet()            # the nodes recorded outside a capture that still live
+_lock = threading.RLock()             # held by whoever adds to it or looks through it
 
 
 def _capturing() -> bool:
@@ -31,9 +33,17 @@ def _leaves(args):
     return [t for t in tensors if t.is_leaf and t.requires_grad]
 
 
+def _note(node, leaves) -> None:
+    node.leaves = [weakref.ref(t) for t in leaves]
+    with _lock:
+        _eager.add(node)
+
+
 def _lives_beside(leaves) -> bool:
     """Whether a node noted outside a capture still lives at one of them."""
-    return any(t is noted() for node in list(_eager) for noted in node.leaves for t in leaves)
+    with _lock:
+        nodes = list(_eager)
+    return any(t is noted() for node in nodes for noted in node.leaves for t in leaves)
 
 
 def _refuse():
@@ -72,8 +82,7 @@ class LeafFunction(torch.autograd.Function):
             # the backward pass: this graph holds it)
             node.beside = beside
         else:
-            node.leaves = [weakref.ref(t) for t in leaves]
-            _eager.add(node)
+            _note(node, leaves)
         return out
 
 

@@ -114,3 +114,37 @@ def test_functions_of_the_package():
         assert issubclass(function, capture.LeafFunction) and not function.late
     for function in (head.LayerNormFunction, head.DistillTopKFunction, linear.NVFP4LinearFunction):
         assert issubclass(function, capture.LateLeafFunction)
+
+
+def test_other_threads_record_meanwhile(capturing):
+    """A capture looks through the noted nodes while other threads add to them."""
+    import sys
+    import threading
+    w = torch.ones(3, requires_grad=True)
+    kept = [Twice.apply(torch.ones(3, requires_grad=True), torch.ones(3)) for _ in range(2000)]
+    stop, failed = threading.Event(), []
+
+    def record():
+        try:
+            while not stop.is_set():
+                capture._note(Node(), [w.detach()])
+        except Exception as e:
+            failed.append(e)
+
+    class Node:
+        pass
+
+    before = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    threads = [threading.Thread(target=record) for _ in range(3)]
+    try:
+        for t in threads:
+            t.start()
+        for _ in range(200):
+            assert not capture._lives_beside([w])
+    finally:
+        stop.set()
+        for t in threads:
+            t.join()
+        sys.setswitchinterval(before)
+    assert not failed and len(kept) == 2000
