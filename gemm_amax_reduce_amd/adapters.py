@@ -60,6 +60,15 @@ class LowRankAdapters(torch.nn.Module):
         torch.nn.init.normal_(self.a, std=in_features ** -0.5)
         self.register_buffer("scale", torch.full((adapters,), scale, device=device, dtype=torch.float32))
 
+    def _apply(self, fn, recurse=True):
+        # the kernels take the scales in float32: they follow the module to a
+        # device, but not to another type
+        scale = self.scale
+        super()._apply(fn, recurse)
+        if self.scale.dtype != torch.float32:
+            self.scale = scale.to(self.scale.device)
+        return self
+
     def forward(self, x, base, offsets, index):
         """base + the adapters' part of x [..., in]; base [..., out], or None
         for the part alone, in x's dtype."""

@@ -378,6 +378,19 @@ def test_modules_refuse_shapes():
             call()
 
 
+@pytest.mark.parametrize("convert", [lambda m: m.to(torch.bfloat16), lambda m: m.bfloat16().float(), lambda m: m.double(),
+                                     lambda m: torch.nn.Sequential(m).to("cpu", torch.bfloat16)[0]])
+def test_adapters_keep_their_scale_in_float32(convert):
+    low = LowRankAdapters(3, 32, 48, 4)
+    low.scale.copy_(torch.tensor([0.1, 1 / 3, 7.0]))
+    want = low.scale.clone()
+    out = convert(low)
+    assert out is low and low.scale.dtype == torch.float32 and torch.equal(low.scale, want)
+    assert "scale" in dict(low.named_buffers()) and torch.equal(low.state_dict()["scale"], want)
+    low.to("meta")
+    assert low.scale.is_meta and low.scale.dtype == torch.float32
+
+
 @pytest.mark.gpu
 def test_binding_refuses_bad_tensors():
     x = torch.zeros((4, 32), device="cuda")

@@ -184,6 +184,28 @@ def test_adapters_module(with_base):
                            base if with_base else torch.zeros_like(y))
 
 
+def test_adapters_converted_to_another_type():
+    """A module made in float32 and brought to bf16 (beside a head that is, too)
+    is the one made in bf16: forward, gradients, and the part added in place."""
+    torch.manual_seed(10)
+    low = LowRankAdapters(2, 64, 96, 8, scale=0.3)                 # on the CPU
+    torch.nn.init.normal_(low.b)
+    same = LowRankAdapters(2, 64, 96, 8, scale=0.3, device="cuda")
+    with torch.no_grad():
+        same.a.copy_(low.a), same.b.copy_(low.b)
+    low.cuda().to(torch.bfloat16)
+    offsets, index = torch.tensor([0, 5, 20], device="cuda"), torch.tensor([1, 0], device="cuda")
+    x = torch.randn((20, 64), device="cuda", dtype=torch.bfloat16)
+    base = torch.randn((20, 96), device="cuda", dtype=torch.bfloat16)
+    ys = []
+    for m in (low, same):
+        y = m(x, base, offsets, index)
+        y.sum().backward()
+        ys.append(y)
+        assert torch.equal(m.add(x, base.clone(), offsets, index), y)
+    assert torch.equal(*ys) and torch.equal(low.a.grad, same.a.grad) and torch.equal(low.b.grad, same.b.grad)
+
+
 @pytest.mark.parametrize("tokens", [0, 1, 16, 17, 48])
 @pytest.mark.parametrize("norm", ["layer", "rms"])
 def test_answers_with_adapters(tokens, norm):
