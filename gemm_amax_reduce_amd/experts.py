@@ -14,9 +14,9 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (NVFP4Error, NVFP4Tensor, nvfp4_grouped_matmul, nvfp4_grouped_wgrad, nvfp4_quantize,
-               nvfp4_quantize_dual)
-from .capture import LeafFunction
+from . import (NVFP4Error, NVFP4Tensor, nvfp4_dequantize, nvfp4_grouped_matmul, nvfp4_grouped_wgrad,
+               nvfp4_quantize, nvfp4_quantize_dual)
+from .capture import LateLeafFunction, LeafFunction, refuse_beside
 from .head import RMSNorm, _matrix
 
 
@@ -62,6 +62,28 @@ class NVFP4ExpertsFunction(LeafFunction):
         return dx, dw, None
 
 
+class PackedExpertsFunction(LateLeafFunction):
+    """The same with weights that are packed already, and frozen: x alone gets a
+    gradient, from their decoded values quantized along the other axis, in
+    every backward pass (a stack kept in both layouts would take twice the
+    memory that packing is for)."""
+
+    @staticmethod
+    def forward(ctx, x, packed, offsets):
+        offsets = offsets.contiguous()
+        ctx.save_for_backward(offsets, packed.codes, packed.scales, packed.meta)
+        ctx.outer, ctx.k = packed.outer, packed.k
+        return nvfp4_grouped_matmul(packed, _matrix(x), offsets)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        refuse_beside(ctx)
+        offsets, codes, scales, meta = ctx.saved_tensors
+        stack = nvfp4_dequantize(NVFP4Tensor(codes, scales, meta, ctx.outer, ctx.k))
+        return nvfp4_grouped_matmul(nvfp4_quantize(stack, axis=0), _matrix(dy), offsets, transposed=True), None, None
+
+
 class NVFP4Experts(torch.nn.Module):
     """Bias-free linear layers of several experts on rows grouped by expert,
     weights [experts, out, in] in NVFP4 (see group_by_expert)."""
@@ -75,13 +97,13 @@ class NVFP4Experts(torch.nn.Module):
 
     def forward(self, x, offsets, packed: NVFP4Tensor | None = None):
         """x [rows, in] -> [rows, out].  With `packed` (from pack), those
-        weights are used and no gradient is taken."""
+        weights are used, and x alone gets a gradient."""
         if x.dim() != 2 or x.shape[1] != self.weight.shape[2]:
             raise NVFP4Error(f"x must be [rows, {self.weight.shape[2]}], got shape {tuple(x.shape)}")
         if offsets.dim() != 1 or offsets.shape[0] != self.weight.shape[0] + 1:
             raise NVFP4Error(f"offsets must have {self.weight.shape[0] + 1} entries, got shape {tuple(offsets.shape)}")
         if packed is not None:
-            return nvfp4_grouped_matmul(packed, _matrix(x.detach()), offsets)
+            return PackedExpertsFunction.apply(x, packed, offsets)
         return NVFP4ExpertsFunction.apply(x, self.weight, offsets)
 
     @torch.no_grad()
@@ -114,7 +136,7 @@ class NVFP4ExpertBlock(torch.nn.Module):
 
     def forward(self, x, residual, packed=None):
         """x, residual [..., features] -> (y, h).  packed: from pack, for
-        answers without gradients of the experts."""
+        answers, or training around frozen experts."""
         lead, experts = x.shape[:-1], self.router.shape[0]
         n, h = self.norm(x, residual)
         rows = n.reshape(-1, n.shape[-1])

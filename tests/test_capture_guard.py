@@ -112,7 +112,8 @@ def test_functions_of_the_package():
     from gemm_amax_reduce_amd import adapters, experts, head, linear
     for function in (adapters.AdaptersFunction, experts.NVFP4ExpertsFunction, head.RMSNormFunction):
         assert issubclass(function, capture.LeafFunction) and not function.late
-    for function in (head.LayerNormFunction, head.DistillTopKFunction, linear.NVFP4LinearFunction):
+    for function in (head.LayerNormFunction, head.DistillTopKFunction, linear.NVFP4LinearFunction,
+                     experts.PackedExpertsFunction):
         assert issubclass(function, capture.LateLeafFunction)
 
 

@@ -128,6 +128,63 @@ def test_experts_module(sizes, dtype):
     assert torch.equal(layer(x, offsets, layer.pack()), y.detach())
 
 
+@pytest.mark.parametrize("sizes", [[3, 0, 1, 9], [200, 0, 31, 90], [0, 0, 0, 0]])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_packed_experts_pass_the_gradient_on(sizes, dtype):
+    """dx against the packed weights in the data gradient's layout (their decoded
+    values quantized along N), the weights themselves left alone; rows of no
+    group get zeros.  Bounds as of the module that is trained."""
+    torch.manual_seed(11)
+    layer = E.NVFP4Experts(4, 64, 96, device="cuda", dtype=dtype)
+    packed = layer.pack()
+    with torch.no_grad():
+        layer.weight.normal_()                                     # what is packed counts
+    rows = sum(sizes) + 2
+    x = torch.randn((rows, 64), device="cuda").to(dtype).requires_grad_(True)
+    up = torch.randn((rows, 96), device="cuda").to(dtype)
+    ends = [0]
+    for s in sizes:
+        ends.append(ends[-1] + s)
+    offsets = torch.tensor(ends, device="cuda")
+    y = layer(x * 1, offsets, packed)
+    assert torch.equal(y, layer(x.detach(), offsets, packed))
+    first, = torch.autograd.grad(y, [x], up, retain_graph=True)
+    y.backward(up)
+    assert torch.equal(first, x.grad) and x.grad.dtype == dtype and layer.weight.grad is None
+    w1 = nv.nvfp4_dequantize(packed)
+    w0 = nv.nvfp4_dequantize(nv.nvfp4_quantize(w1, axis=0)).t().double().reshape(4, 96, 64)
+    w1 = w1.double().reshape(4, 96, 64)
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else 0.0
+    for e, (b, end) in enumerate(zip(ends, ends[1:])):
+        want, mass = up[b:end].double() @ w0[e], up[b:end].double().abs() @ w0[e].abs()
+        bound = (6 * 96 + 8) * U * mass * 1.02 + half * want.abs() * 1.02
+        assert ((x.grad[b:end].double() - want).abs() <= bound).all()
+        # and the formula's own gradient, as near as the two layouts' weights are
+        off = (x.grad[b:end].double() - up[b:end].double() @ w1[e]).abs()
+        assert (off <= bound + up[b:end].double().abs() @ (w0[e] - w1[e]).abs()).all()
+    assert torch.all(x.grad[ends[-1]:] == 0)
+    assert (w0 - w1).norm() <= 0.2 * w1.norm()
+
+
+def test_a_packed_block_passes_the_gradient_on():
+    """Frozen experts between trained parts: what lies before them gets the
+    gradient that the trained form gives it, to the rounding of the 4-bit
+    layouts: a quantization is off by some 0.1 of the weights' norm, and three of
+    them lie between the two forms' data gradients of each of two products,
+    2 * sqrt(3) * 0.1 < 0.5."""
+    torch.manual_seed(12)
+    block = E.NVFP4ExpertBlock(4, 2, 64, 96, device="cuda", dtype=torch.float32)
+    for p, std in ((block.up.weight, 0.125), (block.down.weight, 0.1), (block.router, 0.125)):
+        torch.nn.init.normal_(p, std=std)
+    x, r, up = torch.randn((3, 40, 64), device="cuda")
+    x.requires_grad_(True)
+    leaves = [x, block.norm.weight, block.router]
+    want = torch.autograd.grad(block(x, r)[0], leaves, up)
+    got = torch.autograd.grad(block(x, r, block.pack())[0], leaves, up)
+    for p, q in zip(got, want):
+        assert (p - q).norm() <= 0.5 * q.norm()
+
+
 def test_experts_backward_twice():
     layer = E.NVFP4Experts(2, 32, 32, device="cuda")
     x = torch.randn((9, 32), device="cuda", dtype=torch.bfloat16, requires_grad=True)
@@ -465,3 +522,32 @@ def test_a_layer_captured_beside_the_graph_of_another():
         with torch.cuda.graph(torch.cuda.CUDAGraph()):
             rms(x)
     assert alive.grad_fn is not None
+
+
+def test_packed_experts_captured():
+    """Beside a live eager graph of x forward alone, its backward pass once that
+    is gone; every replay with the eager result."""
+    layer = E.NVFP4Experts(2, 32, 48, device="cuda")
+    packed, offsets = layer.pack(), torch.tensor([0, 3, 8], device="cuda")
+    x = torch.randn((8, 32), device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    up = torch.randn((8, 48), device="cuda", dtype=torch.bfloat16)
+    alive = layer(x, offsets, packed)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = layer(x, offsets, packed)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, alive)
+    with pytest.raises(nv.NVFP4Error, match="still lives"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            torch.autograd.grad(layer(x, offsets, packed), [x], up)
+    del alive, y, graph
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got, = torch.autograd.grad(layer(x, offsets, packed), [x], up)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        q = nv.nvfp4_quantize(nv.nvfp4_dequantize(packed), axis=0)
+        assert torch.equal(got, nv.nvfp4_grouped_matmul(q, up, offsets, transposed=True))
+        up.copy_(torch.randn_like(up))
