@@ -82,9 +82,15 @@ class RMSNormFunction(LeafFunction):
     def backward(ctx, dy, dh=None):
         h, rstd, weight = ctx.saved_tensors
         grad_dtype = weight.dtype if weight is not None else torch.float32
+        r_dtype = h.dtype
+        if ctx.x_dtype == torch.float32 and r_dtype != torch.float32:
+            # the kernel writes dx in h's type: beside a bf16 stream a float32 x
+            # would get a gradient of 8 bits
+            h, dh = h.float(), None if dh is None else dh.float()
         dx, dw = nvfp4_rms_norm_backward(dy.contiguous(), h, rstd, weight, None if dh is None else dh.contiguous(),
                                          grad_dtype=grad_dtype)
-        return (dx.to(ctx.x_dtype), dx if ctx.has_residual else None, dw if weight is not None else None, None)
+        return (dx.to(ctx.x_dtype), dx.to(r_dtype) if ctx.has_residual else None, dw if weight is not None else None,
+                None)
 
 
 class DistillTopKFunction(LateLeafFunction):

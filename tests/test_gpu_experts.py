@@ -95,6 +95,30 @@ def test_rms_norm_module_types():
     assert torch.equal(norm.weight.grad, torch.zeros_like(norm.weight))
 
 
+@pytest.mark.parametrize("cols", [64, 203])
+def test_rms_norm_module_keeps_a_float32_gradient(cols):
+    """float32 activations beside a bf16 residual: x's gradient carries float32
+    roundings alone (as in test_rms_norm_module, from the sum as it is stored),
+    the residual's that and half a bf16 step."""
+    torch.manual_seed(13)
+    norm = H.RMSNorm(cols, device="cuda", dtype=torch.float32)
+    torch.nn.init.normal_(norm.weight, 1.0, 0.2)
+    x = torch.randn((33, cols), device="cuda", requires_grad=True)
+    r = torch.randn((33, cols), device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    up = torch.randn((33, cols), device="cuda")
+    up_h = torch.randn((33, cols), device="cuda", dtype=torch.bfloat16)
+    y, h = norm(x, r)
+    assert y.dtype == torch.float32 and h.dtype == torch.bfloat16
+    torch.autograd.backward([y, h], [up, up_h])
+    hd, wd = (t.detach().double().requires_grad_(True) for t in (h, norm.weight))
+    ((ref_rms(hd, wd, norm.eps) * up.double()).sum() + (hd * up_h.double()).sum()).backward()
+    assert x.grad.dtype == torch.float32 and r.grad.dtype == torch.bfloat16
+    top = hd.grad.abs().max()
+    assert (x.grad.double() - hd.grad).abs().max() <= 256 * U * top
+    assert ((r.grad.double() - hd.grad).abs() <= 256 * U * top + 2.0 ** -8 * hd.grad.abs()).all()
+    assert (norm.weight.grad.double() - wd.grad).abs().max() <= 256 * U * wd.grad.abs().max()
+
+
 @pytest.mark.parametrize("sizes", [[3, 0, 1, 9], [200, 0, 31, 90], [0, 0, 0, 0]])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_experts_module(sizes, dtype):
