@@ -32,6 +32,12 @@ def group_by_expert(choice: torch.Tensor, experts: int):
     return order, offsets
 
 
+def weighted_sum(parts, share):
+    """The sum over a token's experts of share [tokens, top] times parts
+    [tokens, top, features], in parts' type; formed in float32, rounded once."""
+    return (parts * share[:, :, None]).sum(1).to(parts.dtype)
+
+
 class NVFP4ExpertsFunction(LeafFunction):
     """y [rows, out] of grouped rows x [rows, in], W [experts, out, in]; rows
     of no group are zeros."""
@@ -149,7 +155,7 @@ class NVFP4ExpertBlock(torch.nn.Module):
         out = self.down(torch.nn.functional.silu(gate) * up, offsets, packed and packed[1])
         back = torch.empty_like(order).scatter_(0, order, torch.arange(order.shape[0], device=order.device))
         parts = out[back].reshape(rows.shape[0], self.top, -1)
-        y = (parts * share[:, :, None].to(parts.dtype)).sum(1)
+        y = weighted_sum(parts, share)
         return y.reshape(*lead, -1), h
 
     @torch.no_grad()
