@@ -302,7 +302,8 @@ constexpr int kGradRows = 32, kGradCols = 256;
 template <typename X, int RF, bool DMA> struct Grad {
   static constexpr int kRowX = kGradCols * sizeof(X), kX = kGradRows * kRowX;
   static constexpr int kG = kGradRows * 32 * RF * 4 + 256;            // g's rows lie together, a rank apart
-  static constexpr int kStage = kX + kG, kRing = DMA ? (2 * 3 * kStage <= 160 * 1024 || 3 * kStage <= 160 * 1024 ? 3 : 2) : 2;
+  static constexpr int kStage = kX + kG, kRing = DMA ? 3 : 2;
+  static_assert(kRing * kStage <= 160 * 1024, "the stages fit a CU's LDS");
   // DMA instructions (1 KB) a wave and stage: a wave copies 8 rows of x
   static constexpr int kIX = kX / 4096, kRows = 1024 / kRowX;
 };

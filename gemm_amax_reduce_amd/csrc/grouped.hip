@@ -42,9 +42,6 @@ namespace nvfp4 {
 
 namespace {
 
-typedef uint32_t u32x4_a8 __attribute__((ext_vector_type(4), aligned(8)));
-typedef uint32_t u32x2_a8 __attribute__((ext_vector_type(2), aligned(8)));
-
 constexpr int kThreads = 256;
 constexpr int kStage = 128;                        // k of one LDS buffer
 constexpr int kXcds = 8;
@@ -502,16 +499,15 @@ __device__ __forceinline__ f32x4_t quad_turn(float a, float b, float c, float d)
   const float af = dpp<0x4E>(a1), bf = dpp<0x4E>(b1), cf = dpp<0x4E>(c1), df = dpp<0x4E>(d1);
   return (f32x4_t){high ? cf : a1, high ? df : b1, high ? c1 : af, high ? d1 : bf};
 }
-// N (2 or 4) neighbouring elements k .. of a row of K.
-template <int N>
-__device__ __forceinline__ void store_run(void *out, int bf16, int64_t row, int64_t k, int64_t K, const f32x4_t &v) {
-  if (N == 4 && k + 4 <= K) {
+// 4 neighbouring elements k .. of a row of K.
+__device__ __forceinline__ void store4(void *out, int bf16, int64_t row, int64_t k, int64_t K, const f32x4_t &v) {
+  if (k + 4 <= K) {
     if (bf16) *reinterpret_cast<u32x2_a2 *>((uint16_t *)out + row + k) = (u32x2_a2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
     else *reinterpret_cast<f32x4_a4 *>((float *)out + row + k) = v;
     return;
   }
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
+  for (int i = 0; i < 4; ++i) {
     if (k + i >= K) continue;
     if (bf16) ((uint16_t *)out)[row + k + i] = (uint16_t)pack_bf16(v[i], 0.0f);
     else ((float *)out)[row + k + i] = v[i];
@@ -720,13 +716,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_grouped_wgrad(Groups g, Operand
       if constexpr (FK == 4) {
         const int64_t k = k0 + (wave & 1) * 128 + 32 * (lane & 3) + (lane & 28);
         const f32x4_t v = quad_turn(acc[f][0][i], acc[f][1][i], acc[f][2][i], acc[f][3][i]);
-        if (n < N && k < K) store_run<4>(out, bf16, (base + n) * K, k, K, v);
+        if (n < N && k < K) store4(out, bf16, (base + n) * K, k, K, v);
       } else {
         // two fragments: rows n and n + 1 of the pair (i, i + 1) make the quad's four
         if (i & 1) continue;
         const f32x4_t v = quad_turn(acc[f][0][i], acc[f][1][i], acc[f][0][i + 1], acc[f][1][i + 1]);
         const int64_t m = n + ((lane >> 1) & 1), k = k0 + (wave & 1) * 64 + 32 * (lane & 1) + (lane & 28);
-        if (m < N && k < K) store_run<4>(out, bf16, (base + m) * K, k, K, v);
+        if (m < N && k < K) store4(out, bf16, (base + m) * K, k, K, v);
       }
     }
 }

@@ -38,9 +38,7 @@ struct GroupTile {
   int64_t begin, end;   // the group's rows
 };
 
-// The id-th of all tiles (units for each tile of rows), counted over the
-// groups in their order, found by a wave 64 groups at a time; `total` becomes
-// the number of all of them.  Every lane has the result.
+// A value that is the same in every lane, for the compiler to know.
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
   return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
                    (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
@@ -50,6 +48,7 @@ __device__ __forceinline__ int wave_total(int v) {
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
   return v;
 }
+// How many tiles all groups have.
 __device__ __forceinline__ int count_tiles(const Groups &g, int tile) {
   const int lane = threadIdx.x & 63;
   int total = 0;
@@ -59,8 +58,10 @@ __device__ __forceinline__ int count_tiles(const Groups &g, int tile) {
   }
   return __builtin_amdgcn_readfirstlane(total);
 }
-// `index` counts tiles of rows times `units` (the tiles of a row of tiles);
-// local is the place among the group's tiles x units.
+// The index-th of all tiles, counted over the groups in their order, found by a
+// wave 64 groups at a time; every lane has the result.  `index` counts tiles of
+// rows times `units` (the tiles of a row of tiles); local is the place among the
+// group's tiles x units.
 __device__ __forceinline__ GroupTile find_tile(const Groups &g, int tile, int units, int index) {
   const int lane = threadIdx.x & 63;
   GroupTile t = {-1, 0, 0, 0, 0};

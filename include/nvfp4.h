@@ -559,9 +559,9 @@ int64_t nvfp4_matvec_workspace_bytes(int64_t n, int64_t k, int64_t tokens, int x
  * bf16 products are exact; with a float32 operand products are off by at most
  * 2^-23 of their magnitude, and those with an infinity are infinite or NaN.
  * Sums are binary32, in a fixed order: deterministic on one device.  Enqueues
- * one kernel, one more for each operand that is float32 or not of whole words
- * (an odd number of columns, rows at odd places), and one where few tiles share
- * long groups.
+ * one kernel, one more for the operands that are float32 and one for bf16 ones
+ * not of whole words (an odd number of columns, rows at odd places), and one
+ * where few tiles share long groups.
  */
 int nvfp4_grouped_matmul(const nvfp4_tensor *w, int transposed, const void *x, int x_dtype, int64_t rows, int64_t ldx,
                          const void *offsets, int index_bits, int64_t experts, void *y, int y_dtype, int64_t ldy,
