@@ -149,3 +149,15 @@ def test_other_threads_record_meanwhile(capturing):
             t.join()
         sys.setswitchinterval(before)
     assert not failed and len(kept) == 2000
+
+
+def test_nodes_that_are_gone_are_swept_out(capturing):
+    w = torch.ones(3, requires_grad=True)
+    alive = [Twice.apply(torch.ones(3), w) for _ in range(5)]
+    for _ in range(3000):
+        Twice.apply(torch.ones(3), w)
+    assert len(capture._eager) <= 512 + 2 * 2005                   # (another test's nodes may still live)
+    capturing[0] = True
+    assert capture._lives_beside([w])
+    del alive
+    assert not capture._lives_beside([w])
