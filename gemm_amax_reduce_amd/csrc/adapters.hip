@@ -157,7 +157,8 @@ __global__ __launch_bounds__(RF * MT > 4 ? 512 : 1024) void k_shrink(Segments s,
 //
 // Bound by HBM: 4099 rows of 20480 columns, bf16 base and result, rank 32: 97 us
 // (336 MB, 3.5 TB/s); 8192 x 5120 48 us.  160 registers leave three waves a SIMD;
-// four (and spilled registers) took 209 us instead of 133 for the whole call.
+// four (and spilled registers) took 209 us instead of 133 for the whole call, which
+// takes 125 to 133 from card to card.
 template <typename T>
 __device__ __forceinline__ void load_ranks(Row8<T> &q, const T *row, int at, int rank, bool eights) {
   if (eights) {
@@ -583,7 +584,13 @@ __global__ __launch_bounds__(256) void k_turn(Segments s, const W *b, W *b_turne
 template <typename X, typename W>
 void shrink(const Segments &s, const X *x, int64_t ldx, int64_t C, const W *w, int rank, const float *scale, float *out,
             hipStream_t stream) {
-  // 32 rows a tile where 16 would make more than two rounds of the CUs
+  // 32 rows a tile where 16 would make more than two rounds of the CUs.  us a
+  // call (K 5120, N 64; tiles of 16 rows / of 32) of rank 16, 32, 64: bf16 8200
+  // rows 37 / 39, 54 / 49, 83 / 69, 32768 rows 105 / 98, 156 / 128, 244 / 170;
+  // float32 x, bf16 weights 8200 rows 59 / 69, 74 / 109, 144 / 98, 32768 rows 169 /
+  // 174, 216 / 278, 438 / 243.  (Float32 of rank up to 32 loses by it: the
+  // registers of that form spill.  4099 bf16 rows would gain: 28 / 24, 39 / 29,
+  // 59 / 39.)
   const bool pairs = s.g.rows > 16 * 2 * (int64_t)device_cus() && rank <= 64;
   const int64_t tile = pairs ? 32 : 16, tiles = s.g.rows / tile + std::min<int64_t>(s.g.count, s.g.rows);
   const auto launch = [&](auto kernel, int rf) {

@@ -18,8 +18,8 @@
 // by that.
 //
 // Bound by the matrix pipe where groups are long: 4096 rows of 8 experts
-// 20480 x 5120 in bf16 take 800 us (NVFP4; 1075 TFLOP/s, a large bf16 product of
-// the library reaches 1425), of which partly filled tiles at the groups' ends
+// 20480 x 5120 in bf16 take 800 to 816 us (NVFP4; 1050 to 1075 TFLOP/s, a large bf16
+// product of the library reaches 1440), of which partly filled tiles at the groups' ends
 // are an eighth, decoding a tenth and the LDS traffic of the copies a fifth.
 // 1531 float32 rows of 24 experts transposed, 5120 x 1280 (three products each):
 // 101 us, bound by copies that are one stage ahead (60 KB a CU on their way), and
