@@ -425,11 +425,8 @@ def gemm_workspace(device=None, stream=None) -> torch.Tensor:
     cleared by the graph itself, and is not kept: graphs captured on one stream
     may be replayed in any order, on any streams."""
     device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-    if stream is not None:
-        with torch.cuda.stream(stream):          # its memory and its clearing are that stream's
-            return _stream_workspace(device, stream)
-    with torch.cuda.device(device):
-        return _stream_workspace(device, torch.cuda.current_stream(device))
+    with _on(device, stream):                    # its memory and its clearing are the stream's
+        return _stream_workspace(device, stream if stream is not None else torch.cuda.current_stream(device))
 
 
 def _stream_workspace(device, s) -> torch.Tensor:
