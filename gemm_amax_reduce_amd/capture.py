@@ -3,12 +3,12 @@ capture.
 
 A leaf has one gradient accumulator for all graphs that it is part of, bound to
 the stream of the first.  A backward pass captured while an eager graph of the
-same leaf lives would make the captured stream wait for that other stream, and
-the process ends inside autograd's worker thread.  So each function here notes
-its node and the leaves that it starts from, and refuses to be captured beside
-an eager one: some at once, others, whose forward pass alone may be captured
-there, in their backward pass.  Without gradients no node is recorded, and
-nothing is refused.
+same leaf lives makes that other stream part of the capture, which the default
+stream cannot be: the process ends inside autograd's worker thread.  So each
+function here notes its node and the leaves that it starts from, and refuses to
+be captured beside an eager one of the default stream: some at once, others,
+whose forward pass alone may be captured there, in their backward pass.  Without
+gradients no node is recorded, and nothing is refused.
 """
 from __future__ import annotations
 
@@ -17,15 +17,15 @@ import weakref
 
 import torch
 
-from . import NVFP4Error
+from . import NVFP4Error, _current_handle
 
-# (node, its leaves) of those recorded outside a capture, as weak references;
-# what is dead is swept out when the list has doubled.  (With a weak set,
-# whose entries are called at each node's end, noting took 6.4 us of a call's
-# time on the host, so 4.2.)
-_eager: list = []
+# (node, its leaves) of the nodes that the default stream recorded, or that hold
+# an accumulator of its, by weak references; what is dead is swept out when the
+# list has doubled, or is looked through.  (A weak set, whose entries are called
+# at each node's end, made noting 2 us longer on the host.)
+_noted: list = []
 _sweep_at = 256
-_lock = threading.RLock()             # held by whoever adds to it or copies it
+_lock = threading.RLock()             # held by whoever adds to it or looks through it
 
 
 def _capturing() -> bool:
@@ -44,25 +44,34 @@ def _leaves(args) -> list:
     return found
 
 
+def _default_stream(device) -> bool:
+    return device.type == "cuda" and _current_handle(device) == 0
+
+
+def _sweep() -> None:
+    global _noted, _sweep_at
+    _noted = [e for e in _noted if e[0]() is not None]
+    _sweep_at = max(256, 2 * len(_noted))
+
+
 def _note(node, leaves) -> None:
-    global _eager, _sweep_at
     entry = (weakref.ref(node), [weakref.ref(t) for t in leaves])
     with _lock:
-        if len(_eager) >= _sweep_at:
-            _eager = [e for e in _eager if e[0]() is not None]
-            _sweep_at = max(256, 2 * len(_eager))
-        _eager.append(entry)
+        if len(_noted) >= _sweep_at:
+            _sweep()
+        _noted.append(entry)
 
 
 def _lives_beside(leaves) -> bool:
-    """Whether a node noted outside a capture still lives at one of them."""
+    """Whether a noted node still lives at one of them."""
     with _lock:
-        entries = list(_eager)
+        _sweep()
+        entries = list(_noted)
     return any(node() is not None and any(t is leaf() for leaf in noted for t in leaves) for node, noted in entries)
 
 
 def _refuse():
-    raise NVFP4Error("a graph of this parameter or input, made outside the capture, still lives: delete its outputs "
+    raise NVFP4Error("a graph of this parameter or input, made on the default stream, still lives: delete its outputs "
                      "before the capture")
 
 
@@ -74,8 +83,8 @@ def refuse_beside(ctx) -> None:
 
 class LeafFunction(torch.autograd.Function):
     """An autograd function whose nodes are noted; under capture, apply raises
-    NVFP4Error if a node noted outside a capture still lives at a leaf of the
-    call's."""
+    NVFP4Error if a node that the default stream recorded still lives at a leaf of
+    the call's."""
 
     late = False
 
@@ -93,10 +102,10 @@ class LeafFunction(torch.autograd.Function):
         out = super().apply(*args)
         node = (out[0] if isinstance(out, tuple) else out).grad_fn
         if capturing:
-            # (the accumulator stays the eager graph's, also where that is gone by
-            # the backward pass: this graph holds it)
             node.beside = beside
-        else:
+        # (beside another node a node holds the same accumulator, also when that one
+        # is gone)
+        if beside if capturing else _default_stream(leaves[0].device) or _lives_beside(leaves):
             _note(node, leaves)
         return out
 

@@ -575,3 +575,48 @@ def test_packed_experts_captured():
         q = nv.nvfp4_quantize(nv.nvfp4_dequantize(packed), axis=0)
         assert torch.equal(got, nv.nvfp4_grouped_matmul(q, up, offsets, transposed=True))
         up.copy_(torch.randn_like(up))
+
+
+@pytest.mark.parametrize("part", ["linear", "layer norm", "rms norm", "experts", "adapters", "packed experts"])
+def test_captured_beside_the_graph_of_a_warm_up(part):
+    """The usual way to a captured training step: a warm-up on a side stream, whose
+    outputs stay in scope, then the capture."""
+    torch.manual_seed(14)
+    x = torch.randn((32, 64), device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    offsets, index = torch.tensor([0, 10, 32], device="cuda"), torch.tensor([1, 0], device="cuda")
+    experts, low = E.NVFP4Experts(2, 64, 64, device="cuda"), LowRankAdapters(2, 64, 64, 4, device="cuda")
+    torch.nn.init.normal_(low.b)
+    packed, linear = experts.pack(), H.NVFP4Linear(64, 64, device="cuda")
+    linear.weight.requires_grad_(part == "linear")
+    norm = (H.LayerNorm if part == "layer norm" else H.RMSNorm)(64, device="cuda")
+    call, leaves = {"linear": (lambda: linear(x), [x, linear.weight]), "layer norm": (lambda: norm(x), [x, norm.weight]),
+                    "rms norm": (lambda: norm(x), [x, norm.weight]),
+                    "experts": (lambda: experts(x, offsets), [x, experts.weight]),
+                    "adapters": (lambda: low(x, None, offsets, index), [x, low.a, low.b]),
+                    "packed experts": (lambda: experts(x, offsets, packed), [x])}[part]
+    up = torch.randn((32, 64), device="cuda", dtype=torch.bfloat16)
+
+    def step():
+        y = call()
+        y.backward(up)
+        return y
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            alive = step()
+    torch.cuda.current_stream().wait_stream(side)
+    for leaf in leaves:
+        leaf.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = step()
+    grads = [leaf.grad for leaf in leaves]
+    for _ in range(3):
+        for g in grads:
+            g.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, alive)
+        assert all(torch.isfinite(g).all() and g.abs().max() > 0 for g in grads)
