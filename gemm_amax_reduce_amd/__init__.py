@@ -411,9 +411,7 @@ def nvfp4_gemm(a: NVFP4Tensor, b: NVFP4Tensor, out_dtype=torch.float32, out: tor
 
 
 _workspaces: dict = {}
-
-
-# of it, what the kernel needs zero-filled (its flags)
+# of one, what the kernel needs zero-filled (its flags)
 _WORKSPACE_FLAGS = 1 << 16
 
 
@@ -424,7 +422,9 @@ def gemm_workspace(device=None, stream=None) -> torch.Tensor:
     used by two calls at once.  Under capture it is a new one, its flags
     cleared by the graph itself, and is not kept: graphs captured on one stream
     may be replayed in any order, on any streams."""
-    device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    device = torch.device(device if device is not None else "cuda")
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
     with _on(device, stream):                    # its memory and its clearing are the stream's
         return _stream_workspace(device, stream if stream is not None else torch.cuda.current_stream(device))
 

@@ -36,6 +36,16 @@ def test_captured_graphs_share_none():
         assert torch.all(t[:1 << 16] == 0)
 
 
+def test_one_for_each_stream():
+    side = torch.cuda.Stream()
+    a, b = nv.gemm_workspace(), nv.gemm_workspace(stream=side)
+    assert a.data_ptr() != b.data_ptr()
+    for device in (None, 0, "cuda", "cuda:0", torch.device("cuda")):
+        assert nv.gemm_workspace(device) is a and nv.gemm_workspace(device, side) is b
+    with torch.cuda.stream(side):
+        assert nv.gemm_workspace() is b
+
+
 def test_cleared_in_its_streams_order():
     """The current stream is busy, and its allocator holds a block of ones."""
     size = int(nv.lib().nvfp4_gemm_workspace_bytes())
