@@ -22,8 +22,8 @@
 // product of the library reaches 1440), of which partly filled tiles at the groups' ends
 // are an eighth, decoding a tenth and the LDS traffic of the copies a fifth.
 // 1531 float32 rows of 24 experts transposed, 5120 x 1280 (three products each):
-// 101 us, bound by copies that are one stage ahead (60 KB a CU on their way), and
-// 7.5 for the parts.
+// 101 to 107 us, bound by copies that are one stage ahead (60 KB a CU on their
+// way), and 7.5 for the parts.
 //
 // The weight gradient has tokens along the reduction: both operands lie in LDS
 // as they come, by DMA three stages deep, and reach the lanes by transposing
